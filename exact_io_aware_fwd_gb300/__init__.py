@@ -8,6 +8,7 @@ the seeded synthetic workloads.
 from .binding import (  # noqa: F401
     EXPORTED,
     FA_ERR_CUDA,
+    FA_ERR_INDEX,
     FA_ERR_INVALID_ARG,
     FA_ERR_TIMEOUT,
     FA_ERR_UNSUPPORTED,
@@ -37,5 +38,17 @@ from .binding import (  # noqa: F401
     fa_status_string,
     load_library,
     workspace_for,
+)
+from .serving import (  # noqa: F401
+    fa_fwd_paged,
+    fa_fwd_paged_workspace_size,
+    fa_fwd_shared_prefix,
+    fa_fwd_shared_prefix_workspace_size,
+    fa_kv_append,
+    fa_qk_norm_rope_bwd,
+    fa_qk_norm_rope_bwd_workspace_size,
+    fa_qk_norm_rope_fwd,
+    fa_rope_table,
+    rope_frequencies,
 )
 from .build_lib import LIB_PATH, build  # noqa: F401

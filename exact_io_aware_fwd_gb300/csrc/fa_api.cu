@@ -5,9 +5,8 @@
 #include <cstdlib>
 #include <cstring>
 
-#include <cudaTypedefs.h>
-
 #include "fa.h"
+#include "fa_host.h"
 #include "fa_internal.h"
 
 namespace {
@@ -15,6 +14,10 @@ namespace {
 __device__ int g_fa_status = 0;  // first device-side error since the last fa_get_error()
 
 constexpr int kMaxDevices = 64;
+
+}  // namespace
+
+namespace fa {
 
 // Per-device address of the status word (looked up once per device; calls from several host
 // threads may race to look it up, and all of them store the same value).
@@ -48,6 +51,28 @@ uint64_t wait_timeout_ns() {
   return 2000ull * 1000000ull;
 }
 
+// The kernels are built for sm_103a only (compute capability 10.3); on any other GPU no image
+// would load, so the call is refused before any launch.
+fa_status check_device() {
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return (major == 10 && minor == 3) ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+fa_status check_workspace(void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return FA_ERR_INVALID_ARG;
+  if (bytes < need) return FA_ERR_WORKSPACE;
+  return FA_OK;
+}
+
+float resolve_scale(float scale, int d) {
+  return (scale < 0.f) ? 1.0f / std::sqrt(static_cast<float>(d)) : scale;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {  // looked up once, thread-safely
     void* p = nullptr;
@@ -60,6 +85,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   }();
   return fn;
 }
+
+}  // namespace fa
+
+namespace {
+
+using fa::check_device;
+using fa::check_workspace;
+using fa::encode_fn;
+using fa::resolve_scale;
+using fa::status_ptr;
+using fa::wait_timeout_ns;
 
 // [B*H][N][d] bf16 viewed as a 3-D tensor (d, N, B*H); boxes of 64 x 128 x 1 elements with the
 // 128-byte swizzle.  Rows past N are out of bounds: zero-filled on load, dropped on store.
@@ -107,29 +143,7 @@ fa_status check_sizes(int B, int H, int N, int d) {
   return FA_OK;
 }
 
-float resolve_scale(float scale, int d) {
-  return (scale < 0.f) ? 1.0f / std::sqrt(static_cast<float>(d)) : scale;
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
-
-// The kernels are built for sm_103a only (compute capability 10.3); on any other GPU no image
-// would load, so the call is refused before any launch.
-fa_status check_device() {
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-    return FA_ERR_CUDA;
-  return (major == 10 && minor == 3) ? FA_OK : FA_ERR_UNSUPPORTED;
-}
-
-fa_status check_workspace(void* ws, size_t bytes, size_t need) {
-  if (ws == nullptr) return FA_ERR_WORKSPACE;
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return FA_ERR_INVALID_ARG;
-  if (bytes < need) return FA_ERR_WORKSPACE;
-  return FA_OK;
-}
 
 // One attention problem as every entry point describes it.
 struct Problem {
@@ -354,6 +368,7 @@ const char* fa_status_string(fa_status s) {
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_TIMEOUT: return "device pipeline wait timed out";
     case FA_ERR_WORKSPACE: return "workspace missing or too small";
+    case FA_ERR_INDEX: return "page, position or length in device memory out of range";
   }
   return "unknown status";
 }
@@ -541,6 +556,7 @@ fa_status fa_get_error(void* stream) {
   switch (v) {
     case 0: return FA_OK;
     case 4: return FA_ERR_TIMEOUT;
+    case 6: return FA_ERR_INDEX;
     default: return FA_ERR_CUDA;
   }
 }

@@ -1,0 +1,148 @@
+// Internal interface of the operators around attention: the norm + rotation pass, the paged
+// cache and the attention that reads it.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace fa {
+
+enum : int { kErrIndex = 6 };  // FA_ERR_INDEX in the status word
+
+// Page that holds key `key` of a sequence whose block-table row is `row` (max_pages entries), or
+// -1 when the entry or the page lies outside its range.
+__host__ __device__ inline int resolve_page(const int32_t* row, int max_pages, int num_pages,
+                                            int page_shift, int key) {
+  const int i = key >> page_shift;
+  if (key < 0 || i >= max_pages) return -1;
+  const int p = row[i];
+  return (p < 0 || p >= num_pages) ? -1 : p;
+}
+
+// Bounds of new tokens [cu[b], cu[b + 1]) in packed tensors of `total` tokens, clamped like
+// seq_bounds (cu == nullptr: one token per sequence).
+__host__ __device__ inline void token_bounds(const int32_t* cu, int b, int total, int& start,
+                                             int& n) {
+  int s0 = cu != nullptr ? cu[b] : b;
+  int s1 = cu != nullptr ? cu[b + 1] : b + 1;
+  s0 = s0 < 0 ? 0 : (s0 > total ? total : s0);
+  s1 = s1 < s0 ? s0 : (s1 > total ? total : s1);
+  start = s0;
+  n = s1 - s0;
+}
+// Sequence whose tokens include t: the last b with cu[b] <= t (empty sequences skipped), or -1
+// when t lies behind cu[B] or before cu[0].
+__host__ __device__ inline int token_sequence(const int32_t* cu, int B, int t) {
+  if (cu == nullptr) return t < B ? t : -1;
+  if (t < cu[0] || t >= cu[B]) return -1;
+  int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---- norm + rotation pass (fa_rope.cu)
+struct RowView {
+  __nv_bfloat16* p;
+  int64_t batch, token, head;
+};
+
+struct RopeArgs {
+  RowView q, k, v;     // inputs (backward: gradients of the outputs); q.p / v.p may be null
+  RowView qo, ko, vo;  // outputs (backward: gradients of the inputs); paged: qo alone
+  RowView qx, kx;      // backward with norms: the forward's inputs
+  int B, N, H, Hkv;
+  int tokens;          // B * N
+  int chunk;           // heads of one work item
+  const int32_t* positions;
+  const float* table;
+  int n_pos, rot;
+  const float *wq, *wk;
+  float eps;
+  float* partial;      // backward with norms: [blocks][2][d] weight-gradient partials
+  // paged destination of K and V
+  __nv_bfloat16 *k_cache, *v_cache;
+  const int32_t *block_table, *kv_lens, *cu, *pos_offset;
+  int max_pages, num_pages, page_shift, seqs;
+  int* status;
+};
+
+constexpr int kRopeBwdBlocks = 152 * 8;  // most blocks (and partials) of the backward with norms
+
+cudaError_t launch_rope_table(const double* inv_freq, int rot, int n_pos, float amplitude,
+                              float* table, cudaStream_t s);
+cudaError_t launch_rope_fwd(int d, bool interleaved, bool paged, const RopeArgs& a,
+                            cudaStream_t s);
+cudaError_t launch_rope_bwd(int d, bool interleaved, const RopeArgs& a, float* dwq, float* dwk,
+                            cudaStream_t s);
+
+// ---- attention over the paged cache (fa_paged.cu)
+//
+// One launch covers a list of key ranges: the sequences of a batch with their own pages, or the
+// groups of a batch with the pages of their shared prefix (group_cu set).  Entry b has packed
+// query tokens [start, start + n) and len keys.
+struct KeyList {
+  int count;                // entries
+  const int32_t* lens;      // [count]
+  const int32_t* table;     // [count][max_pages]
+  int max_pages, max_len, max_q;
+  const int32_t* group_cu;  // groups: [count + 1] over sequences, or nullptr
+  int causal;
+};
+
+// Partial results of one list.  Its rows (query token x head of the key/value head's group) are
+// cut into tiles of R rows; tile r of entry b has index row_tile0(b) + r in [0, row_tiles()).
+// spans[hk][tile] = (first CTA, number of CTAs) that worked on the tile's keys.  One CTA: it wrote
+// the result (a joined list: into the row buffer).  Several: CTA i left its part in slot
+// 2 i + (1 when it began the tile's keys), and the join kernel adds them up in key order.
+struct PartialLayout {
+  int R;
+  int2* spans;
+  int span_tiles;  // tiles per key/value head
+  float* slots;    // [ctas][2][R * (D + 2)]: unnormalised O, then m (log2 units), then l
+  int ctas;
+};
+__host__ __device__ inline int row_tiles_bound(int total, int G, int R, int count) {
+  return (total * G + R - 1) / R + count;
+}
+__host__ __device__ inline int row_tile0(int start, int G, int R, int b) {
+  return (start * G + R - 1) / R + b;  // never overlaps entry b - 1's tiles
+}
+
+struct PagedArgs {
+  const __nv_bfloat16 *q, *k_cache, *v_cache;
+  __nv_bfloat16* o;
+  float* lse;
+  const int32_t* cu;
+  int B, total, H, Hkv, G;
+  int num_pages, page_shift;
+  float scale_log2;
+  KeyList list;
+  PartialLayout part;
+  float* rowbuf;  // joined lists: [total * H] rows of O, then m, then l; else nullptr
+  int* status;
+};
+
+struct JoinArgs {
+  __nv_bfloat16* o;
+  float* lse;
+  const int32_t* cu;
+  int B, total, H, Hkv, G;
+  KeyList list[2];
+  PartialLayout part[2];
+  const float* rowbuf[2];
+  int lists;
+};
+
+constexpr int kPagedRows = 16;           // rows of a tile
+constexpr int kPagedMaxCtas = 152 * 3;   // most CTAs of a launch (and pairs of slots)
+
+cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s);
+cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s);
+
+}  // namespace fa

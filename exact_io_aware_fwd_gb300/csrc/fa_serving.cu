@@ -1,0 +1,370 @@
+// C-ABI entry points (declared in include/fa.h) of the operators around attention: the norm and
+// rotation pass, the paged cache and the attention that reads it.  Every argument is checked
+// before the first launch; nothing here allocates device memory.
+#include <cmath>
+
+#include "fa.h"
+#include "fa_host.h"
+#include "fa_internal.h"
+#include "fa_paged.h"
+
+namespace {
+
+using fa::aligned_to;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxInt = 0x7fffffff;
+
+// A view that rows of 16-byte pieces can be read from or written to; the stride of a dimension
+// of one element does not matter.
+bool view_ok(const fa_view& v, int B, int N, int H) {
+  return v.data != nullptr && aligned_to(v.data, 16) && (B == 1 || v.batch % 8 == 0) &&
+         (N == 1 || v.token % 8 == 0) && (H == 1 || v.head % 8 == 0);
+}
+fa::RowView row_view(const fa_view& v) {
+  return {static_cast<__nv_bfloat16*>(v.data), v.batch, v.token, v.head};
+}
+
+fa_status check_heads(int H, int Hkv, int d) {
+  if (H <= 0 || Hkv <= 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(H) + 2LL * Hkv > 65535) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa_status check_transform(const fa_qk_transform* t, int d) {
+  if (t == nullptr) return FA_ERR_INVALID_ARG;
+  if (t->table != nullptr) {
+    if (t->rot < 16 || t->rot > d || t->rot % 16 != 0 || t->n_pos < 1) return FA_ERR_INVALID_ARG;
+    if (!aligned_to(t->table, 16)) return FA_ERR_INVALID_ARG;
+  }
+  if ((t->q_weight == nullptr) != (t->k_weight == nullptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned_to(t->q_weight, 16) || !aligned_to(t->k_weight, 16)) return FA_ERR_INVALID_ARG;
+  if (t->q_weight != nullptr && !(std::isfinite(t->eps) && t->eps >= 0.f)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+void set_transform(fa::RopeArgs& a, const fa_qk_transform& t) {
+  a.table = t.table;
+  a.n_pos = t.n_pos;
+  a.rot = t.table != nullptr ? t.rot : 0;
+  a.wq = t.q_weight;
+  a.wk = t.k_weight;
+  a.eps = t.eps;
+}
+
+fa_status device_ready(int*& status) {
+  const fa_status st = fa::check_device();
+  if (st != FA_OK) return st;
+  status = fa::status_ptr();
+  return status == nullptr ? FA_ERR_CUDA : FA_OK;
+}
+
+int page_shift(int page_size) {
+  switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+  }
+  return -1;
+}
+
+fa_status check_cache(const fa_paged_kv* c) {
+  if (c == nullptr || c->k_cache == nullptr || c->v_cache == nullptr || c->kv_lens == nullptr)
+    return FA_ERR_INVALID_ARG;
+  if (!aligned_to(c->k_cache, 16) || !aligned_to(c->v_cache, 16)) return FA_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->max_pages < 0 || (c->max_pages > 0 && c->block_table == nullptr))
+    return FA_ERR_INVALID_ARG;
+  if (page_shift(c->page_size) < 0) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace of a paged call: the spans and slots of each list, then (joined lists) row buffers.
+struct PagedWorkspace {
+  size_t spans[2], slots[2], rowbuf[2], total;
+};
+PagedWorkspace paged_workspace(const int (&count)[2], int lists, int total, int H, int Hkv, int d) {
+  PagedWorkspace w{};
+  size_t at = 0;
+  for (int i = 0; i < lists; ++i) {
+    w.spans[i] = at;
+    at += up256(static_cast<size_t>(Hkv) *
+                fa::row_tiles_bound(total, H / Hkv, fa::kPagedRows, count[i]) * sizeof(int2));
+    w.slots[i] = at;
+    at += up256(static_cast<size_t>(fa::kPagedMaxCtas) * 2 * fa::kPagedRows * (d + 2) * 4);
+    if (lists > 1) {
+      w.rowbuf[i] = at;
+      at += up256(static_cast<size_t>(total) * H * (d + 2) * 4);
+    }
+  }
+  w.total = at;
+  return w;
+}
+
+fa_status check_paged_sizes(int B, int total, int H, int Hkv, int d) {
+  fa_status st = check_heads(H, Hkv, d);
+  if (st != FA_OK) return st;
+  if (B <= 0 || total < 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (H / Hkv > 128) return FA_ERR_UNSUPPORTED;
+  // rows of every tile and the index of a (token, head) row fit 32 bits
+  if ((static_cast<long long>(total) + B) * H + 128LL * B > kMaxInt) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* prefix, void* O,
+                     float* LSE, const int32_t* cu, int B, int max_q, int max_kv, int total,
+                     int H, int Hkv, int d, int causal, float scale, void* ws, size_t ws_bytes,
+                     cudaStream_t s) {
+  fa_status st = check_paged_sizes(B, total, H, Hkv, d);
+  if (st != FA_OK) return st;
+  if (max_q < 1 || max_kv < 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (cu == nullptr && total != B) return FA_ERR_INVALID_ARG;
+  if ((st = check_cache(cache)) != FA_OK) return st;
+  if (prefix != nullptr &&
+      (prefix->groups < 1 || prefix->max_len < 0 || prefix->max_pages < 0 ||
+       (prefix->max_pages > 0 && prefix->table == nullptr) || prefix->lens == nullptr ||
+       prefix->group_cu == nullptr))
+    return FA_ERR_INVALID_ARG;
+  if (total == 0) return FA_OK;
+  if (!Q || !O || !LSE || !aligned_to(Q, 16) || !aligned_to(O, 16)) return FA_ERR_INVALID_ARG;
+  const int lists = prefix != nullptr ? 2 : 1;
+  const int count[2] = {B, prefix != nullptr ? prefix->groups : 0};
+  if (lists == 2 && (static_cast<long long>(total) + count[1]) * H + 128LL * count[1] > kMaxInt)
+    return FA_ERR_INVALID_ARG;
+  const PagedWorkspace w = paged_workspace(count, lists, total, H, Hkv, d);
+  if ((st = fa::check_workspace(ws, ws_bytes, w.total)) != FA_OK) return st;
+  int* status = nullptr;
+  if ((st = device_ready(status)) != FA_OK) return st;
+
+  char* base = static_cast<char*>(ws);
+  fa::PagedArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(Q);
+  a.k_cache = static_cast<const __nv_bfloat16*>(cache->k_cache);
+  a.v_cache = static_cast<const __nv_bfloat16*>(cache->v_cache);
+  a.o = static_cast<__nv_bfloat16*>(O);
+  a.lse = LSE;
+  a.cu = cu;
+  a.B = B;
+  a.total = total;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = H / Hkv;
+  a.num_pages = cache->num_pages;
+  a.page_shift = page_shift(cache->page_size);
+  a.scale_log2 = fa::resolve_scale(scale, d) * kLog2e;
+  a.status = status;
+  fa::JoinArgs j{};
+  j.o = a.o;
+  j.lse = LSE;
+  j.cu = cu;
+  j.B = B;
+  j.total = total;
+  j.H = H;
+  j.Hkv = Hkv;
+  j.G = a.G;
+  j.lists = lists;
+  for (int i = 0; i < lists; ++i) {
+    fa::KeyList& l = a.list;
+    l.count = count[i];
+    l.lens = i == 0 ? cache->kv_lens : prefix->lens;
+    l.table = i == 0 ? cache->block_table : prefix->table;
+    l.max_pages = i == 0 ? cache->max_pages : prefix->max_pages;
+    l.max_len = i == 0 ? max_kv : prefix->max_len;
+    l.max_q = i == 0 ? max_q : kMaxInt;
+    l.group_cu = i == 0 ? nullptr : prefix->group_cu;
+    l.causal = i == 0 && causal ? 1 : 0;
+    a.part.R = fa::kPagedRows;
+    a.part.span_tiles = fa::row_tiles_bound(total, a.G, a.part.R, l.count);
+    a.part.spans = reinterpret_cast<int2*>(base + w.spans[i]);
+    a.part.slots = reinterpret_cast<float*>(base + w.slots[i]);
+    a.part.ctas = fa::kPagedMaxCtas;
+    a.rowbuf = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
+    const long long tokens = i == 0 && max_q < total ? max_q : total;
+    const long long units = static_cast<long long>(l.count) * Hkv *
+                            ((tokens * a.G + a.part.R - 1) / a.part.R) * (l.max_len / 64 + 1);
+    if ((st = status_of(fa::launch_paged(d, a, units, s))) != FA_OK) return st;
+    j.list[i] = l;
+    j.part[i] = a.part;
+    j.rowbuf[i] = a.rowbuf;
+  }
+  return status_of(fa::launch_paged_join(d, j, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rope_table(const double* inv_freq, int rot, int n_pos, float amplitude,
+                        float* table, void* stream) {
+  if (!inv_freq || !table || rot < 2 || rot > 1024 || rot % 2 != 0 || n_pos < 1)
+    return FA_ERR_INVALID_ARG;
+  if (!aligned_to(inv_freq, 8) || !aligned_to(table, 4) || !std::isfinite(amplitude))
+    return FA_ERR_INVALID_ARG;
+  const fa_status st = fa::check_device();
+  if (st != FA_OK) return st;
+  return status_of(fa::launch_rope_table(inv_freq, rot, n_pos, amplitude, table,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_qk_norm_rope_fwd(fa_view q, fa_view k, fa_view v, fa_view q_out, fa_view k_out,
+                              fa_view v_out, const int32_t* positions, int B, int N, int H,
+                              int Hkv, int d, const fa_qk_transform* t, void* stream) {
+  fa_status st = check_heads(H, Hkv, d);
+  if (st != FA_OK) return st;
+  if ((st = check_transform(t, d)) != FA_OK) return st;
+  if (B <= 0 || N < 0 || static_cast<long long>(B) * N > kMaxInt) return FA_ERR_INVALID_ARG;
+  if (N == 0) return FA_OK;
+  if (t->table != nullptr && positions == nullptr && N > t->n_pos) return FA_ERR_INVALID_ARG;
+  if (!view_ok(q, B, N, H) || !view_ok(q_out, B, N, H) || !view_ok(k, B, N, Hkv) ||
+      !view_ok(k_out, B, N, Hkv))
+    return FA_ERR_INVALID_ARG;
+  if (v.data != nullptr && (!view_ok(v, B, N, Hkv) || !view_ok(v_out, B, N, Hkv)))
+    return FA_ERR_INVALID_ARG;
+  fa::RopeArgs a{};
+  if ((st = device_ready(a.status)) != FA_OK) return st;
+  set_transform(a, *t);
+  a.q = row_view(q);
+  a.k = row_view(k);
+  a.v = row_view(v);
+  a.qo = row_view(q_out);
+  a.ko = row_view(k_out);
+  a.vo = row_view(v_out);
+  a.B = B;
+  a.N = N;
+  a.tokens = B * N;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.positions = positions;
+  return status_of(fa::launch_rope_fwd(d, t->interleaved != 0, /*paged=*/false, a,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
+  if (d != 64 && d != 128) return 0;
+  return static_cast<size_t>(fa::kRopeBwdBlocks) * 2 * d * sizeof(float);
+}
+
+fa_status fa_qk_norm_rope_bwd(fa_view dq, fa_view dk, fa_view dv, fa_view q, fa_view k,
+                              fa_view dq_in, fa_view dk_in, fa_view dv_in, float* dq_weight,
+                              float* dk_weight, const int32_t* positions, int B, int N, int H,
+                              int Hkv, int d, const fa_qk_transform* t, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  fa_status st = check_heads(H, Hkv, d);
+  if (st != FA_OK) return st;
+  if ((st = check_transform(t, d)) != FA_OK) return st;
+  if (B <= 0 || N < 0 || static_cast<long long>(B) * N > kMaxInt) return FA_ERR_INVALID_ARG;
+  const bool norm = t->q_weight != nullptr;
+  if (norm) {
+    if (!dq_weight || !dk_weight) return FA_ERR_INVALID_ARG;
+    if ((st = fa::check_workspace(workspace, workspace_bytes,
+                                  fa_qk_norm_rope_bwd_workspace_size(d))) != FA_OK)
+      return st;
+  }
+  if (N == 0 && !norm) return FA_OK;
+  if (t->table != nullptr && positions == nullptr && N > t->n_pos) return FA_ERR_INVALID_ARG;
+  if (N > 0) {
+    if (!view_ok(dq, B, N, H) || !view_ok(dq_in, B, N, H) || !view_ok(dk, B, N, Hkv) ||
+        !view_ok(dk_in, B, N, Hkv))
+      return FA_ERR_INVALID_ARG;
+    if (dv.data != nullptr && (!view_ok(dv, B, N, Hkv) || !view_ok(dv_in, B, N, Hkv)))
+      return FA_ERR_INVALID_ARG;
+    if (norm && (!view_ok(q, B, N, H) || !view_ok(k, B, N, Hkv))) return FA_ERR_INVALID_ARG;
+  }
+  fa::RopeArgs a{};
+  if ((st = device_ready(a.status)) != FA_OK) return st;
+  set_transform(a, *t);
+  a.q = row_view(dq);
+  a.k = row_view(dk);
+  a.v = row_view(dv);
+  a.qo = row_view(dq_in);
+  a.ko = row_view(dk_in);
+  a.vo = row_view(dv_in);
+  a.qx = row_view(q);
+  a.kx = row_view(k);
+  a.B = B;
+  a.N = N;
+  a.tokens = B * N;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.positions = positions;
+  a.partial = static_cast<float*>(workspace);
+  return status_of(fa::launch_rope_bwd(d, t->interleaved != 0, a, dq_weight, dk_weight,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_kv_append(fa_view q, fa_view k, fa_view v, fa_view q_out, const fa_paged_kv* cache,
+                       const int32_t* cu_seqlens, const int32_t* pos_offset, int B, int total,
+                       int H, int Hkv, int d, const fa_qk_transform* t, void* stream) {
+  fa_status st = check_heads(H, Hkv, d);
+  if (st != FA_OK) return st;
+  if ((st = check_transform(t, d)) != FA_OK) return st;
+  if ((st = check_cache(cache)) != FA_OK) return st;
+  if (B <= 0 || total < 0 || cache->max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (cu_seqlens == nullptr && total != B) return FA_ERR_INVALID_ARG;
+  if (total == 0) return FA_OK;
+  if (!view_ok(k, 1, total, Hkv) || !view_ok(v, 1, total, Hkv)) return FA_ERR_INVALID_ARG;
+  if (q.data != nullptr && (!view_ok(q, 1, total, H) || !view_ok(q_out, 1, total, H)))
+    return FA_ERR_INVALID_ARG;
+  fa::RopeArgs a{};
+  if ((st = device_ready(a.status)) != FA_OK) return st;
+  set_transform(a, *t);
+  a.q = row_view(q);
+  a.k = row_view(k);
+  a.v = row_view(v);
+  a.qo = row_view(q_out);
+  a.B = 1;
+  a.N = total;
+  a.tokens = total;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.k_cache = static_cast<__nv_bfloat16*>(cache->k_cache);
+  a.v_cache = static_cast<__nv_bfloat16*>(cache->v_cache);
+  a.block_table = cache->block_table;
+  a.kv_lens = cache->kv_lens;
+  a.cu = cu_seqlens;
+  a.pos_offset = pos_offset;
+  a.max_pages = cache->max_pages;
+  a.num_pages = cache->num_pages;
+  a.page_shift = page_shift(cache->page_size);
+  a.seqs = B;
+  return status_of(fa::launch_rope_fwd(d, t->interleaved != 0, /*paged=*/true, a,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_fwd_paged_workspace_size(int B, int total, int H, int Hkv, int d) {
+  if (check_paged_sizes(B, total, H, Hkv, d) != FA_OK) return 0;
+  const int count[2] = {B, 0};
+  return paged_workspace(count, 1, total, H, Hkv, d).total;
+}
+
+fa_status fa_fwd_paged(const void* Q, const fa_paged_kv* cache, void* O, float* LSE,
+                       const int32_t* cu_seqlens, int B, int max_q, int max_kv, int total, int H,
+                       int Hkv, int d, int causal, float scale, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return paged_impl(Q, cache, nullptr, O, LSE, cu_seqlens, B, max_q, max_kv, total, H, Hkv, d,
+                    causal, scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_fwd_shared_prefix_workspace_size(int B, int groups, int total, int H, int Hkv, int d) {
+  if (check_paged_sizes(B, total, H, Hkv, d) != FA_OK || groups < 1) return 0;
+  if ((static_cast<long long>(total) + groups) * H + 128LL * groups > kMaxInt) return 0;
+  const int count[2] = {B, groups};
+  return paged_workspace(count, 2, total, H, Hkv, d).total;
+}
+
+fa_status fa_fwd_shared_prefix(const void* Q, const fa_paged_kv* cache, const fa_prefix* prefix,
+                               void* O, float* LSE, const int32_t* cu_seqlens, int B, int max_q,
+                               int max_kv, int total, int H, int Hkv, int d, int causal,
+                               float scale, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (prefix == nullptr) return FA_ERR_INVALID_ARG;
+  return paged_impl(Q, cache, prefix, O, LSE, cu_seqlens, B, max_q, max_kv, total, H, Hkv, d,
+                    causal, scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

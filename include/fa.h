@@ -47,7 +47,9 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2,  /* head dimension other than 64/128, or the GPU is not sm_103 */
   FA_ERR_CUDA = 3,         /* a CUDA runtime/driver call or a kernel launch failed */
   FA_ERR_TIMEOUT = 4,      /* a device pipeline wait ran past its limit (see fa_get_error) */
-  FA_ERR_WORKSPACE = 5     /* workspace pointer NULL or smaller than fa_bwd_workspace_size() */
+  FA_ERR_WORKSPACE = 5,    /* workspace pointer NULL or smaller than fa_bwd_workspace_size() */
+  FA_ERR_INDEX = 6         /* a page, position or length read from device memory is out of its
+                              range (device-side, see fa_get_error) */
 } fa_status;
 
 /*
@@ -224,6 +226,154 @@ fa_status fa_bwd_noalloc(const void* Q, const void* K, const void* V, const void
                          const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
                          int B, int H, int N, int d, int causal, float scale,
                          const int32_t* kv_lens, void* stream);
+
+/*
+ * ------------------------------------------------------------------------------------------
+ * Before attention: norms and rotary positions of queries and keys
+ *
+ * A strided view of bf16 rows: element e of head h of token n of batch b is at
+ * data[b * batch + n * token + h * head + e]; the d elements of a row are contiguous.  Strides
+ * count elements and are multiples of 8; data is 16-byte aligned.  A fused projection output
+ * [B, N, H + 2 Hkv, d] is three such views, and so is the attention layout [B, H, N, d]
+ * (batch = H*N*d, token = d, head = N*d) or the packed one [total, H, d] (B = 1).
+ */
+typedef struct {
+  void* data;
+  int64_t batch, token, head;
+} fa_view;
+
+/*
+ * What happens to each row of Q and of K: an RMS norm over the head dimension (q_weight,
+ * k_weight: DEVICE float32[d], 16-byte aligned; both NULL for no norm), then the rotation of its
+ * first `rot` elements (table NULL: none).  Statistics and products are float32; each row is
+ * rounded to bf16 once.
+ *   norm:      y = x * rsqrt(mean(x^2) + eps) * weight
+ *   rotation:  (a, b) -> (a cos - b sin, a sin + b cos) for the pairs (y[i], y[i + rot/2])
+ *              (interleaved == 0) or (y[2i], y[2i + 1]) (interleaved != 0), i < rot/2.
+ * table: DEVICE float32 [n_pos][rot], cos of every pair and then sin (fa_rope_table makes it).
+ * rot is a multiple of 16, at most d; elements past it are not rotated.
+ */
+typedef struct {
+  const float* table;
+  int n_pos, rot, interleaved;
+  const float* q_weight;
+  const float* k_weight;
+  float eps;
+} fa_qk_transform;
+
+/*
+ * table[p][i] = amplitude * cos(p * inv_freq[i]), table[p][rot/2 + i] = amplitude * sin(...) for
+ * p < n_pos, i < rot/2; the angle is a float64 product, so far positions keep their precision.
+ * inv_freq: DEVICE float64[rot / 2]; scaling for long contexts is a choice of inv_freq and
+ * amplitude.  rot: even, 2..1024.
+ */
+fa_status fa_rope_table(const double* inv_freq, int rot, int n_pos, float amplitude,
+                        float* table, void* stream);
+
+/*
+ * Q, K: [B, N] tokens of H and Hkv heads, transformed and written through q_out, k_out; V copied
+ * through v_out (v.data NULL: no V).  One pass over the data: each input read once, each output
+ * written once.  positions: DEVICE int32[B*N], the table row of each token, or NULL: n.  A
+ * position outside [0, n_pos) uses the nearest row and records FA_ERR_INDEX.  An output may be
+ * the identical view of its input (in place); otherwise outputs overlap nothing.
+ */
+fa_status fa_qk_norm_rope_fwd(fa_view q, fa_view k, fa_view v, fa_view q_out, fa_view k_out,
+                              fa_view v_out, const int32_t* positions, int B, int N, int H,
+                              int Hkv, int d, const fa_qk_transform* t, void* stream);
+
+/*
+ * Gradients of fa_qk_norm_rope_fwd.  dq, dk, dv: of its outputs; q, k: its inputs (read only
+ * when there is a norm, else data may be NULL); dq_in, dk_in, dv_in: of its inputs (dv copied;
+ * dv.data NULL: no V).  dq_weight, dk_weight: float32[d], of the norm's weights, summed over
+ * tokens and heads in a fixed order (bit-identical from run to run); NULL without a norm.
+ * workspace: DEVICE, fa_qk_norm_rope_bwd_workspace_size(d) bytes, 256-byte aligned (needed with
+ * a norm only).  dq_in, dk_in, dv_in may be the identical views of dq, dk, dv.
+ */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+fa_status fa_qk_norm_rope_bwd(fa_view dq, fa_view dk, fa_view dv, fa_view q, fa_view k,
+                              fa_view dq_in, fa_view dk_in, fa_view dv_in, float* dq_weight,
+                              float* dk_weight, const int32_t* positions, int B, int N, int H,
+                              int Hkv, int d, const fa_qk_transform* t, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * ------------------------------------------------------------------------------------------
+ * Paged key/value cache
+ *
+ * k_cache, v_cache: DEVICE bf16 [num_pages][Hkv][page_size][d], 16-byte aligned; page_size is
+ * 16, 32, 64 or 128.  block_table: DEVICE int32 [B][max_pages]; keys [i * page_size, (i + 1) *
+ * page_size) of sequence b are in page block_table[b][i].  kv_lens: DEVICE int32[B], the keys of
+ * each sequence, its new tokens included, so one array serves fa_kv_append and the attention
+ * after it.  Entries past a sequence's length are not read.
+ * cu_seqlens: DEVICE int32[B + 1], offsets of each sequence's new tokens in the packed tensors
+ * (NULL: one token each, total == B).  Token i of n new ones is key kv_lens[b] - n + i.
+ * Tokens behind cu_seqlens[B] are left as they were.
+ * What the library reads from device memory is checked on the device: a page outside
+ * [0, num_pages) is neither read nor written (its keys count as masked), lengths are clamped to
+ * [0, max_pages * page_size] (and the bounds a call takes), and FA_ERR_INDEX is recorded.
+ */
+typedef struct {
+  void* k_cache;
+  void* v_cache;
+  int num_pages, page_size;
+  const int32_t* block_table;
+  int max_pages;
+  const int32_t* kv_lens;
+} fa_paged_kv;
+
+/*
+ * Appends the new tokens' K (transformed as above) and V to the cache and writes the transformed
+ * Q [total, H, d] through q_out, in one launch.  q.data NULL: no Q.  The rotation's position is
+ * the key's index plus pos_offset[b] (DEVICE int32[B], or NULL: 0; for pages behind a prefix
+ * that other pages hold).  Views: [total] tokens (their batch stride is not used).  A token of
+ * negative key index is not written.  No two tokens of one call may have the same place.
+ */
+fa_status fa_kv_append(fa_view q, fa_view k, fa_view v, fa_view q_out, const fa_paged_kv* cache,
+                       const int32_t* cu_seqlens, const int32_t* pos_offset, int B, int total,
+                       int H, int Hkv, int d, const fa_qk_transform* t, void* stream);
+
+/*
+ * Attention of packed queries Q [total, H, d] over the cache: O [total, H, d] bf16 and LSE
+ * [H, total] fp32, as fa_fwd_varlen with keys and values in pages.  causal != 0: new token i of
+ * n sees keys <= kv_lens[b] - n + i (aligned to the end); else all of them.  A query that sees
+ * no key gets O = 0, LSE = -inf.  max_q, max_kv: at least the most new tokens and keys of any
+ * sequence (tokens and keys beyond them are not computed, and FA_ERR_INDEX is recorded).
+ * H % Hkv == 0, H / Hkv <= 128.
+ * The keys are split over the whole GPU, partial results joined in a fixed order: the same
+ * inputs give bit-identical outputs.  V of a key that some query of the same tile may see must
+ * be finite, as in fa_fwd; cache rows past a sequence's length may hold anything.
+ * workspace: fa_fwd_paged_workspace_size(B, total, H, Hkv, d) bytes, 256-byte aligned, contents
+ * on entry irrelevant; calls that overlap on the GPU need one each.
+ */
+size_t fa_fwd_paged_workspace_size(int B, int total, int H, int Hkv, int d);
+fa_status fa_fwd_paged(const void* Q, const fa_paged_kv* cache, void* O, float* LSE,
+                       const int32_t* cu_seqlens, int B, int max_q, int max_kv, int total, int H,
+                       int Hkv, int d, int causal, float scale, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * fa_fwd_paged for a batch whose sequences share prefixes: sequences [group_cu[g],
+ * group_cu[g + 1]) (DEVICE int32[groups + 1], group_cu[0] = 0, group_cu[groups] = B) all begin
+ * with the prefix_lens[g] keys in pages prefix_table[g] (DEVICE int32 [groups][prefix_pages],
+ * pages of the same cache), followed by their own kv_lens[b] keys.  Every query sees its whole
+ * prefix; causal concerns the own keys.  A prefix is read once for all queries of its group.
+ * kv_lens[b] and prefix_lens[g] may be 0.  max_prefix: at least the longest prefix.
+ * workspace: fa_fwd_shared_prefix_workspace_size(...) bytes, else as fa_fwd_paged.
+ */
+typedef struct {
+  const int32_t* table;
+  int max_pages;
+  const int32_t* lens;
+  const int32_t* group_cu;
+  int groups, max_len;
+} fa_prefix;
+
+size_t fa_fwd_shared_prefix_workspace_size(int B, int groups, int total, int H, int Hkv, int d);
+fa_status fa_fwd_shared_prefix(const void* Q, const fa_paged_kv* cache, const fa_prefix* prefix,
+                               void* O, float* LSE, const int32_t* cu_seqlens, int B, int max_q,
+                               int max_kv, int total, int H, int Hkv, int d, int causal,
+                               float scale, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 /*
  * Synchronises `stream`, returns the first device-side error recorded since the previous call

@@ -1,0 +1,524 @@
+"""The paged cache (fa_kv_append), attention over it (fa_fwd_paged) and attention behind shared
+prefixes (fa_fwd_shared_prefix) against the fp64 reference.
+
+Tolerances.  P is rounded to bf16 (half a step, 2^-8 of each weight) before P V and O once more, so
+|O - ref| <= 2^-8 (sum p|v|) + 2^-8 |ref|; float32 sums and exponentials (2^-22 each, relative to
+score magnitudes of at most a few tens) stay inside 2^-14 sum p|v|.  LSE: the scores' float32
+dot products are off by at most 2^-24 (d + 16) scale sum|q k|, the exponentials and the logarithm
+by 2^-20."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_fwd_gb300 as fa
+from oracle.serving import attend, norm_rope, paged_keys
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    fa.build()
+    fa.load_library()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def cumulative(n):
+    return [0] + np.cumsum(n).tolist()
+
+
+class Cache:
+    """A shuffled pool whose unused rows, and rows past a length, hold NaN."""
+
+    def __init__(self, lens, Hkv, d, page, seed, sigma=1.0, extra=3):
+        g = torch.Generator().manual_seed(seed)
+        need = [-(-n // page) for n in lens]
+        order = torch.randperm(sum(need) + extra, generator=g).tolist()
+        width = max(1, max(need, default=1))
+        self.k, self.v = (torch.full((sum(need) + extra, Hkv, page, d), float("nan"), dtype=BF16)
+                          for _ in range(2))
+        self.table = torch.full((len(lens), width), -1, dtype=torch.int32)
+        for b, n in enumerate(lens):
+            for i in range(need[b]):
+                p = order.pop()
+                m = min(page, n - i * page)
+                self.table[b, i] = p
+                self.k[p, :, :m] = (sigma * torch.randn(Hkv, m, d, generator=g)).to(BF16)
+                self.v[p, :, :m] = torch.randn(Hkv, m, d, generator=g).to(BF16)
+        self.lens, self.page = list(lens), page
+        self.np = (self.k.float().numpy(), self.v.float().numpy())
+
+    def dev(self):
+        return self.k.to(DEV), self.v.to(DEV), self.table.to(DEV), i32(self.lens)
+
+    def keys(self, b):
+        return [paged_keys(c, self.table[b].numpy(), self.lens[b]) for c in self.np]
+
+
+def check(out, lse, q, cu, per_seq, scale, label=""):
+    """per_seq: (K, V, limits) of each sequence."""
+    out, lse, q = f64(out), f64(lse), f64(q)
+    d = q.shape[-1]
+    for b, (K, V, limits) in enumerate(per_seq):
+        a, e = cu[b], cu[b + 1]
+        O, L, A, size = attend(q[a:e], K, V, scale, limits)
+        excess = np.abs(out[a:e] - O) - ((2.0 ** -8 + 2.0 ** -14) * A + 2.0 ** -8 * np.abs(O))
+        assert np.all(excess <= 1e-30), (label, b, float(excess.max()))
+        got = lse[:, a:e].T
+        assert np.array_equal(np.isfinite(got), np.isfinite(L)), (label, b)
+        fin = np.isfinite(L)
+        assert np.all(got[~fin] == L[~fin])
+        bound = 2.0 ** -24 * (d + 16) * size + 2.0 ** -20 * (1 + np.abs(np.where(fin, L, 0)))
+        assert np.all(np.abs(got[fin] - L[fin]) <= bound[fin]), (label, b)
+
+
+def limits_of(n, length, causal):
+    return [length - n + i + 1 if causal else length for i in range(n)]
+
+
+def run_paged(case_q, lens, H, Hkv, d, page, causal, seed, sigma=1.0, scale=None, **kw):
+    cache = Cache(lens, Hkv, d, page, seed, sigma)
+    cu = cumulative(case_q)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (sigma * torch.randn(cu[-1], H, d, generator=g)).to(BF16)
+    args = dict(cu_seqlens=i32(cu), max_q=max(max(case_q), 1), max_kv=max(lens), causal=causal, scale=scale)
+    args.update(kw)
+    out, lse = fa.fa_fwd_paged(q.to(DEV), *cache.dev(), **args)
+    assert fa.fa_get_error() == fa.FA_OK
+    per = [(*cache.keys(b), limits_of(case_q[b], lens[b], causal)) for b in range(len(lens))]
+    check(out, lse, q, cu, per, d ** -0.5 if scale is None else scale, str((case_q, lens, H, Hkv, d, page)))
+    return cache, q, out, lse
+
+
+LENGTHS = [
+    ([1], [1]),
+    ([1], [17]),
+    ([1, 1, 1, 1, 1, 1, 1, 1], [0, 1, 15, 16, 63, 64, 65, 129]),
+    ([1, 1, 1], [511, 512, 513]),
+    ([1, 1, 1, 1], [5000, 3, 700, 1]),         # split over the keys, next to short ones
+    ([3, 0, 1, 5, 2], [40, 9, 1, 5, 300]),     # several new tokens, none, as many as keys
+    ([4, 2], [2, 0]),                          # more new tokens than keys: rows without a key
+]
+
+
+@pytest.mark.parametrize("heads", [(1, 1, 64, 16), (8, 2, 128, 64), (6, 2, 64, 32), (32, 1, 128, 128),
+                                   (12, 12, 128, 16), (5, 1, 64, 128)],
+                         ids=lambda h: "H%dkv%dd%dpage%d" % h)
+@pytest.mark.parametrize("causal", [False, True], ids=["all", "causal"])
+@pytest.mark.parametrize("lengths", LENGTHS, ids=lambda x: "-".join(map(str, x[1])))
+def test_paged(lengths, causal, heads):
+    H, Hkv, d, page = heads
+    run_paged(*lengths, H, Hkv, d, page, causal, seed=sum(lengths[1]) + H)
+
+
+@pytest.mark.parametrize("nq,lens", [([40, 1, 130], [900, 31, 130]), ([257, 64], [1500, 64]), ([300], [300])])
+@pytest.mark.parametrize("heads", [(8, 2, 128, 64), (3, 1, 64, 16), (4, 4, 128, 32)],
+                         ids=lambda h: "H%dkv%dd%dpage%d" % h)
+def test_paged_chunks(nq, lens, heads):
+    """Chunks of prompts, many rows a head, with the causal mask ending inside tiles."""
+    H, Hkv, d, page = heads
+    for causal in (True, False):
+        run_paged(nq, lens, H, Hkv, d, page, causal, seed=len(nq) + H)
+
+
+def test_paged_many_ragged_sequences():
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 900, 150).tolist()
+    run_paged([1] * 150, lens, 4, 2, 64, 16, True, seed=9)
+    nq = rng.integers(0, 4, 150).tolist()
+    run_paged(nq, lens, 4, 2, 64, 16, True, seed=10)
+
+
+@pytest.mark.parametrize("scale,sigma", [(0.0, 1.0), (1.5, 1.0), (None, 4.0)])
+def test_paged_scales(scale, sigma):
+    run_paged([1, 2], [700, 70], 4, 2, 64, 16, True, seed=4, scale=scale, sigma=sigma)
+
+
+def test_paged_defaults_and_capacity():
+    """One token per sequence without cu_seqlens, bounds from the block table: the same bits as
+    with close bounds where the lengths are split the same way."""
+    cache, q, out, lse = run_paged([1] * 5, [100, 2000, 1, 64, 900], 8, 2, 128, 16, True, seed=12)
+    k, v, table, lens = cache.dev()
+    wide = torch.full((5, 4 * table.shape[1]), -1, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    o2, l2 = fa.fa_fwd_paged(q.to(DEV), k, v, wide, lens)
+    assert fa.fa_get_error() == fa.FA_OK
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_paged_is_bitwise_repeatable_and_leaves_other_rows():
+    cache = Cache([3000, 10, 1200], 2, 128, 64, seed=21)
+    q = torch.randn(9, 8, 128, device=DEV).to(BF16)
+    cu = i32([0, 2, 2, 5])  # tokens 5..8 belong to no sequence
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((8, 9), 7.0, device=DEV)
+    first = None
+    for _ in range(3):
+        o, l = fa.fa_fwd_paged(q, *cache.dev(), cu_seqlens=cu, max_q=3, causal=True, out=out, lse=lse)
+        assert torch.all(o[5:] == 7.0) and torch.all(l[:, 5:] == 7.0)
+        assert not torch.any(o[:5] == 7.0)
+        first = first or (o.clone(), l.clone())
+        assert torch.equal(o, first[0]) and torch.equal(l, first[1])
+    assert fa.fa_get_error() == fa.FA_OK
+
+
+def test_paged_bad_pages_are_masked_and_reported():
+    """Pages outside the pool are neither read nor counted: the result is attention over the other
+    keys, and the status says so."""
+    lens, Hkv, d, page = [200, 90], 2, 64, 32
+    cache = Cache(lens, Hkv, d, page, seed=31)
+    k, v, table, ln = cache.dev()
+    table[0, 1], table[0, 4], table[1, 0] = -5, k.shape[0], 1 << 30
+    q = torch.randn(2, 4, d, device=DEV).to(BF16)
+    out, lse = fa.fa_fwd_paged(q, k, v, table, ln)
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX and fa.fa_get_error() == fa.FA_OK
+    per = []
+    for b, gone in ((0, [1, 4]), (1, [0])):
+        keep = [j for j in range(lens[b]) if j // page not in gone]
+        K, V = (x[:, keep] for x in cache.keys(b))
+        per.append((K, V, [len(keep)]))
+    check(out, lse, q, [0, 1, 2], per, d ** -0.5)
+
+
+def test_paged_lengths_past_their_bounds():
+    cache = Cache([100], 1, 64, 16, seed=5)
+    k, v, table, _ = cache.dev()
+    q = torch.randn(1, 1, 64, device=DEV).to(BF16)
+    full, _ = fa.fa_fwd_paged(q, k, v, table[:, :6].contiguous(), i32([96]))
+    assert fa.fa_get_error() == fa.FA_OK
+    for lens, kw in ((500, {}), (100, dict(max_kv=96))):
+        out, _ = fa.fa_fwd_paged(q, k, v, table[:, :6].contiguous(), i32([lens]), **kw)
+        assert fa.fa_get_error() == fa.FA_ERR_INDEX
+        assert torch.equal(out, full)
+    out, lse = fa.fa_fwd_paged(q, k, v, table, i32([-3]))
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    assert not out.any() and torch.isinf(lse).all()
+    # more new tokens than max_q: the first max_q of them are computed, the others left
+    q5 = torch.randn(5, 1, 64, device=DEV).to(BF16)
+    want, _ = fa.fa_fwd_paged(q5, k, v, table, i32([100]), cu_seqlens=i32([0, 5]), causal=True)
+    out = torch.full_like(q5, 7.0)
+    fa.fa_fwd_paged(q5, k, v, table, i32([100]), cu_seqlens=i32([0, 5]), max_q=2, causal=True, out=out)
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    assert torch.equal(out[:2], want[:2]) and torch.all(out[2:] == 7.0)
+
+
+def test_paged_offsets_past_32_bits():
+    """A pool of more than 2^31 elements (and 2^32 bytes): the last pages are read and written."""
+    Hkv, page, d = 8, 128, 128
+    pages = (1 << 31) // (Hkv * page * d) + 40
+    k = torch.empty(pages, Hkv, page, d, dtype=BF16, device=DEV)
+    v = torch.empty(pages, Hkv, page, d, dtype=BF16, device=DEV)
+    lens = [300, 140]
+    table = torch.tensor([[pages - 1, 3, pages - 7], [pages - 2, pages - 3, -1]], dtype=torch.int32)
+    new = torch.randn(sum(lens), 2 * Hkv, d).to(BF16)
+    nk, nv = new[:, :Hkv].to(DEV), new[:, Hkv:].to(DEV)
+    fa.fa_kv_append(None, nk, nv, k, v, table.to(DEV), i32(lens), cu_seqlens=i32(cumulative(lens)))
+    assert torch.equal(k[pages - 7, :, 43], nk[299]) and torch.equal(v[pages - 3, :, 11], nv[439])
+    q = torch.randn(2, Hkv, d, device=DEV).to(BF16)
+    out, lse = fa.fa_fwd_paged(q, k, v, table.to(DEV), i32(lens))
+    assert fa.fa_get_error() == fa.FA_OK
+    cut = cumulative(lens)
+    per = [(f64(nk[cut[b]:cut[b + 1]]).transpose(1, 0, 2), f64(nv[cut[b]:cut[b + 1]]).transpose(1, 0, 2), [lens[b]])
+           for b in range(2)]
+    check(out, lse, q, [0, 1, 2], per, d ** -0.5)
+
+
+def test_paged_streams_and_graphs():
+    cache = Cache([2500, 30, 700], 2, 64, 16, seed=41)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(3, 4, 64, device=DEV).to(BF16)
+    want = fa.fa_fwd_paged(q, k, v, table, lens)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = fa.fa_fwd_paged(q, k, v, table, lens, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    # two graphs with a workspace each, replayed at once on two streams
+    graphs, outs, qs, streams = [], [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(2):
+        qs.append(q.clone())
+        ws = torch.empty(fa.fa_fwd_paged_workspace_size(3, 3, 4, 2, 64), dtype=torch.uint8, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((fa.fa_fwd_paged(qs[i], k, v, table, lens, workspace=ws), ws))
+        graphs.append(g)
+    qs[1].copy_(q.flip(0))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs[0][0]))
+    ref = fa.fa_fwd_paged(q.flip(0).contiguous(), k, v, table, lens)
+    assert all(torch.equal(a, b) for a, b in zip(ref, outs[1][0]))
+    # lengths that grow between replays of one graph
+    lens.copy_(i32([2400, 29, 690]))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    ref = fa.fa_fwd_paged(q, k, v, table, lens)
+    assert all(torch.equal(a, b) for a, b in zip(ref, outs[0][0]))
+    assert fa.fa_get_error() == fa.FA_OK
+
+
+def test_paged_empty_and_refusals():
+    cache = Cache([5, 6], 2, 64, 16, seed=1)
+    k, v, table, lens = cache.dev()
+    q = torch.empty(0, 4, 64, dtype=BF16, device=DEV)
+    out, lse = fa.fa_fwd_paged(q, k, v, table, lens, cu_seqlens=i32([0, 0, 0]))
+    assert out.numel() == 0 and lse.numel() == 0
+    q = torch.zeros(2, 4, 64, dtype=BF16, device=DEV)
+    for bad in (dict(q=q[:, :3]), dict(q=q.float()), dict(table=table.long()), dict(table=table[:1]),
+                dict(lens=lens[:1]), dict(v=v[:, :1]), dict(v=v[:3]), dict(k=k.float()),
+                dict(cu_seqlens=i32([0, 2])), dict(q=torch.zeros(3, 4, 64, dtype=BF16, device=DEV)),
+                dict(out=torch.zeros(2, 4, 64, device=DEV)), dict(lse=torch.zeros(2, 4, device=DEV)),
+                dict(table=table.cpu()), dict(k=k.transpose(1, 2), v=v.transpose(1, 2))):
+        a = dict(q=q, k=k, v=v, table=table, lens=lens)
+        a.update({n: t for n, t in bad.items() if n in a})
+        kw = {n: t for n, t in bad.items() if n not in a}
+        with pytest.raises(ValueError):
+            fa.fa_fwd_paged(a["q"], a["k"], a["v"], a["table"], a["lens"], **kw)
+    with pytest.raises(fa.binding.FAError):
+        fa.fa_fwd_paged(q, k, v, table, lens, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    odd = torch.zeros(4, 2, 24, 64, dtype=BF16, device=DEV)
+    with pytest.raises(fa.binding.FAError):
+        fa.fa_fwd_paged(q, odd, odd, table, lens)
+
+
+# ------------------------------------------------------------------------------------------ append
+@pytest.mark.parametrize("heads", [(8, 2, 128, 64, 128, False, True), (3, 3, 64, 16, 32, True, False),
+                                   (16, 1, 128, 128, 64, False, True), (4, 2, 64, 32, 0, False, False)],
+                         ids=lambda h: "H%dkv%dd%dpage%dr%d%s%s" % (*h[:5], "i" if h[5] else "", "n" if h[6] else ""))
+@pytest.mark.parametrize("lengths", [([1, 1, 1], [1, 64, 300]), ([130, 0, 1, 17], [130, 5, 33, 200]),
+                                     ([3, 6], [1, 6])], ids=["decode", "prompts", "more than keys"])
+def test_append(lengths, heads):
+    H, Hkv, d, page, rot, inter, norm = heads
+    nq, lens = lengths
+    cache = Cache(lens, Hkv, d, page, seed=50 + H)
+    k, v, table, ln = cache.dev()
+    cu, T = cumulative(nq), sum(nq)
+    qkv = torch.randn(T + 2, H + 2 * Hkv, d, device=DEV).to(BF16)  # two tokens behind the last sequence
+    q, kn, vn = qkv.split([H, Hkv, Hkv], dim=1)
+    w = [1 + 0.2 * torch.randn(d, device=DEV) if norm else None for _ in range(2)]
+    inv = fa.rope_frequencies(rot)[0] if rot else None
+    tab = fa.fa_rope_table(4096, rot, inv_freq=inv) if rot else None
+    off = i32([7 * b for b in range(len(lens))])
+    q_out = torch.full((T + 2, H, d), 7.0, dtype=BF16, device=DEV)
+    k0, v0 = k.clone(), v.clone()
+    got = fa.fa_kv_append(q, kn, vn, k, v, table, ln, cu_seqlens=i32(cu), pos_offset=off, table=tab,
+                          interleaved=inter, q_weight=w[0], k_weight=w[1], q_out=q_out)
+    assert fa.fa_get_error() == fa.FA_OK and got is q_out
+    assert torch.all(q_out[T:] == 7.0)
+    ref = dict(inv_freq=None if inv is None else inv.numpy(), interleaved=inter)
+    written = torch.zeros(k.shape[0], page, dtype=torch.bool)
+    for b in range(len(lens)):
+        a, e = cu[b], cu[b + 1]
+        key = np.arange(lens[b] - nq[b], lens[b])
+        pos = np.where(key >= 0, key + 7 * b, 0)
+        for x, wt, target in ((q, w[0], got[a:e]), (kn, w[1], None)):
+            r = norm_rope(f64(x[a:e]), pos, None if wt is None else f64(wt), **ref)
+            if target is None:
+                for i in range(nq[b]):
+                    if key[i] < 0:
+                        continue
+                    p, o = int(table[b, key[i] // page]), int(key[i] % page)
+                    written[p, o] = True
+                    err = np.abs(f64(k[p, :, o]) - r[i]) - (2.0 ** -8 * np.abs(r[i]) + 2.0 ** -18 * np.abs(r[i]).max())
+                    assert err.max() <= 0
+                    assert torch.equal(v[p, :, o], vn[a + i])
+            elif r.size:
+                err = np.abs(f64(target) - r) - (2.0 ** -8 * np.abs(r) + 2.0 ** -18 * np.abs(r).max(-1, keepdims=True))
+                assert err.max() <= 0
+    same = ~written.to(DEV)[:, None, :, None].expand_as(k)  # nothing else of the pool moved
+    assert torch.equal(torch.nan_to_num(k)[same], torch.nan_to_num(k0)[same])
+    assert torch.equal(torch.nan_to_num(v)[same], torch.nan_to_num(v0)[same])
+
+
+def test_append_bad_pages_write_nothing():
+    k = torch.full((4, 1, 16, 64), 5.0, dtype=BF16, device=DEV)
+    v = k.clone()
+    x = torch.ones(5, 1, 64, dtype=BF16, device=DEV)
+    table = i32([[4], [-1], [2], [0], [1 << 30]])
+    q = fa.fa_kv_append(x, x, x, k, v, table, i32([3, 3, 17, 2, 1]))
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    assert torch.equal(q, x)
+    assert torch.equal(k[0, 0, 1], x[3, 0]) and k.sum() == v.sum() == 5.0 * k.numel() - 4 * 64
+    fa.fa_kv_append(None, x[:1], x[:1], k, v, i32([[1]]), i32([-2]))
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    assert k.sum() == 5.0 * k.numel() - 4 * 64
+
+
+def test_append_refusals():
+    k = torch.zeros(4, 2, 16, 64, dtype=BF16, device=DEV)
+    x = torch.zeros(2, 2, 64, dtype=BF16, device=DEV)
+    table, lens = i32([[0], [1]]), i32([1, 1])
+    for bad in (dict(k=x[:, :1]), dict(v=x[:1]), dict(q=x[:1]), dict(k=x.float()),
+                dict(pos_offset=i32([1])), dict(cu_seqlens=i32([0, 1])),
+                dict(k=torch.zeros(3, 2, 64, dtype=BF16, device=DEV))):
+        a = dict(q=x, k=x, v=x)
+        a.update({n: t for n, t in bad.items() if n in a})
+        with pytest.raises(ValueError):
+            fa.fa_kv_append(a["q"], a["k"], a["v"], k, k.clone(), table, lens,
+                            **{n: t for n, t in bad.items() if n not in a})
+    assert fa.fa_kv_append(x[:0], x[:0], x[:0], k, k.clone(), table, lens, cu_seqlens=i32([0, 0, 0])).shape[0] == 0
+
+
+# --------------------------------------------------------------------------------- shared prefixes
+def run_prefix(groups, pre, nq, lens, H, Hkv, d, page, causal, seed, **kw):
+    """groups: how many sequences behind each prefix."""
+    cache = Cache(list(lens) + list(pre), Hkv, d, page, seed)
+    k, v, table, ln = cache.dev()
+    B, cu = len(lens), cumulative(nq)
+    gcu = cumulative(groups)
+    q = torch.randn(cu[-1], H, d, generator=torch.Generator().manual_seed(seed)).to(BF16)
+    args = dict(cu_seqlens=i32(cu), max_q=max(nq), max_kv=max(lens), max_prefix=max(pre), causal=causal)
+    args.update(kw)
+    out, lse = fa.fa_fwd_shared_prefix(q.to(DEV), k, v, table[:B].contiguous(), ln[:B].contiguous(),
+                                       table[B:].contiguous(), ln[B:].contiguous(), i32(gcu), **args)
+    assert fa.fa_get_error() == fa.FA_OK
+    per = []
+    for b in range(B):
+        g = int(np.searchsorted(gcu, b, side="right")) - 1
+        both = [np.concatenate([p, s], 1) for p, s in zip(cache.keys(B + g), cache.keys(b))]
+        per.append((*both, [pre[g] + max(0, x) for x in limits_of(nq[b], lens[b], causal)]))
+    check(out, lse, q, cu, per, d ** -0.5, str((groups, pre, nq, lens)))
+    return out, lse
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 128, 64), (1, 1, 64, 16), (24, 3, 64, 32), (32, 1, 128, 128)],
+                         ids=lambda h: "H%dkv%dd%dpage%d" % h)
+@pytest.mark.parametrize("batch", [
+    ([1], [100], [1], [5]),
+    ([3], [1000], [1, 1, 1], [0, 1, 200]),
+    ([2, 0, 4], [70, 33, 2100], [1] * 6, [1, 0, 16, 100, 64, 3]),
+    ([2, 3], [0, 17], [2, 1, 0, 3, 1], [2, 0, 9, 800, 1]),
+    ([40], [600], [1] * 40, list(range(40))),
+], ids=lambda b: "%s-%s" % (b[0], b[1]))
+def test_shared_prefix(batch, heads):
+    H, Hkv, d, page = heads
+    for causal in (True, False):
+        run_prefix(*batch, H, Hkv, d, page, causal, seed=60 + H)
+
+
+def test_shared_prefix_large_groups():
+    """Hundreds of query rows a key/value head behind one prefix, in two groups."""
+    rng = np.random.default_rng(8)
+    run_prefix([70, 9], [1500, 40], [2] * 79, rng.integers(2, 90, 79).tolist(), 8, 2, 128, 64, True, seed=71)
+    run_prefix([150], [777], [1] * 150, rng.integers(0, 30, 150).tolist(), 6, 2, 64, 16, True, seed=72)
+
+
+def test_shared_prefix_defaults_repeat_and_graph():
+    cache = Cache([20, 300, 41, 900, 700], 2, 64, 16, seed=81)
+    k, v, table, ln = cache.dev()
+    q = torch.randn(3, 8, 64, device=DEV).to(BF16)
+    args = (k, v, table[:3].contiguous(), ln[:3].contiguous(), table[3:].contiguous(), ln[3:].contiguous(),
+            i32([0, 2, 3]))
+    want = fa.fa_fwd_shared_prefix(q, *args)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(want, fa.fa_fwd_shared_prefix(q, *args)))
+    g = torch.cuda.CUDAGraph()
+    static = torch.zeros_like(q)
+    with torch.cuda.graph(g):
+        out = fa.fa_fwd_shared_prefix(static, *args)
+    static.copy_(q)
+    g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(want, out))
+    # a prefix in the sequences' own block tables is the same attention
+    cat = torch.full((3, 200), -1, dtype=torch.int32, device=DEV)
+    lens = []
+    for b, grp in enumerate((3, 3, 4)):
+        own, shared = -(-cache.lens[b] // 16), cache.lens[grp] // 16
+        cat[b, :shared], cat[b, shared:shared + own] = table[grp, :shared], table[b, :own]
+        lens.append(shared * 16 + cache.lens[b])
+    whole = i32([c // 16 * 16 for c in cache.lens[3:]])  # whole pages of the prefixes
+    a = fa.fa_fwd_shared_prefix(q, *args[:5], whole, args[6])
+    b = fa.fa_fwd_paged(q, k, v, cat, i32(lens))
+    assert torch.allclose(a[0].float(), b[0].float(), atol=2.0 ** -6) and torch.allclose(a[1], b[1], atol=1e-5)
+    assert fa.fa_get_error() == fa.FA_OK
+
+
+def test_shared_prefix_refusals():
+    cache = Cache([5, 6, 20], 2, 64, 16, seed=1)
+    k, v, table, ln = cache.dev()
+    q = torch.zeros(2, 4, 64, dtype=BF16, device=DEV)
+    good = [q, k, v, table[:2].contiguous(), ln[:2].contiguous(), table[2:].contiguous(),
+            ln[2:].contiguous(), i32([0, 2])]
+    fa.fa_fwd_shared_prefix(*good)
+    for at, bad in ((5, table[2]), (5, table[2:].long()), (6, ln), (7, i32([0, 1, 2])), (7, i32([0, 2]).cpu())):
+        args = list(good)
+        args[at] = bad
+        with pytest.raises(ValueError):
+            fa.fa_fwd_shared_prefix(*args)
+    with pytest.raises(fa.binding.FAError):
+        fa.fa_fwd_shared_prefix(*good, max_prefix=-1)
+
+
+# -------------------------------------------------------------------------------------- as one run
+def test_generation_run():
+    """A prompt in one packed pass, its keys into the cache, then tokens one by one, against one
+    causal pass over everything; then the same continuation for four sequences behind the prompt
+    as a shared prefix."""
+    H, Hkv, d, page, prompt, steps = 8, 2, 128, 32, 150, 9
+    total = prompt + steps
+    g = torch.Generator().manual_seed(91)
+    qkv = torch.randn(total, H + 2 * Hkv, d, generator=g).to(BF16).to(DEV)
+    wq, wk = (1 + 0.2 * torch.randn(d, generator=g).to(DEV) for _ in range(2))
+    opts = dict(table=fa.fa_rope_table(512, d), q_weight=wq, k_weight=wk)
+    q, k, v = qkv.split([H, Hkv, Hkv], dim=1)
+    # everything at once
+    qr, kr, vr = fa.fa_qk_norm_rope_fwd(q, k, v, **opts)
+    ref, ref_lse = fa.fa_fwd_varlen(qr, kr, vr, i32([0, total]), total, causal=True)
+    # the prompt, then single tokens
+    kc = torch.full((8, Hkv, page, d), float("nan"), dtype=BF16, device=DEV)
+    vc = kc.clone()
+    table = i32([[5, 2, 7, 0, 3]])
+    qp = fa.fa_kv_append(q[:prompt], k[:prompt], v[:prompt], kc, vc, table, i32([prompt]),
+                         cu_seqlens=i32([0, prompt]), **opts)
+    assert torch.equal(qp, qr[:prompt])
+    parts = [fa.fa_fwd_paged(qp, kc, vc, table, i32([prompt]), cu_seqlens=i32([0, prompt]), max_q=prompt, causal=True)]
+    for t in range(prompt, total):
+        one = slice(t, t + 1)
+        lens = i32([t + 1])
+        qd = fa.fa_kv_append(q[one], k[one], v[one], kc, vc, table, lens, **opts)
+        parts.append(fa.fa_fwd_paged(qd, kc, vc, table, lens))
+    assert fa.fa_get_error() == fa.FA_OK
+    out = torch.cat([p[0] for p in parts])
+    lse = torch.cat([p[1] for p in parts], 1)
+    K, V = f64(kr).transpose(1, 0, 2), f64(vr).transpose(1, 0, 2)
+    check(out, lse, qr, [0, total], [(K, V, range(1, total + 1))], d ** -0.5, "run")
+    assert torch.allclose(lse, ref_lse, atol=1e-5)
+    assert torch.allclose(out.float(), ref.float(), atol=2.0 ** -5)
+    # four sequences that continue from the prompt's first 128 keys (whole pages)
+    shared, B = 128, 4
+    kc2, vc2 = kc.clone(), vc.clone()
+    kc2[[1, 4, 6]], vc2[[1, 4, 6]] = float("nan"), float("nan")
+    pool = torch.cat([kc2, torch.full_like(kc2, float("nan"))])
+    poolv = torch.cat([vc2, torch.full_like(vc2, float("nan"))])
+    own = i32([[1], [4], [6], [9]])
+    cu = i32([0, 2, 4, 6, 8])
+    new = torch.randn(2 * B, H + 2 * Hkv, d, generator=g).to(BF16).to(DEV)
+    qn, kn, vn = new.split([H, Hkv, Hkv], dim=1)
+    qd = fa.fa_kv_append(qn, kn, vn, pool, poolv, own, i32([2] * B), cu_seqlens=cu,
+                         pos_offset=i32([shared] * B), **opts)
+    got, glse = fa.fa_fwd_shared_prefix(qd, pool, poolv, own, i32([2] * B), table[:, :4].contiguous(),
+                                        i32([shared]), i32([0, B]), cu_seqlens=cu, max_q=2, max_kv=2, causal=True)
+    pos = i32([shared, shared + 1] * B)
+    q2, k2, v2 = fa.fa_qk_norm_rope_fwd(qn, kn, vn, positions=pos, **opts)
+    assert torch.equal(q2, qd)
+    per = [(np.concatenate([K[:, :shared], f64(k2[2 * b:2 * b + 2]).transpose(1, 0, 2)], 1),
+            np.concatenate([V[:, :shared], f64(v2[2 * b:2 * b + 2]).transpose(1, 0, 2)], 1),
+            [shared + 1, shared + 2]) for b in range(B)]
+    check(got, glse, q2, [0, 2, 4, 6, 8], per, d ** -0.5, "shared")
+    assert fa.fa_get_error() == fa.FA_OK
