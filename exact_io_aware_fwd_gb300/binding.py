@@ -55,36 +55,6 @@ EXPORTED = [
     "fa_status_string",
 ]
 
-_i64 = ctypes.c_int64
-
-
-class View(ctypes.Structure):
-    """fa_view: strided bf16 rows."""
-    _fields_ = [("data", ctypes.c_void_p), ("batch", _i64), ("token", _i64), ("head", _i64)]
-
-
-class QKTransform(ctypes.Structure):
-    """fa_qk_transform: norms and rotation of Q and K."""
-    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int), ("rot", ctypes.c_int),
-                ("interleaved", ctypes.c_int), ("q_weight", ctypes.c_void_p),
-                ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
-
-
-class PagedKV(ctypes.Structure):
-    """fa_paged_kv: the cache, its block table and the sequences' lengths."""
-    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
-                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
-                ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int),
-                ("kv_lens", ctypes.c_void_p)]
-
-
-class Prefix(ctypes.Structure):
-    """fa_prefix: the shared prefixes of a batch."""
-    _fields_ = [("table", ctypes.c_void_p), ("max_pages", ctypes.c_int),
-                ("lens", ctypes.c_void_p), ("group_cu", ctypes.c_void_p),
-                ("groups", ctypes.c_int), ("max_len", ctypes.c_int)]
-
-
 _lib = None
 
 
@@ -142,25 +112,23 @@ def load_library(path: str | None = None):
     lib.fa_bwd_block_sparse.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f,
                                          vp, vp, i, i, vp, sz, vp]
     lib.fa_bwd_block_sparse.restype = i
-    vw, tr = View, ctypes.POINTER(QKTransform)
-    kv, pre = ctypes.POINTER(PagedKV), ctypes.POINTER(Prefix)
     lib.fa_rope_table.argtypes = [vp, i, i, f, vp, vp]
     lib.fa_rope_table.restype = i
-    lib.fa_qk_norm_rope_fwd.argtypes = [vw] * 6 + [vp, i, i, i, i, i, tr, vp]
+    lib.fa_qk_norm_rope_fwd.argtypes = [vp, vp, vp, i, i, i, i, i, vp, vp]
     lib.fa_qk_norm_rope_fwd.restype = i
     lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [i]
     lib.fa_qk_norm_rope_bwd_workspace_size.restype = sz
-    lib.fa_qk_norm_rope_bwd.argtypes = [vw] * 8 + [vp, vp, vp, i, i, i, i, i, tr, vp, sz, vp]
+    lib.fa_qk_norm_rope_bwd.argtypes = [vp] * 6 + [i, i, i, i, i, vp, vp, sz, vp]
     lib.fa_qk_norm_rope_bwd.restype = i
-    lib.fa_kv_append.argtypes = [vw] * 4 + [kv, vp, vp, i, i, i, i, i, tr, vp]
+    lib.fa_kv_append.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
     lib.fa_kv_append.restype = i
     lib.fa_fwd_paged_workspace_size.argtypes = [i] * 5
     lib.fa_fwd_paged_workspace_size.restype = sz
-    lib.fa_fwd_paged.argtypes = [vp, kv, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, sz, vp]
+    lib.fa_fwd_paged.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, sz, vp]
     lib.fa_fwd_paged.restype = i
     lib.fa_fwd_shared_prefix_workspace_size.argtypes = [i] * 6
     lib.fa_fwd_shared_prefix_workspace_size.restype = sz
-    lib.fa_fwd_shared_prefix.argtypes = [vp, kv, pre, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp,
+    lib.fa_fwd_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp,
                                          sz, vp]
     lib.fa_fwd_shared_prefix.restype = i
     lib.fa_get_error.argtypes = [vp]

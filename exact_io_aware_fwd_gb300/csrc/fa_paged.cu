@@ -23,7 +23,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int R = kPagedRows;
 constexpr int kKeys = 16;             // keys of a warp's step
 constexpr int KT = kKeys * kWarps;    // keys of a tile
-constexpr int kDirectTiles = 8;       // up to 512 keys: one CTA for a whole segment
+constexpr int kDirectTiles = kPagedUnsplitKeys / KT;  // one CTA for a whole segment
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <int D>

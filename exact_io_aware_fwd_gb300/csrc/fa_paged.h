@@ -141,6 +141,7 @@ struct JoinArgs {
 
 constexpr int kPagedRows = 16;           // rows of a tile
 constexpr int kPagedMaxCtas = 152 * 3;   // most CTAs of a launch (and pairs of slots)
+constexpr int kPagedUnsplitKeys = 512;   // where no entry has more keys, none is split
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s);
 cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s);

@@ -192,6 +192,8 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     j.part[i] = a.part;
     j.rowbuf[i] = a.rowbuf;
   }
+  // no entry can have been split (lengths are clamped to max_kv): every result is final
+  if (lists == 1 && max_kv <= fa::kPagedUnsplitKeys) return FA_OK;
   return status_of(fa::launch_paged_join(d, j, s));
 }
 
@@ -211,29 +213,30 @@ fa_status fa_rope_table(const double* inv_freq, int rot, int n_pos, float amplit
                                          static_cast<cudaStream_t>(stream)));
 }
 
-fa_status fa_qk_norm_rope_fwd(fa_view q, fa_view k, fa_view v, fa_view q_out, fa_view k_out,
-                              fa_view v_out, const int32_t* positions, int B, int N, int H,
-                              int Hkv, int d, const fa_qk_transform* t, void* stream) {
+fa_status fa_qk_norm_rope_fwd(const fa_view in[3], const fa_view out[3],
+                              const int32_t* positions, int B, int N, int H, int Hkv, int d,
+                              const fa_qk_transform* t, void* stream) {
   fa_status st = check_heads(H, Hkv, d);
   if (st != FA_OK) return st;
   if ((st = check_transform(t, d)) != FA_OK) return st;
   if (B <= 0 || N < 0 || static_cast<long long>(B) * N > kMaxInt) return FA_ERR_INVALID_ARG;
   if (N == 0) return FA_OK;
   if (t->table != nullptr && positions == nullptr && N > t->n_pos) return FA_ERR_INVALID_ARG;
-  if (!view_ok(q, B, N, H) || !view_ok(q_out, B, N, H) || !view_ok(k, B, N, Hkv) ||
-      !view_ok(k_out, B, N, Hkv))
-    return FA_ERR_INVALID_ARG;
-  if (v.data != nullptr && (!view_ok(v, B, N, Hkv) || !view_ok(v_out, B, N, Hkv)))
-    return FA_ERR_INVALID_ARG;
+  if (in == nullptr || out == nullptr) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (i == 2 && in[2].data == nullptr) break;  // no V
+    if (!view_ok(in[i], B, N, i == 0 ? H : Hkv) || !view_ok(out[i], B, N, i == 0 ? H : Hkv))
+      return FA_ERR_INVALID_ARG;
+  }
   fa::RopeArgs a{};
   if ((st = device_ready(a.status)) != FA_OK) return st;
   set_transform(a, *t);
-  a.q = row_view(q);
-  a.k = row_view(k);
-  a.v = row_view(v);
-  a.qo = row_view(q_out);
-  a.ko = row_view(k_out);
-  a.vo = row_view(v_out);
+  a.q = row_view(in[0]);
+  a.k = row_view(in[1]);
+  a.v = row_view(in[2]);
+  a.qo = row_view(out[0]);
+  a.ko = row_view(out[1]);
+  a.vo = row_view(out[2]);
   a.B = B;
   a.N = N;
   a.tokens = B * N;
@@ -249,11 +252,10 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
   return static_cast<size_t>(fa::kRopeBwdBlocks) * 2 * d * sizeof(float);
 }
 
-fa_status fa_qk_norm_rope_bwd(fa_view dq, fa_view dk, fa_view dv, fa_view q, fa_view k,
-                              fa_view dq_in, fa_view dk_in, fa_view dv_in, float* dq_weight,
-                              float* dk_weight, const int32_t* positions, int B, int N, int H,
-                              int Hkv, int d, const fa_qk_transform* t, void* workspace,
-                              size_t workspace_bytes, void* stream) {
+fa_status fa_qk_norm_rope_bwd(const fa_view grad[3], const fa_view x[2], const fa_view out[3],
+                              float* dq_weight, float* dk_weight, const int32_t* positions,
+                              int B, int N, int H, int Hkv, int d, const fa_qk_transform* t,
+                              void* workspace, size_t workspace_bytes, void* stream) {
   fa_status st = check_heads(H, Hkv, d);
   if (st != FA_OK) return st;
   if ((st = check_transform(t, d)) != FA_OK) return st;
@@ -268,24 +270,29 @@ fa_status fa_qk_norm_rope_bwd(fa_view dq, fa_view dk, fa_view dv, fa_view q, fa_
   if (N == 0 && !norm) return FA_OK;
   if (t->table != nullptr && positions == nullptr && N > t->n_pos) return FA_ERR_INVALID_ARG;
   if (N > 0) {
-    if (!view_ok(dq, B, N, H) || !view_ok(dq_in, B, N, H) || !view_ok(dk, B, N, Hkv) ||
-        !view_ok(dk_in, B, N, Hkv))
-      return FA_ERR_INVALID_ARG;
-    if (dv.data != nullptr && (!view_ok(dv, B, N, Hkv) || !view_ok(dv_in, B, N, Hkv)))
-      return FA_ERR_INVALID_ARG;
-    if (norm && (!view_ok(q, B, N, H) || !view_ok(k, B, N, Hkv))) return FA_ERR_INVALID_ARG;
+    if (grad == nullptr || out == nullptr || (norm && x == nullptr)) return FA_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) {
+      const int h = i == 0 ? H : Hkv;
+      if (i == 2 && grad[2].data == nullptr) break;  // no V
+      if (!view_ok(grad[i], B, N, h) || !view_ok(out[i], B, N, h)) return FA_ERR_INVALID_ARG;
+      if (norm && i < 2 && !view_ok(x[i], B, N, h)) return FA_ERR_INVALID_ARG;
+    }
   }
   fa::RopeArgs a{};
   if ((st = device_ready(a.status)) != FA_OK) return st;
   set_transform(a, *t);
-  a.q = row_view(dq);
-  a.k = row_view(dk);
-  a.v = row_view(dv);
-  a.qo = row_view(dq_in);
-  a.ko = row_view(dk_in);
-  a.vo = row_view(dv_in);
-  a.qx = row_view(q);
-  a.kx = row_view(k);
+  if (N > 0) {
+    a.q = row_view(grad[0]);
+    a.k = row_view(grad[1]);
+    a.v = row_view(grad[2]);
+    a.qo = row_view(out[0]);
+    a.ko = row_view(out[1]);
+    a.vo = row_view(out[2]);
+    if (norm) {
+      a.qx = row_view(x[0]);
+      a.kx = row_view(x[1]);
+    }
+  }
   a.B = B;
   a.N = N;
   a.tokens = B * N;
@@ -297,7 +304,7 @@ fa_status fa_qk_norm_rope_bwd(fa_view dq, fa_view dk, fa_view dv, fa_view q, fa_
                                        static_cast<cudaStream_t>(stream)));
 }
 
-fa_status fa_kv_append(fa_view q, fa_view k, fa_view v, fa_view q_out, const fa_paged_kv* cache,
+fa_status fa_kv_append(const fa_view in[3], const fa_view* q_out, const fa_paged_kv* cache,
                        const int32_t* cu_seqlens, const int32_t* pos_offset, int B, int total,
                        int H, int Hkv, int d, const fa_qk_transform* t, void* stream) {
   fa_status st = check_heads(H, Hkv, d);
@@ -307,16 +314,18 @@ fa_status fa_kv_append(fa_view q, fa_view k, fa_view v, fa_view q_out, const fa_
   if (B <= 0 || total < 0 || cache->max_pages < 1) return FA_ERR_INVALID_ARG;
   if (cu_seqlens == nullptr && total != B) return FA_ERR_INVALID_ARG;
   if (total == 0) return FA_OK;
-  if (!view_ok(k, 1, total, Hkv) || !view_ok(v, 1, total, Hkv)) return FA_ERR_INVALID_ARG;
-  if (q.data != nullptr && (!view_ok(q, 1, total, H) || !view_ok(q_out, 1, total, H)))
+  if (in == nullptr || !view_ok(in[1], 1, total, Hkv) || !view_ok(in[2], 1, total, Hkv))
+    return FA_ERR_INVALID_ARG;
+  const bool with_q = in[0].data != nullptr;
+  if (with_q && (q_out == nullptr || !view_ok(in[0], 1, total, H) || !view_ok(*q_out, 1, total, H)))
     return FA_ERR_INVALID_ARG;
   fa::RopeArgs a{};
   if ((st = device_ready(a.status)) != FA_OK) return st;
   set_transform(a, *t);
-  a.q = row_view(q);
-  a.k = row_view(k);
-  a.v = row_view(v);
-  a.qo = row_view(q_out);
+  a.q = row_view(in[0]);
+  a.k = row_view(in[1]);
+  a.v = row_view(in[2]);
+  if (with_q) a.qo = row_view(*q_out);
   a.B = 1;
   a.N = total;
   a.tokens = total;

@@ -1,6 +1,7 @@
 """Binding of the operators around attention: norms and rotary positions of queries and keys, the
 paged key/value cache, and the attention that reads it (the calls of include/fa.h with the same
-names).  As in binding.py only argument checks and marshalling happen here.
+names).  As in binding.py only argument checks and marshalling happen here; a call is a few
+microseconds of kernel in the smallest cases, so the checks are written to be short.
 
 Calls launch on the tensors' device, on its current stream or on ``stream``; outputs and
 workspaces allocated here for another stream than the current one are recorded on it.
@@ -8,67 +9,90 @@ workspaces allocated here for another stream than the current one are recorded o
 
 from __future__ import annotations
 
-import contextlib
-import ctypes
 import math
+import struct
 
 import torch
 
-from .binding import (PagedKV, Prefix, QKTransform, View, _check, _out, _scale, _want, _workspace,
-                      load_library)
+from .binding import _check, _out, _scale, _workspace, load_library
 
 _BF16 = torch.bfloat16
-_NO_VIEW = View(None, 0, 0, 0)
-_NO_GUARD = contextlib.nullcontext()
+_F32 = torch.float32
+_I32 = torch.int32
+_current_stream = torch._C._cuda_getCurrentRawStream  # stream handle of a device index
+
+# the structures of include/fa.h, in native alignment
+_VIEW = struct.Struct("@Pqqq")          # fa_view: data, batch, token, head
+_VIEWS2 = struct.Struct("@PqqqPqqq")
+_VIEWS3 = struct.Struct("@PqqqPqqqPqqq")
+_TRANSFORM = struct.Struct("@PiiiPPf4x")  # fa_qk_transform
+_PAGED_KV = struct.Struct("@PPiiPiP")     # fa_paged_kv
+_PREFIX = struct.Struct("@PiPPii")        # fa_prefix
+_NO_VIEW = (0, 0, 0, 0)
+_NO_TRANSFORM = _TRANSFORM.pack(0, 0, 0, 0, 0, 0, 0.0)
 
 
-class _Launch:
-    """Device guard, stream handle and the stream that fresh tensors have to be recorded on."""
-
-    def __init__(self, device, stream):
-        self.guard = (_NO_GUARD if device.index == torch.cuda.current_device()
-                      else torch.cuda.device(device))
-        current = torch.cuda.current_stream(device)
-        self.stream = current if stream is None else stream
-        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
-        self.foreign = self.stream.cuda_stream != current.cuda_stream
-
-    def keep(self, *tensors):
-        if self.foreign:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _handle(device, stream):
+    return _current_stream(device.index) if stream is None else stream.cuda_stream
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _keep(stream, device, *tensors):
+    """Records fresh tensors on a given stream that is not the one they were allocated for."""
+    if stream is not None and stream.cuda_stream != _current_stream(device.index):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _launch(device, call, *args):
+    """call(*args) with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
+
+
+def _array(t, dtype, shape, device, name):
+    """Address of a contiguous `dtype` tensor of `shape` on `device`; 0 for None."""
+    if t is None:
+        return 0
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.device != device or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {device}")
+    return t.data_ptr()
+
+
+_DIMS = {"nh": (None, 0, 1), "bnh": (0, 1, 2), "bhn": (0, 2, 1)}  # batch, token, head
 
 
 def _rows(t, order, device, name):
-    """View of a bf16 tensor whose dimensions are (batch, token, head) in `order` ("bnh", "bhn",
-    or "nh" without a batch), then the head's contiguous elements."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != _BF16 or t.device != device
-            or t.dim() != len(order) + 1 or t.stride(-1) != 1):
+    """fa_view fields of a bf16 tensor whose dimensions are (batch, token, head) in `order`
+    ("bnh", "bhn", or "nh" without a batch), then the head's contiguous elements."""
+    ib, i_n, ih = _DIMS[order]
+    if (not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.device != device
+            or t.dim() != len(order) + 1):
         raise ValueError(f"{name} must be a bfloat16 tensor on {device} of {len(order) + 1} "
-                         "dimensions with contiguous rows")
-    strides = {"b": 0, "n": 0, "h": 0}
-    for i, c in enumerate(order):
-        if t.shape[i] > 1:
-            strides[c] = t.stride(i)
-            if strides[c] % 8:
-                raise ValueError(f"{name}: strides must be multiples of 8 elements")
-    if t.data_ptr() % 16:
-        raise ValueError(f"{name} must be 16-byte aligned")
-    return View(t.data_ptr(), strides["b"], strides["n"], strides["h"])
+                         "dimensions")
+    st, ptr = t.stride(), t.data_ptr()
+    b, n, h = 0 if ib is None else st[ib], st[i_n], st[ih]
+    if (b | n | h) & 7:  # the stride of a dimension of one element does not matter
+        sh = t.shape
+        b = 0 if ib is None or sh[ib] == 1 else b
+        n, h = (0 if sh[i_n] == 1 else n), (0 if sh[ih] == 1 else h)
+    if (b | n | h) & 7 or ptr & 15 or st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous rows, 16-byte aligned, at strides that "
+                         "are multiples of 8 elements")
+    return ptr, b, n, h
 
 
 def _own_rows(t, shape, order, device, name):
-    """(tensor, view) of an output: a new contiguous tensor, or the caller's, whose elements must
-    be distinct (no expanded or overlapping dimensions)."""
+    """(tensor, fa_view fields) of an output: a new contiguous tensor, or the caller's, whose
+    elements must be distinct (no expanded or overlapping dimensions)."""
     if t is None:
         t = torch.empty(shape, dtype=_BF16, device=device)
     else:
-        if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape):
+        if not isinstance(t, torch.Tensor) or t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}")
         reach = 1
         for st, n in sorted((t.stride(i), t.shape[i]) for i in range(t.dim()) if t.shape[i] > 1):
@@ -78,26 +102,22 @@ def _own_rows(t, shape, order, device, name):
     return t, _rows(t, order, device, name)
 
 
-def _ints(t, shape, device, name):
-    return None if t is None else _want(t, shape, torch.int32, device, name)
-
-
 def _transform(table, interleaved, q_weight, k_weight, eps, d, device):
-    n_pos = rot = 0
+    if table is None and q_weight is None and k_weight is None:
+        return _NO_TRANSFORM
+    n_pos = rot = at = 0
     if table is not None:
-        if table.dim() != 2:
-            raise ValueError("table must be [positions, rot]")
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be a tensor [positions, rot]")
         n_pos, rot = table.shape
-        _want(table, (n_pos, rot), torch.float32, device, "table")
+        at = _array(table, _F32, table.shape, device, "table")
         if n_pos < 1 or rot < 16 or rot > d or rot % 16:
             raise ValueError("the rotated part must be a multiple of 16 elements, at most d")
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _want(w, (d,), torch.float32, device, name)
-    return QKTransform(_at(table), n_pos, rot, int(bool(interleaved)), _at(q_weight),
-                       _at(k_weight), float(eps))
+    return _TRANSFORM.pack(at, n_pos, rot, 1 if interleaved else 0,
+                           _array(q_weight, _F32, (d,), device, "q_weight"),
+                           _array(k_weight, _F32, (d,), device, "k_weight"), eps)
 
 
 def _cuda(t, name):
@@ -132,7 +152,8 @@ def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_len=N
         raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
     if original_len is None or original_len < 1 or not beta_fast > beta_slow > 0:
         raise ValueError("yarn needs original_len and beta_fast > beta_slow > 0")
-    # the ramp is linear in the pair's index between the pairs that turn beta_fast and beta_slow times
+    # the ramp is linear in the pair's index, between the pairs that turn beta_fast and beta_slow
+    # times over original_len positions
     index = lambda t: (rot / 2) * math.log(original_len / (2 * math.pi * t)) / math.log(base)  # noqa: E731
     lo, hi = index(beta_fast), index(beta_slow)
     keep = 1.0 - ((i - lo) / (hi - lo)).clamp(0.0, 1.0)
@@ -155,28 +176,13 @@ def fa_rope_table(n_pos, rot, base=10000.0, scaling=None, factor=1.0, original_l
         inv_freq, amplitude = rope_frequencies(rot, base, scaling, factor, original_len)
     if inv_freq.dtype != torch.float64 or tuple(inv_freq.shape) != (rot // 2,):
         raise ValueError("inv_freq must be float64 [rot / 2]")
-    launch = _Launch(device, stream)
-    with launch.guard, torch.cuda.stream(launch.stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
         freq = inv_freq.to(device).contiguous()
-        table = torch.empty((n_pos, rot), dtype=torch.float32, device=device)
+        table = torch.empty((n_pos, rot), dtype=_F32, device=device)
         st = load_library().fa_rope_table(freq.data_ptr(), rot, n_pos, float(amplitude),
-                                          table.data_ptr(), launch.handle)
+                                          table.data_ptr(), _handle(device, stream))
     _check(st, "fa_rope_table")
     return table
-
-
-def _qkv_shapes(q, k, name_q="q"):
-    """(B, N, H, Hkv, d, input order, output order, output shape) of [B, N, H, d] or packed
-    [total, H, d] queries and keys."""
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
-        raise ValueError(f"{name_q} must be [B, N, H, d] or packed [total, H, d]")
-    if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
-        raise ValueError("q and k must agree in tokens and head dimension")
-    H, d, Hkv = q.shape[-2], q.shape[-1], k.shape[-2]
-    if q.dim() == 3:
-        return 1, q.shape[0], H, Hkv, d, "nh", "nh", lambda h: (q.shape[0], h, d)
-    B, N = q.shape[:2]
-    return B, N, H, Hkv, d, "bnh", "bhn", lambda h: (B, h, N, d)
 
 
 def fa_qk_norm_rope_fwd(q, k, v=None, table=None, positions=None, interleaved=False,
@@ -189,29 +195,34 @@ def fa_qk_norm_rope_fwd(q, k, v=None, table=None, positions=None, interleaved=Fa
     or None; positions: int32 [B, N] or [total], default each token's index n in its row.
     Returns (q, k, v or None)."""
     device = _cuda(q, "q")
-    B, N, H, Hkv, d, order, out_order, shape = _qkv_shapes(q, k)
-    t = _transform(table, interleaved, q_weight, k_weight, eps, d, device)
-    _ints(positions, q.shape[:-2], device, "positions")
-    if v is not None and tuple(v.shape) != tuple(k.shape):
+    shape, shape_k = q.shape, k.shape
+    if len(shape) not in (3, 4) or shape_k[:-2] != shape[:-2] or shape_k[-1] != shape[-1]:
+        raise ValueError("q and k must be [B, N, heads, d] or packed [total, heads, d], alike in "
+                         "tokens and head dimension")
+    if v is not None and v.shape != shape_k:
         raise ValueError("v must have k's shape")
-    if N == 0 or B == 0:
-        return tuple(torch.empty(shape(h), dtype=_BF16, device=device) if x is not None else None
-                     for x, h in ((q, H), (k, Hkv), (v, Hkv)))
-    views = [_rows(q, order, device, "q"), _rows(k, order, device, "k"),
-             _NO_VIEW if v is None else _rows(v, order, device, "v")]
-    launch = _Launch(device, stream)
-    q_out, vq = _own_rows(q_out, shape(H), out_order, device, "q_out")
-    k_out, vk = _own_rows(k_out, shape(Hkv), out_order, device, "k_out")
-    vv = _NO_VIEW
-    if v is not None:
-        v_out, vv = _own_rows(v_out, shape(Hkv), out_order, device, "v_out")
+    H, d, Hkv = shape[-2], shape[-1], shape_k[-2]
+    if len(shape) == 3:
+        B, N, order, out_order = 1, shape[0], "nh", "nh"
     else:
-        v_out = None
-    launch.keep(q_out, k_out, v_out)
-    with launch.guard:
-        st = load_library().fa_qk_norm_rope_fwd(*views, vq, vk, vv, _at(positions), B, N, H, Hkv,
-                                                d, ctypes.byref(t), launch.handle)
-    _check(st, "fa_qk_norm_rope_fwd")
+        B, N, order, out_order = shape[0], shape[1], "bnh", "bhn"
+        shape, shape_k = (B, H, N, d), (B, Hkv, N, d)
+    t = _transform(table, interleaved, q_weight, k_weight, eps, d, device)
+    pos = _array(positions, _I32, q.shape[:-2], device, "positions")
+    if B == 0 or N == 0:
+        return tuple(None if x is None else torch.empty(s, dtype=_BF16, device=device)
+                     for x, s in ((q, shape), (k, shape_k), (v, shape_k)))
+    views = _VIEWS3.pack(*_rows(q, order, device, "q"), *_rows(k, order, device, "k"),
+                         *(_NO_VIEW if v is None else _rows(v, order, device, "v")))
+    q_out, vq = _own_rows(q_out, shape, out_order, device, "q_out")
+    k_out, vk = _own_rows(k_out, shape_k, out_order, device, "k_out")
+    if v is None:
+        v_out, vv = None, _NO_VIEW
+    else:
+        v_out, vv = _own_rows(v_out, shape_k, out_order, device, "v_out")
+    _keep(stream, device, q_out, k_out, v_out)
+    _check(_launch(device, load_library().fa_qk_norm_rope_fwd, views, _VIEWS3.pack(*vq, *vk, *vv),
+                   pos, B, N, H, Hkv, d, t, _handle(device, stream)), "fa_qk_norm_rope_fwd")
     return q_out, k_out, v_out
 
 
@@ -242,74 +253,64 @@ def fa_qk_norm_rope_bwd(dq, dk, dv=None, q=None, k=None, table=None, positions=N
         want = (N, Hkv, d)
     else:
         raise ValueError("dq must be [B, H, N, d] or packed [total, H, d]")
-    for x, name in ((dk, "dk"), (dv, "dv")):
-        if x is not None and tuple(x.shape) != want:
-            raise ValueError(f"{name} must agree with dq")
+    if dk.shape != want or (dv is not None and dv.shape != want):
+        raise ValueError("dk and dv must agree with dq")
     t = _transform(table, interleaved, q_weight, k_weight, eps, d, device)
-    _ints(positions, lead, device, "positions")
-    for x, h, name in ((q, H, "q"), (k, Hkv, "k")):
-        if norm and (x is None or tuple(x.shape) != (*lead, h, d)):
-            raise ValueError(f"{name} (the forward's input) is needed with norms")
-    launch = _Launch(device, stream)
+    pos = _array(positions, _I32, lead, device, "positions")
+    if norm and (q is None or k is None or q.shape != (*lead, H, d) or k.shape != (*lead, Hkv, d)):
+        raise ValueError("q and k (the forward's inputs) are needed with norms")
     if dq_in is None and dk_in is None and dv_in is None:
         fused = torch.empty((*lead, H + (2 if dv is not None else 1) * Hkv, d), dtype=_BF16,
                             device=device)
-        dq_in, dk_in = fused[..., :H, :], fused[..., H:H + Hkv, :]
-        dv_in = fused[..., H + Hkv:, :] if dv is not None else None
-        launch.keep(fused)
+        parts = fused.split([H, Hkv, Hkv] if dv is not None else [H, Hkv], dim=-2)
+        dq_in, dk_in = parts[:2]
+        dv_in = parts[2] if dv is not None else None
     empty = B == 0 or N == 0
-    views = [_NO_VIEW] * 8
+    grad = out = x = None
     if not empty:
-        views[0] = _rows(dq, order, device, "dq")
-        views[1] = _rows(dk, order, device, "dk")
-        if norm:
-            views[3] = _rows(q, out_order, device, "q")
-            views[4] = _rows(k, out_order, device, "k")
-        dq_in, views[5] = _own_rows(dq_in, (*lead, H, d), out_order, device, "dq_in")
-        dk_in, views[6] = _own_rows(dk_in, (*lead, Hkv, d), out_order, device, "dk_in")
-        launch.keep(dq_in, dk_in)
+        dq_in, vq = _own_rows(dq_in, (*lead, H, d), out_order, device, "dq_in")
+        dk_in, vk = _own_rows(dk_in, (*lead, Hkv, d), out_order, device, "dk_in")
+        vv, gv = _NO_VIEW, _NO_VIEW
         if dv is not None:
-            views[2] = _rows(dv, order, device, "dv")
-            dv_in, views[7] = _own_rows(dv_in, (*lead, Hkv, d), out_order, device, "dv_in")
-            launch.keep(dv_in)
-    dwq = dwk = ws = None
-    ws_bytes = 0
+            gv = _rows(dv, order, device, "dv")
+            dv_in, vv = _own_rows(dv_in, (*lead, Hkv, d), out_order, device, "dv_in")
+        grad = _VIEWS3.pack(*_rows(dq, order, device, "dq"), *_rows(dk, order, device, "dk"), *gv)
+        out = _VIEWS3.pack(*vq, *vk, *vv)
+        if norm:
+            x = _VIEWS2.pack(*_rows(q, out_order, device, "q"), *_rows(k, out_order, device, "k"))
+    dw = ws = None
+    ws_at = ws_bytes = dw_at = 0
     if norm:
-        dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=device).unbind(0)
+        dw = torch.empty((2, d), dtype=_F32, device=device)
+        dw_at = dw.data_ptr()
         ws, ws_bytes = _workspace(workspace, fa_qk_norm_rope_bwd_workspace_size(d), device)
-        launch.keep(dwq, dwk, ws)
-    with launch.guard:
-        st = load_library().fa_qk_norm_rope_bwd(*views, _at(dwq), _at(dwk), _at(positions),
-                                                max(B, 1), 0 if empty else N, H, Hkv, d,
-                                                ctypes.byref(t), _at(ws), ws_bytes,
-                                                launch.handle)
-    _check(st, "fa_qk_norm_rope_bwd")
+        ws_at = ws.data_ptr()
+    _keep(stream, device, dq_in, dk_in, dv_in, dw, ws)
+    _check(_launch(device, load_library().fa_qk_norm_rope_bwd, grad, x, out, dw_at,
+                   dw_at + 4 * d if norm else 0, pos, max(B, 1), 0 if empty else N, H, Hkv, d, t,
+                   ws_at, ws_bytes, _handle(device, stream)), "fa_qk_norm_rope_bwd")
+    dwq, dwk = dw.unbind(0) if norm else (None, None)
     return dq_in, dk_in, dv_in if dv is not None else None, dwq, dwk
 
 
 # ------------------------------------------------------------------------------------- paged cache
 def _cache(k_cache, v_cache, block_table, kv_lens, device):
-    """(fa_paged_kv, B, Hkv, page size, d) after the checks of the cache's tensors."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, Hkv, page_size, d]")
-    pages, Hkv, page, d = k_cache.shape
-    _want(k_cache, k_cache.shape, _BF16, device, "k_cache")
-    _want(v_cache, k_cache.shape, _BF16, device, "v_cache")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, max_pages = block_table.shape
-    _ints(block_table, (B, max_pages), device, "block_table")
-    _ints(kv_lens, (B,), device, "kv_lens")
-    return (PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), pages, page, block_table.data_ptr(),
-                    max_pages, kv_lens.data_ptr()), B, Hkv, page, d)
+    """(fa_paged_kv, cache shape, block table's shape) after the checks of the cache's tensors."""
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache must be [pages, Hkv, page_size, d], block_table [B, max_pages]")
+    shape, of_table = k_cache.shape, block_table.shape
+    return _PAGED_KV.pack(_array(k_cache, _BF16, shape, device, "k_cache"),
+                          _array(v_cache, _BF16, shape, device, "v_cache"), shape[0], shape[2],
+                          _array(block_table, _I32, of_table, device, "block_table"), of_table[1],
+                          _array(kv_lens, _I32, of_table[:1], device, "kv_lens")), shape, of_table
 
 
 def _tokens(cu_seqlens, B, total, device):
     if cu_seqlens is None:
         if total != B:
             raise ValueError("without cu_seqlens there is one token per sequence")
-    else:
-        _ints(cu_seqlens, (B + 1,), device, "cu_seqlens")
+        return 0
+    return _array(cu_seqlens, _I32, (B + 1,), device, "cu_seqlens")
 
 
 def fa_kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None,
@@ -321,34 +322,29 @@ def fa_kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=Non
     offsets, default one token per sequence; pos_offset: int32 [B] added to the rotation's
     positions.  Returns the transformed q (None without q)."""
     device = _cuda(k, "k")
-    cache, B, Hkv, _, d = _cache(k_cache, v_cache, block_table, kv_lens, device)
-    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, d) or tuple(v.shape) != tuple(k.shape):
+    cache, (_, Hkv, _, d), (B, _) = _cache(k_cache, v_cache, block_table, kv_lens, device)
+    if k.dim() != 3 or k.shape[1:] != (Hkv, d) or v.shape != k.shape:
         raise ValueError("k and v must be [total, Hkv, d] with the cache's heads")
-    total = k.shape[0]
-    H = Hkv
+    total, H = k.shape[0], Hkv
     if q is not None:
         if q.dim() != 3 or q.shape[0] != total or q.shape[2] != d:
             raise ValueError("q must be [total, H, d]")
         H = q.shape[1]
-    _tokens(cu_seqlens, B, total, device)
-    _ints(pos_offset, (B,), device, "pos_offset")
+    cu = _tokens(cu_seqlens, B, total, device)
+    offset = _array(pos_offset, _I32, (B,), device, "pos_offset")
     t = _transform(table, interleaved, q_weight, k_weight, eps, d, device)
     if total == 0:
         return None if q is None else torch.empty((0, H, d), dtype=_BF16, device=device)
-    launch = _Launch(device, stream)
-    vq = vo = _NO_VIEW
-    if q is not None:
+    if q is None:
+        q_out, vq, vo = None, _NO_VIEW, None
+    else:
         vq = _rows(q, "nh", device, "q")
         q_out, vo = _own_rows(q_out, (total, H, d), "nh", device, "q_out")
-        launch.keep(q_out)
-    else:
-        q_out = None
-    with launch.guard:
-        st = load_library().fa_kv_append(vq, _rows(k, "nh", device, "k"),
-                                         _rows(v, "nh", device, "v"), vo, ctypes.byref(cache),
-                                         _at(cu_seqlens), _at(pos_offset), B, total, H, Hkv, d,
-                                         ctypes.byref(t), launch.handle)
-    _check(st, "fa_kv_append")
+        vo = _VIEW.pack(*vo)
+        _keep(stream, device, q_out)
+    views = _VIEWS3.pack(*vq, *_rows(k, "nh", device, "k"), *_rows(v, "nh", device, "v"))
+    _check(_launch(device, load_library().fa_kv_append, views, vo, cache, cu, offset, B, total, H,
+                   Hkv, d, t, _handle(device, stream)), "fa_kv_append")
     return q_out
 
 
@@ -362,37 +358,34 @@ def fa_fwd_shared_prefix_workspace_size(B, groups, total, H, Hkv, d) -> int:
         int(B), int(groups), int(total), int(H), int(Hkv), int(d)))
 
 
-def _paged(q, k_cache, v_cache, block_table, kv_lens, prefix_of, cu_seqlens, max_q, max_kv, causal,
-           scale, out, lse, workspace, stream, where):
-    device = _cuda(q, "q")
-    cache, B, Hkv, page, d = _cache(k_cache, v_cache, block_table, kv_lens, device)
+def _paged(q, k_cache, v_cache, block_table, kv_lens, prefix, groups, cu_seqlens, max_q, max_kv,
+           causal, scale, out, lse, workspace, stream, device, where):
+    cache, (_, Hkv, page, d), (B, pages) = _cache(k_cache, v_cache, block_table, kv_lens, device)
     if q.dim() != 3 or q.shape[2] != d or q.shape[1] % Hkv:
         raise ValueError("q must be [total, H, d] with H a multiple of the cache's heads")
     total, H, _ = q.shape
-    _want(q, q.shape, _BF16, device, "q")
-    _tokens(cu_seqlens, B, total, device)
-    prefix = prefix_of(device)
+    at = _array(q, _BF16, q.shape, device, "q")
+    cu = _tokens(cu_seqlens, B, total, device)
     if max_q is None:
         max_q = 1 if cu_seqlens is None else max(total, 1)
     if max_kv is None:
-        max_kv = min(cache.max_pages * page, 0x7fffffff)
-    launch = _Launch(device, stream)
-    out = _out(out, q.shape, _BF16, device, "out")
-    lse = _out(lse, (H, total), torch.float32, device, "lse")
+        max_kv = min(pages * page, 0x7fffffff)
+    out = torch.empty_like(q) if out is None else _out(out, q.shape, _BF16, device, "out")
+    lse = _out(lse, (H, total), _F32, device, "lse")
     lib = load_library()
     if prefix is None:
         need = lib.fa_fwd_paged_workspace_size(B, total, H, Hkv, d)
+        call = lib.fa_fwd_paged
+        head = (at, cache)
     else:
-        need = lib.fa_fwd_shared_prefix_workspace_size(B, prefix.groups, total, H, Hkv, d)
+        need = lib.fa_fwd_shared_prefix_workspace_size(B, groups, total, H, Hkv, d)
+        call = lib.fa_fwd_shared_prefix
+        head = (at, cache, prefix)
     ws, ws_bytes = _workspace(workspace, need, device)
-    launch.keep(out, lse, ws)
-    head = (q.data_ptr(), ctypes.byref(cache))
-    tail = (out.data_ptr(), lse.data_ptr(), _at(cu_seqlens), B, int(max_q), int(max_kv), total, H,
-            Hkv, d, int(bool(causal)), _scale(scale), ws.data_ptr(), ws_bytes, launch.handle)
-    with launch.guard:
-        st = (lib.fa_fwd_paged(*head, *tail) if prefix is None
-              else lib.fa_fwd_shared_prefix(*head, ctypes.byref(prefix), *tail))
-    _check(st, where)
+    _keep(stream, device, out, lse, ws)
+    _check(_launch(device, call, *head, out.data_ptr(), lse.data_ptr(), cu, B, max_q, max_kv,
+                   total, H, Hkv, d, 1 if causal else 0, _scale(scale), ws.data_ptr(), ws_bytes,
+                   _handle(device, stream)), where)
     return out, lse
 
 
@@ -404,8 +397,8 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, max
     sequence; causal aligns them to the end of the sequence.  max_q and max_kv bound the query
     tokens and keys of a sequence (defaults: total, and the block table's reach); close bounds
     let the launch fit the work."""
-    return _paged(q, k_cache, v_cache, block_table, kv_lens, lambda device: None, cu_seqlens,
-                  max_q, max_kv, causal, scale, out, lse, workspace, stream, "fa_fwd_paged")
+    return _paged(q, k_cache, v_cache, block_table, kv_lens, None, 0, cu_seqlens, max_q, max_kv,
+                  causal, scale, out, lse, workspace, stream, _cuda(q, "q"), "fa_fwd_paged")
 
 
 def fa_fwd_shared_prefix(q, k_cache, v_cache, block_table, kv_lens, prefix_table, prefix_lens,
@@ -415,16 +408,16 @@ def fa_fwd_shared_prefix(q, k_cache, v_cache, block_table, kv_lens, prefix_table
     """fa_fwd_paged for sequences that share prefixes held in the same cache (see include/fa.h):
     sequences [group_cu[g], group_cu[g + 1]) begin with the prefix_lens[g] keys in pages
     prefix_table[g]; block_table and kv_lens are their own keys behind it."""
-    def prefix_of(device):
-        if prefix_table.dim() != 2:
-            raise ValueError("prefix_table must be [groups, pages]")
-        groups, pages = prefix_table.shape
-        _ints(prefix_table, (groups, pages), device, "prefix_table")
-        _ints(prefix_lens, (groups,), device, "prefix_lens")
-        _ints(group_cu, (groups + 1,), device, "group_cu")
-        reach = min(pages * k_cache.shape[2], 0x7fffffff)
-        return Prefix(prefix_table.data_ptr(), pages, prefix_lens.data_ptr(),
-                      group_cu.data_ptr(), groups, reach if max_prefix is None else int(max_prefix))
-
-    return _paged(q, k_cache, v_cache, block_table, kv_lens, prefix_of, cu_seqlens, max_q, max_kv,
-                  causal, scale, out, lse, workspace, stream, "fa_fwd_shared_prefix")
+    device = _cuda(q, "q")
+    if prefix_table.dim() != 2:
+        raise ValueError("prefix_table must be [groups, pages]")
+    groups, pages = prefix_table.shape
+    if max_prefix is None:
+        max_prefix = min(pages * k_cache.shape[2], 0x7fffffff)
+    prefix = _PREFIX.pack(_array(prefix_table, _I32, (groups, pages), device, "prefix_table"),
+                          pages, _array(prefix_lens, _I32, (groups,), device, "prefix_lens"),
+                          _array(group_cu, _I32, (groups + 1,), device, "group_cu"), groups,
+                          max_prefix)
+    return _paged(q, k_cache, v_cache, block_table, kv_lens, prefix, groups, cu_seqlens, max_q,
+                  max_kv, causal, scale, out, lse, workspace, stream, device,
+                  "fa_fwd_shared_prefix")

@@ -271,30 +271,30 @@ fa_status fa_rope_table(const double* inv_freq, int rot, int n_pos, float amplit
                         float* table, void* stream);
 
 /*
- * Q, K: [B, N] tokens of H and Hkv heads, transformed and written through q_out, k_out; V copied
- * through v_out (v.data NULL: no V).  One pass over the data: each input read once, each output
- * written once.  positions: DEVICE int32[B*N], the table row of each token, or NULL: n.  A
- * position outside [0, n_pos) uses the nearest row and records FA_ERR_INDEX.  An output may be
- * the identical view of its input (in place); otherwise outputs overlap nothing.
+ * in: the views of Q, K and V, [B, N] tokens of H, Hkv and Hkv heads; out: those of the results.
+ * Q and K are transformed, V is copied (in[2].data NULL: no V).  One pass over the data: each
+ * input read once, each output written once.  positions: DEVICE int32[B*N], the table row of
+ * each token, or NULL: n.  A position outside [0, n_pos) uses the nearest row and records
+ * FA_ERR_INDEX.  An output may be the identical view of its input (in place); otherwise outputs
+ * overlap nothing.
  */
-fa_status fa_qk_norm_rope_fwd(fa_view q, fa_view k, fa_view v, fa_view q_out, fa_view k_out,
-                              fa_view v_out, const int32_t* positions, int B, int N, int H,
-                              int Hkv, int d, const fa_qk_transform* t, void* stream);
+fa_status fa_qk_norm_rope_fwd(const fa_view in[3], const fa_view out[3],
+                              const int32_t* positions, int B, int N, int H, int Hkv, int d,
+                              const fa_qk_transform* t, void* stream);
 
 /*
- * Gradients of fa_qk_norm_rope_fwd.  dq, dk, dv: of its outputs; q, k: its inputs (read only
- * when there is a norm, else data may be NULL); dq_in, dk_in, dv_in: of its inputs (dv copied;
- * dv.data NULL: no V).  dq_weight, dk_weight: float32[d], of the norm's weights, summed over
- * tokens and heads in a fixed order (bit-identical from run to run); NULL without a norm.
+ * Gradients of fa_qk_norm_rope_fwd.  grad: of its three outputs; x: its inputs Q and K (read
+ * only with norms, else NULL); out: the gradients of its three inputs (V's copied; grad[2].data
+ * NULL: no V).  dq_weight, dk_weight: float32[d], of the norm's weights, summed over tokens and
+ * heads in a fixed order (bit-identical from run to run); NULL without norms.
  * workspace: DEVICE, fa_qk_norm_rope_bwd_workspace_size(d) bytes, 256-byte aligned (needed with
- * a norm only).  dq_in, dk_in, dv_in may be the identical views of dq, dk, dv.
+ * norms only).  out may be the identical views of grad.
  */
 size_t fa_qk_norm_rope_bwd_workspace_size(int d);
-fa_status fa_qk_norm_rope_bwd(fa_view dq, fa_view dk, fa_view dv, fa_view q, fa_view k,
-                              fa_view dq_in, fa_view dk_in, fa_view dv_in, float* dq_weight,
-                              float* dk_weight, const int32_t* positions, int B, int N, int H,
-                              int Hkv, int d, const fa_qk_transform* t, void* workspace,
-                              size_t workspace_bytes, void* stream);
+fa_status fa_qk_norm_rope_bwd(const fa_view grad[3], const fa_view x[2], const fa_view out[3],
+                              float* dq_weight, float* dk_weight, const int32_t* positions,
+                              int B, int N, int H, int Hkv, int d, const fa_qk_transform* t,
+                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * ------------------------------------------------------------------------------------------
@@ -323,12 +323,13 @@ typedef struct {
 
 /*
  * Appends the new tokens' K (transformed as above) and V to the cache and writes the transformed
- * Q [total, H, d] through q_out, in one launch.  q.data NULL: no Q.  The rotation's position is
- * the key's index plus pos_offset[b] (DEVICE int32[B], or NULL: 0; for pages behind a prefix
- * that other pages hold).  Views: [total] tokens (their batch stride is not used).  A token of
- * negative key index is not written.  No two tokens of one call may have the same place.
+ * Q [total, H, d] through q_out, in one launch.  in: the views of Q, K and V (in[0].data NULL:
+ * no Q); their batch stride is not used.  The rotation's position is the key's index plus
+ * pos_offset[b] (DEVICE int32[B], or NULL: 0; for pages behind a prefix that other pages hold).
+ * A token of negative key index is not written.  No two tokens of one call may have the same
+ * place in the cache.
  */
-fa_status fa_kv_append(fa_view q, fa_view k, fa_view v, fa_view q_out, const fa_paged_kv* cache,
+fa_status fa_kv_append(const fa_view in[3], const fa_view* q_out, const fa_paged_kv* cache,
                        const int32_t* cu_seqlens, const int32_t* pos_offset, int B, int total,
                        int H, int Hkv, int d, const fa_qk_transform* t, void* stream);
 

@@ -2,7 +2,6 @@
 for the host, argument refusals of the C ABI and of the binding, the rotary frequencies, and the
 fp64 reference (its gradients against differences)."""
 
-import ctypes
 import math
 import os
 import subprocess
@@ -12,7 +11,7 @@ import pytest
 import torch
 
 import exact_io_aware_fwd_gb300 as fa
-from exact_io_aware_fwd_gb300 import binding, build_lib, serving
+from exact_io_aware_fwd_gb300 import build_lib, serving
 from oracle import attention_forward
 from oracle.serving import attend, norm_rope, norm_rope_backward, paged_keys, rotate
 
@@ -51,13 +50,44 @@ def test_unit_owners(C, W):
 
 # ------------------------------------------------------------------------------- C ABI refusals
 def _view(p=P, batch=8, token=8, head=8):
-    return binding.View(p, batch, token, head)
+    return serving._VIEW.pack(p or 0, batch, token, head)
+
+
+def _pack(layout, values):
+    return layout.pack(*(0 if v is None else v for v in values))
 
 
 def _transform(**kw):
     d = dict(table=P, n_pos=64, rot=64, interleaved=0, q_weight=None, k_weight=None, eps=1e-6)
     d.update(kw)
-    return binding.QKTransform(*d.values())
+    return _pack(serving._TRANSFORM, d.values())
+
+
+def test_structures_have_the_headers_layout(tmp_path):
+    """The packed structures agree with the compiler's for include/fa.h, field by field."""
+    fields = {"fa_view": ("_VIEW", "data batch token head"),
+              "fa_qk_transform": ("_TRANSFORM", "table n_pos rot interleaved q_weight k_weight eps"),
+              "fa_paged_kv": ("_PAGED_KV", "k_cache v_cache num_pages page_size block_table max_pages kv_lens"),
+              "fa_prefix": ("_PREFIX", "table max_pages lens group_cu groups max_len")}
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "fa.h"\nint main(void) {\n' + "".join(
+        f'printf("%zu {n} {f}\\n", offsetof({n}, {f}));\n' for n, (_, fs) in fields.items() for f in fs.split())
+        + "".join(f'printf("%zu {n} size\\n", sizeof({n}));\n' for n in fields) + "return 0;}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(os.path.dirname(HERE), "include"), str(src), "-o", str(exe)],
+                   check=True)
+    told = {}
+    for line in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.splitlines():
+        at, n, f = line.split()
+        told[n, f] = int(at)
+    for n, (name, fs) in fields.items():
+        layout = getattr(serving, name)
+        assert layout.size == told[n, "size"], n
+        fs = fs.split()
+        for i, f in enumerate(fs):  # only field i set: the nonzero byte is at its offset
+            raw = layout.pack(*(1 if j == i else 0 for j in range(len(fs))))
+            first = next(b for b, x in enumerate(raw) if x)
+            assert first == told[n, f] + (2 if f == "eps" else 0), (n, f)  # 1.0f is 00 00 80 3f
 
 
 def test_rope_table_refusals(lib):
@@ -72,8 +102,8 @@ def test_rope_table_refusals(lib):
 def test_norm_rope_refusals(lib):
     def fwd(views=None, B=1, N=8, H=4, Hkv=2, d=64, t=None, pos=None):
         v = views or [_view() for _ in range(6)]
-        return lib.fa_qk_norm_rope_fwd(*v, pos, B, N, H, Hkv, d,
-                                       ctypes.byref(t or _transform()), None)
+        return lib.fa_qk_norm_rope_fwd(b"".join(v[:3]), b"".join(v[3:]), pos, B, N, H, Hkv, d,
+                                       t or _transform(), None)
 
     bad = fa.FA_ERR_INVALID_ARG
     assert fwd(d=96) == fa.FA_ERR_UNSUPPORTED
@@ -96,8 +126,8 @@ def test_norm_rope_refusals(lib):
 
     def bwd(views=None, dw=(P, P), ws=P, nbytes=1 << 24, t=None, N=8):
         v = views or [_view() for _ in range(8)]
-        return lib.fa_qk_norm_rope_bwd(*v, *dw, None, 1, N, 4, 2, 64,
-                                       ctypes.byref(t or _transform(q_weight=P, k_weight=P)), ws,
+        return lib.fa_qk_norm_rope_bwd(b"".join(v[:3]), b"".join(v[3:5]), b"".join(v[5:]), *dw, None,
+                                       1, N, 4, 2, 64, t or _transform(q_weight=P, k_weight=P), ws,
                                        nbytes, None)
 
     assert lib.fa_qk_norm_rope_bwd_workspace_size(96) == 0
@@ -107,8 +137,6 @@ def test_norm_rope_refusals(lib):
     assert bwd(ws=None) == fa.FA_ERR_WORKSPACE and bwd(nbytes=need - 1) == fa.FA_ERR_WORKSPACE
     assert bwd(ws=P + 16) == bad
     for i in range(8):
-        if i in (2,):
-            continue  # no dv at all is allowed
         views = [_view() for _ in range(8)]
         views[i] = _view(P + 2)
         assert bwd(views) == bad, i
@@ -118,7 +146,7 @@ def test_norm_rope_refusals(lib):
 def _kv(**kw):
     d = dict(k_cache=P, v_cache=P, num_pages=8, page_size=16, block_table=P, max_pages=4, kv_lens=P)
     d.update(kw)
-    return binding.PagedKV(*d.values())
+    return _pack(serving._PAGED_KV, d.values())
 
 
 CACHE_FAULTS = [dict(k_cache=None), dict(v_cache=None), dict(k_cache=P + 8), dict(num_pages=0),
@@ -128,8 +156,8 @@ CACHE_FAULTS = [dict(k_cache=None), dict(v_cache=None), dict(k_cache=P + 8), dic
 def test_append_refusals(lib):
     def call(cache=None, views=None, B=2, total=5, cu=P, t=None):
         v = views or [_view() for _ in range(4)]
-        return lib.fa_kv_append(*v, ctypes.byref(cache or _kv()), cu, None, B, total, 4, 2, 64,
-                                ctypes.byref(t or _transform()), None)
+        return lib.fa_kv_append(b"".join(v[:3]), v[3], cache or _kv(), cu, None, B, total, 4, 2, 64,
+                                t or _transform(), None)
 
     bad = fa.FA_ERR_INVALID_ARG
     for kw in CACHE_FAULTS + [dict(max_pages=0)]:
@@ -148,7 +176,7 @@ def test_append_refusals(lib):
 def test_paged_attention_refusals(lib):
     def call(cache=None, q=P, o=P, lse=P, cu=P, B=2, max_q=3, max_kv=64, total=5, H=4, Hkv=2, d=64,
              scale=-1.0, ws=P, nbytes=1 << 30):
-        return lib.fa_fwd_paged(q, ctypes.byref(cache or _kv()), o, lse, cu, B, max_q, max_kv,
+        return lib.fa_fwd_paged(q, cache or _kv(), o, lse, cu, B, max_q, max_kv,
                                 total, H, Hkv, d, 1, scale, ws, nbytes, None)
 
     bad = fa.FA_ERR_INVALID_ARG
@@ -170,13 +198,13 @@ def test_paged_attention_refusals(lib):
     assert lib.fa_fwd_paged_workspace_size(2, 5, 4, 3, 64) == 0
 
     def shared(prefix, nbytes=1 << 30):
-        return lib.fa_fwd_shared_prefix(P, ctypes.byref(_kv()), prefix, P, P, P, 2, 3, 64, 5, 4, 2,
+        return lib.fa_fwd_shared_prefix(P, _kv(), prefix, P, P, P, 2, 3, 64, 5, 4, 2,
                                         64, 1, -1.0, P, nbytes, None)
 
     def pre(**kw):
         d = dict(table=P, max_pages=4, lens=P, group_cu=P, groups=2, max_len=64)
         d.update(kw)
-        return ctypes.byref(binding.Prefix(*d.values()))
+        return _pack(serving._PREFIX, d.values())
 
     assert shared(None) == bad
     for kw in (dict(table=None), dict(max_pages=-1), dict(lens=None), dict(group_cu=None),
@@ -201,7 +229,7 @@ def test_binding_refuses_host_tensors_and_bad_views(lib):
     cpu = torch.device("cpu")
     wide = torch.zeros(4, 6, 64, dtype=torch.bfloat16)
     v = serving._rows(wide[:, 2:4], "nh", cpu, "x")
-    assert (v.data, v.token, v.head) == (wide.data_ptr() + 2 * 64 * 2, 6 * 64, 64)
+    assert v == (wide.data_ptr() + 2 * 64 * 2, 0, 6 * 64, 64)
     for t, order in ((wide.float(), "nh"), (wide[..., ::2], "nh"), (wide, "bnh"),
                      (wide[:, :, 4:], "nh"), (torch.zeros(4, 6, 68, dtype=torch.bfloat16)[..., :64], "nh")):
         with pytest.raises(ValueError):
@@ -210,7 +238,9 @@ def test_binding_refuses_host_tensors_and_bad_views(lib):
         serving._own_rows(wide[:, :1].expand(4, 6, 64), (4, 6, 64), "nh", cpu, "x")
     with pytest.raises(ValueError):
         serving._own_rows(wide, (4, 5, 64), "nh", cpu, "x")
-    assert serving._own_rows(wide.transpose(0, 1), (6, 4, 64), "hn", cpu, "x")[1].token == 6 * 64
+    assert serving._own_rows(wide.transpose(0, 1), (6, 4, 64), "nh", cpu, "x")[1][2:] == (64, 6 * 64)
+    one = torch.zeros(1, 64, dtype=torch.bfloat16).as_strided((1, 1, 64), (3, 5, 1))
+    assert serving._rows(one, "nh", cpu, "x")[2:] == (0, 0)  # strides of single elements
 
 
 # ----------------------------------------------------------------------------- rotary frequencies
