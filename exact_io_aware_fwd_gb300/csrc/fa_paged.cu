@@ -88,27 +88,13 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D>::kCtasPerSm)
   const KeyList& l = a.list;
   const uint32_t ring = smem_u32(smem) + warp * (S * L::kStage);
 
-  int b = sh.b;
-  int64_t within = sh.off;
-  Entry e = entry_of<R, KT>(l, a, b, false);
-  for (int64_t u = sh.u0; u < sh.u1;) {
-    const int su = sh.direct ? 1 : e.tiles;  // units of a segment
-    if (within >= static_cast<int64_t>(su) * e.rt * a.Hkv) {  // next entry with tokens
-      do {
-        if (++b >= l.count) return;  // cannot happen while u < W
-        e = entry_of<R, KT>(l, a, b, false);
-      } while (e.rt == 0);
-      within = 0;
-      continue;
-    }
-    const int seg = static_cast<int>(within / su), toff = static_cast<int>(within % su);
-    const int hk = seg / e.rt, rtile = seg % e.rt;
-    const int take = static_cast<int>(min(static_cast<int64_t>(su - toff), sh.u1 - u));
-    const int tile_a = sh.direct ? 0 : toff;
-    const int tile_e = sh.direct ? e.tiles : toff + take;
-    const bool whole = sh.direct || take == su;
-    u += take;
-    within += take;
+  Walk<R, KT> walk(sh, a);
+  Piece piece;
+  while (walk.next(a, piece)) {
+    const Entry& e = walk.e;
+    const int b = walk.b, hk = piece.hk, rtile = piece.r;
+    const int tile_a = piece.ta, tile_e = piece.te;
+    const bool whole = piece.whole;
 
     // ---- the rows' queries as A fragments: thread holds rows lane / 4 and lane / 4 + 8
     const int rows = min(R, e.nc * a.G - rtile * R);
@@ -119,8 +105,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D>::kCtasPerSm)
       const int rr = (lane >> 2) + 8 * i;
       const int row = rtile * R + rr;
       const int tok = row / a.G;
-      lim[i] = l.causal ? min(e.len, e.len - e.n + tok + 1) : e.len;
-      if (rr >= rows) lim[i] = e.len;
+      lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row) : e.len;
       const __nv_bfloat16* qp =
           a.q + (static_cast<int64_t>(e.start + tok) * a.H + hk * a.G + (row - tok * a.G)) * D +
           (lane & 3) * 2;
@@ -131,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D>::kCtasPerSm)
       }
     }
     // smallest limit of the tile: its first token's
-    const int lim_min = l.causal ? min(e.len, e.len - e.n + (rtile * R) / a.G + 1) : e.len;
+    const int lim_min = row_limit(e, l.causal, a.G, rtile * R);
 
     // ---- this warp's steps: keys [(t * kWarps + warp) * kKeys, + kKeys) of tiles t
     const int32_t* trow = l.table + static_cast<int64_t>(b) * l.max_pages;
@@ -282,12 +267,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D>::kCtasPerSm)
     }
     __syncthreads();
     const int tile = row_tile0(e.start, a.G, R, b) + rtile;
-    if (tid == 0 && tile_a == 0) {  // this CTA began the segment
-      const int64_t s0 = u - take - toff;
-      const int last = whole ? static_cast<int>(blockIdx.x) : owner_of(sh, s0 + su - 1);
-      a.part.spans[static_cast<int64_t>(hk) * a.part.span_tiles + tile] =
-          make_int2(blockIdx.x, last - static_cast<int>(blockIdx.x) + 1);
-    }
+    if (tid == 0 && tile_a == 0)  // this CTA began the segment
+      a.part.spans[static_cast<int64_t>(hk) * a.part.span_tiles + tile] = span_of(sh, piece);
     {
       const int rr = tid / 8, c8 = tid % 8;  // 8 threads a row
       float w[kWarps], mx = -INFINITY, lsum = 0.f;

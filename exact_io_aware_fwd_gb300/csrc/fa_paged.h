@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -143,7 +144,13 @@ constexpr int kPagedRows = 16;           // rows of a tile
 constexpr int kPagedMaxCtas = 152 * 3;   // most CTAs of a launch (and pairs of slots)
 constexpr int kPagedUnsplitKeys = 512;   // where no entry has more keys, none is split
 
+constexpr int kPagedMmaRows = 256;       // the same of the tensor-core kernel: two query tiles,
+constexpr int kPagedMmaCtas = 152;       // one CTA per SM
+
 cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s);
+cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedArgs& a, int64_t max_units, uint64_t timeout_ns,
+                             cudaStream_t s);
 cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s);
 
 }  // namespace fa

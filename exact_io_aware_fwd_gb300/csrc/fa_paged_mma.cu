@@ -1,0 +1,499 @@
+// Attention of many query rows over a paged key/value cache on the tcgen05 tensor cores: chunks
+// of prompts, and all the queries of a batch against the prefix that they share.
+//
+// The method is fa_fwd's (two 128-row query tiles per CTA that alternate on the tensor core, one
+// thread per row in the softmax, O~ rescaled in tensor memory only when a row's maximum moved);
+// what differs is where rows and keys come from and where results go:
+//  * a row tile is 256 consecutive (token, group member) rows of one key/value head, so the heads
+//    of a group share every K, V tile; rows are gathered with plain loads into the swizzled Q
+//    tiles (any group size), K and V come page by page through a TMA map of the pool, whose
+//    out-of-range coordinate gives zeros for pages past the end or outside the pool;
+//  * the rows of the last page past the sequence's end may hold anything (an infinity times a
+//    zero weight would be NaN), so the softmax warps clear them in the V tile before P V;
+//  * CTAs are persistent and take equal shares of all key tiles (paged_plan.cuh): the TMA warp
+//    runs ahead into the next segment while the softmax warps finish the last one, and a segment
+//    that several CTAs share leaves float32 parts for the join kernel.
+// Bound by the tensor pipe when both query tiles are full (512 flops per K, V byte at 256 rows);
+// with one tile of few rows by the copies from memory.
+#include "fa_internal.h"
+#include "fa_paged.h"
+#include "paged_plan.cuh"
+#include "sm103.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int kThreads = 384;  // warp 0: TMA, warp 1: MMA, warps 4-7 and 8-11: softmax
+constexpr int R = kPagedMmaRows;
+constexpr int KT = 128;
+constexpr int kDirectTiles = 4;
+constexpr float kLn2 = 0.693147180559945309f;
+
+template <int D>
+struct MmaLayout {
+  static constexpr uint32_t kTile = 128u * D * 2u;
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + 2 * kTile;
+  static constexpr uint32_t kV = kK + kStages * kTile;
+  static constexpr uint32_t kBar = kV + kStages * kTile;
+  // q_full, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2], p_full[2], o_full[2], done
+  static constexpr int kNumBars = 1 + 4 * kStages + 7;
+  static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
+  static constexpr uint32_t kAbort = kTmemSlot + 4;
+  static constexpr uint32_t kBad = kAbort + 4;  // [2 S]: pages of a position outside the pool
+  static constexpr uint32_t kBytes = kBad + 2 * kStages * 4;
+  static constexpr uint32_t kColS0 = 0, kColO0 = 256;
+  static constexpr uint32_t kTmemCols = 512;
+};
+
+// A softmax warp's walk over the CTA's pieces, kept in shared memory: the 128 scores of a row
+// leave no registers for it.
+struct WarpWalk {
+  Walk<R, KT> walk;
+  Piece piece;
+  bool more;
+};
+
+// Key tiles of query tile t (rows [256 r + 128 t, + 128)) inside the piece's range.
+__device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, int causal, int G,
+                                              int t) {
+  const int r0 = p.r * R + 128 * t, rows = e.nc * G;
+  if (r0 >= rows) return 0;
+  const int lim = max(0, row_limit(e, causal, G, min(rows, r0 + 128) - 1));
+  return max(0, min(p.te, (lim + KT - 1) / KT) - p.ta);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_mma_kernel(const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const PagedArgs a,
+                     const uint64_t timeout_ns, const uint32_t smem_bytes) {
+  using L = MmaLayout<D>;
+  constexpr int S = L::kStages, P = D / 64;  // 64-column panels of a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  uint8_t* sm = smem_raw + pad;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* k_empty = k_full + S;
+  uint64_t* v_full = k_empty + S;
+  uint64_t* v_empty = v_full + S;
+  uint64_t* s_full = v_empty + S;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* mma_done = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmemSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kAbort);
+  volatile uint32_t* bad_pages = reinterpret_cast<volatile uint32_t*>(sm + L::kBad);
+  __shared__ __align__(8) uint8_t walks[8][sizeof(WarpWalk)];
+  const Ctl ctl{abort_flag, a.status, timeout_ns};
+  const uint32_t warp = warp_id(), lane = lane_id();
+  if (pad + L::kBytes > smem_bytes) {  // cannot happen with the host's sizing; never proceed
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, kErrLayout);
+    return;
+  }
+  const Share sh = make_share<R, KT, kThreads, kDirectTiles>(a);
+  if (sh.u0 >= sh.u1) return;  // uniform over the CTA
+  const KeyList& l = a.list;
+
+  if (warp == 0 && lane == 0) {
+    *abort_flag = 0;
+    mbar_init(q_full, 8);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    mbar_init(mma_done, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t sbase = smem_u32(sm);
+  // Every role walks the CTA's pieces for itself.  Registers: the launch gives 384 x 168; warps
+  // 0-3 keep 72 and the softmax warps take 216 (128 x 72 + 256 x 216 = 384 x 168), enough for a
+  // row's scores and weights without spills.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      Walk<R, KT> walk(sh, a);
+      Piece piece;
+      // ================= TMA producer: one box (page x 64 columns) per lane
+      const int page_size = 1 << a.page_shift, pages = KT >> a.page_shift;
+      const int pg = lane & (pages - 1), panel = lane / pages;
+      const bool mine = panel < P;
+      int jk = 0, jv = 0;  // positions whose K and V copies have been issued
+      bool ok = true;
+      while (ok && walk.next(a, piece)) {
+        const Entry& e = walk.e;
+        const int npos = max(tiles_in_piece(e, piece, l.causal, a.G, 0),
+                             tiles_in_piece(e, piece, l.causal, a.G, 1));
+        const int32_t* trow = l.table + static_cast<int64_t>(walk.b) * l.max_pages;
+        // page of this lane's box at key tile kt: out of range past the end, bad outside the pool
+        auto find = [&](int kt, bool& bad) {
+          const int key = kt * KT + pg * page_size;
+          const int p = key < e.len ? resolve_page(trow, l.max_pages, a.num_pages, a.page_shift, key)
+                                    : -1;
+          bad = key < e.len && p < 0;
+          return p < 0 ? a.num_pages * a.Hkv : p * a.Hkv + piece.hk;
+        };
+        bool bad = false, bad_next = false;
+        int z = 0, z_next = npos > 0 ? find(piece.ta, bad_next) : 0;
+        for (int j = 0; j < npos; ++j) {
+          const int s = jk % S;
+          const uint32_t ph = (jk / S) & 1;
+          z = z_next;
+          bad = bad_next;
+          if (j + 1 < npos) z_next = find(piece.ta + j + 1, bad_next);
+          const uint32_t mask = __ballot_sync(~0u, bad) & ((1u << pages) - 1u);
+          if (!(ok = mbar_wait_warp(&k_empty[s], ph ^ 1, ctl))) break;
+          if (lane == 0) {
+            if (mask != 0) atomicCAS(a.status, 0, kErrIndex);
+            bad_pages[jk % (2 * S)] = mask;
+            mbar_arrive_expect_tx(&k_full[s], L::kTile);
+          }
+          __syncwarp();
+          const uint32_t at = s * L::kTile + panel * 16384 + pg * (page_size * 128);
+          if (mine) tma_load_3d(sm + L::kK + at, &tmK, &k_full[s], panel * 64, 0, z);
+          ++jk;
+          if (!(ok = mbar_wait_warp(&v_empty[s], ph ^ 1, ctl))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&v_full[s], L::kTile);
+          __syncwarp();
+          if (mine) tma_load_3d(sm + L::kV + at, &tmV, &v_full[s], panel * 64, 0, z);
+          ++jv;
+        }
+      }
+      // no copy into this CTA's shared memory may still be in flight when the CTA exits
+      if (lane == 0) {
+        for (int j = max(0, jk - S); j < jk; ++j) drain_wait(&k_full[j % S], (j / S) & 1, ctl);
+        for (int j = max(0, jv - S); j < jv; ++j) drain_wait(&v_full[j % S], (j / S) & 1, ctl);
+      }
+    } else if (warp == 1) {
+      // ================= MMA issuer
+      if (lane == 0) {
+        Walk<R, KT> walk(sh, a);
+        Piece piece;
+        constexpr uint32_t idS = idesc_bf16(128, 128, false, false);  // S = Q K^T, both K-major
+        constexpr uint32_t idO = idesc_bf16(128, D, false, true);     // O += P V, V is MN-major
+        int base = 0, segs = 0;  // positions and pieces before this one
+        int issued[2] = {0, 0};  // S MMAs per query tile, over all pieces
+        bool ok = true;
+        while (ok && walk.next(a, piece)) {
+          const int n[2] = {tiles_in_piece(walk.e, piece, l.causal, a.G, 0),
+                            tiles_in_piece(walk.e, piece, l.causal, a.G, 1)};
+          const int npos = max(n[0], n[1]);
+          if (npos == 0) continue;
+          if (!(ok = mbar_wait(q_full, segs & 1, ctl))) break;
+          ++segs;
+          tc_fence_after();
+          for (int j = 0; ok && j <= npos; ++j) {
+            const int jg = base + j, s = jg % S, sp = (jg + S - 1) % S;
+            if (j < npos && !(ok = mbar_wait(&k_full[s], (jg / S) & 1, ctl))) break;
+            if (j >= 1 && !(ok = mbar_wait(&v_full[sp], ((jg - 1) / S) & 1, ctl))) break;
+            tc_fence_after();
+  #pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (j >= 1 && j - 1 < n[t]) {
+                if (!(ok = mbar_wait(&p_full[t], (issued[t] - 1) & 1, ctl))) break;
+                tc_fence_after();
+                mma_ts_k128_step8(tmem + L::kColO0 + D * t, tmem + L::kColS0 + 128 * t,
+                                  sdesc_sw128(sbase + L::kV + sp * L::kTile, 16384, 1024), idO,
+                                  j > 1 ? 1u : 0u);
+                if (j == n[t]) mma_commit(&o_full[t]);  // the tile's last P V
+              }
+              if (j < n[t]) {  // S_t overwrites P_t: after the tile's own P V
+                mma_ss_kmajor<D>(tmem + L::kColS0 + 128 * t,
+                                 sdesc_sw128(sbase + L::kQ + t * L::kTile, 16384, 1024),
+                                 sdesc_sw128(sbase + L::kK + s * L::kTile, 16384, 1024), idS, 0u);
+                mma_commit(&s_full[t]);
+                ++issued[t];
+              }
+            }
+            if (!ok) break;
+            if (j < npos) mma_commit(&k_empty[s]);
+            if (j >= 1) mma_commit(&v_empty[sp]);
+          }
+          base += npos;
+        }
+        // every MMA issued by this thread has finished before tensor memory is released
+        mma_commit(mma_done);
+        drain_wait(mma_done, 0, ctl);
+      }
+    }
+  } else {
+    // ================= softmax warpgroups: one per query tile, one thread per row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int t = (warp - 4) >> 2;
+    const uint32_t quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const uint32_t lanes = (quad * 32u) << 16;
+    const uint32_t tS = tmem + lanes + L::kColS0 + 128 * t;
+    const uint32_t tO = tmem + lanes + L::kColO0 + D * t;
+    const uint32_t q_tile = sbase + L::kQ + t * L::kTile;
+    const float c2 = a.scale_log2;
+    int base = 0, segs = 0;  // positions and pieces with keys before this one
+    int seen = 0, outs = 0;  // S tiles and results of this query tile before this piece
+    bool ok = true;
+    WarpWalk& ww = *reinterpret_cast<WarpWalk*>(walks[warp - 4]);
+    if (lane == 0) ww.walk = Walk<R, KT>(sh, a);
+    const Piece& piece = ww.piece;
+    const Entry& e = ww.walk.e;
+    while (true) {
+      __syncwarp();
+      if (lane == 0) ww.more = ww.walk.next(a, ww.piece);
+      __syncwarp();
+      if (!ww.more) break;
+      const int n_mine = tiles_in_piece(e, piece, l.causal, a.G, t);
+      const int npos = max(n_mine, tiles_in_piece(e, piece, l.causal, a.G, 1 - t));
+      const int rows = e.nc * a.G, r0 = piece.r * R + 128 * t;  // r0: the tile's first row
+      if (npos > 0) {
+        // ---- the tile's queries: lanes 0-15 and 16-31 (d = 128) gather one row each time
+        if (n_mine > 0) {
+          constexpr int GR = D / 8, RI = 32 / GR;  // granules of a row, rows per step
+          const int g = lane % GR;
+#pragma unroll 4
+          for (int i = 0; i < 32 / RI; ++i) {
+            const int rr = quad * 32 + i * RI + lane / GR, gr = r0 + rr;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (gr < rows) {
+              const int tok = gr / a.G;
+              v = *reinterpret_cast<const uint4*>(
+                  a.q + (static_cast<int64_t>(e.start + tok) * a.H + piece.hk * a.G +
+                         (gr - tok * a.G)) * D + g * 8);
+            }
+            st_shared_v4(q_tile + (g / 8) * 16384 + sw128_offset(rr, g % 8), v.x, v.y, v.z, v.w);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();  // this warp's reads of the last piece's O precede its next MMAs
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        // no warp arrives for a later piece before every warp has for this one
+        if (!(ok = mbar_wait_warp(q_full, segs & 1, ctl))) break;
+        ++segs;
+      }
+      const int lim = r0 + row < rows ? row_limit(e, l.causal, a.G, r0 + row) : e.len;
+      const int lim_min = r0 < rows ? row_limit(e, l.causal, a.G, r0) : e.len;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = 0; j < n_mine; ++j) {
+        const int jg = base + j;
+        if (!(ok = mbar_wait_warp(&s_full[t], (seen + j) & 1, ctl))) break;
+        tc_fence_after();
+        uint32_t s[128];
+        tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+        tmem_wait_ld();
+        reg_fence(s);
+        const int k0 = (piece.ta + j) * KT;
+        const uint32_t bad = bad_pages[jg % (2 * S)];
+        const bool masked = k0 + KT > lim_min || bad != 0;
+        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (masked) {
+          // masked scores become -inf in place (never an input to arithmetic below)
+#pragma unroll
+          for (int c = 0; c < 128; ++c) {
+            const bool vis = k0 + c < lim && !((bad >> (c >> a.page_shift)) & 1u);
+            if (!vis) s[c] = 0xff800000u;
+            else mxv[c & 3] = fmaxf(mxv[c & 3], __uint_as_float(s[c]));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            mxv[0] = max3(mxv[0], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            mxv[1] = max3(mxv[1], __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+            mxv[2] = max3(mxv[2], __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+            mxv[3] = max3(mxv[3], __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+          }
+        }
+        const float mx = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3]));
+        const float m_tile = mx * c2;
+        float alpha = 1.f;
+        bool rescale = false;
+        if (m_tile > m_run) {
+          rescale = true;
+          alpha = ex2(m_run - m_tile);  // 0 at the row's first visible key
+          l_run *= alpha;
+          m_run = m_tile;
+        }
+        const float2 cc = make_float2(c2, c2);
+        const float2 nm = make_float2(-m_run, -m_run);
+        float2 sumv[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t p[64];
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
+            const float2 x = fma2(make_float2(s0, s1), cc, nm);
+            const float x0 = s0 == -INFINITY ? 0.f : ex2(x.x);
+            const float x1 = s1 == -INFINITY ? 0.f : ex2(x.y);
+            p[c] = pack_bf16(x0, x1);
+            sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float2 x = fma2(
+                make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cc, nm);
+            const float x0 = ex2(x.x), x1 = ex2(x.y);
+            p[c] = pack_bf16(x0, x1);
+            sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
+          }
+        }
+        l_run += (sumv[0].x + sumv[1].x) + (sumv[0].y + sumv[1].y);
+        tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+        tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+            reg_fence(o);
+            const float2 aa = make_float2(alpha, alpha);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                    aa);
+              o[i] = __float_as_uint(v.x);
+              o[i + 1] = __float_as_uint(v.y);
+            }
+            tmem_st32(tO + 32 * c, o);
+          }
+        }
+        // V rows of the last page past the end: cleared before this tile's P V may read them
+        // (both warpgroups do, each before its own; zeros over zeros are harmless)
+        const int past = e.len - k0;
+        if (past < KT && (past & ((1 << a.page_shift) - 1)) != 0) {
+          if (!(ok = mbar_wait_warp(&v_full[jg % S], (jg / S) & 1, ctl))) break;
+          const int rows_end = ((past >> a.page_shift) + 1) << a.page_shift;
+          const uint32_t vt = sbase + L::kV + (jg % S) * L::kTile;
+          for (int i = row; i < (rows_end - past) * (D / 8); i += 128) {
+            const int rr = past + i / (D / 8), g = i % (D / 8);
+            st_shared_v4(vt + (g / 8) * 16384 + rr * 128 + (g % 8) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+      }
+      seen += n_mine;
+      base += npos;
+      if (ok && n_mine > 0) ok = mbar_wait_warp(&o_full[t], outs++ & 1, ctl);
+      if (!ok) break;
+      tc_fence_after();
+
+      // ---- this row's result, or its part of it
+      const int tile = row_tile0(e.start, a.G, R, ww.walk.b) + piece.r;
+      const bool began = piece.ta == 0;
+      if (began && warp == 4 && lane == 0)
+        a.part.spans[static_cast<int64_t>(piece.hk) * a.part.span_tiles + tile] = span_of(sh, piece);
+      const int gr = r0 + row;
+      if (r0 < rows) {  // uniform over the warpgroup
+        const bool live = gr < rows;
+        const int tok = gr / a.G, head = piece.hk * a.G + (gr - tok * a.G);
+        const int64_t at = static_cast<int64_t>(e.start + tok) * a.H + head;
+        const bool final_out = piece.whole && a.rowbuf == nullptr;
+        const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
+        float* slot = a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (began ? 1 : 0)) *
+                                         (static_cast<int64_t>(R) * (D + 2));
+        float* dst = piece.whole ? a.rowbuf + at * D : slot + (128 * t + row) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (n_mine > 0) {
+            tmem_ld32(tO + 32 * c, o);
+            tmem_wait_ld();
+            reg_fence(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (!live) continue;
+          if (final_out) {
+            uint4* out = reinterpret_cast<uint4*>(a.o + at * D + 32 * c);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                pk[i] = pack_bf16(__uint_as_float(o[8 * g + 2 * i]) * inv,
+                                  __uint_as_float(o[8 * g + 2 * i + 1]) * inv);
+              out[g] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else {
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              st_v4(dst + 32 * c + 4 * g, __uint_as_float(o[4 * g]), __uint_as_float(o[4 * g + 1]),
+                    __uint_as_float(o[4 * g + 2]), __uint_as_float(o[4 * g + 3]));
+          }
+        }
+        if (live) {
+          if (final_out) {
+            a.lse[static_cast<int64_t>(head) * a.total + e.start + tok] =
+                l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+          } else if (piece.whole) {
+            float* st = a.rowbuf + static_cast<int64_t>(a.total) * a.H * D;
+            st[at] = m_run;
+            st[static_cast<int64_t>(a.total) * a.H + at] = l_run;
+          } else {
+            slot[R * D + 128 * t + row] = m_run;
+            slot[R * D + R + 128 * t + row] = l_run;
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+                     int64_t max_units, uint64_t timeout_ns, cudaStream_t s) {
+  using L = MmaLayout<D>;
+  const uint32_t smem = L::kBytes + 1024;
+  cudaError_t e = ensure_smem_limit<paged_mma_kernel<D>>(smem);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = max_units < kPagedMmaCtas ? max_units : kPagedMmaCtas;
+  paged_mma_kernel<D><<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(tk, tv, a, timeout_ns,
+                                                                         smem);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedArgs& a, int64_t max_units, uint64_t timeout_ns,
+                             cudaStream_t s) {
+  return d == 64 ? launch_d<64>(tk, tv, a, max_units, timeout_ns, s)
+                 : launch_d<128>(tk, tv, a, max_units, timeout_ns, s);
+}
+
+}  // namespace fa

@@ -74,7 +74,7 @@ fa_status check_cache(const fa_paged_kv* c) {
   if (c == nullptr || c->k_cache == nullptr || c->v_cache == nullptr || c->kv_lens == nullptr)
     return FA_ERR_INVALID_ARG;
   if (!aligned_to(c->k_cache, 16) || !aligned_to(c->v_cache, 16)) return FA_ERR_INVALID_ARG;
-  if (c->num_pages < 1 || c->max_pages < 0 || (c->max_pages > 0 && c->block_table == nullptr))
+  if (c->num_pages < 1 || c->num_pages > (1 << 30) || c->max_pages < 0 || (c->max_pages > 0 && c->block_table == nullptr))
     return FA_ERR_INVALID_ARG;
   if (page_shift(c->page_size) < 0) return FA_ERR_UNSUPPORTED;
   return FA_OK;
@@ -84,19 +84,45 @@ fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CU
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Cache pool as a 3-D tensor (d, page_size, pages x heads): boxes of one page x 64 columns with
+// the 128-byte swizzle.  The coordinate num_pages * Hkv lies outside and reads as zeros.
+bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int Hkv, int d) {
+  auto fn = fa::encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t page = static_cast<cuuint64_t>(c.page_size);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), page,
+                        static_cast<cuuint64_t>(c.num_pages) * static_cast<cuuint64_t>(Hkv)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, page * static_cast<cuuint64_t>(d) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(c.page_size), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows per key/value head above which a list goes to the tensor-core kernel.
+constexpr long long kMmaRows = 32;
+
 // Workspace of a paged call: the spans and slots of each list, then (joined lists) row buffers.
+// Which kernel a list takes is decided by max_q; with few rows in all it cannot be the
+// tensor-core one.
 struct PagedWorkspace {
   size_t spans[2], slots[2], rowbuf[2], total;
 };
 PagedWorkspace paged_workspace(const int (&count)[2], int lists, int total, int H, int Hkv, int d) {
   PagedWorkspace w{};
   size_t at = 0;
+  size_t slots = static_cast<size_t>(fa::kPagedMaxCtas) * 2 * fa::kPagedRows * (d + 2) * 4;
+  if (static_cast<long long>(total) * (H / Hkv) > kMmaRows) {
+    const size_t mma = static_cast<size_t>(fa::kPagedMmaCtas) * 2 * fa::kPagedMmaRows * (d + 2) * 4;
+    if (mma > slots) slots = mma;
+  }
   for (int i = 0; i < lists; ++i) {
     w.spans[i] = at;
     at += up256(static_cast<size_t>(Hkv) *
                 fa::row_tiles_bound(total, H / Hkv, fa::kPagedRows, count[i]) * sizeof(int2));
     w.slots[i] = at;
-    at += up256(static_cast<size_t>(fa::kPagedMaxCtas) * 2 * fa::kPagedRows * (d + 2) * 4);
+    at += up256(slots);
     if (lists > 1) {
       w.rowbuf[i] = at;
       at += up256(static_cast<size_t>(total) * H * (d + 2) * 4);
@@ -134,6 +160,8 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   if (!Q || !O || !LSE || !aligned_to(Q, 16) || !aligned_to(O, 16)) return FA_ERR_INVALID_ARG;
   const int lists = prefix != nullptr ? 2 : 1;
   const int count[2] = {B, prefix != nullptr ? prefix->groups : 0};
+  // pages x heads is a tensor-map coordinate
+  if (static_cast<long long>(cache->num_pages) * Hkv > kMaxInt) return FA_ERR_INVALID_ARG;
   if (lists == 2 && (static_cast<long long>(total) + count[1]) * H + 128LL * count[1] > kMaxInt)
     return FA_ERR_INVALID_ARG;
   const PagedWorkspace w = paged_workspace(count, lists, total, H, Hkv, d);
@@ -178,16 +206,30 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     l.max_q = i == 0 ? max_q : kMaxInt;
     l.group_cu = i == 0 ? nullptr : prefix->group_cu;
     l.causal = i == 0 && causal ? 1 : 0;
-    a.part.R = fa::kPagedRows;
+    a.rowbuf = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
+    // query rows of an entry: at most those of max_q tokens; of a group, its share of the batch
+    const long long tokens = i == 0 && max_q < total ? max_q : total;
+    const long long rows = (i == 0 ? tokens : (total + l.count - 1) / l.count) * a.G;
+    const bool mma = rows > kMmaRows;
+    a.part.R = mma ? fa::kPagedMmaRows : fa::kPagedRows;
+    a.part.ctas = mma ? fa::kPagedMmaCtas : fa::kPagedMaxCtas;
     a.part.span_tiles = fa::row_tiles_bound(total, a.G, a.part.R, l.count);
     a.part.spans = reinterpret_cast<int2*>(base + w.spans[i]);
     a.part.slots = reinterpret_cast<float*>(base + w.slots[i]);
-    a.part.ctas = fa::kPagedMaxCtas;
-    a.rowbuf = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
-    const long long tokens = i == 0 && max_q < total ? max_q : total;
     const long long units = static_cast<long long>(l.count) * Hkv *
-                            ((tokens * a.G + a.part.R - 1) / a.part.R) * (l.max_len / 64 + 1);
-    if ((st = status_of(fa::launch_paged(d, a, units, s))) != FA_OK) return st;
+                            ((tokens * a.G + a.part.R - 1) / a.part.R) *
+                            (l.max_len / (mma ? 128 : 64) + 1);
+    cudaError_t e;
+    if (mma) {
+      CUtensorMap tk, tv;
+      if (!make_pool_map(&tk, cache->k_cache, *cache, Hkv, d) ||
+          !make_pool_map(&tv, cache->v_cache, *cache, Hkv, d))
+        return FA_ERR_CUDA;
+      e = fa::launch_paged_mma(d, tk, tv, a, units, fa::wait_timeout_ns(), s);
+    } else {
+      e = fa::launch_paged(d, a, units, s);
+    }
+    if ((st = status_of(e)) != FA_OK) return st;
     j.list[i] = l;
     j.part[i] = a.part;
     j.rowbuf[i] = a.rowbuf;

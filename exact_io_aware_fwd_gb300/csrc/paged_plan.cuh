@@ -1,12 +1,12 @@
 // How the CTAs of a paged-attention launch share its keys.
 //
-// The work of entry b is one segment per (key/value head, row tile), each of ceil(len / KT) key
-// tiles.  Laid end to end, the segments' key tiles are units 0 .. W - 1, and CTA c takes units
-// [c W / C, (c + 1) W / C): equal shares whatever the lengths, at most two unfinished segments
-// per CTA, so the partial results take 2 C slots however long the cache is.  When no entry has
-// more than kDirectTiles key tiles, splitting would cost more than it gives (a join kernel has
-// to read the parts back): then a unit is a whole segment.  Lengths live on the device, so every
-// CTA works this out for itself from one pass over them.
+// The work of entry b is one segment per (key/value head, row tile), each of as many key tiles
+// (KT keys) as the tile's last row sees.  Laid end to end, the segments' key tiles are units
+// 0 .. W - 1, and CTA c takes units [c W / C, (c + 1) W / C): equal shares whatever the lengths,
+// at most two unfinished segments per CTA, so the partial results take 2 C slots however long
+// the cache is.  When no segment has more than kDirectTiles key tiles, splitting would cost more
+// than it gives (a join kernel has to read the parts back): then a unit is a whole segment.
+// Lengths live on the device, so every CTA works this out for itself from one pass over them.
 #pragma once
 
 #include "fa_paged.h"
@@ -16,8 +16,20 @@ namespace fa {
 struct Entry {
   int start, n, nc;  // first token, new tokens, and how many of them are computed
   int len;           // keys (clamped)
-  int tiles, rt;     // key tiles (at least 1) and row tiles (0: no tokens)
+  int rt;            // row tiles (0: no tokens)
+  int64_t tiles;     // key tiles of all its row tiles, for one key/value head
 };
+
+// Keys that row `row` (new token x group member) of an entry sees.
+__device__ __forceinline__ int row_limit(const Entry& e, int causal, int G, int row) {
+  return causal ? min(e.len, e.len - e.n + row / G + 1) : e.len;
+}
+// Key tiles of row tile r (at least one, so that a tile without keys is visited and written).
+template <int R, int KT>
+__device__ __forceinline__ int tiles_of(const Entry& e, int causal, int G, int r) {
+  const int last = min(e.nc * G, (r + 1) * R) - 1;
+  return max(1, (row_limit(e, causal, G, last) + KT - 1) / KT);
+}
 
 template <int R, int KT>
 __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b, bool report) {
@@ -40,8 +52,13 @@ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, 
   e.len = min(max(len, 0), cap);
   e.nc = min(e.n, l.max_q);
   if (report && (e.len != len || e.nc != e.n)) atomicCAS(a.status, 0, kErrIndex);
-  e.tiles = max(1, (e.len + KT - 1) / KT);
   e.rt = (e.nc * a.G + R - 1) / R;
+  if (l.causal) {
+    e.tiles = 0;
+    for (int r = 0; r < e.rt; ++r) e.tiles += tiles_of<R, KT>(e, 1, a.G, r);
+  } else {
+    e.tiles = static_cast<int64_t>(e.rt) * max(1, (e.len + KT - 1) / KT);
+  }
   return e;
 }
 
@@ -66,10 +83,9 @@ __device__ Share make_share(const PagedArgs& a) {
   int mx = 0;
   for (int b = tid; b < l.count; b += kThreads) {
     const Entry e = entry_of<R, KT>(l, a, b, blockIdx.x == 0);
-    const long long s = static_cast<long long>(e.rt) * a.Hkv;
-    seg += s;
-    til += s * e.tiles;
-    if (s > 0) mx = max(mx, e.tiles);
+    seg += static_cast<long long>(e.rt) * a.Hkv;
+    til += e.tiles * a.Hkv;
+    if (e.rt > 0) mx = max(mx, tiles_of<R, KT>(e, l.causal, a.G, e.rt - 1));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -110,7 +126,7 @@ __device__ Share make_share(const PagedArgs& a) {
     long long units = 0;
     if (b < l.count) {
       const Entry e = entry_of<R, KT>(l, a, b, false);
-      units = static_cast<long long>(e.rt) * a.Hkv * (sh.direct ? 1 : e.tiles);
+      units = (sh.direct ? e.rt : e.tiles) * a.Hkv;
     }
     long long incl = units;
 #pragma unroll
@@ -141,9 +157,73 @@ __device__ Share make_share(const PagedArgs& a) {
   return sh;
 }
 
+// A CTA's piece of one segment: key tiles [ta, te) of row tile r for key/value head hk.
+struct Piece {
+  int hk, r, ta, te;
+  bool whole;    // no other CTA works on the segment
+  int64_t unit;  // the segment's first unit
+  int tiles;     // its key tiles
+};
+
+// Walks the pieces of a CTA's share in order; e is the entry b of the current piece.
+template <int R, int KT>
+struct Walk {
+  int64_t u, u1, within;
+  int b;
+  bool direct;
+  Entry e;
+
+  __device__ Walk(const Share& sh, const PagedArgs& a)
+      : u(sh.u0), u1(sh.u1), within(sh.off), b(sh.b), direct(sh.direct) {
+    e = entry_of<R, KT>(a.list, a, b, false);
+  }
+  __device__ bool next(const PagedArgs& a, Piece& p) {
+    if (u >= u1) return false;
+    while (within >= (direct ? e.rt : e.tiles) * a.Hkv) {  // next entry with tokens
+      if (++b >= a.list.count) return false;               // cannot happen while u < W
+      e = entry_of<R, KT>(a.list, a, b, false);
+      within = 0;
+    }
+    const int64_t per_head = direct ? e.rt : e.tiles;
+    p.hk = static_cast<int>(within / per_head);
+    int64_t rem = within - p.hk * per_head;
+    p.r = 0;
+    if (direct) {
+      p.r = static_cast<int>(rem);
+      p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
+      p.ta = 0;
+      p.te = p.tiles;
+      p.whole = true;
+      p.unit = u;
+      ++u;
+      ++within;
+      return true;
+    }
+    p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, 0);
+    while (rem >= p.tiles) {
+      rem -= p.tiles;
+      ++p.r;
+      p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
+    }
+    p.ta = static_cast<int>(rem);
+    const int64_t take = min(static_cast<int64_t>(p.tiles - p.ta), u1 - u);
+    p.te = p.ta + static_cast<int>(take);
+    p.whole = take == p.tiles;
+    p.unit = u - p.ta;
+    u += take;
+    within += take;
+    return true;
+  }
+};
+
 // CTA that owns unit u: the largest c with floor(c W / C) <= u.
 __device__ __forceinline__ int owner_of(const Share& sh, int64_t u) {
   return static_cast<int>(((u + 1) * sh.C - 1) / sh.W);
+}
+// (first CTA, number of CTAs) of the segment that this CTA begins.
+__device__ __forceinline__ int2 span_of(const Share& sh, const Piece& p) {
+  const int first = blockIdx.x;
+  return make_int2(first, p.whole ? 1 : owner_of(sh, p.unit + p.tiles - 1) - first + 1);
 }
 
 }  // namespace fa
