@@ -10,9 +10,10 @@
 //    out-of-range coordinate gives zeros for pages past the end or outside the pool;
 //  * the rows of the last page past the sequence's end may hold anything (an infinity times a
 //    zero weight would be NaN), so the softmax warps clear them in the V tile before P V;
-//  * CTAs are persistent and take equal shares of all key tiles (paged_plan.cuh): the TMA warp
-//    runs ahead into the next segment while the softmax warps finish the last one, and a segment
-//    that several CTAs share leaves float32 parts for the join kernel.
+//  * CTAs are persistent and take equal shares of all key tiles (paged_plan.cuh).  Warp 2 works
+//    out the CTA's pieces and hands them to the other roles through a ring in shared memory, so
+//    the TMA warp runs ahead into the next piece while the softmax warps finish the last one; a
+//    segment that several CTAs share leaves float32 parts for the join kernel.
 // Bound by the tensor pipe when both query tiles are full (512 flops per K, V byte at 256 rows);
 // with one tile of few rows by the copies from memory.
 #include "fa_internal.h"
@@ -24,11 +25,24 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 384;  // warp 0: TMA, warp 1: MMA, warps 4-7 and 8-11: softmax
+constexpr int kThreads = 384;  // warp 0: TMA, 1: MMA, 2: pieces, 4-7 and 8-11: softmax
 constexpr int R = kPagedMmaRows;
 constexpr int KT = 128;
 constexpr int kDirectTiles = 4;
 constexpr float kLn2 = 0.693147180559945309f;
+
+// What the roles need to know of a piece, in a ring of shared memory.
+struct PieceInfo {
+  int n[2];        // key tiles of each query tile (the first n of the piece's); -1: no more pieces
+  int ta;          // first key tile
+  int hk, row0;    // key/value head, first row of the row tile
+  int start, rows; // the entry's first token and its rows (computed tokens x group)
+  int len, shift;  // keys, and keys minus tokens (row r sees shift + r / G + 1 keys if causal)
+  int tile;        // row tile's index in the spans
+  int whole;       // no other CTA works on the segment
+  const int32_t* table;  // the entry's block-table row
+};
+constexpr int kRing = 4;
 
 template <int D>
 struct MmaLayout {
@@ -39,21 +53,15 @@ struct MmaLayout {
   static constexpr uint32_t kV = kK + kStages * kTile;
   static constexpr uint32_t kBar = kV + kStages * kTile;
   // q_full, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2], p_full[2], o_full[2], done
-  static constexpr int kNumBars = 1 + 4 * kStages + 7;
+  // piece_full[kRing], piece_empty[kRing]
+  static constexpr int kNumBars = 1 + 4 * kStages + 7 + 2 * kRing;
   static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
   static constexpr uint32_t kAbort = kTmemSlot + 4;
   static constexpr uint32_t kBad = kAbort + 4;  // [2 S]: pages of a position outside the pool
-  static constexpr uint32_t kBytes = kBad + 2 * kStages * 4;
+  static constexpr uint32_t kPieces = (kBad + 2 * kStages * 4 + 7) & ~7u;
+  static constexpr uint32_t kBytes = kPieces + kRing * sizeof(PieceInfo);
   static constexpr uint32_t kColS0 = 0, kColO0 = 256;
   static constexpr uint32_t kTmemCols = 512;
-};
-
-// A softmax warp's walk over the CTA's pieces, kept in shared memory: the 128 scores of a row
-// leave no registers for it.
-struct WarpWalk {
-  Walk<R, KT> walk;
-  Piece piece;
-  bool more;
 };
 
 // Key tiles of query tile t (rows [256 r + 128 t, + 128)) inside the piece's range.
@@ -89,7 +97,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmemSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kAbort);
   volatile uint32_t* bad_pages = reinterpret_cast<volatile uint32_t*>(sm + L::kBad);
-  __shared__ __align__(8) uint8_t walks[8][sizeof(WarpWalk)];
+  uint64_t* piece_full = mma_done + 1;
+  uint64_t* piece_empty = piece_full + kRing;
+  PieceInfo* pieces = reinterpret_cast<PieceInfo*>(sm + L::kPieces);
   const Ctl ctl{abort_flag, a.status, timeout_ns};
   const uint32_t warp = warp_id(), lane = lane_id();
   if (pad + L::kBytes > smem_bytes) {  // cannot happen with the host's sizing; never proceed
@@ -115,6 +125,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&o_full[t], 1);
     }
     mbar_init(mma_done, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], 10);  // TMA warp, MMA thread, 8 softmax warps
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -128,41 +142,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t sbase = smem_u32(sm);
-  // Every role walks the CTA's pieces for itself.  Registers: the launch gives 384 x 168; warps
-  // 0-3 keep 72 and the softmax warps take 216 (128 x 72 + 256 x 216 = 384 x 168), enough for a
-  // row's scores and weights without spills.
+  // Registers: the launch gives 384 x 168; warps 0-3 keep 72 and the softmax warps take 216
+  // (128 x 72 + 256 x 216 = 384 x 168), enough for a row's scores and weights without spills.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0) {
-      Walk<R, KT> walk(sh, a);
-      Piece piece;
+    if (warp == 2) {
+      // ================= the CTA's pieces
+      if (lane == 0) {
+        Walk<R, KT> walk(sh, a);
+        const Entry& e = walk.e;
+        Piece piece;
+        for (int i = 0;; ++i) {
+          const bool more = walk.next(a, piece);
+          if (!mbar_wait(&piece_empty[i % kRing], ((i / kRing) & 1) ^ 1, ctl)) break;
+          PieceInfo& p = pieces[i % kRing];
+          if (more) {
+            p.n[0] = tiles_in_piece(e, piece, l.causal, a.G, 0);
+            p.n[1] = tiles_in_piece(e, piece, l.causal, a.G, 1);
+            p.ta = piece.ta;
+            p.hk = piece.hk;
+            p.row0 = piece.r * R;
+            p.start = e.start;
+            p.rows = e.nc * a.G;
+            p.len = e.len;
+            p.shift = e.len - e.n;
+            p.tile = row_tile0(e.start, a.G, R, walk.b) + piece.r;
+            p.whole = piece.whole;
+            p.table = l.table + static_cast<int64_t>(walk.b) * l.max_pages;
+            if (piece.ta == 0)  // this CTA begins the segment
+              a.part.spans[static_cast<int64_t>(piece.hk) * a.part.span_tiles + p.tile] =
+                  span_of(sh, piece);
+          } else {
+            p.n[0] = p.n[1] = -1;
+          }
+          mbar_arrive(&piece_full[i % kRing]);
+          if (!more) break;
+        }
+      }
+    } else if (warp == 0) {
       // ================= TMA producer: one box (page x 64 columns) per lane
       const int page_size = 1 << a.page_shift, pages = KT >> a.page_shift;
       const int pg = lane & (pages - 1), panel = lane / pages;
       const bool mine = panel < P;
       int jk = 0, jv = 0;  // positions whose K and V copies have been issued
       bool ok = true;
-      while (ok && walk.next(a, piece)) {
-        const Entry& e = walk.e;
-        const int npos = max(tiles_in_piece(e, piece, l.causal, a.G, 0),
-                             tiles_in_piece(e, piece, l.causal, a.G, 1));
-        const int32_t* trow = l.table + static_cast<int64_t>(walk.b) * l.max_pages;
+      for (int i = 0;; ++i) {
+        if (!(ok = mbar_wait_warp(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
+        const PieceInfo& p = pieces[i % kRing];
+        const int npos = max(p.n[0], p.n[1]);
+        const int32_t* trow = p.table;
+        const int len = p.len, hk = p.hk, ta = p.ta;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&piece_empty[i % kRing]);  // all of it is in registers
+        if (npos < 0) break;
         // page of this lane's box at key tile kt: out of range past the end, bad outside the pool
         auto find = [&](int kt, bool& bad) {
           const int key = kt * KT + pg * page_size;
-          const int p = key < e.len ? resolve_page(trow, l.max_pages, a.num_pages, a.page_shift, key)
-                                    : -1;
-          bad = key < e.len && p < 0;
-          return p < 0 ? a.num_pages * a.Hkv : p * a.Hkv + piece.hk;
+          const int page =
+              key < len ? resolve_page(trow, l.max_pages, a.num_pages, a.page_shift, key) : -1;
+          bad = key < len && page < 0;
+          return page < 0 ? a.num_pages * a.Hkv : page * a.Hkv + hk;
         };
         bool bad = false, bad_next = false;
-        int z = 0, z_next = npos > 0 ? find(piece.ta, bad_next) : 0;
+        int z = 0, z_next = npos > 0 ? find(ta, bad_next) : 0;
         for (int j = 0; j < npos; ++j) {
           const int s = jk % S;
           const uint32_t ph = (jk / S) & 1;
           z = z_next;
           bad = bad_next;
-          if (j + 1 < npos) z_next = find(piece.ta + j + 1, bad_next);
+          if (j + 1 < npos) z_next = find(ta + j + 1, bad_next);
           const uint32_t mask = __ballot_sync(~0u, bad) & ((1u << pages) - 1u);
           if (!(ok = mbar_wait_warp(&k_empty[s], ph ^ 1, ctl))) break;
           if (lane == 0) {
@@ -180,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (mine) tma_load_3d(sm + L::kV + at, &tmV, &v_full[s], panel * 64, 0, z);
           ++jv;
         }
+        if (!ok) break;
       }
       // no copy into this CTA's shared memory may still be in flight when the CTA exits
       if (lane == 0) {
@@ -189,17 +238,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ================= MMA issuer
       if (lane == 0) {
-        Walk<R, KT> walk(sh, a);
-        Piece piece;
         constexpr uint32_t idS = idesc_bf16(128, 128, false, false);  // S = Q K^T, both K-major
         constexpr uint32_t idO = idesc_bf16(128, D, false, true);     // O += P V, V is MN-major
         int base = 0, segs = 0;  // positions and pieces before this one
         int issued[2] = {0, 0};  // S MMAs per query tile, over all pieces
         bool ok = true;
-        while (ok && walk.next(a, piece)) {
-          const int n[2] = {tiles_in_piece(walk.e, piece, l.causal, a.G, 0),
-                            tiles_in_piece(walk.e, piece, l.causal, a.G, 1)};
+        for (int i = 0; ok; ++i) {
+          if (!(ok = mbar_wait(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
+          const int n[2] = {pieces[i % kRing].n[0], pieces[i % kRing].n[1]};
+          mbar_arrive(&piece_empty[i % kRing]);
           const int npos = max(n[0], n[1]);
+          if (npos < 0) break;
           if (npos == 0) continue;
           if (!(ok = mbar_wait(q_full, segs & 1, ctl))) break;
           ++segs;
@@ -209,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j < npos && !(ok = mbar_wait(&k_full[s], (jg / S) & 1, ctl))) break;
             if (j >= 1 && !(ok = mbar_wait(&v_full[sp], ((jg - 1) / S) & 1, ctl))) break;
             tc_fence_after();
-  #pragma unroll
+#pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (j >= 1 && j - 1 < n[t]) {
                 if (!(ok = mbar_wait(&p_full[t], (issued[t] - 1) & 1, ctl))) break;
@@ -252,34 +301,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     int base = 0, segs = 0;  // positions and pieces with keys before this one
     int seen = 0, outs = 0;  // S tiles and results of this query tile before this piece
     bool ok = true;
-    WarpWalk& ww = *reinterpret_cast<WarpWalk*>(walks[warp - 4]);
-    if (lane == 0) ww.walk = Walk<R, KT>(sh, a);
-    const Piece& piece = ww.piece;
-    const Entry& e = ww.walk.e;
-    while (true) {
-      __syncwarp();
-      if (lane == 0) ww.more = ww.walk.next(a, ww.piece);
-      __syncwarp();
-      if (!ww.more) break;
-      const int n_mine = tiles_in_piece(e, piece, l.causal, a.G, t);
-      const int npos = max(n_mine, tiles_in_piece(e, piece, l.causal, a.G, 1 - t));
-      const int rows = e.nc * a.G, r0 = piece.r * R + 128 * t;  // r0: the tile's first row
+    for (int i = 0;; ++i) {
+      if (!(ok = mbar_wait_warp(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
+      const PieceInfo& piece = pieces[i % kRing];  // held until the piece is done
+      const int n_mine = piece.n[t];
+      if (n_mine < 0) break;
+      const int npos = max(piece.n[0], piece.n[1]);
+      const int rows = piece.rows, r0 = piece.row0 + 128 * t;  // r0: the tile's first row
       if (npos > 0) {
         // ---- the tile's queries: lanes 0-15 and 16-31 (d = 128) gather one row each time
         if (n_mine > 0) {
           constexpr int GR = D / 8, RI = 32 / GR;  // granules of a row, rows per step
           const int g = lane % GR;
-#pragma unroll 4
-          for (int i = 0; i < 32 / RI; ++i) {
-            const int rr = quad * 32 + i * RI + lane / GR, gr = r0 + rr;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (gr < rows) {
-              const int tok = gr / a.G;
-              v = *reinterpret_cast<const uint4*>(
-                  a.q + (static_cast<int64_t>(e.start + tok) * a.H + piece.hk * a.G +
-                         (gr - tok * a.G)) * D + g * 8);
+          // four loads in flight a round; a compact loop, because code that runs once a piece
+          // comes from a cold instruction cache
+#pragma unroll 1
+          for (int k = 0; k < 32 / RI; k += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int gr = r0 + quad * 32 + (k + u) * RI + lane / GR;
+              v[u] = make_uint4(0u, 0u, 0u, 0u);
+              if (gr < rows) {
+                const int tok = gr / a.G;
+                v[u] = *reinterpret_cast<const uint4*>(
+                    a.q + (static_cast<int64_t>(piece.start + tok) * a.H + piece.hk * a.G +
+                           (gr - tok * a.G)) * D + g * 8);
+              }
             }
-            st_shared_v4(q_tile + (g / 8) * 16384 + sw128_offset(rr, g % 8), v.x, v.y, v.z, v.w);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              st_shared_v4(q_tile + (g / 8) * 16384 +
+                               sw128_offset(quad * 32 + (k + u) * RI + lane / GR, g % 8),
+                           v[u].x, v[u].y, v[u].z, v[u].w);
           }
           fence_proxy_async_smem();
         }
@@ -290,8 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait_warp(q_full, segs & 1, ctl))) break;
         ++segs;
       }
-      const int lim = r0 + row < rows ? row_limit(e, l.causal, a.G, r0 + row) : e.len;
-      const int lim_min = r0 < rows ? row_limit(e, l.causal, a.G, r0) : e.len;
+      // keys below lim are visible to this row, and below lim_min to every row of the tile
+      const int len = piece.len, ta = piece.ta;
+      const int lim = l.causal && r0 + row < rows ? min(len, piece.shift + (r0 + row) / a.G + 1) : len;
+      const int lim_min = l.causal ? min(len, piece.shift + r0 / a.G + 1) : len;
+      // position whose last page ends inside it: that page's rows past the end are cleared
+      const int tail = len & ((1 << a.page_shift) - 1), j_tail = tail != 0 ? len / KT - ta : -1;
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = 0; j < n_mine; ++j) {
         const int jg = base + j;
@@ -304,18 +362,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
         tmem_wait_ld();
         reg_fence(s);
-        const int k0 = (piece.ta + j) * KT;
+        const int k0 = (ta + j) * KT;
         const uint32_t bad = bad_pages[jg % (2 * S)];
         const bool masked = k0 + KT > lim_min || bad != 0;
+        auto visible = [&](int c) {
+          return k0 + c < lim && !((bad >> (c >> a.page_shift)) & 1u);
+        };
         float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (masked) {
-          // masked scores become -inf in place (never an input to arithmetic below)
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const bool vis = k0 + c < lim && !((bad >> (c >> a.page_shift)) & 1u);
-            if (!vis) s[c] = 0xff800000u;
-            else mxv[c & 3] = fmaxf(mxv[c & 3], __uint_as_float(s[c]));
-          }
+          for (int c = 0; c < 128; ++c)
+            if (visible(c)) mxv[c & 3] = fmaxf(mxv[c & 3], __uint_as_float(s[c]));
         } else {
 #pragma unroll
           for (int c = 0; c < 128; c += 8) {
@@ -342,10 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (masked) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) {
-            const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
-            const float2 x = fma2(make_float2(s0, s1), cc, nm);
-            const float x0 = s0 == -INFINITY ? 0.f : ex2(x.x);
-            const float x1 = s1 == -INFINITY ? 0.f : ex2(x.y);
+            const float2 x = fma2(
+                make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cc, nm);
+            const float x0 = visible(2 * c) ? ex2(x.x) : 0.f;
+            const float x1 = visible(2 * c + 1) ? ex2(x.y) : 0.f;
             p[c] = pack_bf16(x0, x1);
             sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
           }
@@ -382,12 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // V rows of the last page past the end: cleared before this tile's P V may read them
         // (both warpgroups do, each before its own; zeros over zeros are harmless)
-        const int past = e.len - k0;
-        if (past < KT && (past & ((1 << a.page_shift) - 1)) != 0) {
+        if (j == j_tail) {
           if (!(ok = mbar_wait_warp(&v_full[jg % S], (jg / S) & 1, ctl))) break;
-          const int rows_end = ((past >> a.page_shift) + 1) << a.page_shift;
+          const int past = len - k0, clear = ((1 << a.page_shift) - tail) * (D / 8);
           const uint32_t vt = sbase + L::kV + (jg % S) * L::kTile;
-          for (int i = row; i < (rows_end - past) * (D / 8); i += 128) {
+          for (int i = row; i < clear; i += 128) {
             const int rr = past + i / (D / 8), g = i % (D / 8);
             st_shared_v4(vt + (g / 8) * 16384 + rr * 128 + (g % 8) * 16, 0u, 0u, 0u, 0u);
           }
@@ -405,21 +461,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
 
       // ---- this row's result, or its part of it
-      const int tile = row_tile0(e.start, a.G, R, ww.walk.b) + piece.r;
-      const bool began = piece.ta == 0;
-      if (began && warp == 4 && lane == 0)
-        a.part.spans[static_cast<int64_t>(piece.hk) * a.part.span_tiles + tile] = span_of(sh, piece);
       const int gr = r0 + row;
       if (r0 < rows) {  // uniform over the warpgroup
         const bool live = gr < rows;
         const int tok = gr / a.G, head = piece.hk * a.G + (gr - tok * a.G);
-        const int64_t at = static_cast<int64_t>(e.start + tok) * a.H + head;
+        const int64_t at = static_cast<int64_t>(piece.start + tok) * a.H + head;
         const bool final_out = piece.whole && a.rowbuf == nullptr;
         const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
-        float* slot = a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (began ? 1 : 0)) *
+        float* slot = a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (ta == 0 ? 1 : 0)) *
                                          (static_cast<int64_t>(R) * (D + 2));
         float* dst = piece.whole ? a.rowbuf + at * D : slot + (128 * t + row) * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           if (n_mine > 0) {
@@ -451,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (live) {
           if (final_out) {
-            a.lse[static_cast<int64_t>(head) * a.total + e.start + tok] =
+            a.lse[static_cast<int64_t>(head) * a.total + piece.start + tok] =
                 l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
           } else if (piece.whole) {
             float* st = a.rowbuf + static_cast<int64_t>(a.total) * a.H * D;
@@ -463,6 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&piece_empty[i % kRing]);
     }
   }
 

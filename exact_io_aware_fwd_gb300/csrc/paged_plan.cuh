@@ -7,11 +7,22 @@
 // the cache is.  When no segment has more than kDirectTiles key tiles, splitting would cost more
 // than it gives (a join kernel has to read the parts back): then a unit is a whole segment.
 // Lengths live on the device, so every CTA works this out for itself from one pass over them.
+//
+// A CTA takes the pieces of its share last to first.  Then the CTAs of one head's row tiles all
+// start at key tile 0 of some row tile and walk the keys abreast, and so do they later in the
+// tails they began with in unit order: row tiles meet the same K, V in L2 instead of reading
+// them at different times.
 #pragma once
 
 #include "fa_paged.h"
 
 namespace fa {
+
+// Quotient of non-negative numbers; most fit 32 bits, where the division is several times shorter.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
 
 struct Entry {
   int start, n, nc;  // first token, new tokens, and how many of them are computed
@@ -66,8 +77,8 @@ struct Share {
   int64_t W, u0, u1;  // all units, and this CTA's
   int C;              // CTAs that have units
   bool direct;        // a unit is a whole segment
-  int b;              // entry of unit u0
-  int64_t off;        // its units before u0
+  int b;              // entry of unit u1 - 1
+  int64_t off;        // its units before u1
 };
 
 // Called by all kThreads threads of the CTA.
@@ -79,12 +90,18 @@ __device__ Share make_share(const PagedArgs& a) {
   __shared__ long long at[2];
   const KeyList& l = a.list;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long seg = 0, til = 0;
+  long long seg = 0, til = 0;         // over all entries
+  long long my_seg = 0, my_til = 0;   // of entry tid
   int mx = 0;
   for (int b = tid; b < l.count; b += kThreads) {
     const Entry e = entry_of<R, KT>(l, a, b, blockIdx.x == 0);
-    seg += static_cast<long long>(e.rt) * a.Hkv;
-    til += e.tiles * a.Hkv;
+    const long long s = static_cast<long long>(e.rt) * a.Hkv, t = e.tiles * a.Hkv;
+    if (b == tid) {
+      my_seg = s;
+      my_til = t;
+    }
+    seg += s;
+    til += t;
     if (e.rt > 0) mx = max(mx, tiles_of<R, KT>(e, l.causal, a.G, e.rt - 1));
   }
 #pragma unroll
@@ -114,19 +131,23 @@ __device__ Share make_share(const PagedArgs& a) {
   const long long most = sh.direct ? sh.W : (sh.W + kDirectTiles / 2 - 1) / (kDirectTiles / 2);
   sh.C = static_cast<int>(most < gridDim.x ? most : gridDim.x);
   const int c = blockIdx.x;
-  sh.u0 = c < sh.C ? c * sh.W / sh.C : 0;
-  sh.u1 = c < sh.C ? (c + 1) * sh.W / sh.C : 0;
+  sh.u0 = c < sh.C ? quotient(c * sh.W, sh.C) : 0;
+  sh.u1 = c < sh.C ? quotient((c + 1) * sh.W, sh.C) : 0;
   sh.b = 0;
   sh.off = 0;
   if (sh.u0 >= sh.u1) return sh;  // uniform over the CTA
-  // entry of unit u0: scan the entries kThreads at a time
+  // entry of unit u1 - 1: scan the entries kThreads at a time
+  const int64_t last = sh.u1 - 1;
   long long before = 0;
   for (int b0 = 0; b0 < l.count; b0 += kThreads) {
     const int b = b0 + tid;
-    long long units = 0;
-    if (b < l.count) {
-      const Entry e = entry_of<R, KT>(l, a, b, false);
-      units = (sh.direct ? e.rt : e.tiles) * a.Hkv;
+    long long units = sh.direct ? my_seg : my_til;
+    if (b0 > 0) {
+      units = 0;
+      if (b < l.count) {
+        const Entry e = entry_of<R, KT>(l, a, b, false);
+        units = (sh.direct ? e.rt : e.tiles) * a.Hkv;
+      }
     }
     long long incl = units;
 #pragma unroll
@@ -144,12 +165,12 @@ __device__ Share make_share(const PagedArgs& a) {
       chunk += red[w][0];
     }
     incl += pre;
-    if (units > 0 && incl - units <= sh.u0 && sh.u0 < incl) {
+    if (units > 0 && incl - units <= last && last < incl) {
       at[0] = b;
-      at[1] = sh.u0 - (incl - units);
+      at[1] = sh.u1 - (incl - units);
     }
     before = chunk;
-    if (sh.u0 < before) break;  // uniform
+    if (last < before) break;  // uniform
   }
   __syncthreads();
   sh.b = static_cast<int>(at[0]);
@@ -165,60 +186,60 @@ struct Piece {
   int tiles;     // its key tiles
 };
 
-// Walks the pieces of a CTA's share in order; e is the entry b of the current piece.
+// Walks the pieces of a CTA's share, last to first; e is the entry b of the current piece.
 template <int R, int KT>
 struct Walk {
-  int64_t u, u1, within;
+  int64_t u0, u1;   // what is left of the share
+  int64_t within;   // units of entry b before u1
   int b;
   bool direct;
   Entry e;
 
   __device__ Walk(const Share& sh, const PagedArgs& a)
-      : u(sh.u0), u1(sh.u1), within(sh.off), b(sh.b), direct(sh.direct) {
+      : u0(sh.u0), u1(sh.u1), within(sh.off), b(sh.b), direct(sh.direct) {
     e = entry_of<R, KT>(a.list, a, b, false);
   }
   __device__ bool next(const PagedArgs& a, Piece& p) {
-    if (u >= u1) return false;
-    while (within >= (direct ? e.rt : e.tiles) * a.Hkv) {  // next entry with tokens
-      if (++b >= a.list.count) return false;               // cannot happen while u < W
+    if (u0 >= u1) return false;
+    while (within <= 0) {          // the entry before with tokens
+      if (--b < 0) return false;   // cannot happen while u1 > 0
       e = entry_of<R, KT>(a.list, a, b, false);
-      within = 0;
+      within = (direct ? e.rt : e.tiles) * a.Hkv;
     }
-    const int64_t per_head = direct ? e.rt : e.tiles;
-    p.hk = static_cast<int>(within / per_head);
-    int64_t rem = within - p.hk * per_head;
-    p.r = 0;
+    const int64_t per_head = direct ? e.rt : e.tiles, x = within - 1;
+    p.hk = static_cast<int>(quotient(x, per_head));
+    int64_t rem = x - p.hk * per_head;
     if (direct) {
       p.r = static_cast<int>(rem);
       p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
       p.ta = 0;
       p.te = p.tiles;
       p.whole = true;
-      p.unit = u;
-      ++u;
-      ++within;
+      p.unit = --u1;
+      --within;
       return true;
     }
+    p.r = 0;
     p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, 0);
     while (rem >= p.tiles) {
       rem -= p.tiles;
       ++p.r;
       p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
     }
-    p.ta = static_cast<int>(rem);
-    const int64_t take = min(static_cast<int64_t>(p.tiles - p.ta), u1 - u);
-    p.te = p.ta + static_cast<int>(take);
+    p.te = static_cast<int>(rem) + 1;
+    p.unit = u1 - p.te;
+    const int take = static_cast<int>(min(static_cast<int64_t>(p.te), u1 - u0));
+    p.ta = p.te - take;
     p.whole = take == p.tiles;
-    p.unit = u - p.ta;
-    u += take;
-    within += take;
+    u1 -= take;
+    within -= take;
     return true;
   }
 };
 
 // CTA that owns unit u: the largest c with floor(c W / C) <= u.
 __device__ __forceinline__ int owner_of(const Share& sh, int64_t u) {
-  return static_cast<int>(((u + 1) * sh.C - 1) / sh.W);
+  return static_cast<int>(quotient((u + 1) * sh.C - 1, sh.W));
 }
 // (first CTA, number of CTAs) of the segment that this CTA begins.
 __device__ __forceinline__ int2 span_of(const Share& sh, const Piece& p) {
