@@ -2,13 +2,14 @@
 //
 // O = softmax(scale q K^T) V for the queries of one sequence that share a key/value head (group
 // members x new tokens), 16 rows at a time: each K, V element is used by at most 16 rows, so the
-// kernel is bound by reading the cache once.  A warp takes 16 keys of every 64-key tile and is a
+// kernel is bound by reading the cache once.  A warp takes 16 keys of every 128-key tile and is a
 // pipeline of its own: it copies its keys' rows with cp.async into a private ring of
 // shared-memory stages (keys past the length become zeros, whatever the page holds there), and
 // computes S (m16n8k16), the online softmax and O += P V from the ring, with no barrier between
-// warps until a segment's end, where the four partial (m, l, O) are merged through shared memory.
-// mma.sync is enough here: 16 rows x 4 flops per element and 2 bytes is 32 flops a byte, a few
-// percent of the tensor pipe at full memory bandwidth.
+// warps until a piece's end, where the eight partial (m, l, O) are merged through shared memory.
+// The copies of the next piece's first steps are issued before that, so memory does not wait for
+// the merge.  mma.sync is enough here: 16 rows x 4 flops per element and 2 bytes is 32 flops a
+// byte, a few percent of the tensor pipe at full memory bandwidth.
 #include "fa_internal.h"
 #include "fa_paged.h"
 #include "paged_plan.cuh"
@@ -18,24 +19,26 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kHalfWarps = kWarps / 2;
 constexpr int R = kPagedRows;
 constexpr int kKeys = 16;             // keys of a warp's step
 constexpr int KT = kKeys * kWarps;    // keys of a tile
 constexpr int kDirectTiles = kPagedUnsplitKeys / KT;  // one CTA for a whole segment
 constexpr float kLn2 = 0.693147180559945309f;
 
+// One CTA per SM: a ring of 8 warps x stages (192 KB: with all but one stage of each in flight,
+// 128 to 160 KB cover the latency of memory at full rate), and the merge buffer of half the warps.
 template <int D>
 struct PagedLayout {
-  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr uint32_t kHalf = kKeys * D * 2u;                // K or V of a step
   static constexpr uint32_t kStage = 2 * kHalf;
   static constexpr uint32_t kRing = kWarps * kStages * kStage;
   static constexpr int kPad = D + 4;                               // floats per merged row
-  static constexpr uint32_t kMerge = kWarps * R * (kPad + 2) * 4u;
-  static constexpr uint32_t kBytes = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kCtasPerSm = D == 128 ? 2 : 3;
+  static constexpr uint32_t kMerge = kHalfWarps * R * (kPad + 2) * 4u;
+  static constexpr uint32_t kBytes = kRing + kMerge;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -76,224 +79,272 @@ __device__ __forceinline__ uint32_t step_offset(uint32_t r, uint32_t g) {
   return r * (D * 2u) + ((g ^ (r & 7u)) << 4);  // the xor stays within the granule's 128 bytes
 }
 
+// What a warp needs to copy its steps of a piece.
+struct Source {
+  const int32_t* trow;  // block-table row
+  int hk, len;          // key/value head, keys
+  int first, steps;     // 16-key block of step 0 (the next is kWarps further), number of steps
+  int pages;            // lane i: page of step (issue & ~31) + i
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, PagedLayout<D>::kCtasPerSm)
-    paged_kernel(const PagedArgs a) {
+__device__ __forceinline__ Source source_of(const PagedArgs& a, const Walk<R, KT>& w,
+                                            const Piece& p, int warp) {
+  Source s;
+  s.trow = a.list.table + static_cast<int64_t>(w.b) * a.list.max_pages;
+  s.hk = p.hk;
+  s.len = w.e.len;
+  s.first = p.ta * kWarps + warp;
+  // steps with a key below the length
+  const int blocks = (w.e.len + kKeys - 1) / kKeys;
+  s.steps = min(p.te - p.ta, max(0, (blocks - s.first + kWarps - 1) / kWarps));
+  s.pages = -1;
+  return s;
+}
+
+// Copies step st into its stage; every call commits a group, empty past the last step.  Bit i of
+// `missing`: the page of stage i is out of range.
+template <int D>
+__device__ __forceinline__ void issue_step(const PagedArgs& a, Source& s, int st, uint32_t ring,
+                                           int lane, uint32_t& missing) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages, GR = D / 8;  // granules of a row
+  if (st < s.steps) {
+    if ((st & 31) == 0) {
+      const int blk = s.first + (st + lane) * kWarps;
+      s.pages = st + lane < s.steps ? resolve_page(s.trow, a.list.max_pages, a.num_pages,
+                                                   a.page_shift, blk * kKeys)
+                                    : 0;
+    }
+    const int page = __shfl_sync(~0u, s.pages, st & 31);
+    const int key0 = (s.first + st * kWarps) * kKeys;
+    const int slot = st % S;
+    missing = page < 0 ? missing | (1u << slot) : missing & ~(1u << slot);
+    if (page < 0 && lane == 0) atomicCAS(a.status, 0, kErrIndex);
+    const int64_t base = (((static_cast<int64_t>(max(page, 0)) * a.Hkv + s.hk) << a.page_shift) +
+                          (key0 & ((1 << a.page_shift) - 1))) * D;
+    const uint32_t dst = ring + slot * L::kStage;
+#pragma unroll
+    for (int i = 0; i < kKeys * GR / 32; ++i) {
+      const int r = (i * 32 + lane) / GR, g = (i * 32 + lane) % GR;
+      const bool valid = page >= 0 && key0 + r < s.len;
+      const int64_t off = valid ? base + r * D + g * 8 : 0;
+      cp_async16(dst + step_offset<D>(r, g), a.k_cache + off, valid);
+      cp_async16(dst + L::kHalf + step_offset<D>(r, g), a.v_cache + off, valid);
+    }
+  }
+  cp_commit();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
+  using L = PagedLayout<D>;
+  constexpr int S = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  begin_launch(a.first);
   const Share sh = make_share<R, KT, kThreads, kDirectTiles>(a);
-  if (sh.u0 >= sh.u1) return;
   const KeyList& l = a.list;
   const uint32_t ring = smem_u32(smem) + warp * (S * L::kStage);
+  float* mo = reinterpret_cast<float*>(smem + L::kRing);  // [half the warps][row][kPad]
+  float* mm = mo + kHalfWarps * R * L::kPad;              // [..][row]
+  float* ml = mm + kHalfWarps * R;
 
-  Walk<R, KT> walk(sh, a);
-  Piece piece;
-  while (walk.next(a, piece)) {
-    const Entry& e = walk.e;
-    const int b = walk.b, hk = piece.hk, rtile = piece.r;
-    const int tile_a = piece.ta, tile_e = piece.te;
-    const bool whole = piece.whole;
+  if (sh.u0 < sh.u1) {
+    Walk<R, KT> walk(sh);
+    Piece next_piece;
+    bool more = walk.next(a, next_piece);
+    Source src = source_of<D>(a, walk, next_piece, warp);
+    uint32_t missing = 0;
+    for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane, missing);
+    while (more) {
+      const Piece piece = next_piece;
+      const Entry e = walk.e;
+      const int tile = row_tile0(e.start, a.G, R, walk.b) + piece.r;
+      const int hk = piece.hk;
 
-    // ---- the rows' queries as A fragments: thread holds rows lane / 4 and lane / 4 + 8
-    const int rows = min(R, e.nc * a.G - rtile * R);
-    uint32_t qf[D / 16][4];
-    int lim[2];  // keys below it are visible to the row
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = (lane >> 2) + 8 * i;
-      const int row = rtile * R + rr;
-      const int tok = row / a.G;
-      lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row) : e.len;
-      const __nv_bfloat16* qp =
-          a.q + (static_cast<int64_t>(e.start + tok) * a.H + hk * a.G + (row - tok * a.G)) * D +
-          (lane & 3) * 2;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][i] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
-        qf[k][i + 2] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
-      }
-    }
-    // smallest limit of the tile: its first token's
-    const int lim_min = row_limit(e, l.causal, a.G, rtile * R);
-
-    // ---- this warp's steps: keys [(t * kWarps + warp) * kKeys, + kKeys) of tiles t
-    const int32_t* trow = l.table + static_cast<int64_t>(b) * l.max_pages;
-    const int first = tile_a * kWarps + warp;  // 16-key block of step 0
-    const int blocks = (e.len + kKeys - 1) / kKeys;
-    int steps = tile_e - tile_a;
-    while (steps > 0 && first + (steps - 1) * kWarps >= blocks) --steps;
-    int pages = -1;          // lane i: page of step (issue & ~31) + i
-    uint32_t missing = 0;    // bit s: the page of stage s is out of range
-    auto issue = [&](int st) {
-      if (st < steps) {
-        if ((st & 31) == 0) {
-          const int blk = first + (st + lane) * kWarps;
-          pages = st + lane < steps ? resolve_page(trow, l.max_pages, a.num_pages, a.page_shift,
-                                                   blk * kKeys)
-                                    : 0;
-        }
-        const int page = __shfl_sync(~0u, pages, st & 31);
-        const int key0 = (first + st * kWarps) * kKeys;
-        const int slot = st % S;
-        missing = page < 0 ? missing | (1u << slot) : missing & ~(1u << slot);
-        if (page < 0 && lane == 0) atomicCAS(a.status, 0, kErrIndex);
-        const int64_t base =
-            (((static_cast<int64_t>(max(page, 0)) * a.Hkv + hk) << a.page_shift) +
-             (key0 & ((1 << a.page_shift) - 1))) * D;
-        const uint32_t dst = ring + slot * L::kStage;
-#pragma unroll
-        for (int i = 0; i < kKeys * GR / 32; ++i) {
-          const int r = (i * 32 + lane) / GR, g = (i * 32 + lane) % GR;
-          const bool valid = page >= 0 && key0 + r < e.len;
-          const int64_t off = valid ? base + r * D + g * 8 : 0;
-          cp_async16(dst + step_offset<D>(r, g), a.k_cache + off, valid);
-          cp_async16(dst + L::kHalf + step_offset<D>(r, g), a.v_cache + off, valid);
-        }
-      }
-      cp_commit();
-    };
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-    for (int st = 0; st < S - 1; ++st) issue(st);
-    for (int st = 0; st < steps; ++st) {
-      cp_wait<S - 2>();
-      __syncwarp();
-      const uint32_t kb = ring + (st % S) * L::kStage, vb = kb + L::kHalf;
-      // S = Q K^T: 16 rows x 16 keys
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        const uint32_t r = (lane & 7) + ((lane >> 4) << 3), gh = (lane >> 3) & 1;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t f[4];
-          ldsm4(kb + step_offset<D>(r, 2 * k + gh), f);
-          mma16816(s[0], qf[k], f[0], f[1]);
-          mma16816(s[1], qf[k], f[2], f[3]);
-        }
-      }
-      const int key0 = (first + st * kWarps) * kKeys;
-      if (key0 + kKeys > lim_min || ((missing >> (st % S)) & 1u)) {
-        const bool gone = (missing >> (st % S)) & 1u;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = key0 + n * 8 + (lane & 3) * 2 + (c & 1);
-            if (gone || key >= lim[c >> 1]) s[n][c] = -INFINITY;
-          }
-      }
-      // online softmax; the row maximum is shared by the four lanes of a row, the sum is joined
-      // at the end
-      bool moved = false;
-      float alpha[2];
+      // ---- the rows' queries as A fragments: thread holds rows lane / 4 and lane / 4 + 8
+      const int row0 = piece.r * R, rows = min(R, e.nc * a.G - row0);
+      uint32_t qf[D / 16][4];
+      int lim[2];  // keys below it are visible to the row
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2)) * a.scale_log2;
-        alpha[i] = 1.f;
-        if (mx > m[i]) {
-          alpha[i] = ex2(m[i] - mx);
-          m[i] = mx;
-          moved = true;
-        }
-        const float ref = m[i] == -INFINITY ? 0.f : m[i];
-        float part = 0.f;
+        const int rr = (lane >> 2) + 8 * i, tok = (row0 + rr) / a.G;
+        lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row0 + rr) : e.len;
+        const __nv_bfloat16* qp = a.q + (static_cast<int64_t>(e.start + tok) * a.H + hk * a.G +
+                                         (row0 + rr - tok * a.G)) * D + (lane & 3) * 2;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            // a masked score stays -inf whatever the scale (0 * inf would be NaN)
-            const float x = s[n][2 * i + c];
-            const float p = x == -INFINITY ? 0.f : ex2(fmaf(x, a.scale_log2, -ref));
-            s[n][2 * i + c] = p;
-            part += p;
-          }
-        sum[i] = sum[i] * alpha[i] + part;
-      }
-      if (__any_sync(~0u, moved)) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[n][0] *= alpha[0];
-          o[n][1] *= alpha[0];
-          o[n][2] *= alpha[1];
-          o[n][3] *= alpha[1];
+        for (int k = 0; k < D / 16; ++k) {
+          qf[k][i] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
+          qf[k][i + 2] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
         }
       }
-      // O += P V; P rounded to bf16 (relative 2^-9, as in fa_fwd), its sum is not
-      const uint32_t pf[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
-                              pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
-      {
-        const uint32_t r = lane & 15, gh = lane >> 4;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t f[4];
-          ldsm4_t(vb + step_offset<D>(r, 2 * n + gh), f);
-          mma16816(o[2 * n], pf, f[0], f[1]);
-          mma16816(o[2 * n + 1], pf, f[2], f[3]);
-        }
-      }
-      __syncwarp();  // every lane has read stage st % S before it is filled again
-      issue(st + S - 1);
-    }
-    cp_wait<0>();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
-      sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
-    }
+      const int lim_min = row_limit(e, l.causal, a.G, row0);  // the first row's: the smallest
 
-    // ---- the four warps' parts meet in shared memory (over the ring)
-    __syncthreads();
-    float* mo = reinterpret_cast<float*>(smem);           // [warp][row][kPad]
-    float* mm = mo + kWarps * R * L::kPad;                // [warp][row]
-    float* ml = mm + kWarps * R;
+      float o[D / 8][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = (lane >> 2) + 8 * i;
-      float* dst = mo + (warp * R + rr) * L::kPad + (lane & 3) * 2;
+      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+      for (int st = 0; st < src.steps; ++st) {
+        cp_wait<S - 2>();
+        __syncwarp();
+        const uint32_t kb = ring + (st % S) * L::kStage, vb = kb + L::kHalf;
+        // S = Q K^T: 16 rows x 16 keys
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        {
+          const uint32_t r = (lane & 7) + ((lane >> 4) << 3), gh = (lane >> 3) & 1;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-        *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
-      if ((lane & 3) == 0) {
-        mm[warp * R + rr] = m[i];
-        ml[warp * R + rr] = sum[i];
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t f[4];
+            ldsm4(kb + step_offset<D>(r, 2 * k + gh), f);
+            mma16816(s[0], qf[k], f[0], f[1]);
+            mma16816(s[1], qf[k], f[2], f[3]);
+          }
+        }
+        const int key0 = (src.first + st * kWarps) * kKeys;
+        const bool gone = (missing >> (st % S)) & 1u;
+        if (key0 + kKeys > lim_min || gone) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int key = key0 + n * 8 + (lane & 3) * 2 + (c & 1);
+              if (gone || key >= lim[c >> 1]) s[n][c] = -INFINITY;
+            }
+        }
+        // online softmax; the row maximum is shared by the four lanes of a row, the sum is
+        // joined at the end
+        bool moved = false;
+        float alpha[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float mx =
+              fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2)) * a.scale_log2;
+          alpha[i] = 1.f;
+          if (mx > m[i]) {
+            alpha[i] = ex2(m[i] - mx);
+            m[i] = mx;
+            moved = true;
+          }
+          const float ref = m[i] == -INFINITY ? 0.f : m[i];
+          float part = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // a masked score stays -inf whatever the scale (0 * inf would be NaN)
+              const float x = s[n][2 * i + c];
+              const float p = x == -INFINITY ? 0.f : ex2(fmaf(x, a.scale_log2, -ref));
+              s[n][2 * i + c] = p;
+              part += p;
+            }
+          sum[i] = sum[i] * alpha[i] + part;
+        }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[n][0] *= alpha[0];
+            o[n][1] *= alpha[0];
+            o[n][2] *= alpha[1];
+            o[n][3] *= alpha[1];
+          }
+        }
+        // O += P V; P rounded to bf16 (half a step, 2^-8, as in fa_fwd), its sum is not
+        const uint32_t pf[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
+                                pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
+        {
+          const uint32_t r = lane & 15, gh = lane >> 4;
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t f[4];
+            ldsm4_t(vb + step_offset<D>(r, 2 * n + gh), f);
+            mma16816(o[2 * n], pf, f[0], f[1]);
+            mma16816(o[2 * n + 1], pf, f[2], f[3]);
+          }
+        }
+        __syncwarp();  // every lane has read stage st % S before it is filled again
+        issue_step<D>(a, src, st + S - 1, ring, lane, missing);
       }
-    }
-    __syncthreads();
-    const int tile = row_tile0(e.start, a.G, R, b) + rtile;
-    if (tid == 0 && tile_a == 0)  // this CTA began the segment
-      a.part.spans[static_cast<int64_t>(hk) * a.part.span_tiles + tile] = span_of(sh, piece);
-    {
-      const int rr = tid / 8, c8 = tid % 8;  // 8 threads a row
-      float w[kWarps], mx = -INFINITY, lsum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, mm[i * R + rr]);
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        w[i] = mx == -INFINITY ? 0.f : ex2(mm[i * R + rr] - mx);
-        lsum = fmaf(w[i], ml[i * R + rr], lsum);
+      // every stage has been read: the next piece's copies start here
+      more = walk.next(a, next_piece);
+      if (more) {
+        src = source_of<D>(a, walk, next_piece, warp);
+        for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane, missing);
       }
-      const int row = rtile * R + rr, tok = row / a.G;
-      const int head = hk * a.G + (row - tok * a.G);
-      const int64_t at = static_cast<int64_t>(e.start + tok) * a.H + head;
-      const bool final_out = whole && a.rowbuf == nullptr;
-      const float inv = lsum > 0.f ? 1.f / lsum : (lsum == 0.f ? 0.f : lsum);  // NaN stays NaN
-      float* slot = whole ? a.rowbuf + at * D
-                          : a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (tile_a == 0)) *
-                                               (R * (D + 2)) + rr * D;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
+        sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
+      }
+
+      // ---- the warps' parts meet in shared memory: the upper half's are added to the lower
+      // half's in registers, then four parts are summed row by row
+      auto put = [&](int w) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int rr = (lane >> 2) + 8 * i;
+          float* dst = mo + (w * R + rr) * L::kPad + (lane & 3) * 2;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+            *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+          if ((lane & 3) == 0) {
+            mm[w * R + rr] = m[i];
+            ml[w * R + rr] = sum[i];
+          }
+        }
+      };
+      __syncthreads();  // the last piece's sums have been read
+      if (warp >= kHalfWarps) put(warp - kHalfWarps);
+      __syncthreads();
+      if (warp < kHalfWarps) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int at = warp * R + (lane >> 2) + 8 * i;
+          const float pm = mm[at], top = fmaxf(m[i], pm);
+          const float wa = m[i] == -INFINITY ? 0.f : ex2(m[i] - top);
+          const float wb = pm == -INFINITY ? 0.f : ex2(pm - top);
+          m[i] = top;
+          sum[i] = sum[i] * wa + ml[at] * wb;
+          const float* from = mo + at * L::kPad + (lane & 3) * 2;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            const float2 v = *reinterpret_cast<const float2*>(from + n * 8);
+            o[n][2 * i] = o[n][2 * i] * wa + v.x * wb;
+            o[n][2 * i + 1] = o[n][2 * i + 1] * wa + v.y * wb;
+          }
+        }
+        __syncwarp();  // lanes of a row have read it before it is overwritten
+        put(warp);
+      }
+      __syncthreads();
+      if (tid == 0 && piece.ta == 0)  // this CTA began the segment
+        a.part.spans[static_cast<int64_t>(hk) * a.part.span_tiles + tile] = span_of(sh, piece);
+      const int rr = tid / 16, c16 = tid % 16;  // 16 threads a row
       if (rr < rows) {
+        float w[kHalfWarps], mx = -INFINITY, lsum = 0.f;
 #pragma unroll
-        for (int g = 0; g < D / 32; ++g) {
-          const int col = g * 32 + c8 * 4;
+        for (int i = 0; i < kHalfWarps; ++i) mx = fmaxf(mx, mm[i * R + rr]);
+#pragma unroll
+        for (int i = 0; i < kHalfWarps; ++i) {
+          w[i] = mx == -INFINITY ? 0.f : ex2(mm[i * R + rr] - mx);
+          lsum = fmaf(w[i], ml[i * R + rr], lsum);
+        }
+        const int row = row0 + rr, tok = row / a.G;
+        const int head = hk * a.G + (row - tok * a.G);
+        const int64_t at = static_cast<int64_t>(e.start + tok) * a.H + head;
+        const bool final_out = piece.whole && a.rowbuf == nullptr;
+        const float inv = lsum > 0.f ? 1.f / lsum : (lsum == 0.f ? 0.f : lsum);  // NaN stays
+        float* part = a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (piece.ta == 0)) *
+                                         (R * (D + 2));
+        float* dst = piece.whole ? a.rowbuf + at * D : part + rr * D;
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g) {
+          const int col = g * 64 + c16 * 4;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) {
+          for (int i = 0; i < kHalfWarps; ++i) {
             const float4 v = *reinterpret_cast<const float4*>(mo + (i * R + rr) * L::kPad + col);
             acc.x = fmaf(w[i], v.x, acc.x);
             acc.y = fmaf(w[i], v.y, acc.y);
@@ -301,70 +352,71 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D>::kCtasPerSm)
             acc.w = fmaf(w[i], v.w, acc.w);
           }
           if (final_out)
-            *reinterpret_cast<uint2*>(a.o + at * D + col) =
-                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+            *reinterpret_cast<uint2*>(a.o + at * D + col) = make_uint2(
+                pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
           else
-            *reinterpret_cast<float4*>(slot + col) = acc;
+            *reinterpret_cast<float4*>(dst + col) = acc;
         }
-        if (c8 == 0) {
+        if (c16 == 0) {
           if (final_out) {
             a.lse[static_cast<int64_t>(head) * a.total + e.start + tok] =
                 lsum == 0.f ? -INFINITY : (mx + log2f(lsum)) * kLn2;
-          } else if (whole) {
+          } else if (piece.whole) {
             float* st = a.rowbuf + static_cast<int64_t>(a.total) * a.H * D;
             st[at] = mx;
             st[static_cast<int64_t>(a.total) * a.H + at] = lsum;
           } else {
-            float* st = a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (tile_a == 0)) *
-                                           (R * (D + 2)) + R * D;
-            st[rr] = mx;
-            st[R + rr] = lsum;
+            part[R * D + rr] = mx;
+            part[R * D + R + rr] = lsum;
           }
         }
       }
     }
-    __syncthreads();  // the ring is free again
+    cp_wait<0>();
   }
+  wait_for_last_launch();
 }
 
-// Joins the parts of each output row: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in the order
-// of the keys.  One warp per (token, head); D / 32 elements a lane.
+// token_sequence by a whole warp: 32 offsets a step.
+__device__ __forceinline__ int token_sequence_warp(const int32_t* cu, int B, int t, int lane) {
+  if (cu == nullptr) return t < B ? t : -1;
+  int lo = 0, n = B + 1;  // the last of n offsets from lo that is <= t
+  int found = -1;
+  while (true) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const bool le = lane * step < n && __ldg(cu + i) <= t;
+    const unsigned hit = __ballot_sync(~0u, le);
+    if (hit == 0) return -1;  // before cu[0]
+    found = lo + (31 - __clz(hit)) * step;
+    if (step == 1) break;
+    n = min(step, lo + n - found);
+    lo = found;
+  }
+  return found < B ? found : -1;  // behind cu[B]
+}
+
+// Joins the parts of each output row: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.  One warp per
+// (token, head).  The lanes first take a part's m and l each, which gives every part's weight,
+// and then sum the parts' O in the order of the keys, D / 32 elements a lane, with loads that
+// depend on nothing but the spans.
 template <int D>
 __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
   constexpr int E = D / 32;
+  let_next_launch();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (id >= static_cast<int64_t>(a.total) * a.H) return;
-  const int t = static_cast<int>(id / a.H), head = static_cast<int>(id % a.H);
-  const int hk = head / a.G;
-  const int seq = token_sequence(a.cu, a.B, t);
-  if (seq < 0) return;
-  float m = -INFINITY, lsum = 0.f, o[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) o[i] = 0.f;
-  auto add = [&](const float* po, float pm, float pl) {
-    if (pm == -INFINITY && pl == 0.f) return;  // no visible key
-    float v[E];
-    if constexpr (E == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(po + lane * 4);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(po + lane * 2);
-      v[0] = x.x; v[1] = x.y;
-    }
-    const float top = fmaxf(m, pm);
-    const float wa = m == -INFINITY ? 0.f : ex2(m - top), wb = ex2(pm - top);
-    lsum = lsum * wa + pl * wb;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * wa + v[i] * wb;
-    m = top;
-  };
-  for (int li = 0; li < a.lists; ++li) {
+  const bool inside = id < static_cast<int64_t>(a.total) * a.H;
+  const int t = inside ? static_cast<int>(id / a.H) : 0;
+  const int head = inside ? static_cast<int>(id % a.H) : 0, hk = head / a.G;
+  const int seq = inside ? token_sequence_warp(a.cu, a.B, t, lane) : -1;
+  // where the row's parts are: its span and row tile in each list (these inputs are the call's)
+  int where[2] = {-1, -1}, rr[2] = {0, 0};
+  bool skip = seq < 0;
+  for (int li = 0; li < a.lists && !skip; ++li) {
     const KeyList& l = a.list[li];
-    const PartialLayout& p = a.part[li];
     int b = seq, start, n;
     if (l.group_cu != nullptr) {
-      b = token_sequence(l.group_cu, l.count, seq);
+      b = token_sequence_warp(l.group_cu, l.count, seq, lane);
       if (b < 0) continue;  // a sequence of no group has no prefix
       const int s0 = min(max(__ldg(l.group_cu + b), 0), a.B);
       start = a.cu != nullptr ? min(max(__ldg(a.cu + s0), 0), a.total) : s0;
@@ -373,23 +425,68 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
       token_bounds(a.cu, b, a.total, start, n);
       n = min(n, l.max_q);
     }
-    if (t - start >= n) return;  // beyond max_q: not computed
+    if (t < start || t - start >= n) {
+      skip = true;  // beyond max_q: not computed
+      break;
+    }
     const int row = (t - start) * a.G + (head - hk * a.G);
-    const int tile = row_tile0(start, a.G, p.R, b) + row / p.R, rr = row % p.R;
-    if (tile < 0 || tile >= p.span_tiles) continue;
-    const int2 span = p.spans[static_cast<int64_t>(hk) * p.span_tiles + tile];
+    const int tile = row_tile0(start, a.G, a.part[li].R, b) + row / a.part[li].R;
+    rr[li] = row % a.part[li].R;
+    if (tile >= 0 && tile < a.part[li].span_tiles) where[li] = hk * a.part[li].span_tiles + tile;
+  }
+  wait_for_last_launch();
+  if (skip) return;
+  float m = -INFINITY, lsum = 0.f, o[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) o[i] = 0.f;
+  for (int li = 0; li < a.lists; ++li) {
+    if (where[li] < 0) continue;
+    const PartialLayout& p = a.part[li];
+    const int2 span = p.spans[where[li]];
     // a launch that gave up leaves no span: nothing out of range is read
     if (span.x < 0 || span.y < 1 || span.x + span.y > p.ctas) continue;
-    if (span.y == 1) {
-      if (a.rowbuf[li] == nullptr) return;  // already final
-      const float* st = a.rowbuf[li] + static_cast<int64_t>(a.total) * a.H * D;
-      add(a.rowbuf[li] + id * D, st[id], st[static_cast<int64_t>(a.total) * a.H + id]);
-      continue;
-    }
-    for (int i = 0; i < span.y; ++i) {
-      const float* slot = p.slots + (static_cast<int64_t>(span.x + i) * 2 + (i == 0)) *
-                                        (p.R * (D + 2));
-      add(slot + rr * D, slot[p.R * D + rr], slot[p.R * D + p.R + rr]);
+    const bool one = span.y == 1;
+    if (one && a.rowbuf[li] == nullptr) return;  // already final
+    const int64_t size = static_cast<int64_t>(p.R) * (D + 2);
+    const int64_t rows = static_cast<int64_t>(a.total) * a.H;
+    auto slot = [&](int i) { return p.slots + ((span.x + i) * 2 + (i == 0)) * size; };
+    for (int i0 = 0; i0 < span.y; i0 += 32) {
+      const int count = min(32, span.y - i0);
+      float pm = -INFINITY, pl = 0.f;
+      if (lane < count) {
+        const float* st = one ? a.rowbuf[li] + rows * D + id : slot(i0 + lane) + p.R * D + rr[li];
+        pm = st[0];
+        pl = st[one ? rows : p.R];
+      }
+      float top = pm;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+      top = fmaxf(top, m);
+      const float keep = m == -INFINITY ? 0.f : ex2(m - top);
+      // a part without a visible key has m = -inf and weighs nothing
+      const float w = pm == -INFINITY ? (pl == 0.f ? 0.f : pl) : ex2(pm - top);
+      float s = w * pl;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+      lsum = lsum * keep + s;
+      m = top;
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[i] *= keep;
+#pragma unroll 8
+      for (int i = 0; i < count; ++i) {
+        const float wi = __shfl_sync(~0u, w, i);
+        const float* po = (one ? a.rowbuf[li] + id * D : slot(i0 + i) + rr[li] * D) + lane * E;
+        float v[E];
+        if constexpr (E == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(po);
+          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(po);
+          v[0] = x.x; v[1] = x.y;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(wi, v[e], o[e]);
+      }
     }
   }
   const float inv = lsum > 0.f ? 1.f / lsum : (lsum == 0.f ? 0.f : lsum);
@@ -409,10 +506,8 @@ cudaError_t launch_paged_d(const PagedArgs& a, int64_t max_units, cudaStream_t s
   using L = PagedLayout<D>;
   cudaError_t e = ensure_smem_limit<paged_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t most = 152 * L::kCtasPerSm;
-  const int64_t ctas = max_units < most ? max_units : most;
-  paged_kernel<D><<<static_cast<unsigned>(ctas), kThreads, L::kBytes, s>>>(a);
-  return cudaGetLastError();
+  const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
+  return launch_chained(paged_kernel<D>, static_cast<unsigned>(ctas), kThreads, L::kBytes, s, a);
 }
 
 }  // namespace
@@ -424,9 +519,8 @@ cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStrea
 cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.total) * a.H;
   const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (d == 64) paged_join_kernel<64><<<grid, 128, 0, s>>>(a);
-  else paged_join_kernel<128><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+  return d == 64 ? launch_chained(paged_join_kernel<64>, grid, 128, 0, s, a)
+                 : launch_chained(paged_join_kernel<128>, grid, 128, 0, s, a);
 }
 
 }  // namespace fa

@@ -12,6 +12,41 @@ namespace fa {
 
 enum : int { kErrIndex = 6 };  // FA_ERR_INDEX in the status word
 
+// Launches that may be scheduled while the kernel ahead of them on the stream still runs, so that
+// their launch and their CTAs' start overlap its end.  Nothing is read or written before it has
+// completed: a call's first kernel waits for it at once (begin_launch); a further kernel of the
+// call, whose inputs were complete before the first one began, waits before it ends (the join:
+// before it reads the parts), so that the last one's end is the whole call's.
+template <typename K, typename... Args>
+cudaError_t launch_chained(K kernel, dim3 grid, unsigned threads, uint32_t smem, cudaStream_t s,
+                           const Args&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+#ifdef __CUDACC__
+// The next kernel on the stream may be scheduled.
+__device__ __forceinline__ void let_next_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// The kernel ahead on the stream has completed and its writes are visible.
+__device__ __forceinline__ void wait_for_last_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void begin_launch(bool first) {
+  if (first) wait_for_last_launch();
+  let_next_launch();
+}
+#endif
+
 // Page that holds key `key` of a sequence whose block-table row is `row` (max_pages entries), or
 // -1 when the entry or the page lies outside its range.
 __host__ __device__ inline int resolve_page(const int32_t* row, int max_pages, int num_pages,
@@ -126,6 +161,7 @@ struct PagedArgs {
   KeyList list;
   PartialLayout part;
   float* rowbuf;  // joined lists: [total * H] rows of O, then m, then l; else nullptr
+  bool first;     // the call's first kernel
   int* status;
 };
 
@@ -141,11 +177,10 @@ struct JoinArgs {
 };
 
 constexpr int kPagedRows = 16;           // rows of a tile
-constexpr int kPagedMaxCtas = 152 * 3;   // most CTAs of a launch (and pairs of slots)
+constexpr int kPagedCtas = 152;          // CTAs of a launch (and pairs of slots): one per SM
 constexpr int kPagedUnsplitKeys = 512;   // where no entry has more keys, none is split
 
-constexpr int kPagedMmaRows = 256;       // the same of the tensor-core kernel: two query tiles,
-constexpr int kPagedMmaCtas = 152;       // one CTA per SM
+constexpr int kPagedMmaRows = 256;       // rows of a tile of the tensor-core kernel
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s);
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,

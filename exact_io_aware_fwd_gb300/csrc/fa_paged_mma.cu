@@ -51,15 +51,7 @@ struct MmaLayout {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + 2 * kTile;
   static constexpr uint32_t kV = kK + kStages * kTile;
-  static constexpr uint32_t kBar = kV + kStages * kTile;
-  // q_full, k_full[S], k_empty[S], v_full[S], v_empty[S], s_full[2], p_full[2], o_full[2], done
-  // piece_full[kRing], piece_empty[kRing]
-  static constexpr int kNumBars = 1 + 4 * kStages + 7 + 2 * kRing;
-  static constexpr uint32_t kTmemSlot = kBar + kNumBars * 8;
-  static constexpr uint32_t kAbort = kTmemSlot + 4;
-  static constexpr uint32_t kBad = kAbort + 4;  // [2 S]: pages of a position outside the pool
-  static constexpr uint32_t kPieces = (kBad + 2 * kStages * 4 + 7) & ~7u;
-  static constexpr uint32_t kBytes = kPieces + kRing * sizeof(PieceInfo);
+  static constexpr uint32_t kBytes = kV + kStages * kTile;
   static constexpr uint32_t kColS0 = 0, kColO0 = 256;
   static constexpr uint32_t kTmemCols = 512;
 };
@@ -84,30 +76,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
   uint8_t* sm = smem_raw + pad;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
-  uint64_t* q_full = bars;
-  uint64_t* k_full = bars + 1;
-  uint64_t* k_empty = k_full + S;
-  uint64_t* v_full = k_empty + S;
-  uint64_t* v_empty = v_full + S;
-  uint64_t* s_full = v_empty + S;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* mma_done = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kTmemSlot);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kAbort);
-  volatile uint32_t* bad_pages = reinterpret_cast<volatile uint32_t*>(sm + L::kBad);
-  uint64_t* piece_full = mma_done + 1;
-  uint64_t* piece_empty = piece_full + kRing;
-  PieceInfo* pieces = reinterpret_cast<PieceInfo*>(sm + L::kPieces);
+  // what the roles signal through: static, so that its addresses are constants and take no registers
+  __shared__ uint64_t q_full[1], k_full[S], k_empty[S], v_full[S], v_empty[S];
+  __shared__ uint64_t s_full[2], p_full[2], o_full[2], mma_done[1];
+  __shared__ uint64_t piece_full[kRing], piece_empty[kRing];
+  __shared__ PieceInfo pieces[kRing];
+  __shared__ volatile uint32_t bad_pages[2 * S];  // pages of a position outside the pool
+  __shared__ uint32_t tmem_slot[1];
+  __shared__ volatile int abort_flag[1];
+  __shared__ Share sh;  // for the warp that walks it
   const Ctl ctl{abort_flag, a.status, timeout_ns};
   const uint32_t warp = warp_id(), lane = lane_id();
   if (pad + L::kBytes > smem_bytes) {  // cannot happen with the host's sizing; never proceed
     if (threadIdx.x == 0) atomicCAS(a.status, 0, kErrLayout);
     return;
   }
-  const Share sh = make_share<R, KT, kThreads, kDirectTiles>(a);
-  if (sh.u0 >= sh.u1) return;  // uniform over the CTA
+  begin_launch(a.first);
+  {
+    const Share mine = make_share<R, KT, kThreads, kDirectTiles>(a);
+    if (mine.u0 >= mine.u1) {  // uniform over the CTA
+      wait_for_last_launch();
+      return;
+    }
+    if (threadIdx.x == 0) sh = mine;
+  }
   const KeyList& l = a.list;
 
   if (warp == 0 && lane == 0) {
@@ -142,14 +134,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t sbase = smem_u32(sm);
-  // Registers: the launch gives 384 x 168; warps 0-3 keep 72 and the softmax warps take 216
-  // (128 x 72 + 256 x 216 = 384 x 168), enough for a row's scores and weights without spills.
+  // Registers: the launch gives 384 x 168; warps 0-3 keep 56 and the softmax warps take 224
+  // (128 x 56 + 256 x 224 = 384 x 168), enough for a row's scores and weights: with 168 for all,
+  // or 72 / 216, the spills in the loop cost up to 15% (2 x 512 tokens over 16384 keys).
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 2) {
       // ================= the CTA's pieces
       if (lane == 0) {
-        Walk<R, KT> walk(sh, a);
+        Walk<R, KT> walk(sh);
         const Entry& e = walk.e;
         Piece piece;
         for (int i = 0;; ++i) {
@@ -289,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ================= softmax warpgroups: one per query tile, one thread per row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int t = (warp - 4) >> 2;
     const uint32_t quad = warp & 3;
     const int row = quad * 32 + lane;
@@ -313,27 +306,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n_mine > 0) {
           constexpr int GR = D / 8, RI = 32 / GR;  // granules of a row, rows per step
           const int g = lane % GR;
-          // four loads in flight a round; a compact loop, because code that runs once a piece
-          // comes from a cold instruction cache
+          // lane i works out row i's place; two rounds of loads that are in flight together
+          const int tok = (r0 + row) / a.G;
+          const int place = r0 + row < rows ? (piece.start + tok) * a.H + piece.hk * a.G +
+                                                  (r0 + row - tok * a.G)
+                                            : -1;
 #pragma unroll 1
-          for (int k = 0; k < 32 / RI; k += 4) {
-            uint4 v[4];
+          for (int k0 = 0; k0 < 32; k0 += 16) {
+            uint4 v[16 / RI];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int gr = r0 + quad * 32 + (k + u) * RI + lane / GR;
-              v[u] = make_uint4(0u, 0u, 0u, 0u);
-              if (gr < rows) {
-                const int tok = gr / a.G;
-                v[u] = *reinterpret_cast<const uint4*>(
-                    a.q + (static_cast<int64_t>(piece.start + tok) * a.H + piece.hk * a.G +
-                           (gr - tok * a.G)) * D + g * 8);
-              }
+            for (int k = 0; k < 16 / RI; ++k) {
+              const int at = __shfl_sync(~0u, place, k0 + k * RI + lane / GR);
+              v[k] = make_uint4(0u, 0u, 0u, 0u);
+              if (at >= 0)
+                v[k] = *reinterpret_cast<const uint4*>(a.q + static_cast<int64_t>(at) * D + g * 8);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int k = 0; k < 16 / RI; ++k)
               st_shared_v4(q_tile + (g / 8) * 16384 +
-                               sw128_offset(quad * 32 + (k + u) * RI + lane / GR, g % 8),
-                           v[u].x, v[u].y, v[u].z, v[u].w);
+                               sw128_offset(quad * 32 + k0 + k * RI + lane / GR, g % 8),
+                           v[k].x, v[k].y, v[k].z, v[k].w);
           }
           fence_proxy_async_smem();
         }
@@ -355,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int jg = base + j;
         if (!(ok = mbar_wait_warp(&s_full[t], (seen + j) & 1, ctl))) break;
         tc_fence_after();
+        const uint32_t bad = bad_pages[jg % (2 * S)];
         uint32_t s[128];
         tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -363,7 +356,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(s);
         const int k0 = (ta + j) * KT;
-        const uint32_t bad = bad_pages[jg % (2 * S)];
         const bool masked = k0 + KT > lim_min || bad != 0;
         auto visible = [&](int c) {
           return k0 + c < lim && !((bad >> (c >> a.page_shift)) & 1u);
@@ -395,30 +387,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 cc = make_float2(c2, c2);
         const float2 nm = make_float2(-m_run, -m_run);
         float2 sumv[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t p[64];
-        if (masked) {
+        // weights in two halves of 64 keys, each stored over S as soon as it is packed (32 fewer
+        // registers alive than with all of P)
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const float2 x = fma2(
-                make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cc, nm);
-            const float x0 = visible(2 * c) ? ex2(x.x) : 0.f;
-            const float x1 = visible(2 * c + 1) ? ex2(x.y) : 0.f;
-            p[c] = pack_bf16(x0, x1);
-            sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
-          }
-        } else {
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t p[32];
+          if (masked) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const float2 x = fma2(
-                make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), cc, nm);
-            const float x0 = ex2(x.x), x1 = ex2(x.y);
-            p[c] = pack_bf16(x0, x1);
-            sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
+            for (int c = 0; c < 32; ++c) {
+              const int k = 64 * hf + 2 * c;
+              const float2 x = fma2(
+                  make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm);
+              const float x0 = visible(k) ? ex2(x.x) : 0.f;
+              const float x1 = visible(k + 1) ? ex2(x.y) : 0.f;
+              p[c] = pack_bf16(x0, x1);
+              sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int k = 64 * hf + 2 * c;
+              const float2 x = fma2(
+                  make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm);
+              const float x0 = ex2(x.x), x1 = ex2(x.y);
+              p[c] = pack_bf16(x0, x1);
+              sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
+            }
           }
+          tmem_st32(tS + 32 * hf, p);
         }
         l_run += (sumv[0].x + sumv[1].x) + (sumv[0].y + sumv[1].y);
-        tmem_st32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
-        tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
         if (j > 0 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -526,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
+  wait_for_last_launch();
 }
 
 template <int D>
@@ -535,10 +534,9 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedAr
   const uint32_t smem = L::kBytes + 1024;
   cudaError_t e = ensure_smem_limit<paged_mma_kernel<D>>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = max_units < kPagedMmaCtas ? max_units : kPagedMmaCtas;
-  paged_mma_kernel<D><<<static_cast<unsigned>(ctas), kThreads, smem, s>>>(tk, tv, a, timeout_ns,
-                                                                         smem);
-  return cudaGetLastError();
+  const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
+  return launch_chained(paged_mma_kernel<D>, static_cast<unsigned>(ctas), kThreads, smem, s, tk,
+                        tv, a, timeout_ns, smem);
 }
 
 }  // namespace

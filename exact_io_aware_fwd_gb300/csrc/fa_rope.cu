@@ -138,6 +138,7 @@ __device__ __forceinline__ __nv_bfloat16* row_of(const RowView& v, int b, int n,
 template <int D, bool kInter, bool kPaged>
 __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
   constexpr int L = D / 8;
+  begin_launch(true);
   const int j = threadIdx.x % L;
   const int64_t t64 = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
   if (t64 >= a.tokens) return;
@@ -244,6 +245,7 @@ template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs a) {
   constexpr int L = D / 8, G = kThreads / L;
   constexpr int kR = 2;  // rows in flight: each brings a gradient and an input
+  begin_launch(true);
   const int j = threadIdx.x % L, grp = threadIdx.x / L;
   const unsigned lane = threadIdx.x & 31u;
   const unsigned mask = ((1u << L) - 1u) << (lane & ~(L - 1u));
@@ -344,15 +346,17 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs a) {
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int blocks, int D,
                                                        float* dwq, float* dwk) {
   __shared__ float sm[32][33];
-  const int col = blockIdx.x * 32 + threadIdx.x;
+  begin_launch(true);
+  const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+  const int col = blockIdx.x * 32 + x;
   float sum = 0.f;
-  for (int r = threadIdx.y; r < blocks; r += 32) sum += partial[static_cast<int64_t>(r) * 2 * D + col];
-  sm[threadIdx.y][threadIdx.x] = sum;
+  for (int r = y; r < blocks; r += 32) sum += partial[static_cast<int64_t>(r) * 2 * D + col];
+  sm[y][x] = sum;
   __syncthreads();
-  if (threadIdx.y == 0) {
+  if (y == 0) {
     float s = 0.f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) s += sm[r][threadIdx.x];
+    for (int r = 0; r < 32; ++r) s += sm[r][x];
     (col < D ? dwq[col] : dwk[col - D]) = s;
   }
 }
@@ -389,8 +393,7 @@ cudaError_t fwd_t(RopeArgs a, cudaStream_t s) {
   const int heads = a.H + 2 * a.Hkv;
   a.chunk = head_chunk(a.tokens, heads, G);
   const dim3 grid((a.tokens + G - 1) / G, (heads + a.chunk - 1) / a.chunk);
-  rope_fwd_kernel<D, kInter, kPaged><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_chained(rope_fwd_kernel<D, kInter, kPaged>, grid, kThreads, 0, s, a);
 }
 
 template <int D, bool kInter>
@@ -401,13 +404,12 @@ cudaError_t bwd_t(RopeArgs a, float* dwq, float* dwk, cudaStream_t s) {
   const int64_t items = (static_cast<int64_t>(a.tokens) + G - 1) / G * ((heads + a.chunk - 1) / a.chunk);
   const int blocks = static_cast<int>(items < kRopeBwdBlocks ? items : kRopeBwdBlocks);
   if (blocks > 0) {
-    rope_bwd_kernel<D, kInter><<<blocks, kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_chained(rope_bwd_kernel<D, kInter>, blocks, kThreads, 0, s, a);
     if (e != cudaSuccess) return e;
   }
   if (a.wq == nullptr) return cudaSuccess;
-  rope_dw_kernel<<<2 * D / 32, dim3(32, 32), 0, s>>>(a.partial, blocks, D, dwq, dwk);
-  return cudaGetLastError();
+  return launch_chained(rope_dw_kernel, 2 * D / 32, 1024, 0, s, static_cast<const float*>(a.partial),
+                        blocks, D, dwq, dwk);
 }
 
 }  // namespace

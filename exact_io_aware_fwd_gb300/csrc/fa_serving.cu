@@ -112,9 +112,9 @@ struct PagedWorkspace {
 PagedWorkspace paged_workspace(const int (&count)[2], int lists, int total, int H, int Hkv, int d) {
   PagedWorkspace w{};
   size_t at = 0;
-  size_t slots = static_cast<size_t>(fa::kPagedMaxCtas) * 2 * fa::kPagedRows * (d + 2) * 4;
+  size_t slots = static_cast<size_t>(fa::kPagedCtas) * 2 * fa::kPagedRows * (d + 2) * 4;
   if (static_cast<long long>(total) * (H / Hkv) > kMmaRows) {
-    const size_t mma = static_cast<size_t>(fa::kPagedMmaCtas) * 2 * fa::kPagedMmaRows * (d + 2) * 4;
+    const size_t mma = static_cast<size_t>(fa::kPagedCtas) * 2 * fa::kPagedMmaRows * (d + 2) * 4;
     if (mma > slots) slots = mma;
   }
   for (int i = 0; i < lists; ++i) {
@@ -164,6 +164,20 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   if (static_cast<long long>(cache->num_pages) * Hkv > kMaxInt) return FA_ERR_INVALID_ARG;
   if (lists == 2 && (static_cast<long long>(total) + count[1]) * H + 128LL * count[1] > kMaxInt)
     return FA_ERR_INVALID_ARG;
+  bool mma[2];
+  long long units[2];
+  for (int i = 0; i < lists; ++i) {
+    // query rows of an entry: at most those of max_q tokens; of a group, its share of the batch
+    const long long tokens = i == 0 && max_q < total ? max_q : total;
+    const long long rows = (i == 0 ? tokens : (total + count[i] - 1) / count[i]) * (H / Hkv);
+    mma[i] = rows > kMmaRows;
+    // row tiles over all entries x heads x key tiles: the units of a launch, which fit 32 bits
+    const long long keys = i == 0 ? max_kv : prefix->max_len;
+    units[i] = Hkv * static_cast<long long>(fa::row_tiles_bound(
+                         total, H / Hkv, mma[i] ? fa::kPagedMmaRows : fa::kPagedRows, count[i])) *
+               (keys / 128 + 1);
+    if (units[i] > kMaxInt) return FA_ERR_UNSUPPORTED;
+  }
   const PagedWorkspace w = paged_workspace(count, lists, total, H, Hkv, d);
   if ((st = fa::check_workspace(ws, ws_bytes, w.total)) != FA_OK) return st;
   int* status = nullptr;
@@ -196,7 +210,14 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   j.Hkv = Hkv;
   j.G = a.G;
   j.lists = lists;
-  for (int i = 0; i < lists; ++i) {
+  CUtensorMap tk, tv;
+  if ((mma[0] || (lists > 1 && mma[1])) &&
+      (!make_pool_map(&tk, cache->k_cache, *cache, Hkv, d) ||
+       !make_pool_map(&tv, cache->v_cache, *cache, Hkv, d)))
+    return FA_ERR_CUDA;
+  // the prefixes first (the heavier list), then the sequences' own keys
+  for (int n = 0; n < lists; ++n) {
+    const int i = lists - 1 - n;
     fa::KeyList& l = a.list;
     l.count = count[i];
     l.lens = i == 0 ? cache->kv_lens : prefix->lens;
@@ -207,27 +228,17 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     l.group_cu = i == 0 ? nullptr : prefix->group_cu;
     l.causal = i == 0 && causal ? 1 : 0;
     a.rowbuf = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
-    // query rows of an entry: at most those of max_q tokens; of a group, its share of the batch
-    const long long tokens = i == 0 && max_q < total ? max_q : total;
-    const long long rows = (i == 0 ? tokens : (total + l.count - 1) / l.count) * a.G;
-    const bool mma = rows > kMmaRows;
-    a.part.R = mma ? fa::kPagedMmaRows : fa::kPagedRows;
-    a.part.ctas = mma ? fa::kPagedMmaCtas : fa::kPagedMaxCtas;
+    a.part.R = mma[i] ? fa::kPagedMmaRows : fa::kPagedRows;
+    a.part.ctas = fa::kPagedCtas;
     a.part.span_tiles = fa::row_tiles_bound(total, a.G, a.part.R, l.count);
     a.part.spans = reinterpret_cast<int2*>(base + w.spans[i]);
     a.part.slots = reinterpret_cast<float*>(base + w.slots[i]);
-    const long long units = static_cast<long long>(l.count) * Hkv *
-                            ((tokens * a.G + a.part.R - 1) / a.part.R) *
-                            (l.max_len / (mma ? 128 : 64) + 1);
+    a.first = n == 0;
     cudaError_t e;
-    if (mma) {
-      CUtensorMap tk, tv;
-      if (!make_pool_map(&tk, cache->k_cache, *cache, Hkv, d) ||
-          !make_pool_map(&tv, cache->v_cache, *cache, Hkv, d))
-        return FA_ERR_CUDA;
-      e = fa::launch_paged_mma(d, tk, tv, a, units, fa::wait_timeout_ns(), s);
+    if (mma[i]) {
+      e = fa::launch_paged_mma(d, tk, tv, a, units[i], fa::wait_timeout_ns(), s);
     } else {
-      e = fa::launch_paged(d, a, units, s);
+      e = fa::launch_paged(d, a, units[i], s);
     }
     if ((st = status_of(e)) != FA_OK) return st;
     j.list[i] = l;

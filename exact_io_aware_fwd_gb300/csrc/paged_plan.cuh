@@ -2,11 +2,12 @@
 //
 // The work of entry b is one segment per (key/value head, row tile), each of as many key tiles
 // (KT keys) as the tile's last row sees.  Laid end to end, the segments' key tiles are units
-// 0 .. W - 1, and CTA c takes units [c W / C, (c + 1) W / C): equal shares whatever the lengths,
-// at most two unfinished segments per CTA, so the partial results take 2 C slots however long
-// the cache is.  When no segment has more than kDirectTiles key tiles, splitting would cost more
-// than it gives (a join kernel has to read the parts back): then a unit is a whole segment.
-// Lengths live on the device, so every CTA works this out for itself from one pass over them.
+// 0 .. W - 1, and CTA c of C takes units [c W / C, (c + 1) W / C): equal shares whatever the
+// lengths, at most two unfinished segments per CTA, so the partial results take 2 C
+// slots however long the cache is.  When no segment has more than kDirectTiles key tiles,
+// splitting would cost more than it gives (a join kernel has to read the parts back): then a
+// unit is a whole segment.  Lengths live on the device, so every CTA works this out for itself
+// from one pass over them.  Units fit 32 bits (the host refuses more).
 //
 // A CTA takes the pieces of its share last to first.  Then the CTAs of one head's row tiles all
 // start at key tile 0 of some row tile and walk the keys abreast, and so do they later in the
@@ -18,17 +19,11 @@
 
 namespace fa {
 
-// Quotient of non-negative numbers; most fit 32 bits, where the division is several times shorter.
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
-}
-
 struct Entry {
   int start, n, nc;  // first token, new tokens, and how many of them are computed
   int len;           // keys (clamped)
   int rt;            // row tiles (0: no tokens)
-  int64_t tiles;     // key tiles of all its row tiles, for one key/value head
+  int tiles;         // key tiles of all its row tiles, for one key/value head
 };
 
 // Keys that row `row` (new token x group member) of an entry sees.
@@ -64,141 +59,143 @@ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, 
   e.nc = min(e.n, l.max_q);
   if (report && (e.len != len || e.nc != e.n)) atomicCAS(a.status, 0, kErrIndex);
   e.rt = (e.nc * a.G + R - 1) / R;
-  if (l.causal) {
+  if (l.causal && e.n > 1) {
     e.tiles = 0;
     for (int r = 0; r < e.rt; ++r) e.tiles += tiles_of<R, KT>(e, 1, a.G, r);
   } else {
-    e.tiles = static_cast<int64_t>(e.rt) * max(1, (e.len + KT - 1) / KT);
+    e.tiles = e.rt * max(1, (e.len + KT - 1) / KT);
   }
   return e;
 }
 
+// Splitting W units over C CTAs: CTA c takes [c W / C, (c + 1) W / C).  (The longer shares are
+// spread over the CTAs on purpose: with all of them first, the CTAs of a tensor-core launch run in
+// lockstep and their bursts of copies slow the MMAs: 249 instead of 226 us for 2 x 512 tokens over
+// 16384 keys.)
+__host__ __device__ inline int share_begin(int W, int C, int c) {
+  return static_cast<int>(static_cast<int64_t>(c) * W / C);
+}
+// CTA that owns unit u: the largest c with c W / C <= u.
+__host__ __device__ inline int share_owner(int W, int C, int u) {
+  return static_cast<int>(((static_cast<int64_t>(u) + 1) * C - 1) / W);
+}
+
 struct Share {
-  int64_t W, u0, u1;  // all units, and this CTA's
-  int C;              // CTAs that have units
-  bool direct;        // a unit is a whole segment
-  int b;              // entry of unit u1 - 1
-  int64_t off;        // its units before u1
+  int W, u0, u1;  // all units, and this CTA's
+  int C;          // CTAs that have units
+  bool direct;    // a unit is a whole segment
+  int b;          // entry of unit u1 - 1
+  int off;        // its units before u1
+  Entry e;        // that entry
 };
 
 // Called by all kThreads threads of the CTA.
 template <int R, int KT, int kThreads, int kDirectTiles>
 __device__ Share make_share(const PagedArgs& a) {
   constexpr int kWarps = kThreads / 32;
-  __shared__ long long red[kWarps][2];
-  __shared__ int red_max[kWarps];
-  __shared__ long long at[2];
+  __shared__ int red[3][kWarps];
+  __shared__ int scan[kWarps];
+  __shared__ int at[2];
+  __shared__ Entry at_entry;
   const KeyList& l = a.list;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long seg = 0, til = 0;         // over all entries
-  long long my_seg = 0, my_til = 0;   // of entry tid
-  int mx = 0;
+  int seg = 0, til = 0, mx = 0;   // over all entries
+  Entry mine{};                   // entry tid, then b0 + tid
   for (int b = tid; b < l.count; b += kThreads) {
     const Entry e = entry_of<R, KT>(l, a, b, blockIdx.x == 0);
-    const long long s = static_cast<long long>(e.rt) * a.Hkv, t = e.tiles * a.Hkv;
-    if (b == tid) {
-      my_seg = s;
-      my_til = t;
-    }
-    seg += s;
-    til += t;
+    if (b == tid) mine = e;
+    seg += e.rt * a.Hkv;
+    til += e.tiles * a.Hkv;
     if (e.rt > 0) mx = max(mx, tiles_of<R, KT>(e, l.causal, a.G, e.rt - 1));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    seg += __shfl_xor_sync(~0u, seg, o);
-    til += __shfl_xor_sync(~0u, til, o);
-    mx = max(mx, __shfl_xor_sync(~0u, mx, o));
-  }
+  seg = __reduce_add_sync(~0u, seg);
+  til = __reduce_add_sync(~0u, til);
+  mx = __reduce_max_sync(~0u, mx);
   if (lane == 0) {
-    red[warp][0] = seg;
-    red[warp][1] = til;
-    red_max[warp] = mx;
+    red[0][warp] = seg;
+    red[1][warp] = til;
+    red[2][warp] = mx;
   }
   __syncthreads();
-  seg = til = 0;
-  mx = 0;
+  seg = til = mx = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    seg += red[w][0];
-    til += red[w][1];
-    mx = max(mx, red_max[w]);
+    seg += red[0][w];
+    til += red[1][w];
+    mx = max(mx, red[2][w]);
   }
   Share sh;
   sh.direct = mx <= kDirectTiles;
   sh.W = sh.direct ? seg : til;
   // a share of fewer than kDirectTiles / 2 tiles is not worth a slot
-  const long long most = sh.direct ? sh.W : (sh.W + kDirectTiles / 2 - 1) / (kDirectTiles / 2);
-  sh.C = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  const int most = sh.direct ? sh.W : (sh.W + kDirectTiles / 2 - 1) / (kDirectTiles / 2);
+  sh.C = min(most, static_cast<int>(gridDim.x));
   const int c = blockIdx.x;
-  sh.u0 = c < sh.C ? quotient(c * sh.W, sh.C) : 0;
-  sh.u1 = c < sh.C ? quotient((c + 1) * sh.W, sh.C) : 0;
+  sh.u0 = c < sh.C ? share_begin(sh.W, sh.C, c) : 0;
+  sh.u1 = c < sh.C ? share_begin(sh.W, sh.C, c + 1) : 0;
   sh.b = 0;
   sh.off = 0;
   if (sh.u0 >= sh.u1) return sh;  // uniform over the CTA
   // entry of unit u1 - 1: scan the entries kThreads at a time
-  const int64_t last = sh.u1 - 1;
-  long long before = 0;
+  const int last = sh.u1 - 1;
+  int before = 0;
   for (int b0 = 0; b0 < l.count; b0 += kThreads) {
     const int b = b0 + tid;
-    long long units = sh.direct ? my_seg : my_til;
     if (b0 > 0) {
-      units = 0;
-      if (b < l.count) {
-        const Entry e = entry_of<R, KT>(l, a, b, false);
-        units = (sh.direct ? e.rt : e.tiles) * a.Hkv;
-      }
+      mine = Entry{};
+      if (b < l.count) mine = entry_of<R, KT>(l, a, b, false);
+      __syncthreads();  // the readers of scan are done
     }
-    long long incl = units;
+    const int units = (sh.direct ? mine.rt : mine.tiles) * a.Hkv;
+    int incl = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(~0u, incl, o);
+      const int v = __shfl_up_sync(~0u, incl, o);
       if (lane >= o) incl += v;
     }
-    __syncthreads();  // earlier readers of red are done
-    if (lane == 31) red[warp][0] = incl;
+    if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    long long pre = before, chunk = before;
+    int chunk = before;
+    incl += before;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) pre += red[w][0];
-      chunk += red[w][0];
+      if (w < warp) incl += scan[w];
+      chunk += scan[w];
     }
-    incl += pre;
     if (units > 0 && incl - units <= last && last < incl) {
       at[0] = b;
       at[1] = sh.u1 - (incl - units);
+      at_entry = mine;
     }
     before = chunk;
     if (last < before) break;  // uniform
   }
   __syncthreads();
-  sh.b = static_cast<int>(at[0]);
+  sh.b = at[0];
   sh.off = at[1];
+  sh.e = at_entry;
   return sh;
 }
 
 // A CTA's piece of one segment: key tiles [ta, te) of row tile r for key/value head hk.
 struct Piece {
   int hk, r, ta, te;
-  bool whole;    // no other CTA works on the segment
-  int64_t unit;  // the segment's first unit
-  int tiles;     // its key tiles
+  bool whole;  // no other CTA works on the segment
+  int unit;    // the segment's first unit
+  int tiles;   // its key tiles
 };
 
 // Walks the pieces of a CTA's share, last to first; e is the entry b of the current piece.
 template <int R, int KT>
 struct Walk {
-  int64_t u0, u1;   // what is left of the share
-  int64_t within;   // units of entry b before u1
+  int u0, u1;   // what is left of the share
+  int within;   // units of entry b before u1
   int b;
   bool direct;
   Entry e;
 
-  __device__ Walk(const Share& sh, const PagedArgs& a)
-      : u0(sh.u0), u1(sh.u1), within(sh.off), b(sh.b), direct(sh.direct) {
-    e = entry_of<R, KT>(a.list, a, b, false);
-  }
+  __device__ explicit Walk(const Share& sh)
+      : u0(sh.u0), u1(sh.u1), within(sh.off), b(sh.b), direct(sh.direct), e(sh.e) {}
   __device__ bool next(const PagedArgs& a, Piece& p) {
     if (u0 >= u1) return false;
     while (within <= 0) {          // the entry before with tokens
@@ -206,11 +203,11 @@ struct Walk {
       e = entry_of<R, KT>(a.list, a, b, false);
       within = (direct ? e.rt : e.tiles) * a.Hkv;
     }
-    const int64_t per_head = direct ? e.rt : e.tiles, x = within - 1;
-    p.hk = static_cast<int>(quotient(x, per_head));
-    int64_t rem = x - p.hk * per_head;
+    const int per_head = direct ? e.rt : e.tiles, x = within - 1;
+    p.hk = x / per_head;
+    int rem = x - p.hk * per_head;
     if (direct) {
-      p.r = static_cast<int>(rem);
+      p.r = rem;
       p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
       p.ta = 0;
       p.te = p.tiles;
@@ -226,9 +223,9 @@ struct Walk {
       ++p.r;
       p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
     }
-    p.te = static_cast<int>(rem) + 1;
+    p.te = rem + 1;
     p.unit = u1 - p.te;
-    const int take = static_cast<int>(min(static_cast<int64_t>(p.te), u1 - u0));
+    const int take = min(p.te, u1 - u0);
     p.ta = p.te - take;
     p.whole = take == p.tiles;
     u1 -= take;
@@ -237,14 +234,11 @@ struct Walk {
   }
 };
 
-// CTA that owns unit u: the largest c with floor(c W / C) <= u.
-__device__ __forceinline__ int owner_of(const Share& sh, int64_t u) {
-  return static_cast<int>(quotient((u + 1) * sh.C - 1, sh.W));
-}
 // (first CTA, number of CTAs) of the segment that this CTA begins.
 __device__ __forceinline__ int2 span_of(const Share& sh, const Piece& p) {
   const int first = blockIdx.x;
-  return make_int2(first, p.whole ? 1 : owner_of(sh, p.unit + p.tiles - 1) - first + 1);
+  const int last = p.whole ? first : share_owner(sh.W, sh.C, p.unit + p.tiles - 1);
+  return make_int2(first, last - first + 1);
 }
 
 }  // namespace fa

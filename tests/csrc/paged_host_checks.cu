@@ -4,6 +4,7 @@
 #include <vector>
 
 #include "fa_paged.h"
+#include "paged_plan.cuh"
 
 static int failures = 0;
 #define CHECK(c) do { if (!(c)) { ++failures; std::printf("line %d: %s\n", __LINE__, #c); } } while (0)
@@ -63,6 +64,20 @@ int main() {
           CHECK(used <= bound);
         }
       }
+  // shares of C CTAs: contiguous, as equal as can be, and the owner of a unit is the CTA whose
+  // share holds it
+  const int sizes[][2] = {{7, 1}, {16, 16}, {16, 152}, {152, 152}, {153, 152}, {303, 152},
+                          {65536, 152}, {12345, 77}, {0x7fffffff, 152}, {0x7fffffff, 1}};
+  for (const auto& wc : sizes) {
+    const int W = wc[0], C = wc[1] < W ? wc[1] : W;
+    CHECK(fa::share_begin(W, C, 0) == 0 && fa::share_begin(W, C, C) == W);
+    for (int k = 0; k < C; ++k) {
+      const int u0 = fa::share_begin(W, C, k), u1 = fa::share_begin(W, C, k + 1);
+      CHECK(u1 - u0 == W / C || u1 - u0 == W / C + 1);
+      CHECK(fa::share_owner(W, C, u0) == k && fa::share_owner(W, C, u1 - 1) == k);
+      CHECK(fa::share_owner(W, C, u0 + (u1 - u0) / 2) == k);
+    }
+  }
   if (failures == 0) std::printf("ok\n");
   return failures != 0;
 }

@@ -27,25 +27,11 @@ def lib():
 
 def test_index_functions_on_the_host(tmp_path):
     exe = tmp_path / "checks"
-    subprocess.run([build_lib._nvcc(), "-O1", "-std=c++17", "-I", build_lib.CSRC,
+    subprocess.run([build_lib._nvcc(), *build_lib.ARCH, "-O1", "-std=c++17", "-I", build_lib.CSRC,
                     os.path.join(HERE, "csrc", "paged_host_checks.cu"), "-o", str(exe)],
                    check=True, capture_output=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
-
-
-@pytest.mark.parametrize("C,W", [(1, 7), (304, 16), (304, 304), (304, 305), (304, 65536), (7, 50),
-                                 (456, 12345), (152, 3 * 10 ** 10)])
-def test_unit_owners(C, W):
-    """CTA c takes units [c W / C, (c + 1) W / C); the owner formula finds c for any unit."""
-    C = min(C, W)
-    rng = np.random.default_rng(C + W)
-    edges = [c * W // C for c in range(C + 1)]
-    units = {0, W - 1} | {e for e in edges if e < W} | {e - 1 for e in edges if e > 0}
-    units |= {int(u) for u in rng.integers(0, W, 200)}
-    for u in units:
-        c = ((u + 1) * C - 1) // W
-        assert edges[c] <= u < edges[c + 1]
 
 
 # ------------------------------------------------------------------------------- C ABI refusals
@@ -194,6 +180,8 @@ def test_paged_attention_refusals(lib):
     assert need > 0 and call(nbytes=need - 1) == fa.FA_ERR_WORKSPACE
     assert call(total=0, q=None, o=None, lse=None, ws=None) == fa.FA_OK
     assert call(total=1 << 29, H=32, Hkv=8) == bad  # (token, head) rows past 32 bits
+    assert call(total=1 << 24, B=64, H=64, Hkv=8, max_kv=1 << 20, nbytes=1 << 50) == fa.FA_ERR_UNSUPPORTED
+    assert call(_kv(num_pages=1 << 30)) == bad  # pages x heads past 32 bits
     assert lib.fa_fwd_paged_workspace_size(0, 5, 4, 2, 64) == 0
     assert lib.fa_fwd_paged_workspace_size(2, 5, 4, 3, 64) == 0
 
