@@ -2,14 +2,15 @@
 //
 // O = softmax(scale q K^T) V for the queries of one sequence that share a key/value head (group
 // members x new tokens), 16 rows at a time: each K, V element is used by at most 16 rows, so the
-// kernel is bound by reading the cache once.  A warp takes 16 keys of every 128-key tile and is a
-// pipeline of its own: it copies its keys' rows with cp.async into a private ring of
-// shared-memory stages (keys past the length become zeros, whatever the page holds there), and
-// computes S (m16n8k16), the online softmax and O += P V from the ring, with no barrier between
-// warps until a piece's end, where the eight partial (m, l, O) are merged through shared memory.
-// The copies of the next piece's first steps are issued before that, so memory does not wait for
-// the merge.  mma.sync is enough here: 16 rows x 4 flops per element and 2 bytes is 32 flops a
-// byte, a few percent of the tensor pipe at full memory bandwidth.
+// kernel is bound by reading the cache once.  Every warp is a worker of its own (paged_plan.cuh):
+// it takes an equal share of all keys, copies 16 keys a step with cp.async into a private ring of
+// shared-memory stages (keys past the length become zeros, whatever the page holds there),
+// computes S (m16n8k16), the online softmax and O += P V from the ring, and writes its result or
+// its part of one straight from registers.  No barrier after the start: warps never wait for each
+// other, and a warp's ring goes on with the next piece while the last one is written.  (With 8
+// warps on one segment and a merge in shared memory at each piece's end, 1024 segments of about
+// 512 keys took 81 us instead of the copies' 40.)  mma.sync is enough here: 16 rows x 4 flops per
+// element and 2 bytes is 32 flops a byte, a few percent of the tensor pipe at full bandwidth.
 #include "fa_internal.h"
 #include "fa_paged.h"
 #include "paged_plan.cuh"
@@ -19,26 +20,20 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kHalfWarps = kWarps / 2;
+constexpr int kWarps = kPagedWarps, kThreads = 32 * kWarps;
 constexpr int R = kPagedRows;
-constexpr int kKeys = 16;             // keys of a warp's step
-constexpr int KT = kKeys * kWarps;    // keys of a tile
-constexpr int kDirectTiles = kPagedUnsplitKeys / KT;  // one CTA for a whole segment
+constexpr int KT = 16;                // keys of a step, and of a tile
+constexpr int kDirectTiles = kPagedUnsplitKeys / KT;  // one warp for a whole segment
 constexpr float kLn2 = 0.693147180559945309f;
 
-// One CTA per SM: a ring of 8 warps x stages (192 KB: with all but one stage of each in flight,
-// 128 to 160 KB cover the latency of memory at full rate), and the merge buffer of half the warps.
+// One CTA per SM: 8 warps x stages of 16 keys (192 KB: with all but one stage of each in flight,
+// 128 to 160 KB cover the latency of memory at full rate).
 template <int D>
 struct PagedLayout {
   static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr uint32_t kHalf = kKeys * D * 2u;                // K or V of a step
+  static constexpr uint32_t kHalf = KT * D * 2u;                // K or V of a step
   static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr uint32_t kRing = kWarps * kStages * kStage;
-  static constexpr int kPad = D + 4;                               // floats per merged row
-  static constexpr uint32_t kMerge = kHalfWarps * R * (kPad + 2) * 4u;
-  static constexpr uint32_t kBytes = kRing + kMerge;
+  static constexpr uint32_t kBytes = kWarps * kStages * kStage;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -79,53 +74,47 @@ __device__ __forceinline__ uint32_t step_offset(uint32_t r, uint32_t g) {
   return r * (D * 2u) + ((g ^ (r & 7u)) << 4);  // the xor stays within the granule's 128 bytes
 }
 
-// What a warp needs to copy its steps of a piece.
+// What a warp needs to copy the steps of a piece.
 struct Source {
   const int32_t* trow;  // block-table row
   int hk, len;          // key/value head, keys
-  int first, steps;     // 16-key block of step 0 (the next is kWarps further), number of steps
+  int first, steps;     // key tile of step 0, number of steps
   int pages;            // lane i: page of step (issue & ~31) + i
 };
 
-template <int D>
 __device__ __forceinline__ Source source_of(const PagedArgs& a, const Walk<R, KT>& w,
-                                            const Piece& p, int warp) {
+                                            const Piece& p) {
   Source s;
   s.trow = a.list.table + static_cast<int64_t>(w.b) * a.list.max_pages;
   s.hk = p.hk;
   s.len = w.e.len;
-  s.first = p.ta * kWarps + warp;
-  // steps with a key below the length
-  const int blocks = (w.e.len + kKeys - 1) / kKeys;
-  s.steps = min(p.te - p.ta, max(0, (blocks - s.first + kWarps - 1) / kWarps));
+  s.first = p.ta;
+  s.steps = min(p.te, (w.e.len + KT - 1) / KT) - p.ta;  // none for an entry without keys
   s.pages = -1;
   return s;
 }
 
-// Copies step st into its stage; every call commits a group, empty past the last step.  Bit i of
-// `missing`: the page of stage i is out of range.
+// Copies step st into its stage (zeros for keys past the length and, reported, for a page outside
+// the pool); every call commits a group, empty past the last step.
 template <int D>
 __device__ __forceinline__ void issue_step(const PagedArgs& a, Source& s, int st, uint32_t ring,
-                                           int lane, uint32_t& missing) {
+                                           int lane) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages, GR = D / 8;  // granules of a row
   if (st < s.steps) {
-    if ((st & 31) == 0) {
-      const int blk = s.first + (st + lane) * kWarps;
+    if ((st & 31) == 0)
       s.pages = st + lane < s.steps ? resolve_page(s.trow, a.list.max_pages, a.num_pages,
-                                                   a.page_shift, blk * kKeys)
+                                                   a.page_shift, (s.first + st + lane) * KT)
                                     : 0;
-    }
     const int page = __shfl_sync(~0u, s.pages, st & 31);
-    const int key0 = (s.first + st * kWarps) * kKeys;
+    const int key0 = (s.first + st) * KT;
     const int slot = st % S;
-    missing = page < 0 ? missing | (1u << slot) : missing & ~(1u << slot);
     if (page < 0 && lane == 0) atomicCAS(a.status, 0, kErrIndex);
     const int64_t base = (((static_cast<int64_t>(max(page, 0)) * a.Hkv + s.hk) << a.page_shift) +
                           (key0 & ((1 << a.page_shift) - 1))) * D;
     const uint32_t dst = ring + slot * L::kStage;
 #pragma unroll
-    for (int i = 0; i < kKeys * GR / 32; ++i) {
+    for (int i = 0; i < KT * GR / 32; ++i) {
       const int r = (i * 32 + lane) / GR, g = (i * 32 + lane) % GR;
       const bool valid = page >= 0 && key0 + r < s.len;
       const int64_t off = valid ? base + r * D + g * 8 : 0;
@@ -141,38 +130,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ Share shares[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   begin_launch(a.first);
-  const Share sh = make_share<R, KT, kThreads, kDirectTiles>(a);
+  make_shares<R, KT, kThreads, kDirectTiles, kWarps>(a, shares);
   const KeyList& l = a.list;
+  const Share& sh = shares[warp];
   const uint32_t ring = smem_u32(smem) + warp * (S * L::kStage);
-  float* mo = reinterpret_cast<float*>(smem + L::kRing);  // [half the warps][row][kPad]
-  float* mm = mo + kHalfWarps * R * L::kPad;              // [..][row]
-  float* ml = mm + kHalfWarps * R;
 
   if (sh.u0 < sh.u1) {
     Walk<R, KT> walk(sh);
     Piece next_piece;
     bool more = walk.next(a, next_piece);
-    Source src = source_of<D>(a, walk, next_piece, warp);
-    uint32_t missing = 0;
-    for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane, missing);
+    Source src = source_of(a, walk, next_piece);
+    for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane);
     while (more) {
       const Piece piece = next_piece;
       const Entry e = walk.e;
       const int tile = row_tile0(e.start, a.G, R, walk.b) + piece.r;
       const int hk = piece.hk;
+      if (lane == 0 && piece.ta == 0)  // this worker begins the segment
+        a.part.spans[static_cast<int64_t>(hk) * a.part.span_tiles + tile] = span_of(sh, piece);
 
       // ---- the rows' queries as A fragments: thread holds rows lane / 4 and lane / 4 + 8
       const int row0 = piece.r * R, rows = min(R, e.nc * a.G - row0);
       uint32_t qf[D / 16][4];
       int lim[2];  // keys below it are visible to the row
+      int at[2];   // (token, head) of the row
+      int head[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int rr = (lane >> 2) + 8 * i, tok = (row0 + rr) / a.G;
         lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row0 + rr) : e.len;
-        const __nv_bfloat16* qp = a.q + (static_cast<int64_t>(e.start + tok) * a.H + hk * a.G +
-                                         (row0 + rr - tok * a.G)) * D + (lane & 3) * 2;
+        head[i] = hk * a.G + (row0 + rr - tok * a.G);
+        at[i] = (e.start + tok) * a.H + head[i];
+        const __nv_bfloat16* qp = a.q + static_cast<int64_t>(at[i]) * D + (lane & 3) * 2;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           qf[k][i] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
@@ -201,15 +193,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
             mma16816(s[1], qf[k], f[2], f[3]);
           }
         }
-        const int key0 = (src.first + st * kWarps) * kKeys;
-        const bool gone = (missing >> (st % S)) & 1u;
-        if (key0 + kKeys > lim_min || gone) {
+        const int key0 = (src.first + st) * KT;
+        if (key0 + KT > lim_min) {
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int key = key0 + n * 8 + (lane & 3) * 2 + (c & 1);
-              if (gone || key >= lim[c >> 1]) s[n][c] = -INFINITY;
+              if (key >= lim[c >> 1]) s[n][c] = -INFINITY;
             }
         }
         // online softmax; the row maximum is shared by the four lanes of a row, the sum is
@@ -234,9 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              // a masked score stays -inf whatever the scale (0 * inf would be NaN)
-              const float x = s[n][2 * i + c];
-              const float p = x == -INFINITY ? 0.f : ex2(fmaf(x, a.scale_log2, -ref));
+              // the scale is never 0, so a hidden score stays -inf and weighs 0
+              const float p = ex2(fmaf(s[n][2 * i + c], a.scale_log2, -ref));
               s[n][2 * i + c] = p;
               part += p;
             }
@@ -265,109 +255,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
           }
         }
         __syncwarp();  // every lane has read stage st % S before it is filled again
-        issue_step<D>(a, src, st + S - 1, ring, lane, missing);
+        issue_step<D>(a, src, st + S - 1, ring, lane);
       }
       // every stage has been read: the next piece's copies start here
       more = walk.next(a, next_piece);
       if (more) {
-        src = source_of<D>(a, walk, next_piece, warp);
-        for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane, missing);
+        src = source_of(a, walk, next_piece);
+        for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane);
       }
+
+      // ---- the rows' results, or this worker's part of them
+      const bool final_out = piece.whole && a.rowbuf == nullptr;
+      float* part = a.part.slots + (static_cast<int64_t>(sh.worker) * 2 + (piece.ta == 0)) *
+                                       (R * (D + 2));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
         sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
-      }
-
-      // ---- the warps' parts meet in shared memory: the upper half's are added to the lower
-      // half's in registers, then four parts are summed row by row
-      auto put = [&](int w) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int rr = (lane >> 2) + 8 * i;
-          float* dst = mo + (w * R + rr) * L::kPad + (lane & 3) * 2;
+        const int rr = (lane >> 2) + 8 * i;
+        if (rr >= rows) continue;
+        const float inv = sum[i] > 0.f ? 1.f / sum[i] : (sum[i] == 0.f ? 0.f : sum[i]);  // NaN stays
+        if (final_out) {
+          uint32_t* dst =
+              reinterpret_cast<uint32_t*>(a.o + static_cast<int64_t>(at[i]) * D) + (lane & 3);
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2*>(dst + n * 8) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
-          if ((lane & 3) == 0) {
-            mm[w * R + rr] = m[i];
-            ml[w * R + rr] = sum[i];
-          }
+            dst[n * 4] = pack_bf16(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+        } else {
+          float* row = piece.whole ? a.rowbuf + static_cast<int64_t>(at[i]) * D : part + rr * D;
+          float2* dst = reinterpret_cast<float2*>(row) + (lane & 3);
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) dst[n * 4] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
         }
-      };
-      __syncthreads();  // the last piece's sums have been read
-      if (warp >= kHalfWarps) put(warp - kHalfWarps);
-      __syncthreads();
-      if (warp < kHalfWarps) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = warp * R + (lane >> 2) + 8 * i;
-          const float pm = mm[at], top = fmaxf(m[i], pm);
-          const float wa = m[i] == -INFINITY ? 0.f : ex2(m[i] - top);
-          const float wb = pm == -INFINITY ? 0.f : ex2(pm - top);
-          m[i] = top;
-          sum[i] = sum[i] * wa + ml[at] * wb;
-          const float* from = mo + at * L::kPad + (lane & 3) * 2;
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            const float2 v = *reinterpret_cast<const float2*>(from + n * 8);
-            o[n][2 * i] = o[n][2 * i] * wa + v.x * wb;
-            o[n][2 * i + 1] = o[n][2 * i + 1] * wa + v.y * wb;
-          }
-        }
-        __syncwarp();  // lanes of a row have read it before it is overwritten
-        put(warp);
-      }
-      __syncthreads();
-      if (tid == 0 && piece.ta == 0)  // this CTA began the segment
-        a.part.spans[static_cast<int64_t>(hk) * a.part.span_tiles + tile] = span_of(sh, piece);
-      const int rr = tid / 16, c16 = tid % 16;  // 16 threads a row
-      if (rr < rows) {
-        float w[kHalfWarps], mx = -INFINITY, lsum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kHalfWarps; ++i) mx = fmaxf(mx, mm[i * R + rr]);
-#pragma unroll
-        for (int i = 0; i < kHalfWarps; ++i) {
-          w[i] = mx == -INFINITY ? 0.f : ex2(mm[i * R + rr] - mx);
-          lsum = fmaf(w[i], ml[i * R + rr], lsum);
-        }
-        const int row = row0 + rr, tok = row / a.G;
-        const int head = hk * a.G + (row - tok * a.G);
-        const int64_t at = static_cast<int64_t>(e.start + tok) * a.H + head;
-        const bool final_out = piece.whole && a.rowbuf == nullptr;
-        const float inv = lsum > 0.f ? 1.f / lsum : (lsum == 0.f ? 0.f : lsum);  // NaN stays
-        float* part = a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (piece.ta == 0)) *
-                                         (R * (D + 2));
-        float* dst = piece.whole ? a.rowbuf + at * D : part + rr * D;
-#pragma unroll
-        for (int g = 0; g < D / 64; ++g) {
-          const int col = g * 64 + c16 * 4;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < kHalfWarps; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(mo + (i * R + rr) * L::kPad + col);
-            acc.x = fmaf(w[i], v.x, acc.x);
-            acc.y = fmaf(w[i], v.y, acc.y);
-            acc.z = fmaf(w[i], v.z, acc.z);
-            acc.w = fmaf(w[i], v.w, acc.w);
-          }
-          if (final_out)
-            *reinterpret_cast<uint2*>(a.o + at * D + col) = make_uint2(
-                pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-          else
-            *reinterpret_cast<float4*>(dst + col) = acc;
-        }
-        if (c16 == 0) {
+        if ((lane & 3) == 0) {
           if (final_out) {
-            a.lse[static_cast<int64_t>(head) * a.total + e.start + tok] =
-                lsum == 0.f ? -INFINITY : (mx + log2f(lsum)) * kLn2;
-          } else if (piece.whole) {
-            float* st = a.rowbuf + static_cast<int64_t>(a.total) * a.H * D;
-            st[at] = mx;
-            st[static_cast<int64_t>(a.total) * a.H + at] = lsum;
+            const int t = (at[i] - head[i]) / a.H;
+            a.lse[static_cast<int64_t>(head[i]) * a.total + t] =
+                sum[i] == 0.f ? -INFINITY : (m[i] + log2f(sum[i])) * kLn2;
           } else {
-            part[R * D + rr] = mx;
-            part[R * D + R + rr] = lsum;
+            float* st = piece.whole ? a.rowbuf + static_cast<int64_t>(a.total) * a.H * D + at[i]
+                                    : part + R * D + rr;
+            st[0] = m[i];
+            st[piece.whole ? a.total * a.H : R] = sum[i];
           }
         }
       }
@@ -444,7 +373,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
     const PartialLayout& p = a.part[li];
     const int2 span = p.spans[where[li]];
     // a launch that gave up leaves no span: nothing out of range is read
-    if (span.x < 0 || span.y < 1 || span.x + span.y > p.ctas) continue;
+    if (span.x < 0 || span.y < 1 || span.x + span.y > p.workers) continue;
     const bool one = span.y == 1;
     if (one && a.rowbuf[li] == nullptr) return;  // already final
     const int64_t size = static_cast<int64_t>(p.R) * (D + 2);

@@ -133,15 +133,15 @@ struct KeyList {
 
 // Partial results of one list.  Its rows (query token x head of the key/value head's group) are
 // cut into tiles of R rows; tile r of entry b has index row_tile0(b) + r in [0, row_tiles()).
-// spans[hk][tile] = (first CTA, number of CTAs) that worked on the tile's keys.  One CTA: it wrote
-// the result (a joined list: into the row buffer).  Several: CTA i left its part in slot
+// spans[hk][tile] = (first worker, number of workers) that had the tile's keys.  One: it wrote
+// the result (a joined list: into the row buffer).  Several: worker i left its part in slot
 // 2 i + (1 when it began the tile's keys), and the join kernel adds them up in key order.
 struct PartialLayout {
   int R;
   int2* spans;
   int span_tiles;  // tiles per key/value head
-  float* slots;    // [ctas][2][R * (D + 2)]: unnormalised O, then m (log2 units), then l
-  int ctas;
+  float* slots;    // [workers][2][R * (D + 2)]: unnormalised O, then m (log2 units), then l
+  int workers;
 };
 __host__ __device__ inline int row_tiles_bound(int total, int G, int R, int count) {
   return (total * G + R - 1) / R + count;
@@ -177,10 +177,12 @@ struct JoinArgs {
 };
 
 constexpr int kPagedRows = 16;           // rows of a tile
-constexpr int kPagedCtas = 152;          // CTAs of a launch (and pairs of slots): one per SM
-constexpr int kPagedUnsplitKeys = 512;   // where no entry has more keys, none is split
+constexpr int kPagedCtas = 152;          // CTAs of a launch: one per SM
+constexpr int kPagedWarps = 8;           // warps of a CTA, each a worker
+constexpr int kPagedUnsplitKeys = 256;   // where no entry has more keys, none is split
 
-constexpr int kPagedMmaRows = 256;       // rows of a tile of the tensor-core kernel
+constexpr int kPagedMmaRows = 256;       // rows of a tile of the tensor-core kernel, whose CTAs
+constexpr int kPagedMmaUnsplitKeys = 512;  // are the workers
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s);
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -28,7 +28,7 @@ namespace {
 constexpr int kThreads = 384;  // warp 0: TMA, 1: MMA, 2: pieces, 4-7 and 8-11: softmax
 constexpr int R = kPagedMmaRows;
 constexpr int KT = 128;
-constexpr int kDirectTiles = 4;
+constexpr int kDirectTiles = kPagedMmaUnsplitKeys / KT;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // What the roles need to know of a piece, in a ring of shared memory.
@@ -81,10 +81,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t s_full[2], p_full[2], o_full[2], mma_done[1];
   __shared__ uint64_t piece_full[kRing], piece_empty[kRing];
   __shared__ PieceInfo pieces[kRing];
-  __shared__ volatile uint32_t bad_pages[2 * S];  // pages of a position outside the pool
   __shared__ uint32_t tmem_slot[1];
   __shared__ volatile int abort_flag[1];
-  __shared__ Share sh;  // for the warp that walks it
+  __shared__ Share sh;
   const Ctl ctl{abort_flag, a.status, timeout_ns};
   const uint32_t warp = warp_id(), lane = lane_id();
   if (pad + L::kBytes > smem_bytes) {  // cannot happen with the host's sizing; never proceed
@@ -92,13 +91,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   begin_launch(a.first);
-  {
-    const Share mine = make_share<R, KT, kThreads, kDirectTiles>(a);
-    if (mine.u0 >= mine.u1) {  // uniform over the CTA
-      wait_for_last_launch();
-      return;
-    }
-    if (threadIdx.x == 0) sh = mine;
+  make_shares<R, KT, kThreads, kDirectTiles, 1>(a, &sh);
+  if (sh.u0 >= sh.u1) {  // uniform over the CTA
+    wait_for_last_launch();
+    return;
   }
   const KeyList& l = a.list;
 
@@ -188,29 +184,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&piece_empty[i % kRing]);  // all of it is in registers
         if (npos < 0) break;
-        // page of this lane's box at key tile kt: out of range past the end, bad outside the pool
-        auto find = [&](int kt, bool& bad) {
+        // page of this lane's box at key tile kt: the map's out-of-range coordinate, which reads
+        // as zeros, past the end and (reported) for a page outside the pool
+        auto find = [&](int kt) {
           const int key = kt * KT + pg * page_size;
-          const int page =
-              key < len ? resolve_page(trow, l.max_pages, a.num_pages, a.page_shift, key) : -1;
-          bad = key < len && page < 0;
+          if (key >= len) return a.num_pages * a.Hkv;
+          const int page = resolve_page(trow, l.max_pages, a.num_pages, a.page_shift, key);
+          if (page < 0) atomicCAS(a.status, 0, kErrIndex);
           return page < 0 ? a.num_pages * a.Hkv : page * a.Hkv + hk;
         };
-        bool bad = false, bad_next = false;
-        int z = 0, z_next = npos > 0 ? find(ta, bad_next) : 0;
+        int z = 0, z_next = npos > 0 ? find(ta) : 0;
         for (int j = 0; j < npos; ++j) {
           const int s = jk % S;
           const uint32_t ph = (jk / S) & 1;
           z = z_next;
-          bad = bad_next;
-          if (j + 1 < npos) z_next = find(ta + j + 1, bad_next);
-          const uint32_t mask = __ballot_sync(~0u, bad) & ((1u << pages) - 1u);
+          if (j + 1 < npos) z_next = find(ta + j + 1);
           if (!(ok = mbar_wait_warp(&k_empty[s], ph ^ 1, ctl))) break;
-          if (lane == 0) {
-            if (mask != 0) atomicCAS(a.status, 0, kErrIndex);
-            bad_pages[jk % (2 * S)] = mask;
-            mbar_arrive_expect_tx(&k_full[s], L::kTile);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&k_full[s], L::kTile);
           __syncwarp();
           const uint32_t at = s * L::kTile + panel * 16384 + pg * (page_size * 128);
           if (mine) tma_load_3d(sm + L::kK + at, &tmK, &k_full[s], panel * 64, 0, z);
@@ -347,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int jg = base + j;
         if (!(ok = mbar_wait_warp(&s_full[t], (seen + j) & 1, ctl))) break;
         tc_fence_after();
-        const uint32_t bad = bad_pages[jg % (2 * S)];
         uint32_t s[128];
         tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -356,23 +345,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(s);
         const int k0 = (ta + j) * KT;
-        const bool masked = k0 + KT > lim_min || bad != 0;
-        auto visible = [&](int c) {
-          return k0 + c < lim && !((bad >> (c >> a.page_shift)) & 1u);
-        };
-        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (masked) {
+        // hidden keys get a score of -inf in place, so that what follows is the same code for
+        // every tile: it has to stay in the instruction cache next to the MMA issuer's loop
+        if (k0 + KT > lim_min) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (visible(c)) mxv[c & 3] = fmaxf(mxv[c & 3], __uint_as_float(s[c]));
-        } else {
+            if (k0 + c >= lim) s[c] = 0xff800000u;
+        }
+        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            mxv[0] = max3(mxv[0], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-            mxv[1] = max3(mxv[1], __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-            mxv[2] = max3(mxv[2], __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
-            mxv[3] = max3(mxv[3], __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
-          }
+        for (int c = 0; c < 128; c += 8) {
+          mxv[0] = max3(mxv[0], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          mxv[1] = max3(mxv[1], __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          mxv[2] = max3(mxv[2], __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+          mxv[3] = max3(mxv[3], __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
         }
         const float mx = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3]));
         const float m_tile = mx * c2;
@@ -385,34 +371,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           m_run = m_tile;
         }
         const float2 cc = make_float2(c2, c2);
-        const float2 nm = make_float2(-m_run, -m_run);
+        const float neg = m_run == -INFINITY ? 0.f : -m_run;  // no visible key yet: all weights 0
+        const float2 nm = make_float2(neg, neg);
         float2 sumv[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // weights in two halves of 64 keys, each stored over S as soon as it is packed (32 fewer
-        // registers alive than with all of P)
+        // registers alive than with all of P).  c2 > 0, so -inf stays -inf and weighs 0.
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           uint32_t p[32];
-          if (masked) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int k = 64 * hf + 2 * c;
-              const float2 x = fma2(
-                  make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm);
-              const float x0 = visible(k) ? ex2(x.x) : 0.f;
-              const float x1 = visible(k + 1) ? ex2(x.y) : 0.f;
-              p[c] = pack_bf16(x0, x1);
-              sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int k = 64 * hf + 2 * c;
-              const float2 x = fma2(
-                  make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm);
-              const float x0 = ex2(x.x), x1 = ex2(x.y);
-              p[c] = pack_bf16(x0, x1);
-              sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
-            }
+          for (int c = 0; c < 32; ++c) {
+            const int k = 64 * hf + 2 * c;
+            const float2 x = fma2(
+                make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), cc, nm);
+            const float x0 = ex2(x.x), x1 = ex2(x.y);
+            p[c] = pack_bf16(x0, x1);
+            sumv[c & 1] = add2(sumv[c & 1], make_float2(x0, x1));
           }
           tmem_st32(tS + 32 * hf, p);
         }

@@ -2,6 +2,7 @@
 // rotation pass, the paged cache and the attention that reads it.  Every argument is checked
 // before the first launch; nothing here allocates device memory.
 #include <cmath>
+#include <limits>
 
 #include "fa.h"
 #include "fa_host.h"
@@ -112,7 +113,7 @@ struct PagedWorkspace {
 PagedWorkspace paged_workspace(const int (&count)[2], int lists, int total, int H, int Hkv, int d) {
   PagedWorkspace w{};
   size_t at = 0;
-  size_t slots = static_cast<size_t>(fa::kPagedCtas) * 2 * fa::kPagedRows * (d + 2) * 4;
+  size_t slots = static_cast<size_t>(fa::kPagedCtas) * fa::kPagedWarps * 2 * fa::kPagedRows * (d + 2) * 4;
   if (static_cast<long long>(total) * (H / Hkv) > kMmaRows) {
     const size_t mma = static_cast<size_t>(fa::kPagedCtas) * 2 * fa::kPagedMmaRows * (d + 2) * 4;
     if (mma > slots) slots = mma;
@@ -175,7 +176,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     const long long keys = i == 0 ? max_kv : prefix->max_len;
     units[i] = Hkv * static_cast<long long>(fa::row_tiles_bound(
                          total, H / Hkv, mma[i] ? fa::kPagedMmaRows : fa::kPagedRows, count[i])) *
-               (keys / 128 + 1);
+               (keys / (mma[i] ? 128 : 16) + 1);
     if (units[i] > kMaxInt) return FA_ERR_UNSUPPORTED;
   }
   const PagedWorkspace w = paged_workspace(count, lists, total, H, Hkv, d);
@@ -198,7 +199,8 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   a.G = H / Hkv;
   a.num_pages = cache->num_pages;
   a.page_shift = page_shift(cache->page_size);
-  a.scale_log2 = fa::resolve_scale(scale, d) * kLog2e;
+  // never quite 0 (a scale of 0): a hidden key's score of -inf has to stay -inf when scaled
+  a.scale_log2 = std::fmax(fa::resolve_scale(scale, d) * kLog2e, std::numeric_limits<float>::denorm_min());
   a.status = status;
   fa::JoinArgs j{};
   j.o = a.o;
@@ -229,7 +231,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     l.causal = i == 0 && causal ? 1 : 0;
     a.rowbuf = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
     a.part.R = mma[i] ? fa::kPagedMmaRows : fa::kPagedRows;
-    a.part.ctas = fa::kPagedCtas;
+    a.part.workers = fa::kPagedCtas * (mma[i] ? 1 : fa::kPagedWarps);
     a.part.span_tiles = fa::row_tiles_bound(total, a.G, a.part.R, l.count);
     a.part.spans = reinterpret_cast<int2*>(base + w.spans[i]);
     a.part.slots = reinterpret_cast<float*>(base + w.slots[i]);
@@ -246,7 +248,8 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     j.rowbuf[i] = a.rowbuf;
   }
   // no entry can have been split (lengths are clamped to max_kv): every result is final
-  if (lists == 1 && max_kv <= fa::kPagedUnsplitKeys) return FA_OK;
+  if (lists == 1 && max_kv <= (mma[0] ? fa::kPagedMmaUnsplitKeys : fa::kPagedUnsplitKeys))
+    return FA_OK;
   return status_of(fa::launch_paged_join(d, j, s));
 }
 

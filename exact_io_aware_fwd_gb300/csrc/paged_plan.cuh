@@ -1,16 +1,17 @@
-// How the CTAs of a paged-attention launch share its keys.
+// How the workers of a paged-attention launch share its keys (a worker: a CTA of the tensor-core
+// kernel, a warp of the other one).
 //
 // The work of entry b is one segment per (key/value head, row tile), each of as many key tiles
 // (KT keys) as the tile's last row sees.  Laid end to end, the segments' key tiles are units
-// 0 .. W - 1, and CTA c of C takes units [c W / C, (c + 1) W / C): equal shares whatever the
-// lengths, at most two unfinished segments per CTA, so the partial results take 2 C
-// slots however long the cache is.  When no segment has more than kDirectTiles key tiles,
-// splitting would cost more than it gives (a join kernel has to read the parts back): then a
-// unit is a whole segment.  Lengths live on the device, so every CTA works this out for itself
-// from one pass over them.  Units fit 32 bits (the host refuses more).
+// 0 .. W - 1, and worker c of C takes units [c W / C, (c + 1) W / C): equal shares whatever the
+// lengths, at most two unfinished segments per worker, so the partial results take 2 C slots
+// however long the cache is.  When no segment has more than kDirectTiles key tiles, splitting
+// would cost more than it gives (a join kernel has to read the parts back): then a unit is a
+// whole segment.  Lengths live on the device, so every CTA works this out for itself from one
+// pass over them.  Units fit 32 bits (the host refuses more).
 //
-// A CTA takes the pieces of its share last to first.  Then the CTAs of one head's row tiles all
-// start at key tile 0 of some row tile and walk the keys abreast, and so do they later in the
+// A worker takes the pieces of its share last to first.  Then the CTAs of one head's row tiles
+// all start at key tile 0 of some row tile and walk the keys abreast, and so do they later in the
 // tails they began with in unit order: row tiles meet the same K, V in L2 instead of reading
 // them at different times.
 #pragma once
@@ -68,35 +69,35 @@ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, 
   return e;
 }
 
-// Splitting W units over C CTAs: CTA c takes [c W / C, (c + 1) W / C).  (The longer shares are
-// spread over the CTAs on purpose: with all of them first, the CTAs of a tensor-core launch run in
-// lockstep and their bursts of copies slow the MMAs: 249 instead of 226 us for 2 x 512 tokens over
-// 16384 keys.)
+// Splitting W units over C workers: worker c takes [c W / C, (c + 1) W / C).  (The longer shares
+// are spread over the workers on purpose: with all of them first, the CTAs of a tensor-core launch
+// run in lockstep and their bursts of copies slow the MMAs: 249 instead of 226 us for 2 x 512
+// tokens over 16384 keys.)
 __host__ __device__ inline int share_begin(int W, int C, int c) {
   return static_cast<int>(static_cast<int64_t>(c) * W / C);
 }
-// CTA that owns unit u: the largest c with c W / C <= u.
+// Worker that owns unit u: the largest c with c W / C <= u.
 __host__ __device__ inline int share_owner(int W, int C, int u) {
   return static_cast<int>(((static_cast<int64_t>(u) + 1) * C - 1) / W);
 }
 
 struct Share {
-  int W, u0, u1;  // all units, and this CTA's
-  int C;          // CTAs that have units
+  int W, C;       // all units, and the workers that have some
   bool direct;    // a unit is a whole segment
-  int b;          // entry of unit u1 - 1
-  int off;        // its units before u1
+  int worker;     // this worker and its units (none: u0 == u1)
+  int u0, u1;
+  int b, off;     // entry of unit u1 - 1, and its units before u1
   Entry e;        // that entry
 };
 
-// Called by all kThreads threads of the CTA.
-template <int R, int KT, int kThreads, int kDirectTiles>
-__device__ Share make_share(const PagedArgs& a) {
+// The shares of the CTA's kWorkers workers (worker w of CTA c is number c + w x CTAs: the first
+// units go to different SMs).  Called by all kThreads threads; `shares` in shared memory is
+// complete when it returns.
+template <int R, int KT, int kThreads, int kDirectTiles, int kWorkers>
+__device__ void make_shares(const PagedArgs& a, Share* shares) {
   constexpr int kWarps = kThreads / 32;
   __shared__ int red[3][kWarps];
   __shared__ int scan[kWarps];
-  __shared__ int at[2];
-  __shared__ Entry at_entry;
   const KeyList& l = a.list;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int seg = 0, til = 0, mx = 0;   // over all entries
@@ -124,20 +125,22 @@ __device__ Share make_share(const PagedArgs& a) {
     til += red[1][w];
     mx = max(mx, red[2][w]);
   }
-  Share sh;
-  sh.direct = mx <= kDirectTiles;
-  sh.W = sh.direct ? seg : til;
+  const bool direct = mx <= kDirectTiles;
+  const int W = direct ? seg : til;
   // a share of fewer than kDirectTiles / 2 tiles is not worth a slot
-  const int most = sh.direct ? sh.W : (sh.W + kDirectTiles / 2 - 1) / (kDirectTiles / 2);
-  sh.C = min(most, static_cast<int>(gridDim.x));
-  const int c = blockIdx.x;
-  sh.u0 = c < sh.C ? share_begin(sh.W, sh.C, c) : 0;
-  sh.u1 = c < sh.C ? share_begin(sh.W, sh.C, c + 1) : 0;
-  sh.b = 0;
-  sh.off = 0;
-  if (sh.u0 >= sh.u1) return sh;  // uniform over the CTA
-  // entry of unit u1 - 1: scan the entries kThreads at a time
-  const int last = sh.u1 - 1;
+  const int most = direct ? W : (W + kDirectTiles / 2 - 1) / (kDirectTiles / 2);
+  const int C = min(most, static_cast<int>(gridDim.x) * kWorkers);
+  if (tid < kWorkers) {
+    Share& s = shares[tid];
+    const int c = blockIdx.x + tid * gridDim.x;
+    s.W = W;
+    s.C = C;
+    s.direct = direct;
+    s.worker = c;
+    s.u0 = c < C ? share_begin(W, C, c) : 0;
+    s.u1 = c < C ? share_begin(W, C, c + 1) : 0;
+  }
+  // entry of each worker's unit u1 - 1: scan the entries kThreads at a time
   int before = 0;
   for (int b0 = 0; b0 < l.count; b0 += kThreads) {
     const int b = b0 + tid;
@@ -146,7 +149,7 @@ __device__ Share make_share(const PagedArgs& a) {
       if (b < l.count) mine = entry_of<R, KT>(l, a, b, false);
       __syncthreads();  // the readers of scan are done
     }
-    const int units = (sh.direct ? mine.rt : mine.tiles) * a.Hkv;
+    const int units = (direct ? mine.rt : mine.tiles) * a.Hkv;
     int incl = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -162,30 +165,32 @@ __device__ Share make_share(const PagedArgs& a) {
       if (w < warp) incl += scan[w];
       chunk += scan[w];
     }
-    if (units > 0 && incl - units <= last && last < incl) {
-      at[0] = b;
-      at[1] = sh.u1 - (incl - units);
-      at_entry = mine;
+    if (units > 0) {
+#pragma unroll 1
+      for (int w = 0; w < kWorkers; ++w) {
+        const int last = shares[w].u1 - 1;
+        if (incl - units <= last && last < incl) {
+          shares[w].b = b;
+          shares[w].off = last + 1 - (incl - units);
+          shares[w].e = mine;
+        }
+      }
     }
     before = chunk;
-    if (last < before) break;  // uniform
+    if (W <= before) break;  // uniform
   }
   __syncthreads();
-  sh.b = at[0];
-  sh.off = at[1];
-  sh.e = at_entry;
-  return sh;
 }
 
-// A CTA's piece of one segment: key tiles [ta, te) of row tile r for key/value head hk.
+// A worker's piece of one segment: key tiles [ta, te) of row tile r for key/value head hk.
 struct Piece {
   int hk, r, ta, te;
-  bool whole;  // no other CTA works on the segment
+  bool whole;  // no other worker has a part of the segment
   int unit;    // the segment's first unit
   int tiles;   // its key tiles
 };
 
-// Walks the pieces of a CTA's share, last to first; e is the entry b of the current piece.
+// Walks the pieces of a worker's share, last to first; e is the entry b of the current piece.
 template <int R, int KT>
 struct Walk {
   int u0, u1;   // what is left of the share
@@ -234,11 +239,10 @@ struct Walk {
   }
 };
 
-// (first CTA, number of CTAs) of the segment that this CTA begins.
+// (first worker, number of workers) of the segment that this worker begins.
 __device__ __forceinline__ int2 span_of(const Share& sh, const Piece& p) {
-  const int first = blockIdx.x;
-  const int last = p.whole ? first : share_owner(sh.W, sh.C, p.unit + p.tiles - 1);
-  return make_int2(first, last - first + 1);
+  const int last = p.whole ? sh.worker : share_owner(sh.W, sh.C, p.unit + p.tiles - 1);
+  return make_int2(sh.worker, last - sh.worker + 1);
 }
 
 }  // namespace fa

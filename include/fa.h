@@ -309,8 +309,9 @@ fa_status fa_qk_norm_rope_bwd(const fa_view grad[3], const fa_view x[2], const f
  * (NULL: one token each, total == B).  Token i of n new ones is key kv_lens[b] - n + i.
  * Tokens behind cu_seqlens[B] are left as they were.
  * What the library reads from device memory is checked on the device: a page outside
- * [0, num_pages) is neither read nor written (its keys count as masked), lengths are clamped to
- * [0, max_pages * page_size] (and the bounds a call takes), and FA_ERR_INDEX is recorded.
+ * [0, num_pages) is neither read nor written (its keys and values count as zeros), lengths are
+ * clamped to [0, max_pages * page_size] (and the bounds a call takes), and FA_ERR_INDEX is
+ * recorded.
  */
 typedef struct {
   void* k_cache;
@@ -340,7 +341,8 @@ fa_status fa_kv_append(const fa_view in[3], const fa_view* q_out, const fa_paged
  * no key gets O = 0, LSE = -inf.  max_q, max_kv: at least the most new tokens and keys of any
  * sequence (tokens and keys beyond them are not computed, and FA_ERR_INDEX is recorded).
  * H % Hkv == 0, H / Hkv <= 128.  FA_ERR_UNSUPPORTED where Hkv (total H / Hkv / 16 + B)
- * (max_kv / 128 + 1) does not fit 31 bits.
+ * (max_kv / 16 + 1) does not fit 31 bits (with at most 32 rows max_q H / Hkv; else with 256 and
+ * 128 for the 16s).
  * The keys are split over the whole GPU, partial results joined in a fixed order: the same
  * inputs give bit-identical outputs.  V of a key that some query of the same tile may see must
  * be finite, as in fa_fwd; cache rows past a sequence's length may hold anything.

@@ -174,22 +174,24 @@ def test_paged_is_bitwise_repeatable_and_leaves_other_rows():
     assert fa.fa_get_error() == fa.FA_OK
 
 
-def test_paged_bad_pages_are_masked_and_reported():
-    """Pages outside the pool are neither read nor counted: the result is attention over the other
-    keys, and the status says so."""
+@pytest.mark.parametrize("nq", [1, 40], ids=["few rows", "many rows"])
+def test_paged_bad_pages_read_as_zeros_and_are_reported(nq):
+    """Pages outside the pool are not read: their keys and values count as zeros, and the status
+    says so."""
     lens, Hkv, d, page = [200, 90], 2, 64, 32
     cache = Cache(lens, Hkv, d, page, seed=31)
     k, v, table, ln = cache.dev()
     table[0, 1], table[0, 4], table[1, 0] = -5, k.shape[0], 1 << 30
-    q = torch.randn(2, 4, d, device=DEV).to(BF16)
-    out, lse = fa.fa_fwd_paged(q, k, v, table, ln)
+    q = torch.randn(2 * nq, 4, d, device=DEV).to(BF16)
+    out, lse = fa.fa_fwd_paged(q, k, v, table, ln, cu_seqlens=i32([0, nq, 2 * nq]), max_q=nq)
     assert fa.fa_get_error() == fa.FA_ERR_INDEX and fa.fa_get_error() == fa.FA_OK
     per = []
     for b, gone in ((0, [1, 4]), (1, [0])):
-        keep = [j for j in range(lens[b]) if j // page not in gone]
-        K, V = (x[:, keep] for x in cache.keys(b))
-        per.append((K, V, [len(keep)]))
-    check(out, lse, q, [0, 1, 2], per, d ** -0.5)
+        K, V = cache.keys(b)
+        for g in gone:
+            K[:, g * page:(g + 1) * page], V[:, g * page:(g + 1) * page] = 0, 0
+        per.append((K, V, [lens[b]] * nq))
+    check(out, lse, q, [0, nq, 2 * nq], per, d ** -0.5)
 
 
 def test_paged_lengths_past_their_bounds():
