@@ -306,46 +306,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
   wait_for_last_launch();
 }
 
-// token_sequence by a whole warp: 32 offsets a step.
-__device__ __forceinline__ int token_sequence_warp(const int32_t* cu, int B, int t, int lane) {
+// ---- join of the parts
+constexpr int kJoinThreads = 128;
+constexpr int kLanes = 8;                          // lanes of a group
+constexpr int kGroups = kJoinThreads / kLanes;     // groups of a CTA
+
+// token_sequence by a group of 8 lanes (`mask`: its lanes of the warp): 8 offsets a step.
+__device__ __forceinline__ int token_sequence_group(const int32_t* cu, int B, int t, int sub,
+                                                    unsigned mask) {
   if (cu == nullptr) return t < B ? t : -1;
-  int lo = 0, n = B + 1;  // the last of n offsets from lo that is <= t
-  int found = -1;
+  int lo = 0, n = B + 1;  // the last of the n offsets from lo that is <= t
   while (true) {
-    const int step = (n + 31) / 32, i = lo + lane * step;
-    const bool le = lane * step < n && __ldg(cu + i) <= t;
-    const unsigned hit = __ballot_sync(~0u, le);
-    if (hit == 0) return -1;  // before cu[0]
-    found = lo + (31 - __clz(hit)) * step;
+    const int step = (n + kLanes - 1) / kLanes;
+    const bool le = sub * step < n && __ldg(cu + lo + sub * step) <= t;
+    const int hits = __popc(__ballot_sync(mask, le) & mask);  // offsets ascend: a prefix of lanes
+    if (hits == 0) return -1;  // before cu[0]
+    n = min(step, n - (hits - 1) * step);
+    lo += (hits - 1) * step;
     if (step == 1) break;
-    n = min(step, lo + n - found);
-    lo = found;
   }
-  return found < B ? found : -1;  // behind cu[B]
+  return lo < B ? lo : -1;  // behind cu[B]
 }
 
-// Joins the parts of each output row: O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i.  One warp per
-// (token, head).  The lanes first take a part's m and l each, which gives every part's weight,
-// and then sum the parts' O in the order of the keys, D / 32 elements a lane, with loads that
-// depend on nothing but the spans.
-template <int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
-  constexpr int E = D / 32;
+// O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i over a row's parts, in the order of the keys.
+// Bound by latency: spans, then m and l, then O, each from the one before.  A group of 8 lanes
+// takes a row (kSplit == 1, 16 rows a CTA: many rows of few parts), or the 16 groups of a CTA
+// take every 16th part of one row and meet in shared memory (kSplit == 16: few rows of many
+// parts, long contexts of small batches: 4 x 131072 keys, 38 parts, 20 us with one warp a row).
+template <int D, int kSplit>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs a) {
+  constexpr int E = D / kLanes / 4;  // float4s of a lane
   let_next_launch();
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const bool inside = id < static_cast<int64_t>(a.total) * a.H;
-  const int t = inside ? static_cast<int>(id / a.H) : 0;
-  const int head = inside ? static_cast<int>(id % a.H) : 0, hk = head / a.G;
-  const int seq = inside ? token_sequence_warp(a.cu, a.B, t, lane) : -1;
+  const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+  const int rows = a.total * a.H;
+  const int64_t id64 = kSplit == 1 ? static_cast<int64_t>(blockIdx.x) * kGroups + group
+                                   : static_cast<int64_t>(blockIdx.x);
+  const bool inside = id64 < rows;
+  const int id = inside ? static_cast<int>(id64) : 0;
+  const int t = id / a.H, head = id - t * a.H, hk = head / a.G;
+  const int seq = token_sequence_group(a.cu, a.B, t, sub, mask);
   // where the row's parts are: its span and row tile in each list (these inputs are the call's)
   int where[2] = {-1, -1}, rr[2] = {0, 0};
-  bool skip = seq < 0;
+  bool skip = !inside || seq < 0;
   for (int li = 0; li < a.lists && !skip; ++li) {
     const KeyList& l = a.list[li];
     int b = seq, start, n;
     if (l.group_cu != nullptr) {
-      b = token_sequence_warp(l.group_cu, l.count, seq, lane);
+      b = token_sequence_group(l.group_cu, l.count, seq, sub, mask);
       if (b < 0) continue;  // a sequence of no group has no prefix
       const int s0 = min(max(__ldg(l.group_cu + b), 0), a.B);
       start = a.cu != nullptr ? min(max(__ldg(a.cu + s0), 0), a.total) : s0;
@@ -354,78 +362,112 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const JoinArgs a) {
       token_bounds(a.cu, b, a.total, start, n);
       n = min(n, l.max_q);
     }
-    if (t < start || t - start >= n) {
-      skip = true;  // beyond max_q: not computed
-      break;
-    }
+    skip = t < start || t - start >= n;  // beyond max_q: not computed
     const int row = (t - start) * a.G + (head - hk * a.G);
     const int tile = row_tile0(start, a.G, a.part[li].R, b) + row / a.part[li].R;
     rr[li] = row % a.part[li].R;
     if (tile >= 0 && tile < a.part[li].span_tiles) where[li] = hk * a.part[li].span_tiles + tile;
   }
   wait_for_last_launch();
-  if (skip) return;
-  float m = -INFINITY, lsum = 0.f, o[E];
+  float m = -INFINITY, lsum = 0.f;
+  float4 o[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i) o[i] = 0.f;
-  for (int li = 0; li < a.lists; ++li) {
+  for (int i = 0; i < E; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool done = false;  // already final
+  for (int li = 0; li < a.lists && !skip; ++li) {
     if (where[li] < 0) continue;
     const PartialLayout& p = a.part[li];
     const int2 span = p.spans[where[li]];
     // a launch that gave up leaves no span: nothing out of range is read
     if (span.x < 0 || span.y < 1 || span.x + span.y > p.workers) continue;
     const bool one = span.y == 1;
-    if (one && a.rowbuf[li] == nullptr) return;  // already final
+    if (one && a.rowbuf[li] == nullptr) {
+      done = true;
+      break;
+    }
     const int64_t size = static_cast<int64_t>(p.R) * (D + 2);
-    const int64_t rows = static_cast<int64_t>(a.total) * a.H;
     auto slot = [&](int i) { return p.slots + ((span.x + i) * 2 + (i == 0)) * size; };
-    for (int i0 = 0; i0 < span.y; i0 += 32) {
-      const int count = min(32, span.y - i0);
+    // this group's parts: i0, i0 + kSplit, ...; eight at a time, one lane each for m and l
+    for (int i0 = kSplit == 1 ? 0 : group; i0 < span.y; i0 += kLanes * kSplit) {
+      const int mine = i0 + sub * kSplit;
       float pm = -INFINITY, pl = 0.f;
-      if (lane < count) {
-        const float* st = one ? a.rowbuf[li] + rows * D + id : slot(i0 + lane) + p.R * D + rr[li];
+      if (mine < span.y) {
+        const float* st = one ? a.rowbuf[li] + static_cast<int64_t>(rows) * D + id
+                              : slot(mine) + p.R * D + rr[li];
         pm = st[0];
         pl = st[one ? rows : p.R];
       }
       float top = pm;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+      for (int x = kLanes / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, x));
       top = fmaxf(top, m);
       const float keep = m == -INFINITY ? 0.f : ex2(m - top);
       // a part without a visible key has m = -inf and weighs nothing
       const float w = pm == -INFINITY ? (pl == 0.f ? 0.f : pl) : ex2(pm - top);
       float s = w * pl;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+      for (int x = kLanes / 2; x > 0; x >>= 1) s += __shfl_xor_sync(mask, s, x);
       lsum = lsum * keep + s;
       m = top;
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[i] *= keep;
-#pragma unroll 8
+      for (int e = 0; e < E; ++e) {
+        o[e].x *= keep; o[e].y *= keep; o[e].z *= keep; o[e].w *= keep;
+      }
+      const int count = min(kLanes, (span.y - i0 + kSplit - 1) / kSplit);
+#pragma unroll 2
       for (int i = 0; i < count; ++i) {
-        const float wi = __shfl_sync(~0u, w, i);
-        const float* po = (one ? a.rowbuf[li] + id * D : slot(i0 + i) + rr[li] * D) + lane * E;
-        float v[E];
-        if constexpr (E == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(po);
-          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(po);
-          v[0] = x.x; v[1] = x.y;
-        }
+        const float wi = __shfl_sync(mask, w, i, kLanes);
+        const float4* po = reinterpret_cast<const float4*>(
+            one ? a.rowbuf[li] + static_cast<int64_t>(id) * D : slot(i0 + i * kSplit) + rr[li] * D);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(wi, v[e], o[e]);
+        for (int e = 0; e < E; ++e) {
+          const float4 v = po[e * kLanes + sub];
+          o[e].x = fmaf(wi, v.x, o[e].x);
+          o[e].y = fmaf(wi, v.y, o[e].y);
+          o[e].z = fmaf(wi, v.z, o[e].z);
+          o[e].w = fmaf(wi, v.w, o[e].w);
+        }
       }
     }
   }
+  if constexpr (kSplit > 1) {
+    __shared__ float4 so[kGroups][D / 4];
+    __shared__ float sm[kGroups], sl[kGroups];
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[group][e * kLanes + sub] = o[e];
+    if (sub == 0) {
+      sm[group] = m;
+      sl[group] = lsum;
+    }
+    __syncthreads();
+    if (group != 0) return;
+    m = -INFINITY;
+    lsum = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sm[g]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < kGroups; ++g) {
+      const float w = sm[g] == -INFINITY ? (sl[g] == 0.f ? 0.f : sl[g]) : ex2(sm[g] - m);
+      lsum = fmaf(w, sl[g], lsum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float4 v = so[g][e * kLanes + sub];
+        o[e].x = fmaf(w, v.x, o[e].x);
+        o[e].y = fmaf(w, v.y, o[e].y);
+        o[e].z = fmaf(w, v.z, o[e].z);
+        o[e].w = fmaf(w, v.w, o[e].w);
+      }
+    }
+  }
+  if (skip || done) return;
   const float inv = lsum > 0.f ? 1.f / lsum : (lsum == 0.f ? 0.f : lsum);
-  __nv_bfloat16* dst = a.o + id * D;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(dst + lane * 4) =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst + lane * 2) = pack_bf16(o[0] * inv, o[1] * inv);
-  if (lane == 0)
+  uint2* dst = reinterpret_cast<uint2*>(a.o + static_cast<int64_t>(id) * D);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    dst[e * kLanes + sub] = make_uint2(pack_bf16(o[e].x * inv, o[e].y * inv),
+                                       pack_bf16(o[e].z * inv, o[e].w * inv));
+  if (sub == 0)
     a.lse[static_cast<int64_t>(head) * a.total + t] =
         lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * kLn2;
 }
@@ -446,10 +488,14 @@ cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStrea
 }
 
 cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(a.total) * a.H;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  return d == 64 ? launch_chained(paged_join_kernel<64>, grid, 128, 0, s, a)
-                 : launch_chained(paged_join_kernel<128>, grid, 128, 0, s, a);
+  const unsigned rows = static_cast<unsigned>(a.total) * static_cast<unsigned>(a.H);
+  // with few rows a row has many parts (all the workers' share in few segments)
+  if (rows <= 4 * kPagedCtas)
+    return d == 64 ? launch_chained(paged_join_kernel<64, kGroups>, rows, kJoinThreads, 0, s, a)
+                   : launch_chained(paged_join_kernel<128, kGroups>, rows, kJoinThreads, 0, s, a);
+  const unsigned grid = (rows + kGroups - 1) / kGroups;
+  return d == 64 ? launch_chained(paged_join_kernel<64, 1>, grid, kJoinThreads, 0, s, a)
+                 : launch_chained(paged_join_kernel<128, 1>, grid, kJoinThreads, 0, s, a);
 }
 
 }  // namespace fa
