@@ -100,7 +100,8 @@ struct RopeArgs {
   int n_pos, rot;
   const float *wq, *wk;
   float eps;
-  float* partial;      // backward with norms: [blocks][2][d] weight-gradient partials
+  float* partial;      // backward with norms: [blocks][d] weight-gradient partials
+  int first_k, first_v;  // backward: first blocks of K's and V's rows
   // paged destination of K and V
   __nv_bfloat16 *k_cache, *v_cache;
   const int32_t *block_table, *kv_lens, *cu, *pos_offset;
@@ -108,7 +109,7 @@ struct RopeArgs {
   int* status;
 };
 
-constexpr int kRopeBwdBlocks = 152 * 8;  // most blocks (and partials) of the backward with norms
+constexpr int kRopeBwdBlocks = 152 * 4;  // blocks of the backward (at most two more: one a kind)
 
 cudaError_t launch_rope_table(const double* inv_freq, int rot, int n_pos, float amplitude,
                               float* table, cudaStream_t s);

@@ -10,7 +10,11 @@
 // lane: with interleaved pairs a lane holds 8 consecutive elements (one 16-byte access); with
 // the half layout it holds 4 consecutive elements of the first half and their 4 partners (two
 // 8-byte accesses, each coalesced over the lanes).  A lane group keeps its token's cos and sin in
-// registers and walks over heads, four rows at a time so that four loads are in flight.
+// registers and walks over heads, four rows at a time so that four rows' loads are in flight.
+// A CTA's rows are all of Q, of K or of V: one set of weights, and no choice per row.  The
+// arithmetic is in packed pairs: with scalar operations and a choice of weights per row the
+// instructions, not memory, set the pace (16384 tokens of 48 heads, forward 82, backward 171 us).
+#include "fa_internal.h"
 #include "fa_paged.h"
 #include "sm103.cuh"
 
@@ -46,55 +50,73 @@ struct Row8 {
 };
 
 template <bool kInter>
-__device__ __forceinline__ Row8 load_row(const __nv_bfloat16* row, int off0, int off1) {
+__device__ __forceinline__ Row8 load_row(const __nv_bfloat16* row, int gap) {
   Row8 r;
   if (kInter) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + off0);
+    const uint4 v = *reinterpret_cast<const uint4*>(row);
     r.a = make_uint2(v.x, v.y);
     r.b = make_uint2(v.z, v.w);
   } else {
-    r.a = *reinterpret_cast<const uint2*>(row + off0);
-    r.b = *reinterpret_cast<const uint2*>(row + off1);
+    r.a = *reinterpret_cast<const uint2*>(row);
+    r.b = *reinterpret_cast<const uint2*>(row + gap);
   }
   return r;
 }
 template <bool kInter>
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, int off0, int off1, const Row8& r) {
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int gap, const Row8& r) {
   if (kInter) {
-    *reinterpret_cast<uint4*>(row + off0) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
+    *reinterpret_cast<uint4*>(row) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
   } else {
-    *reinterpret_cast<uint2*>(row + off0) = r.a;
-    *reinterpret_cast<uint2*>(row + off1) = r.b;
+    *reinterpret_cast<uint2*>(row) = r.a;
+    *reinterpret_cast<uint2*>(row + gap) = r.b;
   }
 }
-__device__ __forceinline__ void unpack(const Row8& r, float (&x)[8]) {
-  x[0] = bf16_lo(r.a.x); x[1] = bf16_hi(r.a.x); x[2] = bf16_lo(r.a.y); x[3] = bf16_hi(r.a.y);
-  x[4] = bf16_lo(r.b.x); x[5] = bf16_hi(r.b.x); x[6] = bf16_lo(r.b.y); x[7] = bf16_hi(r.b.y);
+
+// The lane's eight values as four packed pairs, in memory order.
+struct Vec8 {
+  float2 v[4];
+};
+__device__ __forceinline__ float2 pair_of(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
+__device__ __forceinline__ Vec8 unpack(const Row8& r) {
+  return {{pair_of(r.a.x), pair_of(r.a.y), pair_of(r.b.x), pair_of(r.b.y)}};
 }
-__device__ __forceinline__ Row8 pack(const float (&x)[8]) {
+__device__ __forceinline__ Row8 pack(const Vec8& x) {
   Row8 r;
-  r.a = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-  r.b = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  r.a = make_uint2(pack_bf16(x.v[0].x, x.v[0].y), pack_bf16(x.v[1].x, x.v[1].y));
+  r.b = make_uint2(pack_bf16(x.v[2].x, x.v[2].y), pack_bf16(x.v[3].x, x.v[3].y));
   return r;
 }
-
-// Pair e of the lane is elements (first(e), second(e)) of x.
-template <bool kInter>
-__device__ __forceinline__ constexpr int first_of(int e) { return kInter ? 2 * e : e; }
-template <bool kInter>
-__device__ __forceinline__ constexpr int second_of(int e) { return kInter ? 2 * e + 1 : e + 4; }
-
-// Rotates the lane's four pairs by the angle of (c, s); lanes outside the rotated part keep their
-// elements untouched (not multiplied by 1 and 0: an infinity there must not reach its neighbour).
-template <bool kInter>
-__device__ __forceinline__ void turn(float (&x)[8], const float (&c)[4], const float (&s)[4],
-                                     bool turned) {
-  if (!turned) return;
+__device__ __forceinline__ float dot(const Vec8& a, const Vec8& b) {
+  float2 s = mul2(a.v[0], b.v[0]);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float a = x[first_of<kInter>(e)], b = x[second_of<kInter>(e)];
-    x[first_of<kInter>(e)] = a * c[e] - b * s[e];
-    x[second_of<kInter>(e)] = a * s[e] + b * c[e];
+  for (int i = 1; i < 4; ++i) s = fma2(a.v[i], b.v[i], s);
+  return s.x + s.y;
+}
+
+// cos and sin of the lane's four pairs.
+struct Angles {
+  float2 c[2], s[2];
+};
+
+// Rotates the lane's pairs; lanes outside the rotated part keep their elements untouched (not
+// multiplied by 1 and 0: an infinity there must not reach its neighbour).
+template <bool kInter>
+__device__ __forceinline__ void turn(Vec8& x, const Angles& t, bool turned) {
+  if (!turned) return;
+  if (kInter) {  // v[i] is pair i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = i & 1 ? t.c[i / 2].y : t.c[i / 2].x, s = i & 1 ? t.s[i / 2].y : t.s[i / 2].x;
+      const float a = x.v[i].x, b = x.v[i].y;
+      x.v[i] = fma2(make_float2(-b, a), make_float2(s, s), mul2(make_float2(a, b), make_float2(c, c)));
+    }
+  } else {  // v[i] and v[i + 2] are the first and second elements of pairs 2i, 2i + 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = x.v[i], b = x.v[i + 2];
+      x.v[i] = fma2(make_float2(-b.x, -b.y), t.s[i], mul2(a, t.c[i]));
+      x.v[i + 2] = fma2(b, t.c[i], mul2(a, t.s[i]));
+    }
   }
 }
 
@@ -106,32 +128,51 @@ __device__ __forceinline__ float group_sum(float v, unsigned mask) {
   return v;
 }
 
-__device__ __forceinline__ void load_weight(const float* w, int off0, int off1, float (&r)[8]) {
+__device__ __forceinline__ Vec8 load_weight(const float* w, int off0, int off1) {
   const float4 a = *reinterpret_cast<const float4*>(w + off0);
   const float4 b = *reinterpret_cast<const float4*>(w + off1);
-  r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
-  r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+  return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 
 // cos and sin of the lane's pairs at position pos (clamped to the table).
-__device__ __forceinline__ void load_angle(const RopeArgs& a, int pos, int j, bool turned,
-                                           bool report, float (&c)[4], float (&s)[4]) {
-  if (a.table == nullptr) return;
+__device__ __forceinline__ Angles load_angles(const RopeArgs& a, int pos, int j, bool turned,
+                                              bool report) {
+  Angles t{};
+  if (a.table == nullptr) return t;
   if (pos < 0 || pos >= a.n_pos) {
     if (report) atomicCAS(a.status, 0, kErrIndex);
     pos = pos < 0 ? 0 : a.n_pos - 1;
   }
-  if (!turned) return;
-  const float* t = a.table + static_cast<int64_t>(pos) * a.rot + 4 * j;
-  const float4 cv = *reinterpret_cast<const float4*>(t);
-  const float4 sv = *reinterpret_cast<const float4*>(t + (a.rot >> 1));
-  c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
-  s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+  if (!turned) return t;
+  const float* row = a.table + static_cast<int64_t>(pos) * a.rot + 4 * j;
+  const float4 c = *reinterpret_cast<const float4*>(row);
+  const float4 s = *reinterpret_cast<const float4*>(row + (a.rot >> 1));
+  t.c[0] = make_float2(c.x, c.y);
+  t.c[1] = make_float2(c.z, c.w);
+  t.s[0] = make_float2(s.x, s.y);
+  t.s[1] = make_float2(s.z, s.w);
+  return t;
 }
 
 // Address of row (b, n, head) of a view.
 __device__ __forceinline__ __nv_bfloat16* row_of(const RowView& v, int b, int n, int h) {
   return v.p + b * v.batch + n * v.token + h * v.head;
+}
+
+// Rows h0 .. h1 - 1 of Q, K or V: kind 0, 1, 2.
+struct HeadRange {
+  int kind, h0, h1;
+};
+__host__ __device__ inline int chunks_of(int heads, int chunk) { return (heads + chunk - 1) / chunk; }
+__device__ __forceinline__ HeadRange head_range(const RopeArgs& a, int i) {
+  HeadRange r{0, i * a.chunk, 0};
+  const int cq = chunks_of(a.H, a.chunk), ck = chunks_of(a.Hkv, a.chunk);
+  if (i >= cq) {
+    r.kind = i < cq + ck ? 1 : 2;
+    r.h0 = (i - cq - (r.kind == 2 ? ck : 0)) * a.chunk;
+  }
+  r.h1 = min(r.h0 + a.chunk, r.kind == 0 ? a.H : a.Hkv);
+  return r;
 }
 
 // Forward.  Block: kThreads / (D / 8) tokens; grid y: chunks of heads (q, then k, then v).
@@ -145,8 +186,9 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
   const int t = static_cast<int>(t64);
   const unsigned lane = threadIdx.x & 31u;
   const unsigned mask = ((1u << L) - 1u) << (lane & ~(L - 1u));
-  const int h0 = blockIdx.y * a.chunk;
-  const int h1 = min(h0 + a.chunk, a.H + 2 * a.Hkv);
+  const HeadRange hr = head_range(a, blockIdx.y);
+  const RowView& in = hr.kind == 0 ? a.q : (hr.kind == 1 ? a.k : a.v);
+  if (in.p == nullptr) return;  // no Q, or no V
 
   int b, n, pos;
   int64_t slot = -1;  // paged: element offset of the token's first head, or -1
@@ -162,9 +204,10 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
     n = t;
     pos = key + (a.pos_offset != nullptr ? __ldg(a.pos_offset + seq) : 0);
     if (key >= 0) {
-      const int page = key < limit ? resolve_page(a.block_table + static_cast<int64_t>(seq) * a.max_pages,
-                                                  a.max_pages, a.num_pages, a.page_shift, key)
-                                   : -1;
+      const int page =
+          key < limit ? resolve_page(a.block_table + static_cast<int64_t>(seq) * a.max_pages,
+                                     a.max_pages, a.num_pages, a.page_shift, key)
+                      : -1;
       if (page >= 0)
         slot = ((static_cast<int64_t>(page) * a.Hkv << a.page_shift) +
                 (key & ((1 << a.page_shift) - 1))) * D;
@@ -182,182 +225,262 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
 
   const LanePairs<D, kInter> lp(j, a.rot);
   const bool turned = a.table != nullptr && lp.turned;
-  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  load_angle(a, pos, j, turned, j == 0, c, s);
-  float wq[8], wk[8];
-  const bool norm = a.wq != nullptr;
-  if (norm) {
-    load_weight(a.wq, lp.off0, lp.off1, wq);
-    load_weight(a.wk, lp.off0, lp.off1, wk);
+  const int gap = lp.off1 - lp.off0;
+  const __nv_bfloat16* src = row_of(in, b, n, hr.h0) + lp.off0;
+  __nv_bfloat16* dst;
+  int64_t src_step = in.head, dst_step;
+  if (kPaged && hr.kind != 0) {
+    if (slot < 0) return;
+    dst_step = static_cast<int64_t>(D) << a.page_shift;
+    dst = (hr.kind == 1 ? a.k_cache : a.v_cache) + slot + hr.h0 * dst_step + lp.off0;
+  } else {
+    const RowView& out = hr.kind == 0 ? a.qo : (hr.kind == 1 ? a.ko : a.vo);
+    dst_step = out.head;
+    dst = row_of(out, b, n, hr.h0) + lp.off0;
+  }
+  const float* weight = hr.kind == 0 ? a.wq : a.wk;
+  const bool norm = weight != nullptr;
+  Angles angles{};
+  Vec8 w{};
+  if (hr.kind != 2) {
+    angles = load_angles(a, pos, j, turned, j == 0);
+    if (norm) w = load_weight(weight, lp.off0, lp.off1);
   }
 
-  for (int h = h0; h < h1; h += kRows) {
+  for (int h = hr.h0; h < hr.h1; h += kRows) {
+    const int rows = hr.h1 - h;
     Row8 r[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int hh = h + i;
-      if (hh >= h1) break;
-      const RowView& v = hh < a.H ? a.q : (hh < a.H + a.Hkv ? a.k : a.v);
-      const int hv = hh < a.H ? hh : (hh < a.H + a.Hkv ? hh - a.H : hh - a.H - a.Hkv);
-      if (v.p != nullptr) r[i] = load_row<kInter>(row_of(v, b, n, hv), lp.off0, lp.off1);
-    }
+    for (int i = 0; i < kRows; ++i)
+      if (i < rows) r[i] = load_row<kInter>(src + i * src_step, gap);
+    if (hr.kind != 2) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int hh = h + i;
-      if (hh >= h1) break;
-      const bool is_q = hh < a.H, is_v = hh >= a.H + a.Hkv;
-      if ((is_q && a.q.p == nullptr) || (is_v && a.v.p == nullptr)) continue;
-      if (!is_v) {
-        float x[8];
-        unpack(r[i], x);
+      for (int i = 0; i < kRows; ++i) {
+        if (i >= rows) break;
+        Vec8 x = unpack(r[i]);
         if (norm) {
-          float ss = 0.f;
+          const float rs = rsqrtf(group_sum<L>(dot(x, x), mask) * (1.f / D) + a.eps);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-          const float rs = rsqrtf(group_sum<L>(ss, mask) * (1.f / D) + a.eps);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * rs * (is_q ? wq[e] : wk[e]);
+          for (int e = 0; e < 4; ++e) x.v[e] = mul2(x.v[e], mul2(w.v[e], make_float2(rs, rs)));
         }
-        turn<kInter>(x, c, s, turned);
+        turn<kInter>(x, angles, turned);
         r[i] = pack(x);
       }
-      if (is_q) {
-        store_row<kInter>(row_of(a.qo, b, n, hh), lp.off0, lp.off1, r[i]);
-      } else {
-        const int hk = is_v ? hh - a.H - a.Hkv : hh - a.H;
-        if constexpr (kPaged) {
-          if (slot >= 0)
-            store_row<kInter>((is_v ? a.v_cache : a.k_cache) + slot +
-                                  (static_cast<int64_t>(hk) << a.page_shift) * D,
-                              lp.off0, lp.off1, r[i]);
-        } else {
-          store_row<kInter>(row_of(is_v ? a.vo : a.ko, b, n, hk), lp.off0, lp.off1, r[i]);
-        }
-      }
     }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i < rows) store_row<kInter>(dst + i * dst_step, gap, r[i]);
+    src += kRows * src_step;
+    dst += kRows * dst_step;
   }
 }
 
-// Backward.  Work items are (token group, head chunk); with norms the grid is persistent and a
-// thread sums the weight gradients of its elements over all its rows, so that a block leaves one
-// partial [2][D] and the sum over blocks (rope_dw_kernel) has a fixed order.
+// ---- backward
+// Work items are (token group, head chunk).  The grid is persistent and split between Q, K and V
+// (blocks [0, first_k), [first_k, first_v) and the rest), so that with norms a thread sums the
+// weight gradients of its eight elements over all its rows, a block leaves one partial [D], and
+// the sum over blocks (rope_dw_kernel) has a fixed order.  Rows come through a ring of
+// shared-memory stages filled by cp.async, one stage ahead of the arithmetic: each thread reads
+// back only what it copied itself, so the ring needs no barrier and serves as registers that
+// loads can be in flight to.  (16384 tokens of 48 heads: 104 us, with loads into registers alone
+// 110; 8 heads an item 104, 4 heads 123, 16 heads 108: an item's rows are far apart in the
+// attention layout and next to each other in the projection's.)
+constexpr int kBwdRows = 4;    // rows of a stage
+constexpr int kBwdStages = 2;
+constexpr uint32_t kBwdStage = kBwdRows * 2 * 16 * kThreads;  // dz and x, 16 bytes a thread and row
+constexpr uint32_t kBwdSmem = kBwdStages * kBwdStage;
+constexpr int kBwdBlocksPerSm = 4;
+
+template <bool kInter>
+__device__ __forceinline__ void copy_row(uint32_t dst, const __nv_bfloat16* row, int gap) {
+  if (kInter) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row) : "memory");
+  } else {  // the two halves of a row's 16 bytes kThreads * 8 bytes apart: no bank conflicts
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(row) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + kThreads * 8),
+                 "l"(row + gap)
+                 : "memory");
+  }
+}
+template <bool kInter>
+__device__ __forceinline__ Row8 read_row(uint32_t src) {
+  Row8 r;
+  if (kInter) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.b.x), "=r"(r.b.y)
+                 : "r"(src)
+                 : "memory");
+  } else {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.a.x), "=r"(r.a.y) : "r"(src) : "memory");
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(r.b.x), "=r"(r.b.y)
+                 : "r"(src + kThreads * 8)
+                 : "memory");
+  }
+  return r;
+}
+
+// Walks a lane group's rows, kBwdRows at a time.
+template <int G>
+struct RowCursor {
+  int64_t it, items, step;
+  int grp, heads, chunks;
+  int b, n, t, h, h1;  // current token and the heads that are left of the item
+
+  __device__ bool settle(const RopeArgs& a) {  // moves to the first item from `it` that has a token
+    for (; it < items; it += step) {
+      const int64_t t64 = it / chunks * G + grp;
+      if (t64 >= a.tokens) continue;
+      t = static_cast<int>(t64);
+      h = static_cast<int>(it % chunks) * a.chunk;
+      h1 = min(h + a.chunk, heads);
+      b = t / a.N;
+      n = t - b * a.N;
+      return true;
+    }
+    return false;
+  }
+  __device__ bool next(const RopeArgs& a) {
+    h += kBwdRows;
+    if (h < h1) return true;
+    it += step;
+    return settle(a);
+  }
+};
+
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(const RopeArgs a) {
   constexpr int L = D / 8, G = kThreads / L;
-  constexpr int kR = 2;  // rows in flight: each brings a gradient and an input
+  extern __shared__ __align__(16) uint8_t ring[];
   begin_launch(true);
   const int j = threadIdx.x % L, grp = threadIdx.x / L;
   const unsigned lane = threadIdx.x & 31u;
   const unsigned mask = ((1u << L) - 1u) << (lane & ~(L - 1u));
   const LanePairs<D, kInter> lp(j, a.rot);
   const bool turned = a.table != nullptr && lp.turned;
-  const bool norm = a.wq != nullptr;
-  float wq[8], wk[8], dwq[8], dwk[8];
+  const int gap = lp.off1 - lp.off0;
+  const int block = blockIdx.x;
+  const int kind = block < a.first_k ? 0 : (block < a.first_v ? 1 : 2);
+  const int b0 = kind == 0 ? 0 : (kind == 1 ? a.first_k : a.first_v);
+  const int b1 = kind == 0 ? a.first_k : (kind == 1 ? a.first_v : static_cast<int>(gridDim.x));
+  const RowView& in = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
+  const RowView& out = kind == 0 ? a.qo : (kind == 1 ? a.ko : a.vo);
+  const RowView& fwd = kind == 0 ? a.qx : a.kx;
+  const float* weight = kind == 0 ? a.wq : a.wk;
+  const bool norm = kind != 2 && weight != nullptr;
+  Vec8 w{}, dw{};
+  if (norm) w = load_weight(weight, lp.off0, lp.off1);
+  const uint32_t base = smem_u32(ring) + threadIdx.x * (kInter ? 16 : 8);
+
+  RowCursor<G> load;
+  load.heads = kind == 0 ? a.H : a.Hkv;
+  load.chunks = chunks_of(load.heads, a.chunk);
+  load.items = (static_cast<int64_t>(a.tokens) + G - 1) / G * load.chunks;
+  load.it = block - b0;
+  load.step = b1 - b0;
+  load.grp = grp;
+  RowCursor<G> work = load;
+  bool loading = load.settle(a), working = work.settle(a);
+  int filled = 0, done = 0;  // stages
+  auto fill = [&]() {
+    if (loading) {
+      const uint32_t st = base + filled % kBwdStages * kBwdStage;
+      const __nv_bfloat16* src = row_of(in, load.b, load.n, load.h) + lp.off0;
+      const __nv_bfloat16* xs = norm ? row_of(fwd, load.b, load.n, load.h) + lp.off0 : nullptr;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-  if (norm) {
-    load_weight(a.wq, lp.off0, lp.off1, wq);
-    load_weight(a.wk, lp.off0, lp.off1, wk);
-  }
-  const int heads = a.H + 2 * a.Hkv;
-  const int chunks = (heads + a.chunk - 1) / a.chunk;
-  const int64_t items = (static_cast<int64_t>(a.tokens) + G - 1) / G * chunks;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t t64 = it / chunks * G + grp;
-    if (t64 >= a.tokens) continue;  // whole lane groups; nothing below is block-wide
-    const int t = static_cast<int>(t64);
-    const int h0 = static_cast<int>(it % chunks) * a.chunk;
-    const int h1 = min(h0 + a.chunk, heads);
-    const int b = t / a.N, n = t - b * a.N;
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    load_angle(a, a.positions != nullptr ? __ldg(a.positions + t) : n, j, turned, j == 0, c, s);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = -s[e];  // the transpose of the rotation
-    for (int h = h0; h < h1; h += kR) {
-      Row8 r[kR], xr[kR];
-#pragma unroll
-      for (int i = 0; i < kR; ++i) {
-        const int hh = h + i;
-        if (hh >= h1) break;
-        const bool is_q = hh < a.H, is_v = hh >= a.H + a.Hkv;
-        const int hv = is_q ? hh : (is_v ? hh - a.H - a.Hkv : hh - a.H);
-        const RowView& v = is_q ? a.q : (is_v ? a.v : a.k);
-        if (v.p != nullptr) r[i] = load_row<kInter>(row_of(v, b, n, hv), lp.off0, lp.off1);
-        if (norm && !is_v)
-          xr[i] = load_row<kInter>(row_of(is_q ? a.qx : a.kx, b, n, hv), lp.off0, lp.off1);
+      for (int i = 0; i < kBwdRows; ++i) {
+        if (load.h + i >= load.h1) break;
+        copy_row<kInter>(st + i * 2 * 16 * kThreads, src + i * in.head, gap);
+        if (norm) copy_row<kInter>(st + (i * 2 + 1) * 16 * kThreads, xs + i * fwd.head, gap);
       }
-#pragma unroll
-      for (int i = 0; i < kR; ++i) {
-        const int hh = h + i;
-        if (hh >= h1) break;
-        const bool is_q = hh < a.H, is_v = hh >= a.H + a.Hkv;
-        const int hv = is_q ? hh : (is_v ? hh - a.H - a.Hkv : hh - a.H);
-        if (is_v && a.v.p == nullptr) continue;
-        if (!is_v) {
-          float g[8];
-          unpack(r[i], g);
-          turn<kInter>(g, c, s, turned);
-          if (norm) {
-            float x[8];
-            unpack(xr[i], x);
-            float ss = 0.f, ux = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              ss = fmaf(x[e], x[e], ss);
-              ux = fmaf(g[e] * (is_q ? wq[e] : wk[e]), x[e], ux);
-            }
-            ss = group_sum<L>(ss, mask);
-            ux = group_sum<L>(ux, mask);
-            const float rs = rsqrtf(ss * (1.f / D) + a.eps);
-            const float m = ux * rs * (1.f / D);  // mean(u x r)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float xh = x[e] * rs;
-              if (is_q) dwq[e] = fmaf(g[e], xh, dwq[e]);
-              else dwk[e] = fmaf(g[e], xh, dwk[e]);
-              g[e] = rs * (g[e] * (is_q ? wq[e] : wk[e]) - xh * m);
-            }
-          }
-          r[i] = pack(g);
-        }
-        store_row<kInter>(row_of(is_q ? a.qo : (is_v ? a.vo : a.ko), b, n, hv), lp.off0, lp.off1,
-                          r[i]);
-      }
+      loading = load.next(a);
     }
-  }
-  if (!norm) return;
-  __shared__ float part[G][2][D];
+    ++filled;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < kBwdStages - 1; ++i) fill();
+  Angles angles{};
+  int token = -1;
+  while (working) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 2) : "memory");
+    const uint32_t st = base + done % kBwdStages * kBwdStage;
+    if (kind != 2 && token != work.t) {
+      token = work.t;
+      angles = load_angles(a, a.positions != nullptr ? __ldg(a.positions + work.t) : work.n, j,
+                           turned, j == 0);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int at = e < 4 ? lp.off0 + e : lp.off1 + e - 4;
-    part[grp][0][at] = dwq[e];
-    part[grp][1][at] = dwk[e];
+      for (int e = 0; e < 2; ++e) angles.s[e] = make_float2(-angles.s[e].x, -angles.s[e].y);
+    }
+    fill();  // into the stage read one round ago
+    __nv_bfloat16* dst = row_of(out, work.b, work.n, work.h) + lp.off0;
+#pragma unroll
+    for (int i = 0; i < kBwdRows; ++i) {
+      if (work.h + i >= work.h1) break;
+      Row8 r = read_row<kInter>(st + i * 2 * 16 * kThreads);
+      if (kind != 2) {
+        Vec8 g = unpack(r);
+        turn<kInter>(g, angles, turned);
+        if (norm) {
+          const Vec8 x = unpack(read_row<kInter>(st + (i * 2 + 1) * 16 * kThreads));
+          Vec8 u;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u.v[e] = mul2(g.v[e], w.v[e]);
+          const float ss = group_sum<L>(dot(x, x), mask), ux = group_sum<L>(dot(u, x), mask);
+          const float rs = rsqrtf(ss * (1.f / D) + a.eps);
+          // dx = r u - x r^3 mean(u x)
+          const float k = -rs * rs * rs * (ux * (1.f / D));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dw.v[e] = fma2(mul2(g.v[e], make_float2(rs, rs)), x.v[e], dw.v[e]);
+            g.v[e] = fma2(x.v[e], make_float2(k, k), mul2(u.v[e], make_float2(rs, rs)));
+          }
+        }
+        r = pack(g);
+      }
+      store_row<kInter>(dst + i * out.head, gap, r);
+    }
+    ++done;
+    working = work.next(a);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (!norm) return;  // uniform over the block
+  __syncthreads();    // the ring becomes [G][D] sums
+  float* part = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int at = grp * D + (e < 2 ? lp.off0 + 2 * e : lp.off1 + 2 * (e - 2));
+    part[at] = dw.v[e].x;
+    part[at + 1] = dw.v[e].y;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kThreads) {
     float sum = 0.f;
 #pragma unroll
-    for (int g = 0; g < G; ++g) sum += part[g][i / D][i % D];
-    a.partial[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = sum;
+    for (int g = 0; g < G; ++g) sum += part[g * D + i];
+    a.partial[static_cast<int64_t>(block) * D + i] = sum;
   }
 }
 
-// dw[q or k][e] = sum over blocks: 32 columns a block, 32 row lanes, joined in a fixed order.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int blocks, int D,
-                                                       float* dwq, float* dwk) {
+// dw[q or k][e] = sum over the blocks [0, first_k) or [first_k, first_v): 32 columns a block, 32
+// row lanes, joined in a fixed order.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int first_k,
+                                                       int first_v, int D, float* dwq, float* dwk) {
   __shared__ float sm[32][33];
   begin_launch(true);
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const int col = blockIdx.x * 32 + x;
+  const bool of_k = blockIdx.x * 32 >= D;
+  const int col = blockIdx.x * 32 + x - (of_k ? D : 0);
   float sum = 0.f;
-  for (int r = y; r < blocks; r += 32) sum += partial[static_cast<int64_t>(r) * 2 * D + col];
+#pragma unroll 8
+  for (int r = (of_k ? first_k : 0) + y; r < (of_k ? first_v : first_k); r += 32)
+    sum += partial[static_cast<int64_t>(r) * D + col];
   sm[y][x] = sum;
   __syncthreads();
   if (y == 0) {
     float s = 0.f;
 #pragma unroll
     for (int r = 0; r < 32; ++r) s += sm[r][x];
-    (col < D ? dwq[col] : dwk[col - D]) = s;
+    (of_k ? dwk : dwq)[col] = s;
   }
 }
 
@@ -376,13 +499,14 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const double* inv_freq,
   table[p * 2 * half + half + f] = static_cast<float>(amplitude * sn);
 }
 
-// Heads of one work item.  A lane group that walks over many heads loads its token's angles and
-// weights once; few tokens need more groups to cover memory latency.
-int head_chunk(int64_t tokens, int heads, int groups_per_block) {
+// Heads of one work item, at most `most`.  A lane group that walks over many heads loads its
+// token's angles and weights once (forward, 16384 tokens of 48 heads: 65 us with 16, 63 with 32);
+// few tokens need more groups to cover memory latency.
+int head_chunk(int64_t tokens, int heads, int groups_per_block, int most) {
   // about 152 SMs x 8 blocks of lane groups before a group takes more than kRows heads
   const int64_t want = 152ll * 8 * groups_per_block;
   int chunk = kRows;
-  while (chunk < 16 && chunk < heads && tokens * ((heads + 2 * chunk - 1) / (2 * chunk)) >= want)
+  while (chunk < most && chunk < heads && tokens * ((heads + 2 * chunk - 1) / (2 * chunk)) >= want)
     chunk *= 2;
   return chunk;
 }
@@ -390,26 +514,40 @@ int head_chunk(int64_t tokens, int heads, int groups_per_block) {
 template <int D, bool kInter, bool kPaged>
 cudaError_t fwd_t(RopeArgs a, cudaStream_t s) {
   constexpr int G = kThreads / (D / 8);
-  const int heads = a.H + 2 * a.Hkv;
-  a.chunk = head_chunk(a.tokens, heads, G);
-  const dim3 grid((a.tokens + G - 1) / G, (heads + a.chunk - 1) / a.chunk);
+  a.chunk = head_chunk(a.tokens, a.H + 2 * a.Hkv, G, 32);
+  const dim3 grid((a.tokens + G - 1) / G, chunks_of(a.H, a.chunk) + 2 * chunks_of(a.Hkv, a.chunk));
   return launch_chained(rope_fwd_kernel<D, kInter, kPaged>, grid, kThreads, 0, s, a);
 }
 
 template <int D, bool kInter>
 cudaError_t bwd_t(RopeArgs a, float* dwq, float* dwk, cudaStream_t s) {
   constexpr int G = kThreads / (D / 8);
-  const int heads = a.H + 2 * a.Hkv;
-  a.chunk = head_chunk(a.tokens, heads, G);
-  const int64_t items = (static_cast<int64_t>(a.tokens) + G - 1) / G * ((heads + a.chunk - 1) / a.chunk);
-  const int blocks = static_cast<int>(items < kRopeBwdBlocks ? items : kRopeBwdBlocks);
-  if (blocks > 0) {
-    const cudaError_t e = launch_chained(rope_bwd_kernel<D, kInter>, blocks, kThreads, 0, s, a);
+  a.chunk = head_chunk(a.tokens, a.H + 2 * a.Hkv, G, 8);
+  const int64_t groups = (static_cast<int64_t>(a.tokens) + G - 1) / G;
+  const int64_t items[3] = {groups * chunks_of(a.H, a.chunk), groups * chunks_of(a.Hkv, a.chunk),
+                            a.v.p != nullptr ? groups * chunks_of(a.Hkv, a.chunk) : 0};
+  // blocks in proportion to the bytes of a kind's rows (with norms Q and K rows read x too)
+  const double cost = a.wq != nullptr ? 3 : 2;
+  const double bytes[3] = {cost * a.H, cost * a.Hkv, a.v.p != nullptr ? 2.0 * a.Hkv : 0.0};
+  const double all = bytes[0] + bytes[1] + bytes[2];
+  int blocks[3];
+  for (int i = 0; i < 3; ++i) {
+    int64_t n = static_cast<int64_t>(kRopeBwdBlocks * bytes[i] / all);
+    if (n < 1) n = 1;
+    blocks[i] = static_cast<int>(n < items[i] ? n : items[i]);
+  }
+  a.first_k = blocks[0];
+  a.first_v = blocks[0] + blocks[1];
+  const int grid = a.first_v + blocks[2];
+  if (grid > 0) {
+    cudaError_t e = ensure_smem_limit<rope_bwd_kernel<D, kInter>>(kBwdSmem);
+    if (e != cudaSuccess) return e;
+    e = launch_chained(rope_bwd_kernel<D, kInter>, grid, kThreads, kBwdSmem, s, a);
     if (e != cudaSuccess) return e;
   }
   if (a.wq == nullptr) return cudaSuccess;
   return launch_chained(rope_dw_kernel, 2 * D / 32, 1024, 0, s, static_cast<const float*>(a.partial),
-                        blocks, D, dwq, dwk);
+                        a.first_k, a.first_v, D, dwq, dwk);
 }
 
 }  // namespace

@@ -305,7 +305,7 @@ fa_status fa_qk_norm_rope_fwd(const fa_view in[3], const fa_view out[3],
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
   if (d != 64 && d != 128) return 0;
-  return static_cast<size_t>(fa::kRopeBwdBlocks) * 2 * d * sizeof(float);
+  return static_cast<size_t>(fa::kRopeBwdBlocks + 2) * d * sizeof(float);
 }
 
 fa_status fa_qk_norm_rope_bwd(const fa_view grad[3], const fa_view x[2], const fa_view out[3],
