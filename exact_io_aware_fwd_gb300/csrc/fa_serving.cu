@@ -101,8 +101,12 @@ bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int H
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query rows per key/value head above which a list goes to the tensor-core kernel.
-constexpr long long kMmaRows = 32;
+// Query rows per key/value head above which a list goes to the tensor-core kernel.  At d = 128 the
+// other kernel reads the keys once per 16 rows: 16 sequences of 8192 keys take it 94 us with 16
+// rows and 154 with 24, the tensor-core kernel 99 and 100.  At d = 64 a tile's softmax outweighs
+// its copies and the tensor-core kernel needs 84 to 86 us from 4 rows to 32, the other one 56 with
+// 16 and 83 with 32.
+constexpr long long mma_rows(int d) { return d == 64 ? 32 : 16; }
 
 // Workspace of a paged call: the spans and slots of each list, then (joined lists) row buffers.
 // Which kernel a list takes is decided by max_q; with few rows in all it cannot be the
@@ -114,7 +118,7 @@ PagedWorkspace paged_workspace(const int (&count)[2], int lists, int total, int 
   PagedWorkspace w{};
   size_t at = 0;
   size_t slots = static_cast<size_t>(fa::kPagedCtas) * fa::kPagedWarps * 2 * fa::kPagedRows * (d + 2) * 4;
-  if (static_cast<long long>(total) * (H / Hkv) > kMmaRows) {
+  if (static_cast<long long>(total) * (H / Hkv) > mma_rows(d)) {
     const size_t mma = static_cast<size_t>(fa::kPagedCtas) * 2 * fa::kPagedMmaRows * (d + 2) * 4;
     if (mma > slots) slots = mma;
   }
@@ -171,7 +175,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     // query rows of an entry: at most those of max_q tokens; of a group, its share of the batch
     const long long tokens = i == 0 && max_q < total ? max_q : total;
     const long long rows = (i == 0 ? tokens : (total + count[i] - 1) / count[i]) * (H / Hkv);
-    mma[i] = rows > kMmaRows;
+    mma[i] = rows > mma_rows(d);
     // row tiles over all entries x heads x key tiles: the units of a launch, which fit 32 bits
     const long long keys = i == 0 ? max_kv : prefix->max_len;
     units[i] = Hkv * static_cast<long long>(fa::row_tiles_bound(

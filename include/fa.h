@@ -341,8 +341,7 @@ fa_status fa_kv_append(const fa_view in[3], const fa_view* q_out, const fa_paged
  * no key gets O = 0, LSE = -inf.  max_q, max_kv: at least the most new tokens and keys of any
  * sequence (tokens and keys beyond them are not computed, and FA_ERR_INDEX is recorded).
  * H % Hkv == 0, H / Hkv <= 128.  FA_ERR_UNSUPPORTED where Hkv (total H / Hkv / 16 + B)
- * (max_kv / 16 + 1) does not fit 31 bits (with at most 32 rows max_q H / Hkv; else with 256 and
- * 128 for the 16s).
+ * (max_kv / 16 + 1) does not fit 31 bits (the most units of work a launch is split into).
  * The keys are split over the whole GPU, partial results joined in a fixed order: the same
  * inputs give bit-identical outputs.  V of a key that some query of the same tile may see must
  * be finite, as in fa_fwd; cache rows past a sequence's length may hold anything.

@@ -141,6 +141,22 @@ def test_paged_many_ragged_sequences():
     run_paged(nq, lens, 4, 2, 64, 16, True, seed=10)
 
 
+def test_paged_more_sequences_than_threads():
+    """The scan over the sequences takes several rounds (256 and 384 entries at a time)."""
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 60, 900).tolist()
+    lens[700] = 3000
+    run_paged([1] * 900, lens, 2, 1, 64, 16, True, seed=13)
+    nq = rng.integers(0, 3, 900).tolist()
+    nq[3] = 40
+    run_paged(nq, lens, 2, 1, 128, 16, True, seed=14)
+
+
+def test_paged_128_heads_of_one_key_head():
+    run_paged([1, 3], [300, 900], 128, 1, 64, 32, True, seed=15)
+    run_paged([1, 1], [30, 2000], 128, 1, 128, 16, False, seed=16)
+
+
 @pytest.mark.parametrize("scale,sigma", [(0.0, 1.0), (1.5, 1.0), (None, 4.0)])
 def test_paged_scales(scale, sigma):
     run_paged([1, 2], [700, 70], 4, 2, 64, 16, True, seed=4, scale=scale, sigma=sigma)
@@ -273,6 +289,55 @@ def test_paged_streams_and_graphs():
     ref = fa.fa_fwd_paged(q, k, v, table, lens)
     assert all(torch.equal(a, b) for a, b in zip(ref, outs[0][0]))
     assert fa.fa_get_error() == fa.FA_OK
+
+
+def test_calls_in_a_row_wait_for_each_other():
+    """Launches overlap the end of the one before; every call still sees what was written ahead of
+    it on the stream: lengths that a kernel in between advances, keys that the call before appended,
+    a workspace and outputs that the call before used."""
+    B, H, Hkv, d, page, steps = 6, 8, 2, 64, 16, 60
+    k = torch.zeros(B * 40, Hkv, page, d, dtype=BF16, device=DEV)
+    v = torch.zeros_like(k)
+    table = torch.arange(B * 40, device=DEV).view(B, 40).to(torch.int32)
+    new = torch.randn(steps, B, H + 2 * Hkv, d, device=DEV).to(BF16)
+    lens = i32([0, 100, 200, 300, 400, 500])
+    q = torch.empty(B, H, d, dtype=BF16, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(H, B, device=DEV)
+    ws = torch.empty(fa.fa_fwd_paged_workspace_size(B, B, H, Hkv, d), dtype=torch.uint8, device=DEV)
+
+    def run(wait):
+        k.zero_(), v.zero_()
+        ln, outs = lens.clone(), []
+        for s in range(steps):
+            ln += 1
+            x = new[s].split([H, Hkv, Hkv], dim=1)
+            fa.fa_kv_append(*x, k, v, table, ln, q_out=q)
+            wait()
+            fa.fa_fwd_paged(q, k, v, table, ln, out=out, lse=lse, workspace=ws)
+            wait()
+            outs.append((out.clone(), lse.clone()))
+        return outs
+
+    waited = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(waited, run(lambda: None)):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert fa.fa_get_error() == fa.FA_OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tensor_core_kernel_times_out_then_recovers(d, monkeypatch):
+    """Waits of the pipeline that run out end the kernel, the call reports it, and the next call is
+    right again (no fault, nothing left behind)."""
+    args = ([200, 90], [1500, 700], 4, 2, d, 32, True)
+    cache = Cache(args[1], 2, d, 32, seed=3)
+    q = torch.randn(290, 4, d, device=DEV).to(BF16)
+    monkeypatch.setenv("FA_WAIT_TIMEOUT_US", "1")
+    fa.fa_fwd_paged(q, *cache.dev(), cu_seqlens=i32([0, 200, 290]), max_q=200, causal=True)
+    status = fa.fa_get_error()
+    monkeypatch.delenv("FA_WAIT_TIMEOUT_US")
+    assert status == fa.FA_ERR_TIMEOUT, fa.fa_status_string(status)
+    run_paged(*args, seed=17)
 
 
 def test_paged_empty_and_refusals():
