@@ -143,7 +143,7 @@ fa_status check_paged_sizes(int B, int total, int H, int Hkv, int d) {
   if (B <= 0 || total < 0 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (H / Hkv > 128) return FA_ERR_UNSUPPORTED;
   // rows of every tile and the index of a (token, head) row fit 32 bits
-  if ((static_cast<long long>(total) + B) * H + 128LL * B > kMaxInt) return FA_ERR_INVALID_ARG;
+  if ((static_cast<long long>(total) + B) * H + 256LL * B > kMaxInt) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -167,7 +167,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   const int count[2] = {B, prefix != nullptr ? prefix->groups : 0};
   // pages x heads is a tensor-map coordinate
   if (static_cast<long long>(cache->num_pages) * Hkv > kMaxInt) return FA_ERR_INVALID_ARG;
-  if (lists == 2 && (static_cast<long long>(total) + count[1]) * H + 128LL * count[1] > kMaxInt)
+  if (lists == 2 && (static_cast<long long>(total) + count[1]) * H + 256LL * count[1] > kMaxInt)
     return FA_ERR_INVALID_ARG;
   bool mma[2];
   long long units[2];
@@ -421,7 +421,7 @@ fa_status fa_fwd_paged(const void* Q, const fa_paged_kv* cache, void* O, float* 
 
 size_t fa_fwd_shared_prefix_workspace_size(int B, int groups, int total, int H, int Hkv, int d) {
   if (check_paged_sizes(B, total, H, Hkv, d) != FA_OK || groups < 1) return 0;
-  if ((static_cast<long long>(total) + groups) * H + 128LL * groups > kMaxInt) return 0;
+  if ((static_cast<long long>(total) + groups) * H + 256LL * groups > kMaxInt) return 0;
   const int count[2] = {B, groups};
   return paged_workspace(count, 2, total, H, Hkv, d).total;
 }
