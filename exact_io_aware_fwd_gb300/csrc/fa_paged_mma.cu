@@ -48,10 +48,13 @@ template <int D>
 struct MmaLayout {
   static constexpr uint32_t kTile = 128u * D * 2u;
   static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kK = kQ + 2 * kTile;
+  // K and V in front of Q: 3% faster than the other way round (231 -> 223 us for 2 x 512 tokens over
+  // 16384 keys).  192 KB and what is static fit the SM's 196 KB setting; a few KB more, such as a
+  // gap between the buffers, take the next one, leave less L1 and cost 3%.
+  static constexpr uint32_t kK = 0;
   static constexpr uint32_t kV = kK + kStages * kTile;
-  static constexpr uint32_t kBytes = kV + kStages * kTile;
+  static constexpr uint32_t kQ = kV + kStages * kTile;
+  static constexpr uint32_t kBytes = kQ + 2 * kTile;
   static constexpr uint32_t kColS0 = 0, kColO0 = 256;
   static constexpr uint32_t kTmemCols = 512;
 };
