@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
   const Share& sh = shares[warp];
   const uint32_t ring = smem_u32(smem) + warp * (S * L::kStage);
 
-  if (sh.u0 < sh.u1) {
-    Walk<R, KT> walk(sh);
+  if (sh.u0 < sh.u1 && sh.b >= 0) {
+    Walk<R, KT> walk(a, sh);
     Piece next_piece;
     bool more = walk.next(a, next_piece);
     Source src = source_of(a, walk, next_piece);
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
     const PartialLayout& p = a.part[li];
     const int2 span = p.spans[where[li]];
     // a launch that gave up leaves no span: nothing out of range is read
-    if (span.x < 0 || span.y < 1 || span.x + span.y > p.workers) continue;
+    if (span.x < 0 || span.x >= p.workers || span.y < 1 || span.y > p.workers - span.x) continue;
     const bool one = span.y == 1;
     if (one && a.rowbuf[li] == nullptr) {
       done = true;

@@ -68,6 +68,10 @@ __host__ __device__ inline void token_bounds(const int32_t* cu, int b, int total
   start = s0;
   n = s1 - s0;
 }
+// Offsets that ascend inside [0, total]: then no two entries share a token.
+__host__ __device__ inline bool offsets_ok(const int32_t* cu, int b, int total) {
+  return cu == nullptr || (cu[b] >= 0 && cu[b] <= cu[b + 1] && cu[b + 1] <= total);
+}
 // Sequence whose tokens include t: the last b with cu[b] <= t (empty sequences skipped), or -1
 // when t lies behind cu[B] or before cu[0].
 __host__ __device__ inline int token_sequence(const int32_t* cu, int B, int t) {

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) {
       // ================= the CTA's pieces
       if (lane == 0) {
-        Walk<R, KT> walk(sh);
+        Walk<R, KT> walk(a, sh);
         const Entry& e = walk.e;
         Piece piece;
         for (int i = 0;; ++i) {

@@ -197,12 +197,20 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
     if (seq < 0) return;  // behind the last sequence
     int start, count;
     token_bounds(a.cu, seq, a.tokens, start, count);
+    if (t < start || t >= start + count) {  // offsets that do not ascend
+      if (j == 0) atomicCAS(a.status, 0, kErrIndex);
+      return;
+    }
     const int64_t limit = static_cast<int64_t>(a.max_pages) << a.page_shift;
     const int len = __ldg(a.kv_lens + seq);
-    const int key = len - count + (t - start);
+    const int key = max(len, 0) - count + (t - start);
     b = 0;
     n = t;
-    pos = key + (a.pos_offset != nullptr ? __ldg(a.pos_offset + seq) : 0);
+    pos = key;
+    if (a.pos_offset != nullptr) {  // a sum past 32 bits is past the table as well
+      const int64_t p = static_cast<int64_t>(key) + __ldg(a.pos_offset + seq);
+      pos = p < 0 ? -1 : (p < a.n_pos ? static_cast<int>(p) : a.n_pos);
+    }
     if (key >= 0) {
       const int page =
           key < limit ? resolve_page(a.block_table + static_cast<int64_t>(seq) * a.max_pages,

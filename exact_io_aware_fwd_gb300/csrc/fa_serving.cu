@@ -15,6 +15,7 @@ using fa::aligned_to;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxInt = 0x7fffffff;
+constexpr int kMaxKeys = kMaxInt - 255;  // keys rounded up to whole tiles fit 32 bits
 
 // A view that rows of 16-byte pieces can be read from or written to; the stride of a dimension
 // of one element does not matter.
@@ -230,6 +231,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     l.table = i == 0 ? cache->block_table : prefix->table;
     l.max_pages = i == 0 ? cache->max_pages : prefix->max_pages;
     l.max_len = i == 0 ? max_kv : prefix->max_len;
+    if (l.max_len > kMaxKeys) l.max_len = kMaxKeys;
     l.max_q = i == 0 ? max_q : kMaxInt;
     l.group_cu = i == 0 ? nullptr : prefix->group_cu;
     l.causal = i == 0 && causal ? 1 : 0;

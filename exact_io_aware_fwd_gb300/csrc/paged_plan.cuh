@@ -41,7 +41,9 @@ __device__ __forceinline__ int tiles_of(const Entry& e, int causal, int G, int r
 template <int R, int KT>
 __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b, bool report) {
   Entry e;
+  bool ok;
   if (l.group_cu != nullptr) {
+    ok = offsets_ok(l.group_cu, b, a.B);
     int s0 = __ldg(l.group_cu + b), s1 = __ldg(l.group_cu + b + 1);
     s0 = min(max(s0, 0), a.B);
     s1 = min(max(s1, s0), a.B);
@@ -51,6 +53,7 @@ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, 
     e.start = t0;
     e.n = t1 - t0;
   } else {
+    ok = offsets_ok(a.cu, b, a.total);
     token_bounds(a.cu, b, a.total, e.start, e.n);
   }
   const int64_t pages = static_cast<int64_t>(l.max_pages) << a.page_shift;
@@ -58,7 +61,7 @@ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, 
   const int len = __ldg(l.lens + b);
   e.len = min(max(len, 0), cap);
   e.nc = min(e.n, l.max_q);
-  if (report && (e.len != len || e.nc != e.n)) atomicCAS(a.status, 0, kErrIndex);
+  if (report && (!ok || e.len != len || e.nc != e.n)) atomicCAS(a.status, 0, kErrIndex);
   e.rt = (e.nc * a.G + R - 1) / R;
   if (l.causal && e.n > 1) {
     e.tiles = 0;
@@ -86,7 +89,8 @@ struct Share {
   bool direct;    // a unit is a whole segment
   int worker;     // this worker and its units (none: u0 == u1)
   int u0, u1;
-  int b, off;     // entry of unit u1 - 1, and its units before u1
+  int b, off;     // entry of unit u1 - 1, and its units before u1; -1: none (offsets that
+                  // overlap, whose units do not fit 32 bits)
   Entry e;        // that entry
 };
 
@@ -139,6 +143,7 @@ __device__ void make_shares(const PagedArgs& a, Share* shares) {
     s.worker = c;
     s.u0 = c < C ? share_begin(W, C, c) : 0;
     s.u1 = c < C ? share_begin(W, C, c + 1) : 0;
+    s.b = -1;
   }
   // entry of each worker's unit u1 - 1: scan the entries kThreads at a time
   int before = 0;
@@ -191,50 +196,58 @@ struct Piece {
 };
 
 // Walks the pieces of a worker's share, last to first; e is the entry b of the current piece.
+// Only the last unit's row tile is searched for: the ones before it follow by counting down.
 template <int R, int KT>
 struct Walk {
   int u0, u1;   // what is left of the share
-  int within;   // units of entry b before u1
-  int b;
+  int b, hk, r; // the next piece's entry, key/value head and row tile (r < 0: the head before)
+  int te;       // end of the first piece's key tiles; then -1: all of the row tile's
   bool direct;
   Entry e;
 
-  __device__ explicit Walk(const Share& sh)
-      : u0(sh.u0), u1(sh.u1), within(sh.off), b(sh.b), direct(sh.direct), e(sh.e) {}
+  __device__ Walk(const PagedArgs& a, const Share& sh)
+      : u0(sh.u0), u1(sh.b < 0 ? sh.u0 : sh.u1), b(sh.b), hk(0), r(0), te(-1), direct(sh.direct),
+        e(sh.e) {
+    if (u0 >= u1) return;
+    const int per_head = direct ? e.rt : e.tiles;
+    hk = (sh.off - 1) / per_head;
+    int rem = sh.off - 1 - hk * per_head;
+    if (direct) {
+      r = rem;
+      return;
+    }
+    for (int n; rem >= (n = tiles_of<R, KT>(e, a.list.causal, a.G, r)); ++r) rem -= n;
+    te = rem + 1;
+  }
   __device__ bool next(const PagedArgs& a, Piece& p) {
     if (u0 >= u1) return false;
-    while (within <= 0) {          // the entry before with tokens
-      if (--b < 0) return false;   // cannot happen while u1 > 0
-      e = entry_of<R, KT>(a.list, a, b, false);
-      within = (direct ? e.rt : e.tiles) * a.Hkv;
+    if (r < 0) {
+      if (--hk < 0) {
+        do {                           // the entry before with tokens
+          if (--b < 0) return false;   // cannot happen while u1 > u0
+          e = entry_of<R, KT>(a.list, a, b, false);
+        } while (e.rt == 0);
+        hk = a.Hkv - 1;
+      }
+      r = e.rt - 1;
     }
-    const int per_head = direct ? e.rt : e.tiles, x = within - 1;
-    p.hk = x / per_head;
-    int rem = x - p.hk * per_head;
+    p.hk = hk;
+    p.r = r--;
+    p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
     if (direct) {
-      p.r = rem;
-      p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
       p.ta = 0;
       p.te = p.tiles;
       p.whole = true;
       p.unit = --u1;
-      --within;
       return true;
     }
-    p.r = 0;
-    p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, 0);
-    while (rem >= p.tiles) {
-      rem -= p.tiles;
-      ++p.r;
-      p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
-    }
-    p.te = rem + 1;
+    p.te = te >= 0 ? te : p.tiles;
+    te = -1;
     p.unit = u1 - p.te;
     const int take = min(p.te, u1 - u0);
     p.ta = p.te - take;
     p.whole = take == p.tiles;
     u1 -= take;
-    within -= take;
     return true;
   }
 };

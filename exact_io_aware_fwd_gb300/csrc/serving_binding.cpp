@@ -173,10 +173,9 @@ at::Tensor workspace(const at::Tensor* given, size_t need, at::Device dev, size_
   return *given;
 }
 
-// The stream of a call: a handle, or None for the device's current one.
-void* stream_of(PyObject* o, at::Device dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  return reinterpret_cast<void*>(static_cast<intptr_t>(integer(o)));
+// Calls launch on the device's current stream, on which their outputs are allocated too.
+void* stream_of(at::Device dev) {
+  return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
 }
 
 fa_qk_transform transform(PyObject* table_o, PyObject* interleaved, PyObject* wq_o, PyObject* wk_o,
@@ -251,7 +250,7 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded<kBody>(a);
 }
 
-// ---- q, k, v, table, positions, interleaved, q_weight, k_weight, eps, q_out, k_out, v_out, stream
+// ---- q, k, v, table, positions, interleaved, q_weight, k_weight, eps, q_out, k_out, v_out
 PyObject* norm_rope_fwd(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
   const at::Tensor& k = tensor(a[1], "k");
@@ -283,13 +282,13 @@ PyObject* norm_rope_fwd(PyObject* const* a) {
   if (v != nullptr)
     vo = own_rows(tensor_or_none(a[11], "v_out"), shape(Hkv), out_order, dev, "v_out", out[2]);
   check(p_rope_fwd(in, out, pos, dim32(B), dim32(N), dim32(H), dim32(Hkv), dim32(d), &t,
-                   stream_of(a[12], dev)),
+                   stream_of(dev)),
         "fa_qk_norm_rope_fwd");
   return wrap_all({qo, ko, vo});
 }
 
 // ---- dq, dk, dv, q, k, table, positions, interleaved, q_weight, k_weight, eps, dq_in, dk_in,
-//      dv_in, workspace, stream
+//      dv_in, workspace
 PyObject* norm_rope_bwd(PyObject* const* a) {
   const at::Tensor& dq = tensor(a[0], "dq");
   const at::Tensor& dk = tensor(a[1], "dk");
@@ -352,7 +351,7 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
   check(p_rope_bwd(grad, norm ? x : nullptr, out, norm ? dwq.data_ptr<float>() : nullptr,
                    norm ? dwk.data_ptr<float>() : nullptr, pos, B > 0 ? dim32(B) : 1,
                    empty ? 0 : dim32(N), dim32(H), dim32(Hkv), dim32(d), &t,
-                   norm ? ws.data_ptr() : nullptr, ws_bytes, stream_of(a[15], dev)),
+                   norm ? ws.data_ptr() : nullptr, ws_bytes, stream_of(dev)),
         "fa_qk_norm_rope_bwd");
   return wrap_all({out_t[0], out_t[1], out_t[2], dwq, dwk});
 }
@@ -391,7 +390,7 @@ const int32_t* token_offsets(PyObject* o, const Cache& c, int64_t total, at::Dev
 }
 
 // ---- q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, pos_offset, table,
-//      interleaved, q_weight, k_weight, eps, q_out, stream
+//      interleaved, q_weight, k_weight, eps, q_out
 PyObject* kv_append(PyObject* const* a) {
   const at::Tensor* q = tensor_or_none(a[0], "q");
   const at::Tensor& k = tensor(a[1], "k");
@@ -418,7 +417,7 @@ PyObject* kv_append(PyObject* const* a) {
     in[1] = rows(k, kNH, dev, "k");
     in[2] = rows(v, kNH, dev, "v");
     check(p_append(in, &out, &c.kv, cu, offset, dim32(c.B), dim32(total), dim32(H), dim32(c.Hkv),
-                   dim32(c.d), &t, stream_of(a[15], dev)),
+                   dim32(c.d), &t, stream_of(dev)),
           "fa_kv_append");
   } else if (q != nullptr) {
     qo = fresh({0, H, c.d}, at::kBFloat16, dev);
@@ -427,7 +426,7 @@ PyObject* kv_append(PyObject* const* a) {
 }
 
 // ---- q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q, max_kv, causal, scale, out,
-//      lse, workspace, stream; with a prefix: prefix_table, prefix_lens, group_cu, max_prefix too
+//      lse, workspace; with a prefix: prefix_table, prefix_lens, group_cu, max_prefix too
 template <bool kPrefix>
 PyObject* attend(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
@@ -449,15 +448,15 @@ PyObject* attend(PyObject* const* a) {
   const float scale = a[9] == Py_None ? -1.f : real(a[9]);
   fa_prefix pre{};
   if (kPrefix) {
-    const at::Tensor& table = tensor(a[14], "prefix_table");
+    const at::Tensor& table = tensor(a[13], "prefix_table");
     if (table.dim() != 2) refuse("prefix_table must be [groups, pages]");
     const int64_t groups = table.size(0), pages = table.size(1), most = pages * c.page_size;
     pre.table = ints(&table, {groups, pages}, dev, "prefix_table");
     pre.max_pages = dim32(pages);
-    pre.lens = ints(&tensor(a[15], "prefix_lens"), {groups}, dev, "prefix_lens");
-    pre.group_cu = ints(&tensor(a[16], "group_cu"), {groups + 1}, dev, "group_cu");
+    pre.lens = ints(&tensor(a[14], "prefix_lens"), {groups}, dev, "prefix_lens");
+    pre.group_cu = ints(&tensor(a[15], "group_cu"), {groups + 1}, dev, "group_cu");
     pre.groups = dim32(groups);
-    pre.max_len = a[17] != Py_None ? int32_of(a[17], "max_prefix")
+    pre.max_len = a[16] != Py_None ? int32_of(a[16], "max_prefix")
                                    : static_cast<int>(most < INT32_MAX ? most : INT32_MAX);
   }
   const c10::cuda::OptionalCUDAGuard guard(dev);
@@ -469,7 +468,7 @@ PyObject* attend(PyObject* const* a) {
       workspace(tensor_or_none(a[12], "workspace"),
                 kPrefix ? p_prefix_ws(B, pre.groups, T, h, hkv, d) : p_paged_ws(B, T, h, hkv, d),
                 dev, ws_bytes);
-  void* stream = stream_of(a[13], dev);
+  void* stream = stream_of(dev);
   if (kPrefix)
     check(p_prefix(qp, &c.kv, &pre, out.data_ptr(), lse.data_ptr<float>(), cu, B, max_q, max_kv, T,
                    h, hkv, d, causal, scale, ws.data_ptr(), ws_bytes, stream),
@@ -501,11 +500,11 @@ PyObject* bind(PyObject* const* a) {
 #define FA_METHOD(name, body, args) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<body, args>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FA_METHOD("bind", bind, 9),
-                         FA_METHOD("norm_rope_fwd", norm_rope_fwd, 13),
-                         FA_METHOD("norm_rope_bwd", norm_rope_bwd, 16),
-                         FA_METHOD("kv_append", kv_append, 16),
-                         FA_METHOD("fwd_paged", attend<false>, 14),
-                         FA_METHOD("fwd_shared_prefix", attend<true>, 18),
+                         FA_METHOD("norm_rope_fwd", norm_rope_fwd, 12),
+                         FA_METHOD("norm_rope_bwd", norm_rope_bwd, 15),
+                         FA_METHOD("kv_append", kv_append, 15),
+                         FA_METHOD("fwd_paged", attend<false>, 13),
+                         FA_METHOD("fwd_shared_prefix", attend<true>, 17),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

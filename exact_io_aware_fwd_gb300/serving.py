@@ -4,8 +4,8 @@ key/value cache, and the attention that reads it (the calls of include/fa.h with
 As in binding.py only argument checks and marshalling happen on the way to the library; here they
 are compiled (csrc/serving_binding.cpp), because the smallest of these calls are a few
 microseconds of kernel.  Calls launch on the tensors' device, on its current stream or on
-``stream``; outputs and workspaces allocated for another stream than the current one are recorded
-on it.
+``stream``; what a call allocates is allocated on the stream it launches on, and outputs are
+recorded on the current one as well.
 """
 
 from __future__ import annotations
@@ -46,16 +46,19 @@ def _binding():
     return _ext
 
 
-def _keep(stream, *tensors):
-    """Records tensors used on a given stream that is not the current one of their device."""
-    for t in tensors:
-        if t is not None and stream != torch.cuda.current_stream(t.device):
-            t.record_stream(stream)
-
-
-def _bytes_on(like, nbytes):
-    """A workspace for a call on a given stream (recorded on it, which the binding's is not)."""
-    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=like.device)
+def _on(stream, call, q, *args):
+    """The binding's call with `stream` as the current one.  A block that the allocator hands out
+    is free in the order of the stream it belongs to, so outputs and workspaces have to belong to
+    the stream that writes them."""
+    if not isinstance(q, torch.Tensor) or q.device != stream.device:
+        raise ValueError("stream must be one of the tensors' device")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(q, *args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and caller != stream:
+            t.record_stream(caller)
+    return out
 
 
 # ------------------------------------------------------------------------------------------ rotary
@@ -130,11 +133,9 @@ def fa_qk_norm_rope_fwd(q, k, v=None, table=None, positions=None, interleaved=Fa
     ext = _ext or _binding()
     if stream is None:
         return ext.norm_rope_fwd(q, k, v, table, positions, interleaved, q_weight, k_weight, eps,
-                                 q_out, k_out, v_out, None)
-    out = ext.norm_rope_fwd(q, k, v, table, positions, interleaved, q_weight, k_weight, eps,
-                            q_out, k_out, v_out, stream.cuda_stream)
-    _keep(stream, *out)
-    return out
+                                 q_out, k_out, v_out)
+    return _on(stream, ext.norm_rope_fwd, q, k, v, table, positions, interleaved, q_weight,
+               k_weight, eps, q_out, k_out, v_out)
 
 
 def fa_qk_norm_rope_bwd_workspace_size(d) -> int:
@@ -153,13 +154,9 @@ def fa_qk_norm_rope_bwd(dq, dk, dv=None, q=None, k=None, table=None, positions=N
     ext = _ext or _binding()
     if stream is None:
         return ext.norm_rope_bwd(dq, dk, dv, q, k, table, positions, interleaved, q_weight,
-                                 k_weight, eps, dq_in, dk_in, dv_in, workspace, None)
-    if workspace is None and q_weight is not None:
-        workspace = _bytes_on(dq, fa_qk_norm_rope_bwd_workspace_size(dq.shape[-1]))
-    out = ext.norm_rope_bwd(dq, dk, dv, q, k, table, positions, interleaved, q_weight, k_weight,
-                            eps, dq_in, dk_in, dv_in, workspace, stream.cuda_stream)
-    _keep(stream, *out, workspace)
-    return out
+                                 k_weight, eps, dq_in, dk_in, dv_in, workspace)
+    return _on(stream, ext.norm_rope_bwd, dq, dk, dv, q, k, table, positions, interleaved,
+               q_weight, k_weight, eps, dq_in, dk_in, dv_in, workspace)
 
 
 # ------------------------------------------------------------------------------------- paged cache
@@ -172,12 +169,12 @@ def fa_kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=Non
     offsets, default one token per sequence; pos_offset: int32 [B] added to the rotation's
     positions.  Returns the transformed q (None without q)."""
     ext = _ext or _binding()
-    out = ext.kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, pos_offset,
-                        table, interleaved, q_weight, k_weight, eps, q_out,
-                        None if stream is None else stream.cuda_stream)
-    if stream is not None:
-        _keep(stream, out)
-    return out
+    if stream is None:
+        return ext.kv_append(q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens,
+                             pos_offset, table, interleaved, q_weight, k_weight, eps, q_out)
+    return _on(stream, lambda kk, *rest: ext.kv_append(q, kk, *rest), k, v, k_cache, v_cache,
+               block_table, kv_lens, cu_seqlens, pos_offset, table, interleaved, q_weight,
+               k_weight, eps, q_out)
 
 
 def fa_fwd_paged_workspace_size(B, total, H, Hkv, d) -> int:
@@ -201,14 +198,9 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, max
     ext = _ext or _binding()
     if stream is None:
         return ext.fwd_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q, max_kv,
-                             causal, scale, out, lse, workspace, None)
-    if workspace is None:
-        workspace = _bytes_on(q, fa_fwd_paged_workspace_size(
-            block_table.shape[0], *q.shape[:2], *k_cache.shape[1::2]))
-    result = ext.fwd_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q, max_kv,
-                           causal, scale, out, lse, workspace, stream.cuda_stream)
-    _keep(stream, *result, workspace)
-    return result
+                             causal, scale, out, lse, workspace)
+    return _on(stream, ext.fwd_paged, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q,
+               max_kv, causal, scale, out, lse, workspace)
 
 
 def fa_fwd_shared_prefix(q, k_cache, v_cache, block_table, kv_lens, prefix_table, prefix_lens,
@@ -221,14 +213,8 @@ def fa_fwd_shared_prefix(q, k_cache, v_cache, block_table, kv_lens, prefix_table
     ext = _ext or _binding()
     if stream is None:
         return ext.fwd_shared_prefix(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q,
-                                     max_kv, causal, scale, out, lse, workspace, None,
-                                     prefix_table, prefix_lens, group_cu, max_prefix)
-    if workspace is None:
-        workspace = _bytes_on(q, fa_fwd_shared_prefix_workspace_size(
-            block_table.shape[0], prefix_table.shape[0], *q.shape[:2], *k_cache.shape[1::2]))
-    result = ext.fwd_shared_prefix(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q,
-                                   max_kv, causal, scale, out, lse, workspace,
-                                   stream.cuda_stream, prefix_table, prefix_lens, group_cu,
-                                   max_prefix)
-    _keep(stream, *result, workspace)
-    return result
+                                     max_kv, causal, scale, out, lse, workspace, prefix_table,
+                                     prefix_lens, group_cu, max_prefix)
+    return _on(stream, ext.fwd_shared_prefix, q, k_cache, v_cache, block_table, kv_lens,
+               cu_seqlens, max_q, max_kv, causal, scale, out, lse, workspace, prefix_table,
+               prefix_lens, group_cu, max_prefix)

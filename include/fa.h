@@ -310,8 +310,9 @@ fa_status fa_qk_norm_rope_bwd(const fa_view grad[3], const fa_view x[2], const f
  * Tokens behind cu_seqlens[B] are left as they were.
  * What the library reads from device memory is checked on the device: a page outside
  * [0, num_pages) is neither read nor written (its keys and values count as zeros), lengths are
- * clamped to [0, max_pages * page_size] (and the bounds a call takes), and FA_ERR_INDEX is
- * recorded.
+ * clamped to [0, max_pages * page_size] (and the bounds a call takes, and 2^31 - 256), and
+ * FA_ERR_INDEX is recorded.  With offsets that do not ascend inside [0, total] (recorded by the
+ * attention calls) results are undefined, but nothing outside the call's tensors is touched.
  */
 typedef struct {
   void* k_cache;

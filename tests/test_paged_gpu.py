@@ -340,6 +340,80 @@ def test_tensor_core_kernel_times_out_then_recovers(d, monkeypatch):
     run_paged(*args, seed=17)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_join_reads_nothing_out_of_range_after_a_launch_that_gave_up(d, monkeypatch):
+    """A launch that gives up leaves the workspace as it was: spans whose end wraps past 2^31 among
+    what it may hold are skipped by the join."""
+    cache = Cache([4000], 1, d, 64, seed=3)
+    q = torch.randn(1, 64, d, device=DEV).to(BF16)
+    size = fa.fa_fwd_paged_workspace_size(1, 1, 64, 1, d)
+    want, _ = fa.fa_fwd_paged(q, *cache.dev(), max_kv=4000)
+    for span in ([1, 0x7FFFFFFF], [0x7FFFFFFF, 2], [-5, 3], [0x7FFFFFFF, 0x7FFFFFFF]):
+        ws = i32(span).repeat(size // 8).view(torch.uint8)
+        monkeypatch.setenv("FA_WAIT_TIMEOUT_US", "1")
+        fa.fa_fwd_paged(q, *cache.dev(), max_kv=4000, workspace=ws)
+        fa.fa_get_error()
+        monkeypatch.delenv("FA_WAIT_TIMEOUT_US")
+        out, _ = fa.fa_fwd_paged(q, *cache.dev(), max_kv=4000, workspace=ws)
+        assert fa.fa_get_error() == fa.FA_OK and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("G", [1, 64], ids=["few rows", "many rows"])
+def test_paged_length_at_the_end_of_its_type(G):
+    """kv_lens of 2^31 - 1 over pages that are all the same one: clamped to 2^31 - 256 keys and
+    reported.  Scores are 0 and V is 1, so weights are 1, a worker's sums are integers below 2^24
+    (exact), and joining at most 1216 parts leaves 1216 x 2^-24 of relative error."""
+    k = torch.zeros(1, 1, 128, 64, dtype=BF16, device=DEV)
+    v = torch.ones_like(k)
+    table = torch.zeros(1, 1 << 24, dtype=torch.int32, device=DEV)
+    q = torch.ones(1, G, 64, dtype=BF16, device=DEV)
+    out, lse = fa.fa_fwd_paged(q, k, v, table, i32([0x7FFFFFFF]))
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    bound = 1216 * 2.0 ** -24
+    assert np.abs(f64(out) - 1).max() <= 2 * bound + 2.0 ** -8
+    assert np.abs(f64(lse) - np.log(2.0 ** 31 - 256)).max() <= bound + 2.0 ** -20 * 22
+
+
+@pytest.mark.parametrize("nq", [2, 40], ids=["few rows", "many rows"])
+def test_offsets_that_do_not_ascend_are_reported(nq):
+    cache = Cache([700, 20, 300], 2, 64, 16, seed=17)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(3 * nq, 4, 64, device=DEV).to(BF16)
+    n = 3 * nq
+    for cu in ([0, n, 0, n], [-3, nq, 2 * nq, n], [0, nq, 2 * nq, n + 9], [n, 0, n, 0]):
+        fa.fa_fwd_paged(q, k, v, table, lens, cu_seqlens=i32(cu), max_q=n, max_kv=700)
+        assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    groups = i32([0, 3, 1])
+    fa.fa_fwd_shared_prefix(q, k, v, table, lens, table[:2].contiguous(), lens[:2].contiguous(), groups,
+                            cu_seqlens=i32([0, nq, 2 * nq, n]), max_q=nq, max_kv=700)
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+
+
+@pytest.mark.parametrize("nq", [1, 40], ids=["few rows", "many rows"])
+def test_stream_argument_writes_no_memory_that_the_current_stream_still_uses(nq):
+    """Memory freed on the current stream while a kernel there has still to write it is not handed
+    to a call on another stream."""
+    cache = Cache([3000, 40], 2, 128, 64, seed=7)
+    args = cache.dev()
+    q = torch.randn(2 * nq, 8, 128, device=DEV).to(BF16)
+    kw = dict(cu_seqlens=i32([0, nq, 2 * nq]), max_q=nq, max_kv=3000)
+    want = fa.fa_fwd_paged(q, *args, **kw)
+    ws = fa.fa_fwd_paged_workspace_size(2, 2 * nq, 8, 2, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = [torch.empty_like(t) for t in want] + [torch.empty(ws, dtype=torch.uint8, device=DEV)]
+    torch.cuda._sleep(20_000_000)
+    for t in old:
+        t.fill_(9)
+    del old, t
+    got = fa.fa_fwd_paged(q, *args, **kw, stream=side)
+    torch.cuda.synchronize()
+    assert fa.fa_get_error() == fa.FA_OK
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    with pytest.raises(ValueError):
+        fa.fa_fwd_paged(None, *args, stream=side)
+
+
 def test_paged_empty_and_refusals():
     cache = Cache([5, 6], 2, 64, 16, seed=1)
     k, v, table, lens = cache.dev()
@@ -422,8 +496,20 @@ def test_append_bad_pages_write_nothing():
     assert fa.fa_get_error() == fa.FA_ERR_INDEX
     assert torch.equal(q, x)
     assert torch.equal(k[0, 0, 1], x[3, 0]) and k.sum() == v.sum() == 5.0 * k.numel() - 4 * 64
-    fa.fa_kv_append(None, x[:1], x[:1], k, v, i32([[1]]), i32([-2]))
+    for lens in (-2, -0x80000000):
+        fa.fa_kv_append(None, x[:1], x[:1], k, v, i32([[1]]), i32([lens]))
+        assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    # a position past 32 bits is past the table; the key is written all the same
+    rope = fa.fa_rope_table(8, 64)
+    far = fa.fa_kv_append(x[:1], x[:1], x[:1], k, v, i32([[0]]), i32([2]), table=rope, pos_offset=i32([0x7FFFFFFF]))
     assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    last = fa.fa_kv_append(x[:1], x[:1], x[:1], k, v, i32([[0]]), i32([2]), table=rope, pos_offset=i32([6]))
+    assert fa.fa_get_error() == fa.FA_OK and torch.equal(far, last)
+    fa.fa_kv_append(None, x[:1], x[:1], k, v, i32([[0]]), i32([2]))
+    assert k.sum() == 5.0 * k.numel() - 4 * 64
+    # offsets that do not ascend: reported, nothing written outside the sequences' pages
+    fa.fa_kv_append(None, x[:3], x[:3], k, v, i32([[0], [0]]), i32([2, 2]), cu_seqlens=i32([2, 1, 3]))
+    fa.fa_kv_append(None, x[:1], x[:1], k, v, i32([[0]]), i32([2]))
     assert k.sum() == 5.0 * k.numel() - 4 * 64
 
 
