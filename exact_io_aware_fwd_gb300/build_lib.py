@@ -63,7 +63,7 @@ def _binding_command(out):
             "-fvisibility=hidden",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[x for d in dirs for x in ("-isystem", d)], BINDING_SOURCE, "-o", out, "-L", libs,
-            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
             "-Wl,-rpath," + libs]
 
 

@@ -1,6 +1,7 @@
 // C-ABI entry points (declared in include/fa.h) of the operators around attention: the norm and
 // rotation pass, the paged cache and the attention that reads it.  Every argument is checked
 // before the first launch; nothing here allocates device memory.
+#include <atomic>
 #include <cmath>
 #include <limits>
 
@@ -55,9 +56,17 @@ void set_transform(fa::RopeArgs& a, const fa_qk_transform& t) {
   a.eps = t.eps;
 }
 
+// The current device is an sm_103 part (asked once per device); its status word.
 fa_status device_ready(int*& status) {
-  const fa_status st = fa::check_device();
-  if (st != FA_OK) return st;
+  static std::atomic<uint64_t> ready{0};  // bit d: device d is one
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if ((ready.load(std::memory_order_acquire) & bit) == 0) {
+    const fa_status st = fa::check_device();
+    if (st != FA_OK) return st;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   status = fa::status_ptr();
   return status == nullptr ? FA_ERR_CUDA : FA_OK;
 }

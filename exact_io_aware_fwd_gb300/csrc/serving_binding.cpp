@@ -14,7 +14,8 @@
 #include <vector>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -127,8 +128,10 @@ fa_view rows(const at::Tensor& t, Order order, at::Device dev, const char* name)
   return {p, s[0], s[1], s[2]};
 }
 
+// A new tensor, without the dispatcher's detour: between other calls of a program, whose code has
+// taken its place in the host's caches, each such step costs more than in a loop of its own.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
 
 // An output: the caller's, whose elements must be distinct (no expanded or overlapping
@@ -162,15 +165,24 @@ at::Tensor own_array(const at::Tensor* given, at::IntArrayRef shape, at::ScalarT
 
 // The caller's workspace, whose size counts in bytes, or a new one (kept until the call has been
 // launched; the allocator orders its reuse on the current stream).
-at::Tensor workspace(const at::Tensor* given, size_t need, at::Device dev, size_t& bytes) {
+struct Workspace {
+  c10::DataPtr own;
+  void* p = nullptr;
+  size_t bytes = 0;
+};
+Workspace workspace(const at::Tensor* given, size_t need, at::Device dev) {
+  Workspace w;
   if (given == nullptr) {
-    bytes = need > 0 ? need : 1;
-    return fresh({static_cast<int64_t>(bytes)}, at::kByte, dev);
+    w.bytes = need;
+    if (need > 0) w.own = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+    w.p = w.own.get();
+    return w;
   }
   if (given->device() != dev || !given->is_contiguous())
     refuse("workspace must be a contiguous tensor on " + dev.str());
-  bytes = static_cast<size_t>(given->numel()) * given->element_size();
-  return *given;
+  w.bytes = static_cast<size_t>(given->numel()) * given->element_size();
+  w.p = given->data_ptr();
+  return w;
 }
 
 // Calls launch on the device's current stream, on which their outputs are allocated too.
@@ -341,17 +353,17 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
     out_t[i] = own_rows(given[i], shape(i == 0 ? H : Hkv), out_order, dev, names[i], out[i]);
     if (norm && i < 2) x[i] = rows(i == 0 ? *q : *k, out_order, dev, i == 0 ? "q" : "k");
   }
-  at::Tensor dwq, dwk, ws;
-  size_t ws_bytes = 0;
+  at::Tensor dwq, dwk;
+  Workspace ws;
   if (norm) {
     dwq = fresh({d}, at::kFloat, dev);
     dwk = fresh({d}, at::kFloat, dev);
-    ws = workspace(tensor_or_none(a[14], "workspace"), p_rope_bwd_ws(dim32(d)), dev, ws_bytes);
+    ws = workspace(tensor_or_none(a[14], "workspace"), p_rope_bwd_ws(dim32(d)), dev);
   }
   check(p_rope_bwd(grad, norm ? x : nullptr, out, norm ? dwq.data_ptr<float>() : nullptr,
                    norm ? dwk.data_ptr<float>() : nullptr, pos, B > 0 ? dim32(B) : 1,
                    empty ? 0 : dim32(N), dim32(H), dim32(Hkv), dim32(d), &t,
-                   norm ? ws.data_ptr() : nullptr, ws_bytes, stream_of(dev)),
+                   ws.p, ws.bytes, stream_of(dev)),
         "fa_qk_norm_rope_bwd");
   return wrap_all({out_t[0], out_t[1], out_t[2], dwq, dwk});
 }
@@ -463,19 +475,18 @@ PyObject* attend(PyObject* const* a) {
   const at::Tensor out = own_array(tensor_or_none(a[10], "out"), q.sizes(), at::kBFloat16, dev, "out");
   const at::Tensor lse = own_array(tensor_or_none(a[11], "lse"), {H, total}, at::kFloat, dev, "lse");
   const int B = dim32(c.B), T = dim32(total), h = dim32(H), hkv = dim32(c.Hkv), d = dim32(c.d);
-  size_t ws_bytes = 0;
-  const at::Tensor ws =
+  const Workspace ws =
       workspace(tensor_or_none(a[12], "workspace"),
                 kPrefix ? p_prefix_ws(B, pre.groups, T, h, hkv, d) : p_paged_ws(B, T, h, hkv, d),
-                dev, ws_bytes);
+                dev);
   void* stream = stream_of(dev);
   if (kPrefix)
     check(p_prefix(qp, &c.kv, &pre, out.data_ptr(), lse.data_ptr<float>(), cu, B, max_q, max_kv, T,
-                   h, hkv, d, causal, scale, ws.data_ptr(), ws_bytes, stream),
+                   h, hkv, d, causal, scale, ws.p, ws.bytes, stream),
           "fa_fwd_shared_prefix");
   else
     check(p_paged(qp, &c.kv, out.data_ptr(), lse.data_ptr<float>(), cu, B, max_q, max_kv, T, h, hkv,
-                  d, causal, scale, ws.data_ptr(), ws_bytes, stream),
+                  d, causal, scale, ws.p, ws.bytes, stream),
           "fa_fwd_paged");
   return wrap_all({out, lse});
 }
