@@ -27,7 +27,7 @@ SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_block_spar
            "fa_serving.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_mma.cu"]
 HEADERS = [os.path.join(CSRC, "sm103.cuh"), os.path.join(CSRC, "fa_internal.h"),
            os.path.join(CSRC, "fa_host.h"), os.path.join(CSRC, "fa_paged.h"),
-           os.path.join(CSRC, "paged_plan.cuh"),
+           os.path.join(CSRC, "paged_plan.cuh"), os.path.join(CSRC, "paged_rows.cuh"),
            os.path.join(ROOT, "include", "fa.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,19 +1,8 @@
-// Attention of a few query rows over a paged key/value cache, and the join of partial results.
-//
-// O = softmax(scale q K^T) V for the queries of one sequence that share a key/value head (group
-// members x new tokens), 16 rows at a time: each K, V element is used by at most 16 rows, so the
-// kernel is bound by reading the cache once.  Every warp is a worker of its own (paged_plan.cuh):
-// it takes an equal share of all keys, copies 16 keys a step with cp.async into a private ring of
-// shared-memory stages (keys past the length become zeros, whatever the page holds there),
-// computes S (m16n8k16), the online softmax and O += P V from the ring, and writes its result or
-// its part of one straight from registers.  No barrier after the start: warps never wait for each
-// other, and a warp's ring goes on with the next piece while the last one is written.  (With 8
-// warps on one segment and a merge in shared memory at each piece's end, 1024 segments of about
-// 512 keys took 81 us instead of the copies' 40.)  mma.sync is enough here: 16 rows x 4 flops per
-// element and 2 bytes is 32 flops a byte, a few percent of the tensor pipe at full bandwidth.
+// Launches of the attention of a few query rows (paged_rows.cuh), and the join of partial results.
 #include "fa_internal.h"
 #include "fa_paged.h"
 #include "paged_plan.cuh"
+#include "paged_rows.cuh"
 #include "sm103.cuh"
 
 namespace fa {
@@ -21,289 +10,39 @@ namespace fa {
 namespace {
 
 constexpr int kWarps = kPagedWarps, kThreads = 32 * kWarps;
-constexpr int R = kPagedRows;
-constexpr int KT = 16;                // keys of a step, and of a tile
-constexpr int kDirectTiles = kPagedUnsplitKeys / KT;  // one warp for a whole segment
 constexpr float kLn2 = 0.693147180559945309f;
 
-// One CTA per SM: 8 warps x stages of 16 keys (192 KB: with all but one stage of each in flight,
-// 128 to 160 KB cover the latency of memory at full rate).
-template <int D>
-struct PagedLayout {
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr uint32_t kHalf = KT * D * 2u;                // K or V of a step
-  static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr uint32_t kBytes = kWarps * kStages * kStage;
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // 0: the 16 bytes become zeros, src is not read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Byte offset of 16-byte granule g of key row r in a step's K or V: granules are permuted within
-// each 128 bytes by the row, so the eight rows of an ldmatrix fall into different banks.
-template <int D>
-__device__ __forceinline__ uint32_t step_offset(uint32_t r, uint32_t g) {
-  return r * (D * 2u) + ((g ^ (r & 7u)) << 4);  // the xor stays within the granule's 128 bytes
-}
-
-// What a warp needs to copy the steps of a piece.
-struct Source {
-  const int32_t* trow;  // block-table row
-  int hk, len;          // key/value head, keys
-  int first, steps;     // key tile of step 0, number of steps
-  int pages;            // lane i: page of step (issue & ~31) + i
-};
-
-__device__ __forceinline__ Source source_of(const PagedArgs& a, const Walk<R, KT>& w,
-                                            const Piece& p) {
-  Source s;
-  s.trow = a.list.table + static_cast<int64_t>(w.b) * a.list.max_pages;
-  s.hk = p.hk;
-  s.len = w.e.len;
-  s.first = p.ta;
-  s.steps = min(p.te, (w.e.len + KT - 1) / KT) - p.ta;  // none for an entry without keys
-  s.pages = -1;
-  return s;
-}
-
-// Copies step st into its stage (zeros for keys past the length and, reported, for a page outside
-// the pool); every call commits a group, empty past the last step.
-template <int D>
-__device__ __forceinline__ void issue_step(const PagedArgs& a, Source& s, int st, uint32_t ring,
-                                           int lane) {
-  using L = PagedLayout<D>;
-  constexpr int S = L::kStages, GR = D / 8;  // granules of a row
-  if (st < s.steps) {
-    if ((st & 31) == 0)
-      s.pages = st + lane < s.steps ? resolve_page(s.trow, a.list.max_pages, a.num_pages,
-                                                   a.page_shift, (s.first + st + lane) * KT)
-                                    : 0;
-    const int page = __shfl_sync(~0u, s.pages, st & 31);
-    const int key0 = (s.first + st) * KT;
-    const int slot = st % S;
-    if (page < 0 && lane == 0) atomicCAS(a.status, 0, kErrIndex);
-    const int64_t base = (((static_cast<int64_t>(max(page, 0)) * a.Hkv + s.hk) << a.page_shift) +
-                          (key0 & ((1 << a.page_shift) - 1))) * D;
-    const uint32_t dst = ring + slot * L::kStage;
-#pragma unroll
-    for (int i = 0; i < KT * GR / 32; ++i) {
-      const int r = (i * 32 + lane) / GR, g = (i * 32 + lane) % GR;
-      const bool valid = page >= 0 && key0 + r < s.len;
-      const int64_t off = valid ? base + r * D + g * 8 : 0;
-      cp_async16(dst + step_offset<D>(r, g), a.k_cache + off, valid);
-      cp_async16(dst + L::kHalf + step_offset<D>(r, g), a.v_cache + off, valid);
-    }
-  }
-  cp_commit();
-}
-
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) paged_kernel(const PagedArgs a) {
-  using L = PagedLayout<D>;
-  constexpr int S = L::kStages;
+// With two lists the CTAs are divided by the lists' tiles, which cost the same.
+template <int D, int kLists>
+__global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ PagedArgs a) {
+  using rows16::kDirectTiles;
+  using rows16::KT;
+  using rows16::R;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Share shares[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  begin_launch(a.first);
-  make_shares<R, KT, kThreads, kDirectTiles, kWarps>(a, shares);
-  const KeyList& l = a.list;
-  const Share& sh = shares[warp];
-  const uint32_t ring = smem_u32(smem) + warp * (S * L::kStage);
-
-  if (sh.u0 < sh.u1 && sh.b >= 0) {
-    Walk<R, KT> walk(a, sh);
-    Piece next_piece;
-    bool more = walk.next(a, next_piece);
-    Source src = source_of(a, walk, next_piece);
-    for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane);
-    while (more) {
-      const Piece piece = next_piece;
-      const Entry e = walk.e;
-      const int tile = row_tile0(e.start, a.G, R, walk.b) + piece.r;
-      const int hk = piece.hk;
-      if (lane == 0 && piece.ta == 0)  // this worker begins the segment
-        a.part.spans[static_cast<int64_t>(hk) * a.part.span_tiles + tile] = span_of(sh, piece);
-
-      // ---- the rows' queries as A fragments: thread holds rows lane / 4 and lane / 4 + 8
-      const int row0 = piece.r * R, rows = min(R, e.nc * a.G - row0);
-      uint32_t qf[D / 16][4];
-      int lim[2];  // keys below it are visible to the row
-      int at[2];   // (token, head) of the row
-      int head[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = (lane >> 2) + 8 * i, tok = (row0 + rr) / a.G;
-        lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row0 + rr) : e.len;
-        head[i] = hk * a.G + (row0 + rr - tok * a.G);
-        at[i] = (e.start + tok) * a.H + head[i];
-        const __nv_bfloat16* qp = a.q + static_cast<int64_t>(at[i]) * D + (lane & 3) * 2;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          qf[k][i] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
-          qf[k][i + 2] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
-        }
-      }
-      const int lim_min = row_limit(e, l.causal, a.G, row0);  // the first row's: the smallest
-
-      float o[D / 8][4];
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-      for (int st = 0; st < src.steps; ++st) {
-        cp_wait<S - 2>();
-        __syncwarp();
-        const uint32_t kb = ring + (st % S) * L::kStage, vb = kb + L::kHalf;
-        // S = Q K^T: 16 rows x 16 keys
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        {
-          const uint32_t r = (lane & 7) + ((lane >> 4) << 3), gh = (lane >> 3) & 1;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t f[4];
-            ldsm4(kb + step_offset<D>(r, 2 * k + gh), f);
-            mma16816(s[0], qf[k], f[0], f[1]);
-            mma16816(s[1], qf[k], f[2], f[3]);
-          }
-        }
-        const int key0 = (src.first + st) * KT;
-        if (key0 + KT > lim_min) {
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int key = key0 + n * 8 + (lane & 3) * 2 + (c & 1);
-              if (key >= lim[c >> 1]) s[n][c] = -INFINITY;
-            }
-        }
-        // online softmax; the row maximum is shared by the four lanes of a row, the sum is
-        // joined at the end
-        bool moved = false;
-        float alpha[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx =
-              fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2)) * a.scale_log2;
-          alpha[i] = 1.f;
-          if (mx > m[i]) {
-            alpha[i] = ex2(m[i] - mx);
-            m[i] = mx;
-            moved = true;
-          }
-          const float ref = m[i] == -INFINITY ? 0.f : m[i];
-          float part = 0.f;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              // the scale is never 0, so a hidden score stays -inf and weighs 0
-              const float p = ex2(fmaf(s[n][2 * i + c], a.scale_log2, -ref));
-              s[n][2 * i + c] = p;
-              part += p;
-            }
-          sum[i] = sum[i] * alpha[i] + part;
-        }
-        if (__any_sync(~0u, moved)) {
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            o[n][0] *= alpha[0];
-            o[n][1] *= alpha[0];
-            o[n][2] *= alpha[1];
-            o[n][3] *= alpha[1];
-          }
-        }
-        // O += P V; P rounded to bf16 (half a step, 2^-8, as in fa_fwd), its sum is not
-        const uint32_t pf[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
-                                pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
-        {
-          const uint32_t r = lane & 15, gh = lane >> 4;
-#pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            uint32_t f[4];
-            ldsm4_t(vb + step_offset<D>(r, 2 * n + gh), f);
-            mma16816(o[2 * n], pf, f[0], f[1]);
-            mma16816(o[2 * n + 1], pf, f[2], f[3]);
-          }
-        }
-        __syncwarp();  // every lane has read stage st % S before it is filled again
-        issue_step<D>(a, src, st + S - 1, ring, lane);
-      }
-      // every stage has been read: the next piece's copies start here
-      more = walk.next(a, next_piece);
-      if (more) {
-        src = source_of(a, walk, next_piece);
-        for (int st = 0; st < S - 1; ++st) issue_step<D>(a, src, st, ring, lane);
-      }
-
-      // ---- the rows' results, or this worker's part of them
-      const bool final_out = piece.whole && a.rowbuf == nullptr;
-      float* part = a.part.slots + (static_cast<int64_t>(sh.worker) * 2 + (piece.ta == 0)) *
-                                       (R * (D + 2));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
-        sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
-        const int rr = (lane >> 2) + 8 * i;
-        if (rr >= rows) continue;
-        const float inv = sum[i] > 0.f ? 1.f / sum[i] : (sum[i] == 0.f ? 0.f : sum[i]);  // NaN stays
-        if (final_out) {
-          uint32_t* dst =
-              reinterpret_cast<uint32_t*>(a.o + static_cast<int64_t>(at[i]) * D) + (lane & 3);
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n)
-            dst[n * 4] = pack_bf16(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
-        } else {
-          float* row = piece.whole ? a.rowbuf + static_cast<int64_t>(at[i]) * D : part + rr * D;
-          float2* dst = reinterpret_cast<float2*>(row) + (lane & 3);
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) dst[n * 4] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
-        }
-        if ((lane & 3) == 0) {
-          if (final_out) {
-            const int t = (at[i] - head[i]) / a.H;
-            a.lse[static_cast<int64_t>(head[i]) * a.total + t] =
-                sum[i] == 0.f ? -INFINITY : (m[i] + log2f(sum[i])) * kLn2;
-          } else {
-            float* st = piece.whole ? a.rowbuf + static_cast<int64_t>(a.total) * a.H * D + at[i]
-                                    : part + R * D + rr;
-            st[0] = m[i];
-            st[piece.whole ? a.total * a.H : R] = sum[i];
-          }
-        }
-      }
-    }
-    cp_wait<0>();
+  begin_launch();
+  int li = 0;
+  if constexpr (kLists == 1) {
+    make_shares<R, KT, kThreads, kDirectTiles, kWarps>(a, shares);
+  } else {
+    __shared__ int red[2][3][kWarps], scan[kWarps];
+    Entry mine[2];
+    sum_entries<R, KT, kThreads>(a, a.list[0], mine[0], red[0]);
+    sum_entries<R, KT, kThreads>(a, a.list[1], mine[1], red[1]);
+    __syncthreads();
+    const Totals t[2] = {totals_of(red[0]), totals_of(red[1])};
+    const float cost[2] = {1.f, 1.f};
+    const int n1 = ctas_of_second(gridDim.x, t, cost), cta = blockIdx.x;
+    li = cta < n1 ? 1 : 0;
+    share_list<R, KT, kThreads, kDirectTiles, kWarps>(
+        a, a.list[li], li ? t[1] : t[0], li ? mine[1] : mine[0], li ? cta : cta - n1,
+        li ? n1 : static_cast<int>(gridDim.x) - n1, scan, shares);
   }
-  wait_for_last_launch();
+  rows16::work<D>(a, a.list[li], a.part[li], a.rowbuf[li], shares[warp],
+                  smem_u32(smem) + warp * (rows16::PagedLayout<D>::kStages *
+                                           rows16::PagedLayout<D>::kStage),
+                  lane);
 }
 
 // ---- join of the parts
@@ -472,19 +211,21 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
         lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * kLn2;
 }
 
-template <int D>
+template <int D, int kLists>
 cudaError_t launch_paged_d(const PagedArgs& a, int64_t max_units, cudaStream_t s) {
-  using L = PagedLayout<D>;
-  cudaError_t e = ensure_smem_limit<paged_kernel<D>>(L::kBytes);
+  constexpr uint32_t bytes = rows16::PagedLayout<D>::kBytes;
+  cudaError_t e = ensure_smem_limit<paged_kernel<D, kLists>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
-  return launch_chained(paged_kernel<D>, static_cast<unsigned>(ctas), kThreads, L::kBytes, s, a);
+  return launch_chained(paged_kernel<D, kLists>, static_cast<unsigned>(ctas), kThreads, bytes, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s) {
-  return d == 64 ? launch_paged_d<64>(a, max_units, s) : launch_paged_d<128>(a, max_units, s);
+cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s) {
+  if (lists == 2)
+    return d == 64 ? launch_paged_d<64, 2>(a, max_units, s) : launch_paged_d<128, 2>(a, max_units, s);
+  return d == 64 ? launch_paged_d<64, 1>(a, max_units, s) : launch_paged_d<128, 1>(a, max_units, s);
 }
 
 cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s) {

@@ -14,9 +14,8 @@ enum : int { kErrIndex = 6 };  // FA_ERR_INDEX in the status word
 
 // Launches that may be scheduled while the kernel ahead of them on the stream still runs, so that
 // their launch and their CTAs' start overlap its end.  Nothing is read or written before it has
-// completed: a call's first kernel waits for it at once (begin_launch); a further kernel of the
-// call, whose inputs were complete before the first one began, waits before it ends (the join:
-// before it reads the parts), so that the last one's end is the whole call's.
+// completed (begin_launch; the join looks up where its rows' parts are before it waits, from inputs
+// that were complete before the kernel ahead of it began).
 template <typename K, typename... Args>
 cudaError_t launch_chained(K kernel, dim3 grid, unsigned threads, uint32_t smem, cudaStream_t s,
                            const Args&... args) {
@@ -41,8 +40,8 @@ __device__ __forceinline__ void let_next_launch() {
 __device__ __forceinline__ void wait_for_last_launch() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-__device__ __forceinline__ void begin_launch(bool first) {
-  if (first) wait_for_last_launch();
+__device__ __forceinline__ void begin_launch() {
+  wait_for_last_launch();
   let_next_launch();
 }
 #endif
@@ -124,9 +123,9 @@ cudaError_t launch_rope_bwd(int d, bool interleaved, const RopeArgs& a, float* d
 
 // ---- attention over the paged cache (fa_paged.cu)
 //
-// One launch covers a list of key ranges: the sequences of a batch with their own pages, or the
-// groups of a batch with the pages of their shared prefix (group_cu set).  Entry b has packed
-// query tokens [start, start + n) and len keys.
+// A list of key ranges: the sequences of a batch with their own pages, or the groups of a batch
+// with the pages of their shared prefix (group_cu set).  Entry b has packed query tokens [start,
+// start + n) and len keys.
 struct KeyList {
   int count;                // entries
   const int32_t* lens;      // [count]
@@ -134,6 +133,7 @@ struct KeyList {
   int max_pages, max_len, max_q;
   const int32_t* group_cu;  // groups: [count + 1] over sequences, or nullptr
   int causal;
+  int mma;                  // row tiles and key tiles of the tensor-core kernel
 };
 
 // Partial results of one list.  Its rows (query token x head of the key/value head's group) are
@@ -155,6 +155,8 @@ __host__ __device__ inline int row_tile0(int start, int G, int R, int b) {
   return (start * G + R - 1) / R + b;  // never overlaps entry b - 1's tiles
 }
 
+// One launch works on one list, or on both lists of a call with shared prefixes (list 0: the
+// sequences, list 1: the groups) at once, each on its own part of the SMs.
 struct PagedArgs {
   const __nv_bfloat16 *q, *k_cache, *v_cache;
   __nv_bfloat16* o;
@@ -163,10 +165,10 @@ struct PagedArgs {
   int B, total, H, Hkv, G;
   int num_pages, page_shift;
   float scale_log2;
-  KeyList list;
-  PartialLayout part;
-  float* rowbuf;  // joined lists: [total * H] rows of O, then m, then l; else nullptr
-  bool first;     // the call's first kernel
+  KeyList list[2];
+  PartialLayout part[2];
+  float mma_cost;    // a key tile of the tensor-core kernel in key tiles of the other one
+  float* rowbuf[2];  // joined lists: [total * H] rows of O, then m, then l; else nullptr
   int* status;
 };
 
@@ -189,10 +191,10 @@ constexpr int kPagedUnsplitKeys = 256;   // where no entry has more keys, none i
 constexpr int kPagedMmaRows = 256;       // rows of a tile of the tensor-core kernel, whose CTAs
 constexpr int kPagedMmaUnsplitKeys = 512;  // are the workers
 
-cudaError_t launch_paged(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s);
+cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s);
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedArgs& a, int64_t max_units, uint64_t timeout_ns,
-                             cudaStream_t s);
+                             const PagedArgs& a, int lists, int64_t max_units,
+                             uint64_t timeout_ns, cudaStream_t s);
 cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s);
 
 }  // namespace fa

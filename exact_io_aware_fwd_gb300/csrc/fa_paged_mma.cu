@@ -14,11 +14,14 @@
 //    out the CTA's pieces and hands them to the other roles through a ring in shared memory, so
 //    the TMA warp runs ahead into the next piece while the softmax warps finish the last one; a
 //    segment that several CTAs share leaves float32 parts for the join kernel.
+// A call with shared prefixes runs as one launch: the SMs are divided between the groups' prefixes
+// and the sequences' own keys by what their key tiles cost (paged_plan.cuh, kLists == 2).
 // Bound by the tensor pipe when both query tiles are full (512 flops per K, V byte at 256 rows);
 // with one tile of few rows by the copies from memory.
 #include "fa_internal.h"
 #include "fa_paged.h"
 #include "paged_plan.cuh"
+#include "paged_rows.cuh"
 #include "sm103.cuh"
 
 namespace fa {
@@ -59,6 +62,14 @@ struct MmaLayout {
   static constexpr uint32_t kTmemCols = 512;
 };
 
+// Shared memory of a CTA: the tiles, or with two lists the rings of a CTA of few rows.
+template <int D, int kLists>
+__host__ __device__ constexpr uint32_t smem_of() {
+  return kLists == 1 || MmaLayout<D>::kBytes > rows16::PagedLayout<D>::kBytes
+             ? MmaLayout<D>::kBytes
+             : rows16::PagedLayout<D>::kBytes;
+}
+
 // Key tiles of query tile t (rows [256 r + 128 t, + 128)) inside the piece's range.
 __device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, int causal, int G,
                                               int t) {
@@ -68,10 +79,12 @@ __device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, in
   return max(0, min(p.te, (lim + KT - 1) / KT) - p.ta);
 }
 
-template <int D>
+// kLists == 2: a call with shared prefixes, each list on its own part of the SMs.  The CTAs of a
+// list of few rows do what paged_kernel does, with the softmax warps as the workers.
+template <int D, int kLists>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const PagedArgs a,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedArgs a,
                      const uint64_t timeout_ns, const uint32_t smem_bytes) {
   using L = MmaLayout<D>;
   constexpr int S = L::kStages, P = D / 64;  // 64-column panels of a tile
@@ -86,21 +99,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ PieceInfo pieces[kRing];
   __shared__ uint32_t tmem_slot[1];
   __shared__ volatile int abort_flag[1];
-  __shared__ Share sh;
+  __shared__ Share shares[kLists == 2 ? kPagedWarps : 1];
   const Ctl ctl{abort_flag, a.status, timeout_ns};
   const uint32_t warp = warp_id(), lane = lane_id();
-  if (pad + L::kBytes > smem_bytes) {  // cannot happen with the host's sizing; never proceed
+  if (pad + smem_of<D, kLists>() > smem_bytes) {  // cannot happen with the host's sizing; never proceed
     if (threadIdx.x == 0) atomicCAS(a.status, 0, kErrLayout);
     return;
   }
-  begin_launch(a.first);
-  make_shares<R, KT, kThreads, kDirectTiles, 1>(a, &sh);
-  if (sh.u0 >= sh.u1) {  // uniform over the CTA
-    wait_for_last_launch();
-    return;
-  }
-  const KeyList& l = a.list;
-
+  // nothing here depends on what earlier launches write
   if (warp == 0 && lane == 0) {
     *abort_flag = 0;
     mbar_init(q_full, 8);
@@ -131,6 +137,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // the share of the list that this CTA works on
+  begin_launch();
+  int li = 0;
+  if constexpr (kLists == 1) {
+    make_shares<R, KT, kThreads, kDirectTiles, 1>(a, shares);
+  } else {
+    __shared__ int red[2][3][kThreads / 32], scan[kThreads / 32];
+    Entry mine[2];
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      Entry e;
+      if (a.list[i].mma) sum_entries<R, KT, kThreads>(a, a.list[i], e, red[i]);
+      else sum_entries<rows16::R, rows16::KT, kThreads>(a, a.list[i], e, red[i]);
+      if (i == 0) mine[0] = e;
+      else mine[1] = e;
+    }
+    __syncthreads();
+    const Totals t[2] = {totals_of(red[0]), totals_of(red[1])};
+    const float cost[2] = {a.list[0].mma ? a.mma_cost : 1.f, a.list[1].mma ? a.mma_cost : 1.f};
+    const int n1 = ctas_of_second(gridDim.x, t, cost);
+    li = static_cast<int>(blockIdx.x) < n1 ? 1 : 0;
+    const int cta = li ? blockIdx.x : blockIdx.x - n1, ctas = li ? n1 : gridDim.x - n1;
+    const Totals ti = li ? t[1] : t[0];
+    const Entry own = li ? mine[1] : mine[0];
+    if (a.list[li].mma)
+      share_list<R, KT, kThreads, kDirectTiles, 1>(a, a.list[li], ti, own, cta, ctas, scan, shares);
+    else
+      share_list<rows16::R, rows16::KT, kThreads, rows16::kDirectTiles, kPagedWarps>(
+          a, a.list[li], ti, own, cta, ctas, scan, shares);
+  }
+  const KeyList& l = a.list[li];
+  const PartialLayout& part = a.part[li];
+  float* const rowbuf = a.rowbuf[li];
+  const bool few_rows = kLists == 2 && !l.mma;
+  const Share& sh = shares[0];
   const uint32_t tmem = *tmem_slot;
   const uint32_t sbase = smem_u32(sm);
   // Registers: the launch gives 384 x 168; warps 0-3 keep 56 and the softmax warps take 224
@@ -138,14 +179,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // or 72 / 216, the spills in the loop cost up to 15% (2 x 512 tokens over 16384 keys).
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 2) {
+    if (few_rows) {
+    } else if (warp == 2) {
       // ================= the CTA's pieces
       if (lane == 0) {
-        Walk<R, KT> walk(a, sh);
+        Walk<R, KT> walk(a, l, sh);
         const Entry& e = walk.e;
         Piece piece;
         for (int i = 0;; ++i) {
-          const bool more = walk.next(a, piece);
+          const bool more = walk.next(a, l, piece);
           if (!mbar_wait(&piece_empty[i % kRing], ((i / kRing) & 1) ^ 1, ctl)) break;
           PieceInfo& p = pieces[i % kRing];
           if (more) {
@@ -162,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.whole = piece.whole;
             p.table = l.table + static_cast<int64_t>(walk.b) * l.max_pages;
             if (piece.ta == 0)  // this CTA begins the segment
-              a.part.spans[static_cast<int64_t>(piece.hk) * a.part.span_tiles + p.tile] =
+              part.spans[static_cast<int64_t>(piece.hk) * part.span_tiles + p.tile] =
                   span_of(sh, piece);
           } else {
             p.n[0] = p.n[1] = -1;
@@ -287,7 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int base = 0, segs = 0;  // positions and pieces with keys before this one
     int seen = 0, outs = 0;  // S tiles and results of this query tile before this piece
     bool ok = true;
-    for (int i = 0;; ++i) {
+    if (few_rows)
+      rows16::work<D>(a, l, part, rowbuf, shares[kLists == 2 ? warp - 4 : 0],
+                      smem_u32(sm) + (warp - 4) * (rows16::PagedLayout<D>::kStages *
+                                                   rows16::PagedLayout<D>::kStage),
+                      lane);
+    for (int i = 0; !few_rows; ++i) {
       if (!(ok = mbar_wait_warp(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
       const PieceInfo& piece = pieces[i % kRing];  // held until the piece is done
       const int n_mine = piece.n[t];
@@ -441,11 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = gr < rows;
         const int tok = gr / a.G, head = piece.hk * a.G + (gr - tok * a.G);
         const int64_t at = static_cast<int64_t>(piece.start + tok) * a.H + head;
-        const bool final_out = piece.whole && a.rowbuf == nullptr;
+        const bool final_out = piece.whole && rowbuf == nullptr;
         const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
-        float* slot = a.part.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (ta == 0 ? 1 : 0)) *
+        float* slot = part.slots + (static_cast<int64_t>(sh.worker) * 2 + (ta == 0 ? 1 : 0)) *
                                          (static_cast<int64_t>(R) * (D + 2));
-        float* dst = piece.whole ? a.rowbuf + at * D : slot + (128 * t + row) * D;
+        float* dst = piece.whole ? rowbuf + at * D : slot + (128 * t + row) * D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -481,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[static_cast<int64_t>(head) * a.total + piece.start + tok] =
                 l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
           } else if (piece.whole) {
-            float* st = a.rowbuf + static_cast<int64_t>(a.total) * a.H * D;
+            float* st = rowbuf + static_cast<int64_t>(a.total) * a.H * D;
             st[at] = m_run;
             st[static_cast<int64_t>(a.total) * a.H + at] = l_run;
           } else {
@@ -501,28 +548,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
-  wait_for_last_launch();
 }
 
-template <int D>
+template <int D, int kLists>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
                      int64_t max_units, uint64_t timeout_ns, cudaStream_t s) {
-  using L = MmaLayout<D>;
-  const uint32_t smem = L::kBytes + 1024;
-  cudaError_t e = ensure_smem_limit<paged_mma_kernel<D>>(smem);
+  const uint32_t smem = smem_of<D, kLists>() + 1024;
+  cudaError_t e = ensure_smem_limit<paged_mma_kernel<D, kLists>>(smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
-  return launch_chained(paged_mma_kernel<D>, static_cast<unsigned>(ctas), kThreads, smem, s, tk,
-                        tv, a, timeout_ns, smem);
+  return launch_chained(paged_mma_kernel<D, kLists>, static_cast<unsigned>(ctas), kThreads, smem,
+                        s, tk, tv, a, timeout_ns, smem);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedArgs& a, int64_t max_units, uint64_t timeout_ns,
-                             cudaStream_t s) {
-  return d == 64 ? launch_d<64>(tk, tv, a, max_units, timeout_ns, s)
-                 : launch_d<128>(tk, tv, a, max_units, timeout_ns, s);
+                             const PagedArgs& a, int lists, int64_t max_units,
+                             uint64_t timeout_ns, cudaStream_t s) {
+  if (lists == 2)
+    return d == 64 ? launch_d<64, 2>(tk, tv, a, max_units, timeout_ns, s)
+                   : launch_d<128, 2>(tk, tv, a, max_units, timeout_ns, s);
+  return d == 64 ? launch_d<64, 1>(tk, tv, a, max_units, timeout_ns, s)
+                 : launch_d<128, 1>(tk, tv, a, max_units, timeout_ns, s);
 }
 
 }  // namespace fa

@@ -179,7 +179,7 @@ __device__ __forceinline__ HeadRange head_range(const RopeArgs& a, int i) {
 template <int D, bool kInter, bool kPaged>
 __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
   constexpr int L = D / 8;
-  begin_launch(true);
+  begin_launch();
   const int j = threadIdx.x % L;
   const int64_t t64 = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
   if (t64 >= a.tokens) return;
@@ -360,7 +360,7 @@ template <int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(const RopeArgs a) {
   constexpr int L = D / 8, G = kThreads / L;
   extern __shared__ __align__(16) uint8_t ring[];
-  begin_launch(true);
+  begin_launch();
   const int j = threadIdx.x % L, grp = threadIdx.x / L;
   const unsigned lane = threadIdx.x & 31u;
   const unsigned mask = ((1u << L) - 1u) << (lane & ~(L - 1u));
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(con
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int first_k,
                                                        int first_v, int D, float* dwq, float* dwk) {
   __shared__ float sm[32][33];
-  begin_launch(true);
+  begin_launch();
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
   const bool of_k = blockIdx.x * 32 >= D;
   const int col = blockIdx.x * 32 + x - (of_k ? D : 0);

@@ -118,6 +118,14 @@ bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int H
 // 16 and 83 with 32.
 constexpr long long mma_rows(int d) { return d == 64 ? 32 : 16; }
 
+// How a call with shared prefixes divides the SMs (lists of both kinds of row tiles): a key tile of
+// the tensor-core kernel counts as this many of the other's.  One works at the tensor core's pace
+// and the other at memory's, so at once they take less than one after the other: 128 sequences of
+// 1..1024 keys behind two prefixes of 32768 138 us instead of 148 (136 with 14, 145 with 20), 64 of
+// 512 keys behind 4096 50 instead of 65; d = 64, 64 of 1024 behind 32768 60 instead of 80 (65 with
+// 20, 67 with 40).  Two lists of few rows: 8 short sequences behind 1000 keys 15 instead of 16.3.
+constexpr float mma_tile_cost(int d) { return d == 64 ? 28.f : 16.f; }
+
 // Workspace of a paged call: the spans and slots of each list, then (joined lists) row buffers.
 // Which kernel a list takes is decided by max_q; with few rows in all it cannot be the
 // tensor-core one.
@@ -227,14 +235,13 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   j.G = a.G;
   j.lists = lists;
   CUtensorMap tk, tv;
-  if ((mma[0] || (lists > 1 && mma[1])) &&
+  const bool any_mma = mma[0] || (lists > 1 && mma[1]);
+  if (any_mma &&
       (!make_pool_map(&tk, cache->k_cache, *cache, Hkv, d) ||
        !make_pool_map(&tv, cache->v_cache, *cache, Hkv, d)))
     return FA_ERR_CUDA;
-  // the prefixes first (the heavier list), then the sequences' own keys
-  for (int n = 0; n < lists; ++n) {
-    const int i = lists - 1 - n;
-    fa::KeyList& l = a.list;
+  for (int i = 0; i < lists; ++i) {
+    fa::KeyList& l = a.list[i];
     l.count = count[i];
     l.lens = i == 0 ? cache->kv_lens : prefix->lens;
     l.table = i == 0 ? cache->block_table : prefix->table;
@@ -244,24 +251,23 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     l.max_q = i == 0 ? max_q : kMaxInt;
     l.group_cu = i == 0 ? nullptr : prefix->group_cu;
     l.causal = i == 0 && causal ? 1 : 0;
-    a.rowbuf = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
-    a.part.R = mma[i] ? fa::kPagedMmaRows : fa::kPagedRows;
-    a.part.workers = fa::kPagedCtas * (mma[i] ? 1 : fa::kPagedWarps);
-    a.part.span_tiles = fa::row_tiles_bound(total, a.G, a.part.R, l.count);
-    a.part.spans = reinterpret_cast<int2*>(base + w.spans[i]);
-    a.part.slots = reinterpret_cast<float*>(base + w.slots[i]);
-    a.first = n == 0;
-    cudaError_t e;
-    if (mma[i]) {
-      e = fa::launch_paged_mma(d, tk, tv, a, units[i], fa::wait_timeout_ns(), s);
-    } else {
-      e = fa::launch_paged(d, a, units[i], s);
-    }
-    if ((st = status_of(e)) != FA_OK) return st;
+    l.mma = mma[i];
+    a.rowbuf[i] = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
+    fa::PartialLayout& p = a.part[i];
+    p.R = mma[i] ? fa::kPagedMmaRows : fa::kPagedRows;
+    p.workers = fa::kPagedCtas * (mma[i] ? 1 : fa::kPagedWarps);
+    p.span_tiles = fa::row_tiles_bound(total, a.G, p.R, l.count);
+    p.spans = reinterpret_cast<int2*>(base + w.spans[i]);
+    p.slots = reinterpret_cast<float*>(base + w.slots[i]);
     j.list[i] = l;
-    j.part[i] = a.part;
-    j.rowbuf[i] = a.rowbuf;
+    j.part[i] = p;
+    j.rowbuf[i] = a.rowbuf[i];
   }
+  a.mma_cost = mma_tile_cost(d);
+  const long long all = units[0] + (lists > 1 ? units[1] : 0);
+  if ((st = status_of(any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, all, fa::wait_timeout_ns(), s)
+                              : fa::launch_paged(d, a, lists, all, s))) != FA_OK)
+    return st;
   // no entry can have been split (lengths are clamped to max_kv): every result is final
   if (lists == 1 && max_kv <= (mma[0] ? fa::kPagedMmaUnsplitKeys : fa::kPagedUnsplitKeys))
     return FA_OK;

@@ -1,5 +1,5 @@
-// How the workers of a paged-attention launch share its keys (a worker: a CTA of the tensor-core
-// kernel, a warp of the other one).
+// How the workers of a paged-attention launch share the keys of a list (a worker: a CTA of the
+// tensor-core kernel, a warp of the other one).
 //
 // The work of entry b is one segment per (key/value head, row tile), each of as many key tiles
 // (KT keys) as the tile's last row sees.  Laid end to end, the segments' key tiles are units
@@ -39,7 +39,8 @@ __device__ __forceinline__ int tiles_of(const Entry& e, int causal, int G, int r
 }
 
 template <int R, int KT>
-__device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b, bool report) {
+__device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b,
+                                            bool report) {
   Entry e;
   bool ok;
   if (l.group_cu != nullptr) {
@@ -75,9 +76,10 @@ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, 
 // Splitting W units over C workers: worker c takes [c W / C, (c + 1) W / C).  (The longer shares
 // are spread over the workers on purpose: with all of them first, the CTAs of a tensor-core launch
 // run in lockstep and their bursts of copies slow the MMAs: 249 instead of 226 us for 2 x 512
-// tokens over 16384 keys.)
+// tokens over 16384 keys.)  c W / C = c (W div C) + c (W mod C) / C: 32-bit divisions, C < 2^16.
 __host__ __device__ inline int share_begin(int W, int C, int c) {
-  return static_cast<int>(static_cast<int64_t>(c) * W / C);
+  const unsigned w = W, n = C, i = c;
+  return static_cast<int>(i * (w / n) + i * (w % n) / n);
 }
 // Worker that owns unit u: the largest c with c W / C <= u.
 __host__ __device__ inline int share_owner(int W, int C, int u) {
@@ -94,18 +96,16 @@ struct Share {
   Entry e;        // that entry
 };
 
-// The shares of the CTA's kWorkers workers (worker w of CTA c is number c + w x CTAs: the first
-// units go to different SMs).  Called by all kThreads threads; `shares` in shared memory is
-// complete when it returns.
-template <int R, int KT, int kThreads, int kDirectTiles, int kWorkers>
-__device__ void make_shares(const PagedArgs& a, Share* shares) {
-  constexpr int kWarps = kThreads / 32;
-  __shared__ int red[3][kWarps];
-  __shared__ int scan[kWarps];
-  const KeyList& l = a.list;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int seg = 0, til = 0, mx = 0;   // over all entries
-  Entry mine{};                   // entry tid, then b0 + tid
+// What a list's entries add up to; red: the warps' sums in shared memory.
+struct Totals {
+  int seg, til, mx;  // segments, key tiles, the most of a segment
+};
+template <int R, int KT, int kThreads>
+__device__ __forceinline__ void sum_entries(const PagedArgs& a, const KeyList& l, Entry& mine,
+                                            int (*red)[kThreads / 32]) {
+  const int tid = threadIdx.x;
+  int seg = 0, til = 0, mx = 0;
+  mine = Entry{};  // entry tid
   for (int b = tid; b < l.count; b += kThreads) {
     const Entry e = entry_of<R, KT>(l, a, b, blockIdx.x == 0);
     if (b == tid) mine = e;
@@ -116,27 +116,42 @@ __device__ void make_shares(const PagedArgs& a, Share* shares) {
   seg = __reduce_add_sync(~0u, seg);
   til = __reduce_add_sync(~0u, til);
   mx = __reduce_max_sync(~0u, mx);
-  if (lane == 0) {
-    red[0][warp] = seg;
-    red[1][warp] = til;
-    red[2][warp] = mx;
+  if ((tid & 31) == 0) {
+    red[0][tid >> 5] = seg;
+    red[1][tid >> 5] = til;
+    red[2][tid >> 5] = mx;
   }
-  __syncthreads();
-  seg = til = mx = 0;
+}
+template <int kWarps>
+__device__ __forceinline__ Totals totals_of(const int (*red)[kWarps]) {
+  Totals t{0, 0, 0};
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    seg += red[0][w];
-    til += red[1][w];
-    mx = max(mx, red[2][w]);
+    t.seg += red[0][w];
+    t.til += red[1][w];
+    t.mx = max(t.mx, red[2][w]);
   }
-  const bool direct = mx <= kDirectTiles;
-  const int W = direct ? seg : til;
+  return t;
+}
+
+// The shares of the kWorkers workers of CTA `cta` of the `ctas` that work on list l (worker w of
+// CTA c is number c + w x ctas: the first units go to different SMs), from the list's totals and
+// this thread's entry.  Called by all kThreads threads; `shares` in shared memory is complete when
+// it returns.
+template <int R, int KT, int kThreads, int kDirectTiles, int kWorkers>
+__device__ __forceinline__ void share_list(const PagedArgs& a, const KeyList& l, const Totals& t,
+                                           Entry mine, int cta, int ctas, int* scan,
+                                           Share* shares) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool direct = t.mx <= kDirectTiles;
+  const int W = direct ? t.seg : t.til;
   // a share of fewer than kDirectTiles / 2 tiles is not worth a slot
   const int most = direct ? W : (W + kDirectTiles / 2 - 1) / (kDirectTiles / 2);
-  const int C = min(most, static_cast<int>(gridDim.x) * kWorkers);
+  const int C = min(most, ctas * kWorkers);
   if (tid < kWorkers) {
     Share& s = shares[tid];
-    const int c = blockIdx.x + tid * gridDim.x;
+    const int c = cta + tid * ctas;
     s.W = W;
     s.C = C;
     s.direct = direct;
@@ -187,6 +202,26 @@ __device__ void make_shares(const PagedArgs& a, Share* shares) {
   __syncthreads();
 }
 
+// One list, all CTAs.
+template <int R, int KT, int kThreads, int kDirectTiles, int kWorkers>
+__device__ __forceinline__ void make_shares(const PagedArgs& a, Share* shares) {
+  __shared__ int red[3][kThreads / 32];
+  __shared__ int scan[kThreads / 32];
+  Entry mine;
+  sum_entries<R, KT, kThreads>(a, a.list[0], mine, red);
+  __syncthreads();
+  share_list<R, KT, kThreads, kDirectTiles, kWorkers>(a, a.list[0], totals_of(red), mine,
+                                                      blockIdx.x, gridDim.x, scan, shares);
+}
+
+// CTAs of `ctas` that work on list 1 when a tile of list i costs cost[i].
+__device__ __forceinline__ int ctas_of_second(int ctas, const Totals (&t)[2],
+                                              const float (&cost)[2]) {
+  if (t[1].til == 0 || t[0].til == 0) return t[1].til == 0 ? 0 : ctas;
+  const float c0 = t[0].til * cost[0], c1 = t[1].til * cost[1];
+  return min(max(__float2int_rn(ctas * (c1 / (c0 + c1))), 1), ctas - 1);
+}
+
 // A worker's piece of one segment: key tiles [ta, te) of row tile r for key/value head hk.
 struct Piece {
   int hk, r, ta, te;
@@ -205,7 +240,7 @@ struct Walk {
   bool direct;
   Entry e;
 
-  __device__ Walk(const PagedArgs& a, const Share& sh)
+  __device__ Walk(const PagedArgs& a, const KeyList& l, const Share& sh)
       : u0(sh.u0), u1(sh.b < 0 ? sh.u0 : sh.u1), b(sh.b), hk(0), r(0), te(-1), direct(sh.direct),
         e(sh.e) {
     if (u0 >= u1) return;
@@ -216,16 +251,16 @@ struct Walk {
       r = rem;
       return;
     }
-    for (int n; rem >= (n = tiles_of<R, KT>(e, a.list.causal, a.G, r)); ++r) rem -= n;
+    for (int n; rem >= (n = tiles_of<R, KT>(e, l.causal, a.G, r)); ++r) rem -= n;
     te = rem + 1;
   }
-  __device__ bool next(const PagedArgs& a, Piece& p) {
+  __device__ bool next(const PagedArgs& a, const KeyList& l, Piece& p) {
     if (u0 >= u1) return false;
     if (r < 0) {
       if (--hk < 0) {
         do {                           // the entry before with tokens
           if (--b < 0) return false;   // cannot happen while u1 > u0
-          e = entry_of<R, KT>(a.list, a, b, false);
+          e = entry_of<R, KT>(l, a, b, false);
         } while (e.rt == 0);
         hk = a.Hkv - 1;
       }
@@ -233,7 +268,7 @@ struct Walk {
     }
     p.hk = hk;
     p.r = r--;
-    p.tiles = tiles_of<R, KT>(e, a.list.causal, a.G, p.r);
+    p.tiles = tiles_of<R, KT>(e, l.causal, a.G, p.r);
     if (direct) {
       p.ta = 0;
       p.te = p.tiles;
