@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Share shares[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  touch(a);
   begin_launch();
   int li = 0;
   if constexpr (kLists == 1) {
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
     auto slot = [&](int i) { return p.slots + ((span.x + i) * 2 + (i == 0)) * size; };
     // this group's parts: i0, i0 + kSplit, ...; eight at a time, one lane each for m and l
     for (int i0 = kSplit == 1 ? 0 : group; i0 < span.y; i0 += kLanes * kSplit) {
-      const int mine = i0 + sub * kSplit;
+      const int mine = i0 + sub * kSplit, count = min(kLanes, (span.y - i0 + kSplit - 1) / kSplit);
       float pm = -INFINITY, pl = 0.f;
       if (mine < span.y) {
         const float* st = one ? a.rowbuf[li] + static_cast<int64_t>(rows) * D + id
@@ -136,6 +137,17 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
         pm = st[0];
         pl = st[one ? rows : p.R];
       }
+      // two parts' O at a time, the first two on the way together with m and l
+      float4 v[2][E];
+      auto fetch = [&](int i, float4 (&to)[E]) {
+        const float4* po = reinterpret_cast<const float4*>(
+            one ? a.rowbuf[li] + static_cast<int64_t>(id) * D : slot(i0 + i * kSplit) + rr[li] * D);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          to[e] = i < count ? po[e * kLanes + sub] : make_float4(0.f, 0.f, 0.f, 0.f);
+      };
+      fetch(0, v[0]);
+      fetch(1, v[1]);
       float top = pm;
 #pragma unroll
       for (int x = kLanes / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, x));
@@ -152,19 +164,19 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
       for (int e = 0; e < E; ++e) {
         o[e].x *= keep; o[e].y *= keep; o[e].z *= keep; o[e].w *= keep;
       }
-      const int count = min(kLanes, (span.y - i0 + kSplit - 1) / kSplit);
-#pragma unroll 2
-      for (int i = 0; i < count; ++i) {
-        const float wi = __shfl_sync(mask, w, i, kLanes);
-        const float4* po = reinterpret_cast<const float4*>(
-            one ? a.rowbuf[li] + static_cast<int64_t>(id) * D : slot(i0 + i * kSplit) + rr[li] * D);
+      for (int i = 0; i < count; i += 2) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float4 v = po[e * kLanes + sub];
-          o[e].x = fmaf(wi, v.x, o[e].x);
-          o[e].y = fmaf(wi, v.y, o[e].y);
-          o[e].z = fmaf(wi, v.z, o[e].z);
-          o[e].w = fmaf(wi, v.w, o[e].w);
+        for (int k = 0; k < 2; ++k) {
+          const float wi = __shfl_sync(mask, w, i + k, kLanes);  // 0 past the last part
+          if (i + k >= count) break;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            o[e].x = fmaf(wi, v[k][e].x, o[e].x);
+            o[e].y = fmaf(wi, v[k][e].y, o[e].y);
+            o[e].z = fmaf(wi, v[k][e].z, o[e].z);
+            o[e].w = fmaf(wi, v[k][e].w, o[e].w);
+          }
+          if (i + k + 2 < count) fetch(i + k + 2, v[k]);
         }
       }
     }

@@ -56,20 +56,18 @@ __host__ __device__ inline int resolve_page(const int32_t* row, int max_pages, i
   return (p < 0 || p >= num_pages) ? -1 : p;
 }
 
-// Bounds of new tokens [cu[b], cu[b + 1]) in packed tensors of `total` tokens, clamped like
-// seq_bounds (cu == nullptr: one token per sequence).
-__host__ __device__ inline void token_bounds(const int32_t* cu, int b, int total, int& start,
-                                             int& n) {
-  int s0 = cu != nullptr ? cu[b] : b;
-  int s1 = cu != nullptr ? cu[b + 1] : b + 1;
+// Tokens [s0, s1) of `total`, clamped.
+__host__ __device__ inline void clamp_tokens(int s0, int s1, int total, int& start, int& n) {
   s0 = s0 < 0 ? 0 : (s0 > total ? total : s0);
   s1 = s1 < s0 ? s0 : (s1 > total ? total : s1);
   start = s0;
   n = s1 - s0;
 }
-// Offsets that ascend inside [0, total]: then no two entries share a token.
-__host__ __device__ inline bool offsets_ok(const int32_t* cu, int b, int total) {
-  return cu == nullptr || (cu[b] >= 0 && cu[b] <= cu[b + 1] && cu[b + 1] <= total);
+// Bounds of new tokens [cu[b], cu[b + 1]) in packed tensors of `total` tokens, clamped like
+// seq_bounds (cu == nullptr: one token per sequence).
+__host__ __device__ inline void token_bounds(const int32_t* cu, int b, int total, int& start,
+                                             int& n) {
+  clamp_tokens(cu != nullptr ? cu[b] : b, cu != nullptr ? cu[b + 1] : b + 1, total, start, n);
 }
 // Sequence whose tokens include t: the last b with cu[b] <= t (empty sequences skipped), or -1
 // when t lies behind cu[B] or before cu[0].

@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   // the share of the list that this CTA works on
+  touch(a);
   begin_launch();
   int li = 0;
   if constexpr (kLists == 1) {

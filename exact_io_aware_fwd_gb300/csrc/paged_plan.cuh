@@ -20,6 +20,14 @@
 
 namespace fa {
 
+// Reads the launch's arguments while the kernel ahead still runs: they are in the constant cache
+// when they are needed.
+__device__ __forceinline__ void touch(const PagedArgs& a) {
+  asm volatile("" ::"r"(a.B), "r"(a.list[0].count), "l"(a.list[0].group_cu), "l"(a.list[1].lens),
+               "r"(a.list[1].causal), "l"(a.part[0].spans), "l"(a.part[1].slots),
+               "l"(a.rowbuf[0]), "l"(a.status));
+}
+
 struct Entry {
   int start, n, nc;  // first token, new tokens, and how many of them are computed
   int len;           // keys (clamped)
@@ -42,24 +50,23 @@ template <int R, int KT>
 __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b,
                                             bool report) {
   Entry e;
+  const int len = __ldg(l.lens + b);  // ahead of the branches: one wait for all of the loads
   bool ok;
   if (l.group_cu != nullptr) {
-    ok = offsets_ok(l.group_cu, b, a.B);
-    int s0 = __ldg(l.group_cu + b), s1 = __ldg(l.group_cu + b + 1);
-    s0 = min(max(s0, 0), a.B);
-    s1 = min(max(s1, s0), a.B);
-    int t0 = a.cu != nullptr ? __ldg(a.cu + s0) : s0, t1 = a.cu != nullptr ? __ldg(a.cu + s1) : s1;
-    t0 = min(max(t0, 0), a.total);
-    t1 = min(max(t1, t0), a.total);
-    e.start = t0;
-    e.n = t1 - t0;
+    const int g0 = __ldg(l.group_cu + b), g1 = __ldg(l.group_cu + b + 1);
+    const int s0 = min(max(g0, 0), a.B), s1 = min(max(g1, s0), a.B);
+    const int t0 = a.cu != nullptr ? __ldg(a.cu + s0) : s0;
+    const int t1 = a.cu != nullptr ? __ldg(a.cu + s1) : s1;
+    ok = (g0 >= 0) & (g0 <= g1) & (g1 <= a.B);
+    clamp_tokens(t0, t1, a.total, e.start, e.n);
   } else {
-    ok = offsets_ok(a.cu, b, a.total);
-    token_bounds(a.cu, b, a.total, e.start, e.n);
+    const int t0 = a.cu != nullptr ? __ldg(a.cu + b) : b;
+    const int t1 = a.cu != nullptr ? __ldg(a.cu + b + 1) : b + 1;
+    ok = (t0 >= 0) & (t0 <= t1) & (t1 <= a.total);
+    clamp_tokens(t0, t1, a.total, e.start, e.n);
   }
   const int64_t pages = static_cast<int64_t>(l.max_pages) << a.page_shift;
   const int cap = pages < l.max_len ? static_cast<int>(pages) : l.max_len;
-  const int len = __ldg(l.lens + b);
   e.len = min(max(len, 0), cap);
   e.nc = min(e.n, l.max_q);
   if (report && (!ok || e.len != len || e.nc != e.n)) atomicCAS(a.status, 0, kErrIndex);

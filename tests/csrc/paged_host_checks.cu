@@ -41,10 +41,6 @@ int main() {
     fa::token_bounds(bad, b, 10, start, n);
     CHECK(start >= 0 && n >= 0 && start + n <= 10);
   }
-  const bool well[4] = {false, false, false, false};
-  for (int b = 0; b < 4; ++b) CHECK(fa::offsets_ok(bad, b, 10) == well[b]);
-  for (int b = 0; b < 5; ++b) CHECK(fa::offsets_ok(cu, b, 4) && fa::offsets_ok(nullptr, b, 4));
-  CHECK(!fa::offsets_ok(cu, 3, 3));
   // row tiles of consecutive entries never overlap and stay inside the bound
   for (int R : {16, 128, 256})
     for (int G : {1, 3, 4, 5, 8, 32, 128})
