@@ -110,7 +110,7 @@ struct RopeArgs {
   int* status;
 };
 
-constexpr int kRopeBwdBlocks = 152 * 4;  // blocks of the backward (at most two more: one a kind)
+constexpr int kRopeBwdBlocks = 152 * 5;  // blocks of the backward (at most two more: one a kind)
 
 cudaError_t launch_rope_table(const double* inv_freq, int rot, int n_pos, float amplitude,
                               float* table, cudaStream_t s);

@@ -288,41 +288,39 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
 // (blocks [0, first_k), [first_k, first_v) and the rest), so that with norms a thread sums the
 // weight gradients of its eight elements over all its rows, a block leaves one partial [D], and
 // the sum over blocks (rope_dw_kernel) has a fixed order.  Rows come through a ring of
-// shared-memory stages filled by cp.async, one stage ahead of the arithmetic: each thread reads
-// back only what it copied itself, so the ring needs no barrier and serves as registers that
-// loads can be in flight to.  (16384 tokens of 48 heads: 104 us, with loads into registers alone
-// 110; 8 heads an item 104, 4 heads 123, 16 heads 108: an item's rows are far apart in the
-// attention layout and next to each other in the projection's.)
+// shared-memory stages filled by cp.async, one stage ahead of the arithmetic; a lane group reads
+// back only its own rows, so a warp-level barrier a stage is all the ring needs.  16384 tokens of
+// 48 heads: 97 us (548 MB, 5.6 TB/s); with each lane copying the two 8-byte halves that it reads,
+// through L1, 103, with loads into registers 110; 5 blocks an SM 97, 4 blocks 100, 6 blocks (no L1
+// left) 101; three stages 102, half as many rows a stage 109; 4 or 16 heads an item 19% and 4%
+// slower (an item's rows are far apart in the attention layout and next to each other in the
+// projection's).
 constexpr int kBwdRows = 4;    // rows of a stage
 constexpr int kBwdStages = 2;
 constexpr uint32_t kBwdStage = kBwdRows * 2 * 16 * kThreads;  // dz and x, 16 bytes a thread and row
 constexpr uint32_t kBwdSmem = kBwdStages * kBwdStage;
-constexpr int kBwdBlocksPerSm = 4;
+constexpr int kBwdBlocksPerSm = 5;
 
-template <bool kInter>
-__device__ __forceinline__ void copy_row(uint32_t dst, const __nv_bfloat16* row, int gap) {
-  if (kInter) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(row) : "memory");
-  } else {  // the two halves of a row's 16 bytes kThreads * 8 bytes apart: no bank conflicts
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(row) : "memory");
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + kThreads * 8),
-                 "l"(row + gap)
-                 : "memory");
-  }
+__device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// The lane's two groups of four of a row in shared memory.
 template <bool kInter>
-__device__ __forceinline__ Row8 read_row(uint32_t src) {
+__device__ __forceinline__ Row8 read_row(uint32_t row, int off0, int off1) {
   Row8 r;
   if (kInter) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.b.x), "=r"(r.b.y)
-                 : "r"(src)
+                 : "r"(row + 2 * off0)
                  : "memory");
   } else {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.a.x), "=r"(r.a.y) : "r"(src) : "memory");
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(r.a.x), "=r"(r.a.y)
+                 : "r"(row + 2 * off0)
+                 : "memory");
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
                  : "=r"(r.b.x), "=r"(r.b.y)
-                 : "r"(src + kThreads * 8)
+                 : "r"(row + 2 * off1)
                  : "memory");
   }
   return r;
@@ -378,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(con
   const bool norm = kind != 2 && weight != nullptr;
   Vec8 w{}, dw{};
   if (norm) w = load_weight(weight, lp.off0, lp.off1);
-  const uint32_t base = smem_u32(ring) + threadIdx.x * (kInter ? 16 : 8);
+  const uint32_t base = smem_u32(ring) + grp * (D * 2);  // row (i, k) of the group: + (2 i + k) 16 kThreads
 
   RowCursor<G> load;
   load.heads = kind == 0 ? a.H : a.Hkv;
@@ -393,13 +391,13 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(con
   auto fill = [&]() {
     if (loading) {
       const uint32_t st = base + filled % kBwdStages * kBwdStage;
-      const __nv_bfloat16* src = row_of(in, load.b, load.n, load.h) + lp.off0;
-      const __nv_bfloat16* xs = norm ? row_of(fwd, load.b, load.n, load.h) + lp.off0 : nullptr;
+      const __nv_bfloat16* src = row_of(in, load.b, load.n, load.h) + 8 * j;
+      const __nv_bfloat16* xs = norm ? row_of(fwd, load.b, load.n, load.h) + 8 * j : nullptr;
 #pragma unroll
       for (int i = 0; i < kBwdRows; ++i) {
         if (load.h + i >= load.h1) break;
-        copy_row<kInter>(st + i * 2 * 16 * kThreads, src + i * in.head, gap);
-        if (norm) copy_row<kInter>(st + (i * 2 + 1) * 16 * kThreads, xs + i * fwd.head, gap);
+        copy16(st + i * 2 * 16 * kThreads + 16 * j, src + i * in.head);
+        if (norm) copy16(st + (i * 2 + 1) * 16 * kThreads + 16 * j, xs + i * fwd.head);
       }
       loading = load.next(a);
     }
@@ -411,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(con
   int token = -1;
   while (working) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 2) : "memory");
+    __syncwarp(mask);  // the group's copies of this stage are here, its reads of the last one done
     const uint32_t st = base + done % kBwdStages * kBwdStage;
     if (kind != 2 && token != work.t) {
       token = work.t;
@@ -424,12 +423,12 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(con
 #pragma unroll
     for (int i = 0; i < kBwdRows; ++i) {
       if (work.h + i >= work.h1) break;
-      Row8 r = read_row<kInter>(st + i * 2 * 16 * kThreads);
+      Row8 r = read_row<kInter>(st + i * 2 * 16 * kThreads, lp.off0, lp.off1);
       if (kind != 2) {
         Vec8 g = unpack(r);
         turn<kInter>(g, angles, turned);
         if (norm) {
-          const Vec8 x = unpack(read_row<kInter>(st + (i * 2 + 1) * 16 * kThreads));
+          const Vec8 x = unpack(read_row<kInter>(st + (i * 2 + 1) * 16 * kThreads, lp.off0, lp.off1));
           Vec8 u;
 #pragma unroll
           for (int e = 0; e < 4; ++e) u.v[e] = mul2(g.v[e], w.v[e]);

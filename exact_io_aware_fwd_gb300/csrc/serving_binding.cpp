@@ -134,6 +134,16 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
   return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
 
+// Rows [first, first + n) of dimension `dim` of a new tensor, as a tensor of its own.
+at::Tensor part_of(const at::Tensor& t, int64_t dim, int64_t first, int64_t n) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(t.storage()),
+                                                   t.key_set(), t.dtype());
+  c10::SmallVector<int64_t, 5> sizes(t.sizes().begin(), t.sizes().end());
+  sizes[dim] = n;
+  impl->set_sizes_and_strides(sizes, t.strides(), t.storage_offset() + first * t.stride(dim));
+  return at::Tensor(std::move(impl));
+}
+
 // An output: the caller's, whose elements must be distinct (no expanded or overlapping
 // dimensions), or a new contiguous tensor.
 at::Tensor own_rows(const at::Tensor* given, at::IntArrayRef shape, Order order, at::Device dev,
@@ -334,9 +344,9 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
   if (given[0] == nullptr && given[1] == nullptr && given[2] == nullptr) {
     // the gradient of a fused projection: slices of one tensor
     const at::Tensor fused = fresh(shape(H + (dv != nullptr ? 2 : 1) * Hkv), at::kBFloat16, dev);
-    out_t[0] = fused.narrow(-2, 0, H);
-    out_t[1] = fused.narrow(-2, H, Hkv);
-    if (dv != nullptr) out_t[2] = fused.narrow(-2, H + Hkv, Hkv);
+    out_t[0] = part_of(fused, nd - 2, 0, H);
+    out_t[1] = part_of(fused, nd - 2, H, Hkv);
+    if (dv != nullptr) out_t[2] = part_of(fused, nd - 2, H + Hkv, Hkv);
     for (int i = 0; i < 3; ++i) given[i] = out_t[i].defined() ? &out_t[i] : nullptr;
   }
   const bool empty = B == 0 || N == 0;
@@ -356,8 +366,9 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
   at::Tensor dwq, dwk;
   Workspace ws;
   if (norm) {
-    dwq = fresh({d}, at::kFloat, dev);
-    dwk = fresh({d}, at::kFloat, dev);
+    const at::Tensor dw = fresh({2 * d}, at::kFloat, dev);
+    dwq = part_of(dw, 0, 0, d);
+    dwk = part_of(dw, 0, d, d);
     ws = workspace(tensor_or_none(a[14], "workspace"), p_rope_bwd_ws(dim32(d)), dev);
   }
   check(p_rope_bwd(grad, norm ? x : nullptr, out, norm ? dwq.data_ptr<float>() : nullptr,
