@@ -15,7 +15,6 @@ constexpr float kLn2 = 0.693147180559945309f;
 // With two lists the CTAs are divided by the lists' tiles, which cost the same.
 template <int D, int kLists>
 __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ PagedArgs a) {
-  using rows16::kDirectTiles;
   using rows16::KT;
   using rows16::R;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -25,7 +24,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   begin_launch();
   int li = 0;
   if constexpr (kLists == 1) {
-    make_shares<R, KT, kThreads, kDirectTiles, kWarps>(a, shares);
+    make_shares<R, KT, kThreads, kWarps>(a, shares);
   } else {
     __shared__ int red[2][3][kWarps], scan[kWarps];
     Entry mine[2];
@@ -36,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     const float cost[2] = {1.f, 1.f};
     const int n1 = ctas_of_second(gridDim.x, t, cost), cta = blockIdx.x;
     li = cta < n1 ? 1 : 0;
-    share_list<R, KT, kThreads, kDirectTiles, kWarps>(
+    share_list<R, KT, kThreads, kWarps>(
         a, a.list[li], li ? t[1] : t[0], li ? mine[1] : mine[0], li ? cta : cta - n1,
         li ? n1 : static_cast<int>(gridDim.x) - n1, scan, shares);
   }

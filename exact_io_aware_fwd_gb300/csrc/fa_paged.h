@@ -132,6 +132,7 @@ struct KeyList {
   const int32_t* group_cu;  // groups: [count + 1] over sequences, or nullptr
   int causal;
   int mma;                  // row tiles and key tiles of the tensor-core kernel
+  int unsplit;              // no segment is split where none has more key tiles
 };
 
 // Partial results of one list.  Its rows (query token x head of the key/value head's group) are
@@ -184,10 +185,9 @@ struct JoinArgs {
 constexpr int kPagedRows = 16;           // rows of a tile
 constexpr int kPagedCtas = 152;          // CTAs of a launch: one per SM
 constexpr int kPagedWarps = 8;           // warps of a CTA, each a worker
-constexpr int kPagedUnsplitKeys = 256;   // where no entry has more keys, none is split
-
-constexpr int kPagedMmaRows = 256;       // rows of a tile of the tensor-core kernel, whose CTAs
-constexpr int kPagedMmaUnsplitKeys = 512;  // are the workers
+constexpr int kPagedKeys = 16;           // keys of a tile
+constexpr int kPagedMmaRows = 256;       // the tensor-core kernel, whose CTAs are the workers
+constexpr int kPagedMmaKeys = 128;
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s);
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -30,8 +30,7 @@ namespace {
 
 constexpr int kThreads = 384;  // warp 0: TMA, 1: MMA, 2: pieces, 4-7 and 8-11: softmax
 constexpr int R = kPagedMmaRows;
-constexpr int KT = 128;
-constexpr int kDirectTiles = kPagedMmaUnsplitKeys / KT;
+constexpr int KT = kPagedMmaKeys;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // What the roles need to know of a piece, in a ring of shared memory.
@@ -142,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   begin_launch();
   int li = 0;
   if constexpr (kLists == 1) {
-    make_shares<R, KT, kThreads, kDirectTiles, 1>(a, shares);
+    make_shares<R, KT, kThreads, 1>(a, shares);
   } else {
     __shared__ int red[2][3][kThreads / 32], scan[kThreads / 32];
     Entry mine[2];
@@ -163,9 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Totals ti = li ? t[1] : t[0];
     const Entry own = li ? mine[1] : mine[0];
     if (a.list[li].mma)
-      share_list<R, KT, kThreads, kDirectTiles, 1>(a, a.list[li], ti, own, cta, ctas, scan, shares);
+      share_list<R, KT, kThreads, 1>(a, a.list[li], ti, own, cta, ctas, scan, shares);
     else
-      share_list<rows16::R, rows16::KT, kThreads, rows16::kDirectTiles, kPagedWarps>(
+      share_list<rows16::R, rows16::KT, kThreads, kPagedWarps>(
           a, a.list[li], ti, own, cta, ctas, scan, shares);
   }
   const KeyList& l = a.list[li];

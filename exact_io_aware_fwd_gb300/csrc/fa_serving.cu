@@ -118,6 +118,16 @@ bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int H
 // 16 and 83 with 32.
 constexpr long long mma_rows(int d) { return d == 64 ? 32 : 16; }
 
+// Keys up to which no entry is split, so that there is nothing to join.  Few rows: a warp takes
+// 0.27 us a tile (16 keys), the join 4 to 5 us, so 128 keys (one sequence of 8 heads and 128 keys:
+// 8.3 us unsplit and 8.7 split, 192 keys: 10.6 and 8.7); where the segments keep half of the warps
+// busy, 256 (64 sequences of 8 heads and 256 keys: 13.4 and 15.2).  The tensor-core kernel: 512 (4
+// sequences of 40 tokens and 300 keys 13.4 and 15.5 us, 32 of 500 keys 28.6 and 44).
+int unsplit_keys(bool mma, int count, int Hkv) {
+  if (mma) return 512;
+  return static_cast<long long>(count) * Hkv >= 2 * fa::kPagedCtas ? 256 : 128;
+}
+
 // How a call with shared prefixes divides the SMs (lists of both kinds of row tiles): a key tile of
 // the tensor-core kernel counts as this many of the other's.  One works at the tensor core's pace
 // and the other at memory's, so at once they take less than one after the other: 128 sequences of
@@ -198,7 +208,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     const long long keys = i == 0 ? max_kv : prefix->max_len;
     units[i] = Hkv * static_cast<long long>(fa::row_tiles_bound(
                          total, H / Hkv, mma[i] ? fa::kPagedMmaRows : fa::kPagedRows, count[i])) *
-               (keys / (mma[i] ? 128 : 16) + 1);
+               (keys / (mma[i] ? fa::kPagedMmaKeys : fa::kPagedKeys) + 1);
     if (units[i] > kMaxInt) return FA_ERR_UNSUPPORTED;
   }
   const PagedWorkspace w = paged_workspace(count, lists, total, H, Hkv, d);
@@ -252,6 +262,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     l.group_cu = i == 0 ? nullptr : prefix->group_cu;
     l.causal = i == 0 && causal ? 1 : 0;
     l.mma = mma[i];
+    l.unsplit = unsplit_keys(mma[i], l.count, Hkv) / (mma[i] ? fa::kPagedMmaKeys : fa::kPagedKeys);
     a.rowbuf[i] = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
     fa::PartialLayout& p = a.part[i];
     p.R = mma[i] ? fa::kPagedMmaRows : fa::kPagedRows;
@@ -269,7 +280,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
                               : fa::launch_paged(d, a, lists, all, s))) != FA_OK)
     return st;
   // no entry can have been split (lengths are clamped to max_kv): every result is final
-  if (lists == 1 && max_kv <= (mma[0] ? fa::kPagedMmaUnsplitKeys : fa::kPagedUnsplitKeys))
+  if (lists == 1 && max_kv <= unsplit_keys(mma[0], B, Hkv))
     return FA_OK;
   return status_of(fa::launch_paged_join(d, j, s));
 }

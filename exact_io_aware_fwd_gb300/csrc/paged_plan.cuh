@@ -5,7 +5,7 @@
 // (KT keys) as the tile's last row sees.  Laid end to end, the segments' key tiles are units
 // 0 .. W - 1, and worker c of C takes units [c W / C, (c + 1) W / C): equal shares whatever the
 // lengths, at most two unfinished segments per worker, so the partial results take 2 C slots
-// however long the cache is.  When no segment has more than kDirectTiles key tiles, splitting
+// however long the cache is.  When no segment has more than `unsplit` key tiles, splitting
 // would cost more than it gives (a join kernel has to read the parts back): then a unit is a
 // whole segment.  Lengths live on the device, so every CTA works this out for itself from one
 // pass over them.  Units fit 32 bits (the host refuses more).
@@ -145,16 +145,17 @@ __device__ __forceinline__ Totals totals_of(const int (*red)[kWarps]) {
 // CTA c is number c + w x ctas: the first units go to different SMs), from the list's totals and
 // this thread's entry.  Called by all kThreads threads; `shares` in shared memory is complete when
 // it returns.
-template <int R, int KT, int kThreads, int kDirectTiles, int kWorkers>
+template <int R, int KT, int kThreads, int kWorkers>
 __device__ __forceinline__ void share_list(const PagedArgs& a, const KeyList& l, const Totals& t,
                                            Entry mine, int cta, int ctas, int* scan,
                                            Share* shares) {
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool direct = t.mx <= kDirectTiles;
+  const bool direct = t.mx <= l.unsplit;
   const int W = direct ? t.seg : t.til;
-  // a share of fewer than kDirectTiles / 2 tiles is not worth a slot
-  const int most = direct ? W : (W + kDirectTiles / 2 - 1) / (kDirectTiles / 2);
+  // shares of one tile are not worth their slots (one sequence of 1000 keys and 8 heads takes 10.1
+  // us either way; shares of at least four take 11.5 us, of eight 13.4)
+  const int most = direct ? W : (W + 1) / 2;
   const int C = min(most, ctas * kWorkers);
   if (tid < kWorkers) {
     Share& s = shares[tid];
@@ -210,14 +211,14 @@ __device__ __forceinline__ void share_list(const PagedArgs& a, const KeyList& l,
 }
 
 // One list, all CTAs.
-template <int R, int KT, int kThreads, int kDirectTiles, int kWorkers>
+template <int R, int KT, int kThreads, int kWorkers>
 __device__ __forceinline__ void make_shares(const PagedArgs& a, Share* shares) {
   __shared__ int red[3][kThreads / 32];
   __shared__ int scan[kThreads / 32];
   Entry mine;
   sum_entries<R, KT, kThreads>(a, a.list[0], mine, red);
   __syncthreads();
-  share_list<R, KT, kThreads, kDirectTiles, kWorkers>(a, a.list[0], totals_of(red), mine,
+  share_list<R, KT, kThreads, kWorkers>(a, a.list[0], totals_of(red), mine,
                                                       blockIdx.x, gridDim.x, scan, shares);
 }
 

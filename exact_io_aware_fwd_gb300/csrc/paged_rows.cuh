@@ -24,8 +24,7 @@ namespace rows16 {
 
 constexpr int kWarps = kPagedWarps, kThreads = 32 * kWarps;
 constexpr int R = kPagedRows;
-constexpr int KT = 16;                // keys of a step, and of a tile
-constexpr int kDirectTiles = kPagedUnsplitKeys / KT;  // one warp for a whole segment
+constexpr int KT = kPagedKeys;        // keys of a step, and of a tile
 constexpr float kLn2 = 0.693147180559945309f;
 
 // One CTA per SM: 8 warps x stages of 16 keys (192 KB: with all but one stage of each in flight,

@@ -141,6 +141,13 @@ def test_paged_many_ragged_sequences():
     run_paged(nq, lens, 4, 2, 64, 16, True, seed=10)
 
 
+@pytest.mark.parametrize("most", [127, 128, 129, 255, 256, 257])
+@pytest.mark.parametrize("B", [3, 80], ids=["few segments", "many segments"])
+def test_paged_at_the_lengths_where_splitting_begins(B, most):
+    lens = [most] + [1 + (37 * b) % most for b in range(1, B)]
+    run_paged([1] * B, lens, 8, 4, 64, 32, True, seed=most)
+
+
 def test_paged_more_sequences_than_threads():
     """The scan over the sequences takes several rounds (256 and 384 entries at a time)."""
     rng = np.random.default_rng(4)
