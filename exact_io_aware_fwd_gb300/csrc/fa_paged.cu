@@ -12,7 +12,7 @@ namespace {
 constexpr int kWarps = kPagedWarps, kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// With two lists the CTAs are divided by the lists' tiles, which cost the same.
+// With two lists the CTAs are divided between them.
 template <int D, int kLists>
 __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ PagedArgs a) {
   using rows16::KT;
@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     sum_entries<R, KT, kThreads>(a, a.list[1], mine[1], red[1]);
     __syncthreads();
     const Totals t[2] = {totals_of(red[0]), totals_of(red[1])};
-    const float cost[2] = {1.f, 1.f};
-    const int n1 = ctas_of_second(gridDim.x, t, cost), cta = blockIdx.x;
+    const int n1 = ctas_of_second(a, gridDim.x, t), cta = blockIdx.x;
     li = cta < n1 ? 1 : 0;
     share_list<R, KT, kThreads, kWarps>(
         a, a.list[li], li ? t[1] : t[0], li ? mine[1] : mine[0], li ? cta : cta - n1,
@@ -68,19 +67,19 @@ __device__ __forceinline__ int token_sequence_group(const int32_t* cu, int B, in
 }
 
 // O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i over a row's parts, in the order of the keys.
-// Bound by latency: spans, then m and l, then O, each from the one before.  A group of 8 lanes
-// takes a row (kSplit == 1, 16 rows a CTA: many rows of few parts), or the 16 groups of a CTA
-// take every 16th part of one row and meet in shared memory (kSplit == 16: few rows of many
-// parts, long contexts of small batches: 4 x 131072 keys, 38 parts, 20 us with one warp a row).
+// Bound by latency: spans, then m and l with the first parts of O, then the other parts.  kSplit
+// groups of 8 lanes take every kSplit-th part of a row and meet in shared memory (the host chooses
+// 1, 4 or 16 by the number of rows).
 template <int D, int kSplit>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs a) {
   constexpr int E = D / kLanes / 4;  // float4s of a lane
   let_next_launch();
+  constexpr int kRowsPerCta = kGroups / kSplit;
   const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int crow = group / kSplit, pick = group % kSplit;  // row of the CTA, first part
   const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
   const int rows = a.total * a.H;
-  const int64_t id64 = kSplit == 1 ? static_cast<int64_t>(blockIdx.x) * kGroups + group
-                                   : static_cast<int64_t>(blockIdx.x);
+  const int64_t id64 = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + crow;
   const bool inside = id64 < rows;
   const int id = inside ? static_cast<int>(id64) : 0;
   const int t = id / a.H, head = id - t * a.H, hk = head / a.G;
@@ -127,7 +126,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
     const int64_t size = static_cast<int64_t>(p.R) * (D + 2);
     auto slot = [&](int i) { return p.slots + ((span.x + i) * 2 + (i == 0)) * size; };
     // this group's parts: i0, i0 + kSplit, ...; eight at a time, one lane each for m and l
-    for (int i0 = kSplit == 1 ? 0 : group; i0 < span.y; i0 += kLanes * kSplit) {
+    for (int i0 = pick; i0 < span.y; i0 += kLanes * kSplit) {
       const int mine = i0 + sub * kSplit, count = min(kLanes, (span.y - i0 + kSplit - 1) / kSplit);
       float pm = -INFINITY, pl = 0.f;
       if (mine < span.y) {
@@ -190,19 +189,19 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
       sl[group] = lsum;
     }
     __syncthreads();
-    if (group != 0) return;
+    if (pick != 0) return;
     m = -INFINITY;
     lsum = 0.f;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sm[g]);
+    for (int g = 0; g < kSplit; ++g) m = fmaxf(m, sm[group + g]);
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int g = 0; g < kGroups; ++g) {
-      const float w = sm[g] == -INFINITY ? (sl[g] == 0.f ? 0.f : sl[g]) : ex2(sm[g] - m);
-      lsum = fmaf(w, sl[g], lsum);
+    for (int g = 0; g < kSplit; ++g) {
+      const float w = sm[group + g] == -INFINITY ? (sl[group + g] == 0.f ? 0.f : sl[group + g]) : ex2(sm[group + g] - m);
+      lsum = fmaf(w, sl[group + g], lsum);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float4 v = so[g][e * kLanes + sub];
+        const float4 v = so[group + g][e * kLanes + sub];
         o[e].x = fmaf(w, v.x, o[e].x);
         o[e].y = fmaf(w, v.y, o[e].y);
         o[e].z = fmaf(w, v.z, o[e].z);
@@ -231,6 +230,15 @@ cudaError_t launch_paged_d(const PagedArgs& a, int64_t max_units, cudaStream_t s
   return launch_chained(paged_kernel<D, kLists>, static_cast<unsigned>(ctas), kThreads, bytes, s, a);
 }
 
+template <int D>
+cudaError_t launch_join_d(const JoinArgs& a, int split, cudaStream_t s) {
+  const unsigned rows = static_cast<unsigned>(a.total) * static_cast<unsigned>(a.H);
+  const unsigned per = kGroups / split, grid = (rows + per - 1) / per;
+  if (split == 16) return launch_chained(paged_join_kernel<D, 16>, grid, kJoinThreads, 0, s, a);
+  if (split == 4) return launch_chained(paged_join_kernel<D, 4>, grid, kJoinThreads, 0, s, a);
+  return launch_chained(paged_join_kernel<D, 1>, grid, kJoinThreads, 0, s, a);
+}
+
 }  // namespace
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s) {
@@ -239,15 +247,8 @@ cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units
   return d == 64 ? launch_paged_d<64, 1>(a, max_units, s) : launch_paged_d<128, 1>(a, max_units, s);
 }
 
-cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s) {
-  const unsigned rows = static_cast<unsigned>(a.total) * static_cast<unsigned>(a.H);
-  // with few rows a row has many parts (all the workers' share in few segments)
-  if (rows <= 4 * kPagedCtas)
-    return d == 64 ? launch_chained(paged_join_kernel<64, kGroups>, rows, kJoinThreads, 0, s, a)
-                   : launch_chained(paged_join_kernel<128, kGroups>, rows, kJoinThreads, 0, s, a);
-  const unsigned grid = (rows + kGroups - 1) / kGroups;
-  return d == 64 ? launch_chained(paged_join_kernel<64, 1>, grid, kJoinThreads, 0, s, a)
-                 : launch_chained(paged_join_kernel<128, 1>, grid, kJoinThreads, 0, s, a);
+cudaError_t launch_paged_join(int d, const JoinArgs& a, int split, cudaStream_t s) {
+  return d == 64 ? launch_join_d<64>(a, split, s) : launch_join_d<128>(a, split, s);
 }
 
 }  // namespace fa

@@ -193,6 +193,7 @@ cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedArgs& a, int lists, int64_t max_units,
                              uint64_t timeout_ns, cudaStream_t s);
-cudaError_t launch_paged_join(int d, const JoinArgs& a, cudaStream_t s);
+// split: groups of 8 lanes that share a row (1, 4 or 16)
+cudaError_t launch_paged_join(int d, const JoinArgs& a, int split, cudaStream_t s);
 
 }  // namespace fa

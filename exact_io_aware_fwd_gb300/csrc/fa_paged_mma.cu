@@ -155,8 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     const Totals t[2] = {totals_of(red[0]), totals_of(red[1])};
-    const float cost[2] = {a.list[0].mma ? a.mma_cost : 1.f, a.list[1].mma ? a.mma_cost : 1.f};
-    const int n1 = ctas_of_second(gridDim.x, t, cost);
+    const int n1 = ctas_of_second(a, gridDim.x, t);
     li = static_cast<int>(blockIdx.x) < n1 ? 1 : 0;
     const int cta = li ? blockIdx.x : blockIdx.x - n1, ctas = li ? n1 : gridDim.x - n1;
     const Totals ti = li ? t[1] : t[0];

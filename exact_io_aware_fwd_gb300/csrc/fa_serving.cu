@@ -131,10 +131,18 @@ int unsplit_keys(bool mma, int count, int Hkv) {
 // How a call with shared prefixes divides the SMs (lists of both kinds of row tiles): a key tile of
 // the tensor-core kernel counts as this many of the other's.  One works at the tensor core's pace
 // and the other at memory's, so at once they take less than one after the other: 128 sequences of
-// 1..1024 keys behind two prefixes of 32768 138 us instead of 148 (136 with 14, 145 with 20), 64 of
-// 512 keys behind 4096 50 instead of 65; d = 64, 64 of 1024 behind 32768 60 instead of 80 (65 with
-// 20, 67 with 40).  Two lists of few rows: 8 short sequences behind 1000 keys 15 instead of 16.3.
-constexpr float mma_tile_cost(int d) { return d == 64 ? 28.f : 16.f; }
+// 1..1024 keys behind two prefixes of 32768 133 us instead of 148 (138 with 14 or 24, 160 with 30),
+// 64 of 512 keys behind 4096 47 instead of 65; d = 64, 64 of 1024 behind 32768 56 instead of 80 (63
+// with 18, 70 with 14).  Two lists of few rows: 8 short sequences behind 1000 keys 12 us.
+constexpr float mma_tile_cost(int d) { return d == 64 ? 30.f : 20.f; }
+
+// Groups of 8 lanes per row of the join.  A group reads its parts two at a time, so few rows, which
+// have many parts, take more groups: 128 rows of 39 parts 292 us with 16, 306 with 1 (4 x 131072
+// keys); 1472 rows of 19 parts 36 with 4, 41 with 1, 40 with 16; 4096 rows of 6 parts 135 with 1,
+// 141 with 4, 160 with 16.
+int join_split(long long rows) {
+  return rows <= 4 * fa::kPagedCtas ? 16 : (rows <= 16 * fa::kPagedCtas ? 4 : 1);
+}
 
 // Workspace of a paged call: the spans and slots of each list, then (joined lists) row buffers.
 // Which kernel a list takes is decided by max_q; with few rows in all it cannot be the
@@ -282,7 +290,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   // no entry can have been split (lengths are clamped to max_kv): every result is final
   if (lists == 1 && max_kv <= unsplit_keys(mma[0], B, Hkv))
     return FA_OK;
-  return status_of(fa::launch_paged_join(d, j, s));
+  return status_of(fa::launch_paged_join(d, j, join_split(static_cast<long long>(total) * H), s));
 }
 
 }  // namespace

@@ -222,11 +222,15 @@ __device__ __forceinline__ void make_shares(const PagedArgs& a, Share* shares) {
                                                       blockIdx.x, gridDim.x, scan, shares);
 }
 
-// CTAs of `ctas` that work on list 1 when a tile of list i costs cost[i].
-__device__ __forceinline__ int ctas_of_second(int ctas, const Totals (&t)[2],
-                                              const float (&cost)[2]) {
+// CTAs of `ctas` that work on list 1.  Costs are in key tiles of the few-row kernel, whose segments
+// cost 8 more each (their queries to load and result to write; 23 sequences without keys of their
+// own behind 24751: 35 us, 42 without the term); those of the tensor-core kernel are few.
+__device__ __forceinline__ float list_cost(const PagedArgs& a, const KeyList& l, const Totals& t) {
+  return l.mma ? t.til * a.mma_cost : t.til + 8.f * t.seg;
+}
+__device__ __forceinline__ int ctas_of_second(const PagedArgs& a, int ctas, const Totals (&t)[2]) {
   if (t[1].til == 0 || t[0].til == 0) return t[1].til == 0 ? 0 : ctas;
-  const float c0 = t[0].til * cost[0], c1 = t[1].til * cost[1];
+  const float c0 = list_cost(a, a.list[0], t[0]), c1 = list_cost(a, a.list[1], t[1]);
   return min(max(__float2int_rn(ctas * (c1 / (c0 + c1))), 1), ctas - 1);
 }
 

@@ -579,6 +579,19 @@ def test_shared_prefix_large_groups():
     run_prefix([150], [777], [1] * 150, rng.integers(0, 30, 150).tolist(), 6, 2, 64, 16, True, seed=72)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_prefix_lists_of_both_kinds(d):
+    """Each list on either kernel's tiles: long chunks behind few or many rows, groups without a
+    sequence, prefixes alone, own keys alone."""
+    rng = np.random.default_rng(18)
+    run_prefix([1, 0, 0, 0, 0, 0, 0, 0], [500] + [20] * 7, [40], [900], 2, 1, d, 64, True, seed=73)
+    run_prefix([2, 3], [3000, 40], [70, 1, 40, 100, 3], [70, 700, 60, 1200, 3], 8, 2, d, 32, True, seed=74)
+    run_prefix([2, 1], [4000, 10], [30, 50, 2], [30, 50, 2], 8, 2, d, 16, False, seed=75)
+    run_prefix([20, 30], [1700, 2400], [1] * 50, [0] * 50, 8, 1, d, 64, True, seed=76)
+    run_prefix([20, 30], [0, 0], [1] * 50, rng.integers(0, 400, 50).tolist(), 8, 1, d, 64, True, seed=77)
+    run_prefix([90], [0], [2] * 90, rng.integers(2, 300, 90).tolist(), 4, 1, d, 16, True, seed=78)
+
+
 def test_shared_prefix_defaults_repeat_and_graph():
     cache = Cache([20, 300, 41, 900, 700], 2, 64, 16, seed=81)
     k, v, table, ln = cache.dev()
