@@ -49,23 +49,6 @@ constexpr int kJoinThreads = 128;
 constexpr int kLanes = 8;                          // lanes of a group
 constexpr int kGroups = kJoinThreads / kLanes;     // groups of a CTA
 
-// token_sequence by a group of 8 lanes (`mask`: its lanes of the warp): 8 offsets a step.
-__device__ __forceinline__ int token_sequence_group(const int32_t* cu, int B, int t, int sub,
-                                                    unsigned mask) {
-  if (cu == nullptr) return t < B ? t : -1;
-  int lo = 0, n = B + 1;  // the last of the n offsets from lo that is <= t
-  while (true) {
-    const int step = (n + kLanes - 1) / kLanes;
-    const bool le = sub * step < n && __ldg(cu + lo + sub * step) <= t;
-    const int hits = __popc(__ballot_sync(mask, le) & mask);  // offsets ascend: a prefix of lanes
-    if (hits == 0) return -1;  // before cu[0]
-    n = min(step, n - (hits - 1) * step);
-    lo += (hits - 1) * step;
-    if (step == 1) break;
-  }
-  return lo < B ? lo : -1;  // behind cu[B]
-}
-
 // O = sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i over a row's parts, in the order of the keys.
 // Bound by latency: spans, then m and l with the first parts of O, then the other parts.  kSplit
 // groups of 8 lanes take every kSplit-th part of a row and meet in shared memory (the host chooses
@@ -83,7 +66,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
   const bool inside = id64 < rows;
   const int id = inside ? static_cast<int>(id64) : 0;
   const int t = id / a.H, head = id - t * a.H, hk = head / a.G;
-  const int seq = token_sequence_group(a.cu, a.B, t, sub, mask);
+  const int seq = token_sequence_group<kLanes>(a.cu, a.B, t, sub, mask);
   // where the row's parts are: its span and row tile in each list (these inputs are the call's)
   int where[2] = {-1, -1}, rr[2] = {0, 0};
   bool skip = !inside || seq < 0;
@@ -91,7 +74,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
     const KeyList& l = a.list[li];
     int b = seq, start, n;
     if (l.group_cu != nullptr) {
-      b = token_sequence_group(l.group_cu, l.count, seq, sub, mask);
+      b = token_sequence_group<kLanes>(l.group_cu, l.count, seq, sub, mask);
       if (b < 0) continue;  // a sequence of no group has no prefix
       const int s0 = min(max(__ldg(l.group_cu + b), 0), a.B);
       start = a.cu != nullptr ? min(max(__ldg(a.cu + s0), 0), a.total) : s0;

@@ -83,6 +83,26 @@ __host__ __device__ inline int token_sequence(const int32_t* cu, int B, int t) {
   return lo;
 }
 
+#ifdef __CUDACC__
+// token_sequence by a group of kLanes lanes (`mask`: its lanes of the warp), kLanes offsets a step.
+template <int kLanes>
+__device__ __forceinline__ int token_sequence_group(const int32_t* cu, int B, int t, int sub,
+                                                    unsigned mask) {
+  if (cu == nullptr) return t < B ? t : -1;
+  int lo = 0, n = B + 1;  // the last of the n offsets from lo that is <= t
+  while (true) {
+    const int step = (n + kLanes - 1) / kLanes;
+    const bool le = sub * step < n && __ldg(cu + lo + sub * step) <= t;
+    const int hits = __popc(__ballot_sync(mask, le) & mask);  // offsets ascend: a prefix of lanes
+    if (hits == 0) return -1;  // before cu[0]
+    n = min(step, n - (hits - 1) * step);
+    lo += (hits - 1) * step;
+    if (step == 1) break;
+  }
+  return lo < B ? lo : -1;  // behind cu[B]
+}
+#endif
+
 // ---- norm + rotation pass (fa_rope.cu)
 struct RowView {
   __nv_bfloat16* p;

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs a) {
   int b, n, pos;
   int64_t slot = -1;  // paged: element offset of the token's first head, or -1
   if constexpr (kPaged) {
-    const int seq = token_sequence(a.cu, a.seqs, t);
+    const int seq = token_sequence_group<L>(a.cu, a.seqs, t, j, mask);
     if (seq < 0) return;  // behind the last sequence
     int start, count;
     token_bounds(a.cu, seq, a.tokens, start, count);
@@ -533,9 +533,12 @@ cudaError_t bwd_t(RopeArgs a, float* dwq, float* dwk, cudaStream_t s) {
   const int64_t groups = (static_cast<int64_t>(a.tokens) + G - 1) / G;
   const int64_t items[3] = {groups * chunks_of(a.H, a.chunk), groups * chunks_of(a.Hkv, a.chunk),
                             a.v.p != nullptr ? groups * chunks_of(a.Hkv, a.chunk) : 0};
-  // blocks in proportion to the bytes of a kind's rows (with norms Q and K rows read x too)
+  // blocks in proportion to a kind's stages and the bytes of their rows (with norms Q and K rows
+  // read x too): a stage of one head takes about as long as one of four (11912 tokens of 4 + 1 + 1
+  // heads: 14 us, by bytes alone 19; with norms 19 and 25)
   const double cost = a.wq != nullptr ? 3 : 2;
-  const double bytes[3] = {cost * a.H, cost * a.Hkv, a.v.p != nullptr ? 2.0 * a.Hkv : 0.0};
+  const double bytes[3] = {cost * chunks_of(a.H, kBwdRows), cost * chunks_of(a.Hkv, kBwdRows),
+                           a.v.p != nullptr ? 2.0 * chunks_of(a.Hkv, kBwdRows) : 0.0};
   const double all = bytes[0] + bytes[1] + bytes[2];
   int blocks[3];
   for (int i = 0; i < 3; ++i) {
