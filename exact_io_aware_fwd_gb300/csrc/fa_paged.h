@@ -210,8 +210,9 @@ constexpr int kPagedMmaRows = 256;       // the tensor-core kernel, whose CTAs a
 constexpr int kPagedMmaKeys = 128;
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s);
+// twin: one list, and no entry has more than 128 rows
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedArgs& a, int lists, int64_t max_units,
+                             const PagedArgs& a, int lists, bool twin, int64_t max_units,
                              uint64_t timeout_ns, cudaStream_t s);
 // split: groups of 8 lanes that share a row (1, 4 or 16)
 cudaError_t launch_paged_join(int d, const JoinArgs& a, int split, cudaStream_t s);

@@ -35,7 +35,8 @@ constexpr float kLn2 = 0.693147180559945309f;
 
 // What the roles need to know of a piece, in a ring of shared memory.
 struct PieceInfo {
-  int n[2];        // key tiles of each query tile (the first n of the piece's); -1: no more pieces
+  int n[2];        // key tiles of each query tile: the first n of the piece's (kTwin: every other
+                   // one); -1: no more pieces
   int ta;          // first key tile
   int hk, row0;    // key/value head, first row of the row tile
   int start, rows; // the entry's first token and its rows (computed tokens x group)
@@ -45,6 +46,11 @@ struct PieceInfo {
   const int32_t* table;  // the entry's block-table row
 };
 constexpr int kRing = 4;
+// Key tiles (positions) of the piece.
+template <bool kTwin>
+__device__ __forceinline__ int positions(int n0, int n1) {
+  return kTwin ? n0 + n1 : max(n0, n1);
+}
 
 template <int D>
 struct MmaLayout {
@@ -80,7 +86,12 @@ __device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, in
 
 // kLists == 2: a call with shared prefixes, each list on its own part of the SMs.  The CTAs of a
 // list of few rows do what paged_kernel does, with the softmax warps as the workers.
-template <int D, int kLists>
+// kTwin: no entry has more than 128 rows, one query tile.  Both tile slots work on it, at alternate
+// positions, and their results are joined at a piece's end: with one slot, the chain S, softmax,
+// P V of a position is all that runs (126 sequences of 18 rows and 1576 keys 149 us, with one slot
+// 166; d = 64, 16 of 36 rows and 8192 keys 67 and 82).  Here K runs a position ahead of V: a V
+// stage is free only two positions later (211 us with K and V together).
+template <int D, int kLists, bool kTwin>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedArgs a,
@@ -93,7 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sm = smem_raw + pad;
   // what the roles signal through: static, so that its addresses are constants and take no registers
   __shared__ uint64_t q_full[1], k_full[S], k_empty[S], v_full[S], v_empty[S];
-  __shared__ uint64_t s_full[2], p_full[2], o_full[2], mma_done[1];
+  __shared__ uint64_t s_full[2], p_full[2], o_full[2], mma_done[1], twin_full[1];
+  __shared__ float twin_m[kTwin ? 128 : 1], twin_l[kTwin ? 128 : 1];
   __shared__ uint64_t piece_full[kRing], piece_empty[kRing];
   __shared__ PieceInfo pieces[kRing];
   __shared__ uint32_t tmem_slot[1];
@@ -101,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Share shares[kLists == 2 ? kPagedWarps : 1];
   const Ctl ctl{abort_flag, a.status, timeout_ns};
   const uint32_t warp = warp_id(), lane = lane_id();
-  if (pad + smem_of<D, kLists>() > smem_bytes) {  // cannot happen with the host's sizing; never proceed
+  if (pad + smem_of<D, kLists>() > smem_bytes) {  // cannot happen: the array is aligned; never proceed
     if (threadIdx.x == 0) atomicCAS(a.status, 0, kErrLayout);
     return;
   }
@@ -121,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&o_full[t], 1);
     }
     mbar_init(mma_done, 1);
+    mbar_init(twin_full, 4);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&piece_full[i], 1);
       mbar_init(&piece_empty[i], 10);  // TMA warp, MMA thread, 8 softmax warps
@@ -190,8 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait(&piece_empty[i % kRing], ((i / kRing) & 1) ^ 1, ctl)) break;
           PieceInfo& p = pieces[i % kRing];
           if (more) {
-            p.n[0] = tiles_in_piece(e, piece, l.causal, a.G, 0);
-            p.n[1] = tiles_in_piece(e, piece, l.causal, a.G, 1);
+            const int n0 = tiles_in_piece(e, piece, l.causal, a.G, 0);
+            p.n[0] = kTwin ? (n0 + 1) / 2 : n0;
+            p.n[1] = kTwin ? n0 / 2 : tiles_in_piece(e, piece, l.causal, a.G, 1);
             p.ta = piece.ta;
             p.hk = piece.hk;
             p.row0 = piece.r * R;
@@ -222,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0;; ++i) {
         if (!(ok = mbar_wait_warp(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
         const PieceInfo& p = pieces[i % kRing];
-        const int npos = max(p.n[0], p.n[1]);
+        const int npos = positions<kTwin>(p.n[0], p.n[1]);
         const int32_t* trow = p.table;
         const int len = p.len, hk = p.hk, ta = p.ta;
         __syncwarp();
@@ -237,23 +251,50 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (page < 0) atomicCAS(a.status, 0, kErrIndex);
           return page < 0 ? a.num_pages * a.Hkv : page * a.Hkv + hk;
         };
-        int z = 0, z_next = npos > 0 ? find(ta) : 0;
-        for (int j = 0; j < npos; ++j) {
-          const int s = jk % S;
-          const uint32_t ph = (jk / S) & 1;
-          z = z_next;
-          if (j + 1 < npos) z_next = find(ta + j + 1);
-          if (!(ok = mbar_wait_warp(&k_empty[s], ph ^ 1, ctl))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&k_full[s], L::kTile);
-          __syncwarp();
-          const uint32_t at = s * L::kTile + panel * 16384 + pg * (page_size * 128);
-          if (mine) tma_load_3d(sm + L::kK + at, &tmK, &k_full[s], panel * 64, 0, z);
-          ++jk;
-          if (!(ok = mbar_wait_warp(&v_empty[s], ph ^ 1, ctl))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&v_full[s], L::kTile);
-          __syncwarp();
-          if (mine) tma_load_3d(sm + L::kV + at, &tmV, &v_full[s], panel * 64, 0, z);
-          ++jv;
+        if constexpr (kTwin) {
+          // K runs one position ahead of V: a V stage is free only after its P V
+          int zk = npos > 0 ? find(ta) : 0, zv = zk;  // K's and V's pages of the next copies
+          for (int j = 0; j <= npos && npos > 0; ++j) {
+            if (j < npos) {
+              const int s = jk % S;
+              if (!(ok = mbar_wait_warp(&k_empty[s], ((jk / S) & 1) ^ 1, ctl))) break;
+              if (lane == 0) mbar_arrive_expect_tx(&k_full[s], L::kTile);
+              __syncwarp();
+              const uint32_t at = s * L::kTile + panel * 16384 + pg * (page_size * 128);
+              if (mine) tma_load_3d(sm + L::kK + at, &tmK, &k_full[s], panel * 64, 0, zk);
+              ++jk;
+            }
+            if (j > 0) {
+              const int s = jv % S;
+              if (!(ok = mbar_wait_warp(&v_empty[s], ((jv / S) & 1) ^ 1, ctl))) break;
+              if (lane == 0) mbar_arrive_expect_tx(&v_full[s], L::kTile);
+              __syncwarp();
+              const uint32_t at = s * L::kTile + panel * 16384 + pg * (page_size * 128);
+              if (mine) tma_load_3d(sm + L::kV + at, &tmV, &v_full[s], panel * 64, 0, zv);
+              ++jv;
+            }
+            zv = zk;
+            if (j + 1 < npos) zk = find(ta + j + 1);
+          }
+        } else {
+          int z = 0, z_next = npos > 0 ? find(ta) : 0;
+          for (int j = 0; j < npos; ++j) {
+            const int s = jk % S;
+            const uint32_t ph = (jk / S) & 1;
+            z = z_next;
+            if (j + 1 < npos) z_next = find(ta + j + 1);
+            if (!(ok = mbar_wait_warp(&k_empty[s], ph ^ 1, ctl))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&k_full[s], L::kTile);
+            __syncwarp();
+            const uint32_t at = s * L::kTile + panel * 16384 + pg * (page_size * 128);
+            if (mine) tma_load_3d(sm + L::kK + at, &tmK, &k_full[s], panel * 64, 0, z);
+            ++jk;
+            if (!(ok = mbar_wait_warp(&v_empty[s], ph ^ 1, ctl))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&v_full[s], L::kTile);
+            __syncwarp();
+            if (mine) tma_load_3d(sm + L::kV + at, &tmV, &v_full[s], panel * 64, 0, z);
+            ++jv;
+          }
         }
         if (!ok) break;
       }
@@ -274,38 +315,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = mbar_wait(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
           const int n[2] = {pieces[i % kRing].n[0], pieces[i % kRing].n[1]};
           mbar_arrive(&piece_empty[i % kRing]);
-          const int npos = max(n[0], n[1]);
+          const int npos = positions<kTwin>(n[0], n[1]);
           if (npos < 0) break;
           if (npos == 0) continue;
           if (!(ok = mbar_wait(q_full, segs & 1, ctl))) break;
           ++segs;
           tc_fence_after();
-          for (int j = 0; ok && j <= npos; ++j) {
-            const int jg = base + j, s = jg % S, sp = (jg + S - 1) % S;
-            if (j < npos && !(ok = mbar_wait(&k_full[s], (jg / S) & 1, ctl))) break;
-            if (j >= 1 && !(ok = mbar_wait(&v_full[sp], ((jg - 1) / S) & 1, ctl))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (j >= 1 && j - 1 < n[t]) {
-                if (!(ok = mbar_wait(&p_full[t], (issued[t] - 1) & 1, ctl))) break;
+          if constexpr (kTwin) {
+            // the slots take turns: P V of a position follows its S by two
+            for (int j = 0; j < npos + 2; ++j) {
+              const int jg = base + j, s = jg % S, sp = (jg - 2 + S) % S, t = j & 1;
+              if (j >= 2) {
+                if (!(ok = mbar_wait(&v_full[sp], ((jg - 2) / S) & 1, ctl))) break;
+                const int count = t == 0 ? issued[0] : issued[1];
+                if (!(ok = mbar_wait(&p_full[t], (count - 1) & 1, ctl))) break;
                 tc_fence_after();
                 mma_ts_k128_step8(tmem + L::kColO0 + D * t, tmem + L::kColS0 + 128 * t,
                                   sdesc_sw128(sbase + L::kV + sp * L::kTile, 16384, 1024), idO,
-                                  j > 1 ? 1u : 0u);
-                if (j == n[t]) mma_commit(&o_full[t]);  // the tile's last P V
+                                  j >= 4 ? 1u : 0u);
+                if (j >= npos) mma_commit(&o_full[t]);  // the slot's last P V
+                mma_commit(&v_empty[sp]);
               }
-              if (j < n[t]) {  // S_t overwrites P_t: after the tile's own P V
+              if (j < npos) {
+                if (!(ok = mbar_wait(&k_full[s], (jg / S) & 1, ctl))) break;
+                tc_fence_after();
                 mma_ss_kmajor<D>(tmem + L::kColS0 + 128 * t,
-                                 sdesc_sw128(sbase + L::kQ + t * L::kTile, 16384, 1024),
+                                 sdesc_sw128(sbase + L::kQ, 16384, 1024),
                                  sdesc_sw128(sbase + L::kK + s * L::kTile, 16384, 1024), idS, 0u);
                 mma_commit(&s_full[t]);
-                ++issued[t];
+                mma_commit(&k_empty[s]);
+                issued[0] += 1 - t;
+                issued[1] += t;
               }
             }
-            if (!ok) break;
-            if (j < npos) mma_commit(&k_empty[s]);
-            if (j >= 1) mma_commit(&v_empty[sp]);
+          } else {
+            for (int j = 0; ok && j <= npos; ++j) {
+              const int jg = base + j, s = jg % S, sp = (jg + S - 1) % S;
+              if (j < npos && !(ok = mbar_wait(&k_full[s], (jg / S) & 1, ctl))) break;
+              if (j >= 1 && !(ok = mbar_wait(&v_full[sp], ((jg - 1) / S) & 1, ctl))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                if (j >= 1 && j - 1 < n[t]) {
+                  if (!(ok = mbar_wait(&p_full[t], (issued[t] - 1) & 1, ctl))) break;
+                  tc_fence_after();
+                  mma_ts_k128_step8(tmem + L::kColO0 + D * t, tmem + L::kColS0 + 128 * t,
+                                    sdesc_sw128(sbase + L::kV + sp * L::kTile, 16384, 1024), idO,
+                                    j > 1 ? 1u : 0u);
+                  if (j == n[t]) mma_commit(&o_full[t]);  // the tile's last P V
+                }
+                if (j < n[t]) {  // S_t overwrites P_t: after the tile's own P V
+                  mma_ss_kmajor<D>(tmem + L::kColS0 + 128 * t,
+                                   sdesc_sw128(sbase + L::kQ + t * L::kTile, 16384, 1024),
+                                   sdesc_sw128(sbase + L::kK + s * L::kTile, 16384, 1024), idS, 0u);
+                  mma_commit(&s_full[t]);
+                  ++issued[t];
+                }
+              }
+              if (!ok) break;
+              if (j < npos) mma_commit(&k_empty[s]);
+              if (j >= 1) mma_commit(&v_empty[sp]);
+            }
           }
           base += npos;
         }
@@ -326,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_tile = sbase + L::kQ + t * L::kTile;
     const float c2 = a.scale_log2;
     int base = 0, segs = 0;  // positions and pieces with keys before this one
-    int seen = 0, outs = 0;  // S tiles and results of this query tile before this piece
+    int seen = 0, outs = 0;  // S tiles and results of this tile slot before this piece
+    int twins = 0;           // twin pieces before this one
     bool ok = true;
     if (few_rows)
       rows16::work<D>(a, l, part, rowbuf, shares[kLists == 2 ? warp - 4 : 0],
@@ -338,11 +409,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const PieceInfo& piece = pieces[i % kRing];  // held until the piece is done
       const int n_mine = piece.n[t];
       if (n_mine < 0) break;
-      const int npos = max(piece.n[0], piece.n[1]);
-      const int rows = piece.rows, r0 = piece.row0 + 128 * t;  // r0: the tile's first row
+      const int npos = positions<kTwin>(piece.n[0], piece.n[1]);
+      const int rows = piece.rows, r0 = piece.row0 + (kTwin ? 0 : 128 * t);  // r0: the tile's first row
       if (npos > 0) {
         // ---- the tile's queries: lanes 0-15 and 16-31 (d = 128) gather one row each time
-        if (n_mine > 0) {
+        if (n_mine > 0 && !(kTwin && t == 1)) {
           constexpr int GR = D / 8, RI = 32 / GR;  // granules of a row, rows per step
           const int g = lane % GR;
           // lane i works out row i's place; two rounds of loads that are in flight together
@@ -382,9 +453,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // position whose last page ends inside it: that page's rows past the end are cleared
       const int tail = len & ((1 << a.page_shift) - 1), j_tail = tail != 0 ? len / KT - ta : -1;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < n_mine; ++j) {
-        const int jg = base + j;
-        if (!(ok = mbar_wait_warp(&s_full[t], (seen + j) & 1, ctl))) break;
+      for (int i_mine = 0; i_mine < n_mine; ++i_mine) {
+        const int j = kTwin ? 2 * i_mine + t : i_mine, jg = base + j;
+        if (!(ok = mbar_wait_warp(&s_full[t], (seen + i_mine) & 1, ctl))) break;
         tc_fence_after();
         uint32_t s[128];
         tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
@@ -440,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st32(tS + 32 * hf, p);
         }
         l_run += (sumv[0].x + sumv[1].x) + (sumv[0].y + sumv[1].y);
-        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+        if (i_mine > 0 && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -480,10 +551,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && n_mine > 0) ok = mbar_wait_warp(&o_full[t], outs++ & 1, ctl);
       if (!ok) break;
       tc_fence_after();
+      // kTwin: slot 1 hands its statistics to slot 0, which joins the two results.  O of slot 1 and
+      // the statistics stay until slot 0 has read them: the next piece's first MMA waits for all
+      // warps on q_full
+      float w0 = 1.f, w1 = 0.f;
+      const bool both = kTwin && npos >= 2;  // slot 1 has had positions
+      if (both) {
+        if (t == 1) {
+          twin_m[row] = m_run;
+          twin_l[row] = l_run;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(twin_full);
+        } else {
+          if (!(ok = mbar_wait_warp(twin_full, twins++ & 1, ctl))) break;
+          tc_fence_after();
+          const float m1 = twin_m[row], l1 = twin_l[row], m = fmaxf(m_run, m1);
+          // without a visible key a slot weighs nothing (NaN stays)
+          w0 = m_run == -INFINITY ? (l_run == 0.f ? 0.f : l_run) : ex2(m_run - m);
+          w1 = m1 == -INFINITY ? (l1 == 0.f ? 0.f : l1) : ex2(m1 - m);
+          m_run = m;
+          l_run = w0 * l_run + w1 * l1;
+        }
+      }
 
       // ---- this row's result, or its part of it
       const int gr = r0 + row;
-      if (r0 < rows) {  // uniform over the warpgroup
+      if (r0 < rows && !(kTwin && t == 1)) {  // uniform over the warpgroup
         const bool live = gr < rows;
         const int tok = gr / a.G, head = piece.hk * a.G + (gr - tok * a.G);
         const int64_t at = static_cast<int64_t>(piece.start + tok) * a.H + head;
@@ -502,6 +596,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (both) {
+            uint32_t o1[32];
+            tmem_ld32(tO + D + 32 * c, o1);
+            tmem_wait_ld();
+            reg_fence(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(w1, __uint_as_float(o1[i]), w0 * __uint_as_float(o[i])));
           }
           if (!live) continue;
           if (final_out) {
@@ -549,27 +652,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, int kLists>
+template <int D, int kLists, bool kTwin>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
                      int64_t max_units, uint64_t timeout_ns, cudaStream_t s) {
-  const uint32_t smem = smem_of<D, kLists>() + 1024;
-  cudaError_t e = ensure_smem_limit<paged_mma_kernel<D, kLists>>(smem);
+  const uint32_t smem = smem_of<D, kLists>();  // the kernel's array is aligned as declared
+  cudaError_t e = ensure_smem_limit<paged_mma_kernel<D, kLists, kTwin>>(smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
-  return launch_chained(paged_mma_kernel<D, kLists>, static_cast<unsigned>(ctas), kThreads, smem,
-                        s, tk, tv, a, timeout_ns, smem);
+  return launch_chained(paged_mma_kernel<D, kLists, kTwin>, static_cast<unsigned>(ctas), kThreads,
+                        smem, s, tk, tv, a, timeout_ns, smem);
+}
+template <int D>
+cudaError_t launch_kind(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
+                        int lists, bool twin, int64_t max_units, uint64_t timeout_ns,
+                        cudaStream_t s) {
+  if (lists == 2) return launch_d<D, 2, false>(tk, tv, a, max_units, timeout_ns, s);
+  return twin ? launch_d<D, 1, true>(tk, tv, a, max_units, timeout_ns, s)
+              : launch_d<D, 1, false>(tk, tv, a, max_units, timeout_ns, s);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
-                             const PagedArgs& a, int lists, int64_t max_units,
+                             const PagedArgs& a, int lists, bool twin, int64_t max_units,
                              uint64_t timeout_ns, cudaStream_t s) {
-  if (lists == 2)
-    return d == 64 ? launch_d<64, 2>(tk, tv, a, max_units, timeout_ns, s)
-                   : launch_d<128, 2>(tk, tv, a, max_units, timeout_ns, s);
-  return d == 64 ? launch_d<64, 1>(tk, tv, a, max_units, timeout_ns, s)
-                 : launch_d<128, 1>(tk, tv, a, max_units, timeout_ns, s);
+  return d == 64 ? launch_kind<64>(tk, tv, a, lists, twin, max_units, timeout_ns, s)
+                 : launch_kind<128>(tk, tv, a, lists, twin, max_units, timeout_ns, s);
 }
 
 }  // namespace fa

@@ -111,12 +111,12 @@ bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int H
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query rows per key/value head above which a list goes to the tensor-core kernel.  At d = 128 the
-// other kernel reads the keys once per 16 rows: 16 sequences of 8192 keys take it 94 us with 16
-// rows and 154 with 24, the tensor-core kernel 99 and 100.  At d = 64 a tile's softmax outweighs
-// its copies and the tensor-core kernel needs 84 to 86 us from 4 rows to 32, the other one 56 with
-// 16 and 83 with 32.
-constexpr long long mma_rows(int d) { return d == 64 ? 32 : 16; }
+// Query rows per key/value head above which a list goes to the tensor-core kernel.  The other
+// kernel reads the keys once per 16 rows: 16 sequences of 8192 keys take it 85 us with 12 to 16 rows
+// and 154 with 24, the tensor-core kernel 89 with 24; at d = 64 it takes 51 with 12 rows and 81 with
+// 20 or 32, the tensor-core kernel 67.  With two lists and d = 64, where a row tile's second slot
+// rests (82), it takes over above 32.
+constexpr long long mma_rows(int d, int lists) { return d == 64 && lists == 2 ? 32 : 16; }
 
 // Keys up to which no entry is split, so that there is nothing to join.  Few rows: a warp takes
 // 0.27 us a tile (16 keys), the join 4 to 5 us, so 128 keys (one sequence of 8 heads and 128 keys:
@@ -154,7 +154,7 @@ PagedWorkspace paged_workspace(const int (&count)[2], int lists, int total, int 
   PagedWorkspace w{};
   size_t at = 0;
   size_t slots = static_cast<size_t>(fa::kPagedCtas) * fa::kPagedWarps * 2 * fa::kPagedRows * (d + 2) * 4;
-  if (static_cast<long long>(total) * (H / Hkv) > mma_rows(d)) {
+  if (static_cast<long long>(total) * (H / Hkv) > mma_rows(d, lists)) {
     const size_t mma = static_cast<size_t>(fa::kPagedCtas) * 2 * fa::kPagedMmaRows * (d + 2) * 4;
     if (mma > slots) slots = mma;
   }
@@ -206,12 +206,14 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   if (lists == 2 && (static_cast<long long>(total) + count[1]) * H + 256LL * count[1] > kMaxInt)
     return FA_ERR_INVALID_ARG;
   bool mma[2];
+  bool twin = false;
   long long units[2];
   for (int i = 0; i < lists; ++i) {
     // query rows of an entry: at most those of max_q tokens; of a group, its share of the batch
     const long long tokens = i == 0 && max_q < total ? max_q : total;
     const long long rows = (i == 0 ? tokens : (total + count[i] - 1) / count[i]) * (H / Hkv);
-    mma[i] = rows > mma_rows(d);
+    mma[i] = rows > mma_rows(d, lists);
+    twin = lists == 1 && rows <= 128;
     // row tiles over all entries x heads x key tiles: the units of a launch, which fit 32 bits
     const long long keys = i == 0 ? max_kv : prefix->max_len;
     units[i] = Hkv * static_cast<long long>(fa::row_tiles_bound(
@@ -284,8 +286,10 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   }
   a.mma_cost = mma_tile_cost(d);
   const long long all = units[0] + (lists > 1 ? units[1] : 0);
-  if ((st = status_of(any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, all, fa::wait_timeout_ns(), s)
-                              : fa::launch_paged(d, a, lists, all, s))) != FA_OK)
+  const cudaError_t e =
+      any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, twin, all, fa::wait_timeout_ns(), s)
+              : fa::launch_paged(d, a, lists, all, s);
+  if ((st = status_of(e)) != FA_OK)
     return st;
   // no entry can have been split (lengths are clamped to max_kv): every result is final
   if (lists == 1 && max_kv <= unsplit_keys(mma[0], B, Hkv))

@@ -133,6 +133,20 @@ def test_paged_chunks(nq, lens, heads):
         run_paged(nq, lens, H, Hkv, d, page, causal, seed=len(nq) + H)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True], ids=["all", "causal"])
+def test_paged_one_query_tile(causal, d):
+    """17 to 128 rows a key/value head (both tile slots on one query tile): no, one, two, three, many
+    key tiles of a row, whole or split, and tokens without a key."""
+    lens = [0, 1, 100, 128, 129, 256, 257, 384, 500, 640, 3000, 5]
+    nq = [3, 1, 5, 32, 2, 9, 1, 32, 17, 30, 32, 20]
+    run_paged(nq, lens, 8, 2, d, 16, causal, seed=31)
+    run_paged([1] * 12, lens, 40, 2, d, 128, causal, seed=32)
+    run_paged([32, 5], [9000, 40], 4, 1, d, 64, causal, seed=33)
+    run_paged([120], [300], 1, 1, d, 32, causal, seed=34)
+    run_paged([5] * 40, [700 + 13 * i for i in range(40)], 32, 8, d, 64, causal, seed=35)
+
+
 def test_paged_many_ragged_sequences():
     rng = np.random.default_rng(3)
     lens = rng.integers(0, 900, 150).tolist()
