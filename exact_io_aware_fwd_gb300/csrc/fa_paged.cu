@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
   constexpr int E = D / kLanes / 4;  // float4s of a lane
   let_next_launch();
   constexpr int kRowsPerCta = kGroups / kSplit;
+  constexpr int kDeep = kSplit == 1 ? 2 : 4;
   const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const int crow = group / kSplit, pick = group % kSplit;  // row of the CTA, first part
   const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
@@ -118,8 +119,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
         pm = st[0];
         pl = st[one ? rows : p.R];
       }
-      // two parts' O at a time, the first two on the way together with m and l
-      float4 v[2][E];
+      // kDeep parts' O at a time, the first ones on the way together with m and l
+      float4 v[kDeep][E];
       auto fetch = [&](int i, float4 (&to)[E]) {
         const float4* po = reinterpret_cast<const float4*>(
             one ? a.rowbuf[li] + static_cast<int64_t>(id) * D : slot(i0 + i * kSplit) + rr[li] * D);
@@ -127,8 +128,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
         for (int e = 0; e < E; ++e)
           to[e] = i < count ? po[e * kLanes + sub] : make_float4(0.f, 0.f, 0.f, 0.f);
       };
-      fetch(0, v[0]);
-      fetch(1, v[1]);
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) fetch(k, v[k]);
       float top = pm;
 #pragma unroll
       for (int x = kLanes / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, x));
@@ -145,9 +146,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
       for (int e = 0; e < E; ++e) {
         o[e].x *= keep; o[e].y *= keep; o[e].z *= keep; o[e].w *= keep;
       }
-      for (int i = 0; i < count; i += 2) {
+      for (int i = 0; i < count; i += kDeep) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kDeep; ++k) {
           const float wi = __shfl_sync(mask, w, i + k, kLanes);  // 0 past the last part
           if (i + k >= count) break;
 #pragma unroll
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
             o[e].z = fmaf(wi, v[k][e].z, o[e].z);
             o[e].w = fmaf(wi, v[k][e].w, o[e].w);
           }
-          if (i + k + 2 < count) fetch(i + k + 2, v[k]);
+          if (i + k + kDeep < count) fetch(i + k + kDeep, v[k]);
         }
       }
     }
