@@ -181,8 +181,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int g = 0; g < kSplit; ++g) {
-      const float w = sm[group + g] == -INFINITY ? (sl[group + g] == 0.f ? 0.f : sl[group + g]) : ex2(sm[group + g] - m);
-      lsum = fmaf(w, sl[group + g], lsum);
+      const float gm = sm[group + g], gl = sl[group + g];
+      const float w = gm == -INFINITY ? (gl == 0.f ? 0.f : gl) : ex2(gm - m);
+      lsum = fmaf(w, gl, lsum);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float4 v = so[group + g][e * kLanes + sub];
@@ -227,7 +228,8 @@ cudaError_t launch_join_d(const JoinArgs& a, int split, cudaStream_t s) {
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s) {
   if (lists == 2)
-    return d == 64 ? launch_paged_d<64, 2>(a, max_units, s) : launch_paged_d<128, 2>(a, max_units, s);
+    return d == 64 ? launch_paged_d<64, 2>(a, max_units, s)
+                   : launch_paged_d<128, 2>(a, max_units, s);
   return d == 64 ? launch_paged_d<64, 1>(a, max_units, s) : launch_paged_d<128, 1>(a, max_units, s);
 }
 

@@ -76,7 +76,9 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* row, int gap, const Row
 struct Vec8 {
   float2 v[4];
 };
-__device__ __forceinline__ float2 pair_of(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
+__device__ __forceinline__ float2 pair_of(uint32_t u) {
+  return make_float2(bf16_lo(u), bf16_hi(u));
+}
 __device__ __forceinline__ Vec8 unpack(const Row8& r) {
   return {{pair_of(r.a.x), pair_of(r.a.y), pair_of(r.b.x), pair_of(r.b.y)}};
 }
@@ -376,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(con
   const bool norm = kind != 2 && weight != nullptr;
   Vec8 w{}, dw{};
   if (norm) w = load_weight(weight, lp.off0, lp.off1);
-  const uint32_t base = smem_u32(ring) + grp * (D * 2);  // row (i, k) of the group: + (2 i + k) 16 kThreads
+  // row i of dz (k = 0) or x (k = 1) of the lane group: + (2 i + k) 16 kThreads
+  const uint32_t base = smem_u32(ring) + grp * (D * 2);
 
   RowCursor<G> load;
   load.heads = kind == 0 ? a.H : a.Hkv;

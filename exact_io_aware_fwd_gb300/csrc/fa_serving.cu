@@ -43,7 +43,8 @@ fa_status check_transform(const fa_qk_transform* t, int d) {
   }
   if ((t->q_weight == nullptr) != (t->k_weight == nullptr)) return FA_ERR_INVALID_ARG;
   if (!aligned_to(t->q_weight, 16) || !aligned_to(t->k_weight, 16)) return FA_ERR_INVALID_ARG;
-  if (t->q_weight != nullptr && !(std::isfinite(t->eps) && t->eps >= 0.f)) return FA_ERR_INVALID_ARG;
+  if (t->q_weight != nullptr && !(std::isfinite(t->eps) && t->eps >= 0.f))
+    return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -85,7 +86,8 @@ fa_status check_cache(const fa_paged_kv* c) {
   if (c == nullptr || c->k_cache == nullptr || c->v_cache == nullptr || c->kv_lens == nullptr)
     return FA_ERR_INVALID_ARG;
   if (!aligned_to(c->k_cache, 16) || !aligned_to(c->v_cache, 16)) return FA_ERR_INVALID_ARG;
-  if (c->num_pages < 1 || c->num_pages > (1 << 30) || c->max_pages < 0 || (c->max_pages > 0 && c->block_table == nullptr))
+  if (c->num_pages < 1 || c->num_pages > (1 << 30) || c->max_pages < 0 ||
+      (c->max_pages > 0 && c->block_table == nullptr))
     return FA_ERR_INVALID_ARG;
   if (page_shift(c->page_size) < 0) return FA_ERR_UNSUPPORTED;
   return FA_OK;
@@ -153,7 +155,8 @@ struct PagedWorkspace {
 PagedWorkspace paged_workspace(const int (&count)[2], int lists, int total, int H, int Hkv, int d) {
   PagedWorkspace w{};
   size_t at = 0;
-  size_t slots = static_cast<size_t>(fa::kPagedCtas) * fa::kPagedWarps * 2 * fa::kPagedRows * (d + 2) * 4;
+  size_t slots = static_cast<size_t>(fa::kPagedCtas) * fa::kPagedWarps * 2 * fa::kPagedRows *
+                 (d + 2) * 4;
   if (static_cast<long long>(total) * (H / Hkv) > mma_rows(d, lists)) {
     const size_t mma = static_cast<size_t>(fa::kPagedCtas) * 2 * fa::kPagedMmaRows * (d + 2) * 4;
     if (mma > slots) slots = mma;
@@ -242,7 +245,8 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   a.num_pages = cache->num_pages;
   a.page_shift = page_shift(cache->page_size);
   // never quite 0 (a scale of 0): a hidden key's score of -inf has to stay -inf when scaled
-  a.scale_log2 = std::fmax(fa::resolve_scale(scale, d) * kLog2e, std::numeric_limits<float>::denorm_min());
+  a.scale_log2 = std::fmax(fa::resolve_scale(scale, d) * kLog2e,
+                           std::numeric_limits<float>::denorm_min());
   a.status = status;
   fa::JoinArgs j{};
   j.o = a.o;
@@ -289,8 +293,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   const cudaError_t e =
       any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, twin, all, fa::wait_timeout_ns(), s)
               : fa::launch_paged(d, a, lists, all, s);
-  if ((st = status_of(e)) != FA_OK)
-    return st;
+  if ((st = status_of(e)) != FA_OK) return st;
   // no entry can have been split (lengths are clamped to max_kv): every result is final
   if (lists == 1 && max_kv <= unsplit_keys(mma[0], B, Hkv))
     return FA_OK;

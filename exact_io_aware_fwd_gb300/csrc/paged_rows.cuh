@@ -98,8 +98,8 @@ __device__ __forceinline__ Source source_of(const KeyList& l, const Walk<R, KT>&
 // Copies step st into its stage (zeros for keys past the length and, reported, for a page outside
 // the pool); every call commits a group, empty past the last step.
 template <int D>
-__device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l, Source& s, int st, uint32_t ring,
-                                           int lane) {
+__device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l, Source& s,
+                                           int st, uint32_t ring, int lane) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages, GR = D / 8;  // granules of a row
   if (st < s.steps) {

@@ -3,7 +3,7 @@
 //
 // The kernels behind these calls take a few microseconds in the smallest cases (a decoding step of
 // a small batch); the same checks and allocations in Python with ctypes took 20 to 30 us a call
-// on the GPU's host, the compiled ones 6 to 9.  Nothing is computed here and nothing is kept
+// on the GPU's host, the compiled ones 3 to 6.  Nothing is computed here and nothing is kept
 // between calls.  The library's entry points come from the Python side (bind), so that there is
 // one loaded instance of it.
 #include <Python.h>
@@ -519,8 +519,9 @@ PyObject* bind(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
-#define FA_METHOD(name, body, args) \
-  {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<body, args>)), METH_FASTCALL, nullptr}
+#define FA_METHOD(name, body, args)                                                         \
+  {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<body, args>)), \
+   METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FA_METHOD("bind", bind, 9),
                          FA_METHOD("norm_rope_fwd", norm_rope_fwd, 12),
                          FA_METHOD("norm_rope_bwd", norm_rope_bwd, 15),

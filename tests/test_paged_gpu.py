@@ -654,6 +654,27 @@ def test_shared_prefix_refusals():
 
 
 # -------------------------------------------------------------------------------------- as one run
+def test_calls_under_inference_mode_and_with_leaves():
+    """Outputs allocated by the binding are ordinary tensors (inference tensors in that mode)."""
+    cache = Cache([200, 90], 2, 64, 16, seed=91)
+    args = cache.dev()
+    q = torch.randn(2, 4, 64, device=DEV).to(BF16)
+    want = fa.fa_fwd_paged(q, *args)[0]
+    with torch.inference_mode():
+        got = fa.fa_fwd_paged(q, *args)[0]
+        assert got.is_inference() and torch.equal(got + 0, want)
+        w = torch.ones(64, device=DEV)
+        grads = fa.fa_qk_norm_rope_bwd(q, q, q, q, q, q_weight=w, k_weight=w)
+        assert all(torch.isfinite(g + 0).all() for g in grads)
+    leaf = q.clone().requires_grad_()
+    out = fa.fa_fwd_paged(leaf, *args)[0]
+    assert not out.requires_grad and torch.equal(out, want)
+    dq, dk, dv, dwq, dwk = fa.fa_qk_norm_rope_bwd(q, q, q, q, q, q_weight=w, k_weight=w)
+    assert dq.stride() == (3 * 4 * 64, 64, 1) and dk.data_ptr() == dq.data_ptr() + 2 * 4 * 64
+    dq.add_(1)
+    assert dwk.data_ptr() == dwq.data_ptr() + 4 * 64 and dwq.shape == dwk.shape == (64,)
+
+
 def test_generation_run():
     """A prompt in one packed pass, its keys into the cache, then tokens one by one, against one
     causal pass over everything; then the same continuation for four sequences behind the prompt
