@@ -44,6 +44,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
                   lane);
 }
 
+// Few short segments: no CTA shares one, no join.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_cta_kernel(const __grid_constant__ PagedArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Share shares[1];
+  touch(a);
+  begin_launch();
+  make_shares<rows16::R, rows16::KT, kThreads, 1>(a, shares);
+  rows16::work_together<D>(a, a.list[0], shares[0], smem, threadIdx.x >> 5, threadIdx.x & 31);
+}
+
 // ---- join of the parts
 constexpr int kJoinThreads = 128;
 constexpr int kLanes = 8;                          // lanes of a group
@@ -216,6 +227,15 @@ cudaError_t launch_paged_d(const PagedArgs& a, int64_t max_units, cudaStream_t s
 }
 
 template <int D>
+cudaError_t launch_cta_d(const PagedArgs& a, int64_t max_units, cudaStream_t s) {
+  constexpr uint32_t bytes = rows16::PagedLayout<D>::kBytes;
+  cudaError_t e = ensure_smem_limit<paged_cta_kernel<D>>(bytes);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
+  return launch_chained(paged_cta_kernel<D>, static_cast<unsigned>(ctas), kThreads, bytes, s, a);
+}
+
+template <int D>
 cudaError_t launch_join_d(const JoinArgs& a, int split, cudaStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.total) * static_cast<unsigned>(a.H);
   const unsigned per = kGroups / split, grid = (rows + per - 1) / per;
@@ -231,6 +251,10 @@ cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units
     return d == 64 ? launch_paged_d<64, 2>(a, max_units, s)
                    : launch_paged_d<128, 2>(a, max_units, s);
   return d == 64 ? launch_paged_d<64, 1>(a, max_units, s) : launch_paged_d<128, 1>(a, max_units, s);
+}
+
+cudaError_t launch_paged_cta(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s) {
+  return d == 64 ? launch_cta_d<64>(a, max_units, s) : launch_cta_d<128>(a, max_units, s);
 }
 
 cudaError_t launch_paged_join(int d, const JoinArgs& a, int split, cudaStream_t s) {

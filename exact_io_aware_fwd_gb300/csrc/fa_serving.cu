@@ -121,10 +121,10 @@ bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int H
 constexpr long long mma_rows(int d, int lists) { return d == 64 && lists == 2 ? 32 : 16; }
 
 // Keys up to which no entry is split, so that there is nothing to join.  Few rows: a warp takes
-// 0.27 us a tile (16 keys), the join 4 to 5 us, so 128 keys (one sequence of 8 heads and 128 keys:
-// 8.3 us unsplit and 8.7 split, 192 keys: 10.6 and 8.7); where the segments keep half of the warps
-// busy, 256 (64 sequences of 8 heads and 256 keys: 13.4 and 15.2).  The tensor-core kernel: 512 (4
-// sequences of 40 tokens and 300 keys 13.4 and 15.5 us, 32 of 500 keys 28.6 and 44).
+// 0.27 us a tile (16 keys), the join 4 to 5 us, so 128 keys; where the segments keep half of the
+// warps busy, 256 (64 sequences of 8 heads and 256 keys: 13.4 and, split, 15.2 us).  The
+// tensor-core kernel: 512 (4 sequences of 40 tokens and 300 keys 13.4 and 15.5 us, 32 of 500 keys
+// 28.6 and 44).
 int unsplit_keys(bool mma, int count, int Hkv) {
   if (mma) return 512;
   return static_cast<long long>(count) * Hkv >= 2 * fa::kPagedCtas ? 256 : 128;
@@ -137,6 +137,17 @@ int unsplit_keys(bool mma, int count, int Hkv) {
 // 64 of 512 keys behind 4096 47 instead of 65; d = 64, 64 of 1024 behind 32768 56 instead of 80 (63
 // with 18, 70 with 14).  Two lists of few rows: 8 short sequences behind 1000 keys 12 us.
 constexpr float mma_tile_cost(int d) { return d == 64 ? 30.f : 20.f; }
+
+// Few rows: whether a CTA takes whole segments, its warps an eighth of the keys each, so that there
+// is nothing to join.  With a segment per SM at most, up to 1024 keys (d = 128, 8 heads, split and
+// whole: one sequence of 128 keys 8.7 and 5.3 us, 500 keys 8.9 and 7.4, 1000 keys 10.2 and 10.2; 16
+// sequences of 1000 keys 15.2 and 11.1); with two, from 64 to 512 (32 sequences of 256 keys 12.4
+// and 10.4, of 500 15.4 and 13.6, of 32, a warp each, 5.8 and 8.4).  Longer ones would be as slow
+// as the longest, and more segments take turns (48 sequences of 256 keys 13.5 and 14.2).
+bool whole_segments(long long segments, int max_kv) {
+  return segments <= fa::kPagedCtas ? max_kv <= 1024
+                                    : segments <= 2 * fa::kPagedCtas && max_kv > 64 && max_kv <= 512;
+}
 
 // Groups of 8 lanes per row of the join.  A group reads its parts two at a time, so few rows, which
 // have many parts, take more groups: 128 rows of 39 parts 292 us with 16, 306 with 1 (4 x 131072
@@ -289,6 +300,15 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     j.rowbuf[i] = a.rowbuf[i];
   }
   a.mma_cost = mma_tile_cost(d);
+  if (lists == 1 && !mma[0]) {
+    const long long tokens = max_q < total ? max_q : total;
+    const long long tiles = (tokens * (H / Hkv) + fa::kPagedRows - 1) / fa::kPagedRows;
+    const long long segments = B * tiles * Hkv;
+    if (whole_segments(segments, max_kv)) {
+      a.list[0].unsplit = kMaxInt;
+      return status_of(fa::launch_paged_cta(d, a, segments, s));
+    }
+  }
   const long long all = units[0] + (lists > 1 ? units[1] : 0);
   const cudaError_t e =
       any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, twin, all, fa::wait_timeout_ns(), s)

@@ -126,6 +126,136 @@ __device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l,
   cp_commit();
 }
 
+// A row tile's queries as A fragments: the thread holds rows lane / 4 and lane / 4 + 8.
+template <int D>
+struct QRows {
+  uint32_t qf[D / 16][4];
+  int lim[2];   // keys below it are visible to the row
+  int at[2];    // (token, head) of the row
+  int head[2];
+  int rows, lim_min;  // rows of the tile; the first row's limit, the smallest
+};
+template <int D>
+__device__ __forceinline__ QRows<D> load_rows(const PagedArgs& a, const KeyList& l, const Entry& e,
+                                              const Piece& p, int lane) {
+  QRows<D> x;
+  const int row0 = p.r * R, rows = min(R, e.nc * a.G - row0);
+  x.rows = rows;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int rr = (lane >> 2) + 8 * i, tok = (row0 + rr) / a.G;
+    x.lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row0 + rr) : e.len;
+    x.head[i] = p.hk * a.G + (row0 + rr - tok * a.G);
+    x.at[i] = (e.start + tok) * a.H + x.head[i];
+    const __nv_bfloat16* qp = a.q + static_cast<int64_t>(x.at[i]) * D + (lane & 3) * 2;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      x.qf[k][i] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
+      x.qf[k][i + 2] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
+    }
+  }
+  x.lim_min = row_limit(e, l.causal, a.G, row0);
+  return x;
+}
+
+// Running O, maximum (log2 units) and sum of the thread's two rows.
+template <int D>
+struct Acc {
+  float o[D / 8][4], m[2], sum[2];
+  __device__ Acc() : m{-INFINITY, -INFINITY}, sum{0.f, 0.f} {
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  }
+};
+
+// The keys of a source, whose first S - 1 steps have been issued.
+template <int D>
+__device__ __forceinline__ void scan_keys(const PagedArgs& a, const KeyList& l, Source& src,
+                                          const QRows<D>& x, uint32_t ring, int lane, Acc<D>& c) {
+  using L = PagedLayout<D>;
+  constexpr int S = L::kStages;
+  for (int st = 0; st < src.steps; ++st) {
+    cp_wait<S - 2>();
+    __syncwarp();
+    const uint32_t kb = ring + (st % S) * L::kStage, vb = kb + L::kHalf;
+    // S = Q K^T: 16 rows x 16 keys
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    {
+      const uint32_t r = (lane & 7) + ((lane >> 4) << 3), gh = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t f[4];
+        ldsm4(kb + step_offset<D>(r, 2 * k + gh), f);
+        mma16816(s[0], x.qf[k], f[0], f[1]);
+        mma16816(s[1], x.qf[k], f[2], f[3]);
+      }
+    }
+    const int key0 = (src.first + st) * KT;
+    if (key0 + KT > x.lim_min) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = key0 + n * 8 + (lane & 3) * 2 + (k & 1);
+          if (key >= x.lim[k >> 1]) s[n][k] = -INFINITY;
+        }
+    }
+    // online softmax; the row maximum is shared by the four lanes of a row, the sum is
+    // joined at the end
+    bool moved = false;
+    float alpha[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx =
+          fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2)) * a.scale_log2;
+      alpha[i] = 1.f;
+      if (mx > c.m[i]) {
+        alpha[i] = ex2(c.m[i] - mx);
+        c.m[i] = mx;
+        moved = true;
+      }
+      const float ref = c.m[i] == -INFINITY ? 0.f : c.m[i];
+      float total = 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          // the scale is never 0, so a hidden score stays -inf and weighs 0
+          const float p = ex2(fmaf(s[n][2 * i + k], a.scale_log2, -ref));
+          s[n][2 * i + k] = p;
+          total += p;
+        }
+      c.sum[i] = c.sum[i] * alpha[i] + total;
+    }
+    if (__any_sync(~0u, moved)) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        c.o[n][0] *= alpha[0];
+        c.o[n][1] *= alpha[0];
+        c.o[n][2] *= alpha[1];
+        c.o[n][3] *= alpha[1];
+      }
+    }
+    // O += P V; P rounded to bf16 (half a step, 2^-8, as in fa_fwd), its sum is not
+    const uint32_t pf[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
+                            pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
+    {
+      const uint32_t r = lane & 15, gh = lane >> 4;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t f[4];
+        ldsm4_t(vb + step_offset<D>(r, 2 * n + gh), f);
+        mma16816(c.o[2 * n], pf, f[0], f[1]);
+        mma16816(c.o[2 * n + 1], pf, f[2], f[3]);
+      }
+    }
+    __syncwarp();  // every lane has read stage st % S before it is filled again
+    issue_step<D>(a, l, src, st + S - 1, ring, lane);
+  }
+}
+
 // A worker's share of a list's keys (one warp).
 template <int D>
 __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
@@ -143,115 +273,12 @@ __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
     const Piece piece = next_piece;
     const Entry e = walk.e;
     const int tile = row_tile0(e.start, a.G, R, walk.b) + piece.r;
-    const int hk = piece.hk;
     if (lane == 0 && piece.ta == 0)  // this worker begins the segment
-      part.spans[static_cast<int64_t>(hk) * part.span_tiles + tile] = span_of(sh, piece);
+      part.spans[static_cast<int64_t>(piece.hk) * part.span_tiles + tile] = span_of(sh, piece);
 
-    // ---- the rows' queries as A fragments: thread holds rows lane / 4 and lane / 4 + 8
-    const int row0 = piece.r * R, rows = min(R, e.nc * a.G - row0);
-    uint32_t qf[D / 16][4];
-    int lim[2];  // keys below it are visible to the row
-    int at[2];   // (token, head) of the row
-    int head[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = (lane >> 2) + 8 * i, tok = (row0 + rr) / a.G;
-      lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row0 + rr) : e.len;
-      head[i] = hk * a.G + (row0 + rr - tok * a.G);
-      at[i] = (e.start + tok) * a.H + head[i];
-      const __nv_bfloat16* qp = a.q + static_cast<int64_t>(at[i]) * D + (lane & 3) * 2;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[k][i] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16) : 0u;
-        qf[k][i + 2] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
-      }
-    }
-    const int lim_min = row_limit(e, l.causal, a.G, row0);  // the first row's: the smallest
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-    for (int st = 0; st < src.steps; ++st) {
-      cp_wait<S - 2>();
-      __syncwarp();
-      const uint32_t kb = ring + (st % S) * L::kStage, vb = kb + L::kHalf;
-      // S = Q K^T: 16 rows x 16 keys
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      {
-        const uint32_t r = (lane & 7) + ((lane >> 4) << 3), gh = (lane >> 3) & 1;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t f[4];
-          ldsm4(kb + step_offset<D>(r, 2 * k + gh), f);
-          mma16816(s[0], qf[k], f[0], f[1]);
-          mma16816(s[1], qf[k], f[2], f[3]);
-        }
-      }
-      const int key0 = (src.first + st) * KT;
-      if (key0 + KT > lim_min) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = key0 + n * 8 + (lane & 3) * 2 + (c & 1);
-            if (key >= lim[c >> 1]) s[n][c] = -INFINITY;
-          }
-      }
-      // online softmax; the row maximum is shared by the four lanes of a row, the sum is
-      // joined at the end
-      bool moved = false;
-      float alpha[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx =
-            fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2)) * a.scale_log2;
-        alpha[i] = 1.f;
-        if (mx > m[i]) {
-          alpha[i] = ex2(m[i] - mx);
-          m[i] = mx;
-          moved = true;
-        }
-        const float ref = m[i] == -INFINITY ? 0.f : m[i];
-        float part = 0.f;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            // the scale is never 0, so a hidden score stays -inf and weighs 0
-            const float p = ex2(fmaf(s[n][2 * i + c], a.scale_log2, -ref));
-            s[n][2 * i + c] = p;
-            part += p;
-          }
-        sum[i] = sum[i] * alpha[i] + part;
-      }
-      if (__any_sync(~0u, moved)) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[n][0] *= alpha[0];
-          o[n][1] *= alpha[0];
-          o[n][2] *= alpha[1];
-          o[n][3] *= alpha[1];
-        }
-      }
-      // O += P V; P rounded to bf16 (half a step, 2^-8, as in fa_fwd), its sum is not
-      const uint32_t pf[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
-                              pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3])};
-      {
-        const uint32_t r = lane & 15, gh = lane >> 4;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t f[4];
-          ldsm4_t(vb + step_offset<D>(r, 2 * n + gh), f);
-          mma16816(o[2 * n], pf, f[0], f[1]);
-          mma16816(o[2 * n + 1], pf, f[2], f[3]);
-        }
-      }
-      __syncwarp();  // every lane has read stage st % S before it is filled again
-      issue_step<D>(a, l, src, st + S - 1, ring, lane);
-    }
+    const QRows<D> x = load_rows<D>(a, l, e, piece, lane);
+    Acc<D> c;
+    scan_keys<D>(a, l, src, x, ring, lane, c);
     // every stage has been read: the next piece's copies start here
     more = walk.next(a, l, next_piece);
     if (more) {
@@ -265,36 +292,122 @@ __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
                                      (R * (D + 2));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
-      sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
+      c.sum[i] += __shfl_xor_sync(~0u, c.sum[i], 1);
+      c.sum[i] += __shfl_xor_sync(~0u, c.sum[i], 2);
       const int rr = (lane >> 2) + 8 * i;
-      if (rr >= rows) continue;
-      const float inv = sum[i] > 0.f ? 1.f / sum[i] : (sum[i] == 0.f ? 0.f : sum[i]);  // NaN stays
+      if (rr >= x.rows) continue;
+      const float inv = c.sum[i] > 0.f ? 1.f / c.sum[i] : (c.sum[i] == 0.f ? 0.f : c.sum[i]);  // NaN stays
       if (final_out) {
         uint32_t* dst =
-            reinterpret_cast<uint32_t*>(a.o + static_cast<int64_t>(at[i]) * D) + (lane & 3);
+            reinterpret_cast<uint32_t*>(a.o + static_cast<int64_t>(x.at[i]) * D) + (lane & 3);
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
-          dst[n * 4] = pack_bf16(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+          dst[n * 4] = pack_bf16(c.o[n][2 * i] * inv, c.o[n][2 * i + 1] * inv);
       } else {
-        float* row = piece.whole ? rowbuf + static_cast<int64_t>(at[i]) * D : slot + rr * D;
+        float* row = piece.whole ? rowbuf + static_cast<int64_t>(x.at[i]) * D : slot + rr * D;
         float2* dst = reinterpret_cast<float2*>(row) + (lane & 3);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) dst[n * 4] = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+        for (int n = 0; n < D / 8; ++n) dst[n * 4] = make_float2(c.o[n][2 * i], c.o[n][2 * i + 1]);
       }
       if ((lane & 3) == 0) {
         if (final_out) {
-          const int t = (at[i] - head[i]) / a.H;
-          a.lse[static_cast<int64_t>(head[i]) * a.total + t] =
-              sum[i] == 0.f ? -INFINITY : (m[i] + log2f(sum[i])) * kLn2;
+          const int t = (x.at[i] - x.head[i]) / a.H;
+          a.lse[static_cast<int64_t>(x.head[i]) * a.total + t] =
+              c.sum[i] == 0.f ? -INFINITY : (c.m[i] + log2f(c.sum[i])) * kLn2;
         } else {
-          float* st = piece.whole ? rowbuf + static_cast<int64_t>(a.total) * a.H * D + at[i]
+          float* st = piece.whole ? rowbuf + static_cast<int64_t>(a.total) * a.H * D + x.at[i]
                                   : slot + R * D + rr;
-          st[0] = m[i];
-          st[piece.whole ? a.total * a.H : R] = sum[i];
+          st[0] = c.m[i];
+          st[piece.whole ? a.total * a.H : R] = c.sum[i];
         }
       }
     }
+  }
+  cp_wait<0>();
+}
+
+// Few short segments: the 8 warps of a CTA take an eighth of a segment's keys each and meet in
+// shared memory (their own rings, whose copies have all been read), so that nothing is left to
+// join.  The Share is the CTA's: its units are whole segments.
+template <int D>
+__device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList& l, const Share& sh,
+                                              uint8_t* smem, int warp, int lane) {
+  using L = PagedLayout<D>;
+  constexpr int S = L::kStages, P = D + 8;  // row pitch of a warp's O in floats
+  constexpr uint32_t kRing = S * L::kStage;
+  static_assert((R * P + 2 * R) * 4 <= kRing, "a warp's O, maxima and sums fit its ring");
+  const uint32_t ring = smem_u32(smem) + warp * kRing;
+  Walk<R, KT> walk(a, l, sh);
+  Piece piece;
+  while (walk.next(a, l, piece)) {
+    const Entry& e = walk.e;
+    Source src = source_of(l, walk, piece);
+    const int t0 = warp * src.steps / kWarps, t1 = (warp + 1) * src.steps / kWarps;
+    src.first += t0;
+    src.steps = t1 - t0;
+    for (int st = 0; st < S - 1; ++st) issue_step<D>(a, l, src, st, ring, lane);
+    const QRows<D> x = load_rows<D>(a, l, e, piece, lane);
+    Acc<D> c;
+    scan_keys<D>(a, l, src, x, ring, lane, c);
+    float* mine = reinterpret_cast<float*>(smem + warp * kRing);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c.sum[i] += __shfl_xor_sync(~0u, c.sum[i], 1);
+      c.sum[i] += __shfl_xor_sync(~0u, c.sum[i], 2);
+      const int rr = (lane >> 2) + 8 * i;
+      float2* dst = reinterpret_cast<float2*>(mine + rr * P) + (lane & 3);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) dst[n * 4] = make_float2(c.o[n][2 * i], c.o[n][2 * i + 1]);
+      if ((lane & 3) == 0) {
+        mine[R * P + rr] = c.m[i];
+        mine[R * P + R + rr] = c.sum[i];
+      }
+    }
+    __syncthreads();
+    // 16 threads a row, E elements each, over the warps in the order of their keys
+    constexpr int E = D / 16;
+    const int rr = threadIdx.x / 16, part = threadIdx.x % 16;
+    float m[kWarps], s[kWarps], top = -INFINITY, sum = 0.f, o[E];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float* from = reinterpret_cast<const float*>(smem + w * kRing) + R * P + rr;
+      m[w] = from[0];
+      s[w] = from[R];
+      top = fmaxf(top, m[w]);
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      // no visible key: weight 0 (NaN stays)
+      const float f = m[w] == -INFINITY ? (s[w] == 0.f ? 0.f : s[w]) : ex2(m[w] - top);
+      sum = fmaf(f, s[w], sum);
+      const float4* from = reinterpret_cast<const float4*>(
+          reinterpret_cast<const float*>(smem + w * kRing) + rr * P + part * E);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const float4 v = from[i];
+        o[4 * i] = fmaf(f, v.x, o[4 * i]);
+        o[4 * i + 1] = fmaf(f, v.y, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(f, v.z, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(f, v.w, o[4 * i + 3]);
+      }
+    }
+    if (rr < x.rows) {
+      const int row = piece.r * R + rr, tok = row / a.G;
+      const int head = piece.hk * a.G + (row - tok * a.G);
+      const int64_t at = static_cast<int64_t>(e.start + tok) * a.H + head;
+      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+      uint2* dst = reinterpret_cast<uint2*>(a.o + at * D + part * E);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i)
+        dst[i] = make_uint2(pack_bf16(o[4 * i] * inv, o[4 * i + 1] * inv),
+                            pack_bf16(o[4 * i + 2] * inv, o[4 * i + 3] * inv));
+      if (part == 0)
+        a.lse[static_cast<int64_t>(head) * a.total + e.start + tok] =
+            sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    __syncthreads();  // the rings are free for the next segment
   }
   cp_wait<0>();
 }

@@ -147,6 +147,21 @@ def test_paged_one_query_tile(causal, d):
     run_paged([5] * 40, [700 + 13 * i for i in range(40)], 32, 8, d, 64, causal, seed=35)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lengths", LENGTHS, ids=lambda x: "-".join(map(str, x[1])))
+def test_paged_loose_bounds(lengths, d):
+    """Short lengths under a bound that allows long ones: the split is chosen on the device."""
+    run_paged(*lengths, 6, 2, d, 16, True, seed=21, max_kv=max(2000, max(lengths[1])))
+
+
+@pytest.mark.parametrize("B,most", [(19, 1024), (19, 1025), (20, 512), (20, 513), (20, 64), (38, 300), (39, 300)])
+def test_paged_where_whole_segments_end(B, most):
+    """152 and 304 segments, 512 and 1024 keys: on both sides of the sizes at which a CTA takes whole
+    segments."""
+    lens = [most] + [(53 * b) % (most + 1) for b in range(1, B)]
+    run_paged([1 + b % 2 for b in range(B)], lens, 24, 8, 64, 64, True, seed=41)
+
+
 def test_paged_many_ragged_sequences():
     rng = np.random.default_rng(3)
     lens = rng.integers(0, 900, 150).tolist()
