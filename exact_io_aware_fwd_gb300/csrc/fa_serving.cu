@@ -144,9 +144,12 @@ constexpr float mma_tile_cost(int d) { return d == 64 ? 30.f : 20.f; }
 // sequences of 1000 keys 15.2 and 11.1); with two, from 64 to 512 (32 sequences of 256 keys 12.4
 // and 10.4, of 500 15.4 and 13.6, of 32, a warp each, 5.8 and 8.4).  Longer ones would be as slow
 // as the longest, and more segments take turns (48 sequences of 256 keys 13.5 and 14.2).
-bool whole_segments(long long segments, int max_kv) {
-  return segments <= fa::kPagedCtas ? max_kv <= 1024
-                                    : segments <= 2 * fa::kPagedCtas && max_kv > 64 && max_kv <= 512;
+// The first rule holds for more than 16 rows as well (13 sequences of 4 to 9 tokens, 8 heads on one
+// and 253 keys: 7.5 us, tensor-core kernel 9.1; one of 256 tokens, 8 heads and 1000 keys: 12.1 and
+// 18.4).
+bool whole_segments(long long segments, bool many_rows, int max_kv) {
+  if (segments <= fa::kPagedCtas) return max_kv <= 1024;
+  return segments <= 2 * fa::kPagedCtas && !many_rows && max_kv > 64 && max_kv <= 512;
 }
 
 // Groups of 8 lanes per row of the join.  A group reads its parts two at a time, so few rows, which
@@ -220,14 +223,20 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   if (lists == 2 && (static_cast<long long>(total) + count[1]) * H + 256LL * count[1] > kMaxInt)
     return FA_ERR_INVALID_ARG;
   bool mma[2];
-  bool twin = false;
+  bool twin = false, whole = false;
+  long long segments = 0;  // of 16 rows at most
   long long units[2];
   for (int i = 0; i < lists; ++i) {
     // query rows of an entry: at most those of max_q tokens; of a group, its share of the batch
     const long long tokens = i == 0 && max_q < total ? max_q : total;
     const long long rows = (i == 0 ? tokens : (total + count[i] - 1) / count[i]) * (H / Hkv);
     mma[i] = rows > mma_rows(d, lists);
-    twin = lists == 1 && rows <= 128;
+    if (lists == 1) {
+      segments = B * ((rows + fa::kPagedRows - 1) / fa::kPagedRows) * Hkv;
+      whole = whole_segments(segments, mma[0], max_kv);
+      mma[0] = mma[0] && !whole;
+      twin = rows <= 128;
+    }
     // row tiles over all entries x heads x key tiles: the units of a launch, which fit 32 bits
     const long long keys = i == 0 ? max_kv : prefix->max_len;
     units[i] = Hkv * static_cast<long long>(fa::row_tiles_bound(
@@ -300,14 +309,9 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     j.rowbuf[i] = a.rowbuf[i];
   }
   a.mma_cost = mma_tile_cost(d);
-  if (lists == 1 && !mma[0]) {
-    const long long tokens = max_q < total ? max_q : total;
-    const long long tiles = (tokens * (H / Hkv) + fa::kPagedRows - 1) / fa::kPagedRows;
-    const long long segments = B * tiles * Hkv;
-    if (whole_segments(segments, max_kv)) {
-      a.list[0].unsplit = kMaxInt;
-      return status_of(fa::launch_paged_cta(d, a, segments, s));
-    }
+  if (whole) {
+    a.list[0].unsplit = kMaxInt;
+    return status_of(fa::launch_paged_cta(d, a, segments, s));
   }
   const long long all = units[0] + (lists > 1 ? units[1] : 0);
   const cudaError_t e =

@@ -130,7 +130,8 @@ def test_paged_chunks(nq, lens, heads):
     """Chunks of prompts, many rows a head, with the causal mask ending inside tiles."""
     H, Hkv, d, page = heads
     for causal in (True, False):
-        run_paged(nq, lens, H, Hkv, d, page, causal, seed=len(nq) + H)
+        for max_kv in (max(lens), 2000):  # the second: not short enough for whole segments a CTA
+            run_paged(nq, lens, H, Hkv, d, page, causal, seed=len(nq) + H, max_kv=max_kv)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -143,7 +144,7 @@ def test_paged_one_query_tile(causal, d):
     run_paged(nq, lens, 8, 2, d, 16, causal, seed=31)
     run_paged([1] * 12, lens, 40, 2, d, 128, causal, seed=32)
     run_paged([32, 5], [9000, 40], 4, 1, d, 64, causal, seed=33)
-    run_paged([120], [300], 1, 1, d, 32, causal, seed=34)
+    run_paged([120], [300], 1, 1, d, 32, causal, seed=34, max_kv=2000)
     run_paged([5] * 40, [700 + 13 * i for i in range(40)], 32, 8, d, 64, causal, seed=35)
 
 
@@ -152,6 +153,15 @@ def test_paged_one_query_tile(causal, d):
 def test_paged_loose_bounds(lengths, d):
     """Short lengths under a bound that allows long ones: the split is chosen on the device."""
     run_paged(*lengths, 6, 2, d, 16, True, seed=21, max_kv=max(2000, max(lengths[1])))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_whole_segments_of_several_row_tiles(d):
+    """More than 16 rows a key/value head where a CTA takes whole segments."""
+    for causal in (True, False):
+        run_paged([40, 1, 0, 17], [300, 1000, 5, 12], 4, 1, d, 16, causal, seed=51)
+        run_paged([130], [130], 6, 2, d, 64, causal, seed=52)
+        run_paged([5] * 19, list(range(1, 20)), 32, 8, d, 32, causal, seed=53)  # 304 row tiles, few keys
 
 
 @pytest.mark.parametrize("B,most", [(19, 1024), (19, 1025), (20, 512), (20, 513), (20, 64), (38, 300), (39, 300)])
@@ -226,8 +236,9 @@ def test_paged_is_bitwise_repeatable_and_leaves_other_rows():
     assert fa.fa_get_error() == fa.FA_OK
 
 
-@pytest.mark.parametrize("nq", [1, 40], ids=["few rows", "many rows"])
-def test_paged_bad_pages_read_as_zeros_and_are_reported(nq):
+@pytest.mark.parametrize("nq,max_kv", [(1, 224), (1, 2000), (40, 224), (40, 2000)],
+                         ids=["whole", "few rows", "whole, tiles", "many rows"])
+def test_paged_bad_pages_read_as_zeros_and_are_reported(nq, max_kv):
     """Pages outside the pool are not read: their keys and values count as zeros, and the status
     says so."""
     lens, Hkv, d, page = [200, 90], 2, 64, 32
@@ -235,7 +246,8 @@ def test_paged_bad_pages_read_as_zeros_and_are_reported(nq):
     k, v, table, ln = cache.dev()
     table[0, 1], table[0, 4], table[1, 0] = -5, k.shape[0], 1 << 30
     q = torch.randn(2 * nq, 4, d, device=DEV).to(BF16)
-    out, lse = fa.fa_fwd_paged(q, k, v, table, ln, cu_seqlens=i32([0, nq, 2 * nq]), max_q=nq)
+    out, lse = fa.fa_fwd_paged(q, k, v, table, ln, cu_seqlens=i32([0, nq, 2 * nq]), max_q=nq,
+                               max_kv=max_kv)
     assert fa.fa_get_error() == fa.FA_ERR_INDEX and fa.fa_get_error() == fa.FA_OK
     per = []
     for b, gone in ((0, [1, 4]), (1, [0])):
@@ -410,18 +422,18 @@ def test_paged_length_at_the_end_of_its_type(G):
     assert np.abs(f64(lse) - np.log(2.0 ** 31 - 256)).max() <= bound + 2.0 ** -20 * 22
 
 
-@pytest.mark.parametrize("nq", [2, 40], ids=["few rows", "many rows"])
-def test_offsets_that_do_not_ascend_are_reported(nq):
+@pytest.mark.parametrize("nq,max_kv", [(2, 700), (2, 2000), (40, 2000)], ids=["whole", "few rows", "many rows"])
+def test_offsets_that_do_not_ascend_are_reported(nq, max_kv):
     cache = Cache([700, 20, 300], 2, 64, 16, seed=17)
     k, v, table, lens = cache.dev()
     q = torch.randn(3 * nq, 4, 64, device=DEV).to(BF16)
     n = 3 * nq
     for cu in ([0, n, 0, n], [-3, nq, 2 * nq, n], [0, nq, 2 * nq, n + 9], [n, 0, n, 0]):
-        fa.fa_fwd_paged(q, k, v, table, lens, cu_seqlens=i32(cu), max_q=n, max_kv=700)
+        fa.fa_fwd_paged(q, k, v, table, lens, cu_seqlens=i32(cu), max_q=n, max_kv=max_kv)
         assert fa.fa_get_error() == fa.FA_ERR_INDEX
     groups = i32([0, 3, 1])
     fa.fa_fwd_shared_prefix(q, k, v, table, lens, table[:2].contiguous(), lens[:2].contiguous(), groups,
-                            cu_seqlens=i32([0, nq, 2 * nq, n]), max_q=nq, max_kv=700)
+                            cu_seqlens=i32([0, nq, 2 * nq, n]), max_q=nq, max_kv=max_kv)
     assert fa.fa_get_error() == fa.FA_ERR_INDEX
 
 
