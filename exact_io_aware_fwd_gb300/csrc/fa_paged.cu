@@ -44,15 +44,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
                   lane);
 }
 
-// Few short segments: no CTA shares one, no join.
-template <int D>
+// Few short segments: no CTA shares one, no join.  kPrefix: list 1 holds the shared prefixes.
+template <int D, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1) paged_cta_kernel(const __grid_constant__ PagedArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Share shares[1];
   touch(a);
   begin_launch();
   make_shares<rows16::R, rows16::KT, kThreads, 1>(a, shares);
-  rows16::work_together<D>(a, a.list[0], shares[0], smem, threadIdx.x >> 5, threadIdx.x & 31);
+  if (kPrefix && blockIdx.x == 0)  // what is out of range in the groups is reported here
+    for (int g = threadIdx.x; g < a.list[1].count; g += kThreads)
+      entry_of<rows16::R, rows16::KT>(a.list[1], a, g, true);
+  rows16::work_together<D, kPrefix>(a, a.list[0], shares[0], smem, threadIdx.x >> 5, threadIdx.x & 31);
 }
 
 // ---- join of the parts
@@ -226,13 +229,14 @@ cudaError_t launch_paged_d(const PagedArgs& a, int64_t max_units, cudaStream_t s
   return launch_chained(paged_kernel<D, kLists>, static_cast<unsigned>(ctas), kThreads, bytes, s, a);
 }
 
-template <int D>
+template <int D, bool kPrefix>
 cudaError_t launch_cta_d(const PagedArgs& a, int64_t max_units, cudaStream_t s) {
   constexpr uint32_t bytes = rows16::PagedLayout<D>::kBytes;
-  cudaError_t e = ensure_smem_limit<paged_cta_kernel<D>>(bytes);
+  cudaError_t e = ensure_smem_limit<paged_cta_kernel<D, kPrefix>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
-  return launch_chained(paged_cta_kernel<D>, static_cast<unsigned>(ctas), kThreads, bytes, s, a);
+  return launch_chained(paged_cta_kernel<D, kPrefix>, static_cast<unsigned>(ctas), kThreads, bytes,
+                        s, a);
 }
 
 template <int D>
@@ -253,8 +257,13 @@ cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units
   return d == 64 ? launch_paged_d<64, 1>(a, max_units, s) : launch_paged_d<128, 1>(a, max_units, s);
 }
 
-cudaError_t launch_paged_cta(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s) {
-  return d == 64 ? launch_cta_d<64>(a, max_units, s) : launch_cta_d<128>(a, max_units, s);
+cudaError_t launch_paged_cta(int d, const PagedArgs& a, int lists, int64_t max_units,
+                             cudaStream_t s) {
+  if (lists == 2)
+    return d == 64 ? launch_cta_d<64, true>(a, max_units, s)
+                   : launch_cta_d<128, true>(a, max_units, s);
+  return d == 64 ? launch_cta_d<64, false>(a, max_units, s)
+                 : launch_cta_d<128, false>(a, max_units, s);
 }
 
 cudaError_t launch_paged_join(int d, const JoinArgs& a, int split, cudaStream_t s) {

@@ -210,8 +210,10 @@ constexpr int kPagedMmaRows = 256;       // the tensor-core kernel, whose CTAs a
 constexpr int kPagedMmaKeys = 128;
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s);
-// One list whose segments are not split; max_units: its segments at most.
-cudaError_t launch_paged_cta(int d, const PagedArgs& a, int64_t max_units, cudaStream_t s);
+// Segments of list 0, with their prefixes (lists == 2), that are not split; max_units: how many at
+// most.
+cudaError_t launch_paged_cta(int d, const PagedArgs& a, int lists, int64_t max_units,
+                             cudaStream_t s);
 // twin: one list, and no entry has more than 128 rows
 cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedArgs& a, int lists, bool twin, int64_t max_units,

@@ -135,7 +135,7 @@ int unsplit_keys(bool mma, int count, int Hkv) {
 // and the other at memory's, so at once they take less than one after the other: 128 sequences of
 // 1..1024 keys behind two prefixes of 32768 133 us instead of 148 (138 with 14 or 24, 160 with 30),
 // 64 of 512 keys behind 4096 47 instead of 65; d = 64, 64 of 1024 behind 32768 56 instead of 80 (63
-// with 18, 70 with 14).  Two lists of few rows: 8 short sequences behind 1000 keys 12 us.
+// with 18, 70 with 14). 
 constexpr float mma_tile_cost(int d) { return d == 64 ? 30.f : 20.f; }
 
 // Few rows: whether a CTA takes whole segments, its warps an eighth of the keys each, so that there
@@ -150,6 +150,17 @@ constexpr float mma_tile_cost(int d) { return d == 64 ? 30.f : 20.f; }
 bool whole_segments(long long segments, bool many_rows, int max_kv) {
   if (segments <= fa::kPagedCtas) return max_kv <= 1024;
   return segments <= 2 * fa::kPagedCtas && !many_rows && max_kv > 64 && max_kv <= 512;
+}
+
+// The same behind a shared prefix, which is then read (from L2) for each sequence: 0.55 us per 100
+// keys and turn at d = 128, 0.4 at d = 64, against 10 to 20 us of two lists and a join.  d = 128, 8
+// heads, prefix + own keys, two lists and whole: 4 sequences of 256 + 16 10.5 and 7.6 us, of 1000 +
+// 24 12.5 and 12.2, 16 of 1000 + 24 17.2 and 12.5, 38 of 500 + 64 (two turns) 23.0 and 16.0 but of
+// 1000 + 24 19.6 and 21.8, 48 of 256 + 256 (three) 28 and 20; d = 64, 8 of 1500 + 64 13.5 and 11.7.
+bool whole_with_prefix(long long segments, int d, long long max_keys) {
+  const long long turns = (segments + fa::kPagedCtas - 1) / fa::kPagedCtas;
+  if (turns == 1) return max_keys <= (d == 64 ? 1536 : 1152);
+  return (turns == 2 && max_keys <= 640) || (turns == 3 && max_keys <= 512);
 }
 
 // Groups of 8 lanes per row of the join.  A group reads its parts two at a time, so few rows, which
@@ -231,11 +242,13 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     const long long tokens = i == 0 && max_q < total ? max_q : total;
     const long long rows = (i == 0 ? tokens : (total + count[i] - 1) / count[i]) * (H / Hkv);
     mma[i] = rows > mma_rows(d, lists);
-    if (lists == 1) {
+    if (i == 0) {
       segments = B * ((rows + fa::kPagedRows - 1) / fa::kPagedRows) * Hkv;
-      whole = whole_segments(segments, mma[0], max_kv);
+      whole = lists == 1 ? whole_segments(segments, mma[0], max_kv)
+                         : whole_with_prefix(segments, d,
+                                             static_cast<long long>(max_kv) + prefix->max_len);
       mma[0] = mma[0] && !whole;
-      twin = rows <= 128;
+      twin = lists == 1 && rows <= 128;
     }
     // row tiles over all entries x heads x key tiles: the units of a launch, which fit 32 bits
     const long long keys = i == 0 ? max_kv : prefix->max_len;
@@ -279,7 +292,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   j.G = a.G;
   j.lists = lists;
   CUtensorMap tk, tv;
-  const bool any_mma = mma[0] || (lists > 1 && mma[1]);
+  const bool any_mma = !whole && (mma[0] || (lists > 1 && mma[1]));
   if (any_mma &&
       (!make_pool_map(&tk, cache->k_cache, *cache, Hkv, d) ||
        !make_pool_map(&tv, cache->v_cache, *cache, Hkv, d)))
@@ -311,7 +324,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   a.mma_cost = mma_tile_cost(d);
   if (whole) {
     a.list[0].unsplit = kMaxInt;
-    return status_of(fa::launch_paged_cta(d, a, segments, s));
+    return status_of(fa::launch_paged_cta(d, a, lists, segments, s));
   }
   const long long all = units[0] + (lists > 1 ? units[1] : 0);
   const cudaError_t e =

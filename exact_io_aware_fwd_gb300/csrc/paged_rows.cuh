@@ -13,6 +13,8 @@
 // element and 2 bytes is 32 flops a byte, a few percent of the tensor pipe at full bandwidth.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "fa_paged.h"
 #include "paged_plan.cuh"
@@ -81,6 +83,24 @@ struct Source {
   int hk, len;          // key/value head, keys
   int first, steps;     // key tile of step 0, number of steps
   int pages;            // lane i: page of step (issue & ~31) + i
+  static constexpr bool kPrefix = false;
+  struct Place {
+    const int32_t* row;  // block-table row
+    int key, len;        // first key of a step and the keys behind that row
+    bool shared;         // of a prefix
+  };
+  __device__ Place place(int st) const { return {trow, (first + st) * KT, len, false}; }
+};
+
+// The same with the keys of a shared prefix in front (key tiles 0 .. pre - 1).
+struct PrefixedSource : Source {
+  const int32_t* prow;
+  int pre, plen;
+  static constexpr bool kPrefix = true;
+  __device__ Place place(int st) const {
+    const int t = first + st;
+    return t < pre ? Place{prow, t * KT, plen, true} : Place{trow, (t - pre) * KT, len, false};
+  }
 };
 
 __device__ __forceinline__ Source source_of(const KeyList& l, const Walk<R, KT>& w,
@@ -97,27 +117,30 @@ __device__ __forceinline__ Source source_of(const KeyList& l, const Walk<R, KT>&
 
 // Copies step st into its stage (zeros for keys past the length and, reported, for a page outside
 // the pool); every call commits a group, empty past the last step.
-template <int D>
-__device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l, Source& s,
-                                           int st, uint32_t ring, int lane) {
+template <int D, typename Src>
+__device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l, Src& s, int st,
+                                           uint32_t ring, int lane) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages, GR = D / 8;  // granules of a row
   if (st < s.steps) {
-    if ((st & 31) == 0)
-      s.pages = st + lane < s.steps ? resolve_page(s.trow, l.max_pages, a.num_pages,
-                                                   a.page_shift, (s.first + st + lane) * KT)
-                                    : 0;
+    if ((st & 31) == 0) {
+      const auto p = s.place(st + lane);
+      const int max_pages = p.shared ? a.list[1].max_pages : l.max_pages;
+      s.pages = st + lane < s.steps
+                    ? resolve_page(p.row, max_pages, a.num_pages, a.page_shift, p.key)
+                    : 0;
+    }
     const int page = __shfl_sync(~0u, s.pages, st & 31);
-    const int key0 = (s.first + st) * KT;
+    const auto p = s.place(st);
     const int slot = st % S;
     if (page < 0 && lane == 0) atomicCAS(a.status, 0, kErrIndex);
     const int64_t base = (((static_cast<int64_t>(max(page, 0)) * a.Hkv + s.hk) << a.page_shift) +
-                          (key0 & ((1 << a.page_shift) - 1))) * D;
+                          (p.key & ((1 << a.page_shift) - 1))) * D;
     const uint32_t dst = ring + slot * L::kStage;
 #pragma unroll
     for (int i = 0; i < KT * GR / 32; ++i) {
       const int r = (i * 32 + lane) / GR, g = (i * 32 + lane) % GR;
-      const bool valid = page >= 0 && key0 + r < s.len;
+      const bool valid = page >= 0 && p.key + r < p.len;
       const int64_t off = valid ? base + r * D + g * 8 : 0;
       cp_async16(dst + step_offset<D>(r, g), a.k_cache + off, valid);
       cp_async16(dst + L::kHalf + step_offset<D>(r, g), a.v_cache + off, valid);
@@ -169,8 +192,8 @@ struct Acc {
 };
 
 // The keys of a source, whose first S - 1 steps have been issued.
-template <int D>
-__device__ __forceinline__ void scan_keys(const PagedArgs& a, const KeyList& l, Source& src,
+template <int D, typename Src>
+__device__ __forceinline__ void scan_keys(const PagedArgs& a, const KeyList& l, Src& src,
                                           const QRows<D>& x, uint32_t ring, int lane, Acc<D>& c) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages;
@@ -190,14 +213,14 @@ __device__ __forceinline__ void scan_keys(const PagedArgs& a, const KeyList& l, 
         mma16816(s[1], x.qf[k], f[2], f[3]);
       }
     }
-    const int key0 = (src.first + st) * KT;
-    if (key0 + KT > x.lim_min) {
+    const auto p = src.place(st);
+    if (p.key + KT > (p.shared ? p.len : x.lim_min)) {  // all of a prefix is visible
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int key = key0 + n * 8 + (lane & 3) * 2 + (k & 1);
-          if (key >= x.lim[k >> 1]) s[n][k] = -INFINITY;
+          const int key = p.key + n * 8 + (lane & 3) * 2 + (k & 1);
+          if (key >= (p.shared ? p.len : x.lim[k >> 1])) s[n][k] = -INFINITY;
         }
     }
     // online softmax; the row maximum is shared by the four lanes of a row, the sum is
@@ -223,9 +246,9 @@ __device__ __forceinline__ void scan_keys(const PagedArgs& a, const KeyList& l, 
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           // the scale is never 0, so a hidden score stays -inf and weighs 0
-          const float p = ex2(fmaf(s[n][2 * i + k], a.scale_log2, -ref));
-          s[n][2 * i + k] = p;
-          total += p;
+          const float e = ex2(fmaf(s[n][2 * i + k], a.scale_log2, -ref));
+          s[n][2 * i + k] = e;
+          total += e;
         }
       c.sum[i] = c.sum[i] * alpha[i] + total;
     }
@@ -328,8 +351,9 @@ __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
 
 // Few short segments: the 8 warps of a CTA take an eighth of a segment's keys each and meet in
 // shared memory (their own rings, whose copies have all been read), so that nothing is left to
-// join.  The Share is the CTA's: its units are whole segments.
-template <int D>
+// join.  The Share is the CTA's: its units are whole segments.  kPrefix: a sequence's keys are those
+// of its group's prefix and then its own; the prefix is read once per sequence, from L2.
+template <int D, bool kPrefix>
 __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList& l, const Share& sh,
                                               uint8_t* smem, int warp, int lane) {
   using L = PagedLayout<D>;
@@ -341,7 +365,17 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
   Piece piece;
   while (walk.next(a, l, piece)) {
     const Entry& e = walk.e;
-    Source src = source_of(l, walk, piece);
+    std::conditional_t<kPrefix, PrefixedSource, Source> src;
+    static_cast<Source&>(src) = source_of(l, walk, piece);
+    if constexpr (kPrefix) {
+      const KeyList& pl = a.list[1];
+      const int g = token_sequence_group<32>(pl.group_cu, pl.count, walk.b, lane, ~0u);
+      // a sequence of no group has no prefix
+      src.plen = g >= 0 ? entry_of<R, KT>(pl, a, g, false).len : 0;
+      src.prow = pl.table + static_cast<int64_t>(max(g, 0)) * pl.max_pages;
+      src.pre = (src.plen + KT - 1) / KT;
+      src.steps += src.pre;
+    }
     const int t0 = warp * src.steps / kWarps, t1 = (warp + 1) * src.steps / kWarps;
     src.first += t0;
     src.steps = t1 - t0;

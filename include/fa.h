@@ -360,7 +360,8 @@ fa_status fa_fwd_paged(const void* Q, const fa_paged_kv* cache, void* O, float* 
  * group_cu[g + 1]) (DEVICE int32[groups + 1], group_cu[0] = 0, group_cu[groups] = B) all begin
  * with the prefix_lens[g] keys in pages prefix_table[g] (DEVICE int32 [groups][prefix_pages],
  * pages of the same cache), followed by their own kv_lens[b] keys.  Every query sees its whole
- * prefix; causal concerns the own keys.  A prefix is read once for all queries of its group.
+ * prefix; causal concerns the own keys.  A prefix is read once for all queries of its group
+ * (small batches of short sequences: from L2 for each sequence).
  * kv_lens[b] and prefix_lens[g] may be 0.  max_prefix: at least the longest prefix.
  * workspace: fa_fwd_shared_prefix_workspace_size(...) bytes, else as fa_fwd_paged.
  */

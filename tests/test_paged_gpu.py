@@ -612,6 +612,8 @@ def test_shared_prefix(batch, heads):
     H, Hkv, d, page = heads
     for causal in (True, False):
         run_prefix(*batch, H, Hkv, d, page, causal, seed=60 + H)
+        # under a bound that is too long for whole sequences a CTA
+        run_prefix(*batch, H, Hkv, d, page, causal, seed=60 + H, max_prefix=5000)
 
 
 def test_shared_prefix_large_groups():
@@ -619,6 +621,53 @@ def test_shared_prefix_large_groups():
     rng = np.random.default_rng(8)
     run_prefix([70, 9], [1500, 40], [2] * 79, rng.integers(2, 90, 79).tolist(), 8, 2, 128, 64, True, seed=71)
     run_prefix([150], [777], [1] * 150, rng.integers(0, 30, 150).tolist(), 6, 2, 64, 16, True, seed=72)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_prefix_whole_sequences(d):
+    """Sequences small enough for a CTA each, prefix and own keys: one, two and three turns, several
+    row tiles, prefixes and sequences without keys, tokens without own keys."""
+    rng = np.random.default_rng(28)
+    run_prefix([1, 3, 15], [1000, 17, 0], [1] * 19, rng.integers(0, 150, 19).tolist(), 32, 8, d, 16, True, seed=81)
+    run_prefix([20, 16], [500, 33], [1] * 36, rng.integers(0, 100, 36).tolist(), 8, 8, d, 64, True, seed=82)
+    run_prefix([50], [256], [1] * 50, rng.integers(0, 256, 50).tolist(), 8, 8, d, 32, False, seed=83)
+    run_prefix([2, 0, 2], [100, 5, 300], [40, 7, 0, 33], [40, 3, 2, 90], 8, 2, d, 128, True, seed=84)
+
+
+def test_shared_prefix_of_the_sequences_own_table():
+    """One table for both: every sequence's own keys are its prefix's pages again."""
+    cache = Cache([100, 37], 2, 64, 32, seed=85)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(2, 4, 64, device=DEV).to(BF16)
+    own = i32([70, 20])
+    for bounds in (dict(max_prefix=100, max_kv=70), dict(max_prefix=4000, max_kv=4000)):
+        out, lse = fa.fa_fwd_shared_prefix(q, k, v, table, own, table, lens, i32([0, 1, 2]), **bounds)
+        assert fa.fa_get_error() == fa.FA_OK
+        per = []
+        for b, n in enumerate((70, 20)):
+            K, V = cache.keys(b)
+            per.append((np.concatenate([K, K[:, :n]], 1), np.concatenate([V, V[:, :n]], 1), [cache.lens[b] + n]))
+        check(out, lse, q, [0, 1, 2], per, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("bound", [300, 5000], ids=["whole", "two lists"])
+def test_shared_prefix_reports_what_is_out_of_range(bound):
+    cache = Cache([20, 30, 200], 1, 64, 16, seed=86)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(2, 2, 64, device=DEV).to(BF16)
+    args = [q, k, v, table[:2].contiguous(), lens[:2].contiguous(), table[2:].contiguous(), lens[2:].contiguous()]
+    want = fa.fa_fwd_shared_prefix(*args, i32([0, 2]), max_prefix=bound, max_kv=30)[0]
+    assert fa.fa_get_error() == fa.FA_OK
+    long = args[:6] + [i32([5000 + bound])]
+    got = fa.fa_fwd_shared_prefix(*long, i32([0, 2]), max_prefix=200, max_kv=30 if bound == 300 else 5000)[0]
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    assert torch.allclose(got.float(), want.float(), atol=2 ** -6)
+    bad = args[5].clone()
+    bad[0, 3] = -1
+    fa.fa_fwd_shared_prefix(*args[:5], bad, args[6], i32([0, 2]), max_prefix=bound, max_kv=30)
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    fa.fa_fwd_shared_prefix(*args, i32([0, 9]), max_prefix=bound, max_kv=30)
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
 
 
 @pytest.mark.parametrize("d", [64, 128])
