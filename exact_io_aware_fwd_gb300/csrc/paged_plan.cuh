@@ -224,9 +224,11 @@ __device__ __forceinline__ void make_shares(const PagedArgs& a, Share* shares) {
 
 // CTAs of `ctas` that work on list 1.  Costs are in key tiles of the few-row kernel, whose segments
 // cost 8 more each (their queries to load and result to write; 23 sequences without keys of their
-// own behind 24751: 35 us, 42 without the term); those of the tensor-core kernel are few.
+// own behind 24751: 35 us, 42 without the term), and a segment of the tensor-core kernel six of
+// its key tiles (100 sequences of 700 keys behind three prefixes of 400: 59 us, 65 with three, 78
+// without; 120 of 900 behind ten of 100: 52, 52 and 83).
 __device__ __forceinline__ float list_cost(const PagedArgs& a, const KeyList& l, const Totals& t) {
-  return l.mma ? t.til * a.mma_cost : t.til + 8.f * t.seg;
+  return l.mma ? (t.til + 6.f * t.seg) * a.mma_cost : t.til + 8.f * t.seg;
 }
 __device__ __forceinline__ int ctas_of_second(const PagedArgs& a, int ctas, const Totals (&t)[2]) {
   if (t[1].til == 0 || t[0].til == 0) return t[1].til == 0 ? 0 : ctas;
