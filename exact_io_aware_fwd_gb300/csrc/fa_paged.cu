@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
                   lane);
 }
 
-// Few short segments: no CTA shares one, no join.  kPrefix: list 1 holds the shared prefixes.
+// Few segments, a CTA as the worker.  kPrefix: whole segments only, list 1 holds the prefixes.
 template <int D, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1) paged_cta_kernel(const __grid_constant__ PagedArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_cta_kernel(const __grid_con
   if (kPrefix && blockIdx.x == 0)  // what is out of range in the groups is reported here
     for (int g = threadIdx.x; g < a.list[1].count; g += kThreads)
       entry_of<rows16::R, rows16::KT>(a.list[1], a, g, true);
-  rows16::work_together<D, kPrefix>(a, a.list[0], shares[0], smem, threadIdx.x >> 5, threadIdx.x & 31);
+  rows16::work_together<D, kPrefix>(a, a.list[0], a.part[0], shares[0], smem, threadIdx.x >> 5, threadIdx.x & 31);
 }
 
 // ---- join of the parts

@@ -210,8 +210,8 @@ constexpr int kPagedMmaRows = 256;       // the tensor-core kernel, whose CTAs a
 constexpr int kPagedMmaKeys = 128;
 
 cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s);
-// Segments of list 0, with their prefixes (lists == 2), that are not split; max_units: how many at
-// most.
+// Few segments: list 0, with its prefixes (lists == 2: segments are then not split).  max_units: as
+// many CTAs as have work.
 cudaError_t launch_paged_cta(int d, const PagedArgs& a, int lists, int64_t max_units,
                              cudaStream_t s);
 // twin: one list, and no entry has more than 128 rows

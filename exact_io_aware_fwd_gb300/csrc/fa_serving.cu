@@ -152,6 +152,15 @@ bool whole_segments(long long segments, bool many_rows, int max_kv) {
   return segments <= 2 * fa::kPagedCtas && !many_rows && max_kv > 64 && max_kv <= 512;
 }
 
+// Few segments that are split: whether CTAs are the workers, an eighth of the parts to join (split
+// over warps and over CTAs: one segment of 4000 keys 10.6 and 8.8 us, of 16000 18.1 and 10.1, of
+// 64000 32.8 and 14.1; 8 segments of 2000 keys 10.8 and 11.5, of 32000 31.5 and 27.5; 16 of 8000
+// 14.5 and 16.0).  Segments of up to 64 tiles are whole.
+constexpr int kUnsplitTilesTogether = 64;
+bool cta_workers(long long segments, int max_kv) {
+  return segments <= 8 && max_kv >= 500 * segments;
+}
+
 // The same behind a shared prefix, which is then read (from L2) for each sequence: 0.55 us per 100
 // keys and turn at d = 128, 0.4 at d = 64, against 10 to 20 us of two lists and a join.  d = 128, 8
 // heads, prefix + own keys, two lists and whole: 4 sequences of 256 + 16 10.5 and 7.6 us, of 1000 +
@@ -327,8 +336,14 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     return status_of(fa::launch_paged_cta(d, a, lists, segments, s));
   }
   const long long all = units[0] + (lists > 1 ? units[1] : 0);
+  const bool together = lists == 1 && !mma[0] && cta_workers(segments, max_kv);
+  if (together) {
+    a.part[0].workers = j.part[0].workers = fa::kPagedCtas;
+    a.list[0].unsplit = j.list[0].unsplit = kUnsplitTilesTogether;
+  }
   const cudaError_t e =
-      any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, twin, all, fa::wait_timeout_ns(), s)
+      together ? fa::launch_paged_cta(d, a, 1, all, s)
+      : any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, twin, all, fa::wait_timeout_ns(), s)
               : fa::launch_paged(d, a, lists, all, s);
   if ((st = status_of(e)) != FA_OK) return st;
   // no entry can have been split (lengths are clamped to max_kv): every result is final

@@ -1,5 +1,5 @@
 // How the workers of a paged-attention launch share the keys of a list (a worker: a CTA of the
-// tensor-core kernel, a warp of the other one).
+// tensor-core kernel or, where segments are few, of the other one, else a warp of that).
 //
 // The work of entry b is one segment per (key/value head, row tile), each of as many key tiles
 // (KT keys) as the tile's last row sees.  Laid end to end, the segments' key tiles are units
@@ -155,7 +155,9 @@ __device__ __forceinline__ void share_list(const PagedArgs& a, const KeyList& l,
   const int W = direct ? t.seg : t.til;
   // shares of one tile are not worth their slots (one sequence of 1000 keys and 8 heads takes 10.1
   // us either way; shares of at least four take 11.5 us, of eight 13.4)
-  const int most = direct ? W : (W + 1) / 2;
+  // (a CTA as the worker of the few-row kernel: two tiles a warp)
+  constexpr int kMin = KT == kPagedKeys && kWorkers == 1 ? 2 * kPagedWarps : 2;
+  const int most = direct ? W : (W + kMin - 1) / kMin;
   const int C = min(most, ctas * kWorkers);
   if (tid < kWorkers) {
     Share& s = shares[tid];

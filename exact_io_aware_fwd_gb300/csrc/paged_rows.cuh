@@ -349,12 +349,13 @@ __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
   cp_wait<0>();
 }
 
-// Few short segments: the 8 warps of a CTA take an eighth of a segment's keys each and meet in
-// shared memory (their own rings, whose copies have all been read), so that nothing is left to
-// join.  The Share is the CTA's: its units are whole segments.  kPrefix: a sequence's keys are those
+// Few segments: the 8 warps of a CTA take an eighth of a piece's keys each and meet in shared memory
+// (their own rings, whose copies have all been read), so that short segments leave nothing to join
+// and long ones an eighth of the parts.  The Share is the CTA's.  kPrefix: a sequence's keys are those
 // of its group's prefix and then its own; the prefix is read once per sequence, from L2.
 template <int D, bool kPrefix>
-__device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList& l, const Share& sh,
+__device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList& l,
+                                              const PartialLayout& parts, const Share& sh,
                                               uint8_t* smem, int warp, int lane) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages, P = D + 8;  // row pitch of a warp's O in floats
@@ -376,7 +377,11 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
       src.pre = (src.plen + KT - 1) / KT;
       src.steps += src.pre;
     }
-    const int t0 = warp * src.steps / kWarps, t1 = (warp + 1) * src.steps / kWarps;
+    if (threadIdx.x == 0 && piece.ta == 0)  // this CTA begins the segment
+      parts.spans[static_cast<int64_t>(piece.hk) * parts.span_tiles +
+                  row_tile0(e.start, a.G, R, walk.b) + piece.r] = span_of(sh, piece);
+    const int t0 = static_cast<int>(static_cast<int64_t>(warp) * src.steps / kWarps);
+    const int t1 = static_cast<int>(static_cast<int64_t>(warp + 1) * src.steps / kWarps);
     src.first += t0;
     src.steps = t1 - t0;
     for (int st = 0; st < S - 1; ++st) issue_step<D>(a, l, src, st, ring, lane);
@@ -427,7 +432,18 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
         o[4 * i + 3] = fmaf(f, v.w, o[4 * i + 3]);
       }
     }
-    if (rr < x.rows) {
+    if (rr < x.rows && !piece.whole) {
+      float* slot = parts.slots + (static_cast<int64_t>(sh.worker) * 2 + (piece.ta == 0)) *
+                                      (R * (D + 2));
+      float4* dst = reinterpret_cast<float4*>(slot + rr * D + part * E);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i)
+        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      if (part == 0) {
+        slot[R * D + rr] = top;
+        slot[R * D + R + rr] = sum;
+      }
+    } else if (rr < x.rows) {
       const int row = piece.r * R + rr, tok = row / a.G;
       const int head = piece.hk * a.G + (row - tok * a.G);
       const int64_t at = static_cast<int64_t>(e.start + tok) * a.H + head;

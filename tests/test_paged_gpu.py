@@ -164,6 +164,18 @@ def test_paged_whole_segments_of_several_row_tiles(d):
         run_paged([5] * 19, list(range(1, 20)), 32, 8, d, 32, causal, seed=53)  # 304 row tiles, few keys
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,lens", [([1], [20000]), ([1, 1, 1, 1], [5000, 0, 1025, 16]), ([3, 0, 2], [9001, 7, 1]),
+                                     ([1] * 8, [4100, 1024, 1030, 1, 0, 4000, 17, 2048]), ([16], [6000])],
+                         ids=lambda x: "-".join(map(str, x)))
+def test_paged_few_long_segments(nq, lens, d):
+    """At most 8 segments: CTAs share their keys."""
+    for H in (1, 4):
+        _, q, out, lse = run_paged(nq, lens, H, 1, d, 64, True, seed=61)
+        again = run_paged(nq, lens, H, 1, d, 64, True, seed=61)
+        assert torch.equal(out, again[2]) and torch.equal(lse, again[3])
+
+
 @pytest.mark.parametrize("B,most", [(19, 1024), (19, 1025), (20, 512), (20, 513), (20, 64), (38, 300), (39, 300)])
 def test_paged_where_whole_segments_end(B, most):
     """152 and 304 segments, 512 and 1024 keys: on both sides of the sizes at which a CTA takes whole
