@@ -437,12 +437,14 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocksPerSm) rope_bwd_kernel(con
           for (int e = 0; e < 4; ++e) u.v[e] = mul2(g.v[e], w.v[e]);
           const float ss = group_sum<L>(dot(x, x), mask), ux = group_sum<L>(dot(u, x), mask);
           const float rs = rsqrtf(ss * (1.f / D) + a.eps);
-          // dx = r u - x r^3 mean(u x)
-          const float k = -rs * rs * rs * (ux * (1.f / D));
+          // with x r, of the size of 1, in place of x: no power of r, which leaves float32's range
+          // long before dx does (rows of rms 1e-13 or 1e15)
+          const float c = -(rs * ux) * (1.f / D);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            dw.v[e] = fma2(mul2(g.v[e], make_float2(rs, rs)), x.v[e], dw.v[e]);
-            g.v[e] = fma2(x.v[e], make_float2(k, k), mul2(u.v[e], make_float2(rs, rs)));
+            const float2 xr = mul2(x.v[e], make_float2(rs, rs));
+            dw.v[e] = fma2(g.v[e], xr, dw.v[e]);
+            g.v[e] = mul2(fma2(xr, make_float2(c, c), u.v[e]), make_float2(rs, rs));
           }
         }
         r = pack(g);

@@ -149,6 +149,35 @@ def test_backward_weight_gradient_over_many_rows():
         assert np.all(np.abs(f64(dw) - ref) <= 7.6e-6 * size)
 
 
+@pytest.mark.parametrize("scale", [1e-18, 1e-12, 1e15, 1e18])
+@pytest.mark.parametrize("d,inter", [(64, True), (128, False)])
+def test_norms_of_very_small_and_large_rows(d, inter, scale):
+    """Rows whose mean square is far from 1 but a float32 (the mean of d squares at 1e18: at most
+    3e37), without eps: results and gradients, of the size of 1 and of 1 / scale, keep the bounds of
+    the other tests, which are relative."""
+    T, H, Hkv = 50, 4, 2
+    g = torch.Generator().manual_seed(d)
+    x = (scale * torch.randn(T, H + Hkv, d, generator=g)).to(torch.bfloat16).to(DEV)
+    wq, wk = ((1 + 0.3 * torch.randn(d, generator=g)).to(DEV) for _ in range(2))
+    inv, _ = fa.rope_frequencies(d)
+    opts = dict(table=fa.fa_rope_table(T, d, inv_freq=inv), interleaved=inter, q_weight=wq, k_weight=wk, eps=0.0)
+    ref = dict(inv_freq=inv.numpy(), interleaved=inter, eps=0.0)
+    q, k = x.split([H, Hkv], dim=-2)
+    out = fa.fa_qk_norm_rope_fwd(q, k, **opts)
+    dz = [torch.randn(T, h, d, generator=g).to(torch.bfloat16).to(DEV) for h in (H, Hkv)]
+    dq, dk, _, dwq, dwk = fa.fa_qk_norm_rope_bwd(*dz, None, q, k, **opts)
+    assert fa.fa_get_error() == fa.FA_OK
+    for o, got, dwg, z, t, w in ((out[0], dq, dwq, dz[0], q, wq), (out[1], dk, dwk, dz[1], k, wk)):
+        r = norm_rope(f64(t), np.arange(T), f64(w), **ref)
+        close(o, r, 2.0 ** -19 * np.abs(r).max(-1, keepdims=True) * 2, "z")
+        r, dw, size = norm_rope_backward(f64(z), f64(t), np.arange(T), f64(w), **ref)
+        rs = 1 / np.sqrt((f64(t) ** 2).mean(-1, keepdims=True))
+        u = np.abs(f64(z)).max(-1, keepdims=True) * 1.5 * np.abs(f64(w)).max()
+        slack = 2.0 ** -16 * rs * u * (1 + (np.abs(f64(t)) * rs).max(-1, keepdims=True) ** 2)
+        close(got, r, slack, "dx")
+        assert np.all(np.abs(f64(dwg) - dw) <= 7.6e-6 * size + 1e-30)
+
+
 def test_table_far_positions_and_amplitude():
     """cos and sin of positions up to 10^6 to half a float32 step of a value of at most 1.2 (the
     angle is a float64 product, off by 2^-53 x 10^6), with yarn's amplitude."""
