@@ -226,6 +226,33 @@ def test_rope_frequencies():
             fa.rope_frequencies(**bad)
 
 
+def test_yarn_ramp_between_whole_pairs():
+    """The ends of the ramp by hand: (rot / 2) ln(len / (2 pi turns)) / ln(base) is 23.6 and 39.65 for
+    rot 128, base 10^6 over 32768 positions at 32 turns and 1, and 20.9 and 45.03 for base 10^4 over
+    4096; rounded outwards 23, 40 and 20, 46."""
+    i = np.arange(64)
+    for base, factor, length, lo, hi in ((1e6, 4.0, 32768, 23, 40), (1e4, 16.0, 4096, 20, 46)):
+        inv = base ** (-i / 64)
+        keep = 1 - np.clip((i - lo) / (hi - lo), 0, 1)
+        got, _ = fa.rope_frequencies(128, base, "yarn", factor, length)
+        np.testing.assert_allclose(got.numpy(), inv * (keep + (1 - keep) / factor), rtol=1e-13)
+        # ends between pairs, on request
+        lo, hi = (64 * math.log(length / (2 * math.pi * t)) / math.log(base) for t in (32, 1))
+        keep = 1 - np.clip((i - lo) / (hi - lo), 0, 1)
+        cut, _ = fa.rope_frequencies(128, base, "yarn", factor, length, whole_pairs=False)
+        np.testing.assert_allclose(cut.numpy(), inv * (keep + (1 - keep) / factor), rtol=1e-13)
+        assert np.abs((cut / got).numpy() - 1).max() > 0.04
+    # every pair turns less than 32 times over 128 positions: the ramp begins at pair 0; short and
+    # long lengths leave it a length
+    got, _ = fa.rope_frequencies(128, 1e4, "yarn", 2.0, 128)
+    assert got[0] == 1.0 and 0.5 < got[1] * 1e4 ** (1 / 64) < 1.0
+    for length in (1, 5, 1 << 40):
+        got, _ = fa.rope_frequencies(64, 1e4, "yarn", 8.0, length)
+        ratio = got.numpy() * 1e4 ** (np.arange(32) / 32)
+        assert np.all((ratio > 1 / 8 - 1e-12) & (ratio < 1 + 1e-12)) and np.all(np.diff(ratio) < 1e-12)
+    assert np.allclose(ratio, 1.0)
+
+
 # ------------------------------------------------------------------------------- the reference
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("norm", [False, True])
