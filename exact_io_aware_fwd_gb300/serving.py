@@ -5,7 +5,8 @@ As in binding.py only argument checks and marshalling happen on the way to the l
 are compiled (csrc/serving_binding.cpp), because the smallest of these calls are a few
 microseconds of kernel.  Calls launch on the tensors' device, on its current stream or on
 ``stream``; what a call allocates is allocated on the stream it launches on, and outputs are
-recorded on the current one as well.
+recorded on the current one as well.  Inputs are not recorded on ``stream``: as everywhere in
+PyTorch, a tensor that is freed while another stream may still read it is the caller's to keep.
 """
 
 from __future__ import annotations
@@ -121,6 +122,9 @@ def fa_rope_table(n_pos, rot, base=10000.0, scaling=None, factor=1.0, original_l
         inv_freq, amplitude = rope_frequencies(rot, base, scaling, factor, original_len)
     if inv_freq.dtype != torch.float64 or tuple(inv_freq.shape) != (rot // 2,):
         raise ValueError("inv_freq must be float64 [rot / 2]")
+    if stream is not None and stream.device != device:
+        raise ValueError("stream must be one of the table's device")
+    caller = torch.cuda.current_stream(device)
     with torch.cuda.device(device), torch.cuda.stream(stream):
         freq = inv_freq.to(device).contiguous()
         table = torch.empty((n_pos, rot), dtype=torch.float32, device=device)
@@ -128,6 +132,8 @@ def fa_rope_table(n_pos, rot, base=10000.0, scaling=None, factor=1.0, original_l
                                           table.data_ptr(),
                                           torch.cuda.current_stream(device).cuda_stream)
     _check(st, "fa_rope_table")
+    if stream is not None and stream != caller:
+        table.record_stream(caller)
     return table
 
 

@@ -255,6 +255,22 @@ def test_strides_in_place_streams_and_graph():
     assert fa.fa_get_error() == fa.FA_OK
 
 
+def test_table_made_on_another_stream_is_kept_while_the_current_one_may_read_it():
+    """A table dropped while work on the caller's stream is still ahead is not handed to the next
+    call on the side stream that made it."""
+    side, first = torch.cuda.Stream(), fa.fa_rope_table(4096, 64)
+    torch.cuda.synchronize()
+    table = fa.fa_rope_table(4096, 64, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(200_000_000)  # about a tenth of a second
+    got, where = table.clone(), table.data_ptr()
+    del table
+    other = fa.fa_rope_table(4096, 64, base=100.0, stream=side)
+    assert other.data_ptr() != where
+    torch.cuda.synchronize()
+    assert torch.equal(got, first) and not torch.equal(other, first)
+
+
 def test_empty_and_refusals():
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
     k = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)

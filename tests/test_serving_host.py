@@ -201,6 +201,13 @@ def test_binding_refuses_host_tensors_and_other_objects(lib):
         fa.fa_fwd_paged(q, cache, cache, table)
 
 
+def test_rope_table_refuses_a_stream_of_another_device():
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError):
+        fa.fa_rope_table(8, 64, device="cuda:0", stream=Elsewhere())
+
 
 # ----------------------------------------------------------------------------- rotary frequencies
 def test_rope_frequencies():
