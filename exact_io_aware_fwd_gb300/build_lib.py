@@ -1,10 +1,10 @@
 """Builds libfa_sm103.so (the C-ABI library) in-tree with nvcc for sm_103a, and the compiled
-Python binding of the operators around attention (_serving_binding.so) with g++.
+Python binding of the operators around attention (_serving_binding.*.so) with g++.
 
 The translation units are compiled in parallel into ``<repo>/_build`` and linked into
 ``exact_io_aware_fwd_gb300/libfa_sm103.so``.  A rebuild happens only when a source or header is
 newer than the library (or when ``force=True``).  The binding compiles next to them; it belongs to
-the PyTorch it was built with.
+the PyTorch and the Python it was built with, whose versions are in its name.
 """
 
 from __future__ import annotations
@@ -16,12 +16,21 @@ import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
+import torch
+
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfa_sm103.so")
-BINDING_PATH = os.path.join(PKG_DIR, "_serving_binding.so")
+
+
+def binding_path(torch_version: str, suffix: str) -> str:
+    """The binding's file for a PyTorch version and Python's suffix of extension modules."""
+    return os.path.join(PKG_DIR, f"_serving_binding.torch-{torch_version}{suffix}")
+
+
+BINDING_PATH = binding_path(torch.__version__, sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_block_sparse.cu", "fa_noalloc.cu",
            "fa_serving.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_mma.cu"]
@@ -50,8 +59,6 @@ def _stale(target, deps):
 
 
 def _binding_command(out):
-    import torch
-
     home = os.path.dirname(os.path.abspath(torch.__file__))
     include = os.path.join(home, "include")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))

@@ -6,13 +6,14 @@ import math
 import os
 import struct
 import subprocess
+import sysconfig
 
 import numpy as np
 import pytest
 import torch
 
 import exact_io_aware_fwd_gb300 as fa
-from exact_io_aware_fwd_gb300 import build_lib
+from exact_io_aware_fwd_gb300 import build_lib, serving
 from oracle import attention_forward
 from oracle.serving import attend, norm_rope, norm_rope_backward, paged_keys, rotate
 
@@ -199,6 +200,20 @@ def test_binding_refuses_host_tensors_and_other_objects(lib):
         fa.fa_qk_norm_rope_bwd(q, None)
     with pytest.raises(TypeError):
         fa.fa_fwd_paged(q, cache, cache, table)
+
+
+def test_binding_belongs_to_one_pytorch_and_python(lib, monkeypatch):
+    """A binding built with another PyTorch or Python is another file: it is neither taken for this
+    one nor loaded in its place."""
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    assert build_lib.BINDING_PATH == build_lib.binding_path(torch.__version__, suffix)
+    assert os.path.exists(build_lib.BINDING_PATH)
+    others = [build_lib.binding_path("1.0", suffix), build_lib.binding_path(torch.__version__, ".cpython-30.so")]
+    assert len({build_lib.BINDING_PATH, *others}) == 3
+    monkeypatch.setattr(serving, "BINDING_PATH", others[0])
+    monkeypatch.setattr(serving, "_ext", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        serving._binding()
 
 
 def test_rope_table_refuses_a_stream_of_another_device():
