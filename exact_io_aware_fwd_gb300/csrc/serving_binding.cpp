@@ -293,9 +293,6 @@ PyObject* norm_rope_fwd(PyObject* const* a) {
   const fa_qk_transform t = transform(a[3], a[5], a[6], a[7], a[8], d, dev);
   const int32_t* pos = ints(tensor_or_none(a[4], "positions"), q.sizes().slice(0, nd - 2), dev, "positions");
   const c10::cuda::OptionalCUDAGuard guard(dev);
-  if (B == 0 || N == 0)
-    return wrap_all({fresh(shape(H), at::kBFloat16, dev), fresh(shape(Hkv), at::kBFloat16, dev),
-                     v != nullptr ? fresh(shape(Hkv), at::kBFloat16, dev) : at::Tensor()});
   fa_view in[3] = {rows(q, in_order, dev, "q"), rows(k, in_order, dev, "k"), {}}, out[3] = {};
   if (v != nullptr) in[2] = rows(*v, in_order, dev, "v");
   at::Tensor qo = own_rows(tensor_or_none(a[9], "q_out"), shape(H), out_order, dev, "q_out", out[0]);
@@ -303,6 +300,7 @@ PyObject* norm_rope_fwd(PyObject* const* a) {
   at::Tensor vo;
   if (v != nullptr)
     vo = own_rows(tensor_or_none(a[11], "v_out"), shape(Hkv), out_order, dev, "v_out", out[2]);
+  if (B == 0 || N == 0) return wrap_all({qo, ko, vo});
   check(p_rope_fwd(in, out, pos, dim32(B), dim32(N), dim32(H), dim32(Hkv), dim32(d), &t,
                    stream_of(dev)),
         "fa_qk_norm_rope_fwd");
@@ -353,11 +351,6 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
   fa_view grad[3] = {}, x[2] = {}, out[3] = {};
   const char* names[3] = {"dq_in", "dk_in", "dv_in"};
   for (int i = 0; i < (dv != nullptr ? 3 : 2); ++i) {
-    if (empty) {
-      if (given[i] == nullptr) out_t[i] = fresh(shape(i == 0 ? H : Hkv), at::kBFloat16, dev);
-      else out_t[i] = *given[i];
-      continue;
-    }
     const at::Tensor& z = i == 0 ? dq : (i == 1 ? dk : *dv);
     grad[i] = rows(z, order, dev, i == 0 ? "dq" : (i == 1 ? "dk" : "dv"));
     out_t[i] = own_rows(given[i], shape(i == 0 ? H : Hkv), out_order, dev, names[i], out[i]);
@@ -432,19 +425,16 @@ PyObject* kv_append(PyObject* const* a) {
   const c10::cuda::OptionalCUDAGuard guard(dev);
   at::Tensor qo;
   fa_view in[3] = {}, out{};
-  if (total > 0) {
-    if (q != nullptr) {
-      in[0] = rows(*q, kNH, dev, "q");
-      qo = own_rows(tensor_or_none(a[14], "q_out"), {total, H, c.d}, kNH, dev, "q_out", out);
-    }
-    in[1] = rows(k, kNH, dev, "k");
-    in[2] = rows(v, kNH, dev, "v");
+  if (q != nullptr) {
+    in[0] = rows(*q, kNH, dev, "q");
+    qo = own_rows(tensor_or_none(a[14], "q_out"), {total, H, c.d}, kNH, dev, "q_out", out);
+  }
+  in[1] = rows(k, kNH, dev, "k");
+  in[2] = rows(v, kNH, dev, "v");
+  if (total > 0)
     check(p_append(in, &out, &c.kv, cu, offset, dim32(c.B), dim32(total), dim32(H), dim32(c.Hkv),
                    dim32(c.d), &t, stream_of(dev)),
           "fa_kv_append");
-  } else if (q != nullptr) {
-    qo = fresh({0, H, c.d}, at::kBFloat16, dev);
-  }
   return wrap(qo);
 }
 
@@ -485,6 +475,7 @@ PyObject* attend(PyObject* const* a) {
   const c10::cuda::OptionalCUDAGuard guard(dev);
   const at::Tensor out = own_array(tensor_or_none(a[10], "out"), q.sizes(), at::kBFloat16, dev, "out");
   const at::Tensor lse = own_array(tensor_or_none(a[11], "lse"), {H, total}, at::kFloat, dev, "lse");
+  if (c.B == 0 && total == 0) return wrap_all({out, lse});  // an empty batch
   const int B = dim32(c.B), T = dim32(total), h = dim32(H), hkv = dim32(c.Hkv), d = dim32(c.d);
   const Workspace ws =
       workspace(tensor_or_none(a[12], "workspace"),

@@ -741,6 +741,33 @@ def test_shared_prefix_refusals():
         fa.fa_fwd_shared_prefix(*good, max_prefix=-1)
 
 
+def test_a_batch_of_no_sequences():
+    """No sequences and no tokens: every call of a step returns empty outputs, the given ones if any."""
+    H, Hkv, d = 4, 2, 64
+    k = torch.full((3, Hkv, 16, d), 5.0, dtype=BF16, device=DEV)
+    v = k.clone()
+    table, lens, zero = torch.empty(0, 4, dtype=torch.int32, device=DEV), i32([]), i32([0])
+    x = torch.empty(0, H + 2 * Hkv, d, dtype=BF16, device=DEV)
+    q_out, out, lse = torch.empty(0, H, d, dtype=BF16, device=DEV), torch.empty(0, H, d, dtype=BF16, device=DEV), \
+        torch.empty(H, 0, device=DEV)
+    for kw in ({}, dict(cu_seqlens=zero)):
+        assert fa.fa_kv_append(*x.split([H, Hkv, Hkv], dim=1), k, v, table, lens, q_out=q_out, **kw) is q_out
+        q = fa.fa_kv_append(*x.split([H, Hkv, Hkv], dim=1), k, v, table, lens, **kw)
+        got = fa.fa_fwd_paged(q, k, v, table, lens, **kw)
+        assert got[0].shape == (0, H, d) and got[1].shape == (H, 0)
+        got = fa.fa_fwd_paged(q, k, v, table, lens, out=out, lse=lse, **kw)
+        assert got[0] is out and got[1] is lse
+        for pre in (dict(table=table, lens=lens, cu=zero), dict(table=i32([[0]]), lens=i32([9]), cu=i32([0, 0]))):
+            got = fa.fa_fwd_shared_prefix(q, k, v, table, lens, pre["table"], pre["lens"], pre["cu"], **kw)
+            assert got[0].shape == (0, H, d) and got[1].shape == (H, 0)
+    assert torch.all(k == 5.0) and torch.all(v == 5.0)
+    with pytest.raises(ValueError):
+        fa.fa_kv_append(*x.split([H, Hkv, Hkv], dim=1), k, v, table, lens, q_out=q_out[:, :1])
+    with pytest.raises(ValueError):
+        fa.fa_fwd_paged(q, k, v, table, lens, out=lse)
+    assert fa.fa_get_error() == fa.FA_OK
+
+
 # -------------------------------------------------------------------------------------- as one run
 def test_calls_under_inference_mode_and_with_leaves():
     """Outputs allocated by the binding are ordinary tensors (inference tensors in that mode)."""

@@ -295,6 +295,26 @@ def test_empty_and_refusals():
         fa.fa_qk_norm_rope_fwd(q[..., :32], k[..., :32][..., ::2])
 
 
+@pytest.mark.parametrize("shape", [(0, 5), (2, 0), (0,)], ids=str)
+def test_empty_calls_return_the_given_outputs(shape):
+    """Calls without tokens check and return the outputs they are given, like the others."""
+    d, H, Hkv = 64, 4, 2
+    new = lambda h: torch.empty(*shape, h, d, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    att = lambda h: new(h) if len(shape) == 1 else new(h).transpose(1, 2).contiguous()  # noqa: E731
+    x, out, grads = [[f(h) for h in (H, Hkv, Hkv)] for f in (new, att, new)]
+    got = fa.fa_qk_norm_rope_fwd(*x, q_out=out[0], k_out=out[1], v_out=out[2])
+    assert all(a is b for a, b in zip(got, out))
+    got = fa.fa_qk_norm_rope_bwd(*out, dq_in=grads[0], dk_in=grads[1], dv_in=grads[2])
+    assert all(a is b for a, b in zip(got, grads)) and got[3] is None
+    assert [t.shape for t in fa.fa_qk_norm_rope_fwd(*x)] == [t.shape for t in out]
+    assert [t.shape for t in fa.fa_qk_norm_rope_bwd(*out)[:3]] == [t.shape for t in x]
+    with pytest.raises(ValueError):
+        fa.fa_qk_norm_rope_fwd(*x, q_out=out[1])
+    with pytest.raises(ValueError):
+        fa.fa_qk_norm_rope_bwd(*out, dk_in=grads[0])
+    assert fa.fa_get_error() == fa.FA_OK
+
+
 @pytest.mark.parametrize("norm", [False, True])
 def test_training_step_around_attention(norm):
     """Projection -> norms, rotation -> attention -> loss, and all gradients back to the fused
