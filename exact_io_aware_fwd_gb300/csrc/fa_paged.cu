@@ -114,8 +114,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
     if (where[li] < 0) continue;
     const PartialLayout& p = a.part[li];
     const int2 span = p.spans[where[li]];
-    // a launch that gave up leaves no span: nothing out of range is read
-    if (span.x < 0 || span.x >= p.workers || span.y < 1 || span.y > p.workers - span.x) continue;
+    if (!span_ok(span.x, span.y, p.workers)) continue;  // a launch that gave up left none
     const bool one = span.y == 1;
     if (one && a.rowbuf[li] == nullptr) {
       done = true;

@@ -174,6 +174,13 @@ __host__ __device__ inline int row_tile0(int start, int G, int R, int b) {
   return (start * G + R - 1) / R + b;  // never overlaps entry b - 1's tiles
 }
 
+// Whether a span read from the workspace names workers whose slots exist.  A launch that gave up
+// leaves spans of its rows unwritten, and the workspace may hold anything: nothing is added that
+// could leave 32 bits.
+__host__ __device__ inline bool span_ok(int first, int count, int workers) {
+  return first >= 0 && first < workers && count >= 1 && count <= workers - first;
+}
+
 // One launch works on one list, or on both lists of a call with shared prefixes (list 0: the
 // sequences, list 1: the groups) at once, each on its own part of the SMs.
 struct PagedArgs {

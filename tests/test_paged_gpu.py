@@ -418,6 +418,32 @@ def test_join_reads_nothing_out_of_range_after_a_launch_that_gave_up(d, monkeypa
         assert fa.fa_get_error() == fa.FA_OK and torch.equal(out, want)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_join_skips_spans_that_a_launch_that_gave_up_did_not_write(d, monkeypatch):
+    """Six or seven segments a CTA, whose pieces wait for one of four places from the fifth on: with a
+    limit of 1 us the launch gives up before it has written every span, and the join finds what the
+    workspace held there.  It skips such spans: their rows become those of a query without keys."""
+    B, nq = 1000, 40
+    cache = Cache([100] * B, 1, d, 64, seed=9)
+    args, q = cache.dev(), torch.randn(B * nq, 1, d, device=DEV).to(BF16)
+    kw = dict(cu_seqlens=i32(list(range(0, B * nq + 1, nq))), max_q=nq, max_kv=2000)
+    want, want_lse = fa.fa_fwd_paged(q, *args, **kw)
+    assert fa.fa_get_error() == fa.FA_OK and torch.isfinite(want_lse).all()
+    size = fa.fa_fwd_paged_workspace_size(B, B * nq, 1, 1, d)
+    for span in ([1, 0x7FFFFFFF], [0x7FFFFFFF, 2], [-5, 3], [0x7FFFFFFF, 0x7FFFFFFF], [151, 2]):
+        ws = i32(span).repeat(size // 8).view(torch.uint8)
+        out, lse = torch.full_like(want, 7.0), torch.full_like(want_lse, 7.0)
+        monkeypatch.setenv("FA_WAIT_TIMEOUT_US", "1")
+        fa.fa_fwd_paged(q, *args, **kw, workspace=ws, out=out, lse=lse)
+        assert fa.fa_get_error() == fa.FA_ERR_TIMEOUT
+        monkeypatch.delenv("FA_WAIT_TIMEOUT_US")
+        skipped = torch.isneginf(lse[0])
+        assert skipped.any() and not out[skipped].any()
+        again = fa.fa_fwd_paged(q, *args, **kw, workspace=ws, out=out, lse=lse)
+        assert fa.fa_get_error() == fa.FA_OK
+        assert torch.equal(again[0], want) and torch.equal(again[1], want_lse)
+
+
 @pytest.mark.parametrize("G", [1, 64], ids=["few rows", "many rows"])
 def test_paged_length_at_the_end_of_its_type(G):
     """kv_lens of 2^31 - 1 over pages that are all the same one: clamped to 2^31 - 256 keys and

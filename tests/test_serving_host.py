@@ -27,6 +27,15 @@ def lib():
     return fa.load_library()
 
 
+def test_plan_functions_on_the_host(tmp_path):
+    exe = tmp_path / "checks"
+    subprocess.run([build_lib._nvcc(), *build_lib.ARCH, "-O1", "-std=c++17", "-I", build_lib.CSRC,
+                    os.path.join(HERE, "csrc", "paged_plan_checks.cu"), "-o", str(exe)],
+                   check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
 def test_index_functions_on_the_host(tmp_path):
     exe = tmp_path / "checks"
     subprocess.run([build_lib._nvcc(), *build_lib.ARCH, "-O1", "-std=c++17", "-I", build_lib.CSRC,
