@@ -69,39 +69,54 @@ __host__ __device__ inline void token_bounds(const int32_t* cu, int b, int total
                                              int& n) {
   clamp_tokens(cu != nullptr ? cu[b] : b, cu != nullptr ? cu[b + 1] : b + 1, total, start, n);
 }
-// Sequence whose tokens include t: the last b with cu[b] <= t (empty sequences skipped), or -1
-// when t lies behind cu[B] or before cu[0].
-__host__ __device__ inline int token_sequence(const int32_t* cu, int B, int t) {
-  if (cu == nullptr) return t < B ? t : -1;
-  if (t < cu[0] || t >= cu[B]) return -1;
-  int lo = 0, hi = B;  // cu[lo] <= t < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= t) lo = mid;
-    else hi = mid;
+// Search for the last of the n offsets cu[lo], ..., that is <= t, by `lanes` lanes: lane i looks at
+// cu[lo + i * step()] (none past the n), offsets ascend, so the lanes that find one <= t are the
+// first `hits` ones.
+struct OffsetSearch {
+  int lo, n;
+  __host__ __device__ int step(int lanes) const { return (n + lanes - 1) / lanes; }
+  __host__ __device__ void narrow(int step, int hits) {
+    const int skip = (hits - 1) * step, left = n - skip;
+    n = step < left ? step : left;
+    lo += skip;
   }
-  return lo;
-}
+};
 
+// Sequence whose tokens include t: the last b with cu[b] <= t (empty sequences skipped), or -1
+// when t lies behind cu[B] or before cu[0] (cu == nullptr: one token per sequence).
 #ifdef __CUDACC__
-// token_sequence by a group of kLanes lanes (`mask`: its lanes of the warp), kLanes offsets a step.
+// By a group of kLanes lanes (`mask`: its lanes of the warp).
 template <int kLanes>
 __device__ __forceinline__ int token_sequence_group(const int32_t* cu, int B, int t, int sub,
                                                     unsigned mask) {
   if (cu == nullptr) return t < B ? t : -1;
-  int lo = 0, n = B + 1;  // the last of the n offsets from lo that is <= t
+  OffsetSearch s{0, B + 1};
   while (true) {
-    const int step = (n + kLanes - 1) / kLanes;
-    const bool le = sub * step < n && __ldg(cu + lo + sub * step) <= t;
-    const int hits = __popc(__ballot_sync(mask, le) & mask);  // offsets ascend: a prefix of lanes
+    const int step = s.step(kLanes);
+    const bool le = sub * step < s.n && __ldg(cu + s.lo + sub * step) <= t;
+    const int hits = __popc(__ballot_sync(mask, le) & mask);
     if (hits == 0) return -1;  // before cu[0]
-    n = min(step, n - (hits - 1) * step);
-    lo += (hits - 1) * step;
+    s.narrow(step, hits);
     if (step == 1) break;
   }
-  return lo < B ? lo : -1;  // behind cu[B]
+  return s.lo < B ? s.lo : -1;  // behind cu[B]
 }
 #endif
+// The same search on the host, lane by lane (checked against every answer in the tests).
+template <int kLanes = 8>
+inline int token_sequence(const int32_t* cu, int B, int t) {
+  if (cu == nullptr) return t < B ? t : -1;
+  OffsetSearch s{0, B + 1};
+  while (true) {
+    const int step = s.step(kLanes);
+    int hits = 0;
+    for (int sub = 0; sub < kLanes; ++sub) hits += sub * step < s.n && cu[s.lo + sub * step] <= t;
+    if (hits == 0) return -1;
+    s.narrow(step, hits);
+    if (step == 1) break;
+  }
+  return s.lo < B ? s.lo : -1;
+}
 
 // ---- norm + rotation pass (fa_rope.cu)
 struct RowView {

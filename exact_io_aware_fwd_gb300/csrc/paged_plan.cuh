@@ -28,6 +28,16 @@ __device__ __forceinline__ void touch(const PagedArgs& a) {
                "l"(a.rowbuf[0]), "l"(a.status));
 }
 
+// (The functions that say how work is cut are compiled for the host as well, where they are tested:
+// every key tile of every segment is some worker's, once.)
+__host__ __device__ __forceinline__ int device_load(const int32_t* p) {
+#ifdef __CUDA_ARCH__
+  return __ldg(p);
+#else
+  return *p;
+#endif
+}
+
 struct Entry {
   int start, n, nc;  // first token, new tokens, and how many of them are computed
   int len;           // keys (clamped)
@@ -36,32 +46,32 @@ struct Entry {
 };
 
 // Keys that row `row` (new token x group member) of an entry sees.
-__device__ __forceinline__ int row_limit(const Entry& e, int causal, int G, int row) {
+__host__ __device__ __forceinline__ int row_limit(const Entry& e, int causal, int G, int row) {
   return causal ? min(e.len, e.len - e.n + row / G + 1) : e.len;
 }
 // Key tiles of row tile r (at least one, so that a tile without keys is visited and written).
 template <int R, int KT>
-__device__ __forceinline__ int tiles_of(const Entry& e, int causal, int G, int r) {
+__host__ __device__ __forceinline__ int tiles_of(const Entry& e, int causal, int G, int r) {
   const int last = min(e.nc * G, (r + 1) * R) - 1;
   return max(1, (row_limit(e, causal, G, last) + KT - 1) / KT);
 }
 
 template <int R, int KT>
-__device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b,
-                                            bool report) {
+__host__ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b,
+                                                   bool report) {
   Entry e;
-  const int len = __ldg(l.lens + b);  // ahead of the branches: one wait for all of the loads
+  const int len = device_load(l.lens + b);  // ahead of the branches: one wait for all of the loads
   bool ok;
   if (l.group_cu != nullptr) {
-    const int g0 = __ldg(l.group_cu + b), g1 = __ldg(l.group_cu + b + 1);
+    const int g0 = device_load(l.group_cu + b), g1 = device_load(l.group_cu + b + 1);
     const int s0 = min(max(g0, 0), a.B), s1 = min(max(g1, s0), a.B);
-    const int t0 = a.cu != nullptr ? __ldg(a.cu + s0) : s0;
-    const int t1 = a.cu != nullptr ? __ldg(a.cu + s1) : s1;
+    const int t0 = a.cu != nullptr ? device_load(a.cu + s0) : s0;
+    const int t1 = a.cu != nullptr ? device_load(a.cu + s1) : s1;
     ok = (g0 >= 0) & (g0 <= g1) & (g1 <= a.B);
     clamp_tokens(t0, t1, a.total, e.start, e.n);
   } else {
-    const int t0 = a.cu != nullptr ? __ldg(a.cu + b) : b;
-    const int t1 = a.cu != nullptr ? __ldg(a.cu + b + 1) : b + 1;
+    const int t0 = a.cu != nullptr ? device_load(a.cu + b) : b;
+    const int t1 = a.cu != nullptr ? device_load(a.cu + b + 1) : b + 1;
     ok = (t0 >= 0) & (t0 <= t1) & (t1 <= a.total);
     clamp_tokens(t0, t1, a.total, e.start, e.n);
   }
@@ -69,7 +79,9 @@ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, 
   const int cap = pages < l.max_len ? static_cast<int>(pages) : l.max_len;
   e.len = min(max(len, 0), cap);
   e.nc = min(e.n, l.max_q);
+#ifdef __CUDA_ARCH__
   if (report && (!ok || e.len != len || e.nc != e.n)) atomicCAS(a.status, 0, kErrIndex);
+#endif
   e.rt = (e.nc * a.G + R - 1) / R;
   if (l.causal && e.n > 1) {
     e.tiles = 0;
@@ -256,7 +268,7 @@ struct Walk {
   bool direct;
   Entry e;
 
-  __device__ Walk(const PagedArgs& a, const KeyList& l, const Share& sh)
+  __host__ __device__ Walk(const PagedArgs& a, const KeyList& l, const Share& sh)
       : u0(sh.u0), u1(sh.b < 0 ? sh.u0 : sh.u1), b(sh.b), hk(0), r(0), te(-1), direct(sh.direct),
         e(sh.e) {
     if (u0 >= u1) return;
@@ -270,7 +282,7 @@ struct Walk {
     for (int n; rem >= (n = tiles_of<R, KT>(e, l.causal, a.G, r)); ++r) rem -= n;
     te = rem + 1;
   }
-  __device__ bool next(const PagedArgs& a, const KeyList& l, Piece& p) {
+  __host__ __device__ bool next(const PagedArgs& a, const KeyList& l, Piece& p) {
     if (u0 >= u1) return false;
     if (r < 0) {
       if (--hk < 0) {
@@ -304,7 +316,7 @@ struct Walk {
 };
 
 // (first worker, number of workers) of the segment that this worker begins.
-__device__ __forceinline__ int2 span_of(const Share& sh, const Piece& p) {
+__host__ __device__ __forceinline__ int2 span_of(const Share& sh, const Piece& p) {
   const int last = p.whole ? sh.worker : share_owner(sh.W, sh.C, p.unit + p.tiles - 1);
   return make_int2(sh.worker, last - sh.worker + 1);
 }
