@@ -16,8 +16,10 @@
 //    segment that several CTAs share leaves float32 parts for the join kernel.
 // A call with shared prefixes runs as one launch: the SMs are divided between the groups' prefixes
 // and the sequences' own keys by what their key tiles cost (paged_plan.cuh, kLists == 2).
-// Bound by the tensor pipe when both query tiles are full (512 flops per K, V byte at 256 rows);
-// with one tile of few rows by the copies from memory.
+// A K or V element takes part in one multiply-add a row: 256 flops a byte at 256 rows, next to the
+// balance of the measured peaks (280).  So one row tile is bound by the copies from memory, several
+// row tiles a head, which share K and V in L2 (the chunk case reads each key once from memory), by
+// the MMAs next to the softmax.
 #include "fa_internal.h"
 #include "fa_paged.h"
 #include "paged_plan.cuh"

@@ -172,8 +172,8 @@ bool whole_with_prefix(long long segments, int d, long long max_keys) {
   return (turns == 2 && max_keys <= 640) || (turns == 3 && max_keys <= 512);
 }
 
-// Groups of 8 lanes per row of the join.  A group reads its parts two at a time, so few rows, which
-// have many parts, take more groups: 128 rows of 39 parts 292 us with 16, 306 with 1 (4 x 131072
+// Groups of 8 lanes per row of the join.  A group reads its parts two at a time (four where
+// several share a row), so few rows, which have many parts, take more groups: 128 rows of 39 parts 292 us with 16, 306 with 1 (4 x 131072
 // keys); 1472 rows of 19 parts 36 with 4, 41 with 1, 40 with 16; 4096 rows of 6 parts 135 with 1,
 // 141 with 4, 160 with 16.
 int join_split(long long rows) {
@@ -181,8 +181,9 @@ int join_split(long long rows) {
 }
 
 // Workspace of a paged call: the spans and slots of each list, then (joined lists) row buffers.
-// Which kernel a list takes is decided by max_q; with few rows in all it cannot be the
-// tensor-core one.
+// Which kernel a list takes is decided by the query rows of an entry (of the sequences by max_q, of
+// the groups by their average) and by the rules for whole segments above; with few rows in all it
+// cannot be the tensor-core one, whose slots are larger.
 struct PagedWorkspace {
   size_t spans[2], slots[2], rowbuf[2], total;
 };

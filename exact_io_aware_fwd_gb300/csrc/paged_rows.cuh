@@ -9,8 +9,9 @@
 // its part of one straight from registers.  No barrier after the start: warps never wait for each
 // other, and a warp's ring goes on with the next piece while the last one is written.  (With 8
 // warps on one segment and a merge in shared memory at each piece's end, 1024 segments of about
-// 512 keys took 81 us instead of the copies' 40.)  mma.sync is enough here: 16 rows x 4 flops per
-// element and 2 bytes is 32 flops a byte, a few percent of the tensor pipe at full bandwidth.
+// 512 keys took 81 us instead of the copies' 40.)  mma.sync is enough here: one multiply-add a
+// row for each 2-byte element is 16 flops a byte at 16 rows, 16 to 18% of the tensor pipe at the
+// memory's rate (measured).
 #pragma once
 
 #include <type_traits>

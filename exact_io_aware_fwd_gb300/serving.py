@@ -209,8 +209,9 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, max
     """O [total, H, d] and LSE [H, total] of packed queries over the paged cache (see
     include/fa.h).  cu_seqlens: offsets of each sequence's query tokens, default one per
     sequence; causal aligns them to the end of the sequence.  max_q and max_kv bound the query
-    tokens and keys of a sequence (defaults: total, and the block table's reach); close bounds
-    let the launch fit the work."""
+    tokens and keys of a sequence (defaults: total, or 1 without cu_seqlens, and the block table's
+    reach).  They choose the kernel and how keys are split, so a loose bound costs time: single
+    tokens passed with cu_seqlens and no max_q are taken for chunks."""
     ext = _ext or _binding()
     if stream is None:
         return ext.fwd_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q, max_kv,
