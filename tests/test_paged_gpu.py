@@ -135,6 +135,63 @@ def test_paged_chunks(nq, lens, heads):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_paged_batches_that_mix_single_tokens_and_a_chunk(d):
+    rng = np.random.default_rng(1)
+    for chunk in (512, 2048):
+        nq, lens = [1] * 63, rng.integers(1, 1500, 64).tolist()
+        nq.insert(20, chunk)
+        lens[20] = chunk + 300
+        run_paged(nq, lens, 8, 2, d, 64, True, seed=7)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_long_chunks(d):
+    run_paged([3000], [5000], 4, 2, d, 64, True, seed=5)
+    run_paged([4096, 1], [4096, 3000], 2, 1, d, 16, True, seed=6)
+
+
+@pytest.mark.parametrize("max_kv", [400, 2000], ids=["whole", "tiles"])
+@pytest.mark.parametrize("heads", [(1, 1, 64, 16), (4, 1, 128, 64), (4, 2, 128, 32)],
+                         ids=lambda h: "H%dkv%dd%dpage%d" % h)
+def test_paged_chunks_longer_than_their_keys(heads, max_kv):
+    """Hundreds of tokens that see no key: a first query tile without keys next to a second with some."""
+    for causal in (True, False):
+        run_paged([300, 5, 700], [50, 400, 300], *heads, causal, seed=3, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,n,max_kv", [(3, 900, 2000), (3, 900, 900), (3, 9000, 9000), (40, 900, 2000), (300, 3000, 3000)],
+                         ids=["few rows", "whole", "long", "one tile", "many rows"])
+def test_paged_hidden_key_that_is_not_finite(nq, n, max_kv, d):
+    """The last key is hidden from all tokens but the last: whatever it holds, their bits stay."""
+    cache = Cache([n], 1, d, 16, seed=4)
+    k, v, table, lens = cache.dev()
+    q = torch.randn(nq, 2, d, device=DEV).to(BF16)
+    kw = dict(cu_seqlens=i32([0, nq]), max_q=nq, max_kv=max_kv, causal=True)
+    want = fa.fa_fwd_paged(q, k, v, table, lens, **kw)
+    page = int(cache.table[0, (n - 1) // 16])
+    for value in (float("inf"), float("-inf"), float("nan")):
+        k[page, :, (n - 1) % 16] = value
+        got = fa.fa_fwd_paged(q, k, v, table, lens, **kw)
+        assert torch.equal(got[0][:-1], want[0][:-1]) and torch.equal(got[1][:, :-1], want[1][:, :-1])
+    assert torch.isnan(got[0][-1]).all()
+    assert fa.fa_get_error() == fa.FA_OK
+
+
+def test_paged_without_pages():
+    """Block tables of no columns: no keys, zeros and -inf."""
+    k = torch.zeros(2, 1, 16, 64, dtype=BF16, device=DEV)
+    table, none = torch.empty(3, 0, dtype=torch.int32, device=DEV), i32([0, 0, 0])
+    q = torch.randn(3, 4, 64, device=DEV).to(BF16)
+    many = torch.randn(120, 4, 64, device=DEV).to(BF16)
+    for out, lse in (fa.fa_fwd_paged(q, k, k, table, none),
+                     fa.fa_fwd_shared_prefix(q, k, k, table, none, table[:1].contiguous(), none[:1].contiguous(), i32([0, 3])),
+                     fa.fa_fwd_paged(many, k, k, table, none, cu_seqlens=i32([0, 40, 80, 120]), max_kv=3000)):
+        assert not out.any() and torch.isneginf(lse).all()
+    assert fa.fa_get_error() == fa.FA_OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal", [False, True], ids=["all", "causal"])
 def test_paged_one_query_tile(causal, d):
     """17 to 128 rows a key/value head (both tile slots on one query tile): no, one, two, three, many

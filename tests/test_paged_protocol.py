@@ -31,6 +31,21 @@ def test_single_pieces(twin, S):
             paged([n], S, seed, twin)
 
 
+@pytest.mark.parametrize("S", [2, 4])
+def test_first_query_tile_without_keys(S):
+    """Rows of the first tile that see none of a piece's keys, next to a second tile that does."""
+    rng = random.Random(9)
+    for n in range(7):
+        for seed in range(4):
+            paged([(0, n)], S, seed, False)
+    for k in range(60):
+        pieces = [(rng.randint(0, 4), rng.randint(0, 4)) for _ in range(rng.randint(1, 9))]
+        spins = paged(pieces, S, k, False).spins
+        for at in sorted(rng.sample(range(1, max(2, spins + 1)), min(3, spins))):
+            sim = paged(pieces, S, k, False, abort_at=at)
+            assert sim.abort and sim.exit_ops == 0 and sim.exit_copies == 0
+
+
 @SHAPES
 def test_pieces_in_a_row(twin, S):
     rng = random.Random(3)

@@ -178,6 +178,22 @@ def test_norms_of_very_small_and_large_rows(d, inter, scale):
         assert np.all(np.abs(f64(dwg) - dw) <= 7.6e-6 * size + 1e-30)
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_in_place(d, inter, norm):
+    T, H, Hkv = 1000, 6, 2
+    dz = [torch.randn(T, h, d, device=DEV).to(torch.bfloat16) for h in (H, Hkv, Hkv)]
+    x, wq, wk = make(T, H, Hkv, d, 13, norm)
+    q, k, _ = x.split([H, Hkv, Hkv], dim=-2)
+    opts = dict(table=fa.fa_rope_table(T, d), interleaved=inter, q_weight=wq, k_weight=wk)
+    want = fa.fa_qk_norm_rope_bwd(*dz, q, k, **opts)
+    got = fa.fa_qk_norm_rope_bwd(*dz, q, k, **opts, dq_in=dz[0], dk_in=dz[1], dv_in=dz[2])
+    assert all(a is b for a, b in zip(got, dz))
+    assert all(a is None or torch.equal(a, b) for a, b in zip(got, want))
+    assert fa.fa_get_error() == fa.FA_OK
+
+
 def test_table_far_positions_and_amplitude():
     """cos and sin of positions up to 10^6 to half a float32 step of a value of at most 1.2 (the
     angle is a float64 product, off by 2^-53 x 10^6), with yarn's amplitude."""
