@@ -41,14 +41,23 @@ from .binding import (  # noqa: F401
 )
 from .serving import (  # noqa: F401
     fa_fwd_paged,
+    fa_fwd_paged_selected,
+    fa_fwd_paged_selected_workspace_size,
+    fa_fwd_paged_tree,
     fa_fwd_paged_workspace_size,
     fa_fwd_shared_prefix,
     fa_fwd_shared_prefix_workspace_size,
     fa_kv_append,
+    fa_kv_evict,
+    fa_kv_weights,
+    fa_page_bounds,
     fa_qk_norm_rope_bwd,
     fa_qk_norm_rope_bwd_workspace_size,
     fa_qk_norm_rope_fwd,
     fa_rope_table,
+    fa_select_pages,
+    fa_select_pages_workspace_size,
+    fa_tree_mask,
     rope_frequencies,
 )
 from .build_lib import LIB_PATH, build  # noqa: F401

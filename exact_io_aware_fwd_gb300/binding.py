@@ -51,6 +51,15 @@ EXPORTED = [
     "fa_fwd_paged",
     "fa_fwd_shared_prefix_workspace_size",
     "fa_fwd_shared_prefix",
+    "fa_tree_mask",
+    "fa_fwd_paged_tree",
+    "fa_page_bounds",
+    "fa_select_pages_workspace_size",
+    "fa_select_pages",
+    "fa_fwd_paged_selected_workspace_size",
+    "fa_fwd_paged_selected",
+    "fa_kv_weights",
+    "fa_kv_evict",
     "fa_get_error",
     "fa_status_string",
 ]
@@ -131,6 +140,24 @@ def load_library(path: str | None = None):
     lib.fa_fwd_shared_prefix.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp,
                                          sz, vp]
     lib.fa_fwd_shared_prefix.restype = i
+    lib.fa_tree_mask.argtypes = [vp, vp, i, i, i, vp, vp]
+    lib.fa_tree_mask.restype = i
+    lib.fa_fwd_paged_tree.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i, f, vp, sz, vp]
+    lib.fa_fwd_paged_tree.restype = i
+    lib.fa_page_bounds.argtypes = [vp, vp, vp, i, i, i, i, vp]
+    lib.fa_page_bounds.restype = i
+    lib.fa_select_pages_workspace_size.argtypes = [i] * 5
+    lib.fa_select_pages_workspace_size.restype = sz
+    lib.fa_select_pages.argtypes = [vp, vp, vp, vp, i, i, i, vp, i, i, i, i, i, i, vp, sz, vp]
+    lib.fa_select_pages.restype = i
+    lib.fa_fwd_paged_selected_workspace_size.argtypes = [i] * 4
+    lib.fa_fwd_paged_selected_workspace_size.restype = sz
+    lib.fa_fwd_paged_selected.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, f, vp, sz, vp]
+    lib.fa_fwd_paged_selected.restype = i
+    lib.fa_kv_weights.argtypes = [vp] * 5 + [i, vp, i, i, i, i, i, i, i, i, f, vp]
+    lib.fa_kv_weights.restype = i
+    lib.fa_kv_evict.argtypes = [vp, i, vp, vp, i, i, i, vp, vp, vp, i, i, i, i, vp]
+    lib.fa_kv_evict.restype = i
     lib.fa_get_error.argtypes = [vp]
     lib.fa_get_error.restype = i
     lib.fa_status_string.argtypes = [i]

@@ -33,10 +33,13 @@ def binding_path(torch_version: str, suffix: str) -> str:
 BINDING_PATH = binding_path(torch.__version__, sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_block_sparse.cu", "fa_noalloc.cu",
-           "fa_serving.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_mma.cu"]
+           "fa_serving.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_mma.cu", "fa_cache.cu", "fa_pages.cu",
+           "fa_evict.cu"]
 HEADERS = [os.path.join(CSRC, "sm103.cuh"), os.path.join(CSRC, "fa_internal.h"),
            os.path.join(CSRC, "fa_host.h"), os.path.join(CSRC, "fa_paged.h"),
            os.path.join(CSRC, "paged_plan.cuh"), os.path.join(CSRC, "paged_rows.cuh"),
+           os.path.join(CSRC, "fa_cache.h"), os.path.join(CSRC, "select_kth.cuh"),
+           os.path.join(CSRC, "serving_checks.h"),
            os.path.join(ROOT, "include", "fa.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

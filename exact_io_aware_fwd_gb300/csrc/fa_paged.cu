@@ -13,12 +13,13 @@ constexpr int kWarps = kPagedWarps, kThreads = 32 * kWarps;
 constexpr float kLn2 = 0.693147180559945309f;
 
 // With two lists the CTAs are divided between them.
-template <int D, int kLists>
+template <int D, int kLists, KeyMode M>
 __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ PagedArgs a) {
   using rows16::KT;
   using rows16::R;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Share shares[kWarps];
+  __shared__ int at[M == kSelectedKeys ? kWarps : 1][rows16::PagedLayout<D>::kStages];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   touch(a);
   begin_launch();
@@ -38,24 +39,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         a, a.list[li], li ? t[1] : t[0], li ? mine[1] : mine[0], li ? cta : cta - n1,
         li ? n1 : static_cast<int>(gridDim.x) - n1, scan, shares);
   }
-  rows16::work<D>(a, a.list[li], a.part[li], a.rowbuf[li], shares[warp],
-                  smem_u32(smem) + warp * (rows16::PagedLayout<D>::kStages *
-                                           rows16::PagedLayout<D>::kStage),
-                  lane);
+  rows16::work<D, M>(a, a.list[li], a.part[li], a.rowbuf[li], shares[warp],
+                     smem_u32(smem) + warp * (rows16::PagedLayout<D>::kStages *
+                                              rows16::PagedLayout<D>::kStage),
+                     at[M == kSelectedKeys ? warp : 0], lane);
 }
 
 // Few segments, a CTA as the worker.  kPrefix: whole segments only, list 1 holds the prefixes.
-template <int D, bool kPrefix>
+template <int D, bool kPrefix, KeyMode M>
 __global__ void __launch_bounds__(kThreads, 1) paged_cta_kernel(const __grid_constant__ PagedArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Share shares[1];
+  __shared__ int at[M == kSelectedKeys ? kWarps : 1][rows16::PagedLayout<D>::kStages];
   touch(a);
   begin_launch();
   make_shares<rows16::R, rows16::KT, kThreads, 1>(a, shares);
   if (kPrefix && blockIdx.x == 0)  // what is out of range in the groups is reported here
     for (int g = threadIdx.x; g < a.list[1].count; g += kThreads)
       entry_of<rows16::R, rows16::KT>(a.list[1], a, g, true);
-  rows16::work_together<D, kPrefix>(a, a.list[0], a.part[0], shares[0], smem, threadIdx.x >> 5, threadIdx.x & 31);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  rows16::work_together<D, kPrefix, M>(a, a.list[0], a.part[0], shares[0], smem,
+                                       at[M == kSelectedKeys ? warp : 0], warp, lane);
 }
 
 // ---- join of the parts
@@ -85,6 +89,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
   // where the row's parts are: its span and row tile in each list (these inputs are the call's)
   int where[2] = {-1, -1}, rr[2] = {0, 0};
   bool skip = !inside || seq < 0;
+  if (a.seq_cu != nullptr && !skip)
+    skip = token_sequence_group<kLanes>(a.seq_cu, a.seqs, t, sub, mask) < 0;
   for (int li = 0; li < a.lists && !skip; ++li) {
     const KeyList& l = a.list[li];
     int b = seq, start, n;
@@ -219,23 +225,39 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const JoinArgs
         lsum == 0.f ? -INFINITY : (m + log2f(lsum)) * kLn2;
 }
 
-template <int D, int kLists>
+template <int D, int kLists, KeyMode M>
 cudaError_t launch_paged_d(const PagedArgs& a, int64_t max_units, cudaStream_t s) {
   constexpr uint32_t bytes = rows16::PagedLayout<D>::kBytes;
-  cudaError_t e = ensure_smem_limit<paged_kernel<D, kLists>>(bytes);
+  cudaError_t e = ensure_smem_limit<paged_kernel<D, kLists, M>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
-  return launch_chained(paged_kernel<D, kLists>, static_cast<unsigned>(ctas), kThreads, bytes, s, a);
+  return launch_chained(paged_kernel<D, kLists, M>, static_cast<unsigned>(ctas), kThreads, bytes, s, a);
+}
+template <int D>
+cudaError_t launch_paged_mode(KeyMode mode, const PagedArgs& a, int lists, int64_t max_units,
+                              cudaStream_t s) {
+  if (mode == kTreeKeys) return launch_paged_d<D, 1, kTreeKeys>(a, max_units, s);
+  if (mode == kSelectedKeys) return launch_paged_d<D, 1, kSelectedKeys>(a, max_units, s);
+  return lists == 2 ? launch_paged_d<D, 2, kAllKeys>(a, max_units, s)
+                    : launch_paged_d<D, 1, kAllKeys>(a, max_units, s);
 }
 
-template <int D, bool kPrefix>
+template <int D, bool kPrefix, KeyMode M>
 cudaError_t launch_cta_d(const PagedArgs& a, int64_t max_units, cudaStream_t s) {
   constexpr uint32_t bytes = rows16::PagedLayout<D>::kBytes;
-  cudaError_t e = ensure_smem_limit<paged_cta_kernel<D, kPrefix>>(bytes);
+  cudaError_t e = ensure_smem_limit<paged_cta_kernel<D, kPrefix, M>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
-  return launch_chained(paged_cta_kernel<D, kPrefix>, static_cast<unsigned>(ctas), kThreads, bytes,
+  return launch_chained(paged_cta_kernel<D, kPrefix, M>, static_cast<unsigned>(ctas), kThreads, bytes,
                         s, a);
+}
+template <int D>
+cudaError_t launch_cta_mode(KeyMode mode, const PagedArgs& a, int lists, int64_t max_units,
+                            cudaStream_t s) {
+  if (mode == kTreeKeys) return launch_cta_d<D, false, kTreeKeys>(a, max_units, s);
+  if (mode == kSelectedKeys) return launch_cta_d<D, false, kSelectedKeys>(a, max_units, s);
+  return lists == 2 ? launch_cta_d<D, true, kAllKeys>(a, max_units, s)
+                    : launch_cta_d<D, false, kAllKeys>(a, max_units, s);
 }
 
 template <int D>
@@ -249,20 +271,16 @@ cudaError_t launch_join_d(const JoinArgs& a, int split, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s) {
-  if (lists == 2)
-    return d == 64 ? launch_paged_d<64, 2>(a, max_units, s)
-                   : launch_paged_d<128, 2>(a, max_units, s);
-  return d == 64 ? launch_paged_d<64, 1>(a, max_units, s) : launch_paged_d<128, 1>(a, max_units, s);
+cudaError_t launch_paged(int d, KeyMode mode, const PagedArgs& a, int lists, int64_t max_units,
+                         cudaStream_t s) {
+  return d == 64 ? launch_paged_mode<64>(mode, a, lists, max_units, s)
+                 : launch_paged_mode<128>(mode, a, lists, max_units, s);
 }
 
-cudaError_t launch_paged_cta(int d, const PagedArgs& a, int lists, int64_t max_units,
+cudaError_t launch_paged_cta(int d, KeyMode mode, const PagedArgs& a, int lists, int64_t max_units,
                              cudaStream_t s) {
-  if (lists == 2)
-    return d == 64 ? launch_cta_d<64, true>(a, max_units, s)
-                   : launch_cta_d<128, true>(a, max_units, s);
-  return d == 64 ? launch_cta_d<64, false>(a, max_units, s)
-                 : launch_cta_d<128, false>(a, max_units, s);
+  return d == 64 ? launch_cta_mode<64>(mode, a, lists, max_units, s)
+                 : launch_cta_mode<128>(mode, a, lists, max_units, s);
 }
 
 cudaError_t launch_paged_join(int d, const JoinArgs& a, int split, cudaStream_t s) {

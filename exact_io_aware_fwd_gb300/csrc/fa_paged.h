@@ -161,7 +161,7 @@ cudaError_t launch_rope_bwd(int d, bool interleaved, const RopeArgs& a, float* d
 // start + n) and len keys.
 struct KeyList {
   int count;                // entries
-  const int32_t* lens;      // [count]
+  const int32_t* lens;      // [count]; nullptr: entry b is token b alone, and each has max_len keys
   const int32_t* table;     // [count][max_pages]
   int max_pages, max_len, max_q;
   const int32_t* group_cu;  // groups: [count + 1] over sequences, or nullptr
@@ -189,6 +189,17 @@ __host__ __device__ inline int row_tile0(int start, int G, int R, int b) {
   return (start * G + R - 1) / R + b;  // never overlaps entry b - 1's tiles
 }
 
+#ifdef __CUDACC__
+// 32 positions of a tree's mask row from `at` on (it has `words` words; what lies before it is
+// context, which every new token sees).
+__device__ __forceinline__ uint32_t tree_window(const uint32_t* row, int words, int at) {
+  const int i = at >> 5;
+  const uint32_t lo = i < 0 ? ~0u : (i < words ? __ldg(row + i) : 0u);
+  const uint32_t hi = i + 1 < 0 ? ~0u : (i + 1 < words ? __ldg(row + i + 1) : 0u);
+  return __funnelshift_r(lo, hi, at & 31);
+}
+#endif
+
 // Whether a span read from the workspace names workers whose slots exist.  A launch that gave up
 // leaves spans of its rows unwritten, and the workspace may hold anything: nothing is added that
 // could leave 32 bits.
@@ -211,7 +222,19 @@ struct PagedArgs {
   float mma_cost;    // a key tile of the tensor-core kernel in key tiles of the other one
   float* rowbuf[2];  // joined lists: [total * H] rows of O, then m, then l; else nullptr
   int* status;
+  // a tree of new tokens: which of its sequence's new tokens each one sees, [total][tree_words]
+  const uint32_t* tree;
+  int tree_words;
+  // selected pages: [total][Hkv][top]; the sequences of the tokens (list 0 has an entry a token)
+  const int32_t* pages;
+  int top;
+  const int32_t *seq_cu, *seq_lens;
+  int seqs;
 };
+
+// What a row sees of its entry's keys: all or the causal ones, the context and a tree's ancestors,
+// or those of the pages selected for it.
+enum KeyMode { kAllKeys, kTreeKeys, kSelectedKeys };
 
 struct JoinArgs {
   __nv_bfloat16* o;
@@ -222,6 +245,8 @@ struct JoinArgs {
   PartialLayout part[2];
   const float* rowbuf[2];
   int lists;
+  const int32_t* seq_cu;  // selected pages: tokens behind seq_cu[seqs] have no result
+  int seqs;
 };
 
 constexpr int kPagedRows = 16;           // rows of a tile
@@ -231,13 +256,15 @@ constexpr int kPagedKeys = 16;           // keys of a tile
 constexpr int kPagedMmaRows = 256;       // the tensor-core kernel, whose CTAs are the workers
 constexpr int kPagedMmaKeys = 128;
 
-cudaError_t launch_paged(int d, const PagedArgs& a, int lists, int64_t max_units, cudaStream_t s);
+// mode other than kAllKeys: one list
+cudaError_t launch_paged(int d, KeyMode mode, const PagedArgs& a, int lists, int64_t max_units,
+                         cudaStream_t s);
 // Few segments: list 0, with its prefixes (lists == 2: segments are then not split).  max_units: as
 // many CTAs as have work.
-cudaError_t launch_paged_cta(int d, const PagedArgs& a, int lists, int64_t max_units,
+cudaError_t launch_paged_cta(int d, KeyMode mode, const PagedArgs& a, int lists, int64_t max_units,
                              cudaStream_t s);
-// twin: one list, and no entry has more than 128 rows
-cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+// twin: one list, and no entry has more than 128 rows; mode: not selected pages
+cudaError_t launch_paged_mma(int d, KeyMode mode, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedArgs& a, int lists, bool twin, int64_t max_units,
                              uint64_t timeout_ns, cudaStream_t s);
 // split: groups of 8 lanes that share a row (1, 4 or 16)

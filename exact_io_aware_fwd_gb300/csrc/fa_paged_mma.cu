@@ -93,7 +93,8 @@ __device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, in
 // P V of a position is all that runs (126 sequences of 18 rows and 1576 keys 149 us, with one slot
 // 166; d = 64, 16 of 36 rows and 8192 keys 67 and 82).  Here K runs a position ahead of V: a V
 // stage is free only two positions later (211 us with K and V together).
-template <int D, int kLists, bool kTwin>
+// M: kAllKeys, or kTreeKeys (one list).
+template <int D, int kLists, bool kTwin, KeyMode M>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedArgs a,
@@ -402,10 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int twins = 0;           // twin pieces before this one
     bool ok = true;
     if (few_rows)
-      rows16::work<D>(a, l, part, rowbuf, shares[kLists == 2 ? warp - 4 : 0],
-                      smem_u32(sm) + (warp - 4) * (rows16::PagedLayout<D>::kStages *
-                                                   rows16::PagedLayout<D>::kStage),
-                      lane);
+      rows16::work<D, kAllKeys>(a, l, part, rowbuf, shares[kLists == 2 ? warp - 4 : 0],
+                                smem_u32(sm) + (warp - 4) * (rows16::PagedLayout<D>::kStages *
+                                                             rows16::PagedLayout<D>::kStage),
+                                nullptr, lane);
     for (int i = 0; !few_rows; ++i) {
       if (!(ok = mbar_wait_warp(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
       const PieceInfo& piece = pieces[i % kRing];  // held until the piece is done
@@ -451,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys below lim are visible to this row, and below lim_min to every row of the tile
       const int len = piece.len, ta = piece.ta;
       const int lim = l.causal && r0 + row < rows ? min(len, piece.shift + (r0 + row) / a.G + 1) : len;
-      const int lim_min = l.causal ? min(len, piece.shift + r0 / a.G + 1) : len;
+      const int lim_min = M == kTreeKeys ? piece.shift
+                                         : (l.causal ? min(len, piece.shift + r0 / a.G + 1) : len);
       // position whose last page ends inside it: that page's rows past the end are cleared
       const int tail = len & ((1 << a.page_shift) - 1), j_tail = tail != 0 ? len / KT - ta : -1;
       float m_run = -INFINITY, l_run = 0.f;
@@ -470,9 +472,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // hidden keys get a score of -inf in place, so that what follows is the same code for
         // every tile: it has to stay in the instruction cache next to the MMA issuer's loop
         if (k0 + KT > lim_min) {
+          if constexpr (M == kTreeKeys) {
+            const int tok = r0 + row < rows ? (r0 + row) / a.G : 0;
+            const uint32_t* bits = a.tree + static_cast<int64_t>(piece.start + tok) * a.tree_words;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (k0 + c >= lim) s[c] = 0xff800000u;
+            for (int x = 0; x < 4; ++x) {
+              const int left = len - k0 - 32 * x;  // keys of these 32 that there are
+              uint32_t see = tree_window(bits, a.tree_words, k0 + 32 * x - lim_min);
+              if (left < 32) see &= (1u << max(left, 0)) - 1u;
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!((see >> c) & 1u)) s[32 * x + c] = 0xff800000u;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (k0 + c >= lim) s[c] = 0xff800000u;
+          }
         }
         float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -654,32 +670,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, int kLists, bool kTwin>
+template <int D, int kLists, bool kTwin, KeyMode M>
 cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
                      int64_t max_units, uint64_t timeout_ns, cudaStream_t s) {
   const uint32_t smem = smem_of<D, kLists>();  // the kernel's array is aligned as declared
-  cudaError_t e = ensure_smem_limit<paged_mma_kernel<D, kLists, kTwin>>(smem);
+  cudaError_t e = ensure_smem_limit<paged_mma_kernel<D, kLists, kTwin, M>>(smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = max_units < kPagedCtas ? max_units : kPagedCtas;
-  return launch_chained(paged_mma_kernel<D, kLists, kTwin>, static_cast<unsigned>(ctas), kThreads,
+  return launch_chained(paged_mma_kernel<D, kLists, kTwin, M>, static_cast<unsigned>(ctas), kThreads,
                         smem, s, tk, tv, a, timeout_ns, smem);
 }
 template <int D>
-cudaError_t launch_kind(const CUtensorMap& tk, const CUtensorMap& tv, const PagedArgs& a,
-                        int lists, bool twin, int64_t max_units, uint64_t timeout_ns,
-                        cudaStream_t s) {
-  if (lists == 2) return launch_d<D, 2, false>(tk, tv, a, max_units, timeout_ns, s);
-  return twin ? launch_d<D, 1, true>(tk, tv, a, max_units, timeout_ns, s)
-              : launch_d<D, 1, false>(tk, tv, a, max_units, timeout_ns, s);
+cudaError_t launch_kind(KeyMode mode, const CUtensorMap& tk, const CUtensorMap& tv,
+                        const PagedArgs& a, int lists, bool twin, int64_t max_units,
+                        uint64_t timeout_ns, cudaStream_t s) {
+  if (mode == kTreeKeys)
+    return twin ? launch_d<D, 1, true, kTreeKeys>(tk, tv, a, max_units, timeout_ns, s)
+                : launch_d<D, 1, false, kTreeKeys>(tk, tv, a, max_units, timeout_ns, s);
+  if (lists == 2) return launch_d<D, 2, false, kAllKeys>(tk, tv, a, max_units, timeout_ns, s);
+  return twin ? launch_d<D, 1, true, kAllKeys>(tk, tv, a, max_units, timeout_ns, s)
+              : launch_d<D, 1, false, kAllKeys>(tk, tv, a, max_units, timeout_ns, s);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_mma(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_paged_mma(int d, KeyMode mode, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedArgs& a, int lists, bool twin, int64_t max_units,
                              uint64_t timeout_ns, cudaStream_t s) {
-  return d == 64 ? launch_kind<64>(tk, tv, a, lists, twin, max_units, timeout_ns, s)
-                 : launch_kind<128>(tk, tv, a, lists, twin, max_units, timeout_ns, s);
+  return d == 64 ? launch_kind<64>(mode, tk, tv, a, lists, twin, max_units, timeout_ns, s)
+                 : launch_kind<128>(mode, tk, tv, a, lists, twin, max_units, timeout_ns, s);
 }
 
 }  // namespace fa

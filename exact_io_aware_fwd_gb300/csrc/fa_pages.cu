@@ -1,0 +1,545 @@
+// Bounds of the cache's pages, and the pages that a query attends to.
+//
+// A page of keys lies in the box lo_e <= k_e <= hi_e (element by element), so
+//   score(q, page) = sum_e max(q_e, 0) hi_e + min(q_e, 0) lo_e
+// is at least q.k for every key of the page: the cheapest score that no key of the page can beat.
+// It costs two rows a page instead of page_size of them.  The page's score for a key/value head is
+// the largest over its group's queries, because the group reads one list of pages.
+#include "fa_cache.h"
+#include "fa_internal.h"
+#include "paged_rows.cuh"
+#include "select_kth.cuh"
+#include "sm103.cuh"
+
+namespace fa {
+
+namespace {
+
+__device__ __forceinline__ __nv_bfloat162 pair2(uint32_t u) {
+  return *reinterpret_cast<__nv_bfloat162*>(&u);
+}
+__device__ __forceinline__ uint32_t bits2(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  return bits2(__hmin2_nan(pair2(a), pair2(b)));
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  return bits2(__hmax2_nan(pair2(a), pair2(b)));
+}
+
+// ---- the mask of a tree: a thread follows its token's parents, whose indices descend, and writes
+// the words of its row from the last to the first.
+constexpr int kTreeThreads = 128;
+
+__global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const int32_t* parents, const int32_t* cu,
+                                                                 int B, int total, int words,
+                                                                 uint64_t* mask, int* status) {
+  begin_launch();
+  const int64_t t64 = static_cast<int64_t>(blockIdx.x) * kTreeThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  // the sequence of the warp's first token, then on from there
+  const int t0 = static_cast<int>(min(t64 - lane, static_cast<int64_t>(total) - 1));
+  int b = token_sequence_group<32>(cu, B, t0, lane, ~0u);
+  if (t64 >= total) return;
+  const int t = static_cast<int>(t64);
+  if (cu == nullptr) b = t < B ? t : -1;
+  else if (b < 0 && t0 < __ldg(cu)) b = 0;  // tokens before the first sequence
+  if (b < 0) return;                        // behind the last sequence
+  int start = 0, n = 0;
+  for (; b < B; ++b) {
+    token_bounds(cu, b, total, start, n);
+    if (t < start + n) break;
+  }
+  if (b == B || t < start) return;
+  int i = t - start;
+  if (i >= 64LL * words) atomicCAS(status, 0, kErrIndex);  // has no bit
+  uint64_t* row = mask + static_cast<int64_t>(t) * words;
+  uint64_t bits = 0;
+  int w = words - 1;
+  while (i >= 0) {
+    if (i < 64LL * words) {
+      for (; w > i >> 6; --w) {
+        row[w] = bits;
+        bits = 0;
+      }
+      bits |= 1ull << (i & 63);
+    }
+    const int p = __ldg(parents + start + i);
+    if (p < -1 || p >= i) {
+      atomicCAS(status, 0, kErrIndex);
+      break;
+    }
+    i = p;
+  }
+  for (; w >= 0; --w) {
+    row[w] = bits;
+    bits = 0;
+  }
+}
+
+// ---- bounds
+// Pages that hold one of the last n keys of a sequence are at most n / page_size + 2, so slot
+// cu[b] / page_size + 2 b + i stands for the i-th of sequence b: disjoint, whatever the lengths.
+__host__ __device__ __forceinline__ int first_slot(const int32_t* cu, int b, int total, int shift) {
+#ifdef __CUDA_ARCH__
+  const int at = cu != nullptr ? __ldg(cu + b) : b;
+#else
+  const int at = cu != nullptr ? cu[b] : b;
+#endif
+  return (min(max(at, 0), total) >> shift) + 2 * b;
+}
+
+constexpr int kBoundThreads = 128;
+
+// One warp a page and head: D / 8 lanes a row, eight rows a lane on the way.  Bound by reading the
+// keys once.
+template <int D>
+__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const BoundsArgs a) {
+  constexpr int L = D / 8, kRows = 32 / L, kAhead = 8;
+  begin_launch();
+  const CacheSeqs& c = a.c;
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kBoundThreads / 32) + (threadIdx.x >> 5);
+  const int64_t slots = static_cast<int64_t>(c.total >> c.page_shift) + 2 * static_cast<int64_t>(c.B);
+  if (unit >= slots * c.Hkv) return;
+  const int slot = static_cast<int>(unit / c.Hkv), h = static_cast<int>(unit - static_cast<int64_t>(slot) * c.Hkv);
+  // the last sequence whose first slot is not behind this one
+  OffsetSearch s{0, c.B};
+  while (true) {
+    const int step = s.step(32), i = lane * step;
+    const bool le = i < s.n && first_slot(c.cu, s.lo + i, c.total, c.page_shift) <= slot;
+    const int hits = __popc(__ballot_sync(~0u, le));
+    if (hits == 0) return;  // offsets that do not ascend
+    s.narrow(step, hits);
+    if (step == 1) break;
+  }
+  const int b = s.lo;
+  int start, n;
+  token_bounds(c.cu, b, c.total, start, n);
+  const int i = slot - first_slot(c.cu, b, c.total, c.page_shift);
+  if (i >= (n >> c.page_shift) + 2) return;  // offsets that do not ascend
+  const int len = keys_of(c, b, lane == 0 && i == 0);
+  const int page = (max(len - n, 0) >> c.page_shift) + i;
+  const int left = len - (page << c.page_shift);  // keys from the page's first one on
+  if (n == 0 || left <= 0) return;
+  const int phys = page_of(c, b, page);
+  if (phys < 0) return;
+  const int rows = min(left, 1 << c.page_shift);
+  const int64_t at = static_cast<int64_t>(phys) * c.Hkv + h;
+  const uint4* src = reinterpret_cast<const uint4*>(a.k_cache + (at << c.page_shift) * D) + lane % L;
+  uint32_t lo[4], hi[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    lo[k] = 0x7f807f80u;
+    hi[k] = 0xff80ff80u;
+  }
+  for (int r0 = 0; r0 < rows; r0 += kRows * kAhead) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)  // past the end: the last row again
+      v[k] = src[min(r0 + k * kRows + lane / L, rows - 1) * L];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      lo[0] = min2(lo[0], v[k].x); hi[0] = max2(hi[0], v[k].x);
+      lo[1] = min2(lo[1], v[k].y); hi[1] = max2(hi[1], v[k].y);
+      lo[2] = min2(lo[2], v[k].z); hi[2] = max2(hi[2], v[k].z);
+      lo[3] = min2(lo[3], v[k].w); hi[3] = max2(hi[3], v[k].w);
+    }
+  }
+#pragma unroll
+  for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lo[k] = min2(lo[k], __shfl_xor_sync(~0u, lo[k], o));
+      hi[k] = max2(hi[k], __shfl_xor_sync(~0u, hi[k], o));
+    }
+  uint4* dst = reinterpret_cast<uint4*>(a.bounds + at * 2 * D) + lane % L;
+  if (lane < L) dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  else if (lane < 2 * L) dst[L] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+}
+
+// ---- scores
+// A warp takes 16 pages of one key/value head as the columns of an m16n8k16 product whose rows are
+// queries: [max(q, 0), min(q, 0)] times [hi, lo].  Each lane loads 16 bytes a time straight into
+// fragments: which element of a row is which k of the product does not matter as long as both sides
+// agree, so lane l % 4 takes eight neighbouring elements as k = 2c, 2c + 1, 2c + 8, 2c + 9 of two
+// products.
+constexpr int kScoreWarps = 4, kScorePages = 16;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectArgs a, int chunks) {
+  constexpr int J = D / 32;  // 16-byte pieces of a lane's part of a row
+  __shared__ float tile[kScoreWarps][16][kScorePages + 1];
+  begin_launch();
+  const CacheSeqs& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bh = static_cast<int>(blockIdx.x) / chunks, chunk = static_cast<int>(blockIdx.x) % chunks;
+  const int b = bh / c.Hkv, hk = bh - b * c.Hkv;
+  const int len = keys_of(c, b, threadIdx.x == 0 && chunk == 0 && hk == 0);
+  int start, n;
+  token_bounds(c.cu, b, c.total, start, n);
+  const int pages = (len + (1 << c.page_shift) - 1) >> c.page_shift;
+  const int p0 = (chunk * kScoreWarps + warp) * kScorePages;
+  if (p0 >= pages || n == 0) return;
+  uint4 lo[2][J], hi[2][J];
+  uint32_t most = 0;  // largest |bound|, as bits: NaN is above infinity
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int p = p0 + 8 * t + (lane >> 2);
+    const int phys = p < pages ? page_of(c, b, p) : -1;
+    const uint4* src = reinterpret_cast<const uint4*>(
+                           a.bounds + (static_cast<int64_t>(max(phys, 0)) * c.Hkv + hk) * 2 * D) + (lane & 3);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      lo[t][j] = hi[t][j] = make_uint4(0u, 0u, 0u, 0u);
+      if (phys >= 0) {
+        lo[t][j] = __ldg(src + 4 * j);
+        hi[t][j] = __ldg(src + D / 8 + 4 * j);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t u[8] = {lo[t][j].x, lo[t][j].y, lo[t][j].z, lo[t][j].w,
+                             hi[t][j].x, hi[t][j].y, hi[t][j].z, hi[t][j].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) most = __vmaxu2(most, u[k] & 0x7fff7fffu);
+    }
+  most = max(most & 0xffffu, most >> 16);
+  most = __reduce_max_sync(~0u, most);
+  if (lane == 0)
+    a.reach[static_cast<int64_t>(bh) * ((a.max_pages + kScorePages - 1) / kScorePages) + p0 / kScorePages] =
+        __uint_as_float(most << 16);
+
+  // tokens of a row tile, or row tiles of a token
+  const int per = a.G <= 16 ? 16 / a.G : 1, tiles = a.G <= 16 ? 1 : (a.G + 15) / 16;
+  const int rows_per = a.G <= 16 ? a.G : 16;
+  float* mine = &tile[warp][0][0];
+  for (int i0 = 0; i0 < n; i0 += per) {
+    float best = -INFINITY;  // of token `lane / 16`, page lane % 16, where a token has several row tiles
+    for (int rt = 0; rt < tiles; ++rt) {
+      const uint4* q[2];
+      bool live[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = (lane >> 2) + 8 * i;
+        const int tok = i0 + rr / rows_per, g = rt * 16 + rr % rows_per;
+        live[i] = rr < per * rows_per && tok < n && g < a.G;
+        q[i] = reinterpret_cast<const uint4*>(
+                   a.q + ((static_cast<int64_t>(start + (live[i] ? tok : 0))) * a.H + hk * a.G +
+                          (live[i] ? g : 0)) * D) + (lane & 3);
+      }
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        uint4 v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = live[i] ? __ldg(q[i] + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t u[4] = {k ? v[0].z : v[0].x, k ? v[1].z : v[1].x, k ? v[0].w : v[0].y,
+                                 k ? v[1].w : v[1].y};
+          uint32_t up[4], dn[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            up[x] = max2(u[x], 0u);
+            dn[x] = min2(u[x], 0u);
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            rows16::mma16816(s[t], up, k ? hi[t][j].z : hi[t][j].x, k ? hi[t][j].w : hi[t][j].y);
+            rows16::mma16816(s[t], dn, k ? lo[t][j].z : lo[t][j].x, k ? lo[t][j].w : lo[t][j].y);
+          }
+        }
+      }
+      __syncwarp();  // the last tile has been read
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = (lane >> 2) + 8 * (k >> 1), col = 8 * t + (lane & 3) * 2 + (k & 1);
+          const float x = s[t][k];
+          // a score that is not a number counts as infinity; a row without a query as nothing
+          mine[row * (kScorePages + 1) + col] = live[k >> 1] ? (x == x ? x : INFINITY) : -INFINITY;
+        }
+      __syncwarp();
+      for (int o = lane; o < per * 16; o += 32) {
+        const int tt = o >> 4, col = o & 15;
+        float m = -INFINITY;
+        for (int r = 0; r < rows_per; ++r) m = fmaxf(m, mine[(tt * rows_per + r) * (kScorePages + 1) + col]);
+        if (tiles > 1) {
+          m = best = fmaxf(best, m);
+          if (rt + 1 < tiles) continue;
+        }
+        if (i0 + tt < n && p0 + col < pages)
+          a.score[(static_cast<int64_t>(start + i0 + tt) * c.Hkv + hk) * a.max_pages + p0 + col] = m;
+      }
+    }
+  }
+}
+
+// ---- selection
+// One CTA a token and key/value head.  A page is in or out by a comparison, so the choice is that of
+// exact scores: the float32 scores above are off by at most delta = 2^-15 sum_e |q_e| max |bound|
+// (16 products of 16 terms each, every addition off by at most 2^-23 of what has been added up so
+// far in magnitude).  With t the k-th largest of them, every page more than 2 delta above t is in and
+// every page more than 2 delta below it is out; the few between are scored again in 64 bits, where
+// the products of two bfloat16 are exact and their sums nearly always too.
+constexpr int kSelectThreads = 256;
+constexpr int kBorder = 512;  // pages next to the border that are ranked in shared memory
+
+template <int D>
+__device__ __forceinline__ double fine_score(const SelectArgs& a, int b, int hk, int t, int p, int lane) {
+  constexpr int E = D / 32;
+  const CacheSeqs& c = a.c;
+  const int phys = page_of(c, b, p);
+  const __nv_bfloat16* box = a.bounds + (static_cast<int64_t>(max(phys, 0)) * c.Hkv + hk) * 2 * D + lane * E;
+  double lo[E], hi[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    lo[e] = phys >= 0 ? static_cast<double>(__bfloat162float(box[e])) : 0.0;
+    hi[e] = phys >= 0 ? static_cast<double>(__bfloat162float(box[D + e])) : 0.0;
+  }
+  const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D + lane * E;
+  double best = -INFINITY;
+  for (int g = 0; g < a.G; ++g) {
+    double x = 0.0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const double v = static_cast<double>(__bfloat162float(q[g * D + e]));
+      x += (v < 0.0 ? 0.0 : v) * hi[e] + (v > 0.0 ? 0.0 : v) * lo[e];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    if (x != x) x = INFINITY;
+    best = x > best ? x : best;
+  }
+  return best;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const SelectArgs a) {
+  constexpr int kWarps = kSelectThreads / 32;
+  __shared__ union {
+    KthShared<kSelectThreads, uint32_t> k32;
+    KthShared<kSelectThreads, uint64_t> k64;
+    struct {
+      double value[kBorder];
+      int page[kBorder];
+    } border;
+  } sh;
+  __shared__ float red[2][kWarps];
+  __shared__ int counts[3][kWarps], border_count;
+  begin_launch();
+  const CacheSeqs& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t = blockIdx.x / c.Hkv, hk = blockIdx.x - t * c.Hkv;
+  const int b = token_sequence_group<32>(c.cu, c.B, t, lane, ~0u);
+  if (b < 0) return;  // behind the last sequence
+  int start, n;
+  token_bounds(c.cu, b, c.total, start, n);
+  if (t < start || t >= start + n) {  // offsets that do not ascend
+    if (tid == 0) atomicCAS(c.status, 0, kErrIndex);
+    return;
+  }
+  const int len = keys_of(c, b, false);
+  const int sees = min(max(len - n + (t - start) + 1, 0), len);
+  const int pages = (sees + (1 << c.page_shift) - 1) >> c.page_shift;
+  int32_t* out = a.pages + static_cast<int64_t>(blockIdx.x) * a.top;
+  if (pages <= a.top) {
+    for (int i = tid; i < a.top; i += kSelectThreads) out[i] = i < pages ? i : -1;
+    return;
+  }
+  for (int i = tid; i < a.first; i += kSelectThreads) out[i] = i;
+  for (int i = tid; i < a.last; i += kSelectThreads) out[a.top - a.last + i] = pages - a.last + i;
+  const int mid = pages - a.first - a.last, k = a.top - a.first - a.last;  // k of mid > k pages
+  if (k == 0) return;
+  float* score = a.score + static_cast<int64_t>(blockIdx.x) * a.max_pages + a.first;
+  double* fine = a.fine + static_cast<int64_t>(blockIdx.x) * a.max_pages + a.first;
+
+  // delta
+  const int groups = (a.max_pages + kScorePages - 1) / kScorePages;
+  const float* reach = a.reach + (static_cast<int64_t>(b) * c.Hkv + hk) * groups;
+  float far = 0.f, size = 0.f;
+  bool odd = false;  // something is not finite
+  for (int i = tid; i < (pages + kScorePages - 1) / kScorePages; i += kSelectThreads) {
+    far = fmaxf(far, reach[i]);
+    odd |= !(reach[i] < INFINITY);
+  }
+  const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D;
+  for (int g = warp; g < a.G; g += kWarps) {
+    float x = 0.f;
+    for (int e = lane; e < D; e += 32) x += fabsf(__bfloat162float(q[g * D + e]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    odd |= !(x < INFINITY);
+    size = fmaxf(size, x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) far = fmaxf(far, __shfl_xor_sync(~0u, far, o));
+  if (lane == 0) {
+    red[0][warp] = far;
+    red[1][warp] = size;
+  }
+  odd = __syncthreads_or(odd);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    far = fmaxf(far, red[0][w]);
+    size = fmaxf(size, red[1][w]);
+  }
+  const float delta = far * size * 0x1p-15f;
+  odd |= !(delta < INFINITY);
+
+  float above = 3.402823466e38f, below = -INFINITY;  // in, and at least in question
+  if (!odd) {
+    const Kth<uint32_t> kth = kth_largest<kSelectThreads, uint32_t>(
+        mid, k, 2, [&](int i, uint32_t& key) { key = ordered(score[i]); return true; }, sh.k32);
+    above = unordered(kth.base + kth.range) + 2.f * delta;
+    below = unordered(kth.base) - 2.f * delta;
+    __syncthreads();  // the bins are free
+  }
+  if (tid == 0) border_count = 0;
+  __syncthreads();
+  int sure = 0;
+  for (int i = tid; i < mid; i += kSelectThreads) {
+    const float x = score[i];
+    if (x > above && !odd) {
+      ++sure;
+    } else if (odd || x >= below) {
+      const int at = atomicAdd(&border_count, 1);
+      if (at < kBorder) sh.border.page[at] = i;
+    }
+  }
+  sure = __reduce_add_sync(~0u, sure);
+  if (lane == 0) counts[0][warp] = sure;
+  __syncthreads();
+  sure = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sure += counts[0][w];
+  const int border = border_count, need = k - sure;  // need <= border
+  if (need == border) {
+    above = -INFINITY;  // all of them: whatever is not below
+  } else if (border <= kBorder) {
+    for (int i = warp; i < border; i += kWarps) {
+      const double x = fine_score<D>(a, b, hk, t, a.first + sh.border.page[i], lane);
+      if (lane == 0) sh.border.value[i] = x;
+    }
+    __syncthreads();
+    for (int i = tid; i < border; i += kSelectThreads) {
+      const double x = sh.border.value[i];
+      const int p = sh.border.page[i];
+      int rank = 0;
+      for (int j = 0; j < border; ++j) {
+        const double y = sh.border.value[j];
+        rank += y > x || (y == x && sh.border.page[j] < p);
+      }
+      score[p] = rank < need ? INFINITY : -INFINITY;
+    }
+    __syncthreads();
+  } else {
+    // many equal or nearly equal pages (or something that is not finite): through memory
+    for (int i = warp; i < mid; i += kWarps) {
+      const float x = score[i];
+      if (!odd && (x > above || x < below)) continue;
+      const double y = fine_score<D>(a, b, hk, t, a.first + i, lane);
+      if (lane == 0) fine[i] = y;
+    }
+    __syncthreads();
+    const Kth<uint64_t> kth = kth_largest<kSelectThreads, uint64_t>(
+        mid, need, 64,
+        [&](int i, uint64_t& key) {
+          const float x = score[i];
+          if (!odd && (x > above || x < below)) return false;
+          key = ordered(fine[i]);
+          return true;
+        },
+        sh.k64);
+    // in order, so that of equal ones the first are taken
+    int taken = 0;
+    for (int i0 = 0; i0 < mid; i0 += kSelectThreads) {
+      const int i = i0 + tid;
+      const float x = i < mid ? score[i] : INFINITY;
+      const bool here = i < mid && (odd || !(x > above || x < below));
+      const uint64_t key = here ? ordered(fine[i]) : 0;
+      const bool tie = here && key >= kth.base && key - kth.base <= kth.range;
+      const unsigned ties = __ballot_sync(~0u, tie);
+      if (lane == 0) counts[0][warp] = __popc(ties);
+      __syncthreads();
+      int before = taken + __popc(ties & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += counts[0][w];
+        taken += counts[0][w];
+      }
+      if (here) score[i] = (tie ? before < kth.need : key > kth.base) ? INFINITY : -INFINITY;
+      __syncthreads();
+    }
+    if (odd) above = 3.402823466e38f;
+  }
+  // the pages in order: each warp has a stretch of them
+  const float least = need == border ? below : above;
+  auto in = [&](float x) { return need == border ? x >= least : x > least; };
+  const int per = (mid + kWarps * 32 - 1) / (kWarps * 32) * 32, w0 = min(mid, warp * per), w1 = min(mid, w0 + per);
+  int count = 0;
+  for (int i = w0; i < w1; i += 32)
+    count += __popc(__ballot_sync(~0u, i + lane < w1 && in(score[i + lane])));
+  if (lane == 0) counts[1][warp] = count;
+  __syncthreads();
+  int at = a.first;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (w < warp) at += counts[1][w];
+  for (int i = w0; i < w1; i += 32) {
+    const bool hit = i + lane < w1 && in(score[i + lane]);
+    const unsigned hits = __ballot_sync(~0u, hit);
+    const int to = at + __popc(hits & ((1u << lane) - 1u));
+    if (hit && to < a.top - a.last) out[to] = a.first + i + lane;  // always, while inputs stay
+    at += __popc(hits);
+  }
+}
+
+template <int D>
+cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t s) {
+  const int chunks = (a.max_pages + kScoreWarps * kScorePages - 1) / (kScoreWarps * kScorePages);
+  const unsigned grid = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv) * static_cast<unsigned>(chunks);
+  if (grid > 0 && a.top > a.first + a.last) {
+    const cudaError_t e = launch_chained(page_score_kernel<D>, grid, 32 * kScoreWarps, 0, s, a, chunks);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_chained(select_pages_kernel<D>, static_cast<unsigned>(a.c.total) * static_cast<unsigned>(a.c.Hkv),
+                        kSelectThreads, 0, s, a);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+cudaError_t launch_tree_mask(const int32_t* parents, const int32_t* cu, int B, int total, int words,
+                             uint64_t* mask, int* status, cudaStream_t s) {
+  const unsigned grid = (static_cast<unsigned>(total) + kTreeThreads - 1) / kTreeThreads;
+  return launch_chained(tree_mask_kernel, grid, kTreeThreads, 0, s, parents, cu, B, total, words, mask, status);
+}
+
+cudaError_t launch_page_bounds(int d, const BoundsArgs& a, cudaStream_t s) {
+  const int64_t units = ((static_cast<int64_t>(a.c.total) >> a.c.page_shift) + 2 * static_cast<int64_t>(a.c.B)) * a.c.Hkv;
+  const unsigned grid = static_cast<unsigned>((units + kBoundThreads / 32 - 1) / (kBoundThreads / 32));
+  return d == 64 ? launch_chained(page_bounds_kernel<64>, grid, kBoundThreads, 0, s, a)
+                 : launch_chained(page_bounds_kernel<128>, grid, kBoundThreads, 0, s, a);
+}
+
+SelectWorkspace select_workspace(int B, int total, int Hkv, int max_pages) {
+  SelectWorkspace w{};
+  const size_t rows = static_cast<size_t>(total) * static_cast<size_t>(Hkv), P = static_cast<size_t>(max_pages);
+  w.score = 0;
+  w.fine = up256(rows * P * 4);
+  w.reach = w.fine + up256(rows * P * 8);
+  w.total = w.reach + up256(static_cast<size_t>(B) * static_cast<size_t>(Hkv) * ((P + 15) / 16) * 4);
+  return w;
+}
+
+cudaError_t launch_select_pages(int d, const SelectArgs& a, cudaStream_t s) {
+  return d == 64 ? launch_select_d<64>(a, s) : launch_select_d<128>(a, s);
+}
+
+}  // namespace fa

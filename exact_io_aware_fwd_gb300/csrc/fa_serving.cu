@@ -1,7 +1,6 @@
 // C-ABI entry points (declared in include/fa.h) of the operators around attention: the norm and
 // rotation pass, the paged cache and the attention that reads it.  Every argument is checked
 // before the first launch; nothing here allocates device memory.
-#include <atomic>
 #include <cmath>
 #include <limits>
 
@@ -9,14 +8,21 @@
 #include "fa_host.h"
 #include "fa_internal.h"
 #include "fa_paged.h"
+#include "serving_checks.h"
 
 namespace {
 
 using fa::aligned_to;
+using fa::check_cache;
+using fa::check_heads;
+using fa::device_ready;
+using fa::kMaxInt;
+using fa::kMaxKeys;
+using fa::page_shift;
+using fa::status_of;
+using fa::up256;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxInt = 0x7fffffff;
-constexpr int kMaxKeys = kMaxInt - 255;  // keys rounded up to whole tiles fit 32 bits
 
 // A view that rows of 16-byte pieces can be read from or written to; the stride of a dimension
 // of one element does not matter.
@@ -26,13 +32,6 @@ bool view_ok(const fa_view& v, int B, int N, int H) {
 }
 fa::RowView row_view(const fa_view& v) {
   return {static_cast<__nv_bfloat16*>(v.data), v.batch, v.token, v.head};
-}
-
-fa_status check_heads(int H, int Hkv, int d) {
-  if (H <= 0 || Hkv <= 0) return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(H) + 2LL * Hkv > 65535) return FA_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
 }
 
 fa_status check_transform(const fa_qk_transform* t, int d) {
@@ -56,46 +55,6 @@ void set_transform(fa::RopeArgs& a, const fa_qk_transform& t) {
   a.wk = t.k_weight;
   a.eps = t.eps;
 }
-
-// The current device is an sm_103 part (asked once per device); its status word.
-fa_status device_ready(int*& status) {
-  static std::atomic<uint64_t> ready{0};  // bit d: device d is one
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
-  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
-  if ((ready.load(std::memory_order_acquire) & bit) == 0) {
-    const fa_status st = fa::check_device();
-    if (st != FA_OK) return st;
-    ready.fetch_or(bit, std::memory_order_release);
-  }
-  status = fa::status_ptr();
-  return status == nullptr ? FA_ERR_CUDA : FA_OK;
-}
-
-int page_shift(int page_size) {
-  switch (page_size) {
-    case 16: return 4;
-    case 32: return 5;
-    case 64: return 6;
-    case 128: return 7;
-  }
-  return -1;
-}
-
-fa_status check_cache(const fa_paged_kv* c) {
-  if (c == nullptr || c->k_cache == nullptr || c->v_cache == nullptr || c->kv_lens == nullptr)
-    return FA_ERR_INVALID_ARG;
-  if (!aligned_to(c->k_cache, 16) || !aligned_to(c->v_cache, 16)) return FA_ERR_INVALID_ARG;
-  if (c->num_pages < 1 || c->num_pages > (1 << 30) || c->max_pages < 0 ||
-      (c->max_pages > 0 && c->block_table == nullptr))
-    return FA_ERR_INVALID_ARG;
-  if (page_shift(c->page_size) < 0) return FA_ERR_UNSUPPORTED;
-  return FA_OK;
-}
-
-fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
-
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Cache pool as a 3-D tensor (d, page_size, pages x heads): boxes of one page x 64 columns with
 // the 128-byte swizzle.  The coordinate num_pages * Hkv lies outside and reads as zeros.
@@ -221,10 +180,16 @@ fa_status check_paged_sizes(int B, int total, int H, int Hkv, int d) {
   return FA_OK;
 }
 
-fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* prefix, void* O,
-                     float* LSE, const int32_t* cu, int B, int max_q, int max_kv, int total,
-                     int H, int Hkv, int d, int causal, float scale, void* ws, size_t ws_bytes,
-                     cudaStream_t s) {
+// never quite 0 (a scale of 0): a hidden key's score of -inf has to stay -inf when scaled
+float scale_log2_of(float scale, int d) {
+  return std::fmax(fa::resolve_scale(scale, d) * kLog2e, std::numeric_limits<float>::denorm_min());
+}
+
+// tree: the mask of a tree of new tokens (causal is then 0), or nullptr.
+fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* prefix,
+                     const uint64_t* tree, int tree_words, void* O, float* LSE, const int32_t* cu,
+                     int B, int max_q, int max_kv, int total, int H, int Hkv, int d, int causal,
+                     float scale, void* ws, size_t ws_bytes, cudaStream_t s) {
   fa_status st = check_paged_sizes(B, total, H, Hkv, d);
   if (st != FA_OK) return st;
   if (max_q < 1 || max_kv < 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
@@ -287,10 +252,11 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   a.G = H / Hkv;
   a.num_pages = cache->num_pages;
   a.page_shift = page_shift(cache->page_size);
-  // never quite 0 (a scale of 0): a hidden key's score of -inf has to stay -inf when scaled
-  a.scale_log2 = std::fmax(fa::resolve_scale(scale, d) * kLog2e,
-                           std::numeric_limits<float>::denorm_min());
+  a.scale_log2 = scale_log2_of(scale, d);
   a.status = status;
+  a.tree = reinterpret_cast<const uint32_t*>(tree);
+  a.tree_words = 2 * tree_words;
+  const fa::KeyMode mode = tree != nullptr ? fa::kTreeKeys : fa::kAllKeys;
   fa::JoinArgs j{};
   j.o = a.o;
   j.lse = LSE;
@@ -334,7 +300,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
   a.mma_cost = mma_tile_cost(d);
   if (whole) {
     a.list[0].unsplit = kMaxInt;
-    return status_of(fa::launch_paged_cta(d, a, lists, segments, s));
+    return status_of(fa::launch_paged_cta(d, mode, a, lists, segments, s));
   }
   const long long all = units[0] + (lists > 1 ? units[1] : 0);
   const bool together = lists == 1 && !mma[0] && cta_workers(segments, max_kv);
@@ -343,13 +309,95 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     a.list[0].unsplit = j.list[0].unsplit = kUnsplitTilesTogether;
   }
   const cudaError_t e =
-      together ? fa::launch_paged_cta(d, a, 1, all, s)
-      : any_mma ? fa::launch_paged_mma(d, tk, tv, a, lists, twin, all, fa::wait_timeout_ns(), s)
-              : fa::launch_paged(d, a, lists, all, s);
+      together ? fa::launch_paged_cta(d, mode, a, 1, all, s)
+      : any_mma ? fa::launch_paged_mma(d, mode, tk, tv, a, lists, twin, all, fa::wait_timeout_ns(), s)
+              : fa::launch_paged(d, mode, a, lists, all, s);
   if ((st = status_of(e)) != FA_OK) return st;
   // no entry can have been split (lengths are clamped to max_kv): every result is final
   if (lists == 1 && max_kv <= unsplit_keys(mma[0], B, Hkv))
     return FA_OK;
+  return status_of(fa::launch_paged_join(d, j, join_split(static_cast<long long>(total) * H), s));
+}
+
+// Attention over selected pages: every token is an entry of its own with top * page_size keys.
+fa_status selected_impl(const void* Q, const fa_paged_kv* cache, const int32_t* pages, int top,
+                        void* O, float* LSE, const int32_t* cu, int B, int total, int H, int Hkv,
+                        int d, float scale, void* ws, size_t ws_bytes, cudaStream_t s) {
+  if (B <= 0 || total < 0 || top < 1 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  fa_status st = check_paged_sizes(total > 0 ? total : 1, total, H, Hkv, d);
+  if (st != FA_OK) return st;
+  if (cu == nullptr && total != B) return FA_ERR_INVALID_ARG;
+  if ((st = check_cache(cache)) != FA_OK) return st;
+  if (total == 0) return FA_OK;
+  if (!Q || !O || !LSE || !pages || !aligned_to(Q, 16) || !aligned_to(O, 16))
+    return FA_ERR_INVALID_ARG;
+  const long long keys = static_cast<long long>(top) * cache->page_size;
+  const int count[2] = {total, 0}, G = H / Hkv;
+  const long long units = Hkv * static_cast<long long>(fa::row_tiles_bound(total, G, fa::kPagedRows, total)) *
+                          (keys / fa::kPagedKeys + 1);
+  if (keys > kMaxKeys || units > kMaxInt) return FA_ERR_UNSUPPORTED;
+  const PagedWorkspace w = paged_workspace(count, 1, total, H, Hkv, d);
+  if ((st = fa::check_workspace(ws, ws_bytes, w.total)) != FA_OK) return st;
+  int* status = nullptr;
+  if ((st = device_ready(status)) != FA_OK) return st;
+
+  char* base = static_cast<char*>(ws);
+  fa::PagedArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(Q);
+  a.k_cache = static_cast<const __nv_bfloat16*>(cache->k_cache);
+  a.v_cache = static_cast<const __nv_bfloat16*>(cache->v_cache);
+  a.o = static_cast<__nv_bfloat16*>(O);
+  a.lse = LSE;
+  a.B = total;
+  a.total = total;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.G = G;
+  a.num_pages = cache->num_pages;
+  a.page_shift = page_shift(cache->page_size);
+  a.scale_log2 = scale_log2_of(scale, d);
+  a.status = status;
+  a.pages = pages;
+  a.top = top;
+  a.seq_cu = cu;
+  a.seq_lens = cache->kv_lens;
+  a.seqs = B;
+  fa::KeyList& l = a.list[0];
+  l.count = total;
+  l.table = cache->block_table;
+  l.max_pages = cache->max_pages;
+  l.max_len = static_cast<int>(keys);
+  l.max_q = kMaxInt;
+  const long long segments = static_cast<long long>(total) * ((G + fa::kPagedRows - 1) / fa::kPagedRows) * Hkv;
+  const bool whole = whole_segments(segments, false, l.max_len);
+  const bool together = !whole && cta_workers(segments, l.max_len);
+  l.unsplit = whole      ? kMaxInt
+              : together ? kUnsplitTilesTogether
+                         : unsplit_keys(false, total, Hkv) / fa::kPagedKeys;
+  fa::PartialLayout& p = a.part[0];
+  p.R = fa::kPagedRows;
+  p.workers = fa::kPagedCtas * (together ? 1 : fa::kPagedWarps);
+  p.span_tiles = fa::row_tiles_bound(total, G, p.R, total);
+  p.spans = reinterpret_cast<int2*>(base + w.spans[0]);
+  p.slots = reinterpret_cast<float*>(base + w.slots[0]);
+  if (whole) return status_of(fa::launch_paged_cta(d, fa::kSelectedKeys, a, 1, segments, s));
+  const cudaError_t e = together ? fa::launch_paged_cta(d, fa::kSelectedKeys, a, 1, units, s)
+                                 : fa::launch_paged(d, fa::kSelectedKeys, a, 1, units, s);
+  if ((st = status_of(e)) != FA_OK) return st;
+  if (l.max_len / fa::kPagedKeys <= l.unsplit) return FA_OK;  // every result is final
+  fa::JoinArgs j{};
+  j.o = a.o;
+  j.lse = LSE;
+  j.B = total;
+  j.total = total;
+  j.H = H;
+  j.Hkv = Hkv;
+  j.G = G;
+  j.lists = 1;
+  j.list[0] = l;
+  j.part[0] = p;
+  j.seq_cu = cu;
+  j.seqs = B;
   return status_of(fa::launch_paged_join(d, j, join_split(static_cast<long long>(total) * H), s));
 }
 
@@ -511,8 +559,33 @@ fa_status fa_fwd_paged(const void* Q, const fa_paged_kv* cache, void* O, float* 
                        const int32_t* cu_seqlens, int B, int max_q, int max_kv, int total, int H,
                        int Hkv, int d, int causal, float scale, void* workspace,
                        size_t workspace_bytes, void* stream) {
-  return paged_impl(Q, cache, nullptr, O, LSE, cu_seqlens, B, max_q, max_kv, total, H, Hkv, d,
+  return paged_impl(Q, cache, nullptr, nullptr, 0, O, LSE, cu_seqlens, B, max_q, max_kv, total, H, Hkv, d,
                     causal, scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+fa_status fa_fwd_paged_tree(const void* Q, const fa_paged_kv* cache, const uint64_t* tree_mask,
+                            int mask_words, void* O, float* LSE, const int32_t* cu_seqlens, int B,
+                            int max_q, int max_kv, int total, int H, int Hkv, int d, float scale,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (mask_words < 1 || mask_words > (1 << 24)) return FA_ERR_INVALID_ARG;
+  if (total > 0 && (!tree_mask || !aligned_to(tree_mask, 8))) return FA_ERR_INVALID_ARG;
+  return paged_impl(Q, cache, nullptr, total > 0 ? tree_mask : nullptr, mask_words, O, LSE, cu_seqlens,
+                    B, max_q, max_kv, total, H, Hkv, d, 0, scale, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_fwd_paged_selected_workspace_size(int total, int H, int Hkv, int d) {
+  if (check_paged_sizes(total > 0 ? total : 1, total, H, Hkv, d) != FA_OK) return 0;
+  const int count[2] = {total, 0};
+  return paged_workspace(count, 1, total, H, Hkv, d).total;
+}
+
+fa_status fa_fwd_paged_selected(const void* Q, const fa_paged_kv* cache, const int32_t* pages,
+                                int top, void* O, float* LSE, const int32_t* cu_seqlens, int B,
+                                int total, int H, int Hkv, int d, float scale, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  return selected_impl(Q, cache, pages, top, O, LSE, cu_seqlens, B, total, H, Hkv, d, scale,
+                       workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 size_t fa_fwd_shared_prefix_workspace_size(int B, int groups, int total, int H, int Hkv, int d) {
@@ -528,7 +601,7 @@ fa_status fa_fwd_shared_prefix(const void* Q, const fa_paged_kv* cache, const fa
                                float scale, void* workspace, size_t workspace_bytes,
                                void* stream) {
   if (prefix == nullptr) return FA_ERR_INVALID_ARG;
-  return paged_impl(Q, cache, prefix, O, LSE, cu_seqlens, B, max_q, max_kv, total, H, Hkv, d,
+  return paged_impl(Q, cache, prefix, nullptr, 0, O, LSE, cu_seqlens, B, max_q, max_kv, total, H, Hkv, d,
                     causal, scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 

@@ -60,6 +60,14 @@ template <int R, int KT>
 __host__ __device__ __forceinline__ Entry entry_of(const KeyList& l, const PagedArgs& a, int b,
                                                    bool report) {
   Entry e;
+  if (l.lens == nullptr) {
+    e.start = b;
+    e.n = e.nc = 1;
+    e.len = l.max_len;
+    e.rt = (a.G + R - 1) / R;
+    e.tiles = e.rt * max(1, (e.len + KT - 1) / KT);
+    return e;
+  }
   const int len = device_load(l.lens + b);  // ahead of the branches: one wait for all of the loads
   bool ok;
   if (l.group_cu != nullptr) {

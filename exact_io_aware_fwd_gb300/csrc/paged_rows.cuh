@@ -84,7 +84,7 @@ struct Source {
   int hk, len;          // key/value head, keys
   int first, steps;     // key tile of step 0, number of steps
   int pages;            // lane i: page of step (issue & ~31) + i
-  static constexpr bool kPrefix = false;
+  static constexpr KeyMode kMode = kAllKeys;
   struct Place {
     const int32_t* row;  // block-table row
     int key, len;        // first key of a step and the keys behind that row
@@ -97,11 +97,15 @@ struct Source {
 struct PrefixedSource : Source {
   const int32_t* prow;
   int pre, plen;
-  static constexpr bool kPrefix = true;
   __device__ Place place(int st) const {
     const int t = first + st;
     return t < pre ? Place{prow, t * KT, plen, true} : Place{trow, (t - pre) * KT, len, false};
   }
+};
+
+// Keys of which a tree hides some.
+struct TreeSource : Source {
+  static constexpr KeyMode kMode = kTreeKeys;
 };
 
 __device__ __forceinline__ Source source_of(const KeyList& l, const Walk<R, KT>& w,
@@ -150,6 +154,80 @@ __device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l,
   cp_commit();
 }
 
+// The keys of the pages selected for one token and key/value head, in the order of its list.
+struct SelectedSource {
+  const int32_t *trow, *list;  // block-table row of the token's sequence, its pages
+  int hk, len;                 // key/value head, keys that the token sees
+  int first, steps;
+  int pages, keys;  // lane i: page (none: -1) and first key of step (issue & ~31) + i
+  bool live;        // the token belongs to a sequence
+  int* at;          // shared memory: first key of the step in each stage
+  static constexpr KeyMode kMode = kSelectedKeys;
+};
+constexpr int kNoKey = 0x7fffff00;  // behind every key: lengths are at most this
+
+__device__ __forceinline__ SelectedSource selected_source(const PagedArgs& a, const KeyList& l,
+                                                          const Walk<R, KT>& w, const Piece& p,
+                                                          int* at, int lane) {
+  SelectedSource s;
+  s.hk = p.hk;
+  s.first = p.ta;
+  s.at = at;
+  s.pages = -1;
+  s.keys = kNoKey;
+  const int t = w.e.start, b = token_sequence_group<32>(a.seq_cu, a.seqs, t, lane, ~0u);
+  int start = 0, n = 0;
+  if (b >= 0) token_bounds(a.seq_cu, b, a.total, start, n);
+  s.live = b >= 0 && t >= start && t < start + n;
+  if (b >= 0 && !s.live && lane == 0) atomicCAS(a.status, 0, kErrIndex);  // do not ascend
+  const int64_t reach = static_cast<int64_t>(l.max_pages) << a.page_shift;
+  const int given = s.live ? __ldg(a.seq_lens + b) : 0;
+  const int len = min(max(given, 0), static_cast<int>(min(reach, static_cast<int64_t>(kNoKey))));
+  if (given != len && lane == 0) atomicCAS(a.status, 0, kErrIndex);
+  s.len = min(max(len - n + (t - start) + 1, 0), len);
+  s.trow = l.table + static_cast<int64_t>(max(b, 0)) * l.max_pages;
+  s.list = a.pages + (static_cast<int64_t>(t) * a.Hkv + p.hk) * a.top;
+  s.steps = s.len > 0 ? min(p.te, (l.max_len + KT - 1) / KT) - p.ta : 0;
+  return s;
+}
+
+// issue_step for selected pages.  An entry of the list that names no page, or one behind what the
+// token sees, has no keys.
+template <int D>
+__device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l, SelectedSource& s,
+                                           int st, uint32_t ring, int lane) {
+  using L = PagedLayout<D>;
+  constexpr int S = L::kStages, GR = D / 8;
+  if (st < s.steps) {
+    if ((st & 31) == 0) {
+      const int tile = s.first + st + lane, j = tile >> (a.page_shift - 4);
+      const int i = st + lane < s.steps ? __ldg(s.list + j) : -1;
+      s.pages = -1;
+      s.keys = kNoKey;
+      if (i >= 0 && i < (s.len + (1 << a.page_shift) - 1) >> a.page_shift) {
+        s.keys = (i << a.page_shift) + (tile & ((1 << (a.page_shift - 4)) - 1)) * KT;
+        s.pages = resolve_page(s.trow, l.max_pages, a.num_pages, a.page_shift, s.keys);
+        if (s.pages < 0) atomicCAS(a.status, 0, kErrIndex);
+      }
+    }
+    const int page = __shfl_sync(~0u, s.pages, st & 31), key = __shfl_sync(~0u, s.keys, st & 31);
+    const int slot = st % S;
+    if (lane == 0) s.at[slot] = key;
+    const int64_t base = (((static_cast<int64_t>(max(page, 0)) * a.Hkv + s.hk) << a.page_shift) +
+                          (key & ((1 << a.page_shift) - 1))) * D;
+    const uint32_t dst = ring + slot * L::kStage;
+#pragma unroll
+    for (int i = 0; i < KT * GR / 32; ++i) {
+      const int r = (i * 32 + lane) / GR, g = (i * 32 + lane) % GR;
+      const bool valid = page >= 0 && key + r < s.len;
+      const int64_t off = valid ? base + r * D + g * 8 : 0;
+      cp_async16(dst + step_offset<D>(r, g), a.k_cache + off, valid);
+      cp_async16(dst + L::kHalf + step_offset<D>(r, g), a.v_cache + off, valid);
+    }
+  }
+  cp_commit();
+}
+
 // A row tile's queries as A fragments: the thread holds rows lane / 4 and lane / 4 + 8.
 template <int D>
 struct QRows {
@@ -158,8 +236,9 @@ struct QRows {
   int at[2];    // (token, head) of the row
   int head[2];
   int rows, lim_min;  // rows of the tile; the first row's limit, the smallest
+  const uint32_t* tree[2];  // kTreeKeys: mask rows; the context ends at lim_min
 };
-template <int D>
+template <int D, KeyMode M>
 __device__ __forceinline__ QRows<D> load_rows(const PagedArgs& a, const KeyList& l, const Entry& e,
                                               const Piece& p, int lane) {
   QRows<D> x;
@@ -171,6 +250,8 @@ __device__ __forceinline__ QRows<D> load_rows(const PagedArgs& a, const KeyList&
     x.lim[i] = rr < rows ? row_limit(e, l.causal, a.G, row0 + rr) : e.len;
     x.head[i] = p.hk * a.G + (row0 + rr - tok * a.G);
     x.at[i] = (e.start + tok) * a.H + x.head[i];
+    if constexpr (M == kTreeKeys)
+      x.tree[i] = a.tree + static_cast<int64_t>(e.start + (rr < rows ? tok : 0)) * a.tree_words;
     const __nv_bfloat16* qp = a.q + static_cast<int64_t>(x.at[i]) * D + (lane & 3) * 2;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
@@ -178,7 +259,7 @@ __device__ __forceinline__ QRows<D> load_rows(const PagedArgs& a, const KeyList&
       x.qf[k][i + 2] = rr < rows ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8) : 0u;
     }
   }
-  x.lim_min = row_limit(e, l.causal, a.G, row0);
+  x.lim_min = M == kTreeKeys ? e.len - e.n : row_limit(e, l.causal, a.G, row0);
   return x;
 }
 
@@ -214,15 +295,42 @@ __device__ __forceinline__ void scan_keys(const PagedArgs& a, const KeyList& l, 
         mma16816(s[1], x.qf[k], f[2], f[3]);
       }
     }
-    const auto p = src.place(st);
-    if (p.key + KT > (p.shared ? p.len : x.lim_min)) {  // all of a prefix is visible
+    if constexpr (Src::kMode == kAllKeys) {
+      const auto p = src.place(st);
+      if (p.key + KT > (p.shared ? p.len : x.lim_min)) {  // all of a prefix is visible
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = p.key + n * 8 + (lane & 3) * 2 + (k & 1);
-          if (key >= (p.shared ? p.len : x.lim[k >> 1])) s[n][k] = -INFINITY;
+          for (int k = 0; k < 4; ++k) {
+            const int key = p.key + n * 8 + (lane & 3) * 2 + (k & 1);
+            if (key >= (p.shared ? p.len : x.lim[k >> 1])) s[n][k] = -INFINITY;
+          }
+      }
+    } else {
+      int key0;
+      uint32_t see[2];  // bit i: the row sees key key0 + i
+      bool all;
+      if constexpr (Src::kMode == kSelectedKeys) {
+        key0 = src.at[st % S];
+        all = key0 + KT <= src.len;
+        see[0] = see[1] = (1u << min(max(src.len - key0, 0), KT)) - 1u;
+      } else {
+        key0 = src.place(st).key;
+        all = key0 + KT <= x.lim_min;
+        if (!all) {
+          const uint32_t there = (1u << min(max(src.len - key0, 0), KT)) - 1u;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            see[i] = tree_window(x.tree[i], a.tree_words, key0 - x.lim_min) & there;
         }
+      }
+      if (!all) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!((see[k >> 1] >> (n * 8 + (lane & 3) * 2 + (k & 1))) & 1u)) s[n][k] = -INFINITY;
+      }
     }
     // online softmax; the row maximum is shared by the four lanes of a row, the sum is
     // joined at the end
@@ -280,18 +388,36 @@ __device__ __forceinline__ void scan_keys(const PagedArgs& a, const KeyList& l, 
   }
 }
 
+// The keys of a piece; `at`: a shared-memory word for each stage of the ring (selected pages).
+template <KeyMode M>
+__device__ __forceinline__ auto make_source(const PagedArgs& a, const KeyList& l,
+                                            const Walk<R, KT>& w, const Piece& p, int* at, int lane) {
+  if constexpr (M == kSelectedKeys) {
+    return selected_source(a, l, w, p, at, lane);
+  } else if constexpr (M == kTreeKeys) {
+    return TreeSource{source_of(l, w, p)};
+  } else {
+    return source_of(l, w, p);
+  }
+}
+template <typename Src>
+__device__ __forceinline__ bool has_result(const Src& s) {
+  if constexpr (Src::kMode == kSelectedKeys) return s.live;
+  return true;
+}
+
 // A worker's share of a list's keys (one warp).
-template <int D>
+template <int D, KeyMode M>
 __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
                                      const PartialLayout& part, float* rowbuf, const Share& sh,
-                                     uint32_t ring, int lane) {
+                                     uint32_t ring, int* at, int lane) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages;
   if (sh.u0 >= sh.u1 || sh.b < 0) return;
   Walk<R, KT> walk(a, l, sh);
   Piece next_piece;
   bool more = walk.next(a, l, next_piece);
-  Source src = source_of(l, walk, next_piece);
+  auto src = make_source<M>(a, l, walk, next_piece, at, lane);
   for (int st = 0; st < S - 1; ++st) issue_step<D>(a, l, src, st, ring, lane);
   while (more) {
     const Piece piece = next_piece;
@@ -300,13 +426,14 @@ __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
     if (lane == 0 && piece.ta == 0)  // this worker begins the segment
       part.spans[static_cast<int64_t>(piece.hk) * part.span_tiles + tile] = span_of(sh, piece);
 
-    const QRows<D> x = load_rows<D>(a, l, e, piece, lane);
+    const QRows<D> x = load_rows<D, M>(a, l, e, piece, lane);
     Acc<D> c;
     scan_keys<D>(a, l, src, x, ring, lane, c);
+    const bool result = has_result(src);
     // every stage has been read: the next piece's copies start here
     more = walk.next(a, l, next_piece);
     if (more) {
-      src = source_of(l, walk, next_piece);
+      src = make_source<M>(a, l, walk, next_piece, at, lane);
       for (int st = 0; st < S - 1; ++st) issue_step<D>(a, l, src, st, ring, lane);
     }
 
@@ -319,7 +446,7 @@ __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
       c.sum[i] += __shfl_xor_sync(~0u, c.sum[i], 1);
       c.sum[i] += __shfl_xor_sync(~0u, c.sum[i], 2);
       const int rr = (lane >> 2) + 8 * i;
-      if (rr >= x.rows) continue;
+      if (rr >= x.rows || !result) continue;
       const float inv = c.sum[i] > 0.f ? 1.f / c.sum[i] : (c.sum[i] == 0.f ? 0.f : c.sum[i]);  // NaN stays
       if (final_out) {
         uint32_t* dst =
@@ -354,10 +481,11 @@ __device__ __forceinline__ void work(const PagedArgs& a, const KeyList& l,
 // (their own rings, whose copies have all been read), so that short segments leave nothing to join
 // and long ones an eighth of the parts.  The Share is the CTA's.  kPrefix: a sequence's keys are those
 // of its group's prefix and then its own; the prefix is read once per sequence, from L2.
-template <int D, bool kPrefix>
+template <int D, bool kPrefix, KeyMode M>
 __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList& l,
                                               const PartialLayout& parts, const Share& sh,
-                                              uint8_t* smem, int warp, int lane) {
+                                              uint8_t* smem, int* at, int warp, int lane) {
+  static_assert(!kPrefix || M == kAllKeys, "prefixes have all of their keys");
   using L = PagedLayout<D>;
   constexpr int S = L::kStages, P = D + 8;  // row pitch of a warp's O in floats
   constexpr uint32_t kRing = S * L::kStage;
@@ -367,8 +495,9 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
   Piece piece;
   while (walk.next(a, l, piece)) {
     const Entry& e = walk.e;
-    std::conditional_t<kPrefix, PrefixedSource, Source> src;
-    static_cast<Source&>(src) = source_of(l, walk, piece);
+    auto source = make_source<M>(a, l, walk, piece, at, lane);
+    std::conditional_t<kPrefix, PrefixedSource, decltype(source)> src;
+    static_cast<decltype(source)&>(src) = source;
     if constexpr (kPrefix) {
       const KeyList& pl = a.list[1];
       const int g = token_sequence_group<32>(pl.group_cu, pl.count, walk.b, lane, ~0u);
@@ -386,9 +515,10 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
     src.first += t0;
     src.steps = t1 - t0;
     for (int st = 0; st < S - 1; ++st) issue_step<D>(a, l, src, st, ring, lane);
-    const QRows<D> x = load_rows<D>(a, l, e, piece, lane);
+    const QRows<D> x = load_rows<D, M>(a, l, e, piece, lane);
     Acc<D> c;
     scan_keys<D>(a, l, src, x, ring, lane, c);
+    const bool result = has_result(src);
     float* mine = reinterpret_cast<float*>(smem + warp * kRing);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -433,7 +563,8 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
         o[4 * i + 3] = fmaf(f, v.w, o[4 * i + 3]);
       }
     }
-    if (rr < x.rows && !piece.whole) {
+    if (!result) {
+    } else if (rr < x.rows && !piece.whole) {
       float* slot = parts.slots + (static_cast<int64_t>(sh.worker) * 2 + (piece.ta == 0)) *
                                       (R * (D + 2));
       float4* dst = reinterpret_cast<float4*>(slot + rr * D + part * E);

@@ -35,6 +35,15 @@ decltype(&fa_fwd_paged) p_paged;
 decltype(&fa_fwd_paged_workspace_size) p_paged_ws;
 decltype(&fa_fwd_shared_prefix) p_prefix;
 decltype(&fa_fwd_shared_prefix_workspace_size) p_prefix_ws;
+decltype(&fa_tree_mask) p_tree_mask;
+decltype(&fa_fwd_paged_tree) p_tree;
+decltype(&fa_page_bounds) p_bounds;
+decltype(&fa_select_pages) p_select;
+decltype(&fa_select_pages_workspace_size) p_select_ws;
+decltype(&fa_fwd_paged_selected) p_selected;
+decltype(&fa_fwd_paged_selected_workspace_size) p_selected_ws;
+decltype(&fa_kv_weights) p_weights;
+decltype(&fa_kv_evict) p_evict;
 PyObject* fa_error;  // FAError(status, where)
 
 struct Refused : std::runtime_error {  // becomes ValueError
@@ -377,27 +386,40 @@ struct Cache {
   fa_paged_kv kv;
   int64_t B, Hkv, d, pages, page_size;
 };
-Cache cache_of(PyObject* const* a, at::Device dev) {
-  const at::Tensor& k = tensor(a[0], "k_cache");
-  const at::Tensor& v = tensor(a[1], "v_cache");
-  const at::Tensor& table = tensor(a[2], "block_table");
-  const at::Tensor& lens = tensor(a[3], "kv_lens");
-  if (k.dim() != 4 || table.dim() != 2)
-    refuse("k_cache must be [pages, Hkv, page_size, d], block_table [B, max_pages]");
+// block_table and kv_lens alone
+Cache table_of(PyObject* const* a, at::Device dev) {
+  const at::Tensor& table = tensor(a[0], "block_table");
+  const at::Tensor& lens = tensor(a[1], "kv_lens");
+  if (table.dim() != 2) refuse("block_table must be [B, max_pages]");
   Cache c{};
   c.B = table.size(0);
   c.pages = table.size(1);
-  c.Hkv = k.size(1);
-  c.page_size = k.size(2);
-  c.d = k.size(3);
-  c.kv.k_cache = array(&k, at::kBFloat16, k.sizes(), dev, "k_cache");
-  c.kv.v_cache = array(&v, at::kBFloat16, k.sizes(), dev, "v_cache");
-  c.kv.num_pages = dim32(k.size(0));
-  c.kv.page_size = dim32(c.page_size);
   c.kv.block_table = ints(&table, {c.B, c.pages}, dev, "block_table");
   c.kv.max_pages = dim32(c.pages);
   c.kv.kv_lens = ints(&lens, {c.B}, dev, "kv_lens");
   return c;
+}
+// with keys (and values, unless v is nullptr)
+Cache keys_of(PyObject* k_o, PyObject* v_o, PyObject* const* table, at::Device dev) {
+  const at::Tensor& k = tensor(k_o, "k_cache");
+  Cache c = table_of(table, dev);
+  if (k.dim() != 4) refuse("k_cache must be [pages, Hkv, page_size, d]");
+  c.Hkv = k.size(1);
+  c.page_size = k.size(2);
+  c.d = k.size(3);
+  c.kv.k_cache = array(&k, at::kBFloat16, k.sizes(), dev, "k_cache");
+  if (v_o != nullptr)
+    c.kv.v_cache = array(&tensor(v_o, "v_cache"), at::kBFloat16, k.sizes(), dev, "v_cache");
+  c.kv.num_pages = dim32(k.size(0));
+  c.kv.page_size = dim32(c.page_size);
+  return c;
+}
+Cache cache_of(PyObject* const* a, at::Device dev) { return keys_of(a[0], a[1], a + 2, dev); }
+
+// The keys of a sequence that a block table reaches.
+int reach_of(const Cache& c) {
+  const int64_t reach = c.pages * c.page_size;
+  return static_cast<int>(reach < INT32_MAX ? reach : INT32_MAX);
 }
 const int32_t* token_offsets(PyObject* o, const Cache& c, int64_t total, at::Device dev) {
   const at::Tensor* cu = tensor_or_none(o, "cu_seqlens");
@@ -439,8 +461,10 @@ PyObject* kv_append(PyObject* const* a) {
 }
 
 // ---- q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q, max_kv, causal, scale, out,
-//      lse, workspace; with a prefix: prefix_table, prefix_lens, group_cu, max_prefix too
-template <bool kPrefix>
+//      lse, workspace; with a prefix: prefix_table, prefix_lens, group_cu, max_prefix too; with a
+//      tree: its mask
+enum Kind { kPlain, kPrefix, kTree };
+template <Kind kKind>
 PyObject* attend(PyObject* const* a) {
   const at::Tensor& q = tensor(a[0], "q");
   const at::Device dev = cuda_device(q, "q");
@@ -453,14 +477,20 @@ PyObject* attend(PyObject* const* a) {
   int max_q = 1;
   if (a[6] != Py_None) max_q = int32_of(a[6], "max_q");
   else if (cu != nullptr) max_q = total > 1 ? dim32(total) : 1;
-  const int64_t reach = c.pages * c.page_size;
-  const int max_kv = a[7] != Py_None ? int32_of(a[7], "max_kv")
-                                     : static_cast<int>(reach < INT32_MAX ? reach : INT32_MAX);
+  const int max_kv = a[7] != Py_None ? int32_of(a[7], "max_kv") : reach_of(c);
   const int causal = PyObject_IsTrue(a[8]);
   if (causal < 0) throw python_error();
   const float scale = a[9] == Py_None ? -1.f : real(a[9]);
   fa_prefix pre{};
-  if (kPrefix) {
+  const uint64_t* mask = nullptr;
+  int words = 1;
+  if (kKind == kTree) {
+    const at::Tensor& m = tensor(a[13], "tree_mask");
+    if (m.dim() != 2) refuse("tree_mask must be [total, words]");
+    mask = static_cast<const uint64_t*>(array(&m, at::kLong, {total, m.size(1)}, dev, "tree_mask"));
+    words = dim32(m.size(1));
+  }
+  if (kKind == kPrefix) {
     const at::Tensor& table = tensor(a[13], "prefix_table");
     if (table.dim() != 2) refuse("prefix_table must be [groups, pages]");
     const int64_t groups = table.size(0), pages = table.size(1), most = pages * c.page_size;
@@ -479,10 +509,15 @@ PyObject* attend(PyObject* const* a) {
   const int B = dim32(c.B), T = dim32(total), h = dim32(H), hkv = dim32(c.Hkv), d = dim32(c.d);
   const Workspace ws =
       workspace(tensor_or_none(a[12], "workspace"),
-                kPrefix ? p_prefix_ws(B, pre.groups, T, h, hkv, d) : p_paged_ws(B, T, h, hkv, d),
+                kKind == kPrefix ? p_prefix_ws(B, pre.groups, T, h, hkv, d)
+                                 : p_paged_ws(B, T, h, hkv, d),
                 dev);
   void* stream = stream_of(dev);
-  if (kPrefix)
+  if (kKind == kTree)
+    check(p_tree(qp, &c.kv, mask, words, out.data_ptr(), lse.data_ptr<float>(), cu, B, max_q, max_kv, T,
+                 h, hkv, d, scale, ws.p, ws.bytes, stream),
+          "fa_fwd_paged_tree");
+  else if (kKind == kPrefix)
     check(p_prefix(qp, &c.kv, &pre, out.data_ptr(), lse.data_ptr<float>(), cu, B, max_q, max_kv, T,
                    h, hkv, d, causal, scale, ws.p, ws.bytes, stream),
           "fa_fwd_shared_prefix");
@@ -491,6 +526,183 @@ PyObject* attend(PyObject* const* a) {
                   d, causal, scale, ws.p, ws.bytes, stream),
           "fa_fwd_paged");
   return wrap_all({out, lse});
+}
+
+// ---- parents, cu_seqlens, max_q, out
+PyObject* tree_mask(PyObject* const* a) {
+  const at::Tensor& parents = tensor(a[0], "parents");
+  const at::Device dev = cuda_device(parents, "parents");
+  if (parents.dim() != 1) refuse("parents must be [total]");
+  const int64_t total = parents.size(0);
+  const int32_t* p = ints(&parents, {total}, dev, "parents");
+  const at::Tensor* cu = tensor_or_none(a[1], "cu_seqlens");
+  if (cu != nullptr && (cu->dim() != 1 || cu->size(0) < 1)) refuse("cu_seqlens must be [B + 1]");
+  const int64_t B = cu != nullptr ? cu->size(0) - 1 : total;
+  const int32_t* offsets = ints(cu, {B + 1}, dev, "cu_seqlens");
+  int64_t most = cu != nullptr ? total : 1;
+  if (a[2] != Py_None) most = int32_of(a[2], "max_q");
+  const int words = most > 0 ? dim32((most + 63) / 64) : 1;
+  const c10::cuda::OptionalCUDAGuard guard(dev);
+  const at::Tensor out =
+      own_array(tensor_or_none(a[3], "out"), {total, words}, at::kLong, dev, "out");
+  if (B > 0 && total > 0)
+    check(p_tree_mask(p, offsets, dim32(B), dim32(total), words,
+                      static_cast<uint64_t*>(out.data_ptr()), stream_of(dev)),
+          "fa_tree_mask");
+  return wrap(out);
+}
+
+// ---- k_cache, block_table, kv_lens, bounds, cu_seqlens, total
+PyObject* page_bounds(PyObject* const* a) {
+  const at::Device dev = cuda_device(tensor(a[0], "k_cache"), "k_cache");
+  const Cache c = keys_of(a[0], nullptr, a + 1, dev);
+  const at::Tensor& bounds = tensor(a[3], "bounds");
+  void* p = array(&bounds, at::kBFloat16, {c.kv.num_pages, c.Hkv, 2, c.d}, dev, "bounds");
+  const at::Tensor* cu = tensor_or_none(a[4], "cu_seqlens");
+  // without a count, any that the block table has room for
+  int64_t total = c.B;
+  if (cu != nullptr) {
+    const int64_t most = c.B * c.pages * c.page_size;
+    total = a[5] != Py_None ? integer(a[5]) : (most < INT32_MAX ? most : INT32_MAX);
+  } else if (a[5] != Py_None && integer(a[5]) != c.B) {
+    refuse("without cu_seqlens there is one token per sequence");
+  }
+  const int32_t* offsets = ints(cu, {c.B + 1}, dev, "cu_seqlens");
+  const c10::cuda::OptionalCUDAGuard guard(dev);
+  if (c.B > 0)
+    check(p_bounds(&c.kv, p, offsets, dim32(c.B), dim32(total), dim32(c.Hkv), dim32(c.d),
+                   stream_of(dev)),
+          "fa_page_bounds");
+  return wrap(bounds);
+}
+
+// ---- q, bounds, block_table, kv_lens, page_size, top, first, last, cu_seqlens, max_kv, out,
+//      workspace
+PyObject* select_pages(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  const at::Tensor& bounds = tensor(a[1], "bounds");
+  const at::Device dev = cuda_device(q, "q");
+  Cache c = table_of(a + 2, dev);
+  if (bounds.dim() != 4 || bounds.size(2) != 2) refuse("bounds must be [pages, Hkv, 2, d]");
+  c.Hkv = bounds.size(1);
+  c.d = bounds.size(3);
+  c.kv.num_pages = dim32(bounds.size(0));
+  c.kv.page_size = int32_of(a[4], "page_size");
+  c.page_size = c.kv.page_size;
+  if (c.page_size < 1) refuse("page_size is out of range");
+  const void* bp = array(&bounds, at::kBFloat16, bounds.sizes(), dev, "bounds");
+  if (q.dim() != 3 || q.size(2) != c.d || c.Hkv < 1 || q.size(1) % c.Hkv != 0)
+    refuse("q must be [total, H, d] with H a multiple of the bounds' heads");
+  const int64_t total = q.size(0), H = q.size(1);
+  const void* qp = array(&q, at::kBFloat16, q.sizes(), dev, "q");
+  const int top = int32_of(a[5], "top"), first = int32_of(a[6], "first"), last = int32_of(a[7], "last");
+  const int32_t* cu = token_offsets(a[8], c, total, dev);
+  const int max_kv = a[9] != Py_None ? int32_of(a[9], "max_kv") : reach_of(c);
+  if (top < 1) refuse("top must be positive");
+  const c10::cuda::OptionalCUDAGuard guard(dev);
+  const at::Tensor out =
+      own_array(tensor_or_none(a[10], "out"), {total, c.Hkv, top}, at::kInt, dev, "out");
+  if (c.B == 0 && total == 0) return wrap(out);  // an empty batch
+  const int B = dim32(c.B), T = dim32(total), hkv = dim32(c.Hkv);
+  const Workspace ws = workspace(tensor_or_none(a[11], "workspace"),
+                                 p_select_ws(B, T, hkv, c.kv.page_size, max_kv), dev);
+  check(p_select(qp, bp, &c.kv, out.data_ptr<int32_t>(), top, first, last, cu, B, max_kv, T, dim32(H),
+                 hkv, dim32(c.d), ws.p, ws.bytes, stream_of(dev)),
+        "fa_select_pages");
+  return wrap(out);
+}
+
+// ---- q, k_cache, v_cache, block_table, kv_lens, pages, cu_seqlens, scale, out, lse, workspace
+PyObject* attend_selected(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  const at::Device dev = cuda_device(q, "q");
+  const Cache c = cache_of(a + 1, dev);
+  if (q.dim() != 3 || q.size(2) != c.d || c.Hkv < 1 || q.size(1) % c.Hkv != 0)
+    refuse("q must be [total, H, d] with H a multiple of the cache's heads");
+  const int64_t total = q.size(0), H = q.size(1);
+  const void* qp = array(&q, at::kBFloat16, q.sizes(), dev, "q");
+  const at::Tensor& pages = tensor(a[5], "pages");
+  if (pages.dim() != 3) refuse("pages must be [total, Hkv, top]");
+  const int top = dim32(pages.size(2));
+  const int32_t* pp = ints(&pages, {total, c.Hkv, pages.size(2)}, dev, "pages");
+  const int32_t* cu = token_offsets(a[6], c, total, dev);
+  const float scale = a[7] == Py_None ? -1.f : real(a[7]);
+  const c10::cuda::OptionalCUDAGuard guard(dev);
+  const at::Tensor out = own_array(tensor_or_none(a[8], "out"), q.sizes(), at::kBFloat16, dev, "out");
+  const at::Tensor lse = own_array(tensor_or_none(a[9], "lse"), {H, total}, at::kFloat, dev, "lse");
+  if (c.B == 0 && total == 0) return wrap_all({out, lse});  // an empty batch
+  const int T = dim32(total), h = dim32(H), hkv = dim32(c.Hkv), d = dim32(c.d);
+  const Workspace ws = workspace(tensor_or_none(a[10], "workspace"), p_selected_ws(T, h, hkv, d), dev);
+  check(p_selected(qp, &c.kv, pp, top, out.data_ptr(), lse.data_ptr<float>(), cu, dim32(c.B), T, h, hkv,
+                   d, scale, ws.p, ws.bytes, stream_of(dev)),
+        "fa_fwd_paged_selected");
+  return wrap_all({out, lse});
+}
+
+// ---- q, lse, k_cache, block_table, kv_lens, weights, cu_seqlens, max_q, max_kv, causal, scale, out
+PyObject* kv_weights(PyObject* const* a) {
+  const at::Tensor& q = tensor(a[0], "q");
+  const at::Device dev = cuda_device(q, "q");
+  const Cache c = keys_of(a[2], nullptr, a + 3, dev);
+  if (q.dim() != 3 || q.size(2) != c.d || c.Hkv < 1 || q.size(1) % c.Hkv != 0)
+    refuse("q must be [total, H, d] with H a multiple of the cache's heads");
+  const int64_t total = q.size(0), H = q.size(1);
+  const void* qp = array(&q, at::kBFloat16, q.sizes(), dev, "q");
+  const float* lse = static_cast<const float*>(
+      array(&tensor(a[1], "lse"), at::kFloat, {H, total}, dev, "lse"));
+  const int32_t* cu = token_offsets(a[6], c, total, dev);
+  int max_q = 1;
+  if (a[7] != Py_None) max_q = int32_of(a[7], "max_q");
+  else if (cu != nullptr) max_q = total > 1 ? dim32(total) : 1;
+  const int max_kv = a[8] != Py_None ? int32_of(a[8], "max_kv") : reach_of(c);
+  const int causal = PyObject_IsTrue(a[9]);
+  if (causal < 0) throw python_error();
+  const float scale = a[10] == Py_None ? -1.f : real(a[10]);
+  const at::Tensor* in = tensor_or_none(a[5], "weights");
+  const at::Tensor* given = tensor_or_none(a[11], "out");
+  if (max_kv < 0) refuse("max_kv is out of range");
+  int64_t cap = max_kv;  // columns: those of weights, of out, or max_kv
+  for (const at::Tensor* t : {given, in}) {
+    if (t == nullptr) continue;
+    if (t->dim() != 3) refuse("weights and out must be [B, Hkv, capacity]");
+    cap = t->size(2);
+  }
+  const float* w = static_cast<const float*>(array(in, at::kFloat, {c.B, c.Hkv, cap}, dev, "weights"));
+  const c10::cuda::OptionalCUDAGuard guard(dev);
+  const at::Tensor out = own_array(given, {c.B, c.Hkv, cap}, at::kFloat, dev, "out");
+  if (c.B > 0)
+    check(p_weights(qp, lse, &c.kv, w, out.data_ptr<float>(), dim32(cap), cu, dim32(c.B), max_q, max_kv,
+                    dim32(total), dim32(H), dim32(c.Hkv), dim32(c.d), causal, scale, stream_of(dev)),
+          "fa_kv_weights");
+  return wrap(out);
+}
+
+// ---- weights, k_cache, v_cache, block_table, kv_lens, new_table, budget, recent, max_kv
+PyObject* kv_evict(PyObject* const* a) {
+  const at::Tensor& w = tensor(a[0], "weights");
+  const at::Device dev = cuda_device(w, "weights");
+  const Cache c = cache_of(a + 1, dev);
+  if (w.dim() != 3) refuse("weights must be [B, Hkv, capacity]");
+  const int64_t cap = w.size(2);
+  const float* wp = static_cast<const float*>(array(&w, at::kFloat, {c.B, c.Hkv, cap}, dev, "weights"));
+  const at::Tensor& table = tensor(a[5], "new_table");
+  if (table.dim() != 2) refuse("new_table must be [B, pages]");
+  const int32_t* tp = ints(&table, {c.B, table.size(1)}, dev, "new_table");
+  const int budget = int32_of(a[6], "budget"), recent = int32_of(a[7], "recent");
+  const int max_kv = a[8] != Py_None ? int32_of(a[8], "max_kv") : reach_of(c);
+  if (budget < 1 || recent < 0 || recent > budget) refuse("0 <= recent <= budget and 1 <= budget");
+  if (table.size(1) * c.page_size < (budget < max_kv ? budget : max_kv))
+    refuse("new_table must have pages for the keys that may be kept");
+  const c10::cuda::OptionalCUDAGuard guard(dev);
+  const at::Tensor lens = fresh({c.B}, at::kInt, dev);
+  const at::Tensor kept = fresh({c.B, c.Hkv, budget}, at::kInt, dev);
+  const at::Tensor left = fresh({c.B, c.Hkv, budget}, at::kFloat, dev);
+  if (c.B > 0)
+    check(p_evict(wp, dim32(cap), &c.kv, tp, dim32(table.size(1)), budget, recent,
+                  lens.data_ptr<int32_t>(), kept.data_ptr<int32_t>(), left.data_ptr<float>(), dim32(c.B),
+                  max_kv, dim32(c.Hkv), dim32(c.d), stream_of(dev)),
+          "fa_kv_evict");
+  return wrap_all({lens, kept, left});
 }
 
 // ---- error class, then the entry points' addresses in the order below
@@ -507,18 +719,34 @@ PyObject* bind(PyObject* const* a) {
   p_paged_ws = reinterpret_cast<decltype(p_paged_ws)>(at(6));
   p_prefix = reinterpret_cast<decltype(p_prefix)>(at(7));
   p_prefix_ws = reinterpret_cast<decltype(p_prefix_ws)>(at(8));
+  p_tree_mask = reinterpret_cast<decltype(p_tree_mask)>(at(9));
+  p_tree = reinterpret_cast<decltype(p_tree)>(at(10));
+  p_bounds = reinterpret_cast<decltype(p_bounds)>(at(11));
+  p_select = reinterpret_cast<decltype(p_select)>(at(12));
+  p_select_ws = reinterpret_cast<decltype(p_select_ws)>(at(13));
+  p_selected = reinterpret_cast<decltype(p_selected)>(at(14));
+  p_selected_ws = reinterpret_cast<decltype(p_selected_ws)>(at(15));
+  p_weights = reinterpret_cast<decltype(p_weights)>(at(16));
+  p_evict = reinterpret_cast<decltype(p_evict)>(at(17));
   Py_RETURN_NONE;
 }
 
 #define FA_METHOD(name, body, args)                                                         \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<body, args>)), \
    METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FA_METHOD("bind", bind, 9),
+PyMethodDef methods[] = {FA_METHOD("bind", bind, 18),
                          FA_METHOD("norm_rope_fwd", norm_rope_fwd, 12),
                          FA_METHOD("norm_rope_bwd", norm_rope_bwd, 15),
                          FA_METHOD("kv_append", kv_append, 15),
-                         FA_METHOD("fwd_paged", attend<false>, 13),
-                         FA_METHOD("fwd_shared_prefix", attend<true>, 17),
+                         FA_METHOD("fwd_paged", attend<kPlain>, 13),
+                         FA_METHOD("fwd_shared_prefix", attend<kPrefix>, 17),
+                         FA_METHOD("fwd_paged_tree", attend<kTree>, 14),
+                         FA_METHOD("tree_mask", tree_mask, 4),
+                         FA_METHOD("page_bounds", page_bounds, 6),
+                         FA_METHOD("select_pages", select_pages, 12),
+                         FA_METHOD("fwd_paged_selected", attend_selected, 11),
+                         FA_METHOD("kv_weights", kv_weights, 12),
+                         FA_METHOD("kv_evict", kv_evict, 9),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

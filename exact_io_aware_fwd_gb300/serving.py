@@ -25,7 +25,10 @@ from .build_lib import BINDING_PATH
 _BF16 = torch.bfloat16
 _ENTRIES = ["fa_qk_norm_rope_fwd", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_bwd_workspace_size",
             "fa_kv_append", "fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_fwd_shared_prefix",
-            "fa_fwd_shared_prefix_workspace_size"]
+            "fa_fwd_shared_prefix_workspace_size", "fa_tree_mask", "fa_fwd_paged_tree",
+            "fa_page_bounds", "fa_select_pages", "fa_select_pages_workspace_size",
+            "fa_fwd_paged_selected", "fa_fwd_paged_selected_workspace_size", "fa_kv_weights",
+            "fa_kv_evict"]
 _ext = None
 
 
@@ -235,3 +238,113 @@ def fa_fwd_shared_prefix(q, k_cache, v_cache, block_table, kv_lens, prefix_table
     return _on(stream, ext.fwd_shared_prefix, q, k_cache, v_cache, block_table, kv_lens,
                cu_seqlens, max_q, max_kv, causal, scale, out, lse, workspace, prefix_table,
                prefix_lens, group_cu, max_prefix)
+
+
+# ------------------------------------------------------------------------------------------- trees
+def fa_tree_mask(parents, cu_seqlens=None, max_q=None, out=None, stream=None):
+    """int64 [total, words] masks of trees of new tokens: bit k of a token's row says whether it sees
+    the k-th new token of its sequence (itself and its ancestors).  parents: int32 [total], each
+    token's parent as an index among its sequence's new tokens, smaller than its own, or -1 behind
+    the context.  cu_seqlens: the sequences' offsets, default one token each; max_q (default: total,
+    or 1 without cu_seqlens) bounds a sequence's tokens and gives the words, 64 tokens each."""
+    ext = _ext or _binding()
+    if stream is None:
+        return ext.tree_mask(parents, cu_seqlens, max_q, out)
+    return _on(stream, ext.tree_mask, parents, cu_seqlens, max_q, out)
+
+
+def fa_fwd_paged_tree(q, k_cache, v_cache, block_table, kv_lens, tree_mask, cu_seqlens=None,
+                      max_q=None, max_kv=None, scale=None, out=None, lse=None, workspace=None,
+                      stream=None):
+    """fa_fwd_paged of trees of drafted tokens (see include/fa.h): a query sees the keys in front of
+    its sequence's new tokens, and those new tokens whose bit is set in its row of tree_mask (int64
+    [total, words], fa_tree_mask's or any other).  The drafted tokens' keys and values are in the
+    cache; their rotary position is that of their depth, so they go there in two steps:
+    fa_qk_norm_rope_fwd with positions, then fa_kv_append without a table."""
+    ext = _ext or _binding()
+    if stream is None:
+        return ext.fwd_paged_tree(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, max_q,
+                                  max_kv, False, scale, out, lse, workspace, tree_mask)
+    return _on(stream, ext.fwd_paged_tree, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens,
+               max_q, max_kv, False, scale, out, lse, workspace, tree_mask)
+
+
+# ---------------------------------------------------------------------------------- selected pages
+def fa_page_bounds(k_cache, block_table, kv_lens, bounds, cu_seqlens=None, total=None, stream=None):
+    """Renews the bounds (bf16 [pages, Hkv, 2, d]: the smallest and the largest of each element of a
+    page's keys) of the pages that hold one of the last n keys of each sequence (see include/fa.h).
+    cu_seqlens: offsets whose differences are n, default 1 each; total: at least their last one, which
+    bounds the launch (default: what the block table has room for).  Returns bounds."""
+    ext = _ext or _binding()
+    if stream is None:
+        return ext.page_bounds(k_cache, block_table, kv_lens, bounds, cu_seqlens, total)
+    return _on(stream, ext.page_bounds, k_cache, block_table, kv_lens, bounds, cu_seqlens, total)
+
+
+def fa_select_pages_workspace_size(B, total, Hkv, page_size, max_kv) -> int:
+    return int(load_library().fa_select_pages_workspace_size(int(B), int(total), int(Hkv),
+                                                             int(page_size), int(max_kv)))
+
+
+def fa_select_pages(q, bounds, block_table, kv_lens, page_size, top, first=1, last=1,
+                    cu_seqlens=None, max_kv=None, out=None, workspace=None, stream=None):
+    """int32 [total, Hkv, top]: the pages that each query token attends to (see include/fa.h): the
+    `first` first and `last` last of those it sees and, of the others, those whose keys may score
+    highest by their bounds; ascending indices into the sequence's row of block_table, -1 where
+    there are fewer.  max_kv bounds a sequence's keys (default: the block table's reach): the
+    workspace grows with it."""
+    ext = _ext or _binding()
+    if stream is None:
+        return ext.select_pages(q, bounds, block_table, kv_lens, page_size, top, first, last,
+                                cu_seqlens, max_kv, out, workspace)
+    return _on(stream, ext.select_pages, q, bounds, block_table, kv_lens, page_size, top, first,
+               last, cu_seqlens, max_kv, out, workspace)
+
+
+def fa_fwd_paged_selected_workspace_size(total, H, Hkv, d) -> int:
+    return int(load_library().fa_fwd_paged_selected_workspace_size(int(total), int(H), int(Hkv),
+                                                                   int(d)))
+
+
+def fa_fwd_paged_selected(q, k_cache, v_cache, block_table, kv_lens, pages, cu_seqlens=None,
+                          scale=None, out=None, lse=None, workspace=None, stream=None):
+    """O [total, H, d] and LSE [H, total] of packed queries over the keys of selected pages (see
+    include/fa.h): each token and key/value head reads the pages in its row of pages (int32 [total,
+    Hkv, top], fa_select_pages' or any other), causally."""
+    ext = _ext or _binding()
+    if stream is None:
+        return ext.fwd_paged_selected(q, k_cache, v_cache, block_table, kv_lens, pages, cu_seqlens,
+                                      scale, out, lse, workspace)
+    return _on(stream, ext.fwd_paged_selected, q, k_cache, v_cache, block_table, kv_lens, pages,
+               cu_seqlens, scale, out, lse, workspace)
+
+
+# ---------------------------------------------------------------------------------------- eviction
+def fa_kv_weights(q, lse, k_cache, block_table, kv_lens, weights=None, cu_seqlens=None, max_q=None,
+                  max_kv=None, causal=False, scale=None, out=None, stream=None):
+    """float32 [B, Hkv, capacity]: weights (None: zeros) plus the attention weights that the queries q
+    [total, H, d] gave to each key, summed over a key/value head's queries (see include/fa.h); lse:
+    the attention's [H, total].  The capacity is that of weights or out, else max_kv; out may be
+    weights.  cu_seqlens, max_q, max_kv, causal, scale: as in the attention call."""
+    ext = _ext or _binding()
+    if stream is None:
+        return ext.kv_weights(q, lse, k_cache, block_table, kv_lens, weights, cu_seqlens, max_q,
+                              max_kv, causal, scale, out)
+    return _on(stream, ext.kv_weights, q, lse, k_cache, block_table, kv_lens, weights, cu_seqlens,
+               max_q, max_kv, causal, scale, out)
+
+
+def fa_kv_evict(weights, k_cache, v_cache, block_table, kv_lens, new_table, budget, recent,
+                max_kv=None, stream=None):
+    """Each sequence and key/value head keeps `budget` keys, the last `recent` and those of the rest
+    with the largest weights (float32 [B, Hkv, capacity]), in their order (see include/fa.h).  They
+    and their values are copied to the pages new_table (int32 [B, pages], unused pages of the
+    cache).  Returns (new_lens int32 [B], kept int32 [B, Hkv, budget]: which keys, -1 behind the
+    last, new_weights float32 [B, Hkv, budget]).  The next token's rotary position stays kv_lens[b]:
+    kv_lens - new_lens is what fa_kv_append's pos_offset grows by."""
+    ext = _ext or _binding()
+    if stream is None:
+        return ext.kv_evict(weights, k_cache, v_cache, block_table, kv_lens, new_table, budget,
+                            recent, max_kv)
+    return _on(stream, ext.kv_evict, weights, k_cache, v_cache, block_table, kv_lens, new_table,
+               budget, recent, max_kv)

@@ -381,6 +381,97 @@ fa_status fa_fwd_shared_prefix(const void* Q, const fa_paged_kv* cache, const fa
                                void* stream);
 
 /*
+ * Attention of trees of drafted tokens over the cache: fa_fwd_paged where the n new tokens of a
+ * sequence are the nodes of a tree and each sees the context and its own branch.  New token i sees
+ * key j when j < kv_lens[b] - n, or when bit j - (kv_lens[b] - n) of its mask is set (and j is
+ * below kv_lens[b]).  tree_mask: DEVICE uint64 [total][mask_words], bit k % 64 of word k / 64: the
+ * sequence's new token k; tokens past the last bit are not seen.  Any mask will do, rows of zeros
+ * (the context alone) too.  The keys and values of the drafted tokens are in the cache already
+ * (rotated by their depth: fa_qk_norm_rope_fwd with positions, then fa_kv_append without a table);
+ * all of them must be finite.  Otherwise as fa_fwd_paged, with its workspace.
+ *
+ * fa_tree_mask: the masks of trees given by parents (DEVICE int32[total]: the index of each token's
+ * parent among its sequence's new tokens, smaller than its own, or -1 behind the context): each
+ * token, its parent, its parent's parent and so on.  A parent that is not ends the branch, and a
+ * token past the last bit is left out; both record FA_ERR_INDEX.
+ */
+fa_status fa_tree_mask(const int32_t* parents, const int32_t* cu_seqlens, int B, int total,
+                       int mask_words, uint64_t* tree_mask, void* stream);
+fa_status fa_fwd_paged_tree(const void* Q, const fa_paged_kv* cache, const uint64_t* tree_mask,
+                            int mask_words, void* O, float* LSE, const int32_t* cu_seqlens, int B,
+                            int max_q, int max_kv, int total, int H, int Hkv, int d, float scale,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention over a few pages of the cache that a cheap score selects for each query.
+ *
+ * fa_page_bounds: the smallest and the largest of each element of a page's keys, bounds: DEVICE
+ * bf16 [num_pages][Hkv][2][d], renewed for the pages that hold one of the last n keys of each
+ * sequence (n new tokens; n = kv_lens[b] renews all), over the keys below kv_lens[b].  A key that
+ * is not a number makes its bounds so.  Other pages' bounds stay as they are.  cache->v_cache is
+ * not used.
+ *
+ * fa_select_pages: the `top` pages that each token's queries attend to, for every key/value head.
+ *   score(page) = max over the head's queries q of sum_e max(q_e, 0) hi_e + min(q_e, 0) lo_e,
+ * which is at least q.k for each key k of the page.  Of the pages that hold keys the token sees
+ * (causal: token i of n sees keys <= kv_lens[b] - n + i) the first `first` and the last `last` are
+ * always selected, and those of the highest scores, `top` in all; of equal scores the lowest page
+ * (a score that is not a number counts as infinity, a page outside the pool as bounds of 0).  The
+ * choice is that of exactly computed scores, whatever the rounding.  pages: DEVICE int32
+ * [total][Hkv][top], indices into the sequence's block-table row, ascending, -1 behind the last
+ * where there are fewer.  first + last <= top.  cache->k_cache and v_cache are not used.
+ * workspace: fa_select_pages_workspace_size(...) bytes, 256-byte aligned.
+ *
+ * fa_fwd_paged_selected: fa_fwd_paged (causal) of each token over the keys of its listed pages
+ * only.  Entries may be in any order; one that names no page with keys that the token sees (-1)
+ * has none, and a page listed twice counts twice.  Tokens behind cu_seqlens[B] are left as they
+ * were, here and in fa_select_pages.
+ * workspace: fa_fwd_paged_selected_workspace_size(...) bytes, 256-byte aligned.
+ */
+fa_status fa_page_bounds(const fa_paged_kv* cache, void* bounds, const int32_t* cu_seqlens, int B,
+                         int total, int Hkv, int d, void* stream);
+size_t fa_select_pages_workspace_size(int B, int total, int Hkv, int page_size, int max_kv);
+fa_status fa_select_pages(const void* Q, const void* bounds, const fa_paged_kv* cache,
+                          int32_t* pages, int top, int first, int last, const int32_t* cu_seqlens,
+                          int B, int max_kv, int total, int H, int Hkv, int d, void* workspace,
+                          size_t workspace_bytes, void* stream);
+size_t fa_fwd_paged_selected_workspace_size(int total, int H, int Hkv, int d);
+fa_status fa_fwd_paged_selected(const void* Q, const fa_paged_kv* cache, const int32_t* pages,
+                                int top, void* O, float* LSE, const int32_t* cu_seqlens, int B,
+                                int total, int H, int Hkv, int d, float scale, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction of the keys that have gathered the least attention.
+ *
+ * fa_kv_weights: out[b][h][j] = weights[b][h][j] + sum over the new tokens that see key j and over
+ * the queries of key/value head h of exp(scale q.k_j - LSE), the weights that fa_fwd_paged gave
+ * the key (LSE [H][total] is its second output).  weights, out: DEVICE float32 [B][Hkv][capacity];
+ * weights NULL: zeros; out may be weights itself.  All of out is written: from kv_lens[b] on it
+ * is weights.  max_q, max_kv: as in fa_fwd_paged (lengths are clamped to capacity as well).  A row
+ * whose LSE is -inf adds nothing.  cache->v_cache is not used.
+ *
+ * fa_kv_evict: every sequence and key/value head keeps `budget` keys, the last `recent` ones and
+ * those of the rest that have the largest weights (of equal ones the earlier; one that is not a
+ * number is the largest), in their order; a sequence of no more keys keeps all.  Keys and values
+ * are copied to the first places of the pages new_table[b] (DEVICE int32 [B][new_pages], pages of
+ * the same cache that hold no key of the call's sequences), so pages that other sequences share
+ * stay as they are.  new_lens: int32[B], how many were kept; kept: int32 [B][Hkv][budget], which
+ * (ascending, -1 behind the last); new_weights: float32 [B][Hkv][budget], their weights (0 behind
+ * the last); all DEVICE and overlapping none of the inputs.  0 <= recent <= budget.  Keys keep the
+ * rotation that they had, so the next token's position is kv_lens[b], not new_lens[b]: the
+ * difference is fa_kv_append's pos_offset.
+ */
+fa_status fa_kv_weights(const void* Q, const float* LSE, const fa_paged_kv* cache,
+                        const float* weights, float* out, int capacity, const int32_t* cu_seqlens,
+                        int B, int max_q, int max_kv, int total, int H, int Hkv, int d, int causal,
+                        float scale, void* stream);
+fa_status fa_kv_evict(const float* weights, int capacity, const fa_paged_kv* cache,
+                      const int32_t* new_table, int new_pages, int budget, int recent,
+                      int32_t* new_lens, int32_t* kept, float* new_weights, int B, int max_kv,
+                      int Hkv, int d, void* stream);
+
+/*
  * Synchronises `stream`, returns the first device-side error recorded since the previous call
  * (FA_OK if none) and clears it.  A pending CUDA error on the stream gives FA_ERR_CUDA.
  */

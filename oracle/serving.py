@@ -81,3 +81,91 @@ def attend(q, k, v, scale, limits):
             A[i, h] = (p / total) @ np.abs(vv)
             size[i, h] = scale * (np.abs(kk) @ np.abs(q[i, h])).max()
     return O, LSE, A, size
+
+
+def attend_where(q, k, v, scale, seen):
+    """attend() where row i sees the keys j with seen[i, head of k, j] (seen [t, Hkv or 1, n])."""
+    t, H, d = q.shape
+    Hkv, n = k.shape[:2]
+    O, A = np.zeros((t, H, d)), np.zeros((t, H, d))
+    LSE, size = np.full((t, H), -np.inf), np.zeros((t, H))
+    seen = np.broadcast_to(seen, (t, Hkv, n))
+    for h in range(H):
+        kk, vv, there = k[h * Hkv // H], v[h * Hkv // H], seen[:, h * Hkv // H]
+        s = np.where(there, scale * (q[:, h] @ kk.T), -np.inf)
+        some = there.any(1)
+        top = np.where(some, s.max(1, initial=-np.inf), 0.0)
+        p = np.exp(s - top[:, None])
+        total = p.sum(1)
+        with np.errstate(divide="ignore"):
+            LSE[:, h] = top + np.log(total)
+        p = p / np.where(some, total, 1.0)[:, None]
+        O[:, h], A[:, h] = p @ vv, p @ np.abs(vv)
+        size[:, h] = scale * np.where(there, np.abs(q[:, h]) @ np.abs(kk).T, 0.0).max(1, initial=0.0)
+    return O, LSE, A, size
+
+
+def tree_sees(parents):
+    """[n, n] bool: token i sees itself and its ancestors."""
+    n = len(parents)
+    out = np.zeros((n, n), dtype=bool)
+    for i in range(n):
+        j = i
+        while j >= 0:
+            out[i, j] = True
+            j = parents[j]
+    return out
+
+
+def page_bounds(k, page):
+    """Smallest and largest of each element of each page's keys: k [Hkv, n, d] -> two [Hkv, pages, d]."""
+    cut = [k[:, i:i + page] for i in range(0, k.shape[1], page)]
+    return np.stack([c.min(1) for c in cut], 1), np.stack([c.max(1) for c in cut], 1)
+
+
+def page_scores(q, lo, hi):
+    """[Hkv, pages]: the largest of the bounds on q.k over the heads of a group; q [H, d]."""
+    Hkv = lo.shape[0]
+    x = q.reshape(Hkv, -1, 1, q.shape[1])
+    with np.errstate(invalid="ignore"):
+        s = (np.maximum(x, 0) * hi[:, None] + np.minimum(x, 0) * lo[:, None]).sum(-1)
+    return np.where(np.isnan(s), np.inf, s).max(1)
+
+
+def largest(values, count):
+    """Indices of the `count` largest values, ties to the lowest index, ascending."""
+    return np.sort(np.lexsort((np.arange(len(values)), -np.asarray(values)))[:count])
+
+
+def select_pages(scores, pages, top, first, last):
+    """The pages of one query and key/value head: the first and last, and of the others the best."""
+    if pages <= top:
+        return np.arange(pages)
+    mid = first + largest(scores[first:pages - last], top - first - last)
+    return np.concatenate([np.arange(first), mid, np.arange(pages - last, pages)])
+
+
+def key_weights(q, k, scale, lse, limits):
+    """[Hkv, n]: the weights exp(scale q.k - lse) of each key summed over queries, and a bound on
+    the sum of |terms| times (1 + the size of their exponents); q [t, H, d], lse [t, H]."""
+    Hkv, n = k.shape[:2]
+    G = q.shape[1] // Hkv
+    w, err = np.zeros((Hkv, n)), np.zeros((Hkv, n))
+    for i in range(q.shape[0]):
+        m = int(max(0, min(limits[i], n)))
+        for h in range(q.shape[1]):
+            if m == 0 or lse[i, h] == -np.inf:
+                continue
+            kk = k[h // G, :m]
+            p = np.exp(scale * (kk @ q[i, h]) - lse[i, h])
+            w[h // G, :m] += p
+            err[h // G, :m] += p * (1 + scale * (np.abs(kk) @ np.abs(q[i, h])) + abs(lse[i, h]))
+    return w, err
+
+
+def evict(weights, n, budget, recent):
+    """Indices of the keys of one sequence and head that stay, ascending."""
+    if n <= budget:
+        return np.arange(n)
+    w = np.where(np.isnan(weights[:n - recent]), np.inf, weights[:n - recent])
+    return np.concatenate([largest(w, budget - recent), np.arange(n - recent, n)])
