@@ -130,7 +130,7 @@ fa_status fa_select_pages(const void* Q, const void* bounds, const fa_paged_kv* 
   a.pages = pages;
   char* base = static_cast<char*>(workspace);
   a.score = reinterpret_cast<float*>(base + w.score);
-  a.fine = reinterpret_cast<double*>(base + w.fine);
+  a.fine = reinterpret_cast<uint64_t*>(base + w.fine);
   a.reach = reinterpret_cast<float*>(base + w.reach);
   return status_of(fa::launch_select_pages(d, a, static_cast<cudaStream_t>(stream)));
 }

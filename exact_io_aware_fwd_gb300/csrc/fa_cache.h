@@ -74,7 +74,7 @@ struct SelectArgs {
   int top, first, last;
   int32_t* pages;     // [total][Hkv][top]
   float* score;       // workspace: [total][Hkv][max_pages]
-  double* fine;       // workspace: the same in 64 bits, where many scores are next to the border
+  uint64_t* fine;     // workspace: the same exactly, where many scores are next to the border
   float* reach;       // workspace: [B][Hkv][ceil(max_pages / 16)] largest |bound| of 16 pages
 };
 struct SelectWorkspace {

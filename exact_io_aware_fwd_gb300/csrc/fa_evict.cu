@@ -110,70 +110,110 @@ __global__ void __launch_bounds__(32 * kWeightWarps) kv_weights_kernel(const Wei
 }
 
 // ---- eviction: which keys stay
-// One CTA a sequence and head: the smallest weight that stays by counting (select_kth.cuh), then one
-// pass in order that lists the keys and their weights.
-constexpr int kEvictThreads = 1024;
+// The smallest weight that stays by counting (select_kth.cuh), then the keys in order.  A sequence
+// and head is a CTA's, or, where a CTA's registers (kRounds weights a thread) do not hold its
+// weights, a cluster's, each CTA with a stretch of them; only what does not fit eight CTAs is read
+// again in every pass.
+constexpr int kRounds = 16;
+constexpr int evict_cluster(int max_len, int threads) {
+  int c = 1;
+  while (c < 8 && c * kRounds * threads < max_len) c *= 2;
+  return c;
+}
 
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const EvictArgs a) {
-  constexpr int kWarps = kEvictThreads / 32;
-  __shared__ KthShared<kEvictThreads, uint32_t> sh;
-  __shared__ int counts[2][kWarps];
+template <int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
+  __shared__ KthShared<kThreads, uint32_t> sh;
+  __shared__ OrderShared<kThreads, kRounds> order_sh;
+  __shared__ alignas(8) unsigned totals[2];  // above the k-th, in its range
   begin_launch();
   const CacheSeqs& c = a.c;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / c.Hkv, hk = blockIdx.x - b * c.Hkv;
-  const int len = keys_of(c, b, tid == 0 && hk == 0);
+  const int rank = kCluster ? cluster_rank() : 0, ctas = kCluster ? cluster_size() : 1;
+  const int row = static_cast<int>(blockIdx.x) / ctas, tid = threadIdx.x, all = rank * kThreads + tid;
+  const int b = row / c.Hkv, hk = row - b * c.Hkv;
+  const int len = keys_of(c, b, all == 0 && hk == 0);
   const int count = min(len, a.budget);
-  if (tid == 0 && hk == 0) a.new_lens[b] = count;
-  const float* w = a.weights + static_cast<int64_t>(blockIdx.x) * a.cap;
-  int32_t* kept = a.kept + static_cast<int64_t>(blockIdx.x) * a.budget;
-  float* left = a.new_weights + static_cast<int64_t>(blockIdx.x) * a.budget;
-  for (int i = count + tid; i < a.budget; i += kEvictThreads) {
+  if (all == 0 && hk == 0) a.new_lens[b] = count;
+  const float* w = a.weights + static_cast<int64_t>(row) * a.cap;
+  int32_t* kept = a.kept + static_cast<int64_t>(row) * a.budget;
+  float* left = a.new_weights + static_cast<int64_t>(row) * a.budget;
+  const int old = len > a.budget ? len - a.recent : 0;  // keys that are chosen from
+  const int k = count - (len - old);                    // and how many of them stay
+  // this CTA's stretch, its first kRounds rounds in registers
+  const int chunk = (old + ctas - 1) / ctas, c0 = min(old, rank * chunk), c1 = min(old, c0 + chunk);
+  float x[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int at = c0 + i * kThreads + tid;
+    x[i] = at < c1 ? w[at] : 0.f;
+  }
+  for (int i = count + all; i < a.budget; i += ctas * kThreads) {
     kept[i] = -1;
     left[i] = 0.f;
   }
-  const int old = len > a.budget ? len - a.recent : 0;  // keys that are chosen from
-  const int k = count - (len - old);                    // and how many of them stay
-  for (int i = old + tid; i < len; i += kEvictThreads) {
+  for (int i = old + all; i < len; i += ctas * kThreads) {
     kept[k + i - old] = i;
     left[k + i - old] = w[i];
   }
-  if (k == 0) return;
-  const Kth<uint32_t> kth = kth_largest<kEvictThreads, uint32_t>(
-      old, k, 32, [&](int i, uint32_t& key) { key = ordered(w[i]); return true; }, sh);
-  int taken = 0, ties = 0;  // listed, and met in the last bin
-  for (int i0 = 0; i0 < old; i0 += kEvictThreads) {
-    const int i = i0 + tid;
-    const float x = i < old ? w[i] : 0.f;
-    const uint32_t key = ordered(x);
-    const bool tie = i < old && key >= kth.base && key - kth.base <= kth.range;
-    const bool over = i < old && key > kth.base && !tie;
-    const unsigned tm = __ballot_sync(~0u, tie), om = __ballot_sync(~0u, over);
-    if (lane == 0) {
-      counts[0][warp] = __popc(tm);
-      counts[1][warp] = __popc(om);
-    }
-    __syncthreads();
-    const unsigned less = (1u << lane) - 1u;
-    int tb = ties + __popc(tm & less), ob = taken + __popc(om & less);
+  if (k == 0) return;  // the whole cluster
+  auto each = [&](auto f) {
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
-      if (v < warp) {
-        tb += counts[0][v];
-        ob += counts[1][v];
-      }
-      ties += counts[0][v];
-      taken += counts[1][v];
-    }
-    if (over || (tie && tb < kth.need)) {
-      const int at = ob + min(tb, kth.need);
-      if (at < k) {  // always, while nobody writes the weights
-        kept[at] = i;
-        left[at] = x;
-      }
-    }
+    for (int i = 0; i < kRounds; ++i)
+      if (c0 + i * kThreads + tid < c1) f(ordered(x[i]));
+    for (int at = c0 + kRounds * kThreads + tid; at < c1; at += kThreads) f(ordered(w[at]));
+  };
+  const Kth<uint32_t> kth = kth_largest<kThreads, kCluster, uint32_t>(k, 32, each, sh);
+  unsigned over0 = 0, tie0 = 0;  // in front of this CTA's stretch
+  if constexpr (kCluster) {
+    if (tid == 0) totals[0] = totals[1] = 0;
     __syncthreads();
+    unsigned over = 0, tie = 0;
+    each([&](uint32_t key) {
+      over += kth.under(key);
+      tie += kth.holds(key);
+    });
+    over = __reduce_add_sync(~0u, over);
+    tie = __reduce_add_sync(~0u, tie);
+    if ((tid & 31) == 0) {
+      atomicAdd(&totals[0], over);
+      atomicAdd(&totals[1], tie);
+    }
+    cluster_sync();
+    for (int p = 0; p < rank; ++p) {
+      const uint2 v = peer_load2(totals, p);
+      over0 += v.x;
+      tie0 += v.y;
+    }
   }
+  Order<kThreads, kRounds> order{order_sh};
+  for (int r0 = c0; r0 < c1; r0 += kRounds * kThreads) {
+    if (r0 > c0) {
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int at = r0 + i * kThreads + tid;
+        x[i] = at < c1 ? w[at] : 0.f;
+      }
+    }
+    auto there = [&](int i) { return r0 + i * kThreads + tid < c1; };
+    auto over = [&](int i) { return there(i) && kth.under(ordered(x[i])); };
+    auto tie = [&](int i) { return there(i) && kth.holds(ordered(x[i])); };
+    const unsigned total = order.scan(over, tie);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const bool o = over(i), t = tie(i);
+      const unsigned before = order.before(i, o, t);
+      const int ties = static_cast<int>(tie0 + (before >> 16));
+      const int at = static_cast<int>(over0 + (before & 0xffffu)) + min(ties, kth.need);
+      if ((o || (t && ties < kth.need)) && at < k) {  // at < k: always, while nobody writes the weights
+        kept[at] = r0 + i * kThreads + tid;
+        left[at] = x[i];
+      }
+    }
+    over0 += total & 0xffffu;
+    tie0 += total >> 16;
+    __syncthreads();  // the counts have been read
+  }
+  if constexpr (kCluster) cluster_sync();  // nobody leaves while others read its shared memory
 }
 
 // ---- eviction: the copies
@@ -238,7 +278,12 @@ cudaError_t launch_kv_weights(int d, const WeightsArgs& a, cudaStream_t s) {
 
 cudaError_t launch_kv_evict(int d, const EvictArgs& a, cudaStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv);
-  const cudaError_t e = launch_chained(evict_select_kernel, rows, kEvictThreads, 0, s, a);
+  const int most = a.c.max_len;
+  const int cluster = evict_cluster(most, 1024);
+  const cudaError_t e =
+      most <= kRounds * 256 ? launch_chained(evict_select_kernel<256, false>, rows, 256, 0, s, a)
+      : cluster == 1 ? launch_chained(evict_select_kernel<1024, false>, rows, 1024, 0, s, a)
+                     : launch_clusters(evict_select_kernel<1024, true>, rows * cluster, cluster, 1024, s, a);
   if (e != cudaSuccess) return e;
   const int chunks = (a.budget + kMoveKeys - 1) / kMoveKeys;
   return d == 64 ? launch_chained(evict_move_kernel<64>, rows * chunks, kMoveThreads, 0, s, a, chunks)

@@ -31,6 +31,24 @@ cudaError_t launch_chained(K kernel, dim3 grid, unsigned threads, uint32_t smem,
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
+// The same in clusters of `cluster` CTAs.
+template <typename K, typename... Args>
+cudaError_t launch_clusters(K kernel, unsigned grid, int cluster, unsigned threads, cudaStream_t s,
+                            const Args&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.stream = s;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  c.attrs = attr;
+  c.numAttrs = 2;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
 #ifdef __CUDACC__
 // The next kernel on the stream may be scheduled.
 __device__ __forceinline__ void let_next_launch() {

@@ -174,44 +174,39 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = static_cast<int>(blockIdx.x) / chunks, chunk = static_cast<int>(blockIdx.x) % chunks;
   const int b = bh / c.Hkv, hk = bh - b * c.Hkv;
+  const int p0 = (chunk * kScoreWarps + warp) * kScorePages;
+  // the pages, the length and the offsets are loaded together
+  int phys[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int p = p0 + 8 * t + (lane >> 2);
+    phys[t] = p < c.max_pages ? __ldg(c.block_table + static_cast<int64_t>(b) * c.max_pages + p) : -1;
+  }
   const int len = keys_of(c, b, threadIdx.x == 0 && chunk == 0 && hk == 0);
   int start, n;
   token_bounds(c.cu, b, c.total, start, n);
   const int pages = (len + (1 << c.page_shift) - 1) >> c.page_shift;
-  const int p0 = (chunk * kScoreWarps + warp) * kScorePages;
   if (p0 >= pages || n == 0) return;
   uint4 lo[2][J], hi[2][J];
-  uint32_t most = 0;  // largest |bound|, as bits: NaN is above infinity
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int p = p0 + 8 * t + (lane >> 2);
-    const int phys = p < pages ? page_of(c, b, p) : -1;
+    if (p0 + 8 * t + (lane >> 2) >= pages) {
+      phys[t] = -1;
+    } else if (phys[t] < 0 || phys[t] >= c.num_pages) {
+      phys[t] = -1;
+      atomicCAS(c.status, 0, kErrIndex);
+    }
     const uint4* src = reinterpret_cast<const uint4*>(
-                           a.bounds + (static_cast<int64_t>(max(phys, 0)) * c.Hkv + hk) * 2 * D) + (lane & 3);
+                           a.bounds + (static_cast<int64_t>(max(phys[t], 0)) * c.Hkv + hk) * 2 * D) + (lane & 3);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       lo[t][j] = hi[t][j] = make_uint4(0u, 0u, 0u, 0u);
-      if (phys >= 0) {
+      if (phys[t] >= 0) {
         lo[t][j] = __ldg(src + 4 * j);
         hi[t][j] = __ldg(src + D / 8 + 4 * j);
       }
     }
   }
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint32_t u[8] = {lo[t][j].x, lo[t][j].y, lo[t][j].z, lo[t][j].w,
-                             hi[t][j].x, hi[t][j].y, hi[t][j].z, hi[t][j].w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) most = __vmaxu2(most, u[k] & 0x7fff7fffu);
-    }
-  most = max(most & 0xffffu, most >> 16);
-  most = __reduce_max_sync(~0u, most);
-  if (lane == 0)
-    a.reach[static_cast<int64_t>(bh) * ((a.max_pages + kScorePages - 1) / kScorePages) + p0 / kScorePages] =
-        __uint_as_float(most << 16);
-
   // tokens of a row tile, or row tiles of a token
   const int per = a.G <= 16 ? 16 / a.G : 1, tiles = a.G <= 16 ? 1 : (a.G + 15) / 16;
   const int rows_per = a.G <= 16 ? a.G : 16;
@@ -277,6 +272,21 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
       }
     }
   }
+  uint32_t most = 0;  // largest |bound|, as bits: NaN is above infinity
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const uint32_t u[8] = {lo[t][j].x, lo[t][j].y, lo[t][j].z, lo[t][j].w,
+                             hi[t][j].x, hi[t][j].y, hi[t][j].z, hi[t][j].w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) most = __vmaxu2(most, u[k] & 0x7fff7fffu);
+    }
+  most = max(most & 0xffffu, most >> 16);
+  most = __reduce_max_sync(~0u, most);
+  if (lane == 0)
+    a.reach[static_cast<int64_t>(bh) * ((a.max_pages + kScorePages - 1) / kScorePages) + p0 / kScorePages] =
+        __uint_as_float(most << 16);
 }
 
 // ---- selection
@@ -284,31 +294,87 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
 // exact scores: the float32 scores above are off by at most delta = 2^-15 sum_e |q_e| max |bound|
 // (16 products of 16 terms each, every addition off by at most 2^-23 of what has been added up so
 // far in magnitude).  With t the k-th largest of them, every page more than 2 delta above t is in and
-// every page more than 2 delta below it is out; the few between are scored again in 64 bits, where
-// the products of two bfloat16 are exact and their sums nearly always too.
-constexpr int kSelectThreads = 256;
+// every page more than 2 delta below it is out; the few between are scored again as exactly as in 64
+// bits.
 constexpr int kBorder = 512;  // pages next to the border that are ranked in shared memory
 
+// What a warp needs of a page and the queries: E elements a lane, of kHeads heads at a time.
+constexpr int kFineHeads = 4;
 template <int D>
-__device__ __forceinline__ double fine_score(const SelectArgs& a, int b, int hk, int t, int p, int lane) {
+struct FineRows {
+  const __nv_bfloat16 *box, *q;
+  bool there;  // a page outside the pool has bounds of 0
+  __device__ FineRows(const SelectArgs& a, int b, int hk, int t, int p, int lane) {
+    const int phys = page_of(a.c, b, p);
+    there = phys >= 0;
+    box = a.bounds + (static_cast<int64_t>(max(phys, 0)) * a.c.Hkv + hk) * 2 * D + lane * (D / 32);
+    q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D + lane * (D / 32);
+  }
+};
+
+// The score as an integer: sum q_e box_e in units of 2^-62 of sum |q_e| max |bound| or more.  q and
+// the bounds are scaled by powers of two so that sum |u_e| <= 1 for the products u_e, which are
+// exact; three times the next 22 bits of a product are taken off as an integer (adding 3/2 2^23
+// rounds to one), and the integers are added up, in any order.  fp64 would do, but at two
+// multiply-adds a cycle and SM it made this the longest part of the kernel (18 us of 33).
+template <int D>
+__device__ __forceinline__ int64_t fine_score(const SelectArgs& a, int b, int hk, int t, int p, int lane,
+                                              float q_scale, float box_scale) {
   constexpr int E = D / 32;
-  const CacheSeqs& c = a.c;
-  const int phys = page_of(c, b, p);
-  const __nv_bfloat16* box = a.bounds + (static_cast<int64_t>(max(phys, 0)) * c.Hkv + hk) * 2 * D + lane * E;
-  double lo[E], hi[E];
+  constexpr float kRound = 12582912.f;  // 3/2 2^23
+  const FineRows<D> r(a, b, hk, t, p, lane);
+  float lo[E], hi[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    lo[e] = phys >= 0 ? static_cast<double>(__bfloat162float(box[e])) : 0.0;
-    hi[e] = phys >= 0 ? static_cast<double>(__bfloat162float(box[D + e])) : 0.0;
+    lo[e] = r.there ? __bfloat162float(r.box[e]) * box_scale : 0.f;
+    hi[e] = r.there ? __bfloat162float(r.box[D + e]) * box_scale : 0.f;
   }
-  const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D + lane * E;
+  int64_t best = INT64_MIN;
+  for (int g = 0; g < a.G; g += kFineHeads) {
+    uint32_t sum[kFineHeads][3];
+#pragma unroll
+    for (int i = 0; i < kFineHeads; ++i) {
+      sum[i][0] = sum[i][1] = sum[i][2] = 0u;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float q = __bfloat162float(r.q[min(g + i, a.G - 1) * D + e]) * q_scale;
+        float u = q * (q > 0.f ? hi[e] : lo[e]), t;
+        t = fmaf(u, 0x1p22f, kRound);
+        u = fmaf(t - kRound, -0x1p-22f, u);
+        sum[i][0] += __float_as_uint(t) - __float_as_uint(kRound);
+        t = fmaf(u, 0x1p44f, kRound);
+        u = fmaf(t - kRound, -0x1p-44f, u);
+        sum[i][1] += __float_as_uint(t) - __float_as_uint(kRound);
+        t = fmaf(u, 0x1p66f, kRound);
+        sum[i][2] += __float_as_uint(t) - __float_as_uint(kRound);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFineHeads; ++i) {
+      const int s0 = __reduce_add_sync(~0u, static_cast<int>(sum[i][0]));
+      const int s1 = __reduce_add_sync(~0u, static_cast<int>(sum[i][1]));
+      const int s2 = __reduce_add_sync(~0u, static_cast<int>(sum[i][2]));
+      const int64_t x = (((static_cast<int64_t>(s0) << 22) + s1) << 18) + (s2 >> 4);
+      best = x > best ? x : best;
+    }
+  }
+  return best;
+}
+
+// In 64 bits, where something is not finite.
+template <int D>
+__device__ __forceinline__ double odd_score(const SelectArgs& a, int b, int hk, int t, int p, int lane) {
+  constexpr int E = D / 32;
+  const FineRows<D> r(a, b, hk, t, p, lane);
   double best = -INFINITY;
   for (int g = 0; g < a.G; ++g) {
     double x = 0.0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const double v = static_cast<double>(__bfloat162float(q[g * D + e]));
-      x += (v < 0.0 ? 0.0 : v) * hi[e] + (v > 0.0 ? 0.0 : v) * lo[e];
+      const double v = static_cast<double>(__bfloat162float(r.q[g * D + e]));
+      const double lo = r.there ? static_cast<double>(__bfloat162float(r.box[e])) : 0.0;
+      const double hi = r.there ? static_cast<double>(__bfloat162float(r.box[D + e])) : 0.0;
+      x += (v < 0.0 ? 0.0 : v) * hi + (v > 0.0 ? 0.0 : v) * lo;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
@@ -317,64 +383,85 @@ __device__ __forceinline__ double fine_score(const SelectArgs& a, int b, int hk,
   }
   return best;
 }
+// The largest power of two whose product with x > 0 is at most 1 (about; x = 0: 1).
+__device__ __forceinline__ float scale_below(float x) {
+  const int e = static_cast<int>(__float_as_uint(x) >> 23);  // x < 2^(e - 126)
+  return x == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(min(max(253 - e, 1), 253)) << 23);
+}
 
-template <int D>
-__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const SelectArgs a) {
-  constexpr int kWarps = kSelectThreads / 32;
+constexpr int kSelectRounds = 4;  // scores of a thread in registers; further ones are read again
+constexpr float kMost = 3.402823466e38f;
+
+// behind_scores: page_score_kernel is the kernel ahead, so what it did not write is complete.
+template <int D, int kSelectThreads>
+__global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const SelectArgs a, const bool behind_scores) {
+  constexpr int kWarps = kSelectThreads / 32, kHeld = kSelectRounds * kSelectThreads;
   __shared__ union {
     KthShared<kSelectThreads, uint32_t> k32;
     KthShared<kSelectThreads, uint64_t> k64;
     struct {
-      double value[kBorder];
+      uint64_t value[kBorder];
       int page[kBorder];
+      bool take[kBorder];
     } border;
   } sh;
+  __shared__ OrderShared<kSelectThreads, kSelectRounds> order_sh;
   __shared__ float red[2][kWarps];
-  __shared__ int counts[3][kWarps], border_count;
-  begin_launch();
+  __shared__ int counts[kWarps], border_count;
+  let_next_launch();
+  if (!behind_scores) wait_for_last_launch();
   const CacheSeqs& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x / c.Hkv, hk = blockIdx.x - t * c.Hkv;
   const int b = token_sequence_group<32>(c.cu, c.B, t, lane, ~0u);
-  if (b < 0) return;  // behind the last sequence
-  int start, n;
-  token_bounds(c.cu, b, c.total, start, n);
-  if (t < start || t >= start + n) {  // offsets that do not ascend
-    if (tid == 0) atomicCAS(c.status, 0, kErrIndex);
-    return;
+  int start = 0, n = 0, pages = -1;
+  if (b >= 0) {
+    token_bounds(c.cu, b, c.total, start, n);
+    if (t < start || t >= start + n) {  // offsets that do not ascend
+      if (tid == 0) atomicCAS(c.status, 0, kErrIndex);
+    } else {
+      const int len = keys_of(c, b, hk == 0 && tid == 0);
+      const int sees = min(max(len - n + (t - start) + 1, 0), len);
+      pages = (sees + (1 << c.page_shift) - 1) >> c.page_shift;
+    }
   }
-  const int len = keys_of(c, b, false);
-  const int sees = min(max(len - n + (t - start) + 1, 0), len);
-  const int pages = (sees + (1 << c.page_shift) - 1) >> c.page_shift;
+  const int mid = pages - a.first - a.last, k = a.top - a.first - a.last;  // k of the pages in between
+  const bool choose = pages > a.top && k > 0;
   int32_t* out = a.pages + static_cast<int64_t>(blockIdx.x) * a.top;
+  float size = 0.f;  // largest sum |q_e| of a head
+  if (choose) {
+    const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D;
+    for (int g = warp; g < a.G; g += kWarps) {
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x += fabsf(__bfloat162float(q[g * D + e * 32 + lane]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+      size = x == x ? fmaxf(size, x) : INFINITY;
+    }
+  }
+  if (behind_scores) wait_for_last_launch();
+  if (pages < 0) return;  // behind the last sequence
   if (pages <= a.top) {
     for (int i = tid; i < a.top; i += kSelectThreads) out[i] = i < pages ? i : -1;
     return;
   }
   for (int i = tid; i < a.first; i += kSelectThreads) out[i] = i;
   for (int i = tid; i < a.last; i += kSelectThreads) out[a.top - a.last + i] = pages - a.last + i;
-  const int mid = pages - a.first - a.last, k = a.top - a.first - a.last;  // k of mid > k pages
   if (k == 0) return;
   float* score = a.score + static_cast<int64_t>(blockIdx.x) * a.max_pages + a.first;
-  double* fine = a.fine + static_cast<int64_t>(blockIdx.x) * a.max_pages + a.first;
-
-  // delta
-  const int groups = (a.max_pages + kScorePages - 1) / kScorePages;
-  const float* reach = a.reach + (static_cast<int64_t>(b) * c.Hkv + hk) * groups;
-  float far = 0.f, size = 0.f;
-  bool odd = false;  // something is not finite
-  for (int i = tid; i < (pages + kScorePages - 1) / kScorePages; i += kSelectThreads) {
-    far = fmaxf(far, reach[i]);
-    odd |= !(reach[i] < INFINITY);
-  }
-  const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D;
-  for (int g = warp; g < a.G; g += kWarps) {
-    float x = 0.f;
-    for (int e = lane; e < D; e += 32) x += fabsf(__bfloat162float(q[g * D + e]));
+  float x[kSelectRounds];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-    odd |= !(x < INFINITY);
-    size = fmaxf(size, x);
+  for (int i = 0; i < kSelectRounds; ++i) {
+    const int at = i * kSelectThreads + tid;
+    x[i] = at < mid ? score[at] : 0.f;
+  }
+  // delta
+  const float* reach = a.reach + (static_cast<int64_t>(b) * c.Hkv + hk) * ((a.max_pages + kScorePages - 1) / kScorePages);
+  float far = 0.f;
+  for (int i = tid; i < (pages + kScorePages - 1) / kScorePages; i += kSelectThreads) {
+    const float r = reach[i];
+    far = r == r ? fmaxf(far, r) : INFINITY;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) far = fmaxf(far, __shfl_xor_sync(~0u, far, o));
@@ -382,120 +469,150 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     red[0][warp] = far;
     red[1][warp] = size;
   }
-  odd = __syncthreads_or(odd);
+  if (tid == 0) border_count = 0;
+  __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     far = fmaxf(far, red[0][w]);
     size = fmaxf(size, red[1][w]);
   }
   const float delta = far * size * 0x1p-15f;
-  odd |= !(delta < INFINITY);
+  // something is not finite, or too large to be scaled below 1: every score in 64 bits
+  const bool odd = !(delta < INFINITY && far < 0x1p126f && size < 0x1p126f);
 
-  float above = 3.402823466e38f, below = -INFINITY;  // in, and at least in question
+  float above = kMost, below = -INFINITY;  // in, and at least in question
   if (!odd) {
-    const Kth<uint32_t> kth = kth_largest<kSelectThreads, uint32_t>(
-        mid, k, 2, [&](int i, uint32_t& key) { key = ordered(score[i]); return true; }, sh.k32);
+    auto each = [&](auto f) {
+#pragma unroll
+      for (int i = 0; i < kSelectRounds; ++i)
+        if (i * kSelectThreads + tid < mid) f(ordered(x[i]));
+      for (int at = kHeld + tid; at < mid; at += kSelectThreads) f(ordered(score[at]));
+    };
+    const Kth<uint32_t> kth = kth_largest<kSelectThreads, false, uint32_t>(k, 2, each, sh.k32);
     above = unordered(kth.base + kth.range) + 2.f * delta;
     below = unordered(kth.base) - 2.f * delta;
     __syncthreads();  // the bins are free
   }
-  if (tid == 0) border_count = 0;
-  __syncthreads();
+  // page i's score exactly, as a number that orders like it
+  const float q_scale = scale_below(size), box_scale = scale_below(far);
+  auto exact = [&](int i) {
+    return odd ? ordered(odd_score<D>(a, b, hk, t, a.first + i, lane))
+               : static_cast<uint64_t>(fine_score<D>(a, b, hk, t, a.first + i, lane, q_scale, box_scale)) ^ (1ull << 63);
+  };
+  // a score next to the border is replaced by its number in the list, as the bits of a NaN
+  auto held = [](int at) { return __int_as_float(0x7fc00000 | at); };
   int sure = 0;
-  for (int i = tid; i < mid; i += kSelectThreads) {
-    const float x = score[i];
-    if (x > above && !odd) {
+  auto classify = [&](float& v, int at) {
+    if (!odd && v > above) {
       ++sure;
-    } else if (odd || x >= below) {
-      const int at = atomicAdd(&border_count, 1);
-      if (at < kBorder) sh.border.page[at] = i;
+    } else if (odd || v >= below) {
+      const int e = atomicAdd(&border_count, 1);
+      if (e < kBorder) {
+        sh.border.page[e] = at;
+        v = held(e);
+      }
     }
+  };
+#pragma unroll
+  for (int i = 0; i < kSelectRounds; ++i)
+    if (i * kSelectThreads + tid < mid) classify(x[i], i * kSelectThreads + tid);
+  for (int at = kHeld + tid; at < mid; at += kSelectThreads) {
+    float v = score[at];
+    classify(v, at);
   }
   sure = __reduce_add_sync(~0u, sure);
-  if (lane == 0) counts[0][warp] = sure;
+  if (lane == 0) counts[warp] = sure;
   __syncthreads();
   sure = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sure += counts[0][w];
+  for (int w = 0; w < kWarps; ++w) sure += counts[w];
   const int border = border_count, need = k - sure;  // need <= border
-  if (need == border) {
-    above = -INFINITY;  // all of them: whatever is not below
-  } else if (border <= kBorder) {
-    for (int i = warp; i < border; i += kWarps) {
-      const double x = fine_score<D>(a, b, hk, t, a.first + sh.border.page[i], lane);
-      if (lane == 0) sh.border.value[i] = x;
-    }
-    __syncthreads();
-    for (int i = tid; i < border; i += kSelectThreads) {
-      const double x = sh.border.value[i];
-      const int p = sh.border.page[i];
-      int rank = 0;
-      for (int j = 0; j < border; ++j) {
-        const double y = sh.border.value[j];
-        rank += y > x || (y == x && sh.border.page[j] < p);
+  if (border <= kBorder) {
+    if (need < border) {
+      for (int e = warp; e < border; e += kWarps) {
+        const uint64_t v = exact(sh.border.page[e]);
+        if (lane == 0) sh.border.value[e] = v;
       }
-      score[p] = rank < need ? INFINITY : -INFINITY;
+      __syncthreads();
+    }
+    for (int e = tid; e < border; e += kSelectThreads) {
+      const uint64_t v = sh.border.value[e];
+      const int p = sh.border.page[e];
+      int rank = 0;
+      if (need < border)
+        for (int j = 0; j < border; ++j) {
+          const uint64_t y = sh.border.value[j];
+          rank += y > v || (y == v && sh.border.page[j] < p);
+        }
+      sh.border.take[e] = rank < need;
+      if (p >= kHeld) score[p] = rank < need ? INFINITY : -INFINITY;
     }
     __syncthreads();
   } else {
-    // many equal or nearly equal pages (or something that is not finite): through memory
+    // many equal or nearly equal pages, or something that is not finite: through memory
+    uint64_t* fine = a.fine + static_cast<int64_t>(blockIdx.x) * a.max_pages + a.first;
+    auto here = [&](float v) { return odd || !(v > above || v < below); };
     for (int i = warp; i < mid; i += kWarps) {
-      const float x = score[i];
-      if (!odd && (x > above || x < below)) continue;
-      const double y = fine_score<D>(a, b, hk, t, a.first + i, lane);
+      if (!here(score[i])) continue;
+      const uint64_t y = exact(i);
       if (lane == 0) fine[i] = y;
     }
     __syncthreads();
-    const Kth<uint64_t> kth = kth_largest<kSelectThreads, uint64_t>(
-        mid, need, 64,
-        [&](int i, uint64_t& key) {
-          const float x = score[i];
-          if (!odd && (x > above || x < below)) return false;
-          key = ordered(fine[i]);
-          return true;
-        },
-        sh.k64);
+    auto each = [&](auto f) {
+      for (int i = tid; i < mid; i += kSelectThreads)
+        if (here(score[i])) f(fine[i]);
+    };
+    const Kth<uint64_t> kth = kth_largest<kSelectThreads, false, uint64_t>(need, 64, each, sh.k64);
     // in order, so that of equal ones the first are taken
     int taken = 0;
     for (int i0 = 0; i0 < mid; i0 += kSelectThreads) {
       const int i = i0 + tid;
-      const float x = i < mid ? score[i] : INFINITY;
-      const bool here = i < mid && (odd || !(x > above || x < below));
-      const uint64_t key = here ? ordered(fine[i]) : 0;
-      const bool tie = here && key >= kth.base && key - kth.base <= kth.range;
+      const bool in = i < mid && here(score[i]);
+      const uint64_t key = in ? fine[i] : 0;
+      const bool tie = in && kth.holds(key);
       const unsigned ties = __ballot_sync(~0u, tie);
-      if (lane == 0) counts[0][warp] = __popc(ties);
+      if (lane == 0) counts[warp] = __popc(ties);
       __syncthreads();
       int before = taken + __popc(ties & ((1u << lane) - 1u));
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += counts[0][w];
-        taken += counts[0][w];
+        if (w < warp) before += counts[w];
+        taken += counts[w];
       }
-      if (here) score[i] = (tie ? before < kth.need : key > kth.base) ? INFINITY : -INFINITY;
+      if (in) score[i] = (tie ? before < kth.need : kth.under(key)) ? INFINITY : -INFINITY;
       __syncthreads();
     }
-    if (odd) above = 3.402823466e38f;
-  }
-  // the pages in order: each warp has a stretch of them
-  const float least = need == border ? below : above;
-  auto in = [&](float x) { return need == border ? x >= least : x > least; };
-  const int per = (mid + kWarps * 32 - 1) / (kWarps * 32) * 32, w0 = min(mid, warp * per), w1 = min(mid, w0 + per);
-  int count = 0;
-  for (int i = w0; i < w1; i += 32)
-    count += __popc(__ballot_sync(~0u, i + lane < w1 && in(score[i + lane])));
-  if (lane == 0) counts[1][warp] = count;
-  __syncthreads();
-  int at = a.first;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (w < warp) at += counts[1][w];
-  for (int i = w0; i < w1; i += 32) {
-    const bool hit = i + lane < w1 && in(score[i + lane]);
-    const unsigned hits = __ballot_sync(~0u, hit);
-    const int to = at + __popc(hits & ((1u << lane) - 1u));
-    if (hit && to < a.top - a.last) out[to] = a.first + i + lane;  // always, while inputs stay
-    at += __popc(hits);
+    for (int i = 0; i < kSelectRounds; ++i)
+      if (i * kSelectThreads + tid < mid) x[i] = score[i * kSelectThreads + tid];
+  }
+  // the pages in order
+  Order<kSelectThreads, kSelectRounds> order{order_sh};
+  int done = a.first;
+  for (int r0 = 0; r0 < mid; r0 += kHeld) {
+    if (r0 > 0) {
+#pragma unroll
+      for (int i = 0; i < kSelectRounds; ++i) {
+        const int at = r0 + i * kSelectThreads + tid;
+        x[i] = at < mid ? score[at] : 0.f;
+      }
+    }
+    auto in = [&](int i) {
+      if (r0 + i * kSelectThreads + tid >= mid) return false;
+      const unsigned u = __float_as_uint(x[i]);
+      if (u - 0x7fc00000u < static_cast<unsigned>(kBorder)) return sh.border.take[u - 0x7fc00000u];
+      return x[i] > above;
+    };
+    auto no = [](int) { return false; };
+    const unsigned total = order.scan(in, no);
+#pragma unroll
+    for (int i = 0; i < kSelectRounds; ++i) {
+      const bool hit = in(i);
+      const int to = done + static_cast<int>(order.before(i, hit, false));
+      if (hit && to < a.top - a.last) out[to] = a.first + r0 + i * kSelectThreads + tid;  // always, while inputs stay
+    }
+    done += static_cast<int>(total);
+    __syncthreads();
   }
 }
 
@@ -503,12 +620,15 @@ template <int D>
 cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t s) {
   const int chunks = (a.max_pages + kScoreWarps * kScorePages - 1) / (kScoreWarps * kScorePages);
   const unsigned grid = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv) * static_cast<unsigned>(chunks);
-  if (grid > 0 && a.top > a.first + a.last) {
+  const bool scores = a.max_pages > a.top && a.top > a.first + a.last;  // else nobody chooses
+  if (scores) {
     const cudaError_t e = launch_chained(page_score_kernel<D>, grid, 32 * kScoreWarps, 0, s, a, chunks);
     if (e != cudaSuccess) return e;
   }
-  return launch_chained(select_pages_kernel<D>, static_cast<unsigned>(a.c.total) * static_cast<unsigned>(a.c.Hkv),
-                        kSelectThreads, 0, s, a);
+  const unsigned rows = static_cast<unsigned>(a.c.total) * static_cast<unsigned>(a.c.Hkv);
+  return a.max_pages <= kSelectRounds * 256
+             ? launch_chained(select_pages_kernel<D, 256>, rows, 256, 0, s, a, scores)
+             : launch_chained(select_pages_kernel<D, 1024>, rows, 1024, 0, s, a, scores);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

@@ -1,20 +1,54 @@
-// The k-th largest of a CTA's keys, by counting: each pass sorts the keys that are still in question
-// into 2048 equal bins and goes on with the bin that holds the k-th.  The bins divide the range that
-// the keys really have, so the first pass spreads them (the leading bits of floats that lie close
-// together are the same) and rarely more than two passes are needed.
+// The k-th largest of many keys held by a CTA or by the CTAs of a cluster, by counting, and the order
+// in which what was selected is listed.
+//
+// Each pass sorts the keys that are still in question into 2048 equal bins and goes on with the bin
+// that holds the k-th.  The bins divide the range that the keys really have, so the first pass
+// spreads them (the leading bits of floats that lie close together are the same) and rarely more
+// than two passes are needed.  A cluster's CTAs add up each other's bins through distributed shared
+// memory, one cluster barrier a pass.
 #pragma once
 
 #include <cstdint>
 
+#include "sm103.cuh"
+
 namespace fa {
+
+// ---- the CTAs of a cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of all its CTAs.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared-memory words of CTA `rank`, at the address that `p` has here.
+__device__ __forceinline__ uint2 peer_load2(const void* p, uint32_t rank) {
+  uint2 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.u32 {%0, %1}, [a];\n\t}"
+      : "=r"(v.x), "=r"(v.y)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
 
 constexpr int kKthBins = 2048;
 
 template <int kThreads, typename Key>
 struct KthShared {
-  unsigned hist[kKthBins];
+  alignas(8) unsigned hist[2][kKthBins];
+  alignas(8) Key lo[kThreads / 32], hi[kThreads / 32];  // of the warps; [0]: then of the CTA
+  alignas(8) Key ends[2];                               // smallest and largest of the CTA
   unsigned warp_sum[kThreads / 32];
-  Key lo[kThreads / 32], hi[kThreads / 32];
   int bin, need, count;
 };
 
@@ -24,27 +58,29 @@ template <typename Key>
 struct Kth {
   Key base, range;
   int need, count;
+  __device__ bool holds(Key key) const { return key >= base && key - base <= range; }
+  __device__ bool under(Key key) const { return key > base && key - base > range; }
 };
 
 __device__ __forceinline__ int bit_length(uint32_t x) { return 32 - __clz(x); }
 __device__ __forceinline__ int bit_length(uint64_t x) { return 64 - __clzll(x); }
 
-// load(i, key): whether element i < n counts, and its key.  1 <= k <= number that count.  Ends when
-// every key of the range is needed, when the range is one key, or after max_passes.  Called by all
-// kThreads threads; sh may be used again after the next barrier.
-template <int kThreads, typename Key, typename Load>
-__device__ Kth<Key> kth_largest(int n, int k, int max_passes, Load load, KthShared<kThreads, Key>& sh) {
+// each(f) calls f(key) for every key of this thread.  1 <= k <= number of keys.  Ends when every key
+// of the range is needed, when the range is one key, or after max_passes.  Called by all threads of
+// the CTA, or (kCluster, 32-bit keys) of the cluster; sh may be used again after the next barrier.
+template <int kThreads, bool kCluster, typename Key, typename Each>
+__device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each,
+                                                KthShared<kThreads, Key>& sh) {
+  static_assert(!kCluster || sizeof(Key) == 4, "peers are read in pairs of words");
   constexpr int kWarps = kThreads / 32, kOwn = kKthBins / kThreads;
-  static_assert(kOwn >= 1 && kOwn * kThreads == kKthBins, "bins per thread");
+  static_assert(kOwn % 2 == 0 && kOwn * kThreads == kKthBins, "bins per thread, in pairs");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t peers = kCluster ? cluster_size() : 1;
   Key lo = ~Key(0), hi = 0;
-  for (int i = tid; i < n; i += kThreads) {
-    Key key;
-    if (load(i, key)) {
-      lo = key < lo ? key : lo;
-      hi = key > hi ? key : hi;
-    }
-  }
+  each([&](Key key) {
+    lo = key < lo ? key : lo;
+    hi = key > hi ? key : hi;
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const Key l = __shfl_xor_sync(~0u, lo, o), h = __shfl_xor_sync(~0u, hi, o);
@@ -55,29 +91,52 @@ __device__ Kth<Key> kth_largest(int n, int k, int max_passes, Load load, KthShar
     sh.lo[warp] = lo;
     sh.hi[warp] = hi;
   }
+#pragma unroll
+  for (int i = 0; i < 2 * kOwn; ++i) (&sh.hist[0][0])[i * kThreads + tid] = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     lo = sh.lo[w] < lo ? sh.lo[w] : lo;
     hi = sh.hi[w] > hi ? sh.hi[w] : hi;
   }
+  if constexpr (kCluster) {
+    if (tid == 0) {
+      sh.ends[0] = lo;
+      sh.ends[1] = hi;
+    }
+    cluster_sync();
+    for (uint32_t p = 0; p < peers; ++p) {
+      const uint2 v = peer_load2(&sh.ends[0], p);
+      lo = v.x < lo ? v.x : lo;
+      hi = v.y > hi ? v.y : hi;
+    }
+  }
   Kth<Key> r{lo, hi - lo, k, -1};
   for (int pass = 0; pass < max_passes; ++pass) {
     const int bits = bit_length(r.range), shift = bits > 11 ? bits - 11 : 0;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) sh.hist[i * kThreads + tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      Key key;
-      if (load(i, key) && key >= r.base && key - r.base <= r.range)
-        atomicAdd(&sh.hist[static_cast<unsigned>((key - r.base) >> shift)], 1u);
-    }
-    __syncthreads();
-    // thread t owns the bins [own0, own0 + kOwn), counted from the top
+    // two sets of bins take turns: this one is empty, and the other is cleared once nobody reads it
+    unsigned* const hist = sh.hist[pass & 1];
+    each([&](Key key) {
+      if (r.holds(key)) atomicAdd(&hist[static_cast<unsigned>((key - r.base) >> shift)], 1u);
+    });
+    if constexpr (kCluster) cluster_sync();
+    else __syncthreads();
+    // thread t owns the kOwn bins from own0 down, counted from the top
     unsigned mine[kOwn], sum = 0;
     const int own0 = kKthBins - 1 - tid * kOwn;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) sum += mine[i] = sh.hist[own0 - i];
+    for (int i = 0; i < kOwn; ++i) mine[i] = 0;
+    for (uint32_t p = 0; p < peers; ++p)
+#pragma unroll
+      for (int i = 0; i < kOwn; i += 2) {
+        uint2 v;
+        if constexpr (kCluster) v = peer_load2(&hist[own0 - i - 1], p);
+        else v = *reinterpret_cast<const uint2*>(&hist[own0 - i - 1]);
+        mine[i] += v.y;
+        mine[i + 1] += v.x;
+      }
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) sum += mine[i];
     unsigned incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -100,6 +159,10 @@ __device__ Kth<Key> kth_largest(int n, int k, int max_passes, Load load, KthShar
       }
       above += mine[i];
     }
+    if (pass > 0) {  // read by others before this pass' barrier; filled after the next one
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) sh.hist[(pass & 1) ^ 1][i * kThreads + tid] = 0;
+    }
     __syncthreads();
     const Key step = static_cast<Key>(sh.bin) << shift;
     r.base += step;
@@ -107,9 +170,59 @@ __device__ Kth<Key> kth_largest(int n, int k, int max_passes, Load load, KthShar
     r.range = left < width ? left : width;
     r.need = sh.need;
     r.count = sh.count;
-    if (shift == 0 || r.need == r.count) break;  // uniform
+    if (shift == 0 || r.need == r.count) break;  // the same everywhere
   }
   return r;
 }
+
+// Places in order: element (i, thread) of a CTA's kRounds x kThreads elements, rounds first, has
+// `over` elements above the k-th and `tie` ones in its range in front of it.
+template <int kThreads, int kRounds>
+struct OrderShared {
+  unsigned count[kRounds * kThreads / 32];  // over, tie << 16 of each round and warp
+  unsigned warp_sum[kThreads / 32];
+};
+template <int kThreads, int kRounds>
+struct Order {
+  static constexpr int kWarps = kThreads / 32, kEntries = kRounds * kWarps;
+  static_assert(kEntries <= kThreads && kRounds * kThreads < 65536, "a thread an entry, 16 bits a count");
+  OrderShared<kThreads, kRounds>& sh;
+
+  // over(i), tie(i): of this thread's element of round i.  Returns the totals (tie << 16).
+  template <typename Over, typename Tie>
+  __device__ __forceinline__ unsigned scan(Over over, Tie tie) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const unsigned o = __ballot_sync(~0u, over(i)), t = __ballot_sync(~0u, tie(i));
+      if (lane == 0) sh.count[i * kWarps + warp] = __popc(o) | __popc(t) << 16;
+    }
+    __syncthreads();
+    const unsigned own = tid < kEntries ? sh.count[tid] : 0u;
+    unsigned incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    unsigned total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) incl += sh.warp_sum[w];
+      total += sh.warp_sum[w];
+    }
+    if (tid < kEntries) sh.count[tid] = incl - own;
+    __syncthreads();
+    return total;
+  }
+  // (over, tie << 16) in front of this thread's element of round i; called by whole warps.
+  __device__ __forceinline__ unsigned before(int i, bool over, bool tie) const {
+    const unsigned lane = threadIdx.x & 31, less = (1u << lane) - 1u;
+    const unsigned o = __ballot_sync(~0u, over), t = __ballot_sync(~0u, tie);
+    return sh.count[i * kWarps + (threadIdx.x >> 5)] + (__popc(o & less) | __popc(t & less) << 16);
+  }
+};
 
 }  // namespace fa

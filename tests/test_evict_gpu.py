@@ -194,9 +194,13 @@ def test_evict(lens, budget, shape):
         Evicted(lens, *shape, budget, sum(lens) + recent).check(recent)
 
 
-def test_evict_of_a_long_sequence():
-    Evicted([70001], 2, 64, 16, 9000, 1).check(100)
-    Evicted([70001], 2, 64, 16, 69999, 2).check(5)
+@pytest.mark.parametrize("n", [4096, 4097, 16384, 16385, 40000, 70001, 131072, 131073, 200001])
+def test_evict_of_a_long_sequence(n):
+    """A CTA's registers, a cluster's, and more than a cluster holds; next to a short sequence."""
+    for budget, recent in ((9, 3), (n // 5, 100), (n - 2, 5)):
+        Evicted([n, 50], 1, 64, 16, budget, n + budget).check(min(recent, budget), max_kv=n)
+    few = torch.randint(0, 3, (1, 1, n), generator=torch.Generator().manual_seed(n)).float()
+    Evicted([n], 1, 64, 16, n // 2, n, few).check(0)  # ties all along
 
 
 def test_evict_of_equal_zero_and_odd_weights():
