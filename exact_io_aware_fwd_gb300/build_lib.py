@@ -34,7 +34,7 @@ BINDING_PATH = binding_path(torch.__version__, sysconfig.get_config_var("EXT_SUF
 BINDING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_dq.cu", "fa_block_sparse.cu", "fa_noalloc.cu",
            "fa_serving.cu", "fa_rope.cu", "fa_paged.cu", "fa_paged_mma.cu", "fa_cache.cu", "fa_pages.cu",
-           "fa_evict.cu"]
+           "fa_weights.cu", "fa_evict.cu"]
 HEADERS = [os.path.join(CSRC, "sm103.cuh"), os.path.join(CSRC, "fa_internal.h"),
            os.path.join(CSRC, "fa_host.h"), os.path.join(CSRC, "fa_paged.h"),
            os.path.join(CSRC, "paged_plan.cuh"), os.path.join(CSRC, "paged_rows.cuh"),

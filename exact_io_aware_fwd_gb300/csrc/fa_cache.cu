@@ -149,24 +149,34 @@ fa_status fa_kv_weights(const void* Q, const float* LSE, const fa_paged_kv* cach
     return FA_ERR_INVALID_ARG;
   if (capacity == 0) return FA_OK;
   if (!out || (total > 0 && (!Q || !LSE || !aligned_to(Q, 16)))) return FA_ERR_INVALID_ARG;
-  // rows of a sequence's queries, and the blocks of the launch
-  if (!fits(total, H, 1) || !fits(B, Hkv, capacity / 128 + 1)) return FA_ERR_UNSUPPORTED;
-  fa::WeightsArgs a{};
-  int* status = nullptr;
-  if ((st = device_ready(status)) != FA_OK) return st;
-  a.c = seqs_of(*cache, cu_seqlens, B, total, max_kv < capacity ? max_kv : capacity, Hkv, status);
+  // the index of a (token, head) row, and the units of the launch
+  const int len = max_kv < capacity ? max_kv : capacity;
+  if (!fits(total, H, 1) || static_cast<long long>(total) * (H / Hkv) > fa::kWeightsRows ||
+      !fits(B, Hkv, len / 128 + 1) || static_cast<long long>(cache->num_pages) * Hkv > kMaxInt)
+    return FA_ERR_UNSUPPORTED;
+  fa::PagedArgs a{};
+  if ((st = device_ready(a.status)) != FA_OK) return st;
+  CUtensorMap tk;
+  if (!fa::make_pool_map(&tk, cache->k_cache, *cache, Hkv, d)) return FA_ERR_CUDA;
   a.q = static_cast<const __nv_bfloat16*>(Q);
-  a.k_cache = static_cast<const __nv_bfloat16*>(cache->k_cache);
-  a.lse = LSE;
-  a.in = weights;
-  a.out = out;
-  a.cap = capacity;
+  a.cu = cu_seqlens;
+  a.B = B;
+  a.total = total;
   a.H = H;
+  a.Hkv = Hkv;
   a.G = H / Hkv;
-  a.max_q = max_q;
-  a.causal = causal != 0;
+  a.num_pages = cache->num_pages;
+  a.page_shift = page_shift(cache->page_size);
   a.scale_log2 = fa::resolve_scale(scale, d) * kLog2e;
-  return status_of(fa::launch_kv_weights(d, a, static_cast<cudaStream_t>(stream)));
+  fa::KeyList& l = a.list[0];
+  l.count = B;
+  l.lens = cache->kv_lens;
+  l.table = cache->block_table;
+  l.max_pages = cache->max_pages;
+  l.max_len = len;
+  l.max_q = max_q;
+  const fa::WeightsOut w{LSE, weights, out, capacity, causal != 0};
+  return status_of(fa::launch_kv_weights(d, tk, a, w, fa::wait_timeout_ns(), static_cast<cudaStream_t>(stream)));
 }
 
 fa_status fa_kv_evict(const float* weights, int capacity, const fa_paged_kv* cache,

@@ -1,6 +1,6 @@
 // Internal interface of the operators that choose and drop keys of the paged cache: the bounds of
-// pages and the selection of pages for each query (fa_pages.cu), accumulated attention weights and
-// eviction (fa_evict.cu).
+// pages and the selection of pages for each query (fa_pages.cu), accumulated attention weights
+// (fa_weights.cu) and eviction (fa_evict.cu).
 #pragma once
 
 #include <cstddef>
@@ -83,18 +83,18 @@ struct SelectWorkspace {
 SelectWorkspace select_workspace(int B, int total, int Hkv, int max_pages);
 cudaError_t launch_select_pages(int d, const SelectArgs& a, cudaStream_t s);
 
-// ---- accumulated weights and eviction (fa_evict.cu)
-struct WeightsArgs {
-  CacheSeqs c;
-  const __nv_bfloat16 *q, *k_cache;
+// ---- accumulated weights (fa_weights.cu): the sequences and queries are those of a PagedArgs with
+// one list, whose causal is 0 (every key is visited)
+struct WeightsOut {
   const float *lse, *in;  // in: nullptr or [B][Hkv][cap]
   float* out;             // [B][Hkv][cap]
-  int cap;
-  int H, G, max_q, causal;
-  float scale_log2;
+  int cap, causal;
 };
-cudaError_t launch_kv_weights(int d, const WeightsArgs& a, cudaStream_t s);
+constexpr long long kWeightsRows = 1 << 29;  // queries of a launch for a key/value head
+cudaError_t launch_kv_weights(int d, const CUtensorMap& tk, const PagedArgs& a, const WeightsOut& w,
+                              uint64_t timeout_ns, cudaStream_t s);
 
+// ---- eviction (fa_evict.cu)
 struct EvictArgs {
   CacheSeqs c;
   const float* weights;   // [B][Hkv][cap]

@@ -1,113 +1,12 @@
-// Attention weights summed over queries, and the eviction of the keys that have gathered least.
+// Eviction of the keys that have gathered the least attention.
 #include "fa_cache.h"
 #include "fa_internal.h"
-#include "paged_rows.cuh"
 #include "select_kth.cuh"
 #include "sm103.cuh"
 
 namespace fa {
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// ---- weights
-// out_j = in_j + sum over a key/value head's queries of exp(scale q.k_j - LSE): the probabilities
-// that attention used, from the LSE it left, so one product instead of two and no maximum to keep.
-// Keys do not depend on each other: a warp takes 32 of them as the columns of an m16n8k16 product
-// and goes through the query rows 16 at a time; what a lane adds up stays its own until the end.
-// Keys are loaded 16 bytes a lane straight into fragments (page_score_kernel's order of k).
-constexpr int kWeightWarps = 4, kWeightKeys = 32;
-
-template <int D>
-__global__ void __launch_bounds__(32 * kWeightWarps) kv_weights_kernel(const WeightsArgs a, int chunks) {
-  constexpr int J = D / 32, T = kWeightKeys / 8;
-  begin_launch();
-  const CacheSeqs& c = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bh = static_cast<int>(blockIdx.x) / chunks, chunk = static_cast<int>(blockIdx.x) % chunks;
-  const int b = bh / c.Hkv, hk = bh - b * c.Hkv;
-  const int k0 = (chunk * kWeightWarps + warp) * kWeightKeys;
-  if (k0 >= a.cap) return;
-  const int len = keys_of(c, b, threadIdx.x == 0 && chunk == 0 && hk == 0);
-  const int64_t row = static_cast<int64_t>(bh) * a.cap;
-  if (k0 >= len) {  // no keys: what there was
-    const int key = k0 + lane;
-    if (a.in != a.out && key < a.cap) a.out[row + key] = a.in != nullptr ? a.in[row + key] : 0.f;
-    return;
-  }
-  int start, n;
-  token_bounds(c.cu, b, c.total, start, n);
-  const int nc = min(n, a.max_q);
-  if (nc < n && threadIdx.x == 0 && chunk == 0 && hk == 0) atomicCAS(c.status, 0, kErrIndex);
-  uint4 kf[T][J];
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-    const int key = k0 + 8 * t + (lane >> 2);
-    const int phys = key < len ? page_of(c, b, key >> c.page_shift) : -1;
-    const uint4* src = reinterpret_cast<const uint4*>(
-                           a.k_cache + (((static_cast<int64_t>(max(phys, 0)) * c.Hkv + hk) << c.page_shift) +
-                                        (key & ((1 << c.page_shift) - 1))) * D) + (lane & 3);
-#pragma unroll
-    for (int j = 0; j < J; ++j) kf[t][j] = phys >= 0 ? __ldg(src + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  float sum[T][2] = {};
-  const int rows = nc * a.G, shift = len - n;
-  for (int r0 = 0; r0 < rows; r0 += 16) {
-    const uint4* q[2];
-    float off[2];  // LSE in log2 units
-    int lim[2];    // keys below it are visible to the row
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = r0 + (lane >> 2) + 8 * i;
-      const bool live = rr < rows;
-      const int tok = live ? rr / a.G : 0, head = hk * a.G + (live ? rr - tok * a.G : 0);
-      q[i] = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(start + tok) * a.H + head) * D) + (lane & 3);
-      const float lse = __ldg(a.lse + static_cast<int64_t>(head) * c.total + start + tok);
-      off[i] = lse == -INFINITY ? INFINITY : lse * kLog2e;  // a row without keys weighs nothing
-      lim[i] = !live ? 0 : (a.causal ? min(len, shift + tok + 1) : len);
-    }
-    float s[T][4];
-#pragma unroll
-    for (int t = 0; t < T; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const uint4 v0 = __ldg(q[0] + 4 * j), v1 = __ldg(q[1] + 4 * j);
-      const uint32_t f0[4] = {v0.x, v1.x, v0.y, v1.y}, f1[4] = {v0.z, v1.z, v0.w, v1.w};
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        rows16::mma16816(s[t], f0, kf[t][j].x, kf[t][j].y);
-        rows16::mma16816(s[t], f1, kf[t][j].z, kf[t][j].w);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int key = k0 + 8 * t + (lane & 3) * 2 + (k & 1);
-        const float p = ex2(fmaf(s[t][k], a.scale_log2, -off[k >> 1]));
-        if (key < lim[k >> 1]) sum[t][k & 1] += p;
-      }
-  }
-#pragma unroll
-  for (int t = 0; t < T; ++t)
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) sum[t][k] += __shfl_xor_sync(~0u, sum[t][k], o);
-  // lane l writes key l: column l % 8 of tile l / 8 is with the lanes of (l % 8) / 2
-  float mine = 0.f;
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-    const float x = __shfl_sync(~0u, sum[t][0], (lane & 7) >> 1), y = __shfl_sync(~0u, sum[t][1], (lane & 7) >> 1);
-    if (lane >> 3 == t) mine = lane & 1 ? y : x;
-  }
-  const int key = k0 + lane;
-  if (key < a.cap) {
-    const float was = a.in != nullptr ? a.in[row + key] : 0.f;
-    a.out[row + key] = key < len ? was + mine : was;
-  }
-}
 
 // ---- eviction: which keys stay
 // The smallest weight that stays by counting (select_kth.cuh), then the keys in order.  A sequence
@@ -267,14 +166,6 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 }
 
 }  // namespace
-
-cudaError_t launch_kv_weights(int d, const WeightsArgs& a, cudaStream_t s) {
-  constexpr int kCta = kWeightWarps * kWeightKeys;
-  const int chunks = (a.cap + kCta - 1) / kCta;
-  const unsigned grid = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv) * static_cast<unsigned>(chunks);
-  return d == 64 ? launch_chained(kv_weights_kernel<64>, grid, 32 * kWeightWarps, 0, s, a, chunks)
-                 : launch_chained(kv_weights_kernel<128>, grid, 32 * kWeightWarps, 0, s, a, chunks);
-}
 
 cudaError_t launch_kv_evict(int d, const EvictArgs& a, cudaStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv);

@@ -18,6 +18,7 @@ using fa::check_heads;
 using fa::device_ready;
 using fa::kMaxInt;
 using fa::kMaxKeys;
+using fa::make_pool_map;
 using fa::page_shift;
 using fa::status_of;
 using fa::up256;
@@ -54,22 +55,6 @@ void set_transform(fa::RopeArgs& a, const fa_qk_transform& t) {
   a.wq = t.q_weight;
   a.wk = t.k_weight;
   a.eps = t.eps;
-}
-
-// Cache pool as a 3-D tensor (d, page_size, pages x heads): boxes of one page x 64 columns with
-// the 128-byte swizzle.  The coordinate num_pages * Hkv lies outside and reads as zeros.
-bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int Hkv, int d) {
-  auto fn = fa::encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t page = static_cast<cuuint64_t>(c.page_size);
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), page,
-                        static_cast<cuuint64_t>(c.num_pages) * static_cast<cuuint64_t>(Hkv)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, page * static_cast<cuuint64_t>(d) * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(c.page_size), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Query rows per key/value head above which a list goes to the tensor-core kernel.  The other

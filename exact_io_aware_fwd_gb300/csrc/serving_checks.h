@@ -61,6 +61,22 @@ inline fa_status check_cache(const fa_paged_kv* c, bool keys = true, bool values
 
 inline fa_status status_of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
+// Cache pool as a 3-D tensor (d, page_size, pages x heads): boxes of one page x 64 columns with
+// the 128-byte swizzle.  The coordinate num_pages * Hkv lies outside and reads as zeros.
+inline bool make_pool_map(CUtensorMap* m, const void* base, const fa_paged_kv& c, int Hkv, int d) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t page = static_cast<cuuint64_t>(c.page_size);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), page,
+                        static_cast<cuuint64_t>(c.num_pages) * static_cast<cuuint64_t>(Hkv)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, page * static_cast<cuuint64_t>(d) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(c.page_size), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace fa

@@ -75,6 +75,34 @@ def test_weights(nq, lens, causal, heads):
     assert fa.fa_get_error() == fa.FA_OK
 
 
+@pytest.mark.parametrize("heads", [(8, 2, 128, 64), (4, 2, 64, 16), (16, 1, 64, 32)], ids=lambda h: "H%dkv%dd%dpage%d" % h)
+@pytest.mark.parametrize("causal", [False, True], ids=["all", "causal"])
+def test_weights_of_many_queries_and_of_many_sequences(heads, causal):
+    """Several jobs of 128 queries a piece, shares that end inside sequences, and many pieces a CTA."""
+    for nq, lens in (([100, 7, 130], [700, 129, 131]), ([33], [20000]), ([1, 0, 2] * 50, [300, 0, 40] * 50),
+                     ([1, 0, 0, 0, 0, 0, 1], [9, 0, 0, 50, 0, 0, 400])):
+        w = Weighted(nq, lens, heads, causal, sum(lens) + heads[0])
+        before = w.before.to(DEV)
+        w.check(fa.fa_kv_weights(*w.args(), before, **w.opts()), w.before)
+        w.check(fa.fa_kv_weights(*w.args(), before, out=before, **w.opts()), w.before)
+        assert fa.fa_get_error() == fa.FA_OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_time_out_and_recover(d, monkeypatch):
+    """Waits of the pipeline that run out end the kernel, the call reports it, and the next call is
+    right again (no fault, nothing left behind)."""
+    w = Weighted([200, 90], [1500, 700], (4, 2, d, 32), True, 3)
+    args, opts = w.args(), w.opts()
+    monkeypatch.setenv("FA_WAIT_TIMEOUT_US", "1")
+    fa.fa_kv_weights(*args, **opts)
+    status = fa.fa_get_error()
+    monkeypatch.delenv("FA_WAIT_TIMEOUT_US")
+    assert status == fa.FA_ERR_TIMEOUT, fa.fa_status_string(status)
+    w.check(fa.fa_kv_weights(*args, **opts), None)
+    assert fa.fa_get_error() == fa.FA_OK
+
+
 def test_weights_of_large_logits_and_after_the_attention_call():
     w = Weighted([2, 1], [500, 300], (8, 2, 128, 16), True, 3, sigma=4.0)
     w.check(fa.fa_kv_weights(*w.args(), **w.opts()), None)
