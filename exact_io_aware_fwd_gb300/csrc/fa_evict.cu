@@ -13,15 +13,17 @@ namespace {
 // and head is a CTA's, or, where a CTA's registers (kRounds weights a thread) do not hold its
 // weights, a cluster's, each CTA with a stretch of them; only what does not fit eight CTAs is read
 // again in every pass.
-constexpr int kRounds = 16;
-constexpr int evict_cluster(int max_len, int threads) {
-  int c = 1;
-  while (c < 8 && c * kRounds * threads < max_len) c *= 2;
+constexpr int kRounds = 8, kClusterRounds = 16;
+constexpr int kClusterThreads = 1024;
+constexpr int evict_cluster(int max_len) {
+  int c = 2;
+  while (c < static_cast<int>(kMostPeers) && c * kClusterRounds * kClusterThreads < max_len) c *= 2;
   return c;
 }
 
-template <int kThreads, bool kCluster>
+template <int kThreads, int kRounds, bool kCluster>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs a) {
+  constexpr int kHeld = kRounds * kThreads;
   __shared__ KthShared<kThreads, uint32_t> sh;
   __shared__ OrderShared<kThreads, kRounds> order_sh;
   __shared__ alignas(8) unsigned totals[2];  // above the k-th, in its range
@@ -38,14 +40,21 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
   float* left = a.new_weights + static_cast<int64_t>(row) * a.budget;
   const int old = len > a.budget ? len - a.recent : 0;  // keys that are chosen from
   const int k = count - (len - old);                    // and how many of them stay
-  // this CTA's stretch, its first kRounds rounds in registers
+  // this CTA's stretch; what its registers hold, as numbers that order like the weights
   const int chunk = (old + ctas - 1) / ctas, c0 = min(old, rank * chunk), c1 = min(old, c0 + chunk);
-  float x[kRounds];
+  // (0, which no weight gives, where there is none).  All loads are on the way before the first is
+  // used.
+  uint32_t x[kRounds];
+  auto read = [&](int r0) {
+    float v[kRounds];
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int at = c0 + i * kThreads + tid;
-    x[i] = at < c1 ? w[at] : 0.f;
-  }
+    for (int i = 0; i < kRounds; ++i) v[i] = w[max(min(r0 + i * kThreads + tid, c1 - 1), 0)];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) asm volatile("" : "+f"(v[i]));
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) x[i] = r0 + i * kThreads + tid < c1 ? ordered(v[i]) : 0u;
+  };
+  if (k > 0) read(c0);
   for (int i = count + all; i < a.budget; i += ctas * kThreads) {
     kept[i] = -1;
     left[i] = 0.f;
@@ -55,57 +64,58 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     left[k + i - old] = w[i];
   }
   if (k == 0) return;  // the whole cluster
+  auto tail = [&](auto f) {
+    for (int at = c0 + kHeld + tid; at < c1; at += kThreads) f(ordered(w[at]));
+  };
   auto each = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < kRounds; ++i)
-      if (c0 + i * kThreads + tid < c1) f(ordered(x[i]));
-    for (int at = c0 + kRounds * kThreads + tid; at < c1; at += kThreads) f(ordered(w[at]));
+      if (x[i] != 0u) f(x[i]);
+    tail(f);
   };
   const Kth<uint32_t> kth = kth_largest<kThreads, kCluster, uint32_t>(k, 32, each, sh);
-  unsigned over0 = 0, tie0 = 0;  // in front of this CTA's stretch
-  if constexpr (kCluster) {
-    if (tid == 0) totals[0] = totals[1] = 0;
-    __syncthreads();
-    unsigned over = 0, tie = 0;
-    each([&](uint32_t key) {
-      over += kth.under(key);
-      tie += kth.holds(key);
-    });
-    over = __reduce_add_sync(~0u, over);
-    tie = __reduce_add_sync(~0u, tie);
-    if ((tid & 31) == 0) {
-      atomicAdd(&totals[0], over);
-      atomicAdd(&totals[1], tie);
-    }
-    cluster_sync();
-    for (int p = 0; p < rank; ++p) {
-      const uint2 v = peer_load2(totals, p);
-      over0 += v.x;
-      tie0 += v.y;
-    }
-  }
   Order<kThreads, kRounds> order{order_sh};
-  for (int r0 = c0; r0 < c1; r0 += kRounds * kThreads) {
-    if (r0 > c0) {
-#pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int at = r0 + i * kThreads + tid;
-        x[i] = at < c1 ? w[at] : 0.f;
+  unsigned over0 = 0, tie0 = 0;  // in front of what comes next
+  for (int r0 = c0; r0 == c0 || r0 < c1; r0 += kHeld) {
+    if (r0 > c0) read(r0);
+    const unsigned total = order.scan([&](int i) { return kth.under(x[i]); }, [&](int i) { return kth.holds(x[i]); });
+    if constexpr (kCluster) {
+      if (r0 == c0) {  // what the CTAs in front have
+        if (tid == 0) {
+          totals[0] = total & 0xffffu;
+          totals[1] = total >> 16;
+        }
+        __syncthreads();
+        if (c1 - c0 > kHeld) {
+          unsigned over = 0, tie = 0;
+          tail([&](uint32_t key) {
+            over += kth.under(key);
+            tie += kth.holds(key);
+          });
+          over = __reduce_add_sync(~0u, over);
+          tie = __reduce_add_sync(~0u, tie);
+          if ((tid & 31) == 0) {
+            atomicAdd(&totals[0], over);
+            atomicAdd(&totals[1], tie);
+          }
+        }
+        cluster_sync();
+        for (int p = 0; p < rank; ++p) {
+          const uint2 v = peer_load2(totals, p);
+          over0 += v.x;
+          tie0 += v.y;
+        }
       }
     }
-    auto there = [&](int i) { return r0 + i * kThreads + tid < c1; };
-    auto over = [&](int i) { return there(i) && kth.under(ordered(x[i])); };
-    auto tie = [&](int i) { return there(i) && kth.holds(ordered(x[i])); };
-    const unsigned total = order.scan(over, tie);
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
-      const bool o = over(i), t = tie(i);
-      const unsigned before = order.before(i, o, t);
+      const unsigned before = order.before(i);
       const int ties = static_cast<int>(tie0 + (before >> 16));
       const int at = static_cast<int>(over0 + (before & 0xffffu)) + min(ties, kth.need);
-      if ((o || (t && ties < kth.need)) && at < k) {  // at < k: always, while nobody writes the weights
+      // at < k: always, while nobody writes the weights
+      if ((order.over(i) || (order.tie(i) && ties < kth.need)) && at < k) {
         kept[at] = r0 + i * kThreads + tid;
-        left[at] = x[i];
+        left[at] = unordered(x[i]);
       }
     }
     over0 += total & 0xffffu;
@@ -170,11 +180,13 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 cudaError_t launch_kv_evict(int d, const EvictArgs& a, cudaStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv);
   const int most = a.c.max_len;
-  const int cluster = evict_cluster(most, 1024);
-  const cudaError_t e =
-      most <= kRounds * 256 ? launch_chained(evict_select_kernel<256, false>, rows, 256, 0, s, a)
-      : cluster == 1 ? launch_chained(evict_select_kernel<1024, false>, rows, 1024, 0, s, a)
-                     : launch_clusters(evict_select_kernel<1024, true>, rows * cluster, cluster, 1024, s, a);
+  const int cluster = evict_cluster(most);
+  cudaError_t e = most <= kRounds * 256   ? launch_chained(evict_select_kernel<256, kRounds, false>, rows, 256, 0, s, a)
+                  : most <= 16 * 256 ? launch_chained(evict_select_kernel<256, 16, false>, rows, 256, 0, s, a)
+                  : most <= kRounds * 1024
+                      ? launch_chained(evict_select_kernel<1024, kRounds, false>, rows, 1024, 0, s, a)
+                      : launch_clusters(evict_select_kernel<kClusterThreads, kClusterRounds, true>, rows * cluster,
+                                        cluster, kClusterThreads, s, a);
   if (e != cudaSuccess) return e;
   const int chunks = (a.budget + kMoveKeys - 1) / kMoveKeys;
   return d == 64 ? launch_chained(evict_move_kernel<64>, rows * chunks, kMoveThreads, 0, s, a, chunks)

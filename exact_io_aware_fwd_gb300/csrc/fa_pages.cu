@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     const unsigned total = order.scan(in, no);
 #pragma unroll
     for (int i = 0; i < kSelectRounds; ++i) {
-      const bool hit = in(i);
-      const int to = done + static_cast<int>(order.before(i, hit, false));
+      const bool hit = order.over(i);
+      const int to = done + static_cast<int>(order.before(i));
       if (hit && to < a.top - a.last) out[to] = a.first + r0 + i * kSelectThreads + tid;  // always, while inputs stay
     }
     done += static_cast<int>(total);

@@ -42,6 +42,7 @@ __device__ __forceinline__ uint2 peer_load2(const void* p, uint32_t rank) {
 }
 
 constexpr int kKthBins = 2048;
+constexpr uint32_t kMostPeers = 8;  // CTAs of a cluster
 
 template <int kThreads, typename Key>
 struct KthShared {
@@ -58,8 +59,8 @@ template <typename Key>
 struct Kth {
   Key base, range;
   int need, count;
-  __device__ bool holds(Key key) const { return key >= base && key - base <= range; }
-  __device__ bool under(Key key) const { return key > base && key - base > range; }
+  __device__ bool holds(Key key) const { return key - base <= range; }  // (a smaller key wraps)
+  __device__ bool under(Key key) const { return key > base + range; }
 };
 
 __device__ __forceinline__ int bit_length(uint32_t x) { return 32 - __clz(x); }
@@ -105,36 +106,46 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
       sh.ends[1] = hi;
     }
     cluster_sync();
-    for (uint32_t p = 0; p < peers; ++p) {
-      const uint2 v = peer_load2(&sh.ends[0], p);
-      lo = v.x < lo ? v.x : lo;
-      hi = v.y > hi ? v.y : hi;
-    }
+    const uint2 v = peer_load2(&sh.ends[0], min(static_cast<uint32_t>(lane), peers - 1));
+    lo = __reduce_min_sync(~0u, v.x);
+    hi = __reduce_max_sync(~0u, v.y);
   }
   Kth<Key> r{lo, hi - lo, k, -1};
   for (int pass = 0; pass < max_passes; ++pass) {
     const int bits = bit_length(r.range), shift = bits > 11 ? bits - 11 : 0;
     // two sets of bins take turns: this one is empty, and the other is cleared once nobody reads it
     unsigned* const hist = sh.hist[pass & 1];
-    each([&](Key key) {
-      if (r.holds(key)) atomicAdd(&hist[static_cast<unsigned>((key - r.base) >> shift)], 1u);
-    });
+    if (pass == 0) {
+      each([&](Key key) { atomicAdd(&hist[static_cast<unsigned>((key - r.base) >> shift)], 1u); });
+    } else {
+      each([&](Key key) {
+        if (r.holds(key)) atomicAdd(&hist[static_cast<unsigned>((key - r.base) >> shift)], 1u);
+      });
+    }
     if constexpr (kCluster) cluster_sync();
     else __syncthreads();
     // thread t owns the kOwn bins from own0 down, counted from the top
     unsigned mine[kOwn], sum = 0;
     const int own0 = kKthBins - 1 - tid * kOwn;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) mine[i] = 0;
-    for (uint32_t p = 0; p < peers; ++p)
+    for (int i = 0; i < kOwn; i += 2) {
+      if constexpr (kCluster) {
+        uint2 v[kMostPeers];  // on the way together
 #pragma unroll
-      for (int i = 0; i < kOwn; i += 2) {
-        uint2 v;
-        if constexpr (kCluster) v = peer_load2(&hist[own0 - i - 1], p);
-        else v = *reinterpret_cast<const uint2*>(&hist[own0 - i - 1]);
-        mine[i] += v.y;
-        mine[i + 1] += v.x;
+        for (uint32_t p = 0; p < kMostPeers; ++p)
+          v[p] = p < peers ? peer_load2(&hist[own0 - i - 1], p) : make_uint2(0u, 0u);
+        mine[i] = mine[i + 1] = 0;
+#pragma unroll
+        for (uint32_t p = 0; p < kMostPeers; ++p) {
+          mine[i] += v[p].y;
+          mine[i + 1] += v[p].x;
+        }
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(&hist[own0 - i - 1]);
+        mine[i] = v.y;
+        mine[i + 1] = v.x;
       }
+    }
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) sum += mine[i];
     unsigned incl = sum;
@@ -188,22 +199,25 @@ struct Order {
   static_assert(kEntries <= kThreads && kRounds * kThreads < 65536, "a thread an entry, 16 bits a count");
   OrderShared<kThreads, kRounds>& sh;
 
+  unsigned o[kRounds], t[kRounds];  // the warp's votes
+
   // over(i), tie(i): of this thread's element of round i.  Returns the totals (tie << 16).
   template <typename Over, typename Tie>
   __device__ __forceinline__ unsigned scan(Over over, Tie tie) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 #pragma unroll
     for (int i = 0; i < kRounds; ++i) {
-      const unsigned o = __ballot_sync(~0u, over(i)), t = __ballot_sync(~0u, tie(i));
-      if (lane == 0) sh.count[i * kWarps + warp] = __popc(o) | __popc(t) << 16;
+      o[i] = __ballot_sync(~0u, over(i));
+      t[i] = __ballot_sync(~0u, tie(i));
+      if (lane == 0) sh.count[i * kWarps + warp] = __popc(o[i]) | __popc(t[i]) << 16;
     }
     __syncthreads();
     const unsigned own = tid < kEntries ? sh.count[tid] : 0u;
     unsigned incl = own;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned v = __shfl_up_sync(~0u, incl, o);
-      if (lane >= o) incl += v;
+    for (int x = 1; x < 32; x <<= 1) {
+      const unsigned v = __shfl_up_sync(~0u, incl, x);
+      if (lane >= x) incl += v;
     }
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
@@ -217,11 +231,12 @@ struct Order {
     __syncthreads();
     return total;
   }
-  // (over, tie << 16) in front of this thread's element of round i; called by whole warps.
-  __device__ __forceinline__ unsigned before(int i, bool over, bool tie) const {
-    const unsigned lane = threadIdx.x & 31, less = (1u << lane) - 1u;
-    const unsigned o = __ballot_sync(~0u, over), t = __ballot_sync(~0u, tie);
-    return sh.count[i * kWarps + (threadIdx.x >> 5)] + (__popc(o & less) | __popc(t & less) << 16);
+  // Whether this thread's element of round i was one, and (over, tie << 16) in front of it.
+  __device__ __forceinline__ bool over(int i) const { return o[i] >> (threadIdx.x & 31) & 1u; }
+  __device__ __forceinline__ bool tie(int i) const { return t[i] >> (threadIdx.x & 31) & 1u; }
+  __device__ __forceinline__ unsigned before(int i) const {
+    const unsigned less = (1u << (threadIdx.x & 31)) - 1u;
+    return sh.count[i * kWarps + (threadIdx.x >> 5)] + (__popc(o[i] & less) | __popc(t[i] & less) << 16);
   }
 };
 
