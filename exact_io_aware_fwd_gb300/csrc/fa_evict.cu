@@ -126,13 +126,16 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
 }
 
 // ---- eviction: the copies
-// D / 8 lanes a row, so that a warp copies the keys and values of 32 / (D / 8) kept keys at a time,
-// four times ahead.  Bound by reading and writing them once.
-constexpr int kMoveThreads = 128, kMoveKeys = 64;  // of a CTA
+// D / 8 lanes a row, the keys and values of two kept keys a thread on the way.  Bound by reading and
+// writing them once.  Neither is read again soon, so neither stays in L2 (90.6 us for 64 sequences of
+// 512 to 4096 keys to 1024; stores that stay 93.8, both 91.8); eight keys a thread, in flight just as
+// long but fewer at a time near the end: 105.
+constexpr int kMoveThreads = 128, kMoveSteps = 2;
+__host__ __device__ constexpr int move_keys(int d) { return kMoveSteps * kMoveThreads * 8 / d; }  // of a CTA
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a, int chunks) {
-  constexpr int L = D / 8, kRows = kMoveThreads / L, kSteps = kMoveKeys / kRows;
+  constexpr int L = D / 8, kRows = kMoveThreads / L, kSteps = kMoveSteps, kMoveKeys = move_keys(D);
   begin_launch();
   const CacheSeqs& c = a.c;
   const int bh = static_cast<int>(blockIdx.x) / chunks, chunk = static_cast<int>(blockIdx.x) % chunks;
@@ -163,15 +166,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   for (int i = 0; i < kSteps; ++i) {
     kv[0][i] = kv[1][i] = make_uint4(0u, 0u, 0u, 0u);  // of a page outside the pool
     if (from[i] >= 0) {
-      kv[0][i] = *reinterpret_cast<const uint4*>(a.k_cache + from[i]);
-      kv[1][i] = *reinterpret_cast<const uint4*>(a.v_cache + from[i]);
+      kv[0][i] = __ldcs(reinterpret_cast<const uint4*>(a.k_cache + from[i]));
+      kv[1][i] = __ldcs(reinterpret_cast<const uint4*>(a.v_cache + from[i]));
     }
   }
 #pragma unroll
   for (int i = 0; i < kSteps; ++i)
     if (to[i] >= 0) {
-      *reinterpret_cast<uint4*>(a.k_cache + to[i]) = kv[0][i];
-      *reinterpret_cast<uint4*>(a.v_cache + to[i]) = kv[1][i];
+      __stcs(reinterpret_cast<uint4*>(a.k_cache + to[i]), kv[0][i]);
+      __stcs(reinterpret_cast<uint4*>(a.v_cache + to[i]), kv[1][i]);
     }
 }
 
@@ -188,7 +191,7 @@ cudaError_t launch_kv_evict(int d, const EvictArgs& a, cudaStream_t s) {
                       : launch_clusters(evict_select_kernel<kClusterThreads, kClusterRounds, true>, rows * cluster,
                                         cluster, kClusterThreads, s, a);
   if (e != cudaSuccess) return e;
-  const int chunks = (a.budget + kMoveKeys - 1) / kMoveKeys;
+  const int chunks = (a.budget + move_keys(d) - 1) / move_keys(d);
   return d == 64 ? launch_chained(evict_move_kernel<64>, rows * chunks, kMoveThreads, 0, s, a, chunks)
                  : launch_chained(evict_move_kernel<128>, rows * chunks, kMoveThreads, 0, s, a, chunks);
 }
