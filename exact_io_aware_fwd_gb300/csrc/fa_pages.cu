@@ -389,11 +389,11 @@ __device__ __forceinline__ float scale_below(float x) {
   return x == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(min(max(253 - e, 1), 253)) << 23);
 }
 
-constexpr int kSelectRounds = 4;  // scores of a thread in registers; further ones are read again
+// kSelectRounds: scores of a thread in registers; further ones are read again.
 constexpr float kMost = 3.402823466e38f;
 
 // behind_scores: page_score_kernel is the kernel ahead, so what it did not write is complete.
-template <int D, int kSelectThreads>
+template <int D, int kSelectThreads, int kSelectRounds>
 __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const SelectArgs a, const bool behind_scores) {
   constexpr int kWarps = kSelectThreads / 32, kHeld = kSelectRounds * kSelectThreads;
   __shared__ union {
@@ -463,19 +463,15 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     const float r = reach[i];
     far = r == r ? fmaxf(far, r) : INFINITY;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) far = fmaxf(far, __shfl_xor_sync(~0u, far, o));
+  far = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(far)));  // (none is negative)
   if (lane == 0) {
     red[0][warp] = far;
     red[1][warp] = size;
   }
   if (tid == 0) border_count = 0;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    far = fmaxf(far, red[0][w]);
-    size = fmaxf(size, red[1][w]);
-  }
+  far = __uint_as_float(__reduce_max_sync(~0u, lane < kWarps ? __float_as_uint(red[0][lane]) : 0u));
+  size = __uint_as_float(__reduce_max_sync(~0u, lane < kWarps ? __float_as_uint(red[1][lane]) : 0u));
   const float delta = far * size * 0x1p-15f;
   // something is not finite, or too large to be scaled below 1: every score in 64 bits
   const bool odd = !(delta < INFINITY && far < 0x1p126f && size < 0x1p126f);
@@ -523,9 +519,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
   sure = __reduce_add_sync(~0u, sure);
   if (lane == 0) counts[warp] = sure;
   __syncthreads();
-  sure = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) sure += counts[w];
+  sure = __reduce_add_sync(~0u, lane < kWarps ? counts[lane] : 0);
   const int border = border_count, need = k - sure;  // need <= border
   if (border <= kBorder) {
     if (need < border) {
@@ -626,9 +620,8 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const unsigned rows = static_cast<unsigned>(a.c.total) * static_cast<unsigned>(a.c.Hkv);
-  return a.max_pages <= kSelectRounds * 256
-             ? launch_chained(select_pages_kernel<D, 256>, rows, 256, 0, s, a, scores)
-             : launch_chained(select_pages_kernel<D, 1024>, rows, 1024, 0, s, a, scores);
+  return a.max_pages <= 4 * 256 ? launch_chained(select_pages_kernel<D, 256, 4>, rows, 256, 0, s, a, scores)
+                                : launch_chained(select_pages_kernel<D, 512, 8>, rows, 512, 0, s, a, scores);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

@@ -41,6 +41,30 @@ __device__ __forceinline__ uint2 peer_load2(const void* p, uint32_t rank) {
   return v;
 }
 
+// Over a warp's lanes.
+__device__ __forceinline__ uint32_t lanes_min(uint32_t x) { return __reduce_min_sync(~0u, x); }
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) { return __reduce_max_sync(~0u, x); }
+__device__ __forceinline__ uint64_t lanes_min(uint64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t y = __shfl_xor_sync(~0u, x, o);
+    x = y < x ? y : x;
+  }
+  return x;
+}
+__device__ __forceinline__ uint64_t lanes_max(uint64_t x) { return ~lanes_min(~x); }
+// Of the warps' values (one each, in shared memory): the sum, and that of the warps before this one.
+template <int kWarps>
+__device__ __forceinline__ unsigned sum_of(const unsigned* v) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(~0u, lane < kWarps ? v[lane] : 0u);
+}
+template <int kWarps>
+__device__ __forceinline__ unsigned sum_before(const unsigned* v) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(~0u, lane < static_cast<int>(threadIdx.x >> 5) ? v[lane] : 0u);
+}
+
 constexpr int kKthBins = 2048;
 constexpr uint32_t kMostPeers = 8;  // CTAs of a cluster
 
@@ -82,12 +106,8 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
     lo = key < lo ? key : lo;
     hi = key > hi ? key : hi;
   });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Key l = __shfl_xor_sync(~0u, lo, o), h = __shfl_xor_sync(~0u, hi, o);
-    lo = l < lo ? l : lo;
-    hi = h > hi ? h : hi;
-  }
+  lo = lanes_min(lo);
+  hi = lanes_max(hi);
   if (lane == 0) {
     sh.lo[warp] = lo;
     sh.hi[warp] = hi;
@@ -95,11 +115,8 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
 #pragma unroll
   for (int i = 0; i < 2 * kOwn; ++i) (&sh.hist[0][0])[i * kThreads + tid] = 0;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    lo = sh.lo[w] < lo ? sh.lo[w] : lo;
-    hi = sh.hi[w] > hi ? sh.hi[w] : hi;
-  }
+  lo = lanes_min(lane < kWarps ? sh.lo[lane] : ~Key(0));
+  hi = lanes_max(lane < kWarps ? sh.hi[lane] : Key(0));
   if constexpr (kCluster) {
     if (tid == 0) {
       sh.ends[0] = lo;
@@ -156,10 +173,7 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
     }
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
-    unsigned above = incl - sum;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (w < warp) above += sh.warp_sum[w];
+    unsigned above = incl - sum + sum_before<kWarps>(sh.warp_sum);
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       const unsigned need = static_cast<unsigned>(r.need);
@@ -221,12 +235,8 @@ struct Order {
     }
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
-    unsigned total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) incl += sh.warp_sum[w];
-      total += sh.warp_sum[w];
-    }
+    incl += sum_before<kWarps>(sh.warp_sum);
+    const unsigned total = sum_of<kWarps>(sh.warp_sum);
     if (tid < kEntries) sh.count[tid] = incl - own;
     __syncthreads();
     return total;
