@@ -166,6 +166,27 @@ struct SelectedSource {
 };
 constexpr int kNoKey = 0x7fffff00;  // behind every key: lengths are at most this
 
+// Entry of the list for step `st` of lane 0, + i of lane i (none: -1).
+__device__ __forceinline__ int listed_page(const PagedArgs& a, const SelectedSource& s, int st, int steps, int lane) {
+  return st + lane < steps ? __ldg(s.list + ((s.first + st + lane) >> (a.page_shift - 4))) : -1;
+}
+// Where that step's keys are: page `i` of the sequence, whose entry of the block table is `page`.  An
+// entry of the list that names no page, or one behind what the token sees, has no keys.
+__device__ __forceinline__ void locate(const PagedArgs& a, SelectedSource& s, int st, int i, int page, int lane) {
+  s.pages = -1;
+  s.keys = kNoKey;
+  if (i >= 0 && i < (s.len + (1 << a.page_shift) - 1) >> a.page_shift) {
+    s.keys = (i << a.page_shift) + ((s.first + st + lane) & ((1 << (a.page_shift - 4)) - 1)) * KT;
+    if (page >= 0 && page < a.num_pages) s.pages = page;
+    else atomicCAS(a.status, 0, kErrIndex);
+  }
+}
+__device__ __forceinline__ int table_entry(const KeyList& l, const SelectedSource& s, int i) {
+  return i >= 0 && i < l.max_pages ? __ldg(s.trow + i) : -1;
+}
+
+// The first steps' pages are looked up on the way: the list while the token's sequence is searched
+// for, the block table together with its length.
 __device__ __forceinline__ SelectedSource selected_source(const PagedArgs& a, const KeyList& l,
                                                           const Walk<R, KT>& w, const Piece& p,
                                                           int* at, int lane) {
@@ -173,9 +194,12 @@ __device__ __forceinline__ SelectedSource selected_source(const PagedArgs& a, co
   s.hk = p.hk;
   s.first = p.ta;
   s.at = at;
-  s.pages = -1;
-  s.keys = kNoKey;
-  const int t = w.e.start, b = token_sequence_group<32>(a.seq_cu, a.seqs, t, lane, ~0u);
+  const int t = w.e.start, most = min(p.te, (l.max_len + KT - 1) / KT) - p.ta;
+  s.list = a.pages + (static_cast<int64_t>(t) * a.Hkv + p.hk) * a.top;
+  const int i = listed_page(a, s, 0, most, lane);
+  const int b = token_sequence_group<32>(a.seq_cu, a.seqs, t, lane, ~0u);
+  s.trow = l.table + static_cast<int64_t>(max(b, 0)) * l.max_pages;
+  const int page = table_entry(l, s, i);
   int start = 0, n = 0;
   if (b >= 0) token_bounds(a.seq_cu, b, a.total, start, n);
   s.live = b >= 0 && t >= start && t < start + n;
@@ -185,30 +209,21 @@ __device__ __forceinline__ SelectedSource selected_source(const PagedArgs& a, co
   const int len = min(max(given, 0), static_cast<int>(min(reach, static_cast<int64_t>(kNoKey))));
   if (given != len && lane == 0) atomicCAS(a.status, 0, kErrIndex);
   s.len = min(max(len - n + (t - start) + 1, 0), len);
-  s.trow = l.table + static_cast<int64_t>(max(b, 0)) * l.max_pages;
-  s.list = a.pages + (static_cast<int64_t>(t) * a.Hkv + p.hk) * a.top;
-  s.steps = s.len > 0 ? min(p.te, (l.max_len + KT - 1) / KT) - p.ta : 0;
+  s.steps = s.len > 0 ? most : 0;
+  locate(a, s, 0, i, page, lane);
   return s;
 }
 
-// issue_step for selected pages.  An entry of the list that names no page, or one behind what the
-// token sees, has no keys.
+// issue_step for selected pages.
 template <int D>
 __device__ __forceinline__ void issue_step(const PagedArgs& a, const KeyList& l, SelectedSource& s,
                                            int st, uint32_t ring, int lane) {
   using L = PagedLayout<D>;
   constexpr int S = L::kStages, GR = D / 8;
   if (st < s.steps) {
-    if ((st & 31) == 0) {
-      const int tile = s.first + st + lane, j = tile >> (a.page_shift - 4);
-      const int i = st + lane < s.steps ? __ldg(s.list + j) : -1;
-      s.pages = -1;
-      s.keys = kNoKey;
-      if (i >= 0 && i < (s.len + (1 << a.page_shift) - 1) >> a.page_shift) {
-        s.keys = (i << a.page_shift) + (tile & ((1 << (a.page_shift - 4)) - 1)) * KT;
-        s.pages = resolve_page(s.trow, l.max_pages, a.num_pages, a.page_shift, s.keys);
-        if (s.pages < 0) atomicCAS(a.status, 0, kErrIndex);
-      }
+    if ((st & 31) == 0 && st > 0) {
+      const int i = listed_page(a, s, st, s.steps, lane);
+      locate(a, s, st, i, table_entry(l, s, i), lane);
     }
     const int page = __shfl_sync(~0u, s.pages, st & 31), key = __shfl_sync(~0u, s.keys, st & 31);
     const int slot = st % S;
@@ -495,7 +510,13 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
   Piece piece;
   while (walk.next(a, l, piece)) {
     const Entry& e = walk.e;
-    auto source = make_source<M>(a, l, walk, piece, at, lane);
+    Piece own = piece;
+    if constexpr (M == kSelectedKeys) {  // looked up for the warp's own steps
+      const int64_t n = piece.te - piece.ta;
+      own.te = piece.ta + static_cast<int>((warp + 1) * n / kWarps);
+      own.ta = piece.ta + static_cast<int>(warp * n / kWarps);
+    }
+    auto source = make_source<M>(a, l, walk, own, at, lane);
     std::conditional_t<kPrefix, PrefixedSource, decltype(source)> src;
     static_cast<decltype(source)&>(src) = source;
     if constexpr (kPrefix) {
@@ -510,10 +531,12 @@ __device__ __forceinline__ void work_together(const PagedArgs& a, const KeyList&
     if (threadIdx.x == 0 && piece.ta == 0)  // this CTA begins the segment
       parts.spans[static_cast<int64_t>(piece.hk) * parts.span_tiles +
                   row_tile0(e.start, a.G, R, walk.b) + piece.r] = span_of(sh, piece);
-    const int t0 = static_cast<int>(static_cast<int64_t>(warp) * src.steps / kWarps);
-    const int t1 = static_cast<int>(static_cast<int64_t>(warp + 1) * src.steps / kWarps);
-    src.first += t0;
-    src.steps = t1 - t0;
+    if constexpr (M != kSelectedKeys) {
+      const int t0 = static_cast<int>(static_cast<int64_t>(warp) * src.steps / kWarps);
+      const int t1 = static_cast<int>(static_cast<int64_t>(warp + 1) * src.steps / kWarps);
+      src.first += t0;
+      src.steps = t1 - t0;
+    }
     for (int st = 0; st < S - 1; ++st) issue_step<D>(a, l, src, st, ring, lane);
     const QRows<D> x = load_rows<D, M>(a, l, e, piece, lane);
     Acc<D> c;
