@@ -191,7 +191,7 @@ fa_status fa_kv_evict(const float* weights, int capacity, const fa_paged_kv* cac
     return FA_ERR_INVALID_ARG;
   if ((capacity > 0 && !weights) || (new_pages > 0 && !new_table) || !new_lens || !kept || !new_weights)
     return FA_ERR_INVALID_ARG;
-  if (!fits(B, Hkv, budget / 16 + 1)) return FA_ERR_UNSUPPORTED;
+  if (!fits(B, Hkv, budget / 16 + 8)) return FA_ERR_UNSUPPORTED;
   fa::EvictArgs a{};
   int* status = nullptr;
   if ((st = device_ready(status)) != FA_OK) return st;

@@ -13,11 +13,12 @@ namespace {
 // and head is a CTA's, or, where a CTA's registers (kRounds weights a thread) do not hold its
 // weights, a cluster's, each CTA with a stretch of them; only what does not fit eight CTAs is read
 // again in every pass.
-constexpr int kRounds = 8, kClusterRounds = 16;
-constexpr int kClusterThreads = 1024;
-constexpr int evict_cluster(int max_len) {
+// Clusters of more than eight CTAs do not all run at once (16 of 512 threads: 37 us for 8 heads of
+// 131072 keys, 8 of 1024: 20).
+constexpr int kRounds = 8, kMoreRounds = 16;
+constexpr int evict_cluster(int max_len, int threads) {
   int c = 2;
-  while (c < static_cast<int>(kMostPeers) && c * kClusterRounds * kClusterThreads < max_len) c *= 2;
+  while (c < static_cast<int>(kMostPeers) && c * kMoreRounds * threads < max_len) c *= 2;
   return c;
 }
 
@@ -183,13 +184,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 cudaError_t launch_kv_evict(int d, const EvictArgs& a, cudaStream_t s) {
   const unsigned rows = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv);
   const int most = a.c.max_len;
-  const int cluster = evict_cluster(most);
-  cudaError_t e = most <= kRounds * 256   ? launch_chained(evict_select_kernel<256, kRounds, false>, rows, 256, 0, s, a)
-                  : most <= 16 * 256 ? launch_chained(evict_select_kernel<256, 16, false>, rows, 256, 0, s, a)
-                  : most <= kRounds * 1024
-                      ? launch_chained(evict_select_kernel<1024, kRounds, false>, rows, 1024, 0, s, a)
-                      : launch_clusters(evict_select_kernel<kClusterThreads, kClusterRounds, true>, rows * cluster,
-                                        cluster, kClusterThreads, s, a);
+  cudaError_t e;
+  if (most <= kRounds * 256) {
+    e = launch_chained(evict_select_kernel<256, kRounds, false>, rows, 256, 0, s, a);
+  } else if (most <= kMoreRounds * 256) {
+    e = launch_chained(evict_select_kernel<256, kMoreRounds, false>, rows, 256, 0, s, a);
+  } else if (most <= kRounds * 1024) {
+    e = launch_chained(evict_select_kernel<1024, kRounds, false>, rows, 1024, 0, s, a);
+  } else if (most <= static_cast<int>(kMostPeers) * kMoreRounds * 512) {
+    const int c = evict_cluster(most, 512);
+    e = launch_clusters(evict_select_kernel<512, kMoreRounds, true>, rows * c, c, 512, s, a);
+  } else {
+    const int c = evict_cluster(most, 1024);
+    e = launch_clusters(evict_select_kernel<1024, kMoreRounds, true>, rows * c, c, 1024, s, a);
+  }
   if (e != cudaSuccess) return e;
   const int chunks = (a.budget + move_keys(d) - 1) / move_keys(d);
   return d == 64 ? launch_chained(evict_move_kernel<64>, rows * chunks, kMoveThreads, 0, s, a, chunks)

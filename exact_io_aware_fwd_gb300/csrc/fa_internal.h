@@ -134,20 +134,6 @@ cudaError_t ensure_smem_limit(uint32_t bytes) {
   return e;
 }
 
-// Allows kernel K clusters of more than eight CTAs, once per device like the limit above.
-template <auto K>
-cudaError_t ensure_wide_clusters() {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
-  if (bit != 0 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(K, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 // Launchers return cudaSuccess or the launch error.
 cudaError_t launch_fwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& to, const FwdArgs& a, cudaStream_t s);

@@ -1,8 +1,8 @@
 // The k-th largest of many keys held by a CTA or by the CTAs of a cluster, by counting, and the order
 // in which what was selected is listed.
 //
-// Each pass sorts the keys that are still in question into 2048 equal bins and goes on with the bin
-// that holds the k-th.  The bins divide the range that the keys really have, so the first pass
+// Each pass sorts the keys that are still in question into 2048 equal bins (a cluster: two a thread of
+// a CTA) and goes on with the bin that holds the k-th.  The bins divide the range that the keys really have, so the first pass
 // spreads them (the leading bits of floats that lie close together are the same) and rarely more
 // than two passes are needed.  A cluster's CTAs add up each other's bins through distributed shared
 // memory, one cluster barrier a pass.
@@ -97,8 +97,10 @@ template <int kThreads, bool kCluster, typename Key, typename Each>
 __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each,
                                                 KthShared<kThreads, Key>& sh) {
   static_assert(!kCluster || sizeof(Key) == 4, "peers are read in pairs of words");
-  constexpr int kWarps = kThreads / 32, kOwn = kKthBins / kThreads;
-  static_assert(kOwn % 2 == 0 && kOwn * kThreads == kKthBins, "bins per thread, in pairs");
+  constexpr int kBins = kCluster ? 2 * kThreads : kKthBins, kBits = kBins == 2048 ? 11 : 10;
+  constexpr int kWarps = kThreads / 32, kOwn = kBins / kThreads;
+  static_assert(kOwn * kThreads == kBins && 1 << kBits == kBins, "bins per thread");
+  static_assert(kOwn % 2 == 0, "bins are read in pairs");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t peers = kCluster ? cluster_size() : 1;
   Key lo = ~Key(0), hi = 0;
@@ -113,7 +115,7 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
     sh.hi[warp] = hi;
   }
 #pragma unroll
-  for (int i = 0; i < 2 * kOwn; ++i) (&sh.hist[0][0])[i * kThreads + tid] = 0;
+  for (int i = 0; i < kOwn; ++i) sh.hist[0][i * kThreads + tid] = sh.hist[1][i * kThreads + tid] = 0;
   __syncthreads();
   lo = lanes_min(lane < kWarps ? sh.lo[lane] : ~Key(0));
   hi = lanes_max(lane < kWarps ? sh.hi[lane] : Key(0));
@@ -129,7 +131,7 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
   }
   Kth<Key> r{lo, hi - lo, k, -1};
   for (int pass = 0; pass < max_passes; ++pass) {
-    const int bits = bit_length(r.range), shift = bits > 11 ? bits - 11 : 0;
+    const int bits = bit_length(r.range), shift = bits > kBits ? bits - kBits : 0;
     // two sets of bins take turns: this one is empty, and the other is cleared once nobody reads it
     unsigned* const hist = sh.hist[pass & 1];
     if (pass == 0) {
@@ -143,21 +145,21 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
     else __syncthreads();
     // thread t owns the kOwn bins from own0 down, counted from the top
     unsigned mine[kOwn], sum = 0;
-    const int own0 = kKthBins - 1 - tid * kOwn;
+    const int own0 = kBins - 1 - tid * kOwn;
+    if constexpr (kCluster) {
+      static_assert(kOwn == 2, "a pair a thread");
+      uint2 v[kMostPeers];  // on the way together
 #pragma unroll
-    for (int i = 0; i < kOwn; i += 2) {
-      if constexpr (kCluster) {
-        uint2 v[kMostPeers];  // on the way together
+      for (uint32_t p = 0; p < kMostPeers; ++p) v[p] = p < peers ? peer_load2(&hist[own0 - 1], p) : make_uint2(0u, 0u);
+      mine[0] = mine[1] = 0;
 #pragma unroll
-        for (uint32_t p = 0; p < kMostPeers; ++p)
-          v[p] = p < peers ? peer_load2(&hist[own0 - i - 1], p) : make_uint2(0u, 0u);
-        mine[i] = mine[i + 1] = 0;
+      for (uint32_t p = 0; p < kMostPeers; ++p) {
+        mine[0] += v[p].y;
+        mine[1] += v[p].x;
+      }
+    } else {
 #pragma unroll
-        for (uint32_t p = 0; p < kMostPeers; ++p) {
-          mine[i] += v[p].y;
-          mine[i + 1] += v[p].x;
-        }
-      } else {
+      for (int i = 0; i < kOwn; i += 2) {
         const uint2 v = *reinterpret_cast<const uint2*>(&hist[own0 - i - 1]);
         mine[i] = v.y;
         mine[i + 1] = v.x;
