@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
       if (x[i] != 0u) f(x[i]);
     tail(f);
   };
-  const Kth<uint32_t> kth = kth_largest<kThreads, kCluster, uint32_t>(k, 32, each, sh);
+  const Kth<uint32_t> kth = kth_largest<kThreads, kCluster, uint32_t>(k, 0, each, sh);
   Order<kThreads, kRounds> order{order_sh};
   unsigned over0 = 0, tie0 = 0;  // in front of what comes next
   for (int r0 = c0; r0 == c0 || r0 < c1; r0 += kHeld) {

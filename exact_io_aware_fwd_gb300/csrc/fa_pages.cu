@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Bounds
 // fragments: which element of a row is which k of the product does not matter as long as both sides
 // agree, so lane l % 4 takes eight neighbouring elements as k = 2c, 2c + 1, 2c + 8, 2c + 9 of two
 // products.
-constexpr int kScoreWarps = 4, kScorePages = 16;
+// (64 sequences of 131072 keys, pages of 64: 112 us; 8 pages a warp 140, 32 123; 4 warps a CTA 115, 8
+// 127.)
+constexpr int kScoreWarps = 2, kScorePages = 16;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectArgs a, int chunks) {
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
 // every page more than 2 delta below it is out; the few between are scored again as exactly as in 64
 // bits.
 constexpr int kBorder = 512;  // pages next to the border that are ranked in shared memory
+constexpr int kFew = 16;      // few enough to be taken for the border without another pass
 
 // What a warp needs of a page and the queries: E elements a lane, of kHeads heads at a time.
 constexpr int kFineHeads = 4;
@@ -413,6 +416,18 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
   const CacheSeqs& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x / c.Hkv, hk = blockIdx.x - t * c.Hkv;
+  float size = 0.f;  // largest sum |q_e| of a head (loaded while the token's sequence is searched for)
+  if (behind_scores) {
+    const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D;
+    for (int g = warp; g < a.G; g += kWarps) {
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) x += fabsf(__bfloat162float(q[g * D + e * 32 + lane]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+      size = x == x ? fmaxf(size, x) : INFINITY;
+    }
+  }
   const int b = token_sequence_group<32>(c.cu, c.B, t, lane, ~0u);
   int start = 0, n = 0, pages = -1;
   if (b >= 0) {
@@ -426,20 +441,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     }
   }
   const int mid = pages - a.first - a.last, k = a.top - a.first - a.last;  // k of the pages in between
-  const bool choose = pages > a.top && k > 0;
   int32_t* out = a.pages + static_cast<int64_t>(blockIdx.x) * a.top;
-  float size = 0.f;  // largest sum |q_e| of a head
-  if (choose) {
-    const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D;
-    for (int g = warp; g < a.G; g += kWarps) {
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) x += fabsf(__bfloat162float(q[g * D + e * 32 + lane]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-      size = x == x ? fmaxf(size, x) : INFINITY;
-    }
-  }
   if (behind_scores) wait_for_last_launch();
   if (pages < 0) return;  // behind the last sequence
   if (pages <= a.top) {
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
         if (i * kSelectThreads + tid < mid) f(ordered(x[i]));
       for (int at = kHeld + tid; at < mid; at += kSelectThreads) f(ordered(score[at]));
     };
-    const Kth<uint32_t> kth = kth_largest<kSelectThreads, false, uint32_t>(k, 2, each, sh.k32);
+    const Kth<uint32_t> kth = kth_largest<kSelectThreads, false, uint32_t>(k, kFew, each, sh.k32);
     above = unordered(kth.base + kth.range) + 2.f * delta;
     below = unordered(kth.base) - 2.f * delta;
     __syncthreads();  // the bins are free
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
       for (int i = tid; i < mid; i += kSelectThreads)
         if (here(score[i])) f(fine[i]);
     };
-    const Kth<uint64_t> kth = kth_largest<kSelectThreads, false, uint64_t>(need, 64, each, sh.k64);
+    const Kth<uint64_t> kth = kth_largest<kSelectThreads, false, uint64_t>(need, 0, each, sh.k64);
     // in order, so that of equal ones the first are taken
     int taken = 0;
     for (int i0 = 0; i0 < mid; i0 += kSelectThreads) {

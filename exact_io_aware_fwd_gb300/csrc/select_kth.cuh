@@ -91,10 +91,11 @@ __device__ __forceinline__ int bit_length(uint32_t x) { return 32 - __clz(x); }
 __device__ __forceinline__ int bit_length(uint64_t x) { return 64 - __clzll(x); }
 
 // each(f) calls f(key) for every key of this thread.  1 <= k <= number of keys.  Ends when every key
-// of the range is needed, when the range is one key, or after max_passes.  Called by all threads of
-// the CTA, or (kCluster, 32-bit keys) of the cluster; sh may be used again after the next barrier.
+// of the range is needed, when the range is one key, or when it holds no more than `few` keys.  Called
+// by all threads of the CTA, or (kCluster, 32-bit keys) of the cluster; sh may be used again after the
+// next barrier.
 template <int kThreads, bool kCluster, typename Key, typename Each>
-__device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each,
+__device__ __forceinline__ Kth<Key> kth_largest(int k, int few, Each each,
                                                 KthShared<kThreads, Key>& sh) {
   static_assert(!kCluster || sizeof(Key) == 4, "peers are read in pairs of words");
   constexpr int kBins = kCluster ? 2 * kThreads : kKthBins, kBits = kBins == 2048 ? 11 : 10;
@@ -130,7 +131,7 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
     hi = __reduce_max_sync(~0u, v.y);
   }
   Kth<Key> r{lo, hi - lo, k, -1};
-  for (int pass = 0; pass < max_passes; ++pass) {
+  for (int pass = 0;; ++pass) {  // a pass leaves at most a 1024th of the range
     const int bits = bit_length(r.range), shift = bits > kBits ? bits - kBits : 0;
     // two sets of bins take turns: this one is empty, and the other is cleared once nobody reads it
     unsigned* const hist = sh.hist[pass & 1];
@@ -197,7 +198,7 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int max_passes, Each each
     r.range = left < width ? left : width;
     r.need = sh.need;
     r.count = sh.count;
-    if (shift == 0 || r.need == r.count) break;  // the same everywhere
+    if (shift == 0 || r.need == r.count || r.count <= few) break;  // the same everywhere
   }
   return r;
 }
