@@ -112,7 +112,7 @@ fa_status fa_select_pages(const void* Q, const void* bounds, const fa_paged_kv* 
   if (!Q || !bounds || !pages || !aligned_to(Q, 16) || !aligned_to(bounds, 16))
     return FA_ERR_INVALID_ARG;
   const long long most = pages_of(max_kv, cache->page_size);
-  if (!fits(B, Hkv, most / 64 + 1) || !fits(total, Hkv, 1)) return FA_ERR_UNSUPPORTED;
+  if (!fits(B, Hkv, most / 32 + 1) || !fits(total, Hkv, 1)) return FA_ERR_UNSUPPORTED;
   const fa::SelectWorkspace w = fa::select_workspace(B, total, Hkv, static_cast<int>(most));
   if ((st = fa::check_workspace(workspace, workspace_bytes, w.total)) != FA_OK) return st;
   fa::SelectArgs a{};

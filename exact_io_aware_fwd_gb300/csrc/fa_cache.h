@@ -21,6 +21,17 @@ struct CacheSeqs {
   int* status;
 };
 
+// Pages that hold one of the last n keys of a sequence are at most n / page_size + 2, so slot
+// cu[b] / page_size + 2 b + i stands for the i-th of sequence b: disjoint, whatever the lengths.
+__host__ __device__ __forceinline__ int first_slot(const int32_t* cu, int b, int total, int shift) {
+#ifdef __CUDA_ARCH__
+  const int at = cu != nullptr ? __ldg(cu + b) : b;
+#else
+  const int at = cu != nullptr ? cu[b] : b;
+#endif
+  return (min(max(at, 0), total) >> shift) + 2 * b;
+}
+
 #ifdef __CUDACC__
 // Keys of sequence b, clamped (and reported).
 __device__ __forceinline__ int keys_of(const CacheSeqs& c, int b, bool report) {

@@ -77,17 +77,6 @@ __global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const int32_t* 
 }
 
 // ---- bounds
-// Pages that hold one of the last n keys of a sequence are at most n / page_size + 2, so slot
-// cu[b] / page_size + 2 b + i stands for the i-th of sequence b: disjoint, whatever the lengths.
-__host__ __device__ __forceinline__ int first_slot(const int32_t* cu, int b, int total, int shift) {
-#ifdef __CUDA_ARCH__
-  const int at = cu != nullptr ? __ldg(cu + b) : b;
-#else
-  const int at = cu != nullptr ? cu[b] : b;
-#endif
-  return (min(max(at, 0), total) >> shift) + 2 * b;
-}
-
 constexpr int kBoundThreads = 128;
 
 // One warp a page and head: D / 8 lanes a row, eight rows a lane on the way.  Bound by reading the

@@ -11,9 +11,9 @@
 // CTAs are persistent and take equal shares of all key tiles (paged_plan.cuh).  Warp 2 works out a
 // CTA's pieces and hands them to the others through a ring; a piece is worked on once for every 128
 // queries (a job), the sums of the later ones on top of the earlier ones' (in global memory, by the
-// same threads).  The two warpgroups of a CTA take alternate key tiles, each with a buffer of tensor
-// memory, and write the next job's queries into shared memory before they turn to this one's tiles.
-// Warp 3 copies what no query sees.
+// same threads).  The warpgroups of a CTA take key tiles in turn, each with a buffer of tensor memory,
+// and write the next job's queries into shared memory before they turn to this one's tiles.  Warp 3
+// copies what no query sees.
 #include "fa_cache.h"
 #include "fa_internal.h"
 #include "paged_plan.cuh"
@@ -23,14 +23,13 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 384;  // warp 0: TMA, 1: MMA, 2: pieces, 3: columns past the keys, 4-11: weights
+constexpr int kGroups = 2;  // warpgroups of weights (four: 43.0 us for 8 x 32 tokens over 16384 keys, two: 41.4)
+constexpr int kWarps = 4 * kGroups;
+constexpr int kThreads = 128 + 32 * kWarps;  // warp 0: TMA, 1: MMA, 2: pieces, 3: columns past the keys
 constexpr int KT = 128;        // keys of a tile
 constexpr int NQ = 128;        // queries of a job
 constexpr int kAllRows = 1 << 30;  // the plan knows one row tile: a piece has all of its queries
 constexpr int kRing = 4;
-// A piece of several jobs is cut into pieces of this many tiles, so that the keys that the later jobs
-// read again are in L2 (16 x 32 KB x 152 CTAs): 8 x 131072 keys and 256 queries YY us, whole ZZ.
-constexpr int kManyJobs = 16;
 constexpr int kStats = 4;  // jobs whose queries' statistics are kept: a warp may be three ahead of another
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -52,7 +51,7 @@ struct Layout {
   static constexpr uint32_t kTile = 128u * D * 2u;
   static constexpr int kStages = D == 128 ? 4 : 8;  // 128 KB on the way
   static constexpr uint32_t kK = 0, kQ = kStages * kTile, kBytes = kQ + 2 * kTile;
-  static constexpr uint32_t kTmemCols = 256;
+  static constexpr uint32_t kTmemCols = NQ * kGroups;
 };
 
 template <int D>
@@ -62,7 +61,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using L = Layout<D>;
   constexpr int S = L::kStages, P = D / 64;
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ uint64_t k_full[S], k_empty[S], q_full[2], q_empty[2], s_full[2], s_empty[2], mma_done[1];
+  __shared__ uint64_t k_full[S], k_empty[S], q_full[2], q_empty[2], s_full[kGroups], s_empty[kGroups],
+      mma_done[1];
   __shared__ uint64_t piece_full[kRing], piece_empty[kRing];
   __shared__ PieceInfo pieces[kRing];
   __shared__ alignas(16) float less[kStats][NQ];  // -LSE in log2 units of a job's queries
@@ -83,15 +83,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&q_full[t], 8);
+      mbar_init(&q_full[t], kWarps);
       mbar_init(&q_empty[t], 1);
+    }
+    for (int t = 0; t < kGroups; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&s_empty[t], 4);
     }
     mbar_init(mma_done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&piece_full[i], 1);
-      mbar_init(&piece_empty[i], 10);  // TMA warp, MMA thread, 8 warps of weights
+      mbar_init(&piece_empty[i], 2 + kWarps);  // TMA warp, MMA thread, warps of weights
     }
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
@@ -114,22 +116,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk<kAllRows, KT> walk(a, l, shares[0]);
       const Entry& e = walk.e;
       Piece piece;
-      int n = 0, ta = 0;  // key tiles that are left of it (a sequence without keys has none), the next one
+      int n = 0;  // key tiles; a sequence without keys has none
       for (int i = 0;; ++i) {
-        bool more = true;
-        if (n == 0) {
-          while ((more = walk.next(a, l, piece)) && (n = min(piece.te, (e.len + KT - 1) / KT) - piece.ta) <= 0) {
-          }
-          ta = piece.ta;
+        bool more;
+        while ((more = walk.next(a, l, piece)) && (n = min(piece.te, (e.len + KT - 1) / KT) - piece.ta) <= 0) {
         }
         if (!mbar_wait(&piece_empty[i % kRing], ((i / kRing) & 1) ^ 1, ctl)) break;
         PieceInfo& p = pieces[i % kRing];
         if (more) {
-          prefetch_l1(l.table + static_cast<int64_t>(walk.b) * l.max_pages + (ta << 7 >> a.page_shift));
-          p.n = e.nc * a.G > NQ ? min(n, kManyJobs) : n;
-          p.ta = ta;
-          n -= p.n;
-          ta += p.n;
+          prefetch_l1(l.table + static_cast<int64_t>(walk.b) * l.max_pages + (piece.ta << 7 >> a.page_shift));
+          p.n = n;
+          p.ta = piece.ta;
           p.bh = walk.b * a.Hkv + piece.hk;
           p.hk = piece.hk;
           p.start = e.start;
@@ -218,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ================= MMA issuer
     if (lane == 0) {
-      int jk = 0, jobs = 0, issued[2] = {0, 0};
+      int jk = 0, jobs = 0;
+      uint32_t turns = 0;  // bit t: an odd number of products into buffer t
       bool ok = true;
       for (int i = 0; ok; ++i) {
         if (!(ok = mbar_wait(&piece_full[i % kRing], (i / kRing) & 1, ctl))) break;
@@ -231,16 +229,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // columns in steps of 16, as the instruction takes them
           const uint32_t id = idesc_bf16(128, (min(NQ, rows - r * NQ) + 15) / 16 * 16, false, false);
           for (int j = 0; j < n; ++j, ++jk) {
-            const int s = jk % S, t = j & 1;
+            const int s = jk % S, t = j % kGroups;
             if (!(ok = mbar_wait(&k_full[s], (jk / S) & 1, ctl))) break;
-            if (!(ok = mbar_wait(&s_empty[t], ((t ? issued[1] : issued[0]) & 1) ^ 1, ctl))) break;
+            if (!(ok = mbar_wait(&s_empty[t], (turns >> t & 1) ^ 1, ctl))) break;
             tc_fence_after();
             mma_ss_kmajor<D>(tmem + NQ * t, sdesc_sw128(sbase + L::kK + s * L::kTile, 16384, 1024),
                              sdesc_sw128(sbase + L::kQ + slot * L::kTile, 16384, 1024), id, 0u);
             mma_commit(&s_full[t]);
             mma_commit(&k_empty[s]);
-            issued[0] += 1 - t;
-            issued[1] += t;
+            turns ^= 1u << t;
           }
           if (ok) mma_commit(&q_empty[slot]);
         }
@@ -250,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_wait(mma_done, 0, ctl);
     }
   } else {
-    // ================= weights: two warpgroups, one thread per key
+    // ================= weights: one thread per key of a tile
     const int t = (warp - 4) >> 2, quad = warp & 3;
     const uint32_t tS = tmem + ((quad * 32u) << 16) + NQ * t;
     const float2 c2 = make_float2(a.scale_log2, a.scale_log2);
@@ -268,29 +265,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       j.r = 0;
       return mbar_wait_warp(&piece_full[j.i % kRing], (j.i / kRing) & 1, ctl);
     };
-    // 16 of a job's queries and their statistics: loaded one job before they are written to the job's
+    // Some of a job's queries and their statistics: loaded one job before they are written to the job's
     // slot, which is one job before it is their turn
-    constexpr int GR = D / 8, RI = 32 / GR;  // granules of a row, rows per step
-    const int q0 = (warp - 4) * 16;
-    uint4 v[16 / RI];
+    constexpr int GR = D / 8, RI = 32 / GR, QW = NQ / kWarps;  // granules of a row, rows per step and warp
+    static_assert(QW >= RI && QW <= 32, "whole steps");
+    const int q0 = (warp - 4) * QW;
+    uint4 v[QW / RI];
     float stat = 0.f;
     int limit = 0;
     bool any = false;  // this warp has queries of the job
     auto fetch = [&](const Job& j) {
       const PieceInfo& p = pieces[j.i % kRing];
-      const int rows = min(NQ, p.rows - j.r * NQ), mine = q0 + (lane & 15), row = j.r * NQ + mine, tok = row / a.G;
+      const int rows = min(NQ, p.rows - j.r * NQ), mine = q0 + (lane & (QW - 1)), row = j.r * NQ + mine, tok = row / a.G;
       const int head = p.hk * a.G + (row - tok * a.G);
       const int place = mine < rows ? (p.start + tok) * a.H + head : -1;
-      any = q0 < rows;
+      any = q0 < (rows + 15) / 16 * 16;  // what the product takes
       if (!any) return;
       stat = -INFINITY;  // the LSE of a row without keys, or of no row
       limit = 0;
-      if (lane < 16 && place >= 0) {
+      if (lane < QW && place >= 0) {
         stat = w.lse[static_cast<int64_t>(head) * a.total + p.start + tok];
         limit = w.causal ? min(p.len, p.shift + tok + 1) : p.len;
       }
 #pragma unroll
-      for (int k = 0; k < 16 / RI; ++k) {
+      for (int k = 0; k < QW / RI; ++k) {
         const int from = __shfl_sync(~0u, place, k * RI + lane / GR);
         v[k] = make_uint4(0u, 0u, 0u, 0u);
         if (from >= 0)
@@ -301,12 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_warp(&q_empty[job & 1], ((job >> 1) & 1) ^ 1, ctl)) return false;
       if (any) {
         const uint32_t q_tile = sbase + L::kQ + (job & 1) * L::kTile;
-        if (lane < 16) {
+        if (lane < QW) {
           less[job % kStats][q0 + lane] = stat == -INFINITY ? -INFINITY : -stat * kLog2e;  // weighs nothing
           sees[job % kStats][q0 + lane] = limit;
         }
 #pragma unroll
-        for (int k = 0; k < 16 / RI; ++k)
+        for (int k = 0; k < QW / RI; ++k)
           st_shared_v4(q_tile + (lane % GR / 8) * 16384 + sw128_offset(q0 + k * RI + lane / GR, lane % 8), v[k].x,
                        v[k].y, v[k].z, v[k].w);
         fence_proxy_async_smem();
@@ -347,10 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t line = static_cast<int64_t>(p.bh) * w.cap;
       float next = r > 0 ? had(cur, t) : ahead;
       if (live(behind) && behind.r == 0) ahead = had(behind, t);
-      for (int j = t; j < p.n; j += 2) {
+      for (int j = t; j < p.n; j += kGroups) {
         const int k0 = (p.ta + j) * KT, key = k0 + quad * 32 + lane;
         const float was = next;
-        next = had(cur, j + 2);
+        next = had(cur, j + kGroups);
         if (!(ok = mbar_wait_warp(&s_full[t], seen++ & 1, ctl))) break;
         tc_fence_after();
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

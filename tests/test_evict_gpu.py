@@ -269,6 +269,42 @@ def test_evict_repeats_in_a_graph_and_on_another_stream():
     assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+def test_evict_of_a_long_sequence_in_a_graph():
+    """A launch of clusters, captured and replayed for other weights and lengths."""
+    e = Evicted([40000, 9000], 2, 64, 16, 1500, 15)
+    e.check(100)
+    args = (e.w.to(DEV), e.k0.clone(), e.v0.clone(), e.table.to(DEV), i32(e.lens), e.new.to(DEV), 1500, 100)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = fa.fa_kv_evict(*args)
+    args[0].copy_(args[0].flip(2))
+    args[4].copy_(i32([39990, 1200]))
+    g.replay()
+    want = fa.fa_kv_evict(*args)
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and got[0].tolist() == [1500, 1200]
+    assert fa.fa_get_error() == fa.FA_OK
+
+
+def test_calls_on_two_streams_at_once():
+    """Nothing is shared between calls: each has its own outputs and workspaces."""
+    e, f = Evicted([3000, 700], 2, 64, 16, 300, 16), Evicted([20000], 2, 64, 16, 900, 17)
+    want = [[t.clone() for t in x.check(20)] for x in (e, f)]
+    w = Weighted([40, 3], [3000, 900], (8, 2, 64, 32), True, 18)
+    a, o = w.args(), w.opts()
+    ref = fa.fa_kv_weights(*a, **o)
+    args = [(x.w.to(DEV), x.k, x.v, x.table.to(DEV), i32(x.lens), x.new.to(DEV), x.budget, 20) for x in (e, f)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append([fa.fa_kv_evict(*args[0], stream=streams[0]), fa.fa_kv_evict(*args[1], stream=streams[1]),
+                    fa.fa_kv_weights(*a, **o, stream=streams[2])])
+    torch.cuda.synchronize()
+    for x, y, z in got:
+        assert all(torch.equal(p, q) for p, q in zip(x, want[0])) and all(torch.equal(p, q) for p, q in zip(y, want[1]))
+        assert torch.equal(z, ref)
+
+
 def test_evict_out_of_range_and_refusals():
     e = Evicted([100, 60], 2, 64, 16, 32, 6)
     e.run(4)

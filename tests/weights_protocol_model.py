@@ -10,23 +10,23 @@ from __future__ import annotations
 from protocol_model import Bar, Buf, Sim
 
 
-def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
+def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None, groups=2):
     """pieces: (key tiles, jobs) of each piece, both at least 1.  `bug` plants a protocol error:
     "mma_no_s_wait", "no_q_wait", "early_k_release", "early_piece_release".  `stats`: places for the
     jobs' statistics.  `abort_at`: the abort_at-th spin of a bounded wait times out.  Returns the Sim."""
     sim = Sim(seed, abort_at)
     wait_ok = sim.wait_ok
     k_full, k_empty = ([Bar(1, f"{n}{s}") for s in range(S)] for n in ("k_full", "k_empty"))
-    q_full, q_empty = ([Bar(c, f"{n}{t}") for t in range(2)] for n, c in (("q_full", 8), ("q_empty", 1)))
-    s_full, s_empty = ([Bar(c, f"{n}{t}") for t in range(2)] for n, c in (("s_full", 1), ("s_empty", 4)))
+    q_full, q_empty = ([Bar(c, f"{n}{t}") for t in range(2)] for n, c in (("q_full", 4 * groups), ("q_empty", 1)))
+    s_full, s_empty = ([Bar(c, f"{n}{t}") for t in range(groups)] for n, c in (("s_full", 1), ("s_empty", 4)))
     mma_done = Bar(1, "mma_done")
     piece_full = [Bar(1, f"piece_full{i}") for i in range(ring)]
-    piece_empty = [Bar(10, f"piece_empty{i}") for i in range(ring)]
+    piece_empty = [Bar(2 + 4 * groups, f"piece_empty{i}") for i in range(ring)]
     slots = [Buf(f"piece{i}") for i in range(ring)]
     Kst = [Buf(f"K{s}") for s in range(S)]
-    Qt = [[Buf(f"Q{t}w{w}") for w in range(8)] for t in range(2)]
-    stat = [[Buf(f"stats{i}w{w}") for w in range(8)] for i in range(stats)]
-    Sreg = [[Buf(f"S{t}q{q}") for q in range(4)] for t in range(2)]
+    Qt = [[Buf(f"Q{t}w{w}") for w in range(4 * groups)] for t in range(2)]
+    stat = [[Buf(f"stats{i}w{w}") for w in range(4 * groups)] for i in range(stats)]
+    Sreg = [[Buf(f"S{t}q{q}") for q in range(4)] for t in range(groups)]
     done = []
     first = [0]  # number of the first job of each piece
     for _, jobs in pieces:
@@ -36,7 +36,7 @@ def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
         for i, n in enumerate(pieces + [None]):
             if not (yield from wait_ok(piece_empty[i % ring], ((i // ring) & 1) ^ 1, i // ring)):
                 return
-            slots[i % ring].write((i, n), readers=10 if n is not None else 0)
+            slots[i % ring].write((i, n), readers=2 + 4 * groups if n is not None else 0)
             piece_full[i % ring].arrive()
 
     def take(i):
@@ -82,10 +82,10 @@ def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
 
     def op_S(job, j, c):
         def fn():
-            for w in range(8):
+            for w in range(4 * groups):
                 Qt[job & 1][w].read(job, consume=True)
             for q in range(4):
-                Sreg[j & 1][q].write((job, j), readers=1)
+                Sreg[j % groups][q].write((job, j), readers=1)
             Kst[c % S].read(c, consume=True)
         sim.issue(fn)
 
@@ -94,7 +94,7 @@ def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
 
     def mma():
         jk = job = i = 0
-        issued = [0, 0]
+        issued = [0] * groups
         ok = True
         while ok:
             got = yield from take(i)
@@ -107,7 +107,7 @@ def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
                 if bug != "no_q_wait":
                     ok = yield from wait_ok(q_full[job & 1], (job >> 1) & 1, (job >> 1) + 1)
                 for j in range(n if ok else 0):
-                    t = j & 1
+                    t = j % groups
                     ok = yield from wait_ok(k_full[jk % S], (jk // S) & 1, jk // S + 1)
                     if ok and bug != "mma_no_s_wait":
                         ok = yield from wait_ok(s_empty[t], (issued[t] & 1) ^ 1, issued[t])
@@ -133,7 +133,7 @@ def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
         if not (yield from wait_ok(q_empty[job & 1], ((job >> 1) & 1) ^ 1, job >> 1)):
             return False
         Qt[job & 1][w].write(job, readers=pieces[at][0])
-        stat[job % stats][w].write(job, readers=8)
+        stat[job % stats][w].write(job, readers=4 * groups)
         q_full[job & 1].arrive()
         return True
 
@@ -170,18 +170,18 @@ def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
                 release(i)
             if not (yield from wait_ok(q_full[job & 1], (job >> 1) & 1, (job >> 1) + 1)):
                 return
-            for j in range(t, n, 2):
+            for j in range(t, n, groups):
                 seen += 1
                 if not (yield from wait_ok(s_full[t], (seen - 1) & 1, seen)):
                     return
                 slots[i % ring].read((i, pieces[i]))
-                for x in range(8):
+                for x in range(4 * groups):
                     stat[job % stats][x].read(job)
                 Sreg[t][q].read((job, j), consume=True)
                 s_empty[t].arrive()
                 yield
                 done.append((job, j, q))
-            for x in range(8):  # the job's statistics are free once all warps are through with it
+            for x in range(4 * groups):  # the job's statistics are free once all warps are through with it
                 stat[job % stats][x].read(job, consume=True)
             job += 1
             if ni != i and bug != "early_piece_release":
@@ -190,7 +190,7 @@ def weights(pieces, S, seed, ring=4, stats=4, bug=None, abort_at=None):
             if i == len(pieces):
                 return
 
-    sim.run([walker(), producer()] + [warp(t, q) for t in range(2) for q in range(4)], mma())
+    sim.run([walker(), producer()] + [warp(t, q) for t in range(groups) for q in range(4)], mma())
     assert sim.exit_ops == 0, f"CTA exits with {sim.exit_ops} MMA operations queued"
     if not sim.abort:
         assert sim.exit_copies == 0, f"CTA exits with {sim.exit_copies} copies in flight"
