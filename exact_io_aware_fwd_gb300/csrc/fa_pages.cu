@@ -381,7 +381,41 @@ __device__ __forceinline__ float scale_below(float x) {
   return x == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(min(max(253 - e, 1), 253)) << 23);
 }
 
-// kSelectRounds: scores of a thread in registers; further ones are read again.
+// The largest sum |q_e| of heads g0, g0 + step, ... of a group (infinite where one is not a number).
+template <int D>
+__device__ __forceinline__ float query_size(const SelectArgs& a, int t, int hk, int g0, int step, int lane) {
+  const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D + lane;
+  float size = 0.f;
+#pragma unroll 4
+  for (int g = g0; g < a.G; g += step) {
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < D; e += 32) x += fabsf(__bfloat162float(q[g * D + e]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    size = x == x ? fmaxf(size, x) : INFINITY;
+  }
+  return size;
+}
+// The pages with keys that token t sees (-1: behind the last sequence), and its sequence; by whole
+// warps.
+__device__ __forceinline__ int visible_pages(const SelectArgs& a, int t, int& b, int lane, bool first, bool head0) {
+  const CacheSeqs& c = a.c;
+  b = token_sequence_group<32>(c.cu, c.B, t, lane, ~0u);
+  if (b < 0) return -1;
+  int start, n;
+  token_bounds(c.cu, b, c.total, start, n);
+  if (t < start || t >= start + n) {  // offsets that do not ascend
+    if (first) atomicCAS(c.status, 0, kErrIndex);
+    return -1;
+  }
+  const int len = keys_of(c, b, head0 && first);
+  const int sees = min(max(len - n + (t - start) + 1, 0), len);
+  return (sees + (1 << c.page_shift) - 1) >> c.page_shift;
+}
+
+// kSelectRounds: scores of a thread in registers; further ones are read again.  (A warp a row that closes
+// in on the k-th by votes, without a barrier: 21.6 us instead of 16.7 for 512 rows of up to 256 pages.)
 constexpr float kMost = 3.402823466e38f;
 
 // behind_scores: page_score_kernel is the kernel ahead, so what it did not write is complete.
@@ -405,30 +439,10 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
   const CacheSeqs& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x / c.Hkv, hk = blockIdx.x - t * c.Hkv;
-  float size = 0.f;  // largest sum |q_e| of a head (loaded while the token's sequence is searched for)
-  if (behind_scores) {
-    const __nv_bfloat16* q = a.q + (static_cast<int64_t>(t) * a.H + hk * a.G) * D;
-    for (int g = warp; g < a.G; g += kWarps) {
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) x += fabsf(__bfloat162float(q[g * D + e * 32 + lane]));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-      size = x == x ? fmaxf(size, x) : INFINITY;
-    }
-  }
-  const int b = token_sequence_group<32>(c.cu, c.B, t, lane, ~0u);
-  int start = 0, n = 0, pages = -1;
-  if (b >= 0) {
-    token_bounds(c.cu, b, c.total, start, n);
-    if (t < start || t >= start + n) {  // offsets that do not ascend
-      if (tid == 0) atomicCAS(c.status, 0, kErrIndex);
-    } else {
-      const int len = keys_of(c, b, hk == 0 && tid == 0);
-      const int sees = min(max(len - n + (t - start) + 1, 0), len);
-      pages = (sees + (1 << c.page_shift) - 1) >> c.page_shift;
-    }
-  }
+  // (loaded while the token's sequence is searched for)
+  float size = behind_scores ? query_size<D>(a, t, hk, warp, kWarps, lane) : 0.f;
+  int b;
+  const int pages = visible_pages(a, t, b, lane, tid == 0, hk == 0);
   const int mid = pages - a.first - a.last, k = a.top - a.first - a.last;  // k of the pages in between
   int32_t* out = a.pages + static_cast<int64_t>(blockIdx.x) * a.top;
   if (behind_scores) wait_for_last_launch();

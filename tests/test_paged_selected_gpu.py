@@ -140,6 +140,14 @@ def test_select(nq, lens, heads):
         s.check(top, first, last)
 
 
+def test_select_of_one_page_more_and_less():
+    """The numbers of pages at which another kernel takes over."""
+    for count in (33, 256, 511, 512, 513, 1024, 1025, 4100):
+        s = Selection([1, 1], [16 * count, 16 * (count // 2) + 1], (4, 2, 64, 16), count)
+        for top, first, last in ((1, 0, 0), (20, 1, 2), (count - 1, 0, 1)):
+            s.check(top, first, last)
+
+
 def test_select_of_many_pages():
     s = Selection([1, 1], [150000, 90001], (8, 2, 64, 16), 3)
     s.check(100, 1, 4)
@@ -163,22 +171,27 @@ def test_select_of_equal_and_nearly_equal_pages():
     big[:, :, :, 2] = tiny[:, None, None]
     s.bounds = big
     s.check(40, 1, 2)
+    s.q[:] = 0.0  # all scores are 0
+    s.check(40, 1, 2)
     few = Selection([1], [16 * 300], heads, 6)
     few.bounds, few.q = big[:few.bounds.shape[0]].clone(), s.q.clone()
     few.check(17, 0, 1)  # all next to the border, ranked in shared memory
     few.bounds[:] = few.bounds[few.table[0, 0].item()].clone()
     few.check(17, 0, 1)
+    few.q[:] = 0.0
+    few.check(17, 0, 1)
 
 
-def test_select_of_scores_that_are_not_finite():
+@pytest.mark.parametrize("count", [100, 512, 513, 700, 1100])
+def test_select_of_scores_that_are_not_finite(count):
     heads = (4, 2, 64, 16)
-    s = Selection([1, 2], [16 * 50, 16 * 700 + 3], heads, 7)
+    s = Selection([1, 2], [16 * 50, 16 * (count - 1) + 3], heads, 7)
     pages = s.table[1].long()
-    s.bounds[pages[100], 0, 1, 3] = float("inf")
-    s.bounds[pages[200], 1, 0, 5] = float("nan")
-    s.bounds[pages[300], 1] = float("nan")
-    s.bounds[pages[400], :, 0] = float("-inf")
-    s.bounds[pages[500]] = 3e38
+    s.bounds[pages[10], 0, 1, 3] = float("inf")
+    s.bounds[pages[20], 1, 0, 5] = float("nan")
+    s.bounds[pages[30], 1] = float("nan")
+    s.bounds[pages[40], :, 0] = float("-inf")
+    s.bounds[pages[50]] = 3e38
     s.check(9, 1, 2)
     s.check(3, 0, 0)
     s.q[0, 0, 0] = float("inf")
