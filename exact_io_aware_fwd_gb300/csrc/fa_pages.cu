@@ -147,19 +147,20 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Bounds
 }
 
 // ---- scores
-// A warp takes 16 pages of one key/value head as the columns of an m16n8k16 product whose rows are
-// queries: [max(q, 0), min(q, 0)] times [hi, lo].  Each lane loads 16 bytes a time straight into
+// A warp takes 16 pages of one key/value head as the rows of an m16n8k16 product whose columns are
+// queries: [hi, lo] times [max(q, 0), min(q, 0)].  Each lane loads 16 bytes a time straight into
 // fragments: which element of a row is which k of the product does not matter as long as both sides
 // agree, so lane l % 4 takes eight neighbouring elements as k = 2c, 2c + 1, 2c + 8, 2c + 9 of two
-// products.
+// products.  (Queries as the rows, twice the products: 16.6 us for 512 rows of up to 256 pages and their
+// selection, this 16.0; all products in one chain 17.3.)
 // (64 sequences of 131072 keys, pages of 64: 112 us; 8 pages a warp 140, 32 123; 4 warps a CTA 115, 8
 // 127.)
-constexpr int kScoreWarps = 2, kScorePages = 16;
+constexpr int kScoreWarps = 2, kScorePages = 16, kScoreCols = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectArgs a, int chunks) {
   constexpr int J = D / 32;  // 16-byte pieces of a lane's part of a row
-  __shared__ float tile[kScoreWarps][16][kScorePages + 1];
+  __shared__ float tile[kScoreWarps][kScorePages][kScoreCols + 1];
   begin_launch();
   const CacheSeqs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -198,72 +199,54 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
       }
     }
   }
-  // tokens of a row tile, or row tiles of a token
-  const int per = a.G <= 16 ? 16 / a.G : 1, tiles = a.G <= 16 ? 1 : (a.G + 15) / 16;
-  const int rows_per = a.G <= 16 ? a.G : 16;
+  // tokens of a tile of columns, or tiles of a token
+  const int per = a.G <= kScoreCols ? kScoreCols / a.G : 1, cols = min(a.G, kScoreCols);
   float* mine = &tile[warp][0][0];
   for (int i0 = 0; i0 < n; i0 += per) {
-    float best = -INFINITY;  // of token `lane / 16`, page lane % 16, where a token has several row tiles
-    for (int rt = 0; rt < tiles; ++rt) {
-      const uint4* q[2];
-      bool live[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int rr = (lane >> 2) + 8 * i;
-        const int tok = i0 + rr / rows_per, g = rt * 16 + rr % rows_per;
-        live[i] = rr < per * rows_per && tok < n && g < a.G;
-        q[i] = reinterpret_cast<const uint4*>(
-                   a.q + ((static_cast<int64_t>(start + (live[i] ? tok : 0))) * a.H + hk * a.G +
-                          (live[i] ? g : 0)) * D) + (lane & 3);
-      }
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    float best = -INFINITY;  // of page `lane` % 16, where a token has several tiles
+    for (int g0 = 0; g0 < a.G; g0 += kScoreCols) {
+      const int col = lane >> 2, tok = i0 + col / cols, g = g0 + col % cols;
+      const bool live = col < per * cols && tok < n && g < a.G;
+      const uint4* q = reinterpret_cast<const uint4*>(
+                           a.q + (static_cast<int64_t>(start + (live ? tok : 0)) * a.H + hk * a.G + (live ? g : 0)) * D) +
+                       (lane & 3);
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, z[3][4] = {};  // four short chains of products
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        uint4 v[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) v[i] = live[i] ? __ldg(q[i] + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t u[4] = {k ? v[0].z : v[0].x, k ? v[1].z : v[1].x, k ? v[0].w : v[0].y,
-                                 k ? v[1].w : v[1].y};
-          uint32_t up[4], dn[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            up[x] = max2(u[x], 0u);
-            dn[x] = min2(u[x], 0u);
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            rows16::mma16816(s[t], up, k ? hi[t][j].z : hi[t][j].x, k ? hi[t][j].w : hi[t][j].y);
-            rows16::mma16816(s[t], dn, k ? lo[t][j].z : lo[t][j].x, k ? lo[t][j].w : lo[t][j].y);
-          }
-        }
+        const uint4 v = live ? __ldg(q + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t h0[4] = {hi[0][j].x, hi[1][j].x, hi[0][j].y, hi[1][j].y};
+        const uint32_t h1[4] = {hi[0][j].z, hi[1][j].z, hi[0][j].w, hi[1][j].w};
+        const uint32_t l0[4] = {lo[0][j].x, lo[1][j].x, lo[0][j].y, lo[1][j].y};
+        const uint32_t l1[4] = {lo[0][j].z, lo[1][j].z, lo[0][j].w, lo[1][j].w};
+        rows16::mma16816(s, h0, max2(v.x, 0u), max2(v.y, 0u));
+        rows16::mma16816(z[0], l0, min2(v.x, 0u), min2(v.y, 0u));
+        rows16::mma16816(z[1], h1, max2(v.z, 0u), max2(v.w, 0u));
+        rows16::mma16816(z[2], l1, min2(v.z, 0u), min2(v.w, 0u));
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] = (s[k] + z[1][k]) + (z[0][k] + z[2][k]);
       __syncwarp();  // the last tile has been read
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = (lane >> 2) + 8 * (k >> 1), col = 8 * t + (lane & 3) * 2 + (k & 1);
-          const float x = s[t][k];
-          // a score that is not a number counts as infinity; a row without a query as nothing
-          mine[row * (kScorePages + 1) + col] = live[k >> 1] ? (x == x ? x : INFINITY) : -INFINITY;
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int row = (lane >> 2) + 8 * (k >> 1), at = (lane & 3) * 2 + (k & 1);
+        // a score that is not a number counts as infinity
+        mine[row * (kScoreCols + 1) + at] = s[k] == s[k] ? s[k] : INFINITY;
+      }
       __syncwarp();
-      for (int o = lane; o < per * 16; o += 32) {
-        const int tt = o >> 4, col = o & 15;
+      for (int o = lane; o < per * kScorePages; o += 32) {
+        const int tt = o / kScorePages, page = o % kScorePages, here = min(cols, a.G - g0);
         float m = -INFINITY;
-        for (int r = 0; r < rows_per; ++r) m = fmaxf(m, mine[(tt * rows_per + r) * (kScorePages + 1) + col]);
-        if (tiles > 1) {
+        for (int x = 0; x < here; ++x) m = fmaxf(m, mine[page * (kScoreCols + 1) + tt * cols + x]);
+        if (a.G > kScoreCols) {
           m = best = fmaxf(best, m);
-          if (rt + 1 < tiles) continue;
+          if (g0 + kScoreCols < a.G) continue;
         }
-        if (i0 + tt < n && p0 + col < pages)
-          a.score[(static_cast<int64_t>(start + i0 + tt) * c.Hkv + hk) * a.max_pages + p0 + col] = m;
+        if (i0 + tt < n && p0 + page < pages)
+          a.score[(static_cast<int64_t>(start + i0 + tt) * c.Hkv + hk) * a.max_pages + p0 + page] = m;
       }
     }
   }
-  uint32_t most = 0;  // largest |bound|, as bits: NaN is above infinity
+  uint32_t most = 0;  // largest |bound| (NaN, if one is)
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -271,9 +254,9 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
       const uint32_t u[8] = {lo[t][j].x, lo[t][j].y, lo[t][j].z, lo[t][j].w,
                              hi[t][j].x, hi[t][j].y, hi[t][j].z, hi[t][j].w};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) most = __vmaxu2(most, u[k] & 0x7fff7fffu);
+      for (int k = 0; k < 8; ++k) most = bits2(__hmax2_nan(pair2(most), __habs2(pair2(u[k]))));
     }
-  most = max(most & 0xffffu, most >> 16);
+  most = max(most & 0x7fffu, most >> 16 & 0x7fffu);  // as bits: NaN is above infinity
   most = __reduce_max_sync(~0u, most);
   if (lane == 0)
     a.reach[static_cast<int64_t>(bh) * ((a.max_pages + kScorePages - 1) / kScorePages) + p0 / kScorePages] =
