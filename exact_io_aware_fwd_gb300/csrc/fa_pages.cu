@@ -26,6 +26,16 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return bits2(__hmax2_nan(pair2(a), pair2(b)));
 }
 
+// 16 bytes that nobody reads again: not kept in L1, and fetched from memory 256 bytes at a time (the
+// scores of 512 rows of up to 256 pages and their selection, cold caches: 18.7 us, plain loads 19.9).
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // ---- the mask of a tree: a thread follows its token's parents, whose indices descend, and writes
 // the words of its row from the last to the first.
 constexpr int kTreeThreads = 128;
@@ -152,7 +162,7 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Bounds
 // fragments: which element of a row is which k of the product does not matter as long as both sides
 // agree, so lane l % 4 takes eight neighbouring elements as k = 2c, 2c + 1, 2c + 8, 2c + 9 of two
 // products.  (Queries as the rows, twice the products: 16.6 us for 512 rows of up to 256 pages and their
-// selection, this 16.0; all products in one chain 17.3.)
+// selection from L2, this 16.0; all products in one chain 17.3.)
 // (64 sequences of 131072 keys, pages of 64: 112 us; 8 pages a warp 140, 32 123; 4 warps a CTA 115, 8
 // 127.)
 constexpr int kScoreWarps = 2, kScorePages = 16, kScoreCols = 8;
@@ -194,8 +204,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
     for (int j = 0; j < J; ++j) {
       lo[t][j] = hi[t][j] = make_uint4(0u, 0u, 0u, 0u);
       if (phys[t] >= 0) {
-        lo[t][j] = __ldg(src + 4 * j);
-        hi[t][j] = __ldg(src + D / 8 + 4 * j);
+        lo[t][j] = load_once(src + 4 * j);
+        hi[t][j] = load_once(src + D / 8 + 4 * j);
       }
     }
   }
