@@ -470,9 +470,11 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
   __syncthreads();
   far = __uint_as_float(__reduce_max_sync(~0u, lane < kWarps ? __float_as_uint(red[0][lane]) : 0u));
   size = __uint_as_float(__reduce_max_sync(~0u, lane < kWarps ? __float_as_uint(red[1][lane]) : 0u));
-  const float delta = far * size * 0x1p-15f;
-  // something is not finite, or too large to be scaled below 1: every score in 64 bits
-  const bool odd = !(delta < INFINITY && far < 0x1p126f && size < 0x1p126f);
+  // (what is added: sums below the smallest normal number have no such relative error)
+  const float delta = fmaf(far * size, 0x1p-15f, 0x1p-117f);
+  // something is not finite, too large to be scaled below 1, or so large that a score with 2 delta
+  // added might not be finite: every score in 64 bits
+  const bool odd = !(far * size < 0x1p126f && far < 0x1p126f && size < 0x1p126f);
 
   float above = kMost, below = -INFINITY;  // in, and at least in question
   if (!odd) {

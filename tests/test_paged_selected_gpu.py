@@ -204,6 +204,30 @@ def test_select_of_scores_that_are_not_finite(count):
     assert got[1, 1].tolist() == [0, 1, 2, 3, 4, P - 1]
 
 
+@pytest.mark.parametrize("count", [60, 900, 1500, 5000])
+def test_select_of_scores_near_the_largest_number(count):
+    """The k-th score plus twice its error bound is not finite: 4 + 2^-6 times the largest bf16 below
+    2^126 is 2^128 (1 - 2^-16), and the bound is 2^-15 of it."""
+    s = Selection([1], [16 * count], (2, 1, 64, 16), count)
+    s.q[:] = 0.0
+    s.q[0, :, 3], s.q[0, :, 40] = 4.0, 2.0 ** -6
+    s.bounds[:] = 0.0
+    s.bounds[:, :, :, 3] = s.bounds[:, :, :, 40] = 1.9921875 * 2.0 ** 125
+    s.check(50, 1, 2)  # all equal
+    s.bounds[s.table[0, 20:40].long()] = 0.0
+    s.check(50, 1, 2)
+
+
+@pytest.mark.parametrize("count", [60, 700, 1500])
+def test_select_of_scores_below_the_smallest_normal_number(count):
+    """Products of 2^-130 have few bits left in float32, and those of 2^-150 none."""
+    s = Selection([1, 2], [16 * count, 16 * count - 5], (4, 2, 64, 16), count)
+    q, bounds = s.q, s.bounds
+    for at, by in ((-20, -110), (-10, -130), (20, -130), (-70, -60), (-100, -100)):
+        s.q, s.bounds = q * 2.0 ** at, bounds * 2.0 ** by
+        s.check(30, 1, 2)
+
+
 def test_select_in_a_graph_and_on_another_stream():
     s = Selection([1, 3], [3000, 9000], (8, 2, 128, 16), 8)
     args = (s.q.to(DEV), s.bounds.to(DEV), s.table.to(DEV), i32(s.lens), 16, 20, 1, 2)
