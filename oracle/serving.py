@@ -167,5 +167,6 @@ def evict(weights, n, budget, recent):
     """Indices of the keys of one sequence and head that stay, ascending."""
     if n <= budget:
         return np.arange(n)
-    w = np.where(np.isnan(weights[:n - recent]), np.inf, weights[:n - recent])
-    return np.concatenate([largest(w, budget - recent), np.arange(n - recent, n)])
+    w, nan = weights[:n - recent], np.isnan(weights[:n - recent])  # a NaN is above infinity
+    best = np.lexsort((np.arange(len(w)), -np.where(nan, np.inf, w), ~nan))[:budget - recent]
+    return np.concatenate([np.sort(best), np.arange(n - recent, n)])

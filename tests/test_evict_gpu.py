@@ -244,7 +244,9 @@ def test_evict_of_equal_zero_and_odd_weights():
     odd[0, 0, 5:900:7] = float("nan")
     odd[0, 1, 3:800:9] = float("inf")
     odd[0, :, 4:800:11] = float("-inf")
-    for w in cases + [signed, odd]:
+    mixed = odd.clone()
+    mixed[0, :, 6:700:5], mixed[0, :, 2:900:8] = float("inf"), float("nan")
+    for w in cases + [signed, odd, mixed]:
         for budget in (1, 100, 1500, 2999):
             Evicted([n], 2, 64, 16, budget, 4, w).check(min(10, budget))
 
