@@ -13,8 +13,8 @@ namespace {
 // and head is a CTA's, or, where a CTA's registers (kRounds weights a thread) do not hold its
 // weights, a cluster's, each CTA with a stretch of them; only what does not fit eight CTAs is read
 // again in every pass.
-// Clusters of more than eight CTAs do not all run at once (16 of 512 threads: 37 us for 8 heads of
-// 131072 keys, 8 of 1024: 20).
+// Clusters of more than eight CTAs do not all run at once (the selection of 8 heads of 131072 keys, cold:
+// 16 of 512 threads 37 us, 8 of 1024 20).
 constexpr int kRounds = 8, kMoreRounds = 16;
 constexpr int evict_cluster(int max_len, int threads) {
   int c = 2;
@@ -101,11 +101,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
           }
         }
         cluster_sync();
-        for (int p = 0; p < rank; ++p) {
-          const uint2 v = peer_load2(totals, p);
-          over0 += v.x;
-          tie0 += v.y;
-        }
+        const int p = tid & 31;
+        const uint2 v = p < rank ? peer_load2(totals, p) : make_uint2(0u, 0u);
+        over0 = __reduce_add_sync(~0u, v.x);
+        tie0 = __reduce_add_sync(~0u, v.y);
+        cluster_arrive();  // nothing of another CTA's is read any more
       }
     }
 #pragma unroll
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     tie0 += total >> 16;
     __syncthreads();  // the counts have been read
   }
-  if constexpr (kCluster) cluster_sync();  // nobody leaves while others read its shared memory
+  if constexpr (kCluster) cluster_wait();  // nobody leaves while others read its shared memory
 }
 
 // ---- eviction: the copies
