@@ -5,6 +5,8 @@
 // is at least q.k for every key of the page: the cheapest score that no key of the page can beat.
 // It costs two rows a page instead of page_size of them.  The page's score for a key/value head is
 // the largest over its group's queries, because the group reads one list of pages.
+#include <algorithm>
+
 #include "fa_cache.h"
 #include "fa_internal.h"
 #include "paged_rows.cuh"
@@ -26,13 +28,15 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return bits2(__hmax2_nan(pair2(a), pair2(b)));
 }
 
-// 16 bytes that nobody reads again: not kept in L1, and fetched from memory 256 bytes at a time (the
-// scores of 512 rows of up to 256 pages and their selection, cold caches: 18.7 us, plain loads 19.9).
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
+// 16 bytes of global memory into shared memory, fetched from memory 256 bytes at a time; zeros where
+// there are none.
+__device__ __forceinline__ void fetch_once(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 from_shared(uint32_t at) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
   return v;
 }
 
@@ -158,19 +162,23 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Bounds
 
 // ---- scores
 // A warp takes 16 pages of one key/value head as the rows of an m16n8k16 product whose columns are
-// queries: [hi, lo] times [max(q, 0), min(q, 0)].  Each lane loads 16 bytes a time straight into
-// fragments: which element of a row is which k of the product does not matter as long as both sides
-// agree, so lane l % 4 takes eight neighbouring elements as k = 2c, 2c + 1, 2c + 8, 2c + 9 of two
-// products.  (Queries as the rows, twice the products: 16.6 us for 512 rows of up to 256 pages and their
-// selection from L2, this 16.0; all products in one chain 17.3.)
-// (64 sequences of 131072 keys, pages of 64: 112 us; 8 pages a warp 140, 32 123; 4 warps a CTA 115, 8
-// 127.)
+// queries: [hi, lo] times [max(q, 0), min(q, 0)].  Which element of a row is which k of the product does
+// not matter as long as both sides agree, so lane l % 4 takes eight neighbouring elements, 16 bytes, as
+// k = 2c, 2c + 1, 2c + 8, 2c + 9 of two products, and each lane reads what it fetched itself.
+// Bound by reading the bounds once.  The bytes on the way wait in shared memory, 24 warps of 8 KB an SM
+// (d = 128); in registers it is 18: 18.6 us for 512 rows of up to 256 pages and their selection, cold
+// caches, this 17.6, and of that this kernel takes 9; 64 sequences of 131072 keys 182 and 171 us.
+// (Before that: queries as the rows, twice the products, 4% slower, all products in one chain 8%, 8
+// pages a warp 25%, 32 10%; 4 warps a CTA and 2 are the same.)
 constexpr int kScoreWarps = 2, kScorePages = 16, kScoreCols = 8;
 
-template <int D>
+// kKeep: the bounds, read by many tiles of queries, stay in registers, of which they take most (2
+// sequences of 128 new tokens and 131072 keys: 190 us, from shared memory 261).
+template <int D, bool kKeep>
 __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const SelectArgs a, int chunks) {
   constexpr int J = D / 32;  // 16-byte pieces of a lane's part of a row
   __shared__ float tile[kScoreWarps][kScorePages][kScoreCols + 1];
+  __shared__ uint4 box[kScoreWarps][4 * J][32];  // what each lane fetched: lo, hi of both its pages
   begin_launch();
   const CacheSeqs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,7 +197,12 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
   token_bounds(c.cu, b, c.total, start, n);
   const int pages = (len + (1 << c.page_shift) - 1) >> c.page_shift;
   if (p0 >= pages || n == 0) return;
-  uint4 lo[2][J], hi[2][J];
+  const uint32_t own = smem_u32(&box[warp][0][lane]);
+  uint4 kept[kKeep ? 4 * J : 1];
+  auto bound = [&](int t, int high, int j) {
+    const int x = (t * 2 + high) * J + j;
+    return kKeep ? kept[kKeep ? x : 0] : from_shared(own + x * 512);
+  };
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     if (p0 + 8 * t + (lane >> 2) >= pages) {
@@ -201,17 +214,19 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
     const uint4* src = reinterpret_cast<const uint4*>(
                            a.bounds + (static_cast<int64_t>(max(phys[t], 0)) * c.Hkv + hk) * 2 * D) + (lane & 3);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      lo[t][j] = hi[t][j] = make_uint4(0u, 0u, 0u, 0u);
-      if (phys[t] >= 0) {
-        lo[t][j] = load_once(src + 4 * j);
-        hi[t][j] = load_once(src + D / 8 + 4 * j);
-      }
-    }
+    for (int x = 0; x < 2 * J; ++x)
+      fetch_once(own + (t * 2 * J + x) * 512, src + x / J * (D / 8) + x % J * 4, phys[t] >= 0);
   }
+  rows16::cp_commit();
   // tokens of a tile of columns, or tiles of a token
   const int per = a.G <= kScoreCols ? kScoreCols / a.G : 1, cols = min(a.G, kScoreCols);
   float* mine = &tile[warp][0][0];
+  bool landed = kKeep;
+  if (kKeep) {
+    rows16::cp_wait<0>();  // (each lane reads what it fetched itself)
+#pragma unroll
+    for (int x = 0; x < 4 * J; ++x) kept[kKeep ? x : 0] = from_shared(own + x * 512);
+  }
   for (int i0 = 0; i0 < n; i0 += per) {
     float best = -INFINITY;  // of page `lane` % 16, where a token has several tiles
     for (int g0 = 0; g0 < a.G; g0 += kScoreCols) {
@@ -220,14 +235,19 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
       const uint4* q = reinterpret_cast<const uint4*>(
                            a.q + (static_cast<int64_t>(start + (live ? tok : 0)) * a.H + hk * a.G + (live ? g : 0)) * D) +
                        (lane & 3);
+      uint4 w[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) w[j] = live ? __ldg(q + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
+      if (!landed) rows16::cp_wait<0>();
+      landed = true;
       float s[4] = {0.f, 0.f, 0.f, 0.f}, z[3][4] = {};  // four short chains of products
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const uint4 v = live ? __ldg(q + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t h0[4] = {hi[0][j].x, hi[1][j].x, hi[0][j].y, hi[1][j].y};
-        const uint32_t h1[4] = {hi[0][j].z, hi[1][j].z, hi[0][j].w, hi[1][j].w};
-        const uint32_t l0[4] = {lo[0][j].x, lo[1][j].x, lo[0][j].y, lo[1][j].y};
-        const uint32_t l1[4] = {lo[0][j].z, lo[1][j].z, lo[0][j].w, lo[1][j].w};
+        const uint4 v = w[j], hi0 = bound(0, 1, j), hi1 = bound(1, 1, j), lo0 = bound(0, 0, j), lo1 = bound(1, 0, j);
+        const uint32_t h0[4] = {hi0.x, hi1.x, hi0.y, hi1.y};
+        const uint32_t h1[4] = {hi0.z, hi1.z, hi0.w, hi1.w};
+        const uint32_t l0[4] = {lo0.x, lo1.x, lo0.y, lo1.y};
+        const uint32_t l1[4] = {lo0.z, lo1.z, lo0.w, lo1.w};
         rows16::mma16816(s, h0, max2(v.x, 0u), max2(v.y, 0u));
         rows16::mma16816(z[0], l0, min2(v.x, 0u), min2(v.y, 0u));
         rows16::mma16816(z[1], h1, max2(v.z, 0u), max2(v.w, 0u));
@@ -261,8 +281,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) page_score_kernel(const Sele
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const uint32_t u[8] = {lo[t][j].x, lo[t][j].y, lo[t][j].z, lo[t][j].w,
-                             hi[t][j].x, hi[t][j].y, hi[t][j].z, hi[t][j].w};
+      const uint4 lo = bound(t, 0, j), hi = bound(t, 1, j);
+      const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
       for (int k = 0; k < 8; ++k) most = bits2(__hmax2_nan(pair2(most), __habs2(pair2(u[k]))));
     }
@@ -616,7 +636,10 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.c.B) * static_cast<unsigned>(a.c.Hkv) * static_cast<unsigned>(chunks);
   const bool scores = a.max_pages > a.top && a.top > a.first + a.last;  // else nobody chooses
   if (scores) {
-    const cudaError_t e = launch_chained(page_score_kernel<D>, grid, 32 * kScoreWarps, 0, s, a, chunks);
+    // more queries of a sequence than one tile has
+    const bool many = static_cast<int64_t>(a.c.total) * a.G > static_cast<int64_t>(a.c.B) * std::max(kScoreCols, a.G);
+    const cudaError_t e = many ? launch_chained(page_score_kernel<D, true>, grid, 32 * kScoreWarps, 0, s, a, chunks)
+                               : launch_chained(page_score_kernel<D, false>, grid, 32 * kScoreWarps, 0, s, a, chunks);
     if (e != cudaSuccess) return e;
   }
   const unsigned rows = static_cast<unsigned>(a.c.total) * static_cast<unsigned>(a.c.Hkv);
