@@ -152,7 +152,7 @@ fa_status fa_kv_weights(const void* Q, const float* LSE, const fa_paged_kv* cach
   // the index of a (token, head) row, and the units of the launch
   const int len = max_kv < capacity ? max_kv : capacity;
   if (!fits(total, H, 1) || static_cast<long long>(total) * (H / Hkv) > fa::kWeightsRows ||
-      !fits(B, Hkv, len / 128 + 1) || static_cast<long long>(cache->num_pages) * Hkv > kMaxInt)
+      !fits(B, Hkv, len / 128 + 3) || static_cast<long long>(cache->num_pages) * Hkv > kMaxInt)
     return FA_ERR_UNSUPPORTED;
   fa::PagedArgs a{};
   if ((st = device_ready(a.status)) != FA_OK) return st;

@@ -28,7 +28,6 @@ constexpr int kWarps = 4 * kGroups;
 constexpr int kThreads = 128 + 32 * kWarps;  // warp 0: TMA, 1: MMA, 2: pieces, 3: columns past the keys
 constexpr int KT = 128;        // keys of a tile
 constexpr int NQ = 128;        // queries of a job
-constexpr int kAllRows = 1 << 30;  // the plan knows one row tile: a piece has all of its queries
 constexpr int kRing = 4;
 constexpr int kStats = 4;  // jobs whose queries' statistics are kept: a warp may be three ahead of another
 constexpr float kLog2e = 1.4426950408889634f;
@@ -116,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Walk<kAllRows, KT> walk(a, l, shares[0]);
       const Entry& e = walk.e;
       Piece piece;
-      int n = 0;  // key tiles; a sequence without keys has none
+      int n = 0;  // key tiles; none of a sequence without keys, or behind the last key
       for (int i = 0;; ++i) {
         bool more;
         while ((more = walk.next(a, l, piece)) && (n = min(piece.te, (e.len + KT - 1) / KT) - piece.ta) <= 0) {
