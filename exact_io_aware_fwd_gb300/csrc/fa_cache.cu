@@ -175,6 +175,9 @@ fa_status fa_kv_weights(const void* Q, const float* LSE, const fa_paged_kv* cach
   l.max_pages = cache->max_pages;
   l.max_len = len;
   l.max_q = max_q;
+  // (one token of 64 sequences of 512 to 4096 keys: 56.8 us, with 0 58.8; 256 such sequences 206 and 211;
+  // the CTAs' times fit 0.9 to 1.1 tiles a segment at 4 queries and 2.2 at 128)
+  l.extra = static_cast<long long>(total) * a.G >= 64LL * B ? 2 : 1;
   const fa::WeightsOut w{LSE, weights, out, capacity, causal != 0};
   return status_of(fa::launch_kv_weights(d, tk, a, w, fa::wait_timeout_ns(), static_cast<cudaStream_t>(stream)));
 }

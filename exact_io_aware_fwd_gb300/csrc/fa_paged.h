@@ -186,6 +186,7 @@ struct KeyList {
   int causal;
   int mma;                  // row tiles and key tiles of the tensor-core kernel
   int unsplit;              // no segment is split where none has more key tiles
+  int extra;                // key tiles that a segment counts besides its own
 };
 
 // Partial results of one list.  Its rows (query token x head of the key/value head's group) are

@@ -27,6 +27,7 @@ constexpr int kGroups = 2;  // warpgroups of weights (four: 43.0 us for 8 x 32 t
 constexpr int kWarps = 4 * kGroups;
 constexpr int kThreads = 128 + 32 * kWarps;  // warp 0: TMA, 1: MMA, 2: pieces, 3: columns past the keys
 constexpr int KT = 128;        // keys of a tile
+constexpr int kAllRows = 1 << 30;  // the plan knows one row tile: a piece has all of its queries
 constexpr int NQ = 128;        // queries of a job
 constexpr int kRing = 4;
 constexpr int kStats = 4;  // jobs whose queries' statistics are kept: a warp may be three ahead of another

@@ -42,28 +42,25 @@ struct Entry {
   int start, n, nc;  // first token, new tokens, and how many of them are computed
   int len;           // keys (clamped)
   int rt;            // row tiles (0: no tokens)
-  int tiles;         // key tiles of all its row tiles, for one key/value head
+  int tiles;         // units of all its row tiles, for one key/value head
 };
 
 // Keys that row `row` (new token x group member) of an entry sees.
 __host__ __device__ __forceinline__ int row_limit(const Entry& e, int causal, int G, int row) {
   return causal ? min(e.len, e.len - e.n + row / G + 1) : e.len;
 }
-// R of the kernel that takes all of an entry's rows at once (weights of keys).  Its segments are longer by
-// what one costs besides its keys: the way from one to the next, and the queries to load.  A worker that
-// gets the tiles behind the last key passes over them.  (One token of 64 sequences of 512 to 4096 keys:
-// 56.8 us, without 58.8; 256 such sequences 206 and 211; the workers' times fit 0.9 to 1.1 tiles a
-// segment at 4 queries and 2.2 at 128.)
-constexpr int kAllRows = 1 << 30;
-template <int R>
-__host__ __device__ __forceinline__ int segment_cost(const Entry& e, int G) {
-  return R != kAllRows ? 0 : (e.nc * G < 64 ? 1 : 2);
-}
 // Key tiles of row tile r (at least one, so that a tile without keys is visited and written).
 template <int R, int KT>
 __host__ __device__ __forceinline__ int tiles_of(const Entry& e, int causal, int G, int r) {
   const int last = min(e.nc * G, (r + 1) * R) - 1;
-  return max(1, (row_limit(e, causal, G, last) + KT - 1) / KT) + segment_cost<R>(e, G);
+  return max(1, (row_limit(e, causal, G, last) + KT - 1) / KT);
+}
+// The units that they count: where a segment costs much besides its keys (its queries to load, its result
+// to write, the way to the next one), a list says how many tiles that is worth.  Whoever gets them
+// finds no keys there.
+template <int R, int KT>
+__host__ __device__ __forceinline__ int units_of(const KeyList& l, const Entry& e, int G, int r) {
+  return tiles_of<R, KT>(e, l.causal, G, r) + l.extra;
 }
 
 template <int R, int KT>
@@ -103,9 +100,9 @@ __host__ __device__ __forceinline__ Entry entry_of(const KeyList& l, const Paged
   e.rt = (e.nc * a.G + R - 1) / R;
   if (l.causal && e.n > 1) {
     e.tiles = 0;
-    for (int r = 0; r < e.rt; ++r) e.tiles += tiles_of<R, KT>(e, 1, a.G, r);
+    for (int r = 0; r < e.rt; ++r) e.tiles += units_of<R, KT>(l, e, a.G, r);
   } else {
-    e.tiles = e.rt * (max(1, (e.len + KT - 1) / KT) + segment_cost<R>(e, a.G));
+    e.tiles = e.rt * (max(1, (e.len + KT - 1) / KT) + l.extra);
   }
   return e;
 }
@@ -297,7 +294,7 @@ struct Walk {
       r = rem;
       return;
     }
-    for (int n; rem >= (n = tiles_of<R, KT>(e, l.causal, a.G, r)); ++r) rem -= n;
+    for (int n; rem >= (n = units_of<R, KT>(l, e, a.G, r)); ++r) rem -= n;
     te = rem + 1;
   }
   __host__ __device__ bool next(const PagedArgs& a, const KeyList& l, Piece& p) {
@@ -314,7 +311,7 @@ struct Walk {
     }
     p.hk = hk;
     p.r = r--;
-    p.tiles = tiles_of<R, KT>(e, l.causal, a.G, p.r);
+    p.tiles = units_of<R, KT>(l, e, a.G, p.r);
     if (direct) {
       p.ta = 0;
       p.te = p.tiles;

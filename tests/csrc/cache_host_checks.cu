@@ -29,7 +29,7 @@ static int sequence_of(const int32_t* cu, int B, int total, int shift, int slot)
 
 // The pieces of all workers, as weights_kernel takes them.
 static void pieces(const fa::PagedArgs& a, int workers) {
-  constexpr int R = fa::kAllRows, KT = 128;
+  constexpr int R = 1 << 30, KT = 128;
   const fa::KeyList& l = a.list[0];
   std::vector<fa::Entry> e;
   std::vector<int> first(1, 0);  // units ahead of entry b
@@ -117,6 +117,7 @@ int main() {
     l.lens = lens.data();
     l.max_pages = 2000;
     l.max_len = random(4) == 0 ? 500 : 32000;
+    l.extra = random(3);
     l.max_q = random(4) == 0 ? 2 : 0x7fffffff;
     for (int workers : {1, 1 + random(152), 152}) pieces(a, workers);
   }
