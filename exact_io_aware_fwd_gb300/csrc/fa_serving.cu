@@ -85,10 +85,12 @@ constexpr float mma_tile_cost(int d) { return d == 64 ? 30.f : 20.f; }
 // Key tiles that a segment of the tensor-core kernel counts besides its own in a call with a tree: a CTA
 // takes 7.4 us longer for each piece of its share, as for 3.6 key tiles (queries to load, the pipeline
 // to empty and fill, a result to write).  32 trees of 48 to 64 tokens, 8 heads and 2048 to 8192 keys:
-// 168.0 us, with 0 179.8, 3 168.3, 6 170.6; 64 of them over 512 to 2048 keys 131 and 148; of 20 to 30
-// tokens (64 over 2048 to 8192 keys) 237 and 252.  Calls without a mask keep their division of the work,
-// and with it their results bit for bit.
-constexpr int kTreeExtra = 4;
+// 162.1 us (with 3 163.0, 2 165.3, 0 172.9); 64 of them over 512 to 2048 keys 128 and, with 0, 144; of 20
+// to 30 tokens, 64 over 2048 to 8192 keys, 236 and 251.  With fewer sequences and heads than CTAs the
+// parts are what costs: 4 trees over 700 keys 22.3 us, with 2 20.6, over 2000 26.3 and 24.6 (with 0
+// 28.9).  Calls without a mask keep their division of the work, and with it their results
+// bit for bit.
+int tree_extra(int B, int Hkv) { return static_cast<long long>(B) * Hkv >= fa::kPagedCtas ? 4 : 2; }
 
 // Few rows: whether a CTA takes whole segments, its warps an eighth of the keys each, so that there
 // is nothing to join.  With a segment per SM at most, up to 1024 keys (d = 128, 8 heads, split and
@@ -222,7 +224,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     const long long keys = i == 0 ? max_kv : prefix->max_len;
     units[i] = Hkv * static_cast<long long>(fa::row_tiles_bound(
                          total, H / Hkv, mma[i] ? fa::kPagedMmaRows : fa::kPagedRows, count[i])) *
-               (keys / (mma[i] ? fa::kPagedMmaKeys : fa::kPagedKeys) + 1 + (tree != nullptr && mma[i] ? kTreeExtra : 0));
+               (keys / (mma[i] ? fa::kPagedMmaKeys : fa::kPagedKeys) + 1 + (tree != nullptr && mma[i] ? tree_extra(B, Hkv) : 0));
     if (units[i] > kMaxInt) return FA_ERR_UNSUPPORTED;
   }
   const PagedWorkspace w = paged_workspace(count, lists, total, H, Hkv, d);
@@ -279,7 +281,7 @@ fa_status paged_impl(const void* Q, const fa_paged_kv* cache, const fa_prefix* p
     l.causal = i == 0 && causal ? 1 : 0;
     l.mma = mma[i];
     l.unsplit = unsplit_keys(mma[i], l.count, Hkv) / (mma[i] ? fa::kPagedMmaKeys : fa::kPagedKeys);
-    l.extra = tree != nullptr && mma[i] ? kTreeExtra : 0;
+    l.extra = tree != nullptr && mma[i] ? tree_extra(B, Hkv) : 0;
     a.rowbuf[i] = lists > 1 ? reinterpret_cast<float*>(base + w.rowbuf[i]) : nullptr;
     fa::PartialLayout& p = a.part[i];
     p.R = mma[i] ? fa::kPagedMmaRows : fa::kPagedRows;

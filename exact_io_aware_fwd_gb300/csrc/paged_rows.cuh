@@ -194,7 +194,7 @@ __device__ __forceinline__ SelectedSource selected_source(const PagedArgs& a, co
   s.hk = p.hk;
   s.first = p.ta;
   s.at = at;
-  const int t = w.e.start, most = min(p.te, (l.max_len + KT - 1) / KT) - p.ta;
+  const int t = w.e.start, most = max(min(p.te, (l.max_len + KT - 1) / KT) - p.ta, 0);
   s.list = a.pages + (static_cast<int64_t>(t) * a.Hkv + p.hk) * a.top;
   const int i = listed_page(a, s, 0, most, lane);
   const int b = token_sequence_group<32>(a.seq_cu, a.seqs, t, lane, ~0u);
