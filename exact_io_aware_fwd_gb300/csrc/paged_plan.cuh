@@ -72,7 +72,7 @@ __host__ __device__ __forceinline__ Entry entry_of(const KeyList& l, const Paged
     e.n = e.nc = 1;
     e.len = l.max_len;
     e.rt = (a.G + R - 1) / R;
-    e.tiles = e.rt * max(1, (e.len + KT - 1) / KT);
+    e.tiles = e.rt * (max(1, (e.len + KT - 1) / KT) + l.extra);
     return e;
   }
   const int len = device_load(l.lens + b);  // ahead of the branches: one wait for all of the loads

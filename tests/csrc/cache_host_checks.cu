@@ -120,6 +120,19 @@ int main() {
     l.extra = random(3);
     l.max_q = random(4) == 0 ? 2 : 0x7fffffff;
     for (int workers : {1, 1 + random(152), 152}) pieces(a, workers);
+    // an entry's units are those of its row tiles, of sequences and of tokens alone
+    fa::KeyList tokens = l;
+    tokens.lens = nullptr;
+    for (const fa::KeyList& x : {l, tokens})
+      for (int causal : {0, 1}) {
+        fa::KeyList y = x;
+        y.causal = causal && x.lens != nullptr;
+        const int b = random(B);
+        const fa::Entry e = fa::entry_of<16, 16>(y, a, b, false);
+        int units = 0;
+        for (int r = 0; r < e.rt; ++r) units += fa::units_of<16, 16>(y, e, a.G, r);
+        CHECK(e.tiles == units);
+      }
   }
   std::printf(failures == 0 ? "ok\n" : "%d failures\n", failures);
   return failures == 0 ? 0 : 1;
