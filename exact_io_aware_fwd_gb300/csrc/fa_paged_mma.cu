@@ -111,8 +111,9 @@ __device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, in
 // stage is free only two positions later (211 us with K and V together).
 // M: kAllKeys, or kTreeKeys (one list).
 // A warp's results leave for the workspace 32 bytes a thread at a time, whole sectors (32 trees of 48 to 64
-// tokens over 2048 to 8192 keys: 165.6 us, 168.4 with 16), and the queries of the next pieces are fetched
-// into L2 (167.8; of a tree, with the slack in the maximum, all three: 162.8).
+// tokens over 2048 to 8192 keys: 165.6 us, 168.4 with 16).  Of a tree, the queries of the next pieces are
+// fetched into L2 (167.8; with the slack in the maximum, all three: 162.8).  With two lists that is
+// slower (128 sequences behind two prefixes of 32768 keys 137.5 us, without 136.0).
 template <int D, int kLists, bool kTwin, KeyMode M>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -215,45 +216,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (few_rows) {
     } else if (warp == 2) {
-      // ================= the CTA's pieces, and their queries on the way to L2
-      Walk<R, KT> walk(a, l, sh);
-      const Entry& e = walk.e;
-      Piece piece;
-      for (int i = 0;; ++i) {
-        const bool more = walk.next(a, l, piece);
-        if (!mbar_wait_warp(&piece_empty[i % kRing], ((i / kRing) & 1) ^ 1, ctl)) break;
-        if (lane == 0) {
-          PieceInfo& p = pieces[i % kRing];
-          if (more) {
-            const int n0 = tiles_in_piece(e, piece, l.causal, a.G, 0);
-            p.n[0] = kTwin ? (n0 + 1) / 2 : n0;
-            p.n[1] = kTwin ? n0 / 2 : tiles_in_piece(e, piece, l.causal, a.G, 1);
-            p.ta = piece.ta;
-            p.hk = piece.hk;
-            p.row0 = piece.r * R;
-            p.start = e.start;
-            p.rows = e.nc * a.G;
-            p.len = e.len;
-            p.shift = e.len - e.n;
-            p.tile = row_tile0(e.start, a.G, R, walk.b) + piece.r;
-            p.whole = piece.whole;
-            p.table = l.table + static_cast<int64_t>(walk.b) * l.max_pages;
-            if (piece.ta == 0)  // this CTA begins the segment
-              part.spans[static_cast<int64_t>(piece.hk) * part.span_tiles + p.tile] =
-                  span_of(sh, piece);
-          } else {
-            p.n[0] = p.n[1] = -1;
+      // ================= the CTA's pieces; of a tree, with their queries on the way to L2
+      constexpr bool kFetch = M == kTreeKeys;
+      if (kFetch || lane == 0) {
+        Walk<R, KT> walk(a, l, sh);
+        const Entry& e = walk.e;
+        Piece piece;
+        for (int i = 0;; ++i) {
+          const bool more = walk.next(a, l, piece);
+          const uint32_t parity = ((i / kRing) & 1) ^ 1;
+          if (!(kFetch ? mbar_wait_warp(&piece_empty[i % kRing], parity, ctl)
+                       : mbar_wait(&piece_empty[i % kRing], parity, ctl)))
+            break;
+          if (lane == 0) {
+            PieceInfo& p = pieces[i % kRing];
+            if (more) {
+              const int n0 = tiles_in_piece(e, piece, l.causal, a.G, 0);
+              p.n[0] = kTwin ? (n0 + 1) / 2 : n0;
+              p.n[1] = kTwin ? n0 / 2 : tiles_in_piece(e, piece, l.causal, a.G, 1);
+              p.ta = piece.ta;
+              p.hk = piece.hk;
+              p.row0 = piece.r * R;
+              p.start = e.start;
+              p.rows = e.nc * a.G;
+              p.len = e.len;
+              p.shift = e.len - e.n;
+              p.tile = row_tile0(e.start, a.G, R, walk.b) + piece.r;
+              p.whole = piece.whole;
+              p.table = l.table + static_cast<int64_t>(walk.b) * l.max_pages;
+              if (piece.ta == 0)  // this CTA begins the segment
+                part.spans[static_cast<int64_t>(piece.hk) * part.span_tiles + p.tile] =
+                    span_of(sh, piece);
+            } else {
+              p.n[0] = p.n[1] = -1;
+            }
+            mbar_arrive(&piece_full[i % kRing]);
           }
-          mbar_arrive(&piece_full[i % kRing]);
-        }
-        if (!more) break;
-        // rows of one token and key/value head are neighbours
-        const int rows = min(e.nc * a.G - piece.r * R, R), line = D * 2 / 128;
-        for (int x = lane; x < rows * line; x += 32) {
-          const int gr = piece.r * R + x / line, tok = gr / a.G;
-          const char* q = reinterpret_cast<const char*>(
-              a.q + (static_cast<int64_t>(e.start + tok) * a.H + piece.hk * a.G + (gr - tok * a.G)) * D);
-          prefetch_l2(q + x % line * 128);
+          if (!more) break;
+          if constexpr (!kFetch) continue;
+          // rows of one token and key/value head are neighbours
+          const int rows = min(e.nc * a.G - piece.r * R, R), line = D * 2 / 128;
+          for (int x = lane; x < rows * line; x += 32) {
+            const int gr = piece.r * R + x / line, tok = gr / a.G;
+            const char* q = reinterpret_cast<const char*>(
+                a.q + (static_cast<int64_t>(e.start + tok) * a.H + piece.hk * a.G + (gr - tok * a.G)) * D);
+            prefetch_l2(q + x % line * 128);
+          }
         }
       }
     } else if (warp == 0) {
