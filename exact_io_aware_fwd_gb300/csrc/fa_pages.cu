@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(kTreeThreads) tree_mask_kernel(const int32_t* 
 constexpr int kBoundThreads = 128;
 
 // One warp a page and head: D / 8 lanes a row, eight rows a lane on the way.  Bound by reading the
-// keys once.
+// keys once: 16 prompts of 512 to 4096 tokens, 16 heads, pages of 16: 28.0 us (6.1 TB/s); one page of each of
+// 64 sequences 3.9 us, which are the launch and three dependent reads.
 template <int D>
 __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const BoundsArgs a) {
   constexpr int L = D / 8, kRows = 32 / L, kAhead = 8;
@@ -428,7 +429,7 @@ __device__ __forceinline__ int visible_pages(const SelectArgs& a, int t, int& b,
 }
 
 // kSelectRounds: scores of a thread in registers; further ones are read again.  (A warp a row that closes
-// in on the k-th by votes, without a barrier: 21.6 us instead of 16.7 for 512 rows of up to 256 pages.)
+// in on the k-th by votes, without a barrier: 21.6 us instead of 16.7 for 512 rows of up to 256 pages in L2.)
 constexpr float kMost = 3.402823466e38f;
 
 // behind_scores: page_score_kernel is the kernel ahead, so what it did not write is complete.
