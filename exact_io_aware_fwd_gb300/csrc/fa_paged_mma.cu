@@ -77,12 +77,6 @@ __host__ __device__ constexpr uint32_t smem_of() {
              : rows16::PagedLayout<D>::kBytes;
 }
 
-// Of a tree: a row's maximum is renewed, and its result so far rescaled, only when it grows by more than this
-// (log2 units).  Weights are then at most 2^8 instead of 1, which costs no accuracy: P keeps its 8 bits
-// and sums their 24, and the last maximum used goes into LSE.  (167.1 us, always 168.4.  Calls without a
-// mask keep their results bit for bit.)
-constexpr float kSlack = 8.f;
-
 // 32 bytes, 32-byte aligned.
 __device__ __forceinline__ void st_v8(float* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -112,7 +106,7 @@ __device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, in
 // M: kAllKeys, or kTreeKeys (one list).
 // A warp's results leave for the workspace 32 bytes a thread at a time, whole sectors (32 trees of 48 to 64
 // tokens over 2048 to 8192 keys: 165.6 us, 168.4 with 16).  Of a tree, the queries of the next pieces are
-// fetched into L2 (167.8; with the slack in the maximum, all three: 162.8).  With two lists that is
+// fetched into L2 (167.8).  With two lists that is
 // slower (128 sequences behind two prefixes of 32768 keys 137.5 us, without 136.0).
 template <int D, int kLists, bool kTwin, KeyMode M>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -537,7 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_tile = mx * c2;
         float alpha = 1.f;
         bool rescale = false;
-        if (m_tile > (M == kTreeKeys ? m_run + kSlack : m_run)) {
+        // (whenever it grows, by however little: the row's largest weight is then exactly 1, and its
+        // rounding to bf16 none; with 2^8 of slack O was off by twice as much at large logits, for 0.8%)
+        if (m_tile > m_run) {
           rescale = true;
           alpha = ex2(m_run - m_tile);  // 0 at the row's first visible key
           l_run *= alpha;

@@ -273,3 +273,63 @@ def test_refusals():
         fa.fa_tree_mask(torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError):
         fa.fa_tree_mask(good)
+
+
+# ------------------------------------------------------------- the largest weight (tensor-core kernel)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [5, 20])
+def test_a_rows_largest_weight_is_not_rounded(nq, d):
+    """One key outweighs the others, later than they come: 2^-7 of weight in each key tile, then a key
+    128.5 times as heavy.  Every key has the same value, so O is that value.  Weights but the largest are
+    off by 2^-8 of at most 11 / 128.5 of the sum, 2^-11.5, and float32 by 2^-14: less than the 2^-9 that
+    a value of 255 / 128 times a power of two has to its next ones.  128.5 rounded to 8 bits is off by
+    that much.  5 tokens of 8 heads a group are one query tile, 20 two."""
+    H, Hkv, page, B, n = 32, 4, 16, 40, 1500
+    cache = Cache([n] * B, Hkv, d, page, 40 + nq)
+    keys = torch.zeros(n, d)
+    keys[:, 0] = -30.0
+    keys[5:1400:128, 0] = 0.0
+    keys[1450, 0], keys[1450, 1] = 4.84375, float(np.log(128.5)) - 4.84375
+    value = 1.9921875 * 2.0 ** torch.randint(-3, 3, (d,), generator=torch.Generator().manual_seed(d))
+    for b in range(B):
+        for i in range(-(-n // page)):
+            p, part = int(cache.table[b, i]), keys[i * page:(i + 1) * page]
+            cache.k[p, :, :len(part)] = part.to(BF16)
+            cache.v[p, :, :len(part)] = value.to(BF16)
+    q = torch.zeros(B * nq, H, d, dtype=BF16, device=DEV)
+    q[:, :, :2] = 1.0
+    mask = torch.cat([pack(np.tri(nq, dtype=bool), 1)] * B).to(DEV)
+    out, _ = fa.fa_fwd_paged_tree(q, *cache.dev(), mask, cu_seqlens=i32([nq * b for b in range(B + 1)]), max_q=nq,
+                                  max_kv=n, scale=1.0)
+    assert fa.fa_get_error() == fa.FA_OK
+    assert torch.equal(out, value.to(BF16).to(DEV).expand_as(out))
+
+
+@pytest.mark.parametrize("sigma", [3.0, 6.0])
+@pytest.mark.parametrize("heads", [(8, 2, 128, 64), (16, 2, 64, 16)], ids=lambda h: "H%dkv%dd%dpage%d" % h)
+def test_large_logits_of_a_chain_as_those_of_a_causal_call(heads, sigma):
+    """Both have the bound of check() without the largest weight, which is exactly 1: 2^-8 of the other
+    weights times |v| and of |O|, and 2^-14 of sum p|v|; logits of up to 400 make exponents off by
+    2^-24 (d + 16) sum|q k| scale, that is relative weights by as much."""
+    H, Hkv, d, page = heads
+    for nq, lens in (([6, 9], [2500, 1300]), ([40], [3000])):
+        chain = [np.tri(n, dtype=bool) for n in nq]
+        cache, q, mask, out, lse = run(nq, lens, heads, 50 + nq[0], chain, sigma=sigma)
+        cu = cumulative(nq)
+        ref, _ = fa.fa_fwd_paged(q.to(DEV), *cache.dev(), cu_seqlens=i32(cu), max_q=max(nq), max_kv=max(lens),
+                                 causal=True)
+        for b, n in enumerate(nq):
+            K, V = cache.keys(b)
+            for i in range(n):
+                sees, qi = lens[b] - n + i + 1, f64(q[cu[b] + i])
+                for h in range(H):
+                    k, v = K[h * Hkv // H][:sees], V[h * Hkv // H][:sees]
+                    s = k @ qi[h] * d ** -0.5
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    O, A, top = p @ v, p @ np.abs(v), int(p.argmax())
+                    size = d ** -0.5 * float((np.abs(k) @ np.abs(qi[h])).max())
+                    bound = (2.0 ** -8 * (A - p[top] * np.abs(v[top])) + 2.0 ** -8 * np.abs(O) +
+                             (2.0 ** -14 + 2 * 2.0 ** -24 * (d + 16) * size) * (A + np.abs(O)))
+                    for x in (out, ref):
+                        assert np.all(np.abs(f64(x[cu[b] + i, h]) - O) <= bound), (b, i, h, x is out)
