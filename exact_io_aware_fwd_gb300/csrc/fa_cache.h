@@ -32,6 +32,17 @@ __host__ __device__ __forceinline__ int first_slot(const int32_t* cu, int b, int
   return (min(max(at, 0), total) >> shift) + 2 * b;
 }
 
+// Whether offsets [t0, t1) of a sequence of `len` keys leave its pages out: they are none, or `total`
+// cuts new tokens off whose pages its other ones do not lie in.
+__host__ __device__ inline bool pages_left_out(int t0, int t1, int total, int len, int shift) {
+  if (t0 < 0 || t1 < t0) return true;
+  int start, n;
+  clamp_tokens(t0, t1, total, start, n);
+  if (n == t1 - t0 || len == 0) return false;
+  const int all = t1 - t0 < len ? len - (t1 - t0) : 0, some = n < len ? len - n : 0;
+  return n == 0 || some >> shift > all >> shift;
+}
+
 #ifdef __CUDACC__
 // Keys of sequence b, clamped (and reported).
 __device__ __forceinline__ int keys_of(const CacheSeqs& c, int b, bool report) {

@@ -105,6 +105,11 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const Bounds
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kBoundThreads / 32) + (threadIdx.x >> 5);
   const int64_t slots = static_cast<int64_t>(c.total >> c.page_shift) + 2 * static_cast<int64_t>(c.B);
   if (unit >= slots * c.Hkv) return;
+  if (unit < c.B && c.cu != nullptr && lane == 0) {  // (there are more warps than sequences)
+    const int s = static_cast<int>(unit);
+    if (pages_left_out(__ldg(c.cu + s), __ldg(c.cu + s + 1), c.total, keys_of(c, s, false), c.page_shift))
+      atomicCAS(c.status, 0, kErrIndex);
+  }
   const int slot = static_cast<int>(unit / c.Hkv), h = static_cast<int>(unit - static_cast<int64_t>(slot) * c.Hkv);
   // the last sequence whose first slot is not behind this one
   OffsetSearch s{0, c.B};

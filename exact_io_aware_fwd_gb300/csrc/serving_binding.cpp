@@ -565,6 +565,7 @@ PyObject* page_bounds(PyObject* const* a) {
     const int64_t most = c.B * c.pages * c.page_size;
     total = a[5] != Py_None ? integer(a[5]) : (most < INT32_MAX ? most : INT32_MAX);
   } else if (a[5] != Py_None && integer(a[5]) != c.B) {
+    if (total == 0) total = 1;  // launched, so that offsets that say otherwise are reported
     refuse("without cu_seqlens there is one token per sequence");
   }
   const int32_t* offsets = ints(cu, {c.B + 1}, dev, "cu_seqlens");

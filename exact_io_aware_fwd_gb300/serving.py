@@ -274,7 +274,8 @@ def fa_page_bounds(k_cache, block_table, kv_lens, bounds, cu_seqlens=None, total
     """Renews the bounds (bf16 [pages, Hkv, 2, d]: the smallest and the largest of each element of a
     page's keys) of the pages that hold one of the last n keys of each sequence (see include/fa.h).
     cu_seqlens: offsets whose differences are n, default 1 each; total: at least their last one, which
-    bounds the launch (default: what the block table has room for).  Returns bounds."""
+    bounds the launch (default: what the block table has room for, a warp for each of its pages; pages
+    that a smaller one leaves out are reported).  Returns bounds."""
     ext = _ext or _binding()
     if stream is None:
         return ext.page_bounds(k_cache, block_table, kv_lens, bounds, cu_seqlens, total)

@@ -409,7 +409,9 @@ fa_status fa_fwd_paged_tree(const void* Q, const fa_paged_kv* cache, const uint6
  * bf16 [num_pages][Hkv][2][d], renewed for the pages that hold one of the last n keys of each
  * sequence (n new tokens; n = kv_lens[b] renews all), over the keys below kv_lens[b].  A key that
  * is not a number makes its bounds so.  Other pages' bounds stay as they are.  cache->v_cache is
- * not used.
+ * not used.  total: at least cu_seqlens[B]; it bounds the launch (0: no new tokens, nothing is
+ * launched).  Pages that a smaller one leaves out record FA_ERR_INDEX, and so do offsets that do not
+ * ascend from 0.
  *
  * fa_select_pages: the `top` pages that each token's queries attend to, for every key/value head.
  *   score(page) = max over the head's queries q of sum_e max(q_e, 0) hi_e + min(q_e, 0) lo_e,

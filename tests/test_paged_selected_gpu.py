@@ -85,6 +85,29 @@ def test_bounds_out_of_range():
     fa.fa_get_error()
 
 
+def test_bounds_of_fewer_tokens_than_there_are():
+    """A total below the last offset leaves pages out, which is reported; where it leaves none out the
+    bounds are right."""
+    cache = Cache([40, 50], 2, 64, 16, 3)
+    kc, _, table, kv = cache.dev()
+    cu = i32([0, 30, 60])
+    want = torch.zeros(kc.shape[0], 2, 2, 64, dtype=BF16, device=DEV)
+    fa.fa_page_bounds(kc, table, kv, want, cu_seqlens=cu, total=60)
+    assert fa.fa_get_error() == fa.FA_OK
+    for total, left_out in ((59, False), (49, False), (48, True), (30, True), (20, True), (0, True)):
+        got = torch.zeros_like(want)
+        fa.fa_page_bounds(kc, table, kv, got, cu_seqlens=cu, total=total)
+        assert fa.fa_get_error() == (fa.FA_ERR_INDEX if left_out else fa.FA_OK), total
+        assert torch.equal(got, want) != left_out
+    # without a count: what the block table has room for, here 128 tokens
+    got = torch.zeros_like(want)
+    fa.fa_page_bounds(kc, table, kv, got, cu_seqlens=i32([0, 500, 501]))
+    assert fa.fa_get_error() == fa.FA_ERR_INDEX
+    for odd in ([0, 30, 5], [50, 2, 9], [-3, 7, 9]):
+        fa.fa_page_bounds(kc, table, kv, got, cu_seqlens=i32(odd), total=60)
+        assert fa.fa_get_error() == fa.FA_ERR_INDEX, odd
+
+
 # --------------------------------------------------------------------------------------- selection
 class Selection:
     """Bounds of a shuffled pool, queries, and the reference's choice."""
