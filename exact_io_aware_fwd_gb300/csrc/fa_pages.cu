@@ -323,22 +323,38 @@ struct FineRows {
   }
 };
 
-// The score as an integer: sum q_e box_e in units of 2^-62 of sum |q_e| max |bound| or more.  q and
-// the bounds are scaled by powers of two so that sum |u_e| <= 1 for the products u_e, which are
-// exact; three times the next 22 bits of a product are taken off as an integer (adding 3/2 2^23
-// rounds to one), and the integers are added up, in any order.  fp64 would do, but at two
+// A power of two, as two factors that are applied one after the other: what scales a number below the
+// smallest normal one to about 1 is no float.
+struct Scale {
+  float pre, by;
+  __device__ float operator()(float x) const { return x * pre * by; }
+};
+// x > 0 to [1/2, 1) (x < 2^126; 0: anything).
+__device__ __forceinline__ Scale scale_to_one(float x) {
+  const float pre = x < 0x1p-126f ? 0x1p64f : 1.f;
+  const int e = static_cast<int>(__float_as_uint(x * pre) >> 23);  // x pre < 2^(e - 126)
+  return {pre, x == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(max(253 - e, 1)) << 23)};
+}
+
+// The score as an integer: sum q_e box_e in units of 2^-62, where S = sum |q_e| max |bound| has been
+// scaled to [1/2, 1) by powers of two (S may be off by its float32 sum, 2^-19 of it).  The products u_e
+// are exact and below 1.  Their next 22, 23 and 23 bits are taken off as integers one after the other
+// (adding 3/2 2^23 rounds to one; what is left is at most half of the last one's unit, so the next are
+// at most 2^22), and the integers are added up, in any order.  D products rounded at 2^-69 are off by
+// 2^-62 together, cutting the sum to units of 2^-62 by less than that: of two scores that are 3 2^-62,
+// below 2^-59 S, apart or more, the larger one stays the larger.  fp64 would do, but at two
 // multiply-adds a cycle and SM it made this the longest part of the kernel (18 us of 33).
 template <int D>
 __device__ __forceinline__ int64_t fine_score(const SelectArgs& a, int b, int hk, int t, int p, int lane,
-                                              float q_scale, float box_scale) {
+                                              Scale q_scale, Scale box_scale) {
   constexpr int E = D / 32;
   constexpr float kRound = 12582912.f;  // 3/2 2^23
   const FineRows<D> r(a, b, hk, t, p, lane);
   float lo[E], hi[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    lo[e] = r.there ? __bfloat162float(r.box[e]) * box_scale : 0.f;
-    hi[e] = r.there ? __bfloat162float(r.box[D + e]) * box_scale : 0.f;
+    lo[e] = r.there ? box_scale(__bfloat162float(r.box[e])) : 0.f;
+    hi[e] = r.there ? box_scale(__bfloat162float(r.box[D + e])) : 0.f;
   }
   int64_t best = INT64_MIN;
   for (int g = 0; g < a.G; g += kFineHeads) {
@@ -348,15 +364,15 @@ __device__ __forceinline__ int64_t fine_score(const SelectArgs& a, int b, int hk
       sum[i][0] = sum[i][1] = sum[i][2] = 0u;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float q = __bfloat162float(r.q[min(g + i, a.G - 1) * D + e]) * q_scale;
+        const float q = q_scale(__bfloat162float(r.q[min(g + i, a.G - 1) * D + e]));
         float u = q * (q > 0.f ? hi[e] : lo[e]), t;
         t = fmaf(u, 0x1p22f, kRound);
         u = fmaf(t - kRound, -0x1p-22f, u);
         sum[i][0] += __float_as_uint(t) - __float_as_uint(kRound);
-        t = fmaf(u, 0x1p44f, kRound);
-        u = fmaf(t - kRound, -0x1p-44f, u);
+        t = fmaf(u, 0x1p45f, kRound);
+        u = fmaf(t - kRound, -0x1p-45f, u);
         sum[i][1] += __float_as_uint(t) - __float_as_uint(kRound);
-        t = fmaf(u, 0x1p66f, kRound);
+        t = fmaf(u, 0x1p68f, kRound);
         sum[i][2] += __float_as_uint(t) - __float_as_uint(kRound);
       }
     }
@@ -365,14 +381,15 @@ __device__ __forceinline__ int64_t fine_score(const SelectArgs& a, int b, int hk
       const int s0 = __reduce_add_sync(~0u, static_cast<int>(sum[i][0]));
       const int s1 = __reduce_add_sync(~0u, static_cast<int>(sum[i][1]));
       const int s2 = __reduce_add_sync(~0u, static_cast<int>(sum[i][2]));
-      const int64_t x = (((static_cast<int64_t>(s0) << 22) + s1) << 18) + (s2 >> 4);
+      const int64_t x = (((static_cast<int64_t>(s0) << 23) + s1) << 17) + (s2 >> 6);
       best = x > best ? x : best;
     }
   }
   return best;
 }
 
-// In 64 bits, where something is not finite.
+// In 64 bits, where something is not finite or S or one of its factors is 2^126 or more (sums of products
+// that are exact, off by 2^-49 S).
 template <int D>
 __device__ __forceinline__ double odd_score(const SelectArgs& a, int b, int hk, int t, int p, int lane) {
   constexpr int E = D / 32;
@@ -394,12 +411,6 @@ __device__ __forceinline__ double odd_score(const SelectArgs& a, int b, int hk, 
   }
   return best;
 }
-// The largest power of two whose product with x > 0 is at most 1 (about; x = 0: 1).
-__device__ __forceinline__ float scale_below(float x) {
-  const int e = static_cast<int>(__float_as_uint(x) >> 23);  // x < 2^(e - 126)
-  return x == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(min(max(253 - e, 1), 253)) << 23);
-}
-
 // The largest sum |q_e| of heads g0, g0 + step, ... of a group (infinite where one is not a number).
 template <int D>
 __device__ __forceinline__ float query_size(const SelectArgs& a, int t, int hk, int g0, int step, int lane) {
@@ -516,7 +527,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_pages_kernel(const Sele
     __syncthreads();  // the bins are free
   }
   // page i's score exactly, as a number that orders like it
-  const float q_scale = scale_below(size), box_scale = scale_below(far);
+  const Scale q_scale = scale_to_one(size);
+  Scale box_scale = scale_to_one(far);
+  if (q_scale(size) * box_scale(far) < 0.5f) box_scale.by *= 2.f;
   auto exact = [&](int i) {
     return odd ? ordered(odd_score<D>(a, b, hk, t, a.first + i, lane))
                : static_cast<uint64_t>(fine_score<D>(a, b, hk, t, a.first + i, lane, q_scale, box_scale)) ^ (1ull << 63);

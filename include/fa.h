@@ -419,8 +419,9 @@ fa_status fa_fwd_paged_tree(const void* Q, const fa_paged_kv* cache, const uint6
  * (causal: token i of n sees keys <= kv_lens[b] - n + i) the first `first` and the last `last` are
  * always selected, and those of the highest scores, `top` in all; of equal scores the lowest page
  * (a score that is not a number counts as infinity, a page outside the pool as bounds of 0).  The
- * choice is that of exactly computed scores (to 2^-60 of the largest sum |q_e| times the largest
- * bound; scores closer than that may count as equal), whatever the rounding.  pages: DEVICE int32
+ * choice is that of exactly computed scores, whatever the rounding, to 2^-59 of S, the largest sum
+ * |q_e| times the largest bound (2^-48 where S or one of its factors is 2^126 or more): scores closer
+ * than that count as equal or in either order.  pages: DEVICE int32
  * [total][Hkv][top], indices into the sequence's block-table row, ascending, -1 behind the last
  * where there are fewer.  first + last <= top.  cache->k_cache and v_cache are not used.
  * workspace: fa_select_pages_workspace_size(...) bytes, 256-byte aligned.

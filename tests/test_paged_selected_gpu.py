@@ -205,6 +205,27 @@ def test_select_of_equal_and_nearly_equal_pages():
     few.check(17, 0, 1)
 
 
+@pytest.mark.parametrize("count", [60, 700, 1500])
+@pytest.mark.parametrize("bound,rest", [(2.0 ** -5, 2.0 ** -65), (2.0 ** -133, 2.0 ** -59), (2.0 ** -130, 2.0 ** -62),
+                                        (2.0 ** 100, 2.0 ** -64)])
+def test_select_of_scores_a_little_apart(count, bound, rest):
+    """Two pages at the border whose scores are 0 and 127 products of `rest` and `bound`, more than 2^-59
+    of the largest bound times sum |q|, which is 1 here; the higher one has the higher index."""
+    s = Selection([1], [16 * count], (1, 1, 128, 16), count)
+    s.q[:] = rest
+    s.q[:, :, 0] = 1.0
+    pages = s.table[0].long()
+    s.bounds[:] = 0.0
+    s.bounds[:, :, :, 0] = -bound
+    s.bounds[pages[3:9], :, :, 0] = bound
+    s.bounds[pages[20], :, :, 0] = s.bounds[pages[50], :, :, 0] = 0.0
+    s.bounds[pages[50], :, :, 1:] = bound
+    got = s.check(7, 0, 0)
+    assert got.flatten().tolist() == [3, 4, 5, 6, 7, 8, 50]
+    s.bounds[pages[50], :, :, 1:] = 0.0
+    assert s.check(7, 0, 0).flatten().tolist() == [3, 4, 5, 6, 7, 8, 20]
+
+
 @pytest.mark.parametrize("count", [100, 512, 513, 700, 1100])
 def test_select_of_scores_that_are_not_finite(count):
     heads = (4, 2, 64, 16)
