@@ -347,6 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int* const lim = sees[jobs % kStats];
       const int all = w.causal ? min(len, p.shift + r * NQ / a.G + 1) : len;  // keys that every query sees
       const int64_t line = static_cast<int64_t>(p.bh) * w.cap;
+      bool left_out = false;  // a query with an LSE of -inf: its scores may be anything
+#pragma unroll
+      for (int c = 0; c < NQ; c += 32)
+        if (c + static_cast<int>(lane) < rows) left_out |= off[c + lane] == -INFINITY;
+      left_out = __any_sync(~0u, left_out);
       float next = r > 0 ? had(cur, t) : ahead;
       if (live(behind) && behind.r == 0) ahead = had(behind, t);
       for (int j = t; j < p.n; j += kGroups) {
@@ -367,6 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[t]);
+          }
+          if (left_out) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (off[c + k] == -INFINITY) s[k] = 0u;
           }
           if (!masked && c + 32 <= rows) {
 #pragma unroll

@@ -128,6 +128,23 @@ def test_weights_of_rows_without_keys_and_of_other_statistics():
         assert torch.equal(got[0, 0], ref[0, 0]) if ok else torch.all(got[0, 0, :40].isnan())
 
 
+@pytest.mark.parametrize("causal", [False, True], ids=["all", "causal"])
+@pytest.mark.parametrize("heads", [(8, 2, 128, 64), (4, 2, 64, 16)], ids=lambda h: "H%dkv%dd%dpage%d" % h)
+def test_weights_of_queries_that_are_left_out(heads, causal):
+    """A query whose LSE is -inf adds nothing whatever it holds, next to 32 and more that do."""
+    w = Weighted([70, 9, 3], [900, 300, 70], heads, causal, 21)
+    out = [3, 33, 65, 70, 79, 80, 81]
+    w.lse[:, out] = float("-inf")
+    w.q[out] = 0.0
+    before = w.before.to(DEV)
+    want = fa.fa_kv_weights(*w.args(), before, **w.opts())
+    w.check(want, w.before)
+    for odd in (float("nan"), float("inf"), -float("inf"), 3e38):
+        w.q[out] = odd
+        assert torch.equal(fa.fa_kv_weights(*w.args(), before, **w.opts()), want)
+    assert fa.fa_get_error() == fa.FA_OK
+
+
 def test_weights_repeat_in_a_graph_and_on_another_stream():
     w = Weighted([20, 3], [900, 400], (8, 2, 128, 64), True, 5)
     args, opts = w.args(), w.opts()
