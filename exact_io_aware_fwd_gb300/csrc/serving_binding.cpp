@@ -8,6 +8,7 @@
 // one loaded instance of it.
 #include <Python.h>
 
+#include <algorithm>
 #include <stdexcept>
 #include <string>
 #include <utility>
@@ -564,8 +565,8 @@ PyObject* page_bounds(PyObject* const* a) {
   if (cu != nullptr) {
     const int64_t most = c.B * c.pages * c.page_size;
     total = a[5] != Py_None ? integer(a[5]) : (most < INT32_MAX ? most : INT32_MAX);
-  } else if (a[5] != Py_None && integer(a[5]) != c.B) {
     if (total == 0) total = 1;  // launched, so that offsets that say otherwise are reported
+  } else if (a[5] != Py_None && integer(a[5]) != c.B) {
     refuse("without cu_seqlens there is one token per sequence");
   }
   const int32_t* offsets = ints(cu, {c.B + 1}, dev, "cu_seqlens");
@@ -692,7 +693,7 @@ PyObject* kv_evict(PyObject* const* a) {
   const int budget = int32_of(a[6], "budget"), recent = int32_of(a[7], "recent");
   const int max_kv = a[8] != Py_None ? int32_of(a[8], "max_kv") : reach_of(c);
   if (budget < 1 || recent < 0 || recent > budget) refuse("0 <= recent <= budget and 1 <= budget");
-  if (table.size(1) * c.page_size < (budget < max_kv ? budget : max_kv))
+  if (table.size(1) * c.page_size < std::min<int64_t>({budget, max_kv, cap}))
     refuse("new_table must have pages for the keys that may be kept");
   const c10::cuda::OptionalCUDAGuard guard(dev);
   const at::Tensor lens = fresh({c.B}, at::kInt, dev);

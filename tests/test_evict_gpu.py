@@ -351,6 +351,18 @@ def test_evict_out_of_range_and_refusals():
             fa.fa_kv_evict(*wrong)
 
 
+def test_evict_to_pages_for_the_keys_that_there_are():
+    """No more keys are kept than the weights have columns for, however far the block table and the
+    budget reach."""
+    e = Evicted([100, 60], 2, 64, 16, 200, 23)
+    e.table = torch.cat([e.table, torch.full((2, 13), -1, dtype=torch.int32)], 1).contiguous()  # 320 keys
+    assert e.w.shape[2] == 102 and e.new.shape[1] == 7  # 112 keys
+    e.check(10)
+    e.new = e.new[:, :6].contiguous()
+    with pytest.raises(ValueError):
+        e.run(10)
+
+
 # ------------------------------------------------------------------------------- as it is used
 def test_weights_eviction_and_decoding_on():
     """Weights gathered over steps, an eviction, and attention over what is left: as plain attention
