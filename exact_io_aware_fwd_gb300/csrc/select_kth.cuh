@@ -148,7 +148,7 @@ __device__ __forceinline__ Kth<Key> kth_largest(int k, int few, Each each,
     hi = __reduce_max_sync(~0u, v.y);
   }
   Kth<Key> r{lo, hi - lo, k, -1};
-  for (int pass = 0;; ++pass) {  // a pass leaves at most a 1024th of the range
+  for (int pass = 0;; ++pass) {  // a pass leaves at most a 1024th of the range (clusters: a 512th)
     const int bits = bit_length(r.range), shift = bits > kBits ? bits - kBits : 0;
     // two sets of bins take turns: this one is empty, and the other is cleared once nobody reads it
     unsigned* const hist = sh.hist[pass & 1];
