@@ -342,7 +342,9 @@ def fa_kv_evict(weights, k_cache, v_cache, block_table, kv_lens, new_table, budg
     and their values are copied to the pages new_table (int32 [B, pages], unused pages of the
     cache).  Returns (new_lens int32 [B], kept int32 [B, Hkv, budget]: which keys, -1 behind the
     last, new_weights float32 [B, Hkv, budget]).  The next token's rotary position stays kv_lens[b]:
-    kv_lens - new_lens is what fa_kv_append's pos_offset grows by."""
+    kv_lens - new_lens is what fa_kv_append's pos_offset grows by.  The new pages have no bounds yet
+    (fa_page_bounds with cu_seqlens that count new_lens tokens), and new_weights has no columns for
+    further keys."""
     ext = _ext or _binding()
     if stream is None:
         return ext.kv_evict(weights, k_cache, v_cache, block_table, kv_lens, new_table, budget,

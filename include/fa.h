@@ -464,7 +464,9 @@ fa_status fa_fwd_paged_selected(const void* Q, const fa_paged_kv* cache, const i
  * (ascending, -1 behind the last); new_weights: float32 [B][Hkv][budget], their weights (0 behind
  * the last); all DEVICE and overlapping none of the inputs.  0 <= recent <= budget.  Keys keep the
  * rotation that they had, so the next token's position is kv_lens[b], not new_lens[b]: the
- * difference is fa_kv_append's pos_offset.
+ * difference is fa_kv_append's pos_offset.  The new pages' bounds are the caller's to renew
+ * (fa_page_bounds with new_lens[b] new tokens), and weights of further tokens' keys need more columns
+ * than the `budget` of new_weights.
  */
 fa_status fa_kv_weights(const void* Q, const float* LSE, const fa_paged_kv* cache,
                         const float* weights, float* out, int capacity, const int32_t* cu_seqlens,

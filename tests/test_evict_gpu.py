@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import exact_io_aware_fwd_gb300 as fa
-from oracle.serving import attend, evict, key_weights
+from oracle.serving import attend, evict, key_weights, page_bounds, page_scores, select_pages
 from test_paged_gpu import Cache, _built, cumulative, f64, i32, limits_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -407,3 +407,51 @@ def test_weights_eviction_and_decoding_on():
             kk, vv = np.stack(kk + [kn[at]]), np.stack(vv + [vn[at]])
             O, L, A, _ = attend(f64(q[b:b + 1, h:h + 1]), kk[None], vv[None], d ** -0.5, [budget + 1])
             assert np.all(np.abs(f64(o[b, h]) - O[0, 0]) <= (2.0 ** -8 + 2.0 ** -14) * A[0, 0] + 2.0 ** -8 * np.abs(O[0, 0]))
+
+
+def test_decoding_on_after_an_eviction():
+    """An eviction of keys whose pages are selected: the new pages' bounds, the weights in their wider
+    array, and steps of appending, selecting, attending and gathering from there, as the reference."""
+    H, Hkv, d, page, budget, top, steps = 8, 2, 64, 16, 70, 3, 12
+    lens = [150, 40, 99]
+    kept_lens = [min(n, budget) for n in lens]
+    g = torch.Generator().manual_seed(12)
+    cache = Cache([*lens, *(n + steps for n in kept_lens)], Hkv, d, page, 13)
+    kc, vc, table, _ = cache.dev()
+    new_table = table[3:, :-(-(budget + steps) // page)].contiguous()
+    bounds = torch.full((kc.shape[0], Hkv, 2, d), float("nan"), dtype=BF16, device=DEV)
+    weights = torch.rand(3, Hkv, 160, generator=g).to(DEV)
+    block_table, kv_lens = table[:3].contiguous(), i32(lens)
+    new_lens, kept, new_weights = fa.fa_kv_evict(weights, kc, vc, block_table, kv_lens, new_table, budget, 9)
+    pos_offset = kv_lens - new_lens
+    block_table, kv_lens = new_table, new_lens
+    weights.zero_()
+    weights[:, :, :budget] = new_weights
+    cu = torch.nn.functional.pad(kv_lens.cumsum(0, dtype=torch.int32), (1, 0))
+    fa.fa_page_bounds(kc, block_table, kv_lens, bounds, cu_seqlens=cu)
+    rope = fa.fa_rope_table(256, d, device=DEV)
+    want, err = f64(weights), np.zeros(weights.shape)
+    for step in range(steps):
+        kv_lens = kv_lens + 1
+        x = torch.randn(3, H + 2 * Hkv, d, generator=g).to(BF16).to(DEV)
+        q, k, v = x.split([H, Hkv, Hkv], dim=1)
+        q = fa.fa_kv_append(q, k, v, kc, vc, block_table, kv_lens, pos_offset=pos_offset, table=rope)
+        fa.fa_page_bounds(kc, block_table, kv_lens, bounds)
+        pages = fa.fa_select_pages(q, bounds, block_table, kv_lens, page, top)
+        fa.fa_fwd_paged_selected(q, kc, vc, block_table, kv_lens, pages)
+        o, lse = fa.fa_fwd_paged(q, kc, vc, block_table, kv_lens)
+        fa.fa_kv_weights(q, lse, kc, block_table, kv_lens, weights, out=weights)
+        assert fa.fa_get_error() == fa.FA_OK
+        pool = f64(kc)
+        for b, n in enumerate(kv_lens.tolist()):
+            at = [(block_table[b, j // page].item(), j % page) for j in range(n)]
+            K = np.stack([pool[p, :, r] for p, r in at], 1)
+            score = page_scores(f64(q[b]), *page_bounds(K, page))
+            for h in range(Hkv):
+                pick = select_pages(score[h], -(-n // page), top, 1, 1).tolist()
+                assert pages[b, h].tolist() == pick + [-1] * (top - len(pick))
+            w, e = key_weights(f64(q[b:b + 1]), K, d ** -0.5, f64(lse[:, b:b + 1].T), [n])
+            want[b, :, :n] += w
+            err[b, :, :n] += 2.0 ** -24 * (d + 24 + H // Hkv) * e
+    # the terms' errors, and a rounding of the whole a step
+    assert np.all(np.abs(f64(weights) - want) <= err + 2.0 ** -23 * steps * want)
