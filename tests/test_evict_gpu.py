@@ -145,6 +145,17 @@ def test_weights_of_queries_that_are_left_out(heads, causal):
     assert fa.fa_get_error() == fa.FA_OK
 
 
+def test_weights_of_a_wide_array():
+    """Columns far past the keys keep what they have, in place or not, and are zeros without weights."""
+    w = Weighted([1, 3, 0], [700, 40, 9], (8, 2, 128, 64), True, 22)
+    w.before = torch.exp(torch.randn(3, 2, 100003, generator=torch.Generator().manual_seed(22)))
+    before = w.before.to(DEV)
+    w.check(fa.fa_kv_weights(*w.args(), before, **w.opts()), w.before)
+    out = torch.full_like(before, float("nan"))
+    w.check(fa.fa_kv_weights(*w.args(), out=out, **w.opts()), None)
+    w.check(fa.fa_kv_weights(*w.args(), before, out=before, **w.opts()), w.before)
+
+
 def test_weights_repeat_in_a_graph_and_on_another_stream():
     w = Weighted([20, 3], [900, 400], (8, 2, 128, 64), True, 5)
     args, opts = w.args(), w.opts()
