@@ -1,6 +1,6 @@
 // How the cache's operators divide their work, on the host.  The places that fa_page_bounds gives to the
 // pages of a ragged batch: every page that holds a new key has one, no two share one, all lie in the
-// launch, and the search finds each place's sequence.  The pieces of fa_kv_weights' workers: every key
+// launch, and the search finds each place's sequence; and which totals leave pages out.  The pieces of fa_kv_weights' workers: every key
 // tile of every sequence that has queries is in one, and no more.  Prints one line per failed check.
 #include <cstdio>
 #include <map>
@@ -96,6 +96,18 @@ int main() {
           CHECK(used[static_cast<size_t>(slot)]++ == 0);
           CHECK(sequence_of(offsets, B, total, shift, slot) == b);
         }
+        // pages of the last n keys, all counted and with a total that cuts some off
+        const int cut = random(total + 2);
+        int s0, some;
+        fa::clamp_tokens(start, start + n, cut, s0, some);
+        bool out = false;
+        for (int key = len > n ? len - n : 0; key < len; ++key) {
+          bool renewed = false;
+          for (int k = len > some ? len - some : 0; k < len; ++k) renewed = renewed || k >> shift == key >> shift;
+          out = out || !renewed;
+        }
+        CHECK(fa::pages_left_out(start, start + n, cut, len, shift) == out);
+        CHECK(fa::pages_left_out(-1, n, total, len, shift) && fa::pages_left_out(n + 1, n, n + 1, len, shift));
       }
     }
   for (int round = 0; round < 300; ++round) {
