@@ -106,8 +106,8 @@ __device__ __forceinline__ int tiles_in_piece(const Entry& e, const Piece& p, in
 // M: kAllKeys, or kTreeKeys (one list).
 // A warp's results leave for the workspace 32 bytes a thread at a time, whole sectors (32 trees of 48 to 64
 // tokens over 2048 to 8192 keys: 165.6 us, 168.4 with 16).  Of a tree, the queries of the next pieces are
-// fetched into L2 (167.8).  With two lists that is
-// slower (128 sequences behind two prefixes of 32768 keys 137.5 us, without 136.0).
+// fetched into L2 (167.8; both: 164.2).  With two lists that is slower (128 sequences behind two prefixes of
+// 32768 keys 137.5 us, without 136.0).
 template <int D, int kLists, bool kTwin, KeyMode M>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_mma_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -532,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale = false;
         // (whenever it grows, by however little: the row's largest weight is then exactly 1, and its
-        // rounding to bf16 none; with 2^8 of slack O was off by twice as much at large logits, for 0.8%)
+        // rounding to bf16 none; with 2^8 of slack O was off by up to twice as much at large logits, and the
+        // trees above took 162.6 us)
         if (m_tile > m_run) {
           rescale = true;
           alpha = ex2(m_run - m_tile);  // 0 at the row's first visible key

@@ -85,11 +85,11 @@ constexpr float mma_tile_cost(int d) { return d == 64 ? 30.f : 20.f; }
 // Key tiles that a segment of the tensor-core kernel counts besides its own in a call with a tree: a CTA
 // takes 7.4 us longer for each piece of its share, as for 3.6 key tiles (queries to load, the pipeline
 // to empty and fill, a result to write).  32 trees of 48 to 64 tokens, 8 heads and 2048 to 8192 keys:
-// 162.1 us (with 3 163.0, 2 165.3, 0 172.9); 64 of them over 512 to 2048 keys 128 and, with 0, 144; of 20
-// to 30 tokens, 64 over 2048 to 8192 keys, 236 and 251.  With fewer sequences and heads than CTAs the
-// parts are what costs: 4 trees over 700 keys 22.3 us, with 2 20.6, over 2000 26.3 and 24.6 (with 0
-// 28.9).  Calls without a mask keep their division of the work, and with it their results
-// bit for bit.
+// 164.2 us (of a version 1% faster, whose maxima were not exact: 162.1, with 3 163.0, 2 165.3, 0
+// 172.9); 64 of them over 512 to 2048 keys 128 and, with 0, 144; of 20 to 30 tokens, 64 over 2048 to
+// 8192 keys, 236 and 251.  With fewer sequences and heads than CTAs the parts are what costs: 4 trees
+// over 700 keys 22.3 us, with 2 20.6, over 2000 26.3 and 24.6 (with 0 28.9).  Calls without a mask keep
+// their division of the work, and with it their results bit for bit.
 int tree_extra(int B, int Hkv) { return static_cast<long long>(B) * Hkv >= fa::kPagedCtas ? 4 : 2; }
 
 // Few rows: whether a CTA takes whole segments, its warps an eighth of the keys each, so that there
